@@ -441,6 +441,169 @@ MPOPT_API opt_status opt_selftest_wait_timeout(const float* G, float* O, int64_t
                                                void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Feed-forward operators
+ * ----------------------
+ * The operators around the parameters: the bf16 model copies the step writes
+ * are their weights, and the fp32 main_grad buffers the step reads are their
+ * outputs.  A residual block is
+ *
+ *   h = x + residual;  y = rmsnorm(h) * gamma          opt_rmsnorm_forward
+ *   u = act(y w1^T + b1)                                opt_linear_forward
+ *   out = u w2^T + b2 + h                               opt_linear_forward
+ *
+ * and the gradients run through opt_linear_backward and opt_rmsnorm_backward
+ * into main_grad.  Conventions beyond the shared ones:
+ *
+ *  - Matrices are row-major with elements of a row contiguous; `*_ld` is the
+ *    distance between rows in elements (>= the row's length).  With one row
+ *    the distance is not used.  Rows may be slices of wider rows.
+ *  - Sums, norms and products are accumulated in fp32; an output is rounded
+ *    once, to its own type, round-to-nearest-even.
+ *  - 8-bit values are e4m3 with one fp32 scale per row, value = q * scale:
+ *      scale = max(max_j |y_j|, 1e-30) / 448,   q_j = rne_e4m3(y_j * (1 / scale))
+ *    so the largest magnitude of a row maps to 448, and a row of zeros has
+ *    q = 0.  A NaN stays a NaN; a row that holds an infinity has scale = inf
+ *    and stands for NaN throughout.
+ *  - Zero rows (rows or m = 0) are allowed: nothing is read, and gradients of
+ *    parameters are left as they are (accumulate) or set to zero.
+ *  - The workspace of opt_linear_* and opt_rmsnorm_backward is 256-byte aligned
+ *    device memory.  The first 256 bytes of a linear workspace must be zero
+ *    before its first use (cudaMemset); every call leaves them zero unless a
+ *    bounded device-side wait ran out.  opt_device_status() reports that, and
+ *    the workspace must be zeroed again before its next use.
+ */
+enum { OPT_DTYPE_FP32 = 0, OPT_DTYPE_BF16 = 1, OPT_DTYPE_E4M3 = 2 };
+
+/* Activations: u; max(u, 0) (a NaN stays one); u (1 + tanh(sqrt(2/pi) (u +
+   0.044715 u^3))) / 2; u / (1 + exp(-u)). */
+enum { OPT_ACT_NONE = 0, OPT_ACT_RELU = 1, OPT_ACT_GELU = 2, OPT_ACT_SILU = 3 };
+
+/*
+ * RMS norm with the residual's addition, one row (token) at a time, cols <= 49152:
+ *   h = x + residual          (residual NULL: h = x)
+ *   rstd = 1 / sqrt(mean_j h_j^2 + eps)
+ *   y_j = h_j * rstd * gamma_j
+ * y is formed from the unrounded h.  Outputs that are NULL are not written.
+ */
+typedef struct {
+  const void* x;          /* [rows][cols], dtype                               */
+  const void* residual;   /* [rows][cols], dtype, or NULL                      */
+  const void* gamma;      /* [cols], gamma_dtype (FP32 or BF16)                */
+  void* h;                /* [rows][cols], dtype; may be x or residual itself
+                             (same pointer and row distance)                   */
+  uint16_t* y;            /* [rows][cols] bf16                                 */
+  uint8_t* q;             /* [rows][cols] e4m3 of y; needs q_scale             */
+  float* q_scale;         /* [rows]; needs q                                   */
+  float* rstd;            /* [rows]                                            */
+  int64_t rows, cols;
+  int64_t x_ld, residual_ld, h_ld, y_ld, q_ld;
+  int32_t dtype;          /* FP32 or BF16                                      */
+  int32_t gamma_dtype;
+  float eps;              /* >= 0                                              */
+  int32_t reserved;
+} opt_rmsnorm_args;
+
+MPOPT_API opt_status opt_rmsnorm_forward(const opt_rmsnorm_args* args, void* stream);
+
+/*
+ * Gradient of opt_rmsnorm_forward at h, with n_j = h_j rstd and g_j = dy_j gamma_j:
+ *   dx_j = rstd (g_j - n_j mean_i(g_i n_i)) + dh_j     (x and residual both get dx)
+ *   dgamma_j (+)= sum over rows of dy_j n_j            (fp32, in a fixed order)
+ * cols <= 24576.  With dgamma the call needs a workspace of
+ * opt_rmsnorm_workspace_size(rows, cols) bytes (its contents do not matter).
+ */
+typedef struct {
+  const uint16_t* dy;     /* [rows][cols] bf16                                 */
+  const void* h;          /* [rows][cols], dtype                               */
+  const void* gamma;      /* [cols], gamma_dtype                               */
+  const float* rstd;      /* [rows]                                            */
+  const void* dh;         /* [rows][cols], dtype: gradient reaching h past the
+                             norm, or NULL                                     */
+  void* dx;               /* [rows][cols], dtype; may be dh itself, or NULL    */
+  float* dgamma;          /* [cols] main_grad of gamma, or NULL                */
+  int64_t rows, cols;
+  int64_t dy_ld, h_ld, dh_ld, dx_ld;
+  int32_t dtype;
+  int32_t gamma_dtype;
+  int32_t accumulate;     /* nonzero: dgamma += ...; zero: dgamma = ...        */
+  int32_t reserved;
+} opt_rmsnorm_grad_args;
+
+MPOPT_API opt_status opt_rmsnorm_backward(const opt_rmsnorm_grad_args* args, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+MPOPT_API size_t opt_rmsnorm_workspace_size(int64_t rows, int64_t cols);
+
+/*
+ * Rows in e4m3 with a scale each (see above): x [rows][cols] of dtype FP32 or
+ * BF16, cols <= 49152.  For a weight [n][k] this is the operand that
+ * opt_linear_forward reads in 8 bits.
+ */
+MPOPT_API opt_status opt_quantize_rows(const void* x, int64_t x_ld, int32_t dtype, int64_t rows, int64_t cols,
+                                       uint8_t* q, int64_t q_ld, float* scale, void* stream);
+
+/*
+ * Linear layer with a fused epilogue, on the tensor cores:
+ *   z = x w^T + bias;  y = act(z) + residual
+ * Operands are both BF16, or both E4M3 with x_scale [m] and w_scale [n]
+ * (products in 8 bits, fp32 sums, scaled in the epilogue).
+ */
+typedef struct {
+  const void* x;            /* [m][k] dtype                                    */
+  const void* w;            /* [n][k] dtype                                    */
+  const float* x_scale;     /* [m], E4M3 only                                  */
+  const float* w_scale;     /* [n], E4M3 only                                  */
+  const void* bias;         /* [n] bias_dtype (FP32 or BF16), or NULL          */
+  const uint16_t* residual; /* [m][n] bf16, or NULL                            */
+  uint16_t* y;              /* [m][n] bf16; may be residual itself             */
+  uint16_t* z;              /* [m][n] bf16 pre-activation for the gradient, or NULL */
+  int64_t m, n, k;          /* m >= 0, n, k >= 1                               */
+  int64_t x_ld, w_ld, residual_ld, y_ld, z_ld;
+  int32_t dtype;            /* BF16 or E4M3                                    */
+  int32_t bias_dtype;
+  int32_t act;              /* OPT_ACT_*                                       */
+  int32_t reserved;
+} opt_linear_args;
+
+MPOPT_API opt_status opt_linear_forward(const opt_linear_args* args, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
+/*
+ * Gradients of z = x w^T + bias for a given dz (bf16):
+ *   dx = (dz w) * act_prev'(z_prev)   bf16; with z_prev, x = act_prev(z_prev) is
+ *        taken to be the previous layer's output and dx is that layer's dz
+ *   dw (+)= dz^T x                    fp32 main_grad of w
+ *   dbias (+)= column sums of dz      fp32 main_grad of the bias
+ * Outputs that are NULL are not computed, and what only they need may be NULL.
+ * Every sum has a fixed order: a call gives the same bits each time.
+ */
+typedef struct {
+  const uint16_t* dz;       /* [m][n] bf16                                     */
+  const uint16_t* x;        /* [m][k] bf16 (for dw)                            */
+  const uint16_t* w;        /* [n][k] bf16 (for dx)                            */
+  const uint16_t* z_prev;   /* [m][k] bf16, or NULL                            */
+  uint16_t* dx;             /* [m][k] bf16, or NULL                            */
+  float* dw;                /* [n][k] fp32, dense, or NULL                     */
+  float* dbias;             /* [n] fp32, or NULL                               */
+  int64_t m, n, k;
+  int64_t dz_ld, x_ld, w_ld, z_prev_ld, dx_ld;
+  int32_t act_prev;         /* OPT_ACT_* (with z_prev)                         */
+  int32_t accumulate;       /* nonzero: dw, dbias += ...; zero: = ...          */
+} opt_linear_grad_args;
+
+MPOPT_API opt_status opt_linear_backward(const opt_linear_grad_args* args, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/*
+ * Workspace bytes for opt_linear_forward and opt_linear_backward of these
+ * sizes.  The tensor cores' operands are read in 16-byte pieces: an operand
+ * whose base or row distance is not a multiple of 16 bytes is first copied
+ * into the workspace.  flags 0: room for the operands whose dense layout
+ * needs that; OPT_LINEAR_ANY_LAYOUT: room for all of them.
+ */
+enum { OPT_LINEAR_ANY_LAYOUT = 1 };
+MPOPT_API size_t opt_linear_workspace_size(int64_t m, int64_t n, int64_t k, int32_t flags);
+
+/*
  * Optional launch instrumentation (off by default).  After
  *   opt_profile_launches(events, info, capacity, &count)
  * every kernel this library launches from the calling thread is bracketed by
@@ -473,8 +636,18 @@ enum {
   OPT_KERNEL_GRAD_NORM = 8,     /* clipping: sums of squares of the gradients      */
   OPT_KERNEL_CLIP_FINALIZE = 9, /* clipping: total norm and factor                 */
   OPT_KERNEL_MUON_SAMPLE = 10,  /* per-matrix power-of-two scale of the iterate    */
-  OPT_KERNEL_NS_SYM = 11        /* grouped iterations: product of two commuting
+  OPT_KERNEL_NS_SYM = 11,       /* grouped iterations: product of two commuting
                                    symmetric [A][A] matrices, fp16 tensor cores  */
+  OPT_KERNEL_RMSNORM = 12,      /* feed-forward operators: a = rows (m), b = cols (n);
+                                   count is 1                                    */
+  OPT_KERNEL_RMSNORM_GRAD = 13,
+  OPT_KERNEL_RMSNORM_DGAMMA = 14, /* joins the partial sums of dgamma            */
+  OPT_KERNEL_QUANTIZE = 15,
+  OPT_KERNEL_LINEAR = 16,       /* y                                             */
+  OPT_KERNEL_LINEAR_DX = 17,
+  OPT_KERNEL_LINEAR_DW = 18,
+  OPT_KERNEL_LINEAR_DBIAS = 19,
+  OPT_KERNEL_LINEAR_REPACK = 20 /* an operand copied to 16-byte aligned rows     */
 };
 
 MPOPT_API opt_status opt_profile_launches(void* const* events, opt_launch_info* info, int32_t capacity,
@@ -486,7 +659,8 @@ MPOPT_API const char* opt_strerror(opt_status status);
 /* Text of the last CUDA error seen by this thread's calls ("" if none). */
 MPOPT_API const char* opt_last_cuda_error(void);
 
-/* ABI version: (major << 16) | minor (2.0: Muon variants, scale shapes, clipping). */
+/* ABI version: (major << 16) | minor (2.0: Muon variants, scale shapes, clipping;
+   2.1: feed-forward operators). */
 MPOPT_API int32_t opt_abi_version(void);
 
 #ifdef __cplusplus

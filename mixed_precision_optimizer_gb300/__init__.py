@@ -15,6 +15,9 @@ Entry points (same names as the C ABI, without the ``opt_`` prefix):
 * ``workspace_size``  -- device scratch bytes a call needs
 * ``ns_plan``         -- how a matrix's Newton-Schulz iterations are grouped
 * ``device_status``   -- reads the device-side status word of a workspace
+* ``rmsnorm``, ``rmsnorm_backward``, ``quantize_rows``, ``linear``,
+  ``linear_backward`` -- the feed-forward operators around the parameters
+  (``feedforward``)
 * ``sharded.shard_plan`` -- opt_shard_plan: the data-parallel sharding plan
   (``sharded`` also holds the per-rank views and the bf16 exchange)
 """
@@ -86,11 +89,14 @@ EXPORTED = ("opt_workspace_size", "opt_adamw_step", "opt_muon_step", "opt_mixed_
             "opt_copy_from_host",
             "opt_selftest_wait_timeout", "opt_profile_launches",
             "opt_strerror",
-            "opt_last_cuda_error", "opt_abi_version")
+            "opt_last_cuda_error", "opt_abi_version",
+            "opt_rmsnorm_forward", "opt_rmsnorm_backward", "opt_rmsnorm_workspace_size", "opt_quantize_rows",
+            "opt_linear_forward", "opt_linear_backward", "opt_linear_workspace_size")
 
 KERNEL_NAMES = {0: "ns_gram", 1: "ns_poly", 2: "ns_bx", 3: "adamw", 4: "muon_momentum", 5: "muon_norm",
                 6: "muon_apply", 7: "muon_fixup", 8: "grad_norm", 9: "clip_finalize", 10: "muon_sample",
-                11: "ns_sym"}
+                11: "ns_sym", 12: "rmsnorm", 13: "rmsnorm_grad", 14: "rmsnorm_dgamma", 15: "quantize_rows",
+                16: "linear", 17: "linear_dx", 18: "linear_dw", 19: "linear_dbias", 20: "linear_repack"}
 WORKSPACE_CLIP = 0x10
 WORKSPACE_GROUPED = 0x20
 
@@ -155,6 +161,7 @@ def lib():
     L.opt_last_cuda_error.restype = ctypes.c_char_p
     L.opt_abi_version.argtypes = []
     L.opt_abi_version.restype = i32
+    feedforward.declare(L)
     _lib = L
     return L
 
@@ -472,3 +479,9 @@ class LaunchProfiler:
             out.append(dict(kernel=KERNEL_NAMES.get(inf.kernel, str(inf.kernel)), count=int(inf.count),
                             a=int(inf.a), b=int(inf.b), ms=float(ms)))
         return out
+
+
+# the feed-forward operators (this module is complete by here: they build on its marshalling)
+from . import feedforward  # noqa: E402
+from .feedforward import (linear, linear_backward, linear_workspace, linear_workspace_size,  # noqa: E402,F401
+                          quantize_rows, rmsnorm, rmsnorm_backward, rmsnorm_workspace, rmsnorm_workspace_size)

@@ -73,6 +73,12 @@ opt_status cuda_fail(cudaError_t e, const char* where) {
   return OPT_ERR_CUDA;
 }
 
+}  // namespace
+
+int record_cuda_error(cudaError_t e, const char* where) { return static_cast<int>(cuda_fail(e, where)); }
+
+namespace {
+
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 int64_t pad_to(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
@@ -930,7 +936,7 @@ opt_status opt_profile_launches(void* const* events, opt_launch_info* info, int3
   return OPT_OK;
 }
 
-int32_t opt_abi_version(void) { return (2 << 16) | 0; }
+int32_t opt_abi_version(void) { return (2 << 16) | 1; }
 
 }  // extern "C"
 

@@ -254,6 +254,77 @@ cudaError_t launch_reload(const ReloadBatch& batch, cudaStream_t stream);
 // (opt_copy_from_host); src is the device-visible address of the host buffer.
 cudaError_t launch_copy_from_host(void* dst, const void* src, size_t bytes, cudaStream_t stream);
 
+// ------------------------------------------------- feed-forward operators --
+
+enum : int { kFp32 = 0, kBf16 = 1, kE4m3 = 2 };   // OPT_DTYPE_*
+
+constexpr int64_t kNormMaxCols = 49152;       // a row in fp32 in shared memory
+constexpr int64_t kNormGradMaxCols = 24576;   // two of them
+constexpr int64_t kNormPartialRows = 304;     // partial sums of dgamma: CTAs of the backward pass at most
+
+struct RmsnormArgs {
+  const void *x, *residual, *gamma;
+  void* h;
+  uint16_t* y;
+  uint8_t* q;
+  float *q_scale, *rstd;
+  int64_t rows, cols, x_ld, residual_ld, h_ld, y_ld, q_ld;
+  int dtype, gamma_dtype;
+  float eps;
+  int norm;        // 0: y = x, nothing is normalised (opt_quantize_rows)
+};
+cudaError_t launch_rmsnorm(const RmsnormArgs& a, cudaStream_t stream);
+
+struct RmsnormGradArgs {
+  const uint16_t* dy;
+  const void *h, *gamma;
+  const float* rstd;
+  const void* dh;
+  void* dx;
+  float *dgamma, *partial;   // partial: [kNormPartialRows][cols]
+  int64_t rows, cols, dy_ld, h_ld, dh_ld, dx_ld;
+  int dtype, gamma_dtype, accumulate;
+};
+cudaError_t launch_rmsnorm_grad(const RmsnormGradArgs& a, cudaStream_t stream);
+
+// One product out[b][a] = sum_k A[a][k] B[b][k] of the linear layer.  `a` is
+// the index that is contiguous in the output: y = x w^T has A = w and B = x,
+// dx = dz w has A = w^T and B = dz, dw = dz^T x has A = x^T and B = dz^T.
+struct LinearOperand {
+  const void* p;
+  int64_t ld;      // elements between stored rows; base and distance are multiples of 16 bytes
+  int mn_major;    // stored [k][index] instead of [index][k]
+};
+enum LinearMode : int { kLinearForward = 0, kLinearDx = 1, kLinearDw = 2 };
+struct LinearArgs {
+  int mode;
+  int fp8;
+  LinearOperand A, B;
+  int64_t na, nb, nk;
+  const float *a_scale, *b_scale;       // fp8: per index of A and of B
+  const void* bias;                     // forward: [na]
+  int bias_dtype;
+  int act;                              // forward: applied; dx: differentiated at z
+  const uint16_t* residual;             // forward
+  const uint16_t* z_in;                 // dx: pre-activation [nb][na]
+  uint16_t *y, *z_out;                  // y: bf16 output of forward and dx
+  float* dw;                            // dw: fp32 output
+  int accumulate;
+  int64_t residual_ld, z_ld, y_ld, dw_ld;
+  uint32_t* header;                     // workspace header (kLinearHeaderBytes), zero
+};
+constexpr size_t kLinearHeaderBytes = 256;
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream);
+// dbias[n] (+)= column sums of dz [m][n]
+cudaError_t launch_column_sums(const uint16_t* dz, int64_t ld, int64_t m, int64_t n, float* out, int accumulate,
+                               cudaStream_t stream);
+// dst rows (dst_ld elements apart) <- src rows, elements of `esize` bytes (1 or 2)
+cudaError_t launch_repack(const void* src, int64_t src_ld, void* dst, int64_t dst_ld, int64_t rows, int64_t cols,
+                          int esize, cudaStream_t stream);
+
+// Records the CUDA error's text for opt_last_cuda_error; returns OPT_ERR_CUDA's value.
+int record_cuda_error(cudaError_t e, const char* where);
+
 int num_sms();   // SM count of the current device (cached per device)
 
 // Launch instrumentation (opt_profile_launches).  A launch site calls

@@ -1,0 +1,283 @@
+"""Feed-forward operators of ``libmpopt.so``: the layers around the parameters.
+
+The bf16 model copies that the optimizer step writes are the weights here, and
+the fp32 ``main_grad`` buffers that it reads are the outputs:
+
+* ``rmsnorm``           -- h = x + residual, y = rmsnorm(h) * gamma in bf16
+  and / or in e4m3 with a scale per row
+* ``rmsnorm_backward``  -- its gradient; dgamma into fp32 main_grad
+* ``quantize_rows``     -- a matrix in e4m3 with a scale per row
+* ``linear``            -- y = act(x w^T + bias) + residual, bf16 or e4m3 operands
+* ``linear_backward``   -- dx, and dw and dbias into fp32 main_grad
+
+As in the rest of the package the caller owns every buffer: outputs are
+passed in and written in place, on the current CUDA stream or on ``stream``.
+Matrices are 2-D (or more leading dimensions that collapse into rows without a
+copy; a vector is one row) with contiguous rows that may be slices of wider
+ones.  ``include/mpopt.h`` defines every operator; arguments it refuses raise
+``MpoptError``, tensors of a wrong type, device or shape ``TypeError`` or
+``ValueError``.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import mixed_precision_optimizer_gb300 as mp
+
+_vp, _i32, _i64, _sz, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+
+DTYPE_FP32, DTYPE_BF16, DTYPE_E4M3 = 0, 1, 2
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+LINEAR_ANY_LAYOUT = 1
+LINEAR_HEADER_BYTES = 256
+
+
+class OptRmsnormArgs(ctypes.Structure):
+    _fields_ = [("x", _vp), ("residual", _vp), ("gamma", _vp), ("h", _vp), ("y", _vp), ("q", _vp), ("q_scale", _vp),
+                ("rstd", _vp), ("rows", _i64), ("cols", _i64), ("x_ld", _i64), ("residual_ld", _i64), ("h_ld", _i64),
+                ("y_ld", _i64), ("q_ld", _i64), ("dtype", _i32), ("gamma_dtype", _i32), ("eps", _f32),
+                ("reserved", _i32)]
+
+
+class OptRmsnormGradArgs(ctypes.Structure):
+    _fields_ = [("dy", _vp), ("h", _vp), ("gamma", _vp), ("rstd", _vp), ("dh", _vp), ("dx", _vp), ("dgamma", _vp),
+                ("rows", _i64), ("cols", _i64), ("dy_ld", _i64), ("h_ld", _i64), ("dh_ld", _i64), ("dx_ld", _i64),
+                ("dtype", _i32), ("gamma_dtype", _i32), ("accumulate", _i32), ("reserved", _i32)]
+
+
+class OptLinearArgs(ctypes.Structure):
+    _fields_ = [("x", _vp), ("w", _vp), ("x_scale", _vp), ("w_scale", _vp), ("bias", _vp), ("residual", _vp),
+                ("y", _vp), ("z", _vp), ("m", _i64), ("n", _i64), ("k", _i64), ("x_ld", _i64), ("w_ld", _i64),
+                ("residual_ld", _i64), ("y_ld", _i64), ("z_ld", _i64), ("dtype", _i32), ("bias_dtype", _i32),
+                ("act", _i32), ("reserved", _i32)]
+
+
+class OptLinearGradArgs(ctypes.Structure):
+    _fields_ = [("dz", _vp), ("x", _vp), ("w", _vp), ("z_prev", _vp), ("dx", _vp), ("dw", _vp), ("dbias", _vp),
+                ("m", _i64), ("n", _i64), ("k", _i64), ("dz_ld", _i64), ("x_ld", _i64), ("w_ld", _i64),
+                ("z_prev_ld", _i64), ("dx_ld", _i64), ("act_prev", _i32), ("accumulate", _i32)]
+
+
+def declare(L):
+    """Argument types of this module's entry points."""
+    P = ctypes.POINTER
+    for name, args, res in (
+            ("opt_rmsnorm_forward", [P(OptRmsnormArgs), _vp], ctypes.c_int),
+            ("opt_rmsnorm_backward", [P(OptRmsnormGradArgs), _vp, _sz, _vp], ctypes.c_int),
+            ("opt_rmsnorm_workspace_size", [_i64, _i64], _sz),
+            ("opt_quantize_rows", [_vp, _i64, _i32, _i64, _i64, _vp, _i64, _vp, _vp], ctypes.c_int),
+            ("opt_linear_forward", [P(OptLinearArgs), _vp, _sz, _vp], ctypes.c_int),
+            ("opt_linear_backward", [P(OptLinearGradArgs), _vp, _sz, _vp], ctypes.c_int),
+            ("opt_linear_workspace_size", [_i64, _i64, _i64, _i32], _sz)):
+        f = getattr(L, name)
+        f.argtypes, f.restype = args, res
+
+
+# --------------------------------------------------------------------------
+# marshalling
+# --------------------------------------------------------------------------
+
+_DTYPES = {}
+
+
+def _dtype_code(t, what, allowed):
+    import torch
+    if not _DTYPES:
+        _DTYPES.update({torch.float32: DTYPE_FP32, torch.bfloat16: DTYPE_BF16, torch.float8_e4m3fn: DTYPE_E4M3})
+    code = _DTYPES.get(t.dtype)
+    if code not in allowed:
+        raise TypeError(f"{what} has an unsupported type, {t.dtype}")
+    return code
+
+
+_FLOAT = (DTYPE_FP32, DTYPE_BF16)
+
+
+def _shape2(t, what):
+    """(rows, cols) of a matrix argument; leading dimensions are rows."""
+    d = t.dim()
+    if d == 2:
+        return t.shape
+    if d == 0:
+        raise ValueError(f"{what} must have at least one dimension")
+    rows = 1
+    for n in t.shape[:-1]:
+        rows *= n
+    return rows, t.shape[-1]
+
+
+def _mat(t, dtype, rows, cols, what):
+    """(pointer, distance between rows) of a matrix argument."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dim() != 2:
+        r, c = _shape2(t, what)
+        t = t.view(r, c)          # raises when the rows are not evenly spaced
+    if t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {(rows, cols)}")
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return t.data_ptr(), ld
+
+
+def _vec(t, dtype, n, what):
+    """Pointer of a dense vector argument."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous with {n} elements")
+    return t.data_ptr()
+
+
+def _workspace(ws):
+    if ws is None:
+        return None, 0
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+# --------------------------------------------------------------------------
+# RMS norm and 8-bit rows
+# --------------------------------------------------------------------------
+
+def rmsnorm(x, gamma, eps=1e-6, residual=None, h=None, y=None, q=None, q_scale=None, rstd=None, stream=None):
+    """h = x + residual (x and residual bf16 or fp32, h of their type);
+    y = h / sqrt(mean(h^2) + eps) * gamma per row, written as bf16 (y), as
+    e4m3 with fp32 row scales (q, q_scale), or both; rstd [rows] fp32 is what
+    rmsnorm_backward needs.  Outputs left out are not written.  h may be x or
+    residual itself."""
+    import torch
+    rows, cols = _shape2(x, "x")
+    code, gcode = _dtype_code(x, "x", _FLOAT), _dtype_code(gamma, "gamma", _FLOAT)
+    xp, xl = _mat(x, x.dtype, rows, cols, "x")
+    rp, rl = _mat(residual, x.dtype, rows, cols, "residual")
+    hp, hl = _mat(h, x.dtype, rows, cols, "h")
+    yp, yl = _mat(y, torch.bfloat16, rows, cols, "y")
+    qp, ql = _mat(q, torch.float8_e4m3fn, rows, cols, "q")
+    a = OptRmsnormArgs(xp, rp, _vec(gamma, gamma.dtype, cols, "gamma"), hp, yp, qp,
+                       _vec(q_scale, torch.float32, rows, "q_scale"), _vec(rstd, torch.float32, rows, "rstd"),
+                       rows, cols, xl, rl, hl, yl, ql, code, gcode, eps, 0)
+    mp._check(mp.lib().opt_rmsnorm_forward(ctypes.byref(a), mp._stream(stream)), "opt_rmsnorm_forward")
+
+
+def rmsnorm_backward(dy, h, gamma, rstd, dx, dh=None, dgamma=None, accumulate=True, workspace=None, stream=None):
+    """Gradient of rmsnorm at h (its output, or x without a residual): dy bf16;
+    dx (of h's type) is the gradient of x and of the residual, dh (optional)
+    the gradient reaching h past the norm; dgamma fp32 [cols] is added to, or
+    overwritten with accumulate=False, and needs rmsnorm_workspace(rows, cols)."""
+    import torch
+    rows, cols = _shape2(h, "h")
+    code, gcode = _dtype_code(h, "h", _FLOAT), _dtype_code(gamma, "gamma", _FLOAT)
+    yp, yl = _mat(dy, torch.bfloat16, rows, cols, "dy")
+    hp, hl = _mat(h, h.dtype, rows, cols, "h")
+    sp, sl = _mat(dh, h.dtype, rows, cols, "dh")
+    xp, xl = _mat(dx, h.dtype, rows, cols, "dx")
+    a = OptRmsnormGradArgs(yp, hp, _vec(gamma, gamma.dtype, cols, "gamma"), _vec(rstd, torch.float32, rows, "rstd"),
+                           sp, xp, _vec(dgamma, torch.float32, cols, "dgamma"), rows, cols, yl, hl, sl, xl, code,
+                           gcode, 1 if accumulate else 0, 0)
+    w, nb = _workspace(workspace)
+    mp._check(mp.lib().opt_rmsnorm_backward(ctypes.byref(a), w, nb, mp._stream(stream)), "opt_rmsnorm_backward")
+
+
+def rmsnorm_workspace_size(rows, cols) -> int:
+    return int(mp.lib().opt_rmsnorm_workspace_size(int(rows), int(cols)))
+
+
+def rmsnorm_workspace(rows, cols, device=None):
+    """Workspace of rmsnorm_backward for up to this many rows and columns."""
+    return mp.alloc_workspace(rmsnorm_workspace_size(rows, cols), device)
+
+
+def quantize_rows(x, q, scale, stream=None):
+    """q [rows][cols] (float8_e4m3fn), scale [rows] (fp32) <- x (bf16 or
+    fp32): x ~ q * scale with the largest magnitude of a row at 448."""
+    import torch
+    rows, cols = _shape2(x, "x")
+    code = _dtype_code(x, "x", _FLOAT)
+    xp, xl = _mat(x, x.dtype, rows, cols, "x")
+    qp, ql = _mat(q, torch.float8_e4m3fn, rows, cols, "q")
+    mp._check(mp.lib().opt_quantize_rows(xp, xl, code, rows, cols, qp, ql, _vec(scale, torch.float32, rows, "scale"),
+                                         mp._stream(stream)), "opt_quantize_rows")
+
+
+# --------------------------------------------------------------------------
+# linear layer
+# --------------------------------------------------------------------------
+
+def linear_workspace_size(m, n, k, any_layout=False) -> int:
+    """Workspace bytes of linear and linear_backward for x [m][k], w [n][k];
+    any_layout: also for operands whose rows do not start on 16 bytes although
+    dense ones of these sizes would."""
+    return int(mp.lib().opt_linear_workspace_size(int(m), int(n), int(k), LINEAR_ANY_LAYOUT if any_layout else 0))
+
+
+def linear_workspace(m, n, k, any_layout=False, device=None):
+    """A workspace of linear_workspace_size bytes with its header zeroed.  One
+    workspace serves any calls of these sizes or smaller, in stream order."""
+    ws = mp.alloc_workspace(linear_workspace_size(m, n, k, any_layout), device)
+    if ws is not None:
+        ws[:LINEAR_HEADER_BYTES].zero_()
+    return ws
+
+
+def linear(x, w, y, bias=None, act="none", residual=None, z=None, x_scale=None, w_scale=None, workspace=None,
+           stream=None):
+    """y [m][n] = act(x w^T + bias) + residual (bf16).  x [m][k] and w [n][k]
+    are bf16, or float8_e4m3fn with x_scale [m] and w_scale [n]; bias [n] is
+    bf16 or fp32; z [m][n] (bf16, optional) receives the pre-activation.  y may
+    be residual itself.  act: "none", "relu", "gelu" (tanh form), "silu"."""
+    import torch
+    m, k = _shape2(x, "x")
+    n = _shape2(w, "w")[0]
+    code = _dtype_code(x, "x", (DTYPE_BF16, DTYPE_E4M3))
+    if act not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {act!r}")
+    bf16, f32 = torch.bfloat16, torch.float32
+    xp, xl = _mat(x, x.dtype, m, k, "x")
+    wp, wl = _mat(w, x.dtype, n, k, "w")
+    rp, rl = _mat(residual, bf16, m, n, "residual")
+    yp, yl = _mat(y, bf16, m, n, "y")
+    zp, zl = _mat(z, bf16, m, n, "z")
+    bcode = _dtype_code(bias, "bias", _FLOAT) if bias is not None else DTYPE_BF16
+    a = OptLinearArgs(xp, wp, _vec(x_scale, f32, m, "x_scale"), _vec(w_scale, f32, n, "w_scale"),
+                      _vec(bias, bias.dtype, n, "bias") if bias is not None else None, rp, yp, zp, m, n, k, xl, wl, rl,
+                      yl, zl, code, bcode, ACTIVATIONS[act], 0)
+    ws, nb = _workspace(workspace)
+    mp._check(mp.lib().opt_linear_forward(ctypes.byref(a), ws, nb, mp._stream(stream)), "opt_linear_forward")
+
+
+def linear_backward(dz, x, w, dx=None, z_prev=None, act_prev="none", dw=None, dbias=None, accumulate=True,
+                    workspace=None, stream=None):
+    """Gradients of z = x w^T + bias for dz [m][n] (bf16): dx [m][k] bf16 =
+    (dz w) * act_prev'(z_prev) (without z_prev: dz w); dw [n][k] and dbias [n]
+    fp32 main_grad buffers, added to or overwritten (accumulate=False).
+    Outputs left out are not computed; x and w may be None when only the other
+    one's product is asked for."""
+    import torch
+    m, n = _shape2(dz, "dz")
+    if x is None and w is None and dbias is None:
+        raise ValueError("linear_backward: nothing to compute")
+    k = _shape2(x, "x")[1] if x is not None else _shape2(w, "w")[1] if w is not None else 1
+    if act_prev not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {act_prev!r}")
+    bf16, f32 = torch.bfloat16, torch.float32
+    zp, zl = _mat(dz, bf16, m, n, "dz")
+    xp, xl = _mat(x, bf16, m, k, "x")
+    wp, wl = _mat(w, bf16, n, k, "w")
+    pp, pl = _mat(z_prev, bf16, m, k, "z_prev")
+    dp, dl = _mat(dx, bf16, m, k, "dx")
+    if dw is not None and tuple(dw.shape) != (n, k):
+        raise ValueError(f"dw has shape {tuple(dw.shape)}, expected {(n, k)}")
+    a = OptLinearGradArgs(zp, xp, wp, pp, dp, _vec(dw, f32, n * k, "dw"), _vec(dbias, f32, n, "dbias"), m, n, k, zl,
+                          xl, wl, pl, dl, ACTIVATIONS[act_prev], 1 if accumulate else 0)
+    ws, nb = _workspace(workspace)
+    mp._check(mp.lib().opt_linear_backward(ctypes.byref(a), ws, nb, mp._stream(stream)), "opt_linear_backward")

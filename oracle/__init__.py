@@ -25,9 +25,14 @@ the pages by eye.
   Source: "02 · Optimizer：算法与 infra" §11.1 (definition) and §11.4 (one
   global norm shared by the Muon and AdamW groups).
 
-Every function is pinned by a CPU test in ``tests/test_oracle_pins.py``
+* ``feedforward`` -- RMS norm with the residual's addition, e4m3 rows, the
+  linear layer and their gradients, fp64; pinned in
+  ``tests/test_feedforward_host.py`` by central differences and by torch's
+  e4m3 conversion.
+
+Every other function is pinned by a CPU test in ``tests/test_oracle_pins.py``
 against values the pages print, closed forms, or library routines.  No
 function here is "parity unpinned".
 """
 
-from . import adamw, clip, muon  # noqa: F401
+from . import adamw, clip, feedforward, muon  # noqa: F401
