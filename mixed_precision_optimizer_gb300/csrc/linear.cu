@@ -12,9 +12,11 @@
 // [k][index] (w in dx, both operands of dw) MN-major: no transposed copy is
 // made.
 //
-// One CTA per 128 x 128 tile: warp 0 loads k-blocks of 128 bytes by TMA into a
-// ring, warp 1 issues the MMAs, warps 2-5 run the epilogue.  Out-of-range rows
-// and columns are filled with zeros by the TMA and never stored.
+// linear_pair_kernel takes large products (below).  linear_kernel takes the
+// others, one CTA per 128 x 128 tile: warp 0 loads k-blocks of 128 bytes by
+// TMA into a ring, warp 1 issues the MMAs, warps 2-5 run the epilogue.
+// Out-of-range rows and columns are filled with zeros by the TMA and never
+// stored.
 
 #include <cuda_bf16.h>
 
@@ -130,51 +132,87 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
 
 // -------------------------------------------------------------- epilogue --
 
-// Column j of the tile is output row b0 + j; this lane is output column `a`.
-template <bool kFp8>
-__device__ __forceinline__ void epilogue_columns(const LinearArgs& g, int64_t a, int64_t b0, const float (&v)[32]) {
-  if (a >= g.na) return;
-  const int n = static_cast<int>(g.nb - b0 < 32 ? g.nb - b0 : 32);
-  if (g.mode == kLinearDw) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < n) {
-        float* p = g.dw + (b0 + j) * g.dw_ld + a;
-        *p = g.accumulate ? *p + v[j] : v[j];
-      }
-    return;
+// What the epilogue needs of this lane's output column `a` throughout a tile.
+struct LaneColumn {
+  int64_t a;
+  float scale, bias;
+};
+
+template <int kMode, bool kFp8>
+__device__ __forceinline__ LaneColumn lane_column(const LinearArgs& g, int64_t a) {
+  LaneColumn c{a, 1.f, 0.f};
+  if (kMode == kLinearForward && a < g.na) {
+    if (kFp8) c.scale = g.a_scale[a];
+    if (g.bias)
+      c.bias = g.bias_dtype == kBf16 ? bf16_at(static_cast<const uint16_t*>(g.bias), a)
+                                     : static_cast<const float*>(g.bias)[a];
   }
-  if (g.mode == kLinearDx) {
+  return c;
+}
+
+// kN accumulator columns: column j is output row b0 + j, this lane output
+// column c.a; a warp's accesses of one column are contiguous.
+template <int kMode, bool kFp8, int kN>
+__device__ __forceinline__ void epilogue_columns(const LinearArgs& g, const LaneColumn& c, int64_t b0,
+                                                 const float* v) {
+  if (c.a >= g.na) return;
+  const int n = static_cast<int>(g.nb - b0 < kN ? g.nb - b0 : kN);
+  if constexpr (kMode == kLinearDw) {
+    float* p = g.dw + b0 * g.dw_ld + c.a;
+    float old[kN];
+    if (g.accumulate) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
+      for (int j = 0; j < kN; ++j)
+        if (j < n) old[j] = __ldcs(p + j * g.dw_ld);
+    }
+#pragma unroll
+    for (int j = 0; j < kN; ++j)
+      if (j < n) __stcs(p + j * g.dw_ld, g.accumulate ? old[j] + v[j] : v[j]);
+  } else if constexpr (kMode == kLinearDx) {
+    uint16_t zr[kN];
+    if (g.z_in) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j)
+        if (j < n) zr[j] = __ldcs(g.z_in + (b0 + j) * g.z_ld + c.a);
+    }
+#pragma unroll
+    for (int j = 0; j < kN; ++j)
       if (j < n) {
         float d = v[j];
-        if (g.z_in) d *= activate_grad(bf16_at(g.z_in, (b0 + j) * g.z_ld + a), g.act);
-        g.y[(b0 + j) * g.y_ld + a] = to_bf16(d);
+        if (g.z_in) d *= activate_grad(__uint_as_float(static_cast<uint32_t>(zr[j]) << 16), g.act);
+        g.y[(b0 + j) * g.y_ld + c.a] = to_bf16(d);
       }
-    return;
-  }
-  const float wscale = kFp8 ? g.a_scale[a] : 1.f;
-  float bias = 0.f;
-  if (g.bias)
-    bias = g.bias_dtype == kBf16 ? bf16_at(static_cast<const uint16_t*>(g.bias), a)
-                                 : static_cast<const float*>(g.bias)[a];
+  } else {
+    uint16_t rr[kN];
+    if (g.residual) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (j < n) {
-      float z = v[j];
-      if (kFp8) z *= wscale * g.b_scale[b0 + j];
-      z += bias;
-      if (g.z_out) g.z_out[(b0 + j) * g.z_ld + a] = to_bf16(z);
-      float y = activate(z, g.act);
-      if (g.residual) y += bf16_at(g.residual, (b0 + j) * g.residual_ld + a);
-      g.y[(b0 + j) * g.y_ld + a] = to_bf16(y);
+      for (int j = 0; j < kN; ++j)
+        if (j < n) rr[j] = g.residual[(b0 + j) * g.residual_ld + c.a];
     }
+#pragma unroll
+    for (int j = 0; j < kN; ++j)
+      if (j < n) {
+        float z = v[j];
+        if (kFp8) z *= c.scale * g.b_scale[b0 + j];
+        z += c.bias;
+        if (g.z_out) __stcs(g.z_out + (b0 + j) * g.z_ld + c.a, to_bf16(z));
+        float y = activate(z, g.act);
+        if (g.residual) y += __uint_as_float(static_cast<uint32_t>(rr[j]) << 16);
+        g.y[(b0 + j) * g.y_ld + c.a] = to_bf16(y);
+      }
+  }
 }
+
+// The operands' orders by product: forward K-major both, dx A MN-major, dw both.
+template <int kMode>
+struct Order {
+  static constexpr bool a_mn = kMode != kLinearForward;
+  static constexpr bool b_mn = kMode == kLinearDw;
+};
 
 // ---------------------------------------------------------------- kernel --
 
-template <bool kFp8>
+template <int kMode, bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
               const __grid_constant__ LinearParams P) {
@@ -188,7 +226,7 @@ linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* status = P.g.header;
   constexpr int kElems = kFp8 ? 128 : 64;
-  const bool a_mn = P.g.A.mn_major != 0, b_mn = P.g.B.mn_major != 0;
+  constexpr bool a_mn = Order<kMode>::a_mn, b_mn = Order<kMode>::b_mn;
   const int64_t a0 = static_cast<int64_t>(blockIdx.x % P.tiles_a) * BM;
   const int64_t b0 = static_cast<int64_t>(blockIdx.x / P.tiles_a) * BN;
 
@@ -273,10 +311,11 @@ linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
     const bool ready = mbar_wait(acc_bar, 0, abort_flag, status, kStatusTimeoutAcc) && !*abort_flag;
     if (__all_sync(0xffffffffu, ready)) {
       tc_fence_after();
+      const LaneColumn col = lane_column<kMode, kFp8>(P.g, a0 + quarter * 32 + lane);
       for (int c = 0; c < BN && b0 + c < P.g.nb; c += 32) {
         float v[32];
         tmem_ld32(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + c, v);
-        epilogue_columns<kFp8>(P.g, a0 + quarter * 32 + lane, b0 + c, v);
+        epilogue_columns<kMode, kFp8, 32>(P.g, col, b0 + c, v);
       }
     }
   }
@@ -285,6 +324,351 @@ linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
+  }
+}
+
+// ----------------------------------------------------------- pair kernel --
+//
+// Large products: CTA pairs, persistent over 256 x 256 tiles with
+// cta_group::2 MMAs, the structure of the Newton-Schulz GEMMs.  Each CTA
+// stages its 128 A indices and 128 of the tile's 256 B indices (32 KB per
+// 128-byte k-block, where two separate 128 x 256 tiles would stage 96 KB
+// between them) and receives the accumulators of its own 128 A indices.  Two
+// accumulators of 256 columns let the epilogue of one tile overlap the main
+// loop of the next.
+//   warp 0      TMA producer (both CTAs; bytes counted on the even CTA's barrier)
+//   warp 1      TMEM allocation; in the even CTA the MMA issuer
+//   warps 2-9   epilogue: two warps per TMEM lane quarter, 128 columns each
+//   warp 10     even CTA: claims tiles from a launch-wide counter and publishes
+//               them to both CTAs, so the tiles in flight stay neighbours that
+//               share operand panels in L2
+//
+// dw sums over the tokens, and the tensor cores truncate each addition to the
+// accumulator: a sum of m tokens comes out low by about m 2^-30 of its value
+// (1.6e-5 at 16384).  So dw runs in segments of kDwSegment k-blocks (512
+// tokens, 5e-7): the epilogue adds each segment's accumulator to registers
+// with rounding additions while the MMAs of the next segment run into the
+// other accumulator.
+
+constexpr int kPairStages = 7;
+constexpr int kPairBN = 256;
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairThreads = 96 + 32 * kPairEpiWarps;
+constexpr int kPairTmemCols = 512;
+constexpr int kDwSegment = 8;
+constexpr int kTileSlots = 3;
+constexpr uint32_t kTileConsumers = 2 + 1 + 2 * kPairEpiWarps;
+constexpr int kPairBarrierBytes = (2 * kPairStages + 5 + 2 * kTileSlots) * 8 + 8 + 4 * kTileSlots;
+static_assert(kPairBarrierBytes <= 256, "barrier block larger than its 256-byte reservation");
+constexpr uint32_t kPairSmemBytes = kPairStages * kStageBytes + 1024 /*align*/ + 256 /*barriers*/;
+static_assert(kPairSmemBytes <= 232448, "dynamic shared memory above the 227 KB a CTA may use");
+
+struct PairParams {
+  LinearArgs g;
+  int k_blocks;
+  int segment;         // k-blocks accumulated in TMEM at a time
+  int tiles_a, tiles_b, total_tiles;
+};
+
+// Tiles in groups of kGroupB tiles along b, a-major inside a group: about 76
+// tiles are in flight, a block of 8 x 9.5 tiles that shares its panels.
+constexpr int kGroupB = 8;
+
+__device__ __forceinline__ void pair_tile(const PairParams& P, int tile, int& ta, int& tb) {
+  const int per_group = kGroupB * P.tiles_a;
+  const int grp = tile / per_group, r = tile - grp * per_group;
+  const int width = min(kGroupB, P.tiles_b - grp * kGroupB);
+  ta = r / width;
+  tb = grp * kGroupB + (r - ta * width);
+}
+
+template <bool kFp8>
+__device__ __forceinline__ void mma_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  if constexpr (kFp8)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    mma(tmem_d, adesc, bdesc, idesc, accumulate);
+}
+
+// A box of a 2-D map into this CTA's shared memory, completing on `bar`, a
+// shared::cluster address that may be the even CTA's barrier.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+template <int kMode, bool kFp8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                   const __grid_constant__ PairParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairStages * kStageBytes);   // even CTA: both CTAs' copies landed
+  uint64_t* empty = full + kPairStages;            // both CTAs: stage free again
+  uint64_t* acc_full = empty + kPairStages;        // [2] both CTAs: accumulator ready
+  uint64_t* acc_empty = acc_full + 2;              // [2] even CTA: both epilogues have read it
+  uint64_t* drain = acc_empty + 2;                 // even CTA: all MMAs complete
+  uint64_t* tile_full = drain + 1;                 // [kTileSlots] both CTAs: next tile published
+  uint64_t* tile_empty = tile_full + kTileSlots;   // [kTileSlots] even CTA: every role has read it
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tile_empty + kTileSlots);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  volatile int* tile_ring = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [kTileSlots]
+
+  constexpr int kElems = kFp8 ? 128 : 64;
+  constexpr bool a_mn = Order<kMode>::a_mn, b_mn = Order<kMode>::b_mn;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  uint32_t* status = P.g.header;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&acc_full[a]), 1);
+      mbar_init(smem_u32(&acc_empty[a]), 2 * 32 * kPairEpiWarps);
+    }
+    mbar_init(smem_u32(drain), 1);
+    for (int k = 0; k < kTileSlots; ++k) {
+      mbar_init(smem_u32(&tile_full[k]), 1);
+      mbar_init(smem_u32(&tile_empty[k]), kTileConsumers);
+    }
+    *abort_flag = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(kPairTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  cluster_sync();            // barriers of both CTAs initialised, TMEM allocated in both
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      bool ok = true, issued = false;
+      const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+      const uint32_t full0_even = peer_addr(full0, 0);
+      const uint32_t sa0 = smem_u32(smem), sb0 = sa0 + kPairStages * kStageA;
+      const uint32_t tempty_even = peer_addr(smem_u32(&tile_empty[0]), 0);
+      uint32_t s = 0, ph = 0;
+      for (uint32_t seq = 0; ok; ++seq) {
+        const uint32_t slot = seq % kTileSlots, sph = (seq / kTileSlots) & 1u;
+        if (!(rank == 0 ? mbar_wait(smem_u32(&tile_full[slot]), sph, abort_flag, status, kStatusTimeoutTile)
+                        : mbar_wait_acq_cluster(smem_u32(&tile_full[slot]), sph, abort_flag, status,
+                                                kStatusTimeoutTile))) {
+          ok = false;
+          break;
+        }
+        const int tile = tile_ring[slot];
+        if (rank == 0) mbar_arrive_local(smem_u32(&tile_empty[slot]));
+        else mbar_arrive_remote(tempty_even + 8 * slot);
+        if (tile >= P.total_tiles) break;
+        int ta, tb;
+        pair_tile(P, tile, ta, tb);
+        const int ai = ta * 256 + static_cast<int>(rank) * BM, bi = tb * kPairBN + static_cast<int>(rank) * BN;
+        for (int kb = 0; kb < P.k_blocks; ++kb) {
+          if (!mbar_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, status, kStatusTimeoutEmpty)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = full0_even + 8 * s;
+          if (rank == 0) mbar_expect_tx(full0 + 8 * s, 2 * kStageBytes);
+          const uint32_t sa = sa0 + s * kStageA, sb = sb0 + s * kStageB;
+          if constexpr (a_mn) {
+            tma_load_2d_pair(sa, &map_a, fb, ai, kb * kElems);
+            tma_load_2d_pair(sa + kMnBlockBytes, &map_a, fb, ai + 64, kb * kElems);
+          } else {
+            tma_load_2d_pair(sa, &map_a, fb, kb * kElems, ai);
+          }
+          if constexpr (b_mn) {
+            tma_load_2d_pair(sb, &map_b, fb, bi, kb * kElems);
+            tma_load_2d_pair(sb + kMnBlockBytes, &map_b, fb, bi + 64, kb * kElems);
+          } else {
+            tma_load_2d_pair(sb, &map_b, fb, kb * kElems, bi);
+          }
+          issued = true;
+          if (++s == kPairStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (!ok && issued) {
+        // aborting: give copies in flight time to land before the CTA exits
+        const unsigned long long t0 = global_ns();
+        while (global_ns() - t0 < 10000000ull) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = linear_idesc(kFp8, a_mn, b_mn, 256, kPairBN);
+      const uint32_t sa0 = smem_u32(smem), sb0 = sa0 + kPairStages * kStageA;
+      const uint64_t ad0 = a_mn ? smem_desc_mn(sa0) : smem_desc(sa0);
+      const uint64_t bd0 = b_mn ? smem_desc_mn(sb0) : smem_desc(sb0);
+      constexpr uint32_t ka = (a_mn ? 16 * kRowBytes : 32) >> 4, kbs = (b_mn ? 16 * kRowBytes : 32) >> 4;
+      const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+      uint32_t s = 0, ph = 0, use = 0;          // use: accumulator uses so far
+      bool ok = true;
+      for (uint32_t lt = 0; ok; ++lt) {
+        const uint32_t slot = lt % kTileSlots, sph = (lt / kTileSlots) & 1u;
+        if (!mbar_wait(smem_u32(&tile_full[slot]), sph, abort_flag, status, kStatusTimeoutTile)) break;
+        const int tile = tile_ring[slot];
+        mbar_arrive_local(smem_u32(&tile_empty[slot]));
+        if (tile >= P.total_tiles) break;
+        for (int k0 = 0; ok && k0 < P.k_blocks; k0 += P.segment, ++use) {
+          const uint32_t acc = use & 1;
+          if (!mbar_wait(smem_u32(&acc_empty[acc]), ((use >> 1) & 1u) ^ 1u, abort_flag, status,
+                         kStatusTimeoutAccFree)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + acc * kPairBN;
+          const int k1 = min(k0 + P.segment, P.k_blocks);
+          for (int kb = k0; kb < k1; ++kb) {
+            if (!mbar_wait(full0 + 8 * s, ph, abort_flag, status, kStatusTimeoutFull)) {
+              ok = false;
+              break;
+            }
+            const uint64_t ad = ad0 + s * (kStageA >> 4), bd = bd0 + s * (kStageB >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_pair<kFp8>(d_tmem, ad + ka * kk, bd + kbs * kk, idesc, (kb > k0 || kk > 0) ? 1u : 0u);
+            mma_commit_pair(empty0 + 8 * s);
+            if (++s == kPairStages) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+          if (ok) mma_commit_pair(smem_u32(&acc_full[acc]));
+        }
+      }
+      // every MMA issued by this thread has completed before TMEM goes
+      mma_commit_local(smem_u32(drain));
+      const unsigned long long t0 = global_ns();
+      while (!mbar_try(smem_u32(drain), 0)) {
+        if (global_ns() - t0 > kWaitLimitNs) {
+          *abort_flag = 1u;
+          atomicCAS(status, 0u, static_cast<uint32_t>(kStatusTimeoutDrain));
+          break;
+        }
+      }
+    }
+  } else if (warp < 2 + kPairEpiWarps) {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t empty_even = peer_addr(smem_u32(&acc_empty[0]), 0);
+    const uint32_t tempty_even = peer_addr(smem_u32(&tile_empty[0]), 0);
+    uint32_t use = 0;
+    bool ok = true;
+    for (uint32_t lt = 0; ok; ++lt) {
+      const uint32_t slot = lt % kTileSlots, sph = (lt / kTileSlots) & 1u;
+      int tile = 0, got = 1;
+      if (lane == 0) {
+        got = (rank == 0 ? mbar_wait(smem_u32(&tile_full[slot]), sph, abort_flag, status, kStatusTimeoutTile)
+                         : mbar_wait_acq_cluster(smem_u32(&tile_full[slot]), sph, abort_flag, status,
+                                                 kStatusTimeoutTile))
+                  ? 1
+                  : 0;
+        if (got) {
+          tile = tile_ring[slot];
+          if (rank == 0) mbar_arrive_local(smem_u32(&tile_empty[slot]));
+          else mbar_arrive_remote(tempty_even + 8 * slot);
+        }
+      }
+      got = __shfl_sync(0xffffffffu, got, 0);
+      tile = __shfl_sync(0xffffffffu, tile, 0);
+      if (!got || tile >= P.total_tiles) break;
+      int ta, tb;
+      pair_tile(P, tile, ta, tb);
+      const LaneColumn col = lane_column<kMode, kFp8>(
+          P.g, static_cast<int64_t>(ta) * 256 + rank * BM + quarter * 32 + lane);
+      const int64_t b0 = static_cast<int64_t>(tb) * kPairBN + half * 128;
+      const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
+      if constexpr (kMode == kLinearDw) {
+        float sum[128];
+#pragma unroll
+        for (int c = 0; c < 128; ++c) sum[c] = 0.f;
+        for (int k0 = 0; k0 < P.k_blocks; k0 += P.segment, ++use) {
+          const uint32_t acc = use & 1;
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(smem_u32(&acc_full[acc]), (use >> 1) & 1u, abort_flag, status, kStatusTimeoutAcc));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 128; c += 16) {
+            float v[16];
+            tmem_ld16(lane_addr + acc * kPairBN + c, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[c + j] += v[j];
+          }
+          tc_fence_before();
+          mbar_arrive_remote(empty_even + acc * 8);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < 128; c += 8)
+          if (b0 + c < P.g.nb) epilogue_columns<kMode, kFp8, 8>(P.g, col, b0 + c, sum + c);
+      } else {
+        const uint32_t acc = use & 1;
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait(smem_u32(&acc_full[acc]), (use >> 1) & 1u, abort_flag, status, kStatusTimeoutAcc));
+        if (!ok) break;
+        ++use;
+        tc_fence_after();
+        for (int c = 0; c < 128 && b0 + c < P.g.nb; c += 32) {
+          float v[32];
+          tmem_ld32(lane_addr + acc * kPairBN + c, v);
+          epilogue_columns<kMode, kFp8, 32>(P.g, col, b0 + c, v);
+        }
+        tc_fence_before();
+        mbar_arrive_remote(empty_even + acc * 8);
+      }
+    }
+  } else if (lane == 0 && rank == 0) {
+    const uint32_t ring_odd = peer_addr(smem_u32(const_cast<int*>(tile_ring)), 1);
+    const uint32_t tfull_odd = peer_addr(smem_u32(&tile_full[0]), 1);
+    for (uint32_t seq = 0;; ++seq) {
+      const uint32_t slot = seq % kTileSlots, sph = (seq / kTileSlots) & 1u;
+      if (!mbar_wait(smem_u32(&tile_empty[slot]), sph ^ 1u, abort_flag, status, kStatusTimeoutTile)) break;
+      const int tile = seq == 0 ? pair : npairs + static_cast<int>(atomicAdd(status + kSchedWord, 1u));
+      tile_ring[slot] = tile;
+      st_cluster_u32(ring_odd + 4 * slot, static_cast<uint32_t>(tile));
+      mbar_arrive_local(smem_u32(&tile_full[slot]));
+      mbar_arrive_remote(tfull_odd + 8 * slot);
+      if (tile >= P.total_tiles) break;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();            // no CTA leaves while its partner may still signal it
+  if (threadIdx.x == 0) {
+    // the last CTA to finish (every claim is made by then) leaves the header zero
+    __threadfence();
+    if (atomicAdd(status + kSchedWord + 1, 1u) == gridDim.x - 1) {
+      atomicExch(status + kSchedWord, 0u);
+      atomicExch(status + kSchedWord + 1, 0u);
+    }
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kPairTmemCols)
+                 : "memory");
   }
 }
 
@@ -337,13 +721,49 @@ cudaError_t make_operand_map(CUtensorMap* map, const LinearOperand& o, int64_t n
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <bool kFp8>
-cudaError_t launch_typed(const CUtensorMap& ma, const CUtensorMap& mb, const LinearParams& P, int64_t grid,
-                         cudaStream_t stream) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(linear_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e != cudaSuccess) return e;
-  linear_kernel<kFp8><<<static_cast<unsigned>(grid), kThreads, kSmemBytes, stream>>>(ma, mb, P);
+// Raises a kernel's shared-memory limit once per thread and device.
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+  static thread_local int configured_dev = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev == configured_dev) return e;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) configured_dev = dev;
+  return e;
+}
+
+template <int kMode, bool kFp8>
+cudaError_t launch_product(const LinearArgs& a, cudaStream_t stream) {
+  constexpr int kElems = kFp8 ? 128 : 64;
+  const int k_blocks = static_cast<int>((a.nk + kElems - 1) / kElems);
+  CUtensorMap ma, mb;
+  cudaError_t e;
+  if ((e = make_operand_map(&ma, a.A, a.na, a.nk, kFp8, BM)) != cudaSuccess) return e;
+  if ((e = make_operand_map(&mb, a.B, a.nb, a.nk, kFp8, BN)) != cudaSuccess) return e;
+  const int64_t pair_a = (a.na + 255) / 256, pair_b = (a.nb + kPairBN - 1) / kPairBN;
+  const int max_pairs = num_sms() / 2;
+  if (pair_a * pair_b >= max_pairs && pair_a * pair_b < (int64_t(1) << 30)) {
+    PairParams P{};
+    P.g = a;
+    P.k_blocks = k_blocks;
+    P.segment = kMode == kLinearDw ? kDwSegment : k_blocks;
+    P.tiles_a = static_cast<int>(pair_a);
+    P.tiles_b = static_cast<int>(pair_b);
+    P.total_tiles = static_cast<int>(pair_a * pair_b);
+    if ((e = allow_smem<linear_pair_kernel<kMode, kFp8>>(kPairSmemBytes)) != cudaSuccess) return e;
+    const int grid = 2 * (P.total_tiles < max_pairs ? P.total_tiles : max_pairs);
+    linear_pair_kernel<kMode, kFp8><<<grid, kPairThreads, kPairSmemBytes, stream>>>(ma, mb, P);
+    return cudaGetLastError();
+  }
+  LinearParams P{};
+  P.g = a;
+  P.k_blocks = k_blocks;
+  P.tiles_a = (a.na + BM - 1) / BM;
+  const int64_t grid = P.tiles_a * ((a.nb + BN - 1) / BN);
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  if ((e = allow_smem<linear_kernel<kMode, kFp8>>(kSmemBytes)) != cudaSuccess) return e;
+  linear_kernel<kMode, kFp8><<<static_cast<unsigned>(grid), kThreads, kSmemBytes, stream>>>(ma, mb, P);
   return cudaGetLastError();
 }
 
@@ -351,18 +771,9 @@ cudaError_t launch_typed(const CUtensorMap& ma, const CUtensorMap& mb, const Lin
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
   if (a.na <= 0 || a.nb <= 0) return cudaSuccess;
-  LinearParams P{};
-  P.g = a;
-  const int elems = a.fp8 ? 128 : 64;
-  P.k_blocks = static_cast<int>((a.nk + elems - 1) / elems);
-  P.tiles_a = (a.na + BM - 1) / BM;
-  const int64_t grid = P.tiles_a * ((a.nb + BN - 1) / BN);
-  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  CUtensorMap ma, mb;
-  cudaError_t e;
-  if ((e = make_operand_map(&ma, a.A, a.na, a.nk, a.fp8 != 0, BM)) != cudaSuccess) return e;
-  if ((e = make_operand_map(&mb, a.B, a.nb, a.nk, a.fp8 != 0, BN)) != cudaSuccess) return e;
-  return a.fp8 ? launch_typed<true>(ma, mb, P, grid, stream) : launch_typed<false>(ma, mb, P, grid, stream);
+  if (a.mode == kLinearDx) return launch_product<kLinearDx, false>(a, stream);
+  if (a.mode == kLinearDw) return launch_product<kLinearDw, false>(a, stream);
+  return a.fp8 ? launch_product<kLinearForward, true>(a, stream) : launch_product<kLinearForward, false>(a, stream);
 }
 
 cudaError_t launch_column_sums(const uint16_t* dz, int64_t ld, int64_t m, int64_t n, float* out, int accumulate,

@@ -240,6 +240,28 @@ def linear_case(m, n, k, e4m3, layout, seed=0):
 @pytest.mark.parametrize("layout", ["dense", "aligned slice", "odd slice"])
 @pytest.mark.parametrize("kind", ["none", "relu", "gelu", "silu"])
 def test_linear(m, n, k, e4m3, layout, kind):
+    check_linear(m, n, k, e4m3, layout, kind)
+
+
+# at least 76 tiles of 256 x 256 for one of the three products: the persistent
+# kernel, with ragged last tiles, several tiles per CTA pair and few or many k-blocks
+LARGE_SHAPES = [(2100, 2300, 100), (2100, 100, 2300), (100, 2300, 2100), (4096, 2560, 264), (2305, 2311, 2333)]
+
+
+@pytest.mark.parametrize("m,n,k", LARGE_SHAPES)
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("kind,layout", [("silu", "dense"), ("gelu", "aligned slice"), ("relu", "odd slice")])
+def test_linear_large(m, n, k, e4m3, layout, kind):
+    check_linear(m, n, k, e4m3, layout, kind)
+
+
+@pytest.mark.parametrize("m,n,k", LARGE_SHAPES)
+@pytest.mark.parametrize("kind,layout", [("silu", "dense"), ("none", "aligned slice"), ("gelu", "odd slice")])
+def test_linear_backward_large(m, n, k, layout, kind):
+    check_linear_backward(m, n, k, layout, kind)
+
+
+def check_linear(m, n, k, e4m3, layout, kind):
     x, w, xs, wsc = linear_case(m, n, k, e4m3, layout)
     bias = normal(3, (n,), torch.bfloat16 if kind == "relu" else torch.float32) if kind != "gelu" else None
     pad = 0 if layout == "dense" else 3
@@ -274,6 +296,10 @@ def test_linear(m, n, k, e4m3, layout, kind):
 @pytest.mark.parametrize("layout", ["dense", "aligned slice", "odd slice"])
 @pytest.mark.parametrize("kind", ["none", "relu", "gelu", "silu"])
 def test_linear_backward(m, n, k, layout, kind):
+    check_linear_backward(m, n, k, layout, kind)
+
+
+def check_linear_backward(m, n, k, layout, kind):
     pad, off = {"dense": (0, 0), "aligned slice": (24, 8), "odd slice": (5, 3)}[layout]
     dz, x = normal(1, (m, n), pad=pad, off=off), normal(2, (m, k), pad=pad, off=off)
     w = normal(3, (n, k), std=0.1, pad=pad, off=off)
