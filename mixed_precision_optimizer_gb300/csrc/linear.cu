@@ -5,16 +5,15 @@
 //   dw        dz^T x (+ main_grad)                    bf16 operands, fp32 result
 //
 // All three are out[b][a] = sum_k A[a][k] B[b][k], where `a` is the index that
-// is contiguous in the output: a TMEM lane is an `a` and a TMEM column a `b`,
-// so a warp's loads and stores of one column are contiguous whatever the
-// output's row distance and alignment, and the bias and the weight scale of a
-// lane are one register.  An operand stored [index][k] is K-major, one stored
-// [k][index] (w in dx, both operands of dw) MN-major: no transposed copy is
-// made.
+// is contiguous in the output.  An operand stored [index][k] is K-major, one
+// stored [k][index] (w in dx, both operands of dw) MN-major: no transposed
+// copy is made.
 //
 // linear_pair_kernel takes large products (below).  linear_kernel takes the
 // others, one CTA per 128 x 128 tile: warp 0 loads k-blocks of 128 bytes by
-// TMA into a ring, warp 1 issues the MMAs, warps 2-5 run the epilogue.
+// TMA into a ring, warp 1 issues the MMAs, warps 2-5 run the epilogue, with
+// the lanes on `a`: a warp's accesses of one row are contiguous whatever the
+// row distance and alignment.
 // Out-of-range rows and columns are filled with zeros by the TMA and never
 // stored.
 
@@ -49,29 +48,50 @@ struct LinearParams {
 
 // sqrt(2/pi) and the cubic's coefficient of the tanh form of GELU; with
 // (1 + tanh u) / 2 = sigmoid(2 u) both activations are u * sigmoid(t(u)).
-__device__ __forceinline__ float sigmoid(float t) { return 1.f / (1.f + __expf(-t)); }
+// __expf and __fdividef are within 2 units plus 2^-23 |t| of the value, far
+// below the bf16 rounding that follows.
+__device__ __forceinline__ float sigmoid(float t) { return __fdividef(1.f, 1.f + __expf(-t)); }
 
 constexpr float kGelu2 = 1.5957691216057308f;   // 2 sqrt(2/pi)
 constexpr float kGeluCubic = 0.044715f;
 
-__device__ __forceinline__ float activate(float z, int act) {
-  if (act == OPT_ACT_RELU) return z > 0.f || z != z ? z : 0.f;
-  if (act == OPT_ACT_GELU) return z * sigmoid(kGelu2 * (z + kGeluCubic * z * z * z));
-  if (act == OPT_ACT_SILU) return z * sigmoid(z);
+template <int kAct>
+__device__ __forceinline__ float activate(float z) {
+  if constexpr (kAct == OPT_ACT_RELU) return z > 0.f || z != z ? z : 0.f;
+  if constexpr (kAct == OPT_ACT_GELU) return z * sigmoid(kGelu2 * (z + kGeluCubic * z * z * z));
+  if constexpr (kAct == OPT_ACT_SILU) return z * sigmoid(z);
   return z;
 }
 
-__device__ __forceinline__ float activate_grad(float z, int act) {
-  if (act == OPT_ACT_RELU) return z > 0.f ? 1.f : 0.f;
-  if (act == OPT_ACT_GELU) {
+template <int kAct>
+__device__ __forceinline__ float activate_grad(float z) {
+  if constexpr (kAct == OPT_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+  if constexpr (kAct == OPT_ACT_GELU) {
     const float p = sigmoid(kGelu2 * (z + kGeluCubic * z * z * z));
     return p + z * p * (1.f - p) * (kGelu2 * (1.f + 3.f * kGeluCubic * z * z));
   }
-  if (act == OPT_ACT_SILU) {
+  if constexpr (kAct == OPT_ACT_SILU) {
     const float p = sigmoid(z);
     return p + z * p * (1.f - p);
   }
   return 1.f;
+}
+
+template <int kAct>
+struct ActTag {
+  static constexpr int value = kAct;
+};
+
+// Calls f with the activation as a compile-time tag: one branch for a block
+// of elements instead of one for each.
+template <typename F>
+__device__ __forceinline__ void with_activation(int act, F&& f) {
+  switch (act) {
+    case OPT_ACT_RELU: f(ActTag<OPT_ACT_RELU>{}); break;
+    case OPT_ACT_GELU: f(ActTag<OPT_ACT_GELU>{}); break;
+    case OPT_ACT_SILU: f(ActTag<OPT_ACT_SILU>{}); break;
+    default: f(ActTag<OPT_ACT_NONE>{}); break;
+  }
 }
 
 __device__ __forceinline__ float bf16_at(const uint16_t* p, int64_t i) {
@@ -175,13 +195,16 @@ __device__ __forceinline__ void epilogue_columns(const LinearArgs& g, const Lane
       for (int j = 0; j < kN; ++j)
         if (j < n) zr[j] = __ldcs(g.z_in + (b0 + j) * g.z_ld + c.a);
     }
+    with_activation(g.z_in ? g.act : OPT_ACT_NONE, [&](auto act) {
 #pragma unroll
-    for (int j = 0; j < kN; ++j)
-      if (j < n) {
-        float d = v[j];
-        if (g.z_in) d *= activate_grad(__uint_as_float(static_cast<uint32_t>(zr[j]) << 16), g.act);
-        g.y[(b0 + j) * g.y_ld + c.a] = to_bf16(d);
-      }
+      for (int j = 0; j < kN; ++j)
+        if (j < n) {
+          float d = v[j];
+          if (act.value != OPT_ACT_NONE)
+            d *= activate_grad<act.value>(__uint_as_float(static_cast<uint32_t>(zr[j]) << 16));
+          g.y[(b0 + j) * g.y_ld + c.a] = to_bf16(d);
+        }
+    });
   } else {
     uint16_t rr[kN];
     if (g.residual) {
@@ -189,17 +212,19 @@ __device__ __forceinline__ void epilogue_columns(const LinearArgs& g, const Lane
       for (int j = 0; j < kN; ++j)
         if (j < n) rr[j] = g.residual[(b0 + j) * g.residual_ld + c.a];
     }
+    with_activation(g.act, [&](auto act) {
 #pragma unroll
-    for (int j = 0; j < kN; ++j)
-      if (j < n) {
-        float z = v[j];
-        if (kFp8) z *= c.scale * g.b_scale[b0 + j];
-        z += c.bias;
-        if (g.z_out) __stcs(g.z_out + (b0 + j) * g.z_ld + c.a, to_bf16(z));
-        float y = activate(z, g.act);
-        if (g.residual) y += __uint_as_float(static_cast<uint32_t>(rr[j]) << 16);
-        g.y[(b0 + j) * g.y_ld + c.a] = to_bf16(y);
-      }
+      for (int j = 0; j < kN; ++j)
+        if (j < n) {
+          float z = v[j];
+          if (kFp8) z *= c.scale * g.b_scale[b0 + j];
+          z += c.bias;
+          if (g.z_out) __stcs(g.z_out + (b0 + j) * g.z_ld + c.a, to_bf16(z));
+          float y = activate<act.value>(z);
+          if (g.residual) y += __uint_as_float(static_cast<uint32_t>(rr[j]) << 16);
+          g.y[(b0 + j) * g.y_ld + c.a] = to_bf16(y);
+        }
+    });
   }
 }
 
@@ -331,17 +356,25 @@ linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
 //
 // Large products: CTA pairs, persistent over 256 x 256 tiles with
 // cta_group::2 MMAs, the structure of the Newton-Schulz GEMMs.  Each CTA
-// stages its 128 A indices and 128 of the tile's 256 B indices (32 KB per
-// 128-byte k-block, where two separate 128 x 256 tiles would stage 96 KB
-// between them) and receives the accumulators of its own 128 A indices.  Two
-// accumulators of 256 columns let the epilogue of one tile overlap the main
-// loop of the next.
+// stages 128 output rows' and 128 output columns' operand (32 KB per 128-byte
+// k-block, where two separate 128 x 256 tiles would stage 96 KB between them)
+// and receives the accumulators of its own 128 rows.  Two accumulators of 256
+// columns let the epilogue of one tile overlap the main loop of the next.
 //   warp 0      TMA producer (both CTAs; bytes counted on the even CTA's barrier)
 //   warp 1      TMEM allocation; in the even CTA the MMA issuer
 //   warps 2-9   epilogue: two warps per TMEM lane quarter, 128 columns each
 //   warp 10     even CTA: claims tiles from a launch-wide counter and publishes
 //               them to both CTAs, so the tiles in flight stay neighbours that
 //               share operand panels in L2
+//
+// Here a TMEM lane is an output row `b` and a TMEM column an output column
+// `a`: a lane's 32 columns pack into 16-byte pieces of its row, are staged in
+// shared memory and leave by TMA stores (main_grad += by TMA reductions, one
+// addition per element).  With the lanes on `a`, as in linear_kernel, each
+// column was a 64-byte store of its own and the epilogue, not the MMAs, set
+// the pace: 22 us per tile whatever k was, against 17 us of MMAs at k = 4096.
+// Outputs that TMA cannot address (base or row distance not a multiple of 16
+// bytes) are turned in shared memory and stored 64 bytes at a time.
 //
 // dw sums over the tokens, and the tensor cores truncate each addition to the
 // accumulator: a sum of m tokens comes out low by about m 2^-30 of its value
@@ -350,17 +383,20 @@ linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
 // with rounding additions while the MMAs of the next segment run into the
 // other accumulator.
 
-constexpr int kPairStages = 7;
+constexpr int kPairStages = 6;
 constexpr int kPairBN = 256;
 constexpr int kPairEpiWarps = 8;
 constexpr int kPairThreads = 96 + 32 * kPairEpiWarps;
 constexpr int kPairTmemCols = 512;
 constexpr int kDwSegment = 8;
 constexpr int kTileSlots = 3;
+constexpr int kWarpScratch = 4096;     // per epilogue warp: staged 32 x 32 blocks, bf16 y and z or fp32
+constexpr int kBlockBytes = 32 * 32 * 2;
 constexpr uint32_t kTileConsumers = 2 + 1 + 2 * kPairEpiWarps;
 constexpr int kPairBarrierBytes = (2 * kPairStages + 5 + 2 * kTileSlots) * 8 + 8 + 4 * kTileSlots;
 static_assert(kPairBarrierBytes <= 256, "barrier block larger than its 256-byte reservation");
-constexpr uint32_t kPairSmemBytes = kPairStages * kStageBytes + 1024 /*align*/ + 256 /*barriers*/;
+constexpr uint32_t kPairSmemBytes =
+    kPairStages * kStageBytes + kPairEpiWarps * kWarpScratch + 1024 /*align*/ + 256 /*barriers*/;
 static_assert(kPairSmemBytes <= 232448, "dynamic shared memory above the 227 KB a CTA may use");
 
 struct PairParams {
@@ -368,6 +404,8 @@ struct PairParams {
   int k_blocks;
   int segment;         // k-blocks accumulated in TMEM at a time
   int tiles_a, tiles_b, total_tiles;
+  int out_tma;         // y (or dw) moves through map_out, z through map_z
+  int in_vec;          // residual / z_in rows start on 16 bytes
 };
 
 // Tiles in groups of kGroupB tiles along b, a-major inside a group: about 76
@@ -405,13 +443,137 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+__device__ __forceinline__ void tma_store_block(const CUtensorMap* map, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+}
+
+// The block is added to global memory, fp32, each element once.
+__device__ __forceinline__ void tma_add_block(const CUtensorMap* map, uint32_t src, int x, int y) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// Lane t holds row t of a 32 x 32 bf16 block: 64-byte swizzle for a TMA store.
+__device__ __forceinline__ void stage_bf16_rows(uint8_t* buf, int lane, const float (&v)[32]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t phys = static_cast<uint32_t>(q) ^ ((static_cast<uint32_t>(lane) >> 1) & 3u);
+    *reinterpret_cast<uint4*>(buf + lane * 64 + phys * 16) =
+        make_uint4(pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
+                   pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7]));
+  }
+}
+
+// The warp's 32 x 32 words of scratch as a turning table: (row, col) at
+// row * 32 + (col ^ row), free of bank conflicts by rows and by columns.
+__device__ __forceinline__ int turn(int row, int col) { return row * 32 + (col ^ row); }
+
+// A 32 x 32 block of a bf16 input, lane t's row t (row0 + t) in `raw`, two
+// elements to a word; zeros outside the matrix.
+__device__ __forceinline__ void load_block(const uint16_t* p, int64_t ld, int64_t row0, int64_t col0, int64_t rows,
+                                           int64_t cols, bool vec, uint32_t* table, int lane, uint32_t (&raw)[16]) {
+  if (vec && col0 + 32 <= cols) {
+    const bool ok = row0 + lane < rows;
+    const uint4* q = reinterpret_cast<const uint4*>(p + (row0 + lane) * ld + col0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 w = ok ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+      raw[4 * i] = w.x;
+      raw[4 * i + 1] = w.y;
+      raw[4 * i + 2] = w.z;
+      raw[4 * i + 3] = w.w;
+    }
+    return;
+  }
+  const bool ok = col0 + lane < cols;
+#pragma unroll 8
+  for (int r = 0; r < 32; ++r)
+    table[turn(r, lane)] = ok && row0 + r < rows ? p[(row0 + r) * ld + col0 + lane] : 0;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) raw[i] = table[turn(lane, 2 * i)] | (table[turn(lane, 2 * i + 1)] << 16);
+  __syncwarp();
+}
+
+__device__ __forceinline__ float block_elem(const uint32_t (&raw)[16], int j) {
+  return __uint_as_float(j & 1 ? raw[j >> 1] & 0xffff0000u : raw[j >> 1] << 16);
+}
+
+// 32 values that every lane shares: p[col0 .. col0 + 31], 0 past the end.
+__device__ __forceinline__ void load_shared_cols(const void* p, int dtype, int64_t col0, int64_t cols,
+                                                 float (&out)[32]) {
+  if (dtype == kBf16) {
+    const uint16_t* q = static_cast<const uint16_t*>(p) + col0;
+    if (col0 + 32 <= cols && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(q) + i);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          out[8 * i + 2 * k] = __uint_as_float(u[k] << 16);
+          out[8 * i + 2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) out[j] = col0 + j < cols ? bf16_at(q, j) : 0.f;
+    }
+  } else {
+    const float* q = static_cast<const float*>(p) + col0;
+    if (col0 + 32 <= cols && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 w = __ldg(reinterpret_cast<const float4*>(q) + i);
+        out[4 * i] = w.x;
+        out[4 * i + 1] = w.y;
+        out[4 * i + 2] = w.z;
+        out[4 * i + 3] = w.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) out[j] = col0 + j < cols ? q[j] : 0.f;
+    }
+  }
+}
+
+// A block that TMA cannot store: turned through the table, then 32 columns of
+// one row at a time.
+template <typename T, typename F>
+__device__ __forceinline__ void store_turned(T* p, int64_t ld, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
+                                             float* table, int lane, const float (&v)[32], F&& put) {
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 32; ++j) table[turn(lane, j)] = v[j];
+  __syncwarp();
+  if (col0 + lane < cols) {
+    const int n = static_cast<int>(rows - row0 < 32 ? rows - row0 : 32);
+    T* q = p + row0 * ld + col0 + lane;
+#pragma unroll 8
+    for (int r = 0; r < n; ++r) put(q + r * ld, table[turn(r, lane)]);
+  }
+  __syncwarp();
+}
+
 template <int kMode, bool kFp8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                   const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_z,
                    const __grid_constant__ PairParams P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairStages * kStageBytes);   // even CTA: both CTAs' copies landed
+  uint8_t* scratch = smem + kPairStages * kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(scratch + kPairEpiWarps * kWarpScratch);   // even CTA: both CTAs' copies landed
   uint64_t* empty = full + kPairStages;            // both CTAs: stage free again
   uint64_t* acc_full = empty + kPairStages;        // [2] both CTAs: accumulator ready
   uint64_t* acc_empty = acc_full + 2;              // [2] even CTA: both epilogues have read it
@@ -423,7 +585,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   volatile int* tile_ring = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [kTileSlots]
 
   constexpr int kElems = kFp8 ? 128 : 64;
-  constexpr bool a_mn = Order<kMode>::a_mn, b_mn = Order<kMode>::b_mn;
+  // the MMA's A operand holds output rows (the product's B), its B operand output columns
+  constexpr bool a_mn = Order<kMode>::b_mn, b_mn = Order<kMode>::a_mn;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
@@ -479,7 +642,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
         if (tile >= P.total_tiles) break;
         int ta, tb;
         pair_tile(P, tile, ta, tb);
-        const int ai = ta * 256 + static_cast<int>(rank) * BM, bi = tb * kPairBN + static_cast<int>(rank) * BN;
+        const int ai = tb * 256 + static_cast<int>(rank) * BM, bi = ta * kPairBN + static_cast<int>(rank) * BN;
         for (int kb = 0; kb < P.k_blocks; ++kb) {
           if (!mbar_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, status, kStatusTimeoutEmpty)) {
             ok = false;
@@ -573,6 +736,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t empty_even = peer_addr(smem_u32(&acc_empty[0]), 0);
     const uint32_t tempty_even = peer_addr(smem_u32(&tile_empty[0]), 0);
+    uint8_t* stage = scratch + (warp - 2) * kWarpScratch;
     uint32_t use = 0;
     bool ok = true;
     for (uint32_t lt = 0; ok; ++lt) {
@@ -595,9 +759,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       if (!got || tile >= P.total_tiles) break;
       int ta, tb;
       pair_tile(P, tile, ta, tb);
-      const LaneColumn col = lane_column<kMode, kFp8>(
-          P.g, static_cast<int64_t>(ta) * 256 + rank * BM + quarter * 32 + lane);
-      const int64_t b0 = static_cast<int64_t>(tb) * kPairBN + half * 128;
+      const int64_t row0 = static_cast<int64_t>(tb) * 256 + rank * BM + quarter * 32;
+      const int64_t col0 = static_cast<int64_t>(ta) * kPairBN + half * 128;
       const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
       if constexpr (kMode == kLinearDw) {
         float sum[128];
@@ -620,25 +783,110 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
           mbar_arrive_remote(empty_even + acc * 8);
         }
         if (!ok) break;
+        if (row0 < P.g.nb) {
 #pragma unroll
-        for (int c = 0; c < 128; c += 8)
-          if (b0 + c < P.g.nb) epilogue_columns<kMode, kFp8, 8>(P.g, col, b0 + c, sum + c);
+          for (int c = 0; c < 128; c += 32) {
+            if (col0 + c >= P.g.na) break;
+            if (P.out_tma) {
+              if (lane == 0) bulk_wait_read_0();     // the previous block's store has read the staging area
+              __syncwarp();
+#pragma unroll
+              for (int q = 0; q < 8; ++q)            // 128-byte swizzle
+                *reinterpret_cast<float4*>(stage + lane * 128 + ((q ^ (lane & 7)) * 16)) =
+                    make_float4(sum[c + 4 * q], sum[c + 4 * q + 1], sum[c + 4 * q + 2], sum[c + 4 * q + 3]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                const int x = static_cast<int>(col0 + c), y = static_cast<int>(row0);
+                if (P.g.accumulate) tma_add_block(&map_out, smem_u32(stage), x, y);
+                else tma_store_block(&map_out, smem_u32(stage), x, y);
+                bulk_commit();
+              }
+            } else {
+              float v[32];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = sum[c + j];
+              const bool add = P.g.accumulate != 0;
+              store_turned(P.g.dw, P.g.dw_ld, row0, col0 + c, P.g.nb, P.g.na, reinterpret_cast<float*>(stage), lane, v,
+                           [add](float* p, float x) { *p = add ? *p + x : x; });
+            }
+          }
+        }
       } else {
+        const uint16_t* in = kMode == kLinearDx ? P.g.z_in : P.g.residual;
+        const int64_t in_ld = kMode == kLinearDx ? P.g.z_ld : P.g.residual_ld;
+        const bool live = row0 < P.g.nb;
+        float row_scale = 1.f;
+        if (kFp8 && row0 + lane < P.g.nb) row_scale = P.g.b_scale[row0 + lane];
         const uint32_t acc = use & 1;
         ok = __all_sync(0xffffffffu,
                         mbar_wait(smem_u32(&acc_full[acc]), (use >> 1) & 1u, abort_flag, status, kStatusTimeoutAcc));
         if (!ok) break;
         ++use;
         tc_fence_after();
-        for (int c = 0; c < 128 && b0 + c < P.g.nb; c += 32) {
+        for (int c = 0; c < 128 && live && col0 + c < P.g.na; c += 32) {
+          const int64_t col = col0 + c;
+          // the staging area doubles as the turning table of inputs and outputs
+          // that cannot move 16 bytes at a time
+          if (lane == 0) bulk_wait_read_0();
+          __syncwarp();
+          uint32_t raw[16];
+          if (in) load_block(in, in_ld, row0, col, P.g.nb, P.g.na, P.in_vec != 0, reinterpret_cast<uint32_t*>(stage), lane, raw);
           float v[32];
           tmem_ld32(lane_addr + acc * kPairBN + c, v);
-          epilogue_columns<kMode, kFp8, 32>(P.g, col, b0 + c, v);
+          if constexpr (kMode == kLinearDx) {
+            if (in)
+              with_activation(P.g.act, [&](auto act) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] *= activate_grad<act.value>(block_elem(raw, j));
+              });
+          } else {
+            float t[32];
+            if constexpr (kFp8) {
+              load_shared_cols(P.g.a_scale, kFp32, col, P.g.na, t);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] *= row_scale * t[j];
+            }
+            if (P.g.bias) {
+              load_shared_cols(P.g.bias, P.g.bias_dtype, col, P.g.na, t);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] += t[j];
+            }
+            if (P.g.z_out) {
+              if (P.out_tma) stage_bf16_rows(stage + kBlockBytes, lane, v);
+              else
+                store_turned(P.g.z_out, P.g.z_ld, row0, col, P.g.nb, P.g.na, reinterpret_cast<float*>(stage), lane, v,
+                             [](uint16_t* p, float x) { *p = to_bf16(x); });
+            }
+            with_activation(P.g.act, [&](auto act) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = activate<act.value>(v[j]);
+            });
+            if (in) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] += block_elem(raw, j);
+            }
+          }
+          if (P.out_tma) {
+            stage_bf16_rows(stage, lane, v);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              const int x = static_cast<int>(col), y = static_cast<int>(row0);
+              tma_store_block(&map_out, smem_u32(stage), x, y);
+              if (kMode == kLinearForward && P.g.z_out) tma_store_block(&map_z, smem_u32(stage + kBlockBytes), x, y);
+              bulk_commit();
+            }
+          } else {
+            store_turned(P.g.y, P.g.y_ld, row0, col, P.g.nb, P.g.na, reinterpret_cast<float*>(stage), lane, v,
+                         [](uint16_t* p, float x) { *p = to_bf16(x); });
+          }
         }
         tc_fence_before();
         mbar_arrive_remote(empty_even + acc * 8);
       }
     }
+    if (lane == 0) bulk_wait_all();        // stores complete before the CTA exits
   } else if (lane == 0 && rank == 0) {
     const uint32_t ring_odd = peer_addr(smem_u32(const_cast<int*>(tile_ring)), 1);
     const uint32_t tfull_odd = peer_addr(smem_u32(&tile_full[0]), 1);
@@ -721,6 +969,23 @@ cudaError_t make_operand_map(CUtensorMap* map, const LinearOperand& o, int64_t n
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// 2-D map of an output [rows][cols] of 2- or 4-byte elements in 32 x 32
+// blocks (64- or 128-byte swizzle); false when TMA cannot address it.
+bool make_block_map(CUtensorMap* map, const void* p, int64_t ld, int64_t rows, int64_t cols, bool fp32) {
+  const int es = fp32 ? 4 : 2;
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || (reinterpret_cast<uintptr_t>(p) & 15u) != 0 || (rows > 1 && (ld * es) % 16 != 0)) return false;
+  if (rows <= 1) ld = (cols + 7) / 8 * 8;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * es)};
+  const cuuint32_t box[2] = {32, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            fp32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Raises a kernel's shared-memory limit once per thread and device.
 template <auto kKernel>
 cudaError_t allow_smem(int bytes) {
@@ -751,9 +1016,19 @@ cudaError_t launch_product(const LinearArgs& a, cudaStream_t stream) {
     P.tiles_a = static_cast<int>(pair_a);
     P.tiles_b = static_cast<int>(pair_b);
     P.total_tiles = static_cast<int>(pair_a * pair_b);
+    CUtensorMap mo{}, mz{};
+    if constexpr (kMode == kLinearDw) {
+      P.out_tma = make_block_map(&mo, a.dw, a.dw_ld, a.nb, a.na, true);
+    } else {
+      P.out_tma = make_block_map(&mo, a.y, a.y_ld, a.nb, a.na, false) &&
+                  (!a.z_out || make_block_map(&mz, a.z_out, a.z_ld, a.nb, a.na, false));
+      const uint16_t* in = kMode == kLinearDx ? a.z_in : a.residual;
+      const int64_t in_ld = kMode == kLinearDx ? a.z_ld : a.residual_ld;
+      P.in_vec = (reinterpret_cast<uintptr_t>(in) & 15u) == 0 && in_ld % 8 == 0;
+    }
     if ((e = allow_smem<linear_pair_kernel<kMode, kFp8>>(kPairSmemBytes)) != cudaSuccess) return e;
     const int grid = 2 * (P.total_tiles < max_pairs ? P.total_tiles : max_pairs);
-    linear_pair_kernel<kMode, kFp8><<<grid, kPairThreads, kPairSmemBytes, stream>>>(ma, mb, P);
+    linear_pair_kernel<kMode, kFp8><<<grid, kPairThreads, kPairSmemBytes, stream>>>(mb, ma, mo, mz, P);
     return cudaGetLastError();
   }
   LinearParams P{};
