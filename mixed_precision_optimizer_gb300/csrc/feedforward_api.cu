@@ -188,13 +188,19 @@ opt_status opt_rmsnorm_backward(const opt_rmsnorm_grad_args* a, void* workspace,
   return cuda_status(launch_rmsnorm_grad(k, static_cast<cudaStream_t>(stream)), "rmsnorm gradient launch");
 }
 
+// Bytes of the bias gradient's partial sums.
+static size_t column_sum_bytes(int64_t m, int64_t n) {
+  const int64_t s = column_sum_slices(m, n);
+  return s > 1 ? round_up(static_cast<size_t>(s) * static_cast<size_t>(n) * 4, 256) : 0;
+}
+
 size_t opt_linear_workspace_size(int64_t m, int64_t n, int64_t k, int32_t flags) {
   if (!extents_ok(m, n, k)) return 0;
   const bool any = (flags & OPT_LINEAR_ANY_LAYOUT) != 0;
   // 16-byte rows: k a multiple of 16 also serves 8-bit operands
   const size_t x_w = any || k % 16 ? packed_bytes(m, k, 2) + packed_bytes(n, k, 2) : 0;
   const size_t dz = any || n % 8 ? packed_bytes(m, n, 2) : 0;
-  return kLinearHeaderBytes + x_w + dz;
+  return kLinearHeaderBytes + x_w + dz + column_sum_bytes(m, n);
 }
 
 opt_status opt_linear_forward(const opt_linear_args* a, void* workspace, size_t workspace_bytes, void* stream) {
@@ -264,12 +270,15 @@ opt_status opt_linear_backward(const opt_linear_grad_args* a, void* workspace, s
   MPOPT_TRY(check_matrix(a->w, !a->dx, a->w_ld, a->n, a->k, 2));
   MPOPT_TRY(check_matrix(a->z_prev, true, a->z_prev_ld, a->m, a->k, 2));
   MPOPT_TRY(check_matrix(a->dx, true, a->dx_ld, a->m, a->k, 2));
+  const size_t sums = a->dbias ? column_sum_bytes(a->m, a->n) : 0;
+  const size_t products = a->dx || a->dw ? repack_need(a->dz, a->dz_ld, a->m, a->n, 2) +
+                                               (a->dx ? repack_need(a->w, a->w_ld, a->n, a->k, 2) : 0) +
+                                               (a->dw ? repack_need(a->x, a->x_ld, a->m, a->k, 2) : 0)
+                                         : 0;
+  if (a->dx || a->dw || sums) MPOPT_TRY(check_workspace(workspace, workspace_bytes, kLinearHeaderBytes + products + sums));
+  uint8_t* const scratch = static_cast<uint8_t*>(workspace) + kLinearHeaderBytes;
   if (a->dx || a->dw) {
-    const size_t need = kLinearHeaderBytes + repack_need(a->dz, a->dz_ld, a->m, a->n, 2) +
-                        (a->dx ? repack_need(a->w, a->w_ld, a->n, a->k, 2) : 0) +
-                        (a->dw ? repack_need(a->x, a->x_ld, a->m, a->k, 2) : 0);
-    MPOPT_TRY(check_workspace(workspace, workspace_bytes, need));
-    Repacker rp{static_cast<uint8_t*>(workspace) + kLinearHeaderBytes, workspace_bytes - kLinearHeaderBytes, st};
+    Repacker rp{scratch + sums, workspace_bytes - kLinearHeaderBytes - sums, st};
     LinearOperand dz{};
     MPOPT_TRY(rp.operand(a->dz, a->dz_ld, a->m, a->n, 2, 0, &dz));
     if (a->dx) {
@@ -306,7 +315,8 @@ opt_status opt_linear_backward(const opt_linear_grad_args* a, void* workspace, s
   }
   if (a->dbias) {
     prof_begin(OPT_KERNEL_LINEAR_DBIAS, 1, a->m, a->n, st);
-    const cudaError_t e = launch_column_sums(a->dz, a->dz_ld, a->m, a->n, a->dbias, a->accumulate, st);
+    const cudaError_t e = launch_column_sums(a->dz, a->dz_ld, a->m, a->n, a->dbias, reinterpret_cast<float*>(scratch),
+                                             a->accumulate, st);
     prof_end(st);
     MPOPT_TRY(cuda_status(e, "linear bias gradient launch"));
   }

@@ -260,7 +260,7 @@ enum : int { kFp32 = 0, kBf16 = 1, kE4m3 = 2 };   // OPT_DTYPE_*
 
 constexpr int64_t kNormMaxCols = 49152;       // a row in fp32 in shared memory
 constexpr int64_t kNormGradMaxCols = 24576;   // two of them
-constexpr int64_t kNormPartialRows = 304;     // partial sums of dgamma: CTAs of the backward pass at most
+constexpr int64_t kNormPartialRows = 608;     // partial sums of dgamma: CTAs of the backward pass at most
 
 struct RmsnormArgs {
   const void *x, *residual, *gamma;
@@ -315,9 +315,16 @@ struct LinearArgs {
 };
 constexpr size_t kLinearHeaderBytes = 256;
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream);
-// dbias[n] (+)= column sums of dz [m][n]
-cudaError_t launch_column_sums(const uint16_t* dz, int64_t ld, int64_t m, int64_t n, float* out, int accumulate,
-                               cudaStream_t stream);
+// dbias[n] (+)= column sums of dz [m][n], in slices of rows whose sums pass
+// through `partial` [column_sum_slices][n] when there is more than one: enough
+// CTAs of 64 columns to fill the GPU, at least 128 rows to a slice.
+inline int64_t column_sum_slices(int64_t m, int64_t n) {
+  const int64_t by_rows = (m + 127) / 128, wanted = (152 * 4 * 64 + n - 1) / n;
+  const int64_t s = by_rows < wanted ? by_rows : wanted;
+  return s < 1 ? 1 : s > 64 ? 64 : s;
+}
+cudaError_t launch_column_sums(const uint16_t* dz, int64_t ld, int64_t m, int64_t n, float* out, float* partial,
+                               int accumulate, cudaStream_t stream);
 // dst rows (dst_ld elements apart) <- src rows, elements of `esize` bytes (1 or 2)
 cudaError_t launch_repack(const void* src, int64_t src_ld, void* dst, int64_t dst_ld, int64_t rows, int64_t cols,
                           int esize, cudaStream_t stream);

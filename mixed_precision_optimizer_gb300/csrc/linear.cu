@@ -378,17 +378,19 @@ linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
 //
 // dw sums over the tokens, and the tensor cores truncate each addition to the
 // accumulator: a sum of m tokens comes out low by about m 2^-30 of its value
-// (1.6e-5 at 16384).  So dw runs in segments of kDwSegment k-blocks (512
-// tokens, 5e-7): the epilogue adds each segment's accumulator to registers
+// (1.6e-5 at 16384).  So dw runs in segments of kDwSegment k-blocks (768
+// tokens, 7e-7): the epilogue adds each segment's accumulator to registers
 // with rounding additions while the MMAs of the next segment run into the
-// other accumulator.
+// other accumulator.  Two segments are also the time that a tile's stores have
+// before the MMAs stall: 8 k-blocks cost 6 % against one segment for all
+// (8192 tokens, 14336 x 4096), 16 and more 2 % or less.
 
 constexpr int kPairStages = 6;
 constexpr int kPairBN = 256;
 constexpr int kPairEpiWarps = 8;
 constexpr int kPairThreads = 96 + 32 * kPairEpiWarps;
 constexpr int kPairTmemCols = 512;
-constexpr int kDwSegment = 8;
+constexpr int kDwSegment = 12;
 constexpr int kTileSlots = 3;
 constexpr int kWarpScratch = 4096;     // per epilogue warp: staged 32 x 32 blocks, bf16 y and z or fp32
 constexpr int kBlockBytes = 32 * 32 * 2;
@@ -409,8 +411,9 @@ struct PairParams {
 };
 
 // Tiles in groups of kGroupB tiles along b, a-major inside a group: about 76
-// tiles are in flight, a block of 8 x 9.5 tiles that shares its panels.
-constexpr int kGroupB = 8;
+// tiles are in flight, a block of 12 x 6.3 tiles that shares its panels (4 and 6
+// wide: up to 5 % slower on 8192 x 14336 x 4096 and its gradients; 8 and 16 within 2 %).
+constexpr int kGroupB = 12;
 
 __device__ __forceinline__ void pair_tile(const PairParams& P, int tile, int& ta, int& tb) {
   const int per_group = kGroupB * P.tiles_a;
@@ -487,7 +490,7 @@ __device__ __forceinline__ void load_block(const uint16_t* p, int64_t ld, int64_
     const uint4* q = reinterpret_cast<const uint4*>(p + (row0 + lane) * ld + col0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint4 w = ok ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+      const uint4 w = ok ? q[i] : make_uint4(0, 0, 0, 0);   // a plain load: y may be the residual
       raw[4 * i] = w.x;
       raw[4 * i + 1] = w.y;
       raw[4 * i + 2] = w.z;
@@ -922,23 +925,58 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
 
 // ------------------------------------------------------- smaller kernels --
 
-// Column sums of dz, in a fixed order: a CTA takes 32 columns, its 8 warps
-// every eighth row, and the warps' sums are added in order.
+// Column sums of dz in a fixed order.  CTA (x, y) takes 64 columns of the rows
+// of its y-th slice, each warp every eighth of them, two columns to a lane, and
+// adds its warps' sums in order; with one slice that is the result, otherwise
+// the slices' sums go to `partial` and join_sums_kernel adds them in order.
+constexpr int kSumCols = 64;
+
+template <bool kVec>
 __global__ void __launch_bounds__(256)
-column_sums_kernel(const uint16_t* dz, int64_t ld, int64_t m, int64_t n, float* out, int accumulate) {
-  __shared__ float sums[8][32];
+column_sums_kernel(const uint16_t* dz, int64_t ld, int64_t m, int64_t n, float* out, float* partial, int accumulate) {
+  __shared__ float2 sums[8][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  float s = 0.f;
-  if (c < n)
-    for (int64_t r = warp; r < m; r += 8) s += bf16_at(dz, r * ld + c);
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kSumCols + 2 * lane;
+  const int64_t per = (m + gridDim.y - 1) / gridDim.y;
+  const int64_t r0 = per * blockIdx.y, r1 = r0 + per < m ? r0 + per : m;
+  float2 s = make_float2(0.f, 0.f);
+  if (c < n) {
+    const bool two = c + 1 < n;
+#pragma unroll 8
+    for (int64_t r = r0 + warp; r < r1; r += 8) {
+      const uint16_t* p = dz + r * ld + c;
+      if (kVec) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+        s.x += __uint_as_float(w << 16);
+        s.y += __uint_as_float(w & 0xffff0000u);
+      } else {
+        s.x += bf16_at(p, 0);
+        if (two) s.y += bf16_at(p, 1);
+      }
+    }
+  }
   sums[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && c < n) {
-    float t = 0.f;
-    for (int w = 0; w < 8; ++w) t += sums[w][lane];
-    out[c] = accumulate ? out[c] + t : t;
+  if (warp == 0) {
+    for (int w = 1; w < 8; ++w) {
+      s.x += sums[w][lane].x;
+      s.y += sums[w][lane].y;
+    }
+    float* o = gridDim.y > 1 ? partial + static_cast<int64_t>(blockIdx.y) * n : out;
+    const bool add = gridDim.y == 1 && accumulate;
+    if (c < n) o[c] = add ? o[c] + s.x : s.x;
+    if (c + 1 < n) o[c + 1] = add ? o[c + 1] + s.y : s.y;
   }
+}
+
+__global__ void __launch_bounds__(128)
+join_sums_kernel(const float* partial, int slices, int64_t n, float* out, int accumulate) {
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
+  if (c >= n) return;
+  float s = 0.f;
+#pragma unroll 8
+  for (int p = 0; p < slices; ++p) s += partial[p * n + c];
+  out[c] = accumulate ? out[c] + s : s;
 }
 
 template <typename T>
@@ -1051,9 +1089,17 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
   return a.fp8 ? launch_product<kLinearForward, true>(a, stream) : launch_product<kLinearForward, false>(a, stream);
 }
 
-cudaError_t launch_column_sums(const uint16_t* dz, int64_t ld, int64_t m, int64_t n, float* out, int accumulate,
-                               cudaStream_t stream) {
-  column_sums_kernel<<<static_cast<unsigned>((n + 31) / 32), 256, 0, stream>>>(dz, ld, m, n, out, accumulate);
+cudaError_t launch_column_sums(const uint16_t* dz, int64_t ld, int64_t m, int64_t n, float* out, float* partial,
+                               int accumulate, cudaStream_t stream) {
+  const unsigned gx = static_cast<unsigned>((n + kSumCols - 1) / kSumCols);
+  const int64_t gy = column_sum_slices(m, n);
+  const bool vec = n % 2 == 0 && (reinterpret_cast<uintptr_t>(dz) & 3u) == 0 && (m <= 1 || ld % 2 == 0);
+  const dim3 grid(gx, static_cast<unsigned>(gy));
+  if (vec) column_sums_kernel<true><<<grid, 256, 0, stream>>>(dz, ld, m, n, out, partial, accumulate);
+  else column_sums_kernel<false><<<grid, 256, 0, stream>>>(dz, ld, m, n, out, partial, accumulate);
+  if (gy > 1)
+    join_sums_kernel<<<static_cast<unsigned>((n + 127) / 128), 128, 0, stream>>>(partial, static_cast<int>(gy), n, out,
+                                                                                 accumulate);
   return cudaGetLastError();
 }
 

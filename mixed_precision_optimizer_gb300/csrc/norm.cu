@@ -7,8 +7,13 @@
 //   n = h * rstd;  g = dy * gamma;  c = mean(g n)
 //   dx = rstd * (g - n c) + dh;  dgamma = sum over rows of dy n
 //
-// One CTA per row with the row in fp32 in shared memory: every input element
-// is read once and every output written once.
+// All of it is bound by HBM: every input element is read once and every
+// output written once, a row staying in registers between its statistics and
+// its outputs.  A row of up to 1024 columns belongs to one warp (no barrier,
+// eight rows to a CTA), a longer one to a CTA of 128 to 512 threads, up to
+// 16384 columns in registers; longer rows are kept in fp32 in shared memory.
+// Where every row starts on 16 bytes a thread moves 8 elements at a time,
+// otherwise single elements, neighbours in neighbouring lanes.
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -19,144 +24,517 @@
 namespace mpopt {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr float kE4m3Max = 448.f;
 constexpr float kAmaxFloor = 1e-30f;
+constexpr int kLongThreads = 512;             // rows longer than the register kernels take
+constexpr int64_t kRegisterCols = 16384;
 
-__device__ __forceinline__ float load_elem(const void* p, int64_t i, int dtype) {
-  return dtype == kBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
+// ------------------------------------------------------------- elements --
+
+__device__ __forceinline__ float load_elem(const float* p) { return *p; }
+__device__ __forceinline__ float load_elem(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void store_elem(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_elem(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
 }
 
-__device__ __forceinline__ void store_elem(void* p, int64_t i, int dtype, float v) {
-  if (dtype == kBf16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-  else static_cast<float*>(p)[i] = v;
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// Sum and maximum over the CTA, the same value in every thread.
-template <bool kMax>
-__device__ __forceinline__ float block_reduce(float v, float* warp_vals) {
+// Plain loads: an output may be one of the inputs (h over x, dx over dh).
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  unpack8(*reinterpret_cast<const uint4*>(p), v);
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint8_t e4m3(float v) { return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3); }
+
+// A thread's share of a row: kNV groups of 8 columns.  With kVec group i
+// starts at column (i * kTPR + t) * 8, otherwise its element j is column
+// (i * 8 + j) * kTPR + t.
+template <int kTPR, bool kVec>
+__device__ __forceinline__ int64_t column(int i, int j, int t) {
+  return kVec ? (static_cast<int64_t>(i) * kTPR + t) * 8 + j : static_cast<int64_t>(i * 8 + j) * kTPR + t;
+}
+
+template <int kTPR, bool kVec, typename T>
+__device__ __forceinline__ void load_group(const T* row, int i, int t, int64_t cols, float (&v)[8]) {
+  if constexpr (kVec) {
+    const int64_t c = column<kTPR, true>(i, 0, t);
+    if (c < cols) {
+      load8(row + c, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t c = column<kTPR, false>(i, j, t);
+      v[j] = c < cols ? load_elem(row + c) : 0.f;
+    }
+  }
+}
+
+template <int kTPR, bool kVec, typename T>
+__device__ __forceinline__ void store_group(T* row, int i, int t, int64_t cols, const float (&v)[8]) {
+  if constexpr (kVec) {
+    const int64_t c = column<kTPR, true>(i, 0, t);
+    if (c < cols) store8(row + c, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t c = column<kTPR, false>(i, j, t);
+      if (c < cols) store_elem(row + c, v[j]);
+    }
+  }
+}
+
+template <int kTPR, bool kVec>
+__device__ __forceinline__ void load_gamma(const void* gamma, int dtype, int i, int t, int64_t cols, float (&v)[8]) {
+  if (dtype == kBf16) load_group<kTPR, kVec>(static_cast<const __nv_bfloat16*>(gamma), i, t, cols, v);
+  else load_group<kTPR, kVec>(static_cast<const float*>(gamma), i, t, cols, v);
+}
+
+// Sum or maximum over the kTPR threads of a row, the same value in each, in a
+// fixed order.  `vals` is used by one reduction between two barriers.
+template <int kTPR, bool kMax>
+__device__ __forceinline__ float row_reduce(float v, float* vals) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     const float o = __shfl_xor_sync(0xffffffffu, v, off);
     v = kMax ? fmaxf(v, o) : v + o;
   }
-  __syncthreads();                     // the previous reduction has been read
-  if ((threadIdx.x & 31) == 0) warp_vals[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float t = warp_vals[0];
-  for (int w = 1; w < kThreads / 32; ++w) t = kMax ? fmaxf(t, warp_vals[w]) : t + warp_vals[w];
-  return t;
+  if constexpr (kTPR > 32) {
+    if ((threadIdx.x & 31) == 0) vals[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = vals[0];
+#pragma unroll
+    for (int w = 1; w < kTPR / 32; ++w) v = kMax ? fmaxf(v, vals[w]) : v + vals[w];
+  }
+  return v;
 }
 
-__device__ __forceinline__ uint8_t e4m3_bits(float v) {
-  return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
-}
+// -------------------------------------------------------------- forward --
 
-__global__ void __launch_bounds__(kThreads) rmsnorm_kernel(const __grid_constant__ RmsnormArgs a) {
-  extern __shared__ float row[];
-  __shared__ float warp_vals[kThreads / 32];
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+// One row per group of kTPR threads.
+template <typename T, int kTPR, int kNV, bool kVec>
+__global__ void __launch_bounds__(kTPR == 32 ? 256 : kTPR)
+rmsnorm_kernel(const __grid_constant__ RmsnormArgs a) {
+  constexpr int kThreads = kTPR == 32 ? 256 : kTPR;
+  constexpr int kRows = kThreads / kTPR;
+  __shared__ float vals[2][kTPR / 32];
+  const int t = threadIdx.x % kTPR;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kTPR;
+  if (r >= a.rows) return;                       // kTPR == 32: whole warps; otherwise the grid is exact
+  const int64_t cols = a.cols;
+  float v[kNV][8];
+  {
+    const T* x = static_cast<const T*>(a.x) + r * a.x_ld;
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) load_group<kTPR, kVec>(x, i, t, cols, v[i]);
+  }
+  if (a.residual) {
+    const T* p = static_cast<const T*>(a.residual) + r * a.residual_ld;
+    float w[kNV][8];
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) load_group<kTPR, kVec>(p, i, t, cols, w[i]);
+#pragma unroll
+    for (int i = 0; i < kNV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] += w[i][j];
+  }
+  if (a.h) {
+    T* h = static_cast<T*>(a.h) + r * a.h_ld;
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) store_group<kTPR, kVec>(h, i, t, cols, v[i]);
+  }
+  if (a.norm) {
     float ss = 0.f;
-    for (int64_t c = threadIdx.x; c < a.cols; c += kThreads) {
-      float v = load_elem(a.x, r * a.x_ld + c, a.dtype);
-      if (a.residual) v += load_elem(a.residual, r * a.residual_ld + c, a.dtype);
-      if (a.h) store_elem(a.h, r * a.h_ld + c, a.dtype, v);
-      row[c] = v;
-      ss += v * v;
+#pragma unroll
+    for (int i = 0; i < kNV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss += v[i][j] * v[i][j];
+    ss = row_reduce<kTPR, false>(ss, vals[0]);
+    const float rstd = 1.f / sqrtf(ss / static_cast<float>(cols) + a.eps);
+    if (a.rstd && t == 0) a.rstd[r] = rstd;
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+      float g[8];
+      load_gamma<kTPR, kVec>(a.gamma, a.gamma_dtype, i, t, cols, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * g[j];
     }
-    float rstd = 1.f;
-    if (a.norm) {
-      rstd = 1.f / sqrtf(block_reduce<false>(ss, warp_vals) / static_cast<float>(a.cols) + a.eps);
-      if (a.rstd && threadIdx.x == 0) a.rstd[r] = rstd;
-    }
+  }
+  if (a.y) {
+    __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(a.y) + r * a.y_ld;
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) store_group<kTPR, kVec>(y, i, t, cols, v[i]);
+  }
+  if (a.q) {
     float amax = 0.f;
-    for (int64_t c = threadIdx.x; c < a.cols; c += kThreads) {
-      float y = row[c];
-      if (a.norm) y = y * rstd * load_elem(a.gamma, c, a.gamma_dtype);
-      row[c] = y;
-      amax = fmaxf(amax, fabsf(y));
-      if (a.y) store_elem(a.y, r * a.y_ld + c, kBf16, y);
+#pragma unroll
+    for (int i = 0; i < kNV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // columns past the end hold zeros times rstd, which may be NaN: fmaxf drops it
+        amax = fmaxf(amax, fabsf(v[i][j]));
+      }
+    const float scale = fmaxf(row_reduce<kTPR, true>(amax, vals[1]), kAmaxFloor) / kE4m3Max;
+    if (t == 0) a.q_scale[r] = scale;
+    const float inv = 1.f / scale;
+    uint8_t* q = a.q + r * a.q_ld;
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+      if constexpr (kVec) {
+        const int64_t c = column<kTPR, true>(i, 0, t);
+        if (c < cols)
+          *reinterpret_cast<uint2*>(q + c) =
+              make_uint2(e4m3x2(v[i][0] * inv, v[i][1] * inv) | (e4m3x2(v[i][2] * inv, v[i][3] * inv) << 16),
+                         e4m3x2(v[i][4] * inv, v[i][5] * inv) | (e4m3x2(v[i][6] * inv, v[i][7] * inv) << 16));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int64_t c = column<kTPR, false>(i, j, t);
+          if (c < cols) q[c] = e4m3(v[i][j] * inv);
+        }
+      }
     }
-    if (a.q) {
-      const float scale = fmaxf(block_reduce<true>(amax, warp_vals), kAmaxFloor) / kE4m3Max;
-      if (threadIdx.x == 0) a.q_scale[r] = scale;
-      const float inv = 1.f / scale;
-      for (int64_t c = threadIdx.x; c < a.cols; c += kThreads) a.q[r * a.q_ld + c] = e4m3_bits(row[c] * inv);
-    }
-    __syncthreads();                   // the row is free again
   }
 }
 
-// CTA b takes rows b, b + gridDim.x, ... and keeps its part of dgamma in
-// partial[b].
-__global__ void __launch_bounds__(kThreads) rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
+// A long row in fp32 in shared memory.
+template <typename T>
+__global__ void __launch_bounds__(kLongThreads) rmsnorm_long_kernel(const __grid_constant__ RmsnormArgs a) {
+  extern __shared__ float row[];
+  __shared__ float vals[2][kLongThreads / 32];
+  const int64_t r = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + r * a.x_ld;
+  const T* res = a.residual ? static_cast<const T*>(a.residual) + r * a.residual_ld : nullptr;
+  T* h = a.h ? static_cast<T*>(a.h) + r * a.h_ld : nullptr;
+  float ss = 0.f;
+  for (int64_t c = threadIdx.x; c < a.cols; c += kLongThreads) {
+    float v = load_elem(x + c);
+    if (res) v += load_elem(res + c);
+    if (h) store_elem(h + c, v);
+    row[c] = v;
+    ss += v * v;
+  }
+  float rstd = 1.f;
+  if (a.norm) {
+    rstd = 1.f / sqrtf(row_reduce<kLongThreads, false>(ss, vals[0]) / static_cast<float>(a.cols) + a.eps);
+    if (a.rstd && threadIdx.x == 0) a.rstd[r] = rstd;
+  }
+  float amax = 0.f;
+  for (int64_t c = threadIdx.x; c < a.cols; c += kLongThreads) {   // this thread's own columns
+    float y = row[c];
+    if (a.norm)
+      y = y * rstd *
+          (a.gamma_dtype == kBf16 ? load_elem(static_cast<const __nv_bfloat16*>(a.gamma) + c)
+                                  : static_cast<const float*>(a.gamma)[c]);
+    row[c] = y;
+    amax = fmaxf(amax, fabsf(y));
+    if (a.y) store_elem(reinterpret_cast<__nv_bfloat16*>(a.y) + r * a.y_ld + c, y);
+  }
+  if (a.q) {
+    const float scale = fmaxf(row_reduce<kLongThreads, true>(amax, vals[1]), kAmaxFloor) / kE4m3Max;
+    if (threadIdx.x == 0) a.q_scale[r] = scale;
+    const float inv = 1.f / scale;
+    for (int64_t c = threadIdx.x; c < a.cols; c += kLongThreads) a.q[r * a.q_ld + c] = e4m3(row[c] * inv);
+  }
+}
+
+// ------------------------------------------------------------- gradient --
+
+// CTA b takes rows b, b + gridDim.x, ... (kRows at a time when a row belongs to
+// a warp); a thread's columns stay the same, so gamma and its part of dgamma
+// stay in registers, and the CTA writes its partial sums once.
+template <typename T, int kTPR, int kNV, bool kVec>
+__global__ void __launch_bounds__(kTPR == 32 ? 256 : kTPR)
+rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
+  constexpr int kThreads = kTPR == 32 ? 256 : kTPR;
+  constexpr int kRows = kThreads / kTPR;
+  __shared__ float vals[2][kTPR / 32];
+  __shared__ float join[kRows > 1 ? kRows * kTPR * 8 : 1];
+  const int t = threadIdx.x % kTPR, sub = threadIdx.x / kTPR;
+  const int64_t cols = a.cols;
+  const float inv_cols = 1.f / static_cast<float>(cols);
+  float gamma[kNV][8], part[kNV][8];
+#pragma unroll
+  for (int i = 0; i < kNV; ++i) {
+    load_gamma<kTPR, kVec>(a.gamma, a.gamma_dtype, i, t, cols, gamma[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[i][j] = 0.f;
+  }
+  int parity = 0;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + sub; r < a.rows;
+       r += static_cast<int64_t>(gridDim.x) * kRows, parity ^= 1) {
+    const float rstd = a.rstd[r];
+    const T* h = static_cast<const T*>(a.h) + r * a.h_ld;
+    const __nv_bfloat16* dy = reinterpret_cast<const __nv_bfloat16*>(a.dy) + r * a.dy_ld;
+    float n[kNV][8], g[kNV][8];
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+      load_group<kTPR, kVec>(h, i, t, cols, n[i]);
+      load_group<kTPR, kVec>(dy, i, t, cols, g[i]);
+    }
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < kNV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        n[i][j] *= rstd;
+        part[i][j] += g[i][j] * n[i][j];
+        g[i][j] *= gamma[i][j];
+        dot += g[i][j] * n[i][j];
+      }
+    if (a.dx) {
+      const float mean = row_reduce<kTPR, false>(dot, vals[parity]) * inv_cols;
+      T* dx = static_cast<T*>(a.dx) + r * a.dx_ld;
+#pragma unroll
+      for (int i = 0; i < kNV; ++i) {
+        float d[8];
+        if (a.dh) {
+          load_group<kTPR, kVec>(static_cast<const T*>(a.dh) + r * a.dh_ld, i, t, cols, d);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] += rstd * (g[i][j] - n[i][j] * mean);
+        store_group<kTPR, kVec>(dx, i, t, cols, d);
+      }
+    }
+  }
+  if (!a.dgamma) return;
+  float* out = a.partial + static_cast<int64_t>(blockIdx.x) * cols;
+  if constexpr (kRows == 1) {
+#pragma unroll
+    for (int i = 0; i < kNV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int64_t c = column<kTPR, kVec>(i, j, t);
+        if (c < cols) out[c] = part[i][j];
+      }
+  } else {
+    // the warps' sums of 8 * kTPR columns at a time, added in order
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) join[(sub * 8 + j) * kTPR + t] = part[i][j];
+      __syncthreads();
+      for (int e = threadIdx.x; e < 8 * kTPR; e += kThreads) {
+        float s = join[e];
+        for (int w = 1; w < kRows; ++w) s += join[w * 8 * kTPR + e];
+        const int64_t c = column<kTPR, kVec>(i, e / kTPR, e % kTPR);
+        if (c < cols) out[c] = s;
+      }
+    }
+  }
+}
+
+// Rows longer than the registers hold: n and g in shared memory, the partial
+// sums of dgamma in the workspace (each thread its own columns).
+template <typename T>
+__global__ void __launch_bounds__(kLongThreads) rmsnorm_grad_long_kernel(const __grid_constant__ RmsnormGradArgs a) {
   extern __shared__ float rows[];
-  __shared__ float warp_vals[kThreads / 32];
+  __shared__ float vals[2][kLongThreads / 32];
   float* n_row = rows;
   float* g_row = rows + a.cols;
   float* part = a.dgamma ? a.partial + static_cast<int64_t>(blockIdx.x) * a.cols : nullptr;
-  bool first = true;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+  int parity = 0;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, parity ^= 1) {
     const float rstd = a.rstd[r];
+    const T* h = static_cast<const T*>(a.h) + r * a.h_ld;
+    const __nv_bfloat16* dy = reinterpret_cast<const __nv_bfloat16*>(a.dy) + r * a.dy_ld;
     float dot = 0.f;
-    for (int64_t c = threadIdx.x; c < a.cols; c += kThreads) {
-      const float n = load_elem(a.h, r * a.h_ld + c, a.dtype) * rstd;
-      const float dy = load_elem(a.dy, r * a.dy_ld + c, kBf16);
-      const float g = dy * load_elem(a.gamma, c, a.gamma_dtype);
-      if (part) part[c] = first ? dy * n : part[c] + dy * n;   // this thread's own column
+    for (int64_t c = threadIdx.x; c < a.cols; c += kLongThreads) {
+      const float n = load_elem(h + c) * rstd, d = load_elem(dy + c);
+      const float g = d * (a.gamma_dtype == kBf16 ? load_elem(static_cast<const __nv_bfloat16*>(a.gamma) + c)
+                                                  : static_cast<const float*>(a.gamma)[c]);
+      if (part) part[c] = r == blockIdx.x ? d * n : part[c] + d * n;
       n_row[c] = n;
       g_row[c] = g;
       dot += g * n;
     }
-    first = false;
     if (a.dx) {
-      const float mean = block_reduce<false>(dot, warp_vals) / static_cast<float>(a.cols);
-      for (int64_t c = threadIdx.x; c < a.cols; c += kThreads) {
+      const float mean = row_reduce<kLongThreads, false>(dot, vals[parity]) / static_cast<float>(a.cols);
+      T* dx = static_cast<T*>(a.dx) + r * a.dx_ld;
+      for (int64_t c = threadIdx.x; c < a.cols; c += kLongThreads) {
         float v = rstd * (g_row[c] - n_row[c] * mean);
-        if (a.dh) v += load_elem(a.dh, r * a.dh_ld + c, a.dtype);
-        store_elem(a.dx, r * a.dx_ld + c, a.dtype, v);
+        if (a.dh) v += load_elem(static_cast<const T*>(a.dh) + r * a.dh_ld + c);
+        store_elem(dx + c, v);
       }
-      __syncthreads();
     }
   }
 }
 
-__global__ void __launch_bounds__(kThreads)
+// dgamma (+)= the partial sums, in a fixed order: a CTA takes 32 columns, its
+// 8 warps every eighth partial row, and the warps' sums are added in order.
+__global__ void __launch_bounds__(256)
 dgamma_kernel(const float* partial, int n_partial, int64_t cols, float* dgamma, int accumulate) {
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (c >= cols) return;
+  __shared__ float sums[8][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float s = 0.f;
-  for (int p = 0; p < n_partial; ++p) s += partial[static_cast<int64_t>(p) * cols + c];
-  dgamma[c] = accumulate ? dgamma[c] + s : s;
+  if (c < cols) {
+#pragma unroll 8
+    for (int p = warp; p < n_partial; p += 8) s += partial[static_cast<int64_t>(p) * cols + c];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < cols) {
+    for (int w = 1; w < 8; ++w) s += sums[w][lane];
+    dgamma[c] = accumulate ? dgamma[c] + s : s;
+  }
+}
+
+// -------------------------------------------------------------- launches --
+
+bool aligned(const void* p, int64_t ld, int64_t rows, int es, int bytes) {
+  return (reinterpret_cast<uintptr_t>(p) % bytes) == 0 && (rows <= 1 || (ld * es) % bytes == 0);
+}
+
+// Raises a kernel's shared-memory limit once per thread and device.
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+  static thread_local int configured_dev = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev == configured_dev) return e;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) configured_dev = dev;
+  return e;
+}
+
+template <typename T, int kTPR, int kNV>
+cudaError_t forward_config(const RmsnormArgs& a, bool vec, cudaStream_t stream) {
+  constexpr int kThreads = kTPR == 32 ? 256 : kTPR;
+  constexpr int kRows = kThreads / kTPR;
+  const unsigned grid = static_cast<unsigned>((a.rows + kRows - 1) / kRows);
+  if (vec) rmsnorm_kernel<T, kTPR, kNV, true><<<grid, kThreads, 0, stream>>>(a);
+  else rmsnorm_kernel<T, kTPR, kNV, false><<<grid, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t forward_typed(const RmsnormArgs& a, cudaStream_t stream) {
+  const int es = static_cast<int>(sizeof(T));
+  const bool vec = a.cols % 8 == 0 && aligned(a.x, a.x_ld, a.rows, es, 16) &&
+                   aligned(a.residual, a.residual_ld, a.residual ? a.rows : 1, es, 16) &&
+                   aligned(a.h, a.h_ld, a.h ? a.rows : 1, es, 16) && aligned(a.y, a.y_ld, a.y ? a.rows : 1, 2, 16) &&
+                   aligned(a.q, a.q_ld, a.q ? a.rows : 1, 1, 8) && aligned(a.gamma, 0, 1, 1, 16);
+  if (a.cols <= 256) return forward_config<T, 32, 1>(a, vec, stream);
+  if (a.cols <= 512) return forward_config<T, 32, 2>(a, vec, stream);
+  if (a.cols <= 1024) return forward_config<T, 32, 4>(a, vec, stream);
+  if (a.cols <= 2048) return forward_config<T, 128, 2>(a, vec, stream);
+  if (a.cols <= 4096) return forward_config<T, 256, 2>(a, vec, stream);
+  if (a.cols <= 8192) return forward_config<T, 512, 2>(a, vec, stream);
+  if (a.cols <= kRegisterCols) return forward_config<T, 512, 4>(a, vec, stream);
+  const cudaError_t e = allow_smem<rmsnorm_long_kernel<T>>(static_cast<int>(kNormMaxCols * sizeof(float)));
+  if (e != cudaSuccess) return e;
+  rmsnorm_long_kernel<T><<<static_cast<unsigned>(a.rows), kLongThreads, a.cols * sizeof(float), stream>>>(a);
+  return cudaGetLastError();
+}
+
+// CTAs of a kernel that the GPU holds at a time (kept per thread and device).
+template <auto kKernel>
+int resident_ctas(int threads) {
+  static thread_local int cached_dev = -1, cached = 1;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  if (dev != cached_dev) {
+    int per_sm = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kKernel, threads, 0) != cudaSuccess || per_sm < 1)
+      per_sm = 1;
+    cached = per_sm * num_sms();
+    cached_dev = dev;
+  }
+  return cached;
+}
+
+template <typename T, int kTPR, int kNV, bool kVec>
+cudaError_t grad_launch(const RmsnormGradArgs& a, int* grid, cudaStream_t stream) {
+  constexpr int kThreads = kTPR == 32 ? 256 : kTPR;
+  constexpr int kRows = kThreads / kTPR;
+  int64_t n = (a.rows + kRows - 1) / kRows;
+  const int64_t most = resident_ctas<rmsnorm_grad_kernel<T, kTPR, kNV, kVec>>(kThreads);
+  if (n > most) n = most;
+  if (n > kNormPartialRows) n = kNormPartialRows;
+  *grid = static_cast<int>(n);
+  rmsnorm_grad_kernel<T, kTPR, kNV, kVec><<<*grid, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int kTPR, int kNV>
+cudaError_t grad_config(const RmsnormGradArgs& a, bool vec, int* grid, cudaStream_t stream) {
+  return vec ? grad_launch<T, kTPR, kNV, true>(a, grid, stream) : grad_launch<T, kTPR, kNV, false>(a, grid, stream);
+}
+
+template <typename T>
+cudaError_t grad_typed(const RmsnormGradArgs& a, int* grid, cudaStream_t stream) {
+  const int es = static_cast<int>(sizeof(T));
+  const bool vec = a.cols % 8 == 0 && aligned(a.h, a.h_ld, a.rows, es, 16) && aligned(a.dy, a.dy_ld, a.rows, 2, 16) &&
+                   aligned(a.dh, a.dh_ld, a.dh ? a.rows : 1, es, 16) &&
+                   aligned(a.dx, a.dx_ld, a.dx ? a.rows : 1, es, 16) && aligned(a.gamma, 0, 1, 1, 16);
+  if (a.cols <= 256) return grad_config<T, 32, 1>(a, vec, grid, stream);
+  if (a.cols <= 512) return grad_config<T, 32, 2>(a, vec, grid, stream);
+  if (a.cols <= 1024) return grad_config<T, 32, 4>(a, vec, grid, stream);
+  if (a.cols <= 2048) return grad_config<T, 128, 2>(a, vec, grid, stream);
+  if (a.cols <= 4096) return grad_config<T, 256, 2>(a, vec, grid, stream);
+  if (a.cols <= 8192) return grad_config<T, 512, 2>(a, vec, grid, stream);
+  if (a.cols <= kRegisterCols) return grad_config<T, 512, 4>(a, vec, grid, stream);
+  const cudaError_t e = allow_smem<rmsnorm_grad_long_kernel<T>>(static_cast<int>(2 * kNormGradMaxCols * sizeof(float)));
+  if (e != cudaSuccess) return e;
+  const int64_t n = a.rows < num_sms() ? a.rows : num_sms();
+  *grid = static_cast<int>(n < kNormPartialRows ? n : kNormPartialRows);
+  rmsnorm_grad_long_kernel<T><<<*grid, kLongThreads, 2 * a.cols * sizeof(float), stream>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_rmsnorm(const RmsnormArgs& a, cudaStream_t stream) {
   if (a.rows <= 0) return cudaSuccess;
-  const int smem = static_cast<int>(a.cols * sizeof(float));
-  cudaError_t e = cudaFuncSetAttribute(rmsnorm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  const int64_t grid = a.rows < (int64_t(1) << 30) ? a.rows : (int64_t(1) << 30);
-  rmsnorm_kernel<<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  return a.dtype == kBf16 ? forward_typed<__nv_bfloat16>(a, stream) : forward_typed<float>(a, stream);
 }
 
 cudaError_t launch_rmsnorm_grad(const RmsnormGradArgs& a, cudaStream_t stream) {
-  const int64_t grid = a.rows < kNormPartialRows ? a.rows : kNormPartialRows;
-  if (grid > 0) {
-    const int smem = static_cast<int>(2 * a.cols * sizeof(float));
-    cudaError_t e = cudaFuncSetAttribute(rmsnorm_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+  int grid = 0;
+  if (a.rows > 0) {
     prof_begin(OPT_KERNEL_RMSNORM_GRAD, 1, a.rows, a.cols, stream);
-    rmsnorm_grad_kernel<<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(a);
+    const cudaError_t e =
+        a.dtype == kBf16 ? grad_typed<__nv_bfloat16>(a, &grid, stream) : grad_typed<float>(a, &grid, stream);
     prof_end(stream);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (e != cudaSuccess) return e;
   }
   if (!a.dgamma) return cudaSuccess;
   prof_begin(OPT_KERNEL_RMSNORM_DGAMMA, 1, a.rows, a.cols, stream);
-  dgamma_kernel<<<static_cast<unsigned>((a.cols + kThreads - 1) / kThreads), kThreads, 0, stream>>>(
-      a.partial, static_cast<int>(grid), a.cols, a.dgamma, a.accumulate);
+  dgamma_kernel<<<static_cast<unsigned>((a.cols + 31) / 32), 256, 0, stream>>>(a.partial, grid, a.cols, a.dgamma,
+                                                                               a.accumulate);
   prof_end(stream);
   return cudaGetLastError();
 }
