@@ -268,11 +268,47 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_long_kernel(const __grid
 
 // ------------------------------------------------------------- gradient --
 
+// A group of 8 elements as loaded: bf16 stays packed until it is used, so that
+// a thread holds a row of h, dy and dh in few registers and more CTAs fit.
+template <typename T, bool kVec>
+struct Raw {
+  float v[8];
+  template <int kTPR>
+  __device__ __forceinline__ void load(const T* row, int i, int t, int64_t cols) {
+    load_group<kTPR, kVec>(row, i, t, cols, v);
+  }
+  __device__ __forceinline__ void get(float (&out)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) out[j] = v[j];
+  }
+};
+template <>
+struct Raw<__nv_bfloat16, true> {
+  uint4 w;
+  template <int kTPR>
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, int i, int t, int64_t cols) {
+    const int64_t c = column<kTPR, true>(i, 0, t);
+    w = c < cols ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(float (&out)[8]) const { unpack8(w, out); }
+};
+
 // CTA b takes rows b, b + gridDim.x, ... (kRows at a time when a row belongs to
-// a warp); a thread's columns stay the same, so gamma and its part of dgamma
-// stay in registers, and the CTA writes its partial sums once.
+// a warp); a thread's columns stay the same, so its part of dgamma stays in
+// registers, and the CTA writes its partial sums once.  gamma is read again for
+// every row (from L1): keeping it would cost the registers of one more CTA.
+// CTAs that shall fit on an SM: registers for 64 (bf16) or 80 (fp32) a thread
+// at 16 columns each, half as many CTAs at 32.
 template <typename T, int kTPR, int kNV, bool kVec>
-__global__ void __launch_bounds__(kTPR == 32 ? 256 : kTPR)
+constexpr int grad_ctas() {
+  if (!kVec || kNV > 2) return kTPR == 32 && kNV > 2 ? 2 : 1;
+  const int threads = kTPR == 32 ? 256 : kTPR;
+  const int n = (sizeof(T) == 2 ? 1024 : 768) / threads;
+  return n < 1 ? 1 : n;
+}
+
+template <typename T, int kTPR, int kNV, bool kVec>
+__global__ void __launch_bounds__(kTPR == 32 ? 256 : kTPR, (grad_ctas<T, kTPR, kNV, kVec>()))
 rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
   constexpr int kThreads = kTPR == 32 ? 256 : kTPR;
   constexpr int kRows = kThreads / kTPR;
@@ -281,49 +317,63 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
   const int t = threadIdx.x % kTPR, sub = threadIdx.x / kTPR;
   const int64_t cols = a.cols;
   const float inv_cols = 1.f / static_cast<float>(cols);
-  float gamma[kNV][8], part[kNV][8];
+  float part[kNV][8];
 #pragma unroll
-  for (int i = 0; i < kNV; ++i) {
-    load_gamma<kTPR, kVec>(a.gamma, a.gamma_dtype, i, t, cols, gamma[i]);
+  for (int i = 0; i < kNV; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) part[i][j] = 0.f;
-  }
   int parity = 0;
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + sub; r < a.rows;
        r += static_cast<int64_t>(gridDim.x) * kRows, parity ^= 1) {
     const float rstd = a.rstd[r];
-    const T* h = static_cast<const T*>(a.h) + r * a.h_ld;
-    const __nv_bfloat16* dy = reinterpret_cast<const __nv_bfloat16*>(a.dy) + r * a.dy_ld;
-    float n[kNV][8], g[kNV][8];
+    Raw<T, kVec> h[kNV], dh[kNV];
+    Raw<__nv_bfloat16, kVec> dy[kNV];
+    {
+      const T* hp = static_cast<const T*>(a.h) + r * a.h_ld;
+      const __nv_bfloat16* yp = reinterpret_cast<const __nv_bfloat16*>(a.dy) + r * a.dy_ld;
 #pragma unroll
-    for (int i = 0; i < kNV; ++i) {
-      load_group<kTPR, kVec>(h, i, t, cols, n[i]);
-      load_group<kTPR, kVec>(dy, i, t, cols, g[i]);
+      for (int i = 0; i < kNV; ++i) {
+        h[i].template load<kTPR>(hp, i, t, cols);
+        dy[i].template load<kTPR>(yp, i, t, cols);
+      }
+      if (a.dh) {
+        const T* sp = static_cast<const T*>(a.dh) + r * a.dh_ld;
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) dh[i].template load<kTPR>(sp, i, t, cols);
+      }
     }
     float dot = 0.f;
 #pragma unroll
-    for (int i = 0; i < kNV; ++i)
+    for (int i = 0; i < kNV; ++i) {
+      float n[8], g[8], gamma[8];
+      load_gamma<kTPR, kVec>(a.gamma, a.gamma_dtype, i, t, cols, gamma);
+      h[i].get(n);
+      dy[i].get(g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        n[i][j] *= rstd;
-        part[i][j] += g[i][j] * n[i][j];
-        g[i][j] *= gamma[i][j];
-        dot += g[i][j] * n[i][j];
+        n[j] *= rstd;
+        const float p = g[j] * n[j];
+        part[i][j] += p;
+        dot += p * gamma[j];
       }
+    }
     if (a.dx) {
       const float mean = row_reduce<kTPR, false>(dot, vals[parity]) * inv_cols;
       T* dx = static_cast<T*>(a.dx) + r * a.dx_ld;
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
-        float d[8];
+        float n[8], g[8], gamma[8], d[8];
+        load_gamma<kTPR, kVec>(a.gamma, a.gamma_dtype, i, t, cols, gamma);
+        h[i].get(n);
+        dy[i].get(g);
         if (a.dh) {
-          load_group<kTPR, kVec>(static_cast<const T*>(a.dh) + r * a.dh_ld, i, t, cols, d);
+          dh[i].get(d);
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) d[j] = 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] += rstd * (g[i][j] - n[i][j] * mean);
+        for (int j = 0; j < 8; ++j) d[j] += rstd * (g[j] * gamma[j] - n[j] * rstd * mean);
         store_group<kTPR, kVec>(dx, i, t, cols, d);
       }
     }
