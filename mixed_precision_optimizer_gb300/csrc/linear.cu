@@ -9,13 +9,9 @@
 // stored [k][index] (w in dx, both operands of dw) MN-major: no transposed
 // copy is made.
 //
-// linear_pair_kernel takes large products (below).  linear_kernel takes the
-// others, one CTA per 128 x 128 tile: warp 0 loads k-blocks of 128 bytes by
-// TMA into a ring, warp 1 issues the MMAs, warps 2-5 run the epilogue, with
-// the lanes on `a`: a warp's accesses of one row are contiguous whatever the
-// row distance and alignment.
-// Out-of-range rows and columns are filled with zeros by the TMA and never
-// stored.
+// linear_pair_kernel takes large products, linear_split_kernel the others.
+// Both load k-blocks of 128 bytes by TMA; out-of-range rows and columns are
+// filled with zeros there and never stored.
 
 #include <cuda_bf16.h>
 
@@ -26,23 +22,11 @@
 namespace mpopt {
 namespace {
 
-constexpr int BM = 128;                        // A indices of a tile (TMEM lanes)
-constexpr int BN = 128;                        // B indices of a tile (TMEM columns)
-constexpr int kStages = 6;
+constexpr int BM = 128;                        // TMEM lanes of a CTA: output indices of the MMA's A operand
 constexpr int kStageA = BM * kRowBytes;
-constexpr int kStageB = BN * kRowBytes;
+constexpr int kPairBNHalf = 128;               // pair kernel: columns staged by one CTA
+constexpr int kStageB = kPairBNHalf * kRowBytes;
 constexpr int kStageBytes = kStageA + kStageB;
-constexpr int kEpiWarps = 4;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kTmemCols = BN;
-constexpr uint32_t kSmemBytes = kStages * kStageBytes + 1024 /*align*/ + 256 /*barriers*/;
-static_assert(kSmemBytes <= 232448, "dynamic shared memory above the 227 KB a CTA may use");
-
-struct LinearParams {
-  LinearArgs g;
-  int k_blocks;
-  int64_t tiles_a;
-};
 
 // ------------------------------------------------------------ activations --
 
@@ -170,13 +154,14 @@ __device__ __forceinline__ LaneColumn lane_column(const LinearArgs& g, int64_t a
   return c;
 }
 
-// kN accumulator columns: column j is output row b0 + j, this lane output
-// column c.a; a warp's accesses of one column are contiguous.
+// The first n (at most kN) of v's accumulator columns: column j is output row
+// b0 + j, this lane output column c.a; a warp's accesses of one column are
+// contiguous.
 template <int kMode, bool kFp8, int kN>
-__device__ __forceinline__ void epilogue_columns(const LinearArgs& g, const LaneColumn& c, int64_t b0,
+__device__ __forceinline__ void epilogue_columns(const LinearArgs& g, const LaneColumn& c, int64_t b0, int n,
                                                  const float* v) {
   if (c.a >= g.na) return;
-  const int n = static_cast<int>(g.nb - b0 < kN ? g.nb - b0 : kN);
+  n = static_cast<int>(g.nb - b0 < n ? g.nb - b0 : n);
   if constexpr (kMode == kLinearDw) {
     float* p = g.dw + b0 * g.dw_ld + c.a;
     float old[kN];
@@ -235,38 +220,94 @@ struct Order {
   static constexpr bool b_mn = kMode == kLinearDw;
 };
 
-// ---------------------------------------------------------------- kernel --
+// ----------------------------------------------------------- split kernel --
+//
+// Products with too few 256 x 256 tiles for the pair kernel: from one token,
+// where the time is that of reading the weights once, to a few hundred.  A CTA
+// computes 128 output columns (the lanes) x kBN output rows (16 to 128, so that
+// a few tokens do not pay for a wide tile).  Where the tiles are too few for
+// the GPU, a cluster of 2, 4 or 8 CTAs splits the k-blocks of one tile and
+// joins the partial sums through distributed shared memory: rank r adds the
+// ranks' sums of its share of the rows in rank order and runs their epilogue,
+// so the result does not depend on timing and needs no workspace or second
+// launch.  About 100 KB of shared memory a CTA, so that two fit on an SM and
+// one's start and end overlap the other's main loop.
+//   warp 0     TMA producer      warp 1     TMEM allocation, MMA issuer
+//   warps 2-5  epilogue, one TMEM lane quarter each
+// dw runs in segments as in the pair kernel (below).
 
-template <int kMode, bool kFp8>
-__global__ void __launch_bounds__(kThreads, 1)
-linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-              const __grid_constant__ LinearParams P) {
+constexpr int kSplitEpiWarps = 4;
+constexpr int kSplitThreads = 64 + 32 * kSplitEpiWarps;
+constexpr int kMaxSplit = 8;
+constexpr int kDwSegment = 12;               // k-blocks of dw accumulated in TMEM at a time
+
+template <int kBN>
+struct SplitConfig {
+  static constexpr int kStageB = kBN * kRowBytes;
+  static constexpr int kStageBytes = kStageA + kStageB;
+  static constexpr int kStages = kBN <= 16 ? 6 : kBN <= 32 ? 5 : kBN <= 64 ? 4 : 3;
+  static constexpr uint32_t kSmemBytes = kStages * kStageBytes + 1024 /*align*/ + 256 /*barriers*/;
+  static constexpr int kTmemCols = 2 * kBN < 32 ? 32 : 2 * kBN;     // two accumulators
+  static_assert(kSmemBytes <= 116224, "two CTAs shall fit on an SM");
+  static_assert(BM * kBN * 4 <= kStages * kStageBytes, "partial sums larger than the ring they replace");
+};
+
+struct SplitParams {
+  LinearArgs g;
+  int k_blocks;        // of the whole product
+  int per_rank;        // k-blocks of one CTA of the cluster
+  int segment;         // k-blocks accumulated in TMEM at a time
+  int split;           // CTAs per cluster
+  int64_t tiles_a;
+};
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+template <int kMode, bool kFp8, int kBN>
+__global__ void __launch_bounds__(kSplitThreads, 2)
+linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                    const __grid_constant__ SplitParams P) {
+  using C = SplitConfig<kBN>;
+  constexpr int kElems = kFp8 ? 128 : 64;
+  constexpr bool a_mn = Order<kMode>::a_mn, b_mn = Order<kMode>::b_mn;
+  static_assert(!b_mn || kBN % 64 == 0, "MN-major rows are staged 64 at a time");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
-  uint64_t* empty = full + kStages;
-  uint64_t* acc_full = empty + kStages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* acc_full = empty + C::kStages;     // [2]
+  uint64_t* acc_empty = acc_full + 2;          // [2]
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* status = P.g.header;
-  constexpr int kElems = kFp8 ? 128 : 64;
-  constexpr bool a_mn = Order<kMode>::a_mn, b_mn = Order<kMode>::b_mn;
-  const int64_t a0 = static_cast<int64_t>(blockIdx.x % P.tiles_a) * BM;
-  const int64_t b0 = static_cast<int64_t>(blockIdx.x / P.tiles_a) * BN;
+  const int rank = P.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int64_t tile = blockIdx.x / P.split;
+  const int64_t a0 = tile % P.tiles_a * BM, b0 = tile / P.tiles_a * kBN;
+  // this CTA's k-blocks; the last ranks may have none, and their sums are zero
+  const int kb0 = min(rank * P.per_rank, P.k_blocks), kb1 = min(kb0 + P.per_rank, P.k_blocks);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
-    mbar_init(smem_u32(acc_full), 1);
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&acc_full[a]), 1);
+      mbar_init(smem_u32(&acc_empty[a]), 32 * kSplitEpiWarps);
+    }
+    mbar_init(smem_u32(drain), 1);
     *abort_flag = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"(kTmemCols)
+                 "r"(C::kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -274,24 +315,29 @@ linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), acc_bar = smem_u32(acc_full);
+  const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+  const uint32_t sa0 = smem_u32(smem), sb0 = sa0 + C::kStages * kStageA;
+  const int quarter = warp & 3;
+  const LaneColumn col = lane_column<kMode, kFp8>(P.g, a0 + quarter * 32 + lane);
+  constexpr int kSum = kMode == kLinearDw ? kBN : 1;
+  float sum[kSum];
+  bool ready = false;          // epilogue warps: the accumulator holds this CTA's sums
 
   if (warp == 0) {
     if (lane == 0) {
-      const uint32_t sa0 = smem_u32(smem), sb0 = sa0 + kStages * kStageA;
       uint32_t s = 0, ph = 0;
-      int kb = 0;
-      for (; kb < P.k_blocks; ++kb) {
+      int kb = kb0;
+      for (; kb < kb1; ++kb) {
         if (!mbar_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, status, kStatusTimeoutEmpty)) break;
-        mbar_expect_tx(full0 + 8 * s, kStageBytes);
+        mbar_expect_tx(full0 + 8 * s, C::kStageBytes);
         load_operand(sa0 + s * kStageA, &map_a, full0 + 8 * s, a_mn, static_cast<int>(a0), BM, kb, kElems);
-        load_operand(sb0 + s * kStageB, &map_b, full0 + 8 * s, b_mn, static_cast<int>(b0), BN, kb, kElems);
-        if (++s == kStages) {
+        load_operand(sb0 + s * C::kStageB, &map_b, full0 + 8 * s, b_mn, static_cast<int>(b0), kBN, kb, kElems);
+        if (++s == C::kStages) {
           s = 0;
           ph ^= 1u;
         }
       }
-      if (kb < P.k_blocks) {
+      if (kb < kb1) {
         // aborting: give copies in flight time to land before the CTA exits
         const unsigned long long t0 = global_ns();
         while (global_ns() - t0 < 10000000ull) {
@@ -299,31 +345,42 @@ linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = linear_idesc(kFp8, a_mn, b_mn, BM, BN);
-      const uint32_t sa0 = smem_u32(smem), sb0 = sa0 + kStages * kStageA;
+    if (lane == 0 && kb1 > kb0) {
+      constexpr uint32_t idesc = linear_idesc(kFp8, a_mn, b_mn, BM, kBN);
       const uint64_t ad0 = a_mn ? smem_desc_mn(sa0) : smem_desc(sa0);
       const uint64_t bd0 = b_mn ? smem_desc_mn(sb0) : smem_desc(sb0);
       // one MMA's K step: 32 bytes of a K-major row, or 16 rows of an MN-major block
-      const uint32_t ka = (a_mn ? 16 * kRowBytes : 32) >> 4, kb_step = (b_mn ? 16 * kRowBytes : 32) >> 4;
-      uint32_t s = 0, ph = 0;
-      for (int kb = 0; kb < P.k_blocks; ++kb) {
-        if (!mbar_wait(full0 + 8 * s, ph, abort_flag, status, kStatusTimeoutFull)) break;
+      constexpr uint32_t ka = (a_mn ? 16 * kRowBytes : 32) >> 4, kbs = (b_mn ? 16 * kRowBytes : 32) >> 4;
+      uint32_t s = 0, ph = 0, use = 0;
+      bool ok = true;
+      for (int k0 = kb0; ok && k0 < kb1; k0 += P.segment, ++use) {
+        const uint32_t acc = use & 1;
+        if (!mbar_wait(smem_u32(&acc_empty[acc]), ((use >> 1) & 1u) ^ 1u, abort_flag, status, kStatusTimeoutAccFree))
+          break;
         tc_fence_after();
-        const uint64_t ad = ad0 + s * (kStageA >> 4), bd = bd0 + s * (kStageB >> 4);
+        const uint32_t d_tmem = tmem_base + acc * kBN;
+        const int k1 = min(k0 + P.segment, kb1);
+        for (int kb = k0; kb < k1; ++kb) {
+          if (!mbar_wait(full0 + 8 * s, ph, abort_flag, status, kStatusTimeoutFull)) {
+            ok = false;
+            break;
+          }
+          const uint64_t ad = ad0 + s * (kStageA >> 4), bd = bd0 + s * (C::kStageB >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_1cta<kFp8>(tmem_base, ad + ka * kk, bd + kb_step * kk, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
-        commit_1cta(empty0 + 8 * s);
-        if (++s == kStages) {
-          s = 0;
-          ph ^= 1u;
+          for (int kk = 0; kk < 4; ++kk)
+            mma_1cta<kFp8>(d_tmem, ad + ka * kk, bd + kbs * kk, idesc, (kb > k0 || kk > 0) ? 1u : 0u);
+          commit_1cta(empty0 + 8 * s);
+          if (++s == C::kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
+        if (ok) commit_1cta(smem_u32(&acc_full[acc]));
       }
-      // also after an aborted loop: the MMAs issued complete before TMEM goes
-      commit_1cta(acc_bar);
+      // every MMA issued by this thread has completed before TMEM goes
+      commit_1cta(smem_u32(drain));
       const unsigned long long t0 = global_ns();
-      while (!mbar_try(acc_bar, 0)) {
+      while (!mbar_try(smem_u32(drain), 0)) {
         if (global_ns() - t0 > kWaitLimitNs) {
           *abort_flag = 1u;
           atomicCAS(status, 0u, static_cast<uint32_t>(kStatusTimeoutDrain));
@@ -332,23 +389,95 @@ linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
       }
     }
   } else {
-    const int quarter = warp & 3;
-    const bool ready = mbar_wait(acc_bar, 0, abort_flag, status, kStatusTimeoutAcc) && !*abort_flag;
-    if (__all_sync(0xffffffffu, ready)) {
+#pragma unroll
+    for (int c = 0; c < kSum; ++c) sum[c] = 0.f;
+    uint32_t use = 0;
+    ready = true;
+    for (int k0 = kb0; ready && k0 < kb1; k0 += P.segment, ++use) {
+      const uint32_t acc = use & 1;
+      ready = __all_sync(0xffffffffu, mbar_wait(smem_u32(&acc_full[acc]), (use >> 1) & 1u, abort_flag, status,
+                                                kStatusTimeoutAcc));
+      if (!ready) break;
       tc_fence_after();
-      const LaneColumn col = lane_column<kMode, kFp8>(P.g, a0 + quarter * 32 + lane);
-      for (int c = 0; c < BN && b0 + c < P.g.nb; c += 32) {
-        float v[32];
-        tmem_ld32(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + c, v);
-        epilogue_columns<kMode, kFp8, 32>(P.g, col, b0 + c, v);
+      if constexpr (kMode == kLinearDw) {
+#pragma unroll
+        for (int c = 0; c < kBN; c += 16) {
+          float v[16];
+          tmem_ld16(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * kBN + c, v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sum[c + j] += v[j];
+        }
+        tc_fence_before();
+        mbar_arrive_local(smem_u32(&acc_empty[acc]));
       }
     }
+  }
+
+  __syncwarp();
+  // columns c .. c + 15 of this CTA's own sums
+  auto own_sums = [&](int c, float (&v)[16]) {
+    if constexpr (kMode == kLinearDw) {
+#pragma unroll
+      for (int k = 0; k < kBN; k += 16)
+        if (k == c)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = sum[k + j];
+    } else if (kb1 > kb0) {
+      tmem_ld16(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + c, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = 0.f;
+    }
+  };
+  if (P.split == 1) {
+    if (ready) {
+#pragma unroll
+      for (int c = 0; c < kBN; c += 16) {
+        if (b0 + c >= P.g.nb) break;
+        float v[16];
+        own_sums(c, v);
+        epilogue_columns<kMode, kFp8, 16>(P.g, col, b0 + c, 16, v);
+      }
+    }
+  } else {
+    // the sums take the place of the ring: its MMAs have completed (acc_full)
+    float* part = reinterpret_cast<float*>(smem);        // [kBN][BM]
+    if (ready) {
+#pragma unroll
+      for (int c = 0; c < kBN; c += 16) {
+        float v[16];
+        own_sums(c, v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(c + j) * BM + quarter * 32 + lane] = v[j];
+      }
+    }
+    cluster_sync();
+    if (ready) {
+      const int per = kBN / P.split;                     // 2 at least
+      uint32_t peer[kMaxSplit];
+#pragma unroll
+      for (int p = 0; p < kMaxSplit; ++p)
+        peer[p] = p < P.split ? peer_addr(smem_u32(part), static_cast<uint32_t>(p)) : 0u;
+      for (int c = rank * per; c < (rank + 1) * per && b0 + c < P.g.nb; c += 2) {
+        const uint32_t off = (c * BM + quarter * 32 + lane) * 4;
+        float v[2] = {0.f, 0.f};
+#pragma unroll
+        for (int p = 0; p < kMaxSplit; ++p)
+          if (p < P.split) {
+            v[0] += ld_cluster_f32(peer[p] + off);
+            v[1] += ld_cluster_f32(peer[p] + off + BM * 4);
+          }
+        epilogue_columns<kMode, kFp8, 2>(P.g, col, b0 + c, 2, v);
+      }
+    }
+    cluster_sync();          // no CTA leaves while another reads its sums
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::kTmemCols)
+                 : "memory");
   }
 }
 
@@ -370,7 +499,7 @@ linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
 // Here a TMEM lane is an output row `b` and a TMEM column an output column
 // `a`: a lane's 32 columns pack into 16-byte pieces of its row, are staged in
 // shared memory and leave by TMA stores (main_grad += by TMA reductions, one
-// addition per element).  With the lanes on `a`, as in linear_kernel, each
+// addition per element).  With the lanes on `a`, as in the split kernel, each
 // column was a 64-byte store of its own and the epilogue, not the MMAs, set
 // the pace: 22 us per tile whatever k was, against 17 us of MMAs at k = 4096.
 // Outputs that TMA cannot address (base or row distance not a multiple of 16
@@ -390,7 +519,6 @@ constexpr int kPairBN = 256;
 constexpr int kPairEpiWarps = 8;
 constexpr int kPairThreads = 96 + 32 * kPairEpiWarps;
 constexpr int kPairTmemCols = 512;
-constexpr int kDwSegment = 12;
 constexpr int kTileSlots = 3;
 constexpr int kWarpScratch = 4096;     // per epilogue warp: staged 32 x 32 blocks, bf16 y and z or fp32
 constexpr int kBlockBytes = 32 * 32 * 2;
@@ -645,7 +773,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
         if (tile >= P.total_tiles) break;
         int ta, tb;
         pair_tile(P, tile, ta, tb);
-        const int ai = tb * 256 + static_cast<int>(rank) * BM, bi = ta * kPairBN + static_cast<int>(rank) * BN;
+        const int ai = tb * 256 + static_cast<int>(rank) * BM, bi = ta * kPairBN + static_cast<int>(rank) * kPairBNHalf;
         for (int kb = 0; kb < P.k_blocks; ++kb) {
           if (!mbar_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, status, kStatusTimeoutEmpty)) {
             ok = false;
@@ -1037,47 +1165,83 @@ cudaError_t allow_smem(int bytes) {
 }
 
 template <int kMode, bool kFp8>
-cudaError_t launch_product(const LinearArgs& a, cudaStream_t stream) {
-  constexpr int kElems = kFp8 ? 128 : 64;
-  const int k_blocks = static_cast<int>((a.nk + kElems - 1) / kElems);
-  CUtensorMap ma, mb;
+cudaError_t launch_pair(const LinearArgs& a, int k_blocks, int tiles_a, int tiles_b, cudaStream_t stream) {
+  PairParams P{};
+  P.g = a;
+  P.k_blocks = k_blocks;
+  P.segment = kMode == kLinearDw ? kDwSegment : k_blocks;
+  P.tiles_a = tiles_a;
+  P.tiles_b = tiles_b;
+  P.total_tiles = tiles_a * tiles_b;
+  CUtensorMap ma, mb, mo{}, mz{};
   cudaError_t e;
-  if ((e = make_operand_map(&ma, a.A, a.na, a.nk, kFp8, BM)) != cudaSuccess) return e;
-  if ((e = make_operand_map(&mb, a.B, a.nb, a.nk, kFp8, BN)) != cudaSuccess) return e;
-  const int64_t pair_a = (a.na + 255) / 256, pair_b = (a.nb + kPairBN - 1) / kPairBN;
-  const int max_pairs = num_sms() / 2;
-  if (pair_a * pair_b >= max_pairs && pair_a * pair_b < (int64_t(1) << 30)) {
-    PairParams P{};
-    P.g = a;
-    P.k_blocks = k_blocks;
-    P.segment = kMode == kLinearDw ? kDwSegment : k_blocks;
-    P.tiles_a = static_cast<int>(pair_a);
-    P.tiles_b = static_cast<int>(pair_b);
-    P.total_tiles = static_cast<int>(pair_a * pair_b);
-    CUtensorMap mo{}, mz{};
-    if constexpr (kMode == kLinearDw) {
-      P.out_tma = make_block_map(&mo, a.dw, a.dw_ld, a.nb, a.na, true);
-    } else {
-      P.out_tma = make_block_map(&mo, a.y, a.y_ld, a.nb, a.na, false) &&
-                  (!a.z_out || make_block_map(&mz, a.z_out, a.z_ld, a.nb, a.na, false));
-      const uint16_t* in = kMode == kLinearDx ? a.z_in : a.residual;
-      const int64_t in_ld = kMode == kLinearDx ? a.z_ld : a.residual_ld;
-      P.in_vec = (reinterpret_cast<uintptr_t>(in) & 15u) == 0 && in_ld % 8 == 0;
-    }
-    if ((e = allow_smem<linear_pair_kernel<kMode, kFp8>>(kPairSmemBytes)) != cudaSuccess) return e;
-    const int grid = 2 * (P.total_tiles < max_pairs ? P.total_tiles : max_pairs);
-    linear_pair_kernel<kMode, kFp8><<<grid, kPairThreads, kPairSmemBytes, stream>>>(mb, ma, mo, mz, P);
-    return cudaGetLastError();
+  if ((e = make_operand_map(&ma, a.A, a.na, a.nk, kFp8, kPairBNHalf)) != cudaSuccess) return e;
+  if ((e = make_operand_map(&mb, a.B, a.nb, a.nk, kFp8, BM)) != cudaSuccess) return e;
+  if constexpr (kMode == kLinearDw) {
+    P.out_tma = make_block_map(&mo, a.dw, a.dw_ld, a.nb, a.na, true);
+  } else {
+    P.out_tma = make_block_map(&mo, a.y, a.y_ld, a.nb, a.na, false) &&
+                (!a.z_out || make_block_map(&mz, a.z_out, a.z_ld, a.nb, a.na, false));
+    const uint16_t* in = kMode == kLinearDx ? a.z_in : a.residual;
+    const int64_t in_ld = kMode == kLinearDx ? a.z_ld : a.residual_ld;
+    P.in_vec = (reinterpret_cast<uintptr_t>(in) & 15u) == 0 && in_ld % 8 == 0;
   }
-  LinearParams P{};
+  if ((e = allow_smem<linear_pair_kernel<kMode, kFp8>>(kPairSmemBytes)) != cudaSuccess) return e;
+  const int max_pairs = num_sms() / 2;
+  const int grid = 2 * (P.total_tiles < max_pairs ? P.total_tiles : max_pairs);
+  linear_pair_kernel<kMode, kFp8><<<grid, kPairThreads, kPairSmemBytes, stream>>>(mb, ma, mo, mz, P);
+  return cudaGetLastError();
+}
+
+template <int kMode, bool kFp8, int kBN>
+cudaError_t launch_split(const LinearArgs& a, int k_blocks, cudaStream_t stream) {
+  using C = SplitConfig<kBN>;
+  SplitParams P{};
   P.g = a;
   P.k_blocks = k_blocks;
   P.tiles_a = (a.na + BM - 1) / BM;
-  const int64_t grid = P.tiles_a * ((a.nb + BN - 1) / BN);
-  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  if ((e = allow_smem<linear_kernel<kMode, kFp8>>(kSmemBytes)) != cudaSuccess) return e;
-  linear_kernel<kMode, kFp8><<<static_cast<unsigned>(grid), kThreads, kSmemBytes, stream>>>(ma, mb, P);
-  return cudaGetLastError();
+  const int64_t tiles = P.tiles_a * ((a.nb + kBN - 1) / kBN);
+  // split while the clusters still run at once, two CTAs to an SM, and each
+  // CTA keeps 4 k-blocks (about the time its start and the join take)
+  P.split = 1;
+  while (P.split < kMaxSplit && tiles * P.split * 2 <= 2 * num_sms() && k_blocks >= P.split * 2 * 4) P.split *= 2;
+  P.per_rank = (k_blocks + P.split - 1) / P.split;
+  P.segment = kMode == kLinearDw ? kDwSegment : k_blocks;
+  if (tiles * P.split > 0x7fffffff) return cudaErrorInvalidValue;
+  CUtensorMap ma, mb;
+  cudaError_t e;
+  if ((e = make_operand_map(&ma, a.A, a.na, a.nk, kFp8, BM)) != cudaSuccess) return e;
+  if ((e = make_operand_map(&mb, a.B, a.nb, a.nk, kFp8, kBN)) != cudaSuccess) return e;
+  if ((e = allow_smem<linear_split_kernel<kMode, kFp8, kBN>>(C::kSmemBytes)) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * P.split));
+  cfg.blockDim = dim3(kSplitThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(P.split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, linear_split_kernel<kMode, kFp8, kBN>, ma, mb, P);
+}
+
+template <int kMode, bool kFp8>
+cudaError_t launch_product(const LinearArgs& a, cudaStream_t stream) {
+  constexpr int kElems = kFp8 ? 128 : 64;
+  const int k_blocks = static_cast<int>((a.nk + kElems - 1) / kElems);
+  // the pair kernel once every CTA pair has a tile
+  const int64_t pair_a = (a.na + kPairBN - 1) / kPairBN, pair_b = (a.nb + 255) / 256;
+  if (pair_a * pair_b >= num_sms() / 2 && pair_a * pair_b < (int64_t(1) << 30))
+    return launch_pair<kMode, kFp8>(a, k_blocks, static_cast<int>(pair_a), static_cast<int>(pair_b), stream);
+  if constexpr (kMode != kLinearDw) {
+    if (a.nb <= 16) return launch_split<kMode, kFp8, 16>(a, k_blocks, stream);
+    if (a.nb <= 32) return launch_split<kMode, kFp8, 32>(a, k_blocks, stream);
+    if (a.nb <= 64) return launch_split<kMode, kFp8, 64>(a, k_blocks, stream);
+  }
+  return launch_split<kMode, kFp8, 128>(a, k_blocks, stream);
 }
 
 }  // namespace

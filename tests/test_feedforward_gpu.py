@@ -218,7 +218,8 @@ def test_quantize_rows(rows, cols, dtype, layout):
 # ----------------------------------------------------------------- linear --
 
 LINEAR_SHAPES = [(1, 1, 1), (1, 8, 16), (2, 129, 65), (17, 64, 1023), (130, 257, 33), (64, 512, 256), (129, 128, 4096),
-                 (300, 1000, 777), (5, 300, 8200), (512, 768, 128), (1, 4096, 1024), (257, 513, 64), (31, 2049, 136)]
+                 (300, 1000, 777), (5, 300, 8200), (512, 768, 128), (1, 4096, 1024), (257, 513, 64), (31, 2049, 136),
+                 (3, 128, 2100), (40, 640, 4000), (200, 384, 1500)]
 
 
 def linear_case(m, n, k, e4m3, layout, seed=0):
