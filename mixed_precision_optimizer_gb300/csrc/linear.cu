@@ -431,12 +431,19 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
   };
   if (P.split == 1) {
     if (ready) {
+      constexpr int kN = kMode == kLinearDw || kBN < 32 ? 16 : 32;
 #pragma unroll
-      for (int c = 0; c < kBN; c += 16) {
+      for (int c = 0; c < kBN; c += kN) {
         if (b0 + c >= P.g.nb) break;
-        float v[16];
-        own_sums(c, v);
-        epilogue_columns<kMode, kFp8, 16>(P.g, col, b0 + c, 16, v);
+        float v[kN];
+#pragma unroll
+        for (int i = 0; i < kN; i += 16) {
+          float w[16];
+          own_sums(c + i, w);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[i + j] = w[j];
+        }
+        epilogue_columns<kMode, kFp8, kN>(P.g, col, b0 + c, kN, v);
       }
     }
   } else {
@@ -458,16 +465,27 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
 #pragma unroll
       for (int p = 0; p < kMaxSplit; ++p)
         peer[p] = p < P.split ? peer_addr(smem_u32(part), static_cast<uint32_t>(p)) : 0u;
-      for (int c = rank * per; c < (rank + 1) * per && b0 + c < P.g.nb; c += 2) {
+      // up to 16 rows at a time: their loads, from the peers and from global
+      // memory, overlap (2 at a time, a tile of 128 rows spent 20 us here)
+      constexpr int kN = kBN < 32 ? 8 : 16;
+      for (int c = rank * per; c < (rank + 1) * per && b0 + c < P.g.nb; c += kN) {
+        const int n = min(kN, (rank + 1) * per - c);
         const uint32_t off = (c * BM + quarter * 32 + lane) * 4;
-        float v[2] = {0.f, 0.f};
+        float v[kN];
+#pragma unroll
+        for (int j = 0; j < kN; ++j) v[j] = 0.f;
 #pragma unroll
         for (int p = 0; p < kMaxSplit; ++p)
           if (p < P.split) {
-            v[0] += ld_cluster_f32(peer[p] + off);
-            v[1] += ld_cluster_f32(peer[p] + off + BM * 4);
+            float w[kN];
+#pragma unroll
+            for (int j = 0; j < kN; ++j)
+              if (j < n) w[j] = ld_cluster_f32(peer[p] + off + j * (BM * 4));
+#pragma unroll
+            for (int j = 0; j < kN; ++j)
+              if (j < n) v[j] += w[j];
           }
-        epilogue_columns<kMode, kFp8, 2>(P.g, col, b0 + c, 2, v);
+        epilogue_columns<kMode, kFp8, kN>(P.g, col, b0 + c, n, v);
       }
     }
     cluster_sync();          // no CTA leaves while another reads its sums

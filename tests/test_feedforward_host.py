@@ -223,3 +223,12 @@ def test_python_checks():
         mp.linear_backward(b(2, 4), None, None)
     with pytest.raises(ValueError, match="CUDA"):
         mp.quantize_rows(f(2, 8), torch.zeros(2, 8, dtype=torch.float8_e4m3fn), f(2))
+
+
+def test_packed_arguments_match_the_structs():
+    """The functions pack their argument structs by format string: field by
+    field the same bytes as the ctypes structs of the header."""
+    for pack, cls in ((ff._PACK_NORM, ff.OptRmsnormArgs), (ff._PACK_NORM_GRAD, ff.OptRmsnormGradArgs),
+                      (ff._PACK_LINEAR, ff.OptLinearArgs), (ff._PACK_LINEAR_GRAD, ff.OptLinearGradArgs)):
+        vals = [0.5 if t is ctypes.c_float else 1 + i for i, (_, t) in enumerate(cls._fields_)]
+        assert pack(*vals) == bytes(cls(*vals))
