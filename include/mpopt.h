@@ -647,7 +647,8 @@ enum {
   OPT_KERNEL_LINEAR_DX = 17,
   OPT_KERNEL_LINEAR_DW = 18,
   OPT_KERNEL_LINEAR_DBIAS = 19,
-  OPT_KERNEL_LINEAR_REPACK = 20 /* an operand copied to 16-byte aligned rows     */
+  OPT_KERNEL_LINEAR_REPACK = 20 /* operands (count of them) copied to 16-byte
+                                   aligned rows; a, b of the largest             */
 };
 
 MPOPT_API opt_status opt_profile_launches(void* const* events, opt_launch_info* info, int32_t capacity,

@@ -60,30 +60,42 @@ bool tma_readable(const void* p, int64_t ld, int64_t rows, int es) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows <= 1 || (ld * es) % 16 == 0);
 }
 
-// Hands out the workspace behind the header to operand copies.
+// Hands out the workspace behind the header to operand copies; launch() makes
+// them all at once.
 struct Repacker {
   uint8_t* next;
   size_t left;
-  cudaStream_t stream;
+  int es;
+  RepackBatch batch{};
+  int64_t rows = 0, cols = 0;      // of the largest copy, for the launch record
 
   // `o` <- an operand of [rows][cols] elements that the TMA can read: the
   // caller's own, or a copy with 16-byte aligned rows.
-  opt_status operand(const void* p, int64_t ld, int64_t rows, int64_t cols, int es, int mn_major, LinearOperand* o) {
-    if (tma_readable(p, ld, rows, es)) {
-      *o = LinearOperand{p, rows > 1 ? ld : packed_ld(cols, es), mn_major};
+  opt_status operand(const void* p, int64_t ld, int64_t n_rows, int64_t n_cols, int mn_major, LinearOperand* o) {
+    if (tma_readable(p, ld, n_rows, es)) {
+      *o = LinearOperand{p, n_rows > 1 ? ld : packed_ld(n_cols, es), mn_major};
       return OPT_OK;
     }
-    const size_t bytes = packed_bytes(rows, cols, es);
+    const size_t bytes = packed_bytes(n_rows, n_cols, es);
     if (bytes > left) return OPT_ERR_WORKSPACE;
-    const int64_t dst_ld = packed_ld(cols, es);
-    prof_begin(OPT_KERNEL_LINEAR_REPACK, 1, rows, cols, stream);
-    const cudaError_t e = launch_repack(p, ld, next, dst_ld, rows, cols, es, stream);
-    prof_end(stream);
-    if (e != cudaSuccess) return cuda_status(e, "linear operand copy");
+    const int64_t dst_ld = packed_ld(n_cols, es);
+    batch.m[batch.n++] = RepackMatrix{p, next, ld, dst_ld, n_cols, n_rows * dst_ld * es / 16};
+    if (n_rows * n_cols > rows * cols) {
+      rows = n_rows;
+      cols = n_cols;
+    }
     *o = LinearOperand{next, dst_ld, mn_major};
     next += bytes;
     left -= bytes;
     return OPT_OK;
+  }
+
+  opt_status launch(cudaStream_t stream) {
+    if (batch.n == 0) return OPT_OK;
+    prof_begin(OPT_KERNEL_LINEAR_REPACK, batch.n, rows, cols, stream);
+    const cudaError_t e = launch_repack(batch, es, stream);
+    prof_end(stream);
+    return cuda_status(e, "linear operand copies");
   }
 };
 
@@ -224,12 +236,13 @@ opt_status opt_linear_forward(const opt_linear_args* a, void* workspace, size_t 
                       repack_need(a->w, a->w_ld, a->n, a->k, es);
   MPOPT_TRY(check_workspace(workspace, workspace_bytes, need));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  Repacker rp{static_cast<uint8_t*>(workspace) + kLinearHeaderBytes, workspace_bytes - kLinearHeaderBytes, st};
+  Repacker rp{static_cast<uint8_t*>(workspace) + kLinearHeaderBytes, workspace_bytes - kLinearHeaderBytes, es};
   LinearArgs g{};
   g.mode = kLinearForward;
   g.fp8 = fp8;
-  MPOPT_TRY(rp.operand(a->w, a->w_ld, a->n, a->k, es, 0, &g.A));
-  MPOPT_TRY(rp.operand(a->x, a->x_ld, a->m, a->k, es, 0, &g.B));
+  MPOPT_TRY(rp.operand(a->w, a->w_ld, a->n, a->k, 0, &g.A));
+  MPOPT_TRY(rp.operand(a->x, a->x_ld, a->m, a->k, 0, &g.B));
+  MPOPT_TRY(rp.launch(st));
   g.na = a->n;
   g.nb = a->m;
   g.nk = a->k;
@@ -278,13 +291,16 @@ opt_status opt_linear_backward(const opt_linear_grad_args* a, void* workspace, s
   if (a->dx || a->dw || sums) MPOPT_TRY(check_workspace(workspace, workspace_bytes, kLinearHeaderBytes + products + sums));
   uint8_t* const scratch = static_cast<uint8_t*>(workspace) + kLinearHeaderBytes;
   if (a->dx || a->dw) {
-    Repacker rp{scratch + sums, workspace_bytes - kLinearHeaderBytes - sums, st};
-    LinearOperand dz{};
-    MPOPT_TRY(rp.operand(a->dz, a->dz_ld, a->m, a->n, 2, 0, &dz));
+    Repacker rp{scratch + sums, workspace_bytes - kLinearHeaderBytes - sums, 2};
+    LinearOperand dz{}, w{}, x{};
+    MPOPT_TRY(rp.operand(a->dz, a->dz_ld, a->m, a->n, 0, &dz));
+    if (a->dx) MPOPT_TRY(rp.operand(a->w, a->w_ld, a->n, a->k, 1, &w));
+    if (a->dw) MPOPT_TRY(rp.operand(a->x, a->x_ld, a->m, a->k, 1, &x));
+    MPOPT_TRY(rp.launch(st));
     if (a->dx) {
       LinearArgs g{};
       g.mode = kLinearDx;
-      MPOPT_TRY(rp.operand(a->w, a->w_ld, a->n, a->k, 2, 1, &g.A));
+      g.A = w;
       g.B = dz;
       g.na = a->k;
       g.nb = a->m;
@@ -300,7 +316,7 @@ opt_status opt_linear_backward(const opt_linear_grad_args* a, void* workspace, s
     if (a->dw) {
       LinearArgs g{};
       g.mode = kLinearDw;
-      MPOPT_TRY(rp.operand(a->x, a->x_ld, a->m, a->k, 2, 1, &g.A));
+      g.A = x;
       g.B = dz;
       g.B.mn_major = 1;
       g.na = a->k;

@@ -325,9 +325,19 @@ inline int64_t column_sum_slices(int64_t m, int64_t n) {
 }
 cudaError_t launch_column_sums(const uint16_t* dz, int64_t ld, int64_t m, int64_t n, float* out, float* partial,
                                int accumulate, cudaStream_t stream);
-// dst rows (dst_ld elements apart) <- src rows, elements of `esize` bytes (1 or 2)
-cudaError_t launch_repack(const void* src, int64_t src_ld, void* dst, int64_t dst_ld, int64_t rows, int64_t cols,
-                          int esize, cudaStream_t stream);
+// Copies of operands with rows on 16 bytes: dst rows (dst_ld elements apart, a
+// multiple of 16 bytes) <- src rows, elements of 1 or 2 bytes, zeros behind them.
+struct RepackMatrix {
+  const void* src;
+  void* dst;
+  int64_t src_ld, dst_ld, cols;
+  int64_t pieces;        // rows * dst_ld / (elements in 16 bytes)
+};
+struct RepackBatch {
+  int n;
+  RepackMatrix m[3];
+};
+cudaError_t launch_repack(const RepackBatch& batch, int esize, cudaStream_t stream);
 
 // Records the CUDA error's text for opt_last_cuda_error; returns OPT_ERR_CUDA's value.
 int record_cuda_error(cudaError_t e, const char* where);

@@ -292,6 +292,14 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
   // this CTA's k-blocks; the last ranks may have none, and their sums are zero
   const int kb0 = min(rank * P.per_rank, P.k_blocks), kb1 = min(kb0 + P.per_rank, P.k_blocks);
 
+  const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+  const uint32_t sa0 = smem_u32(smem), sb0 = sa0 + C::kStages * kStageA;
+  // k-block kb into stage s, by the producer
+  auto load_stage = [&](int kb, uint32_t s) {
+    mbar_expect_tx(full0 + 8 * s, C::kStageBytes);
+    load_operand(sa0 + s * kStageA, &map_a, full0 + 8 * s, a_mn, static_cast<int>(a0), BM, kb, kElems);
+    load_operand(sb0 + s * C::kStageB, &map_b, full0 + 8 * s, b_mn, static_cast<int>(b0), kBN, kb, kElems);
+  };
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
@@ -304,6 +312,8 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    // the first loads fly while the CTA sets up: the ring is empty
+    for (int s = 0; s < C::kStages && kb0 + s < kb1; ++s) load_stage(kb0 + s, s);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -315,8 +325,6 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
-  const uint32_t sa0 = smem_u32(smem), sb0 = sa0 + C::kStages * kStageA;
   const int quarter = warp & 3;
   const LaneColumn col = lane_column<kMode, kFp8>(P.g, a0 + quarter * 32 + lane);
   constexpr int kSum = kMode == kLinearDw ? kBN : 1;
@@ -325,13 +333,11 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
 
   if (warp == 0) {
     if (lane == 0) {
-      uint32_t s = 0, ph = 0;
-      int kb = kb0;
+      uint32_t s = 0, ph = 0;                       // second time round the ring and on
+      int kb = kb0 + C::kStages;
       for (; kb < kb1; ++kb) {
-        if (!mbar_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, status, kStatusTimeoutEmpty)) break;
-        mbar_expect_tx(full0 + 8 * s, C::kStageBytes);
-        load_operand(sa0 + s * kStageA, &map_a, full0 + 8 * s, a_mn, static_cast<int>(a0), BM, kb, kElems);
-        load_operand(sb0 + s * C::kStageB, &map_b, full0 + 8 * s, b_mn, static_cast<int>(b0), kBN, kb, kElems);
+        if (!mbar_wait(empty0 + 8 * s, ph, abort_flag, status, kStatusTimeoutEmpty)) break;
+        load_stage(kb, s);
         if (++s == C::kStages) {
           s = 0;
           ph ^= 1u;
@@ -606,6 +612,8 @@ __device__ __forceinline__ void tma_add_block(const CUtensorMap* map, uint32_t s
                "r"(x), "r"(y), "r"(src)
                : "memory");
 }
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
@@ -964,7 +972,15 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       } else {
         const uint16_t* in = kMode == kLinearDx ? P.g.z_in : P.g.residual;
         const int64_t in_ld = kMode == kLinearDx ? P.g.z_ld : P.g.residual_ld;
+        const bool alternate = P.out_tma && (P.in_vec || !in) && !(kMode == kLinearForward && P.g.z_out) &&
+                               col0 + 128 <= P.g.na;      // no block of the tile goes through the table
         const bool live = row0 < P.g.nb;
+        // the tile's residual or pre-activation comes from DRAM while the MMAs run
+        if (in && row0 + lane < P.g.nb && col0 < P.g.na) {
+          const uint16_t* p = in + (row0 + lane) * in_ld + col0;
+          prefetch_l2(p);
+          if (col0 + 64 < P.g.na) prefetch_l2(p + 64);
+        }
         float row_scale = 1.f;
         if (kFp8 && row0 + lane < P.g.nb) row_scale = P.g.b_scale[row0 + lane];
         const uint32_t acc = use & 1;
@@ -975,10 +991,15 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
         tc_fence_after();
         for (int c = 0; c < 128 && live && col0 + c < P.g.na; c += 32) {
           const int64_t col = col0 + c;
-          // the staging area doubles as the turning table of inputs and outputs
-          // that cannot move 16 bytes at a time
-          if (lane == 0) bulk_wait_read_0();
+          // the staging area holds a block of y and one of z, or two of y in
+          // turn; it doubles as the turning table of inputs and outputs that
+          // cannot move 16 bytes at a time
+          if (lane == 0) {
+            if (alternate) bulk_wait_read_1();
+            else bulk_wait_read_0();
+          }
           __syncwarp();
+          uint8_t* const buf = alternate ? stage + (c & 32 ? kBlockBytes : 0) : stage;
           uint32_t raw[16];
           if (in) load_block(in, in_ld, row0, col, P.g.nb, P.g.na, P.in_vec != 0, reinterpret_cast<uint32_t*>(stage), lane, raw);
           float v[32];
@@ -1017,12 +1038,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
             }
           }
           if (P.out_tma) {
-            stage_bf16_rows(stage, lane, v);
+            stage_bf16_rows(buf, lane, v);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
               const int x = static_cast<int>(col), y = static_cast<int>(row0);
-              tma_store_block(&map_out, smem_u32(stage), x, y);
+              tma_store_block(&map_out, smem_u32(buf), x, y);
               if (kMode == kLinearForward && P.g.z_out) tma_store_block(&map_z, smem_u32(stage + kBlockBytes), x, y);
               bulk_commit();
             }
@@ -1125,11 +1146,24 @@ join_sums_kernel(const float* partial, int slices, int64_t n, float* out, int ac
   out[c] = accumulate ? out[c] + s : s;
 }
 
+// Operand copies with rows on 16 bytes, up to three in one launch.  A thread
+// writes one 16-byte piece of a row from as many single-element loads; a warp's
+// loads of one turn lie within 512 bytes of a row.
 template <typename T>
-__global__ void __launch_bounds__(256)
-repack_kernel(const T* src, int64_t src_ld, T* dst, int64_t dst_ld, int64_t rows, int64_t cols) {
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-    for (int64_t c = threadIdx.x; c < cols; c += 256) dst[r * dst_ld + c] = src[r * src_ld + c];
+__global__ void __launch_bounds__(256) repack_kernel(const __grid_constant__ RepackBatch batch) {
+  constexpr int kN = 16 / sizeof(T);
+  int64_t piece = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  int i = 0;
+  while (i < batch.n && piece >= batch.m[i].pieces) piece -= batch.m[i++].pieces;
+  if (i == batch.n) return;
+  const RepackMatrix& m = batch.m[i];
+  const int64_t per_row = m.dst_ld / kN;
+  const int64_t r = piece / per_row, c = (piece - r * per_row) * kN;
+  const T* src = static_cast<const T*>(m.src) + r * m.src_ld + c;
+  alignas(16) T v[kN];
+#pragma unroll
+  for (int j = 0; j < kN; ++j) v[j] = c + j < m.cols ? src[j] : T(0);
+  *reinterpret_cast<uint4*>(static_cast<T*>(m.dst) + r * m.dst_ld + c) = *reinterpret_cast<const uint4*>(v);
 }
 
 // -------------------------------------------------------------- host side --
@@ -1285,15 +1319,14 @@ cudaError_t launch_column_sums(const uint16_t* dz, int64_t ld, int64_t m, int64_
   return cudaGetLastError();
 }
 
-cudaError_t launch_repack(const void* src, int64_t src_ld, void* dst, int64_t dst_ld, int64_t rows, int64_t cols,
-                          int esize, cudaStream_t stream) {
-  const int64_t grid = rows < 65536 ? rows : 65536;
-  if (esize == 1)
-    repack_kernel<uint8_t><<<static_cast<unsigned>(grid), 256, 0, stream>>>(
-        static_cast<const uint8_t*>(src), src_ld, static_cast<uint8_t*>(dst), dst_ld, rows, cols);
-  else
-    repack_kernel<uint16_t><<<static_cast<unsigned>(grid), 256, 0, stream>>>(
-        static_cast<const uint16_t*>(src), src_ld, static_cast<uint16_t*>(dst), dst_ld, rows, cols);
+cudaError_t launch_repack(const RepackBatch& batch, int esize, cudaStream_t stream) {
+  int64_t pieces = 0;
+  for (int i = 0; i < batch.n; ++i) pieces += batch.m[i].pieces;
+  const int64_t grid = (pieces + 255) / 256;
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  if (grid == 0) return cudaSuccess;
+  if (esize == 1) repack_kernel<uint8_t><<<static_cast<unsigned>(grid), 256, 0, stream>>>(batch);
+  else repack_kernel<uint16_t><<<static_cast<unsigned>(grid), 256, 0, stream>>>(batch);
   return cudaGetLastError();
 }
 
