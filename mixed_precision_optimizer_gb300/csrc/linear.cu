@@ -154,26 +154,15 @@ __device__ __forceinline__ LaneColumn lane_column(const LinearArgs& g, int64_t a
   return c;
 }
 
-// The first n (at most kN) of v's accumulator columns: column j is output row
-// b0 + j, this lane output column c.a; a warp's accesses of one column are
-// contiguous.
+// kN accumulator columns: column j is output row b0 + j, this lane output
+// column c.a; a warp's accesses of one column are contiguous.
 template <int kMode, bool kFp8, int kN>
-__device__ __forceinline__ void epilogue_columns(const LinearArgs& g, const LaneColumn& c, int64_t b0, int n,
+__device__ __forceinline__ void epilogue_columns(const LinearArgs& g, const LaneColumn& c, int64_t b0,
                                                  const float* v) {
   if (c.a >= g.na) return;
-  n = static_cast<int>(g.nb - b0 < n ? g.nb - b0 : n);
-  if constexpr (kMode == kLinearDw) {
-    float* p = g.dw + b0 * g.dw_ld + c.a;
-    float old[kN];
-    if (g.accumulate) {
-#pragma unroll
-      for (int j = 0; j < kN; ++j)
-        if (j < n) old[j] = __ldcs(p + j * g.dw_ld);
-    }
-#pragma unroll
-    for (int j = 0; j < kN; ++j)
-      if (j < n) __stcs(p + j * g.dw_ld, g.accumulate ? old[j] + v[j] : v[j]);
-  } else if constexpr (kMode == kLinearDx) {
+  const int n = static_cast<int>(g.nb - b0 < kN ? g.nb - b0 : kN);
+  static_assert(kMode != kLinearDw, "dw has its rows on the lanes");
+  if constexpr (kMode == kLinearDx) {
     uint16_t zr[kN];
     if (g.z_in) {
 #pragma unroll
@@ -213,6 +202,201 @@ __device__ __forceinline__ void epilogue_columns(const LinearArgs& g, const Lane
   }
 }
 
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// kN values that every lane shares: p[col0 .. col0 + kN - 1], 0 past the end.
+template <int kN>
+__device__ __forceinline__ void load_shared_cols(const void* p, int dtype, int64_t col0, int64_t cols, float (&out)[kN]) {
+  if (dtype == kBf16) {
+    const uint16_t* q = static_cast<const uint16_t*>(p) + col0;
+    if (col0 + kN <= cols && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
+#pragma unroll
+      for (int i = 0; i < kN / 8; ++i) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(q) + i);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          out[8 * i + 2 * k] = __uint_as_float(u[k] << 16);
+          out[8 * i + 2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) out[j] = col0 + j < cols ? bf16_at(q, j) : 0.f;
+    }
+  } else {
+    const float* q = static_cast<const float*>(p) + col0;
+    if (col0 + kN <= cols && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
+#pragma unroll
+      for (int i = 0; i < kN / 4; ++i) {
+        const float4 w = __ldg(reinterpret_cast<const float4*>(q) + i);
+        out[4 * i] = w.x;
+        out[4 * i + 1] = w.y;
+        out[4 * i + 2] = w.z;
+        out[4 * i + 3] = w.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) out[j] = col0 + j < cols ? q[j] : 0.f;
+    }
+  }
+}
+
+// Two elements to a word, by index.
+template <int kWords>
+__device__ __forceinline__ float block_elem(const uint32_t (&raw)[kWords], int j) {
+  return __uint_as_float(j & 1 ? raw[j >> 1] & 0xffff0000u : raw[j >> 1] << 16);
+}
+
+// The same with the lanes on output rows: this lane holds columns col .. col +
+// kN - 1 of row `row`.  Rows that start on 16 bytes move in 16-byte pieces;
+// others are turned in the warp's `table`, so that a warp's accesses cover runs
+// of kN columns.
+struct RowAccess {
+  bool in_vec, out_vec;        // residual / z_in, and y, z (or dw)
+};
+
+template <int kN>
+constexpr int kTableWords = 32 * (kN + 1);
+
+template <int kN>
+__device__ __forceinline__ void load_row_in(const uint16_t* p, int64_t ld, int64_t row, int64_t rows, int64_t col,
+                                            int64_t cols, bool vec, uint32_t* table, int lane,
+                                            uint32_t (&raw)[kN / 2]) {
+  if (vec && col + kN <= cols) {
+    const uint4* q = reinterpret_cast<const uint4*>(p + row * ld + col);
+#pragma unroll
+    for (int i = 0; i < kN / 8; ++i) {
+      const uint4 w = row < rows ? q[i] : make_uint4(0, 0, 0, 0);    // a plain load: y may be the residual
+      raw[4 * i] = w.x, raw[4 * i + 1] = w.y, raw[4 * i + 2] = w.z, raw[4 * i + 3] = w.w;
+    }
+    return;
+  }
+  const int sub = lane / kN, c = lane % kN;
+  const int64_t row0 = row - lane;
+  __syncwarp();
+#pragma unroll
+  for (int r = 0; r < 32; r += 32 / kN) {
+    const int64_t rr = row0 + r + sub;
+    table[(r + sub) * (kN + 1) + c] = rr < rows && col + c < cols ? p[rr * ld + col + c] : 0;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kN / 2; ++i)
+    raw[i] = table[lane * (kN + 1) + 2 * i] | (table[lane * (kN + 1) + 2 * i + 1] << 16);
+}
+
+template <int kN>
+__device__ __forceinline__ void store_row_out(uint16_t* p, int64_t ld, int64_t row, int64_t rows, int64_t col,
+                                              int64_t cols, bool vec, uint32_t* table, int lane, const float (&v)[kN]) {
+  if (vec && col + kN <= cols) {
+    if (row < rows) {
+      uint4* q = reinterpret_cast<uint4*>(p + row * ld + col);
+#pragma unroll
+      for (int i = 0; i < kN / 8; ++i)
+        q[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                          pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+    }
+    return;
+  }
+  const int sub = lane / kN, c = lane % kN;
+  const int64_t row0 = row - lane;
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < kN; ++j) table[lane * (kN + 1) + j] = to_bf16(v[j]);
+  __syncwarp();
+#pragma unroll
+  for (int r = 0; r < 32; r += 32 / kN) {
+    const int64_t rr = row0 + r + sub;
+    if (rr < rows && col + c < cols) p[rr * ld + col + c] = static_cast<uint16_t>(table[(r + sub) * (kN + 1) + c]);
+  }
+}
+
+template <int kN>
+__device__ __forceinline__ void store_row_dw(float* p, int64_t ld, int64_t row, int64_t rows, int64_t col,
+                                             int64_t cols, bool vec, bool add, float* table, int lane,
+                                             float (&v)[kN]) {
+  if (vec && col + kN <= cols) {
+    if (row < rows) {
+      float4* q = reinterpret_cast<float4*>(p + row * ld + col);
+      float4 old[kN / 4];
+      if (add) {
+#pragma unroll
+        for (int i = 0; i < kN / 4; ++i) old[i] = q[i];
+#pragma unroll
+        for (int i = 0; i < kN / 4; ++i) {
+          v[4 * i] += old[i].x, v[4 * i + 1] += old[i].y, v[4 * i + 2] += old[i].z, v[4 * i + 3] += old[i].w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kN / 4; ++i) q[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+    return;
+  }
+  const int sub = lane / kN, c = lane % kN;
+  const int64_t row0 = row - lane;
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < kN; ++j) table[lane * (kN + 1) + j] = v[j];
+  __syncwarp();
+#pragma unroll
+  for (int r = 0; r < 32; r += 32 / kN) {
+    const int64_t rr = row0 + r + sub;
+    if (rr < rows && col + c < cols) {
+      float* q = p + rr * ld + col + c;
+      const float x = table[(r + sub) * (kN + 1) + c];
+      *q = add ? *q + x : x;
+    }
+  }
+}
+
+template <int kMode, bool kFp8, int kN>
+__device__ __forceinline__ void epilogue_row(const LinearArgs& g, const RowAccess& access, float row_scale, int64_t row,
+                                             int64_t col, uint32_t* table, int lane, float (&v)[kN]) {
+  if constexpr (kMode == kLinearDw) {
+    store_row_dw<kN>(g.dw, g.dw_ld, row, g.nb, col, g.na, access.out_vec, g.accumulate != 0,
+                     reinterpret_cast<float*>(table), lane, v);
+  } else {
+    const uint16_t* in = kMode == kLinearDx ? g.z_in : g.residual;
+    uint32_t raw[kN / 2];
+    if (in)
+      load_row_in<kN>(in, kMode == kLinearDx ? g.z_ld : g.residual_ld, row, g.nb, col, g.na, access.in_vec, table, lane,
+                      raw);
+    if constexpr (kMode == kLinearDx) {
+      if (in)
+        with_activation(g.act, [&](auto act) {
+#pragma unroll
+          for (int j = 0; j < kN; ++j) v[j] *= activate_grad<act.value>(block_elem(raw, j));
+        });
+    } else {
+      float t[kN];
+      if constexpr (kFp8) {
+        load_shared_cols(g.a_scale, kFp32, col, g.na, t);
+#pragma unroll
+        for (int j = 0; j < kN; ++j) v[j] *= row_scale * t[j];
+      }
+      if (g.bias) {
+        load_shared_cols(g.bias, g.bias_dtype, col, g.na, t);
+#pragma unroll
+        for (int j = 0; j < kN; ++j) v[j] += t[j];
+      }
+      if (g.z_out) store_row_out<kN>(g.z_out, g.z_ld, row, g.nb, col, g.na, access.out_vec, table, lane, v);
+      with_activation(g.act, [&](auto act) {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) v[j] = activate<act.value>(v[j]);
+      });
+      if (in) {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) v[j] += block_elem(raw, j);
+      }
+    }
+    store_row_out<kN>(g.y, g.y_ld, row, g.nb, col, g.na, access.out_vec, table, lane, v);
+  }
+}
+
 // The operands' orders by product: forward K-major both, dx A MN-major, dw both.
 template <int kMode>
 struct Order {
@@ -223,15 +407,19 @@ struct Order {
 // ----------------------------------------------------------- split kernel --
 //
 // Products with too few 256 x 256 tiles for the pair kernel: from one token,
-// where the time is that of reading the weights once, to a few hundred.  A CTA
-// computes 128 output columns (the lanes) x kBN output rows (16 to 128, so that
-// a few tokens do not pay for a wide tile).  Where the tiles are too few for
-// the GPU, a cluster of 2, 4 or 8 CTAs splits the k-blocks of one tile and
-// joins the partial sums through distributed shared memory: rank r adds the
-// ranks' sums of its share of the rows in rank order and runs their epilogue,
-// so the result does not depend on timing and needs no workspace or second
-// launch.  About 100 KB of shared memory a CTA, so that two fit on an SM and
-// one's start and end overlap the other's main loop.
+// where the time is that of reading the weights once, to a few hundred.
+//   kRows false  (up to 32 output rows) a CTA computes 128 output columns, on
+//                the TMEM lanes, x kBN = 16 or 32 rows, so that a few tokens do
+//                not pay for a wide tile
+//   kRows true   128 output rows, on the lanes, x kBN = 64 or 128 columns: a
+//                lane's columns move in 16-byte pieces
+// Where the tiles are too few for the GPU, a cluster of 2, 4 or 8 CTAs splits
+// the k-blocks of one tile and joins the partial sums through distributed
+// shared memory: rank r adds the ranks' sums of its share of the TMEM columns
+// in rank order and runs their epilogue, so the result does not depend on
+// timing and needs no workspace or second launch.  About 100 KB of shared
+// memory a CTA, so that two fit on an SM and one's start and end overlap the
+// other's main loop.
 //   warp 0     TMA producer      warp 1     TMEM allocation, MMA issuer
 //   warps 2-5  epilogue, one TMEM lane quarter each
 // dw runs in segments as in the pair kernel (below).
@@ -249,7 +437,12 @@ struct SplitConfig {
   static constexpr uint32_t kSmemBytes = kStages * kStageBytes + 1024 /*align*/ + 256 /*barriers*/;
   static constexpr int kTmemCols = 2 * kBN < 32 ? 32 : 2 * kBN;     // two accumulators
   static_assert(kSmemBytes <= 116224, "two CTAs shall fit on an SM");
-  static_assert(BM * kBN * 4 <= kStages * kStageBytes, "partial sums larger than the ring they replace");
+  // in the ring's place, once its MMAs are done: the partial sums, then a
+  // turning table for each epilogue warp
+  static constexpr int kPartBytes = BM * kBN * 4;
+  static constexpr int kChunk = kBN == 128 ? 16 : 8;     // columns an epilogue handles at a time; kBN / 8 or less
+  static_assert(kPartBytes + kSplitEpiWarps * kTableWords<kChunk> * 4 <= kStages * kStageBytes,
+                "partial sums and tables larger than the ring they replace");
 };
 
 struct SplitParams {
@@ -258,23 +451,28 @@ struct SplitParams {
   int per_rank;        // k-blocks of one CTA of the cluster
   int segment;         // k-blocks accumulated in TMEM at a time
   int split;           // CTAs per cluster
-  int64_t tiles_a;
+  int64_t tiles_m;     // tiles along the lanes' index
+  RowAccess access;
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr));
   return v;
 }
 
-template <int kMode, bool kFp8, int kBN>
+template <int kMode, bool kFp8, int kBN, bool kRows>
 __global__ void __launch_bounds__(kSplitThreads, 2)
 linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                     const __grid_constant__ SplitParams P) {
   using C = SplitConfig<kBN>;
   constexpr int kElems = kFp8 ? 128 : 64;
-  constexpr bool a_mn = Order<kMode>::a_mn, b_mn = Order<kMode>::b_mn;
-  static_assert(!b_mn || kBN % 64 == 0, "MN-major rows are staged 64 at a time");
+  // the MMA's A operand is the lanes' index: output rows (the product's B) or columns (its A)
+  constexpr bool a_mn = kRows ? Order<kMode>::b_mn : Order<kMode>::a_mn;
+  constexpr bool b_mn = kRows ? Order<kMode>::a_mn : Order<kMode>::b_mn;
+  static_assert(!b_mn || kBN % 64 == 0, "an MN-major operand is staged 64 indices at a time");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
@@ -288,7 +486,8 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
   uint32_t* status = P.g.header;
   const int rank = P.split > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int64_t tile = blockIdx.x / P.split;
-  const int64_t a0 = tile % P.tiles_a * BM, b0 = tile / P.tiles_a * kBN;
+  const int64_t m0 = tile % P.tiles_m * BM, n0 = tile / P.tiles_m * kBN;   // first lane's and first column's index
+  const int64_t n_end = kRows ? P.g.na : P.g.nb;
   // this CTA's k-blocks; the last ranks may have none, and their sums are zero
   const int kb0 = min(rank * P.per_rank, P.k_blocks), kb1 = min(kb0 + P.per_rank, P.k_blocks);
 
@@ -297,8 +496,8 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
   // k-block kb into stage s, by the producer
   auto load_stage = [&](int kb, uint32_t s) {
     mbar_expect_tx(full0 + 8 * s, C::kStageBytes);
-    load_operand(sa0 + s * kStageA, &map_a, full0 + 8 * s, a_mn, static_cast<int>(a0), BM, kb, kElems);
-    load_operand(sb0 + s * C::kStageB, &map_b, full0 + 8 * s, b_mn, static_cast<int>(b0), kBN, kb, kElems);
+    load_operand(sa0 + s * kStageA, &map_a, full0 + 8 * s, a_mn, static_cast<int>(m0), BM, kb, kElems);
+    load_operand(sb0 + s * C::kStageB, &map_b, full0 + 8 * s, b_mn, static_cast<int>(n0), kBN, kb, kElems);
   };
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -326,7 +525,14 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int quarter = warp & 3;
-  const LaneColumn col = lane_column<kMode, kFp8>(P.g, a0 + quarter * 32 + lane);
+  const int64_t index = m0 + quarter * 32 + lane;     // this lane's
+  LaneColumn lane_col{index, 1.f, 0.f};
+  float row_scale = 1.f;
+  if constexpr (kRows) {
+    if (kFp8 && index < P.g.nb) row_scale = P.g.b_scale[index];
+  } else {
+    lane_col = lane_column<kMode, kFp8>(P.g, index);
+  }
   constexpr int kSum = kMode == kLinearDw ? kBN : 1;
   float sum[kSum];
   bool ready = false;          // epilogue warps: the accumulator holds this CTA's sums
@@ -420,6 +626,16 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
   }
 
   __syncwarp();
+  // The sums of kN columns from column c of the tile.
+  auto finish = [&](int c, auto& v) {
+    constexpr int kN = sizeof(v) / sizeof(float);
+    if constexpr (kRows) {
+      uint32_t* table = reinterpret_cast<uint32_t*>(smem + C::kPartBytes) + (warp - 2) * kTableWords<C::kChunk>;
+      epilogue_row<kMode, kFp8, kN>(P.g, P.access, row_scale, index, n0 + c, table, lane, v);
+    } else {
+      epilogue_columns<kMode, kFp8, kN>(P.g, lane_col, n0 + c, v);
+    }
+  };
   // columns c .. c + 15 of this CTA's own sums
   auto own_sums = [&](int c, float (&v)[16]) {
     if constexpr (kMode == kLinearDw) {
@@ -437,63 +653,85 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
   };
   if (P.split == 1) {
     if (ready) {
-      constexpr int kN = kMode == kLinearDw || kBN < 32 ? 16 : 32;
 #pragma unroll
-      for (int c = 0; c < kBN; c += kN) {
-        if (b0 + c >= P.g.nb) break;
-        float v[kN];
+      for (int c = 0; c < kBN; c += 16) {
+        if (n0 + c >= n_end) break;
+        float v[16];
+        own_sums(c, v);
+        if constexpr (C::kChunk == 16) {
+          finish(c, v);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kN; i += 16) {
-          float w[16];
-          own_sums(c + i, w);
+          for (int i = 0; i < 16; i += 8) {
+            float w[8];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[i + j] = w[j];
+            for (int j = 0; j < 8; ++j) w[j] = v[i + j];
+            if (n0 + c + i < n_end) finish(c + i, w);
+          }
         }
-        epilogue_columns<kMode, kFp8, kN>(P.g, col, b0 + c, kN, v);
       }
     }
   } else {
-    // the sums take the place of the ring: its MMAs have completed (acc_full)
-    float* part = reinterpret_cast<float*>(smem);        // [kBN][BM]
+    // the sums take the place of the ring: its MMAs have completed (acc_full).
+    // Four columns of a lane are one 16-byte word: part[column / 4][lane]
+    float4* part = reinterpret_cast<float4*>(smem);
     if (ready) {
 #pragma unroll
       for (int c = 0; c < kBN; c += 16) {
         float v[16];
         own_sums(c, v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(c + j) * BM + quarter * 32 + lane] = v[j];
+        for (int j = 0; j < 16; j += 4)
+          part[(c + j) / 4 * BM + quarter * 32 + lane] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
       }
     }
+    __syncwarp();
     cluster_sync();
     if (ready) {
-      const int per = kBN / P.split;                     // 2 at least
-      uint32_t peer[kMaxSplit];
-#pragma unroll
-      for (int p = 0; p < kMaxSplit; ++p)
-        peer[p] = p < P.split ? peer_addr(smem_u32(part), static_cast<uint32_t>(p)) : 0u;
-      // up to 16 rows at a time: their loads, from the peers and from global
-      // memory, overlap (2 at a time, a tile of 128 rows spent 20 us here)
-      constexpr int kN = kBN < 32 ? 8 : 16;
-      for (int c = rank * per; c < (rank + 1) * per && b0 + c < P.g.nb; c += kN) {
-        const int n = min(kN, (rank + 1) * per - c);
-        const uint32_t off = (c * BM + quarter * 32 + lane) * 4;
-        float v[kN];
-#pragma unroll
-        for (int j = 0; j < kN; ++j) v[j] = 0.f;
+      // this rank's share of the columns, kJoin at a time with every peer's
+      // words in flight together (one peer after the other, a tile of 128
+      // columns spent 5 us here)
+      constexpr int kJoin = kBN / kMaxSplit < 4 ? 4 : kBN / kMaxSplit < C::kChunk ? kBN / kMaxSplit : C::kChunk;
+      const int per = kBN / P.split, first = rank * per;
+      // kBN = 16 split 8 ways: two columns a rank, half of a word
+      const uint32_t base = smem_u32(part) + (quarter * 32 + lane) * 16;
+      for (int c = first; c < first + per && n0 + c < n_end; c += kJoin) {
+        const int c4 = c & ~3;
+        float4 w[kMaxSplit][kJoin / 4];
 #pragma unroll
         for (int p = 0; p < kMaxSplit; ++p)
           if (p < P.split) {
-            float w[kN];
+            const uint32_t peer = peer_addr(base, static_cast<uint32_t>(p));
 #pragma unroll
-            for (int j = 0; j < kN; ++j)
-              if (j < n) w[j] = ld_cluster_f32(peer[p] + off + j * (BM * 4));
-#pragma unroll
-            for (int j = 0; j < kN; ++j)
-              if (j < n) v[j] += w[j];
+            for (int i = 0; i < kJoin / 4; ++i) w[p][i] = ld_cluster_f32x4(peer + (c4 / 4 + i) * (BM * 16));
           }
-        epilogue_columns<kMode, kFp8, kN>(P.g, col, b0 + c, n, v);
+        float v[kJoin];
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j) v[j] = 0.f;
+#pragma unroll
+        for (int p = 0; p < kMaxSplit; ++p)
+          if (p < P.split) {
+#pragma unroll
+            for (int i = 0; i < kJoin / 4; ++i) {
+              v[4 * i] += w[p][i].x;
+              v[4 * i + 1] += w[p][i].y;
+              v[4 * i + 2] += w[p][i].z;
+              v[4 * i + 3] += w[p][i].w;
+            }
+          }
+        if constexpr (kBN / kMaxSplit < 4) {
+          if (per < 4) {
+            float two[2] = {c & 2 ? v[2] : v[0], c & 2 ? v[3] : v[1]};
+            finish(c, two);
+          } else {
+            finish(c, v);
+          }
+        } else {
+          finish(c, v);
+        }
       }
     }
+    __syncwarp();
     cluster_sync();          // no CTA leaves while another reads its sums
   }
   tc_fence_before();
@@ -615,11 +853,6 @@ __device__ __forceinline__ void tma_add_block(const CUtensorMap* map, uint32_t s
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&p);
-}
-
 // Lane t holds row t of a 32 x 32 bf16 block: 64-byte swizzle for a TMA store.
 __device__ __forceinline__ void stage_bf16_rows(uint8_t* buf, int lane, const float (&v)[32]) {
 #pragma unroll
@@ -660,48 +893,6 @@ __device__ __forceinline__ void load_block(const uint16_t* p, int64_t ld, int64_
 #pragma unroll
   for (int i = 0; i < 16; ++i) raw[i] = table[turn(lane, 2 * i)] | (table[turn(lane, 2 * i + 1)] << 16);
   __syncwarp();
-}
-
-__device__ __forceinline__ float block_elem(const uint32_t (&raw)[16], int j) {
-  return __uint_as_float(j & 1 ? raw[j >> 1] & 0xffff0000u : raw[j >> 1] << 16);
-}
-
-// 32 values that every lane shares: p[col0 .. col0 + 31], 0 past the end.
-__device__ __forceinline__ void load_shared_cols(const void* p, int dtype, int64_t col0, int64_t cols,
-                                                 float (&out)[32]) {
-  if (dtype == kBf16) {
-    const uint16_t* q = static_cast<const uint16_t*>(p) + col0;
-    if (col0 + 32 <= cols && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(q) + i);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          out[8 * i + 2 * k] = __uint_as_float(u[k] << 16);
-          out[8 * i + 2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) out[j] = col0 + j < cols ? bf16_at(q, j) : 0.f;
-    }
-  } else {
-    const float* q = static_cast<const float*>(p) + col0;
-    if (col0 + 32 <= cols && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 w = __ldg(reinterpret_cast<const float4*>(q) + i);
-        out[4 * i] = w.x;
-        out[4 * i + 1] = w.y;
-        out[4 * i + 2] = w.z;
-        out[4 * i + 3] = w.w;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) out[j] = col0 + j < cols ? q[j] : 0.f;
-    }
-  }
 }
 
 // A block that TMA cannot store: turned through the table, then 32 columns of
@@ -1187,12 +1378,16 @@ cudaError_t make_operand_map(CUtensorMap* map, const LinearOperand& o, int64_t n
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+bool rows_on_16(const void* p, int64_t ld, int64_t rows, int es) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows <= 1 || (ld * es) % 16 == 0);
+}
+
 // 2-D map of an output [rows][cols] of 2- or 4-byte elements in 32 x 32
 // blocks (64- or 128-byte swizzle); false when TMA cannot address it.
 bool make_block_map(CUtensorMap* map, const void* p, int64_t ld, int64_t rows, int64_t cols, bool fp32) {
   const int es = fp32 ? 4 : 2;
   EncodeTiledFn fn = encode_fn();
-  if (!fn || (reinterpret_cast<uintptr_t>(p) & 15u) != 0 || (rows > 1 && (ld * es) % 16 != 0)) return false;
+  if (!fn || !rows_on_16(p, ld, rows, es)) return false;
   if (rows <= 1) ld = (cols + 7) / 8 * 8;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * es)};
@@ -1236,7 +1431,7 @@ cudaError_t launch_pair(const LinearArgs& a, int k_blocks, int tiles_a, int tile
                 (!a.z_out || make_block_map(&mz, a.z_out, a.z_ld, a.nb, a.na, false));
     const uint16_t* in = kMode == kLinearDx ? a.z_in : a.residual;
     const int64_t in_ld = kMode == kLinearDx ? a.z_ld : a.residual_ld;
-    P.in_vec = (reinterpret_cast<uintptr_t>(in) & 15u) == 0 && in_ld % 8 == 0;
+    P.in_vec = rows_on_16(in, in_ld, a.nb, 2);
   }
   if ((e = allow_smem<linear_pair_kernel<kMode, kFp8>>(kPairSmemBytes)) != cudaSuccess) return e;
   const int max_pairs = num_sms() / 2;
@@ -1245,26 +1440,33 @@ cudaError_t launch_pair(const LinearArgs& a, int k_blocks, int tiles_a, int tile
   return cudaGetLastError();
 }
 
-template <int kMode, bool kFp8, int kBN>
+template <int kMode, bool kFp8, int kBN, bool kRows>
 cudaError_t launch_split(const LinearArgs& a, int k_blocks, cudaStream_t stream) {
   using C = SplitConfig<kBN>;
   SplitParams P{};
   P.g = a;
   P.k_blocks = k_blocks;
-  P.tiles_a = (a.na + BM - 1) / BM;
-  const int64_t tiles = P.tiles_a * ((a.nb + kBN - 1) / kBN);
+  P.tiles_m = ((kRows ? a.nb : a.na) + BM - 1) / BM;
+  const int64_t tiles = P.tiles_m * (((kRows ? a.na : a.nb) + kBN - 1) / kBN);
   // split while the clusters still run at once, two CTAs to an SM, and each
   // CTA keeps 4 k-blocks (about the time its start and the join take)
   P.split = 1;
   while (P.split < kMaxSplit && tiles * P.split * 2 <= 2 * num_sms() && k_blocks >= P.split * 2 * 4) P.split *= 2;
   P.per_rank = (k_blocks + P.split - 1) / P.split;
   P.segment = kMode == kLinearDw ? kDwSegment : k_blocks;
+  if (kMode == kLinearDw) {
+    P.access.out_vec = rows_on_16(a.dw, a.dw_ld, a.nb, 4);
+  } else {
+    P.access.out_vec = rows_on_16(a.y, a.y_ld, a.nb, 2) && (!a.z_out || rows_on_16(a.z_out, a.z_ld, a.nb, 2));
+    P.access.in_vec = kMode == kLinearDx ? rows_on_16(a.z_in, a.z_ld, a.nb, 2)
+                                         : rows_on_16(a.residual, a.residual_ld, a.nb, 2);
+  }
   if (tiles * P.split > 0x7fffffff) return cudaErrorInvalidValue;
   CUtensorMap ma, mb;
   cudaError_t e;
-  if ((e = make_operand_map(&ma, a.A, a.na, a.nk, kFp8, BM)) != cudaSuccess) return e;
-  if ((e = make_operand_map(&mb, a.B, a.nb, a.nk, kFp8, kBN)) != cudaSuccess) return e;
-  if ((e = allow_smem<linear_split_kernel<kMode, kFp8, kBN>>(C::kSmemBytes)) != cudaSuccess) return e;
+  if ((e = make_operand_map(&ma, a.A, a.na, a.nk, kFp8, kRows ? kBN : BM)) != cudaSuccess) return e;
+  if ((e = make_operand_map(&mb, a.B, a.nb, a.nk, kFp8, kRows ? BM : kBN)) != cudaSuccess) return e;
+  if ((e = allow_smem<linear_split_kernel<kMode, kFp8, kBN, kRows>>(C::kSmemBytes)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * P.split));
   cfg.blockDim = dim3(kSplitThreads);
@@ -1277,7 +1479,7 @@ cudaError_t launch_split(const LinearArgs& a, int k_blocks, cudaStream_t stream)
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, linear_split_kernel<kMode, kFp8, kBN>, ma, mb, P);
+  return cudaLaunchKernelEx(&cfg, linear_split_kernel<kMode, kFp8, kBN, kRows>, kRows ? mb : ma, kRows ? ma : mb, P);
 }
 
 template <int kMode, bool kFp8>
@@ -1289,11 +1491,10 @@ cudaError_t launch_product(const LinearArgs& a, cudaStream_t stream) {
   if (pair_a * pair_b >= num_sms() / 2 && pair_a * pair_b < (int64_t(1) << 30))
     return launch_pair<kMode, kFp8>(a, k_blocks, static_cast<int>(pair_a), static_cast<int>(pair_b), stream);
   if constexpr (kMode != kLinearDw) {
-    if (a.nb <= 16) return launch_split<kMode, kFp8, 16>(a, k_blocks, stream);
-    if (a.nb <= 32) return launch_split<kMode, kFp8, 32>(a, k_blocks, stream);
-    if (a.nb <= 64) return launch_split<kMode, kFp8, 64>(a, k_blocks, stream);
+    if (a.nb <= 16) return launch_split<kMode, kFp8, 16, false>(a, k_blocks, stream);
+    if (a.nb <= 32) return launch_split<kMode, kFp8, 32, false>(a, k_blocks, stream);
   }
-  return launch_split<kMode, kFp8, 128>(a, k_blocks, stream);
+  return launch_split<kMode, kFp8, 64, true>(a, k_blocks, stream);
 }
 
 }  // namespace
