@@ -24,9 +24,6 @@ namespace {
 
 constexpr int BM = 128;                        // TMEM lanes of a CTA: output indices of the MMA's A operand
 constexpr int kStageA = BM * kRowBytes;
-constexpr int kPairBNHalf = 128;               // pair kernel: columns staged by one CTA
-constexpr int kStageB = kPairBNHalf * kRowBytes;
-constexpr int kStageBytes = kStageA + kStageB;
 
 // ------------------------------------------------------------ activations --
 
@@ -277,12 +274,15 @@ __device__ __forceinline__ void load_row_in(const uint16_t* p, int64_t ld, int64
   }
   const int sub = lane / kN, c = lane % kN;
   const int64_t row0 = row - lane;
+  uint16_t got[kN];                   // 32 rows, 32 / kN at a time, all loads in flight together
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const int64_t rr = row0 + i * (32 / kN) + sub;
+    got[i] = rr < rows && col + c < cols ? p[rr * ld + col + c] : 0;
+  }
   __syncwarp();
 #pragma unroll
-  for (int r = 0; r < 32; r += 32 / kN) {
-    const int64_t rr = row0 + r + sub;
-    table[(r + sub) * (kN + 1) + c] = rr < rows && col + c < cols ? p[rr * ld + col + c] : 0;
-  }
+  for (int i = 0; i < kN; ++i) table[(i * (32 / kN) + sub) * (kN + 1) + c] = got[i];
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < kN / 2; ++i)
@@ -336,20 +336,26 @@ __device__ __forceinline__ void store_row_dw(float* p, int64_t ld, int64_t row, 
     }
     return;
   }
+  constexpr int kTurns = kN;          // 32 rows, 32 / kN at a time
   const int sub = lane / kN, c = lane % kN;
   const int64_t row0 = row - lane;
+  float old[kTurns];
+  if (add) {
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+      const int64_t rr = row0 + i * (32 / kN) + sub;
+      old[i] = rr < rows && col + c < cols ? p[rr * ld + col + c] : 0.f;
+    }
+  }
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < kN; ++j) table[lane * (kN + 1) + j] = v[j];
   __syncwarp();
 #pragma unroll
-  for (int r = 0; r < 32; r += 32 / kN) {
-    const int64_t rr = row0 + r + sub;
-    if (rr < rows && col + c < cols) {
-      float* q = p + rr * ld + col + c;
-      const float x = table[(r + sub) * (kN + 1) + c];
-      *q = add ? *q + x : x;
-    }
+  for (int i = 0; i < kTurns; ++i) {
+    const int r = i * (32 / kN) + sub;
+    const float x = table[r * (kN + 1) + c];
+    if (row0 + r < rows && col + c < cols) p[(row0 + r) * ld + col + c] = add ? old[i] + x : x;
   }
 }
 
@@ -440,8 +446,7 @@ struct SplitConfig {
   // in the ring's place, once its MMAs are done: the partial sums, then a
   // turning table for each epilogue warp
   static constexpr int kPartBytes = BM * kBN * 4;
-  static constexpr int kChunk = kBN == 128 ? 16 : 8;     // columns an epilogue handles at a time; kBN / 8 or less
-  static_assert(kPartBytes + kSplitEpiWarps * kTableWords<kChunk> * 4 <= kStages * kStageBytes,
+  static_assert(kBN < 64 || kPartBytes + kSplitEpiWarps * kTableWords<32> * 4 <= kStages * kStageBytes,
                 "partial sums and tables larger than the ring they replace");
 };
 
@@ -453,6 +458,13 @@ struct SplitParams {
   int split;           // CTAs per cluster
   int64_t tiles_m;     // tiles along the lanes' index
   RowAccess access;
+};
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+template <int kSplit>
+struct SplitTag {
+  static constexpr int value = kSplit;
 };
 
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t cluster_addr) {
@@ -605,6 +617,20 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     for (int c = 0; c < kSum; ++c) sum[c] = 0.f;
     uint32_t use = 0;
     ready = true;
+    if constexpr (kMode == kLinearDw) {
+      const int64_t c = n0 + rank * (kBN / P.split);
+      if (P.g.accumulate && index < P.g.nb && c < P.g.na) {
+        const float* p = P.g.dw + index * P.g.dw_ld + c;
+        prefetch_l2(p);
+        if (P.split == 1 && c + 32 < P.g.na) prefetch_l2(p + 32);
+      }
+    } else if constexpr (kRows) {
+      // the residual or pre-activation of this rank's share comes from DRAM while the MMAs run
+      const uint16_t* in = kMode == kLinearDx ? P.g.z_in : P.g.residual;
+      const int64_t c = n0 + rank * (kBN / P.split);
+      if (in && index < P.g.nb && c < P.g.na)
+        prefetch_l2(in + index * (kMode == kLinearDx ? P.g.z_ld : P.g.residual_ld) + c);
+    }
     for (int k0 = kb0; ready && k0 < kb1; k0 += P.segment, ++use) {
       const uint32_t acc = use & 1;
       ready = __all_sync(0xffffffffu, mbar_wait(smem_u32(&acc_full[acc]), (use >> 1) & 1u, abort_flag, status,
@@ -626,18 +652,18 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
   }
 
   __syncwarp();
-  // The sums of kN columns from column c of the tile.
+  // The sums of the tile's columns c, c + 1, ...
   auto finish = [&](int c, auto& v) {
     constexpr int kN = sizeof(v) / sizeof(float);
     if constexpr (kRows) {
-      uint32_t* table = reinterpret_cast<uint32_t*>(smem + C::kPartBytes) + (warp - 2) * kTableWords<C::kChunk>;
+      uint32_t* table = reinterpret_cast<uint32_t*>(smem + C::kPartBytes) + (warp - 2) * kTableWords<32>;
       epilogue_row<kMode, kFp8, kN>(P.g, P.access, row_scale, index, n0 + c, table, lane, v);
     } else {
       epilogue_columns<kMode, kFp8, kN>(P.g, lane_col, n0 + c, v);
     }
   };
   // columns c .. c + 15 of this CTA's own sums
-  auto own_sums = [&](int c, float (&v)[16]) {
+  auto own_sums = [&](int c, float* v) {
     if constexpr (kMode == kLinearDw) {
 #pragma unroll
       for (int k = 0; k < kBN; k += 16)
@@ -645,30 +671,75 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
 #pragma unroll
           for (int j = 0; j < 16; ++j) v[j] = sum[k + j];
     } else if (kb1 > kb0) {
-      tmem_ld16(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + c, v);
+      float w[16];
+      tmem_ld16(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + c, w);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = w[j];
     } else {
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] = 0.f;
     }
   };
+  // This rank's share of the columns of a cluster of kSplit, up to 32 at a
+  // time with every peer's words and the epilogue's inputs in flight together
+  // (peers and 8 columns at a time one after the other, a tile of 128 columns
+  // spent 5 us here).
+  auto join = [&](auto split_tag) {
+    constexpr int kSplit = decltype(split_tag)::value, kPer = kBN / kSplit;
+    constexpr int kMost = kMode == kLinearDw ? 16 : 32;          // dw keeps sums and main_grad's old values in registers
+    constexpr int kN = kPer > kMost ? kMost : kPer < 4 ? 4 : kPer;     // kPer 2 (16 columns, 8 ranks): half of a word
+    constexpr int kGroup = kSplit * kN > 128 ? 128 / kSplit : kN;   // columns loaded at a time: 128 registers at most
+    const uint32_t base = smem_u32(smem) + (quarter * 32 + lane) * 16;
+#pragma unroll
+    for (int c0 = 0; c0 < kPer; c0 += kN) {
+      const int c = rank * kPer + c0, c4 = c & ~3;
+      if (n0 + c >= n_end) break;
+      float v[kN];
+#pragma unroll
+      for (int g = 0; g < kN; g += kGroup) {
+        float4 w[kSplit][kGroup / 4];
+#pragma unroll
+        for (int p = 0; p < kSplit; ++p) {
+          const uint32_t peer = peer_addr(base, static_cast<uint32_t>(p));
+#pragma unroll
+          for (int i = 0; i < kGroup / 4; ++i) w[p][i] = ld_cluster_f32x4(peer + ((c4 + g) / 4 + i) * (BM * 16));
+        }
+#pragma unroll
+        for (int i = 0; i < kGroup / 4; ++i) {
+          float4 t = w[0][i];
+#pragma unroll
+          for (int p = 1; p < kSplit; ++p) {
+            t.x += w[p][i].x;
+            t.y += w[p][i].y;
+            t.z += w[p][i].z;
+            t.w += w[p][i].w;
+          }
+          v[g + 4 * i] = t.x;
+          v[g + 4 * i + 1] = t.y;
+          v[g + 4 * i + 2] = t.z;
+          v[g + 4 * i + 3] = t.w;
+        }
+      }
+      if constexpr (kPer < 4) {
+        float part_word[kPer];
+        part_word[0] = c & 2 ? v[2] : v[0];
+        part_word[1] = c & 2 ? v[3] : v[1];
+        finish(c, part_word);
+      } else {
+        finish(c, v);
+      }
+    }
+  };
   if (P.split == 1) {
     if (ready) {
+      constexpr int kN = kBN < 32 || kMode == kLinearDw ? 16 : 32;
 #pragma unroll
-      for (int c = 0; c < kBN; c += 16) {
+      for (int c = 0; c < kBN; c += kN) {
         if (n0 + c >= n_end) break;
-        float v[16];
+        float v[kN];
         own_sums(c, v);
-        if constexpr (C::kChunk == 16) {
-          finish(c, v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; i += 8) {
-            float w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = v[i + j];
-            if (n0 + c + i < n_end) finish(c + i, w);
-          }
-        }
+        if constexpr (kN == 32) own_sums(c + 16, v + 16);
+        finish(c, v);
       }
     }
   } else {
@@ -688,48 +759,9 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     __syncwarp();
     cluster_sync();
     if (ready) {
-      // this rank's share of the columns, kJoin at a time with every peer's
-      // words in flight together (one peer after the other, a tile of 128
-      // columns spent 5 us here)
-      constexpr int kJoin = kBN / kMaxSplit < 4 ? 4 : kBN / kMaxSplit < C::kChunk ? kBN / kMaxSplit : C::kChunk;
-      const int per = kBN / P.split, first = rank * per;
-      // kBN = 16 split 8 ways: two columns a rank, half of a word
-      const uint32_t base = smem_u32(part) + (quarter * 32 + lane) * 16;
-      for (int c = first; c < first + per && n0 + c < n_end; c += kJoin) {
-        const int c4 = c & ~3;
-        float4 w[kMaxSplit][kJoin / 4];
-#pragma unroll
-        for (int p = 0; p < kMaxSplit; ++p)
-          if (p < P.split) {
-            const uint32_t peer = peer_addr(base, static_cast<uint32_t>(p));
-#pragma unroll
-            for (int i = 0; i < kJoin / 4; ++i) w[p][i] = ld_cluster_f32x4(peer + (c4 / 4 + i) * (BM * 16));
-          }
-        float v[kJoin];
-#pragma unroll
-        for (int j = 0; j < kJoin; ++j) v[j] = 0.f;
-#pragma unroll
-        for (int p = 0; p < kMaxSplit; ++p)
-          if (p < P.split) {
-#pragma unroll
-            for (int i = 0; i < kJoin / 4; ++i) {
-              v[4 * i] += w[p][i].x;
-              v[4 * i + 1] += w[p][i].y;
-              v[4 * i + 2] += w[p][i].z;
-              v[4 * i + 3] += w[p][i].w;
-            }
-          }
-        if constexpr (kBN / kMaxSplit < 4) {
-          if (per < 4) {
-            float two[2] = {c & 2 ? v[2] : v[0], c & 2 ? v[3] : v[1]};
-            finish(c, two);
-          } else {
-            finish(c, v);
-          }
-        } else {
-          finish(c, v);
-        }
-      }
+      if (P.split == 2) join(SplitTag<2>{});
+      else if (P.split == 4) join(SplitTag<4>{});
+      else join(SplitTag<8>{});
     }
     __syncwarp();
     cluster_sync();          // no CTA leaves while another reads its sums
@@ -776,20 +808,27 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
 // before the MMAs stall: 8 k-blocks cost 6 % against one segment for all
 // (8192 tokens, 14336 x 4096), 16 and more 2 % or less.
 
-constexpr int kPairStages = 6;
-constexpr int kPairBN = 256;
 constexpr int kPairEpiWarps = 8;
 constexpr int kPairThreads = 96 + 32 * kPairEpiWarps;
-constexpr int kPairTmemCols = 512;
 constexpr int kTileSlots = 3;
-constexpr int kWarpScratch = 4096;     // per epilogue warp: staged 32 x 32 blocks, bf16 y and z or fp32
 constexpr int kBlockBytes = 32 * 32 * 2;
 constexpr uint32_t kTileConsumers = 2 + 1 + 2 * kPairEpiWarps;
-constexpr int kPairBarrierBytes = (2 * kPairStages + 5 + 2 * kTileSlots) * 8 + 8 + 4 * kTileSlots;
-static_assert(kPairBarrierBytes <= 256, "barrier block larger than its 256-byte reservation");
-constexpr uint32_t kPairSmemBytes =
-    kPairStages * kStageBytes + kPairEpiWarps * kWarpScratch + 1024 /*align*/ + 256 /*barriers*/;
-static_assert(kPairSmemBytes <= 232448, "dynamic shared memory above the 227 KB a CTA may use");
+
+template <int kMode, int kBN>
+struct PairConfig {
+  static constexpr int kHalf = kBN / 2;                      // columns staged by one CTA, and of an epilogue warp
+  static constexpr int kStageB = kHalf * kRowBytes;
+  static constexpr int kStageBytes = kStageA + kStageB;
+  // per epilogue warp, staged 32 x 32 blocks: bf16 y and z (or y twice), or two of fp32
+  static constexpr int kWarpScratch = kMode == kLinearDw ? 8192 : 4096;
+  static constexpr int kStages = (227 * 1024 - 1280 - kPairEpiWarps * kWarpScratch) / kStageBytes;
+  static constexpr int kTmemCols = 2 * kBN;                  // two accumulators
+  static constexpr int kBarrierBytes = (2 * kStages + 5 + 2 * kTileSlots) * 8 + 8 + 4 * kTileSlots;
+  static_assert(kBarrierBytes <= 256, "barrier block larger than its 256-byte reservation");
+  static constexpr uint32_t kSmemBytes =
+      kStages * kStageBytes + kPairEpiWarps * kWarpScratch + 1024 /*align*/ + 256 /*barriers*/;
+  static_assert(kSmemBytes <= 232448, "dynamic shared memory above the 227 KB a CTA may use");
+};
 
 struct PairParams {
   LinearArgs g;
@@ -851,8 +890,6 @@ __device__ __forceinline__ void tma_add_block(const CUtensorMap* map, uint32_t s
                : "memory");
 }
 
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
 // Lane t holds row t of a 32 x 32 bf16 block: 64-byte swizzle for a TMA store.
 __device__ __forceinline__ void stage_bf16_rows(uint8_t* buf, int lane, const float (&v)[32]) {
 #pragma unroll
@@ -913,17 +950,18 @@ __device__ __forceinline__ void store_turned(T* p, int64_t ld, int64_t row0, int
   __syncwarp();
 }
 
-template <int kMode, bool kFp8>
+template <int kMode, bool kFp8, int kBN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_z,
                    const __grid_constant__ PairParams P) {
+  using C = PairConfig<kMode, kBN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* scratch = smem + kPairStages * kStageBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(scratch + kPairEpiWarps * kWarpScratch);   // even CTA: both CTAs' copies landed
-  uint64_t* empty = full + kPairStages;            // both CTAs: stage free again
-  uint64_t* acc_full = empty + kPairStages;        // [2] both CTAs: accumulator ready
+  uint8_t* scratch = smem + C::kStages * C::kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(scratch + kPairEpiWarps * C::kWarpScratch);   // even CTA: both CTAs' copies landed
+  uint64_t* empty = full + C::kStages;            // both CTAs: stage free again
+  uint64_t* acc_full = empty + C::kStages;        // [2] both CTAs: accumulator ready
   uint64_t* acc_empty = acc_full + 2;              // [2] even CTA: both epilogues have read it
   uint64_t* drain = acc_empty + 2;                 // even CTA: all MMAs complete
   uint64_t* tile_full = drain + 1;                 // [kTileSlots] both CTAs: next tile published
@@ -941,7 +979,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   uint32_t* status = P.g.header;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kPairStages; ++s) {
+    for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
@@ -959,7 +997,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"(kPairTmemCols)
+                 "r"(C::kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
@@ -973,7 +1011,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       bool ok = true, issued = false;
       const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
       const uint32_t full0_even = peer_addr(full0, 0);
-      const uint32_t sa0 = smem_u32(smem), sb0 = sa0 + kPairStages * kStageA;
+      const uint32_t sa0 = smem_u32(smem), sb0 = sa0 + C::kStages * kStageA;
       const uint32_t tempty_even = peer_addr(smem_u32(&tile_empty[0]), 0);
       uint32_t s = 0, ph = 0;
       for (uint32_t seq = 0; ok; ++seq) {
@@ -990,15 +1028,15 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
         if (tile >= P.total_tiles) break;
         int ta, tb;
         pair_tile(P, tile, ta, tb);
-        const int ai = tb * 256 + static_cast<int>(rank) * BM, bi = ta * kPairBN + static_cast<int>(rank) * kPairBNHalf;
+        const int ai = tb * 256 + static_cast<int>(rank) * BM, bi = ta * kBN + static_cast<int>(rank) * C::kHalf;
         for (int kb = 0; kb < P.k_blocks; ++kb) {
           if (!mbar_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, status, kStatusTimeoutEmpty)) {
             ok = false;
             break;
           }
           const uint32_t fb = full0_even + 8 * s;
-          if (rank == 0) mbar_expect_tx(full0 + 8 * s, 2 * kStageBytes);
-          const uint32_t sa = sa0 + s * kStageA, sb = sb0 + s * kStageB;
+          if (rank == 0) mbar_expect_tx(full0 + 8 * s, 2 * C::kStageBytes);
+          const uint32_t sa = sa0 + s * kStageA, sb = sb0 + s * C::kStageB;
           if constexpr (a_mn) {
             tma_load_2d_pair(sa, &map_a, fb, ai, kb * kElems);
             tma_load_2d_pair(sa + kMnBlockBytes, &map_a, fb, ai + 64, kb * kElems);
@@ -1007,12 +1045,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
           }
           if constexpr (b_mn) {
             tma_load_2d_pair(sb, &map_b, fb, bi, kb * kElems);
-            tma_load_2d_pair(sb + kMnBlockBytes, &map_b, fb, bi + 64, kb * kElems);
+            if constexpr (kBN == 256) tma_load_2d_pair(sb + kMnBlockBytes, &map_b, fb, bi + 64, kb * kElems);
           } else {
             tma_load_2d_pair(sb, &map_b, fb, kb * kElems, bi);
           }
           issued = true;
-          if (++s == kPairStages) {
+          if (++s == C::kStages) {
             s = 0;
             ph ^= 1u;
           }
@@ -1027,8 +1065,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = linear_idesc(kFp8, a_mn, b_mn, 256, kPairBN);
-      const uint32_t sa0 = smem_u32(smem), sb0 = sa0 + kPairStages * kStageA;
+      constexpr uint32_t idesc = linear_idesc(kFp8, a_mn, b_mn, 256, kBN);
+      const uint32_t sa0 = smem_u32(smem), sb0 = sa0 + C::kStages * kStageA;
       const uint64_t ad0 = a_mn ? smem_desc_mn(sa0) : smem_desc(sa0);
       const uint64_t bd0 = b_mn ? smem_desc_mn(sb0) : smem_desc(sb0);
       constexpr uint32_t ka = (a_mn ? 16 * kRowBytes : 32) >> 4, kbs = (b_mn ? 16 * kRowBytes : 32) >> 4;
@@ -1049,19 +1087,19 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
             break;
           }
           tc_fence_after();
-          const uint32_t d_tmem = tmem_base + acc * kPairBN;
+          const uint32_t d_tmem = tmem_base + acc * kBN;
           const int k1 = min(k0 + P.segment, P.k_blocks);
           for (int kb = k0; kb < k1; ++kb) {
             if (!mbar_wait(full0 + 8 * s, ph, abort_flag, status, kStatusTimeoutFull)) {
               ok = false;
               break;
             }
-            const uint64_t ad = ad0 + s * (kStageA >> 4), bd = bd0 + s * (kStageB >> 4);
+            const uint64_t ad = ad0 + s * (kStageA >> 4), bd = bd0 + s * (C::kStageB >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_pair<kFp8>(d_tmem, ad + ka * kk, bd + kbs * kk, idesc, (kb > k0 || kk > 0) ? 1u : 0u);
             mma_commit_pair(empty0 + 8 * s);
-            if (++s == kPairStages) {
+            if (++s == C::kStages) {
               s = 0;
               ph ^= 1u;
             }
@@ -1084,7 +1122,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t empty_even = peer_addr(smem_u32(&acc_empty[0]), 0);
     const uint32_t tempty_even = peer_addr(smem_u32(&tile_empty[0]), 0);
-    uint8_t* stage = scratch + (warp - 2) * kWarpScratch;
+    uint8_t* stage = scratch + (warp - 2) * C::kWarpScratch;
     uint32_t use = 0;
     bool ok = true;
     for (uint32_t lt = 0; ok; ++lt) {
@@ -1108,12 +1146,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       int ta, tb;
       pair_tile(P, tile, ta, tb);
       const int64_t row0 = static_cast<int64_t>(tb) * 256 + rank * BM + quarter * 32;
-      const int64_t col0 = static_cast<int64_t>(ta) * kPairBN + half * 128;
-      const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
+      const int64_t col0 = static_cast<int64_t>(ta) * kBN + half * C::kHalf;
+      const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * C::kHalf;
       if constexpr (kMode == kLinearDw) {
-        float sum[128];
+        float sum[C::kHalf];
 #pragma unroll
-        for (int c = 0; c < 128; ++c) sum[c] = 0.f;
+        for (int c = 0; c < C::kHalf; ++c) sum[c] = 0.f;
         for (int k0 = 0; k0 < P.k_blocks; k0 += P.segment, ++use) {
           const uint32_t acc = use & 1;
           ok = __all_sync(0xffffffffu,
@@ -1121,9 +1159,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < 128; c += 16) {
+          for (int c = 0; c < C::kHalf; c += 16) {
             float v[16];
-            tmem_ld16(lane_addr + acc * kPairBN + c, v);
+            tmem_ld16(lane_addr + acc * kBN + c, v);
 #pragma unroll
             for (int j = 0; j < 16; ++j) sum[c + j] += v[j];
           }
@@ -1133,21 +1171,25 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
         if (!ok) break;
         if (row0 < P.g.nb) {
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) {
+          for (int c = 0; c < C::kHalf; c += 32) {
             if (col0 + c >= P.g.na) break;
             if (P.out_tma) {
-              if (lane == 0) bulk_wait_read_0();     // the previous block's store has read the staging area
+              uint8_t* const buf = stage + (c & 32 ? 4096 : 0);
+              if (lane == 0) {                         // this buffer's previous store has read it
+                if (c > 0) bulk_wait_read_1();
+                else bulk_wait_read_0();               // the last tile may have left either half busy
+              }
               __syncwarp();
 #pragma unroll
               for (int q = 0; q < 8; ++q)            // 128-byte swizzle
-                *reinterpret_cast<float4*>(stage + lane * 128 + ((q ^ (lane & 7)) * 16)) =
+                *reinterpret_cast<float4*>(buf + lane * 128 + ((q ^ (lane & 7)) * 16)) =
                     make_float4(sum[c + 4 * q], sum[c + 4 * q + 1], sum[c + 4 * q + 2], sum[c + 4 * q + 3]);
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) {
                 const int x = static_cast<int>(col0 + c), y = static_cast<int>(row0);
-                if (P.g.accumulate) tma_add_block(&map_out, smem_u32(stage), x, y);
-                else tma_store_block(&map_out, smem_u32(stage), x, y);
+                if (P.g.accumulate) tma_add_block(&map_out, smem_u32(buf), x, y);
+                else tma_store_block(&map_out, smem_u32(buf), x, y);
                 bulk_commit();
               }
             } else {
@@ -1164,13 +1206,13 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
         const uint16_t* in = kMode == kLinearDx ? P.g.z_in : P.g.residual;
         const int64_t in_ld = kMode == kLinearDx ? P.g.z_ld : P.g.residual_ld;
         const bool alternate = P.out_tma && (P.in_vec || !in) && !(kMode == kLinearForward && P.g.z_out) &&
-                               col0 + 128 <= P.g.na;      // no block of the tile goes through the table
+                               col0 + C::kHalf <= P.g.na;      // no block of the tile goes through the table
         const bool live = row0 < P.g.nb;
         // the tile's residual or pre-activation comes from DRAM while the MMAs run
         if (in && row0 + lane < P.g.nb && col0 < P.g.na) {
           const uint16_t* p = in + (row0 + lane) * in_ld + col0;
           prefetch_l2(p);
-          if (col0 + 64 < P.g.na) prefetch_l2(p + 64);
+          if (kBN == 256 && col0 + 64 < P.g.na) prefetch_l2(p + 64);
         }
         float row_scale = 1.f;
         if (kFp8 && row0 + lane < P.g.nb) row_scale = P.g.b_scale[row0 + lane];
@@ -1180,13 +1222,13 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
         if (!ok) break;
         ++use;
         tc_fence_after();
-        for (int c = 0; c < 128 && live && col0 + c < P.g.na; c += 32) {
+        for (int c = 0; c < C::kHalf && live && col0 + c < P.g.na; c += 32) {
           const int64_t col = col0 + c;
           // the staging area holds a block of y and one of z, or two of y in
           // turn; it doubles as the turning table of inputs and outputs that
           // cannot move 16 bytes at a time
           if (lane == 0) {
-            if (alternate) bulk_wait_read_1();
+            if (alternate && c > 0) bulk_wait_read_1();      // the last tile may have left either half busy
             else bulk_wait_read_0();
           }
           __syncwarp();
@@ -1194,7 +1236,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
           uint32_t raw[16];
           if (in) load_block(in, in_ld, row0, col, P.g.nb, P.g.na, P.in_vec != 0, reinterpret_cast<uint32_t*>(stage), lane, raw);
           float v[32];
-          tmem_ld32(lane_addr + acc * kPairBN + c, v);
+          tmem_ld32(lane_addr + acc * kBN + c, v);
           if constexpr (kMode == kLinearDx) {
             if (in)
               with_activation(P.g.act, [&](auto act) {
@@ -1276,7 +1318,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   }
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kPairTmemCols)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::kTmemCols)
                  : "memory");
   }
 }
@@ -1411,8 +1453,9 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
-template <int kMode, bool kFp8>
+template <int kMode, bool kFp8, int kBN>
 cudaError_t launch_pair(const LinearArgs& a, int k_blocks, int tiles_a, int tiles_b, cudaStream_t stream) {
+  using C = PairConfig<kMode, kBN>;
   PairParams P{};
   P.g = a;
   P.k_blocks = k_blocks;
@@ -1422,7 +1465,7 @@ cudaError_t launch_pair(const LinearArgs& a, int k_blocks, int tiles_a, int tile
   P.total_tiles = tiles_a * tiles_b;
   CUtensorMap ma, mb, mo{}, mz{};
   cudaError_t e;
-  if ((e = make_operand_map(&ma, a.A, a.na, a.nk, kFp8, kPairBNHalf)) != cudaSuccess) return e;
+  if ((e = make_operand_map(&ma, a.A, a.na, a.nk, kFp8, C::kHalf)) != cudaSuccess) return e;
   if ((e = make_operand_map(&mb, a.B, a.nb, a.nk, kFp8, BM)) != cudaSuccess) return e;
   if constexpr (kMode == kLinearDw) {
     P.out_tma = make_block_map(&mo, a.dw, a.dw_ld, a.nb, a.na, true);
@@ -1433,10 +1476,10 @@ cudaError_t launch_pair(const LinearArgs& a, int k_blocks, int tiles_a, int tile
     const int64_t in_ld = kMode == kLinearDx ? a.z_ld : a.residual_ld;
     P.in_vec = rows_on_16(in, in_ld, a.nb, 2);
   }
-  if ((e = allow_smem<linear_pair_kernel<kMode, kFp8>>(kPairSmemBytes)) != cudaSuccess) return e;
+  if ((e = allow_smem<linear_pair_kernel<kMode, kFp8, kBN>>(C::kSmemBytes)) != cudaSuccess) return e;
   const int max_pairs = num_sms() / 2;
   const int grid = 2 * (P.total_tiles < max_pairs ? P.total_tiles : max_pairs);
-  linear_pair_kernel<kMode, kFp8><<<grid, kPairThreads, kPairSmemBytes, stream>>>(mb, ma, mo, mz, P);
+  linear_pair_kernel<kMode, kFp8, kBN><<<grid, kPairThreads, C::kSmemBytes, stream>>>(mb, ma, mo, mz, P);
   return cudaGetLastError();
 }
 
@@ -1486,10 +1529,18 @@ template <int kMode, bool kFp8>
 cudaError_t launch_product(const LinearArgs& a, cudaStream_t stream) {
   constexpr int kElems = kFp8 ? 128 : 64;
   const int k_blocks = static_cast<int>((a.nk + kElems - 1) / kElems);
-  // the pair kernel once every CTA pair has a tile
-  const int64_t pair_a = (a.na + kPairBN - 1) / kPairBN, pair_b = (a.nb + 255) / 256;
-  if (pair_a * pair_b >= num_sms() / 2 && pair_a * pair_b < (int64_t(1) << 30))
-    return launch_pair<kMode, kFp8>(a, k_blocks, static_cast<int>(pair_a), static_cast<int>(pair_b), stream);
+  const int64_t tiles_b = (a.nb + 255) / 256, tiles256 = tiles_b * ((a.na + 255) / 256);
+  const int64_t tiles128 = tiles_b * ((a.na + 127) / 128), pairs = num_sms() / 2;
+  if (tiles256 < (int64_t(1) << 30) && tiles128 >= pairs / 2) {
+    // a 128-wide tile takes about 0.6 of a 256-wide one's time: it pays where
+    // the GPU would otherwise be filled badly
+    const int64_t waves256 = (tiles256 + pairs - 1) / pairs, waves128 = (tiles128 + pairs - 1) / pairs;
+    if (5 * waves256 <= 3 * waves128)
+      return launch_pair<kMode, kFp8, 256>(a, k_blocks, static_cast<int>((a.na + 255) / 256),
+                                           static_cast<int>(tiles_b), stream);
+    return launch_pair<kMode, kFp8, 128>(a, k_blocks, static_cast<int>((a.na + 127) / 128), static_cast<int>(tiles_b),
+                                         stream);
+  }
   if constexpr (kMode != kLinearDw) {
     if (a.nb <= 16) return launch_split<kMode, kFp8, 16, false>(a, k_blocks, stream);
     if (a.nb <= 32) return launch_split<kMode, kFp8, 32, false>(a, k_blocks, stream);

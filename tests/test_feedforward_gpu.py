@@ -244,9 +244,10 @@ def test_linear(m, n, k, e4m3, layout, kind):
     check_linear(m, n, k, e4m3, layout, kind)
 
 
-# at least 76 tiles of 256 x 256 for one of the three products: the persistent
-# kernel, with ragged last tiles, several tiles per CTA pair and few or many k-blocks
-LARGE_SHAPES = [(2100, 2300, 100), (2100, 100, 2300), (100, 2300, 2100), (4096, 2560, 264), (2305, 2311, 2333)]
+# enough tiles of 256 x 128 or 256 x 256 for one of the three products to take the
+# persistent kernel: ragged last tiles, several tiles per CTA pair, few or many k-blocks
+LARGE_SHAPES = [(2100, 2300, 100), (2100, 100, 2300), (100, 2300, 2100), (4096, 2560, 264), (2305, 2311, 2333),
+                (700, 4096, 2560), (4099, 2557, 261)]
 
 
 @pytest.mark.parametrize("m,n,k", LARGE_SHAPES)
