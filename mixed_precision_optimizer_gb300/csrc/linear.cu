@@ -29,9 +29,16 @@ constexpr int kStageA = BM * kRowBytes;
 
 // sqrt(2/pi) and the cubic's coefficient of the tanh form of GELU; with
 // (1 + tanh u) / 2 = sigmoid(2 u) both activations are u * sigmoid(t(u)).
-// __expf and __fdividef are within 2 units plus 2^-23 |t| of the value, far
-// below the bf16 rounding that follows.
-__device__ __forceinline__ float sigmoid(float t) { return __fdividef(1.f, 1.f + __expf(-t)); }
+// 1 / (1 + 2^(-t log2 e)) from the two approximate instructions: each is within
+// 2 units, and the rounding of t log2 e adds 2^-23 |t| of the value, far below
+// the bf16 rounding that follows.  (exp and a division as CUDA functions cost
+// 35 issue slots an element in dx's epilogue, against 16 for these.)
+__device__ __forceinline__ float sigmoid(float t) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * t));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
 
 constexpr float kGelu2 = 1.5957691216057308f;   // 2 sqrt(2/pi)
 constexpr float kGeluCubic = 0.044715f;
@@ -512,6 +519,8 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     load_operand(sb0 + s * C::kStageB, &map_b, full0 + 8 * s, b_mn, static_cast<int>(n0), kBN, kb, kElems);
   };
   if (threadIdx.x == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_a)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_b)) : "memory");
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
@@ -811,22 +820,27 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
 constexpr int kPairEpiWarps = 8;
 constexpr int kPairThreads = 96 + 32 * kPairEpiWarps;
 constexpr int kTileSlots = 3;
-constexpr int kBlockBytes = 32 * 32 * 2;
+constexpr int kBlockBytes = 32 * 128;   // a staged block: 32 rows of 128 bytes
 constexpr uint32_t kTileConsumers = 2 + 1 + 2 * kPairEpiWarps;
 
 template <int kMode, int kBN>
 struct PairConfig {
+  static constexpr int kBarrierReserve = 384;
   static constexpr int kHalf = kBN / 2;                      // columns staged by one CTA, and of an epilogue warp
   static constexpr int kStageB = kHalf * kRowBytes;
   static constexpr int kStageBytes = kStageA + kStageB;
-  // per epilogue warp, staged 32 x 32 blocks: bf16 y and z (or y twice), or two of fp32
-  static constexpr int kWarpScratch = kMode == kLinearDw ? 8192 : 4096;
-  static constexpr int kStages = (227 * 1024 - 1280 - kPairEpiWarps * kWarpScratch) / kStageBytes;
+  // per epilogue warp two blocks: y and z; y and the input (residual or
+  // pre-activation), which TMA loads while the MMAs run; or y's or dw's in turn.
+  // The second one is the turning table of inputs and outputs that cannot move
+  // 16 bytes at a time.
+  static constexpr int kWarpScratch = 2 * kBlockBytes;
+  static constexpr int kTableAt = kBlockBytes;
+  static constexpr int kStages = (227 * 1024 - 1024 - kBarrierReserve - kPairEpiWarps * kWarpScratch) / kStageBytes;
   static constexpr int kTmemCols = 2 * kBN;                  // two accumulators
-  static constexpr int kBarrierBytes = (2 * kStages + 5 + 2 * kTileSlots) * 8 + 8 + 4 * kTileSlots;
-  static_assert(kBarrierBytes <= 256, "barrier block larger than its 256-byte reservation");
+  static constexpr int kBarrierBytes = (2 * kStages + 5 + 2 * kTileSlots + kPairEpiWarps) * 8 + 8 + 4 * kTileSlots;
+  static_assert(kBarrierBytes <= kBarrierReserve, "barrier block larger than its reservation");
   static constexpr uint32_t kSmemBytes =
-      kStages * kStageBytes + kPairEpiWarps * kWarpScratch + 1024 /*align*/ + 256 /*barriers*/;
+      kStages * kStageBytes + kPairEpiWarps * kWarpScratch + 1024 /*align*/ + kBarrierReserve;
   static_assert(kSmemBytes <= 232448, "dynamic shared memory above the 227 KB a CTA may use");
 };
 
@@ -837,6 +851,7 @@ struct PairParams {
   int tiles_a, tiles_b, total_tiles;
   int out_tma;         // y (or dw) moves through map_out, z through map_z
   int in_vec;          // residual / z_in rows start on 16 bytes
+  int in_tma;          // and there is no z: the input comes through map_z
 };
 
 // Tiles in groups of kGroupB tiles along b, a-major inside a group: about 76
@@ -890,14 +905,28 @@ __device__ __forceinline__ void tma_add_block(const CUtensorMap* map, uint32_t s
                : "memory");
 }
 
-// Lane t holds row t of a 32 x 32 bf16 block: 64-byte swizzle for a TMA store.
-__device__ __forceinline__ void stage_bf16_rows(uint8_t* buf, int lane, const float (&v)[32]) {
+// Lane t stages 32 columns of row t of a block of 32 rows x 64 bf16 columns
+// (128 bytes, 128-byte swizzle) for a TMA store; `half` 32: the upper ones.
+__device__ __forceinline__ void stage_row(uint8_t* buf, int lane, int half, const float (&v)[32]) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const uint32_t phys = static_cast<uint32_t>(q) ^ ((static_cast<uint32_t>(lane) >> 1) & 3u);
-    *reinterpret_cast<uint4*>(buf + lane * 64 + phys * 16) =
+    const uint32_t phys = static_cast<uint32_t>(q + half / 8) ^ (static_cast<uint32_t>(lane) & 7u);
+    *reinterpret_cast<uint4*>(buf + lane * 128 + phys * 16) =
         make_uint4(pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
                    pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7]));
+  }
+}
+
+// The same columns of a block that TMA loaded, two elements to a word.
+__device__ __forceinline__ void unstage_row(const uint8_t* buf, int lane, int half, uint32_t (&raw)[16]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t phys = static_cast<uint32_t>(q + half / 8) ^ (static_cast<uint32_t>(lane) & 7u);
+    const uint4 w = *reinterpret_cast<const uint4*>(buf + lane * 128 + phys * 16);
+    raw[4 * q] = w.x;
+    raw[4 * q + 1] = w.y;
+    raw[4 * q + 2] = w.z;
+    raw[4 * q + 3] = w.w;
   }
 }
 
@@ -920,6 +949,14 @@ __device__ __forceinline__ void load_block(const uint16_t* p, int64_t ld, int64_
       raw[4 * i + 2] = w.z;
       raw[4 * i + 3] = w.w;
     }
+    return;
+  }
+  if (vec) {                               // the matrix ends inside the block
+    const uint16_t* q = p + (row0 + lane) * ld + col0;
+    const int n = row0 + lane < rows ? static_cast<int>(cols - col0) : 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      raw[i] = (2 * i < n ? q[2 * i] : 0u) | (2 * i + 1 < n ? static_cast<uint32_t>(q[2 * i + 1]) << 16 : 0u);
     return;
   }
   const bool ok = col0 + lane < cols;
@@ -966,7 +1003,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   uint64_t* drain = acc_empty + 2;                 // even CTA: all MMAs complete
   uint64_t* tile_full = drain + 1;                 // [kTileSlots] both CTAs: next tile published
   uint64_t* tile_empty = tile_full + kTileSlots;   // [kTileSlots] even CTA: every role has read it
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tile_empty + kTileSlots);
+  uint64_t* in_full = tile_empty + kTileSlots;     // [kPairEpiWarps] the warp's input block has landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(in_full + kPairEpiWarps);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   volatile int* tile_ring = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [kTileSlots]
 
@@ -992,8 +1030,13 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       mbar_init(smem_u32(&tile_full[k]), 1);
       mbar_init(smem_u32(&tile_empty[k]), kTileConsumers);
     }
+    for (int w = 0; w < kPairEpiWarps; ++w) mbar_init(smem_u32(&in_full[w]), 1);
     *abort_flag = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0 && lane < 4) {
+    const CUtensorMap* map = lane == 0 ? &map_a : lane == 1 ? &map_b : lane == 2 ? &map_out : &map_z;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -1014,18 +1057,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       const uint32_t sa0 = smem_u32(smem), sb0 = sa0 + C::kStages * kStageA;
       const uint32_t tempty_even = peer_addr(smem_u32(&tile_empty[0]), 0);
       uint32_t s = 0, ph = 0;
+      int tile = pair;             // the first tile; the others come through the ring
       for (uint32_t seq = 0; ok; ++seq) {
-        const uint32_t slot = seq % kTileSlots, sph = (seq / kTileSlots) & 1u;
-        if (!(rank == 0 ? mbar_wait(smem_u32(&tile_full[slot]), sph, abort_flag, status, kStatusTimeoutTile)
-                        : mbar_wait_acq_cluster(smem_u32(&tile_full[slot]), sph, abort_flag, status,
-                                                kStatusTimeoutTile))) {
-          ok = false;
-          break;
-        }
-        const int tile = tile_ring[slot];
-        if (rank == 0) mbar_arrive_local(smem_u32(&tile_empty[slot]));
-        else mbar_arrive_remote(tempty_even + 8 * slot);
-        if (tile >= P.total_tiles) break;
         int ta, tb;
         pair_tile(P, tile, ta, tb);
         const int ai = tb * 256 + static_cast<int>(rank) * BM, bi = ta * kBN + static_cast<int>(rank) * C::kHalf;
@@ -1055,6 +1088,18 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
             ph ^= 1u;
           }
         }
+        const uint32_t slot = seq % kTileSlots, sph = (seq / kTileSlots) & 1u;
+        if (!ok) break;
+        if (!(rank == 0 ? mbar_wait(smem_u32(&tile_full[slot]), sph, abort_flag, status, kStatusTimeoutTile)
+                        : mbar_wait_acq_cluster(smem_u32(&tile_full[slot]), sph, abort_flag, status,
+                                                kStatusTimeoutTile))) {
+          ok = false;
+          break;
+        }
+        tile = tile_ring[slot];
+        if (rank == 0) mbar_arrive_local(smem_u32(&tile_empty[slot]));
+        else mbar_arrive_remote(tempty_even + 8 * slot);
+        if (tile >= P.total_tiles) break;
       }
       if (!ok && issued) {
         // aborting: give copies in flight time to land before the CTA exits
@@ -1074,11 +1119,6 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       uint32_t s = 0, ph = 0, use = 0;          // use: accumulator uses so far
       bool ok = true;
       for (uint32_t lt = 0; ok; ++lt) {
-        const uint32_t slot = lt % kTileSlots, sph = (lt / kTileSlots) & 1u;
-        if (!mbar_wait(smem_u32(&tile_full[slot]), sph, abort_flag, status, kStatusTimeoutTile)) break;
-        const int tile = tile_ring[slot];
-        mbar_arrive_local(smem_u32(&tile_empty[slot]));
-        if (tile >= P.total_tiles) break;
         for (int k0 = 0; ok && k0 < P.k_blocks; k0 += P.segment, ++use) {
           const uint32_t acc = use & 1;
           if (!mbar_wait(smem_u32(&acc_empty[acc]), ((use >> 1) & 1u) ^ 1u, abort_flag, status,
@@ -1106,6 +1146,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
           }
           if (ok) mma_commit_pair(smem_u32(&acc_full[acc]));
         }
+        const uint32_t slot = lt % kTileSlots, sph = (lt / kTileSlots) & 1u;
+        if (!ok || !mbar_wait(smem_u32(&tile_full[slot]), sph, abort_flag, status, kStatusTimeoutTile)) break;
+        const int tile = tile_ring[slot];
+        mbar_arrive_local(smem_u32(&tile_empty[slot]));
+        if (tile >= P.total_tiles) break;
       }
       // every MMA issued by this thread has completed before TMEM goes
       mma_commit_local(smem_u32(drain));
@@ -1123,26 +1168,32 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
     const uint32_t empty_even = peer_addr(smem_u32(&acc_empty[0]), 0);
     const uint32_t tempty_even = peer_addr(smem_u32(&tile_empty[0]), 0);
     uint8_t* stage = scratch + (warp - 2) * C::kWarpScratch;
+    uint32_t* table = reinterpret_cast<uint32_t*>(stage + C::kTableAt);
+    const uint32_t in_bar = smem_u32(&in_full[warp - 2]);
+    uint32_t in_phase = 0;
     uint32_t use = 0;
     bool ok = true;
+    int tile = pair;
     for (uint32_t lt = 0; ok; ++lt) {
-      const uint32_t slot = lt % kTileSlots, sph = (lt / kTileSlots) & 1u;
-      int tile = 0, got = 1;
-      if (lane == 0) {
-        got = (rank == 0 ? mbar_wait(smem_u32(&tile_full[slot]), sph, abort_flag, status, kStatusTimeoutTile)
-                         : mbar_wait_acq_cluster(smem_u32(&tile_full[slot]), sph, abort_flag, status,
-                                                 kStatusTimeoutTile))
-                  ? 1
-                  : 0;
-        if (got) {
-          tile = tile_ring[slot];
-          if (rank == 0) mbar_arrive_local(smem_u32(&tile_empty[slot]));
-          else mbar_arrive_remote(tempty_even + 8 * slot);
+      if (lt > 0) {
+        const uint32_t slot = (lt - 1) % kTileSlots, sph = ((lt - 1) / kTileSlots) & 1u;
+        int got = 1;
+        if (lane == 0) {
+          got = (rank == 0 ? mbar_wait(smem_u32(&tile_full[slot]), sph, abort_flag, status, kStatusTimeoutTile)
+                           : mbar_wait_acq_cluster(smem_u32(&tile_full[slot]), sph, abort_flag, status,
+                                                   kStatusTimeoutTile))
+                    ? 1
+                    : 0;
+          if (got) {
+            tile = tile_ring[slot];
+            if (rank == 0) mbar_arrive_local(smem_u32(&tile_empty[slot]));
+            else mbar_arrive_remote(tempty_even + 8 * slot);
+          }
         }
+        got = __shfl_sync(0xffffffffu, got, 0);
+        tile = __shfl_sync(0xffffffffu, tile, 0);
+        if (!got || tile >= P.total_tiles) break;
       }
-      got = __shfl_sync(0xffffffffu, got, 0);
-      tile = __shfl_sync(0xffffffffu, tile, 0);
-      if (!got || tile >= P.total_tiles) break;
       int ta, tb;
       pair_tile(P, tile, ta, tb);
       const int64_t row0 = static_cast<int64_t>(tb) * 256 + rank * BM + quarter * 32;
@@ -1197,7 +1248,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] = sum[c + j];
               const bool add = P.g.accumulate != 0;
-              store_turned(P.g.dw, P.g.dw_ld, row0, col0 + c, P.g.nb, P.g.na, reinterpret_cast<float*>(stage), lane, v,
+              store_turned(P.g.dw, P.g.dw_ld, row0, col0 + c, P.g.nb, P.g.na, reinterpret_cast<float*>(table), lane, v,
                            [add](float* p, float x) { *p = add ? *p + x : x; });
             }
           }
@@ -1205,15 +1256,17 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       } else {
         const uint16_t* in = kMode == kLinearDx ? P.g.z_in : P.g.residual;
         const int64_t in_ld = kMode == kLinearDx ? P.g.z_ld : P.g.residual_ld;
-        const bool alternate = P.out_tma && (P.in_vec || !in) && !(kMode == kLinearForward && P.g.z_out) &&
-                               col0 + C::kHalf <= P.g.na;      // no block of the tile goes through the table
         const bool live = row0 < P.g.nb;
-        // the tile's residual or pre-activation comes from DRAM while the MMAs run
-        if (in && row0 + lane < P.g.nb && col0 < P.g.na) {
-          const uint16_t* p = in + (row0 + lane) * in_ld + col0;
-          prefetch_l2(p);
-          if (kBN == 256 && col0 + 64 < P.g.na) prefetch_l2(p + 64);
-        }
+        // the first input block comes while the MMAs run
+        auto load_in = [&](int c) {
+          if (lane == 0) {
+            mbar_expect_tx(in_bar, kBlockBytes);
+            tma_load_2d(smem_u32(stage + kBlockBytes), &map_z, in_bar, static_cast<int>(col0) + c, static_cast<int>(row0));
+          }
+        };
+        const bool in_tma = P.in_tma != 0;
+        if (in_tma && live && col0 < P.g.na) load_in(0);
+        const bool alternate = P.out_tma && !in && !(kMode == kLinearForward && P.g.z_out);
         float row_scale = 1.f;
         if (kFp8 && row0 + lane < P.g.nb) row_scale = P.g.b_scale[row0 + lane];
         const uint32_t acc = use & 1;
@@ -1224,17 +1277,29 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
         tc_fence_after();
         for (int c = 0; c < C::kHalf && live && col0 + c < P.g.na; c += 32) {
           const int64_t col = col0 + c;
-          // the staging area holds a block of y and one of z, or two of y in
-          // turn; it doubles as the turning table of inputs and outputs that
-          // cannot move 16 bytes at a time
-          if (lane == 0) {
-            if (alternate && c > 0) bulk_wait_read_1();      // the last tile may have left either half busy
-            else bulk_wait_read_0();
-          }
-          __syncwarp();
-          uint8_t* const buf = alternate ? stage + (c & 32 ? kBlockBytes : 0) : stage;
+          uint8_t* const buf = alternate ? stage + (c & 64 ? kBlockBytes : 0) : stage;
           uint32_t raw[16];
-          if (in) load_block(in, in_ld, row0, col, P.g.nb, P.g.na, P.in_vec != 0, reinterpret_cast<uint32_t*>(stage), lane, raw);
+          if (!(c & 32)) {                             // a new block: its staging area's last store has read it
+            if (lane == 0) {
+              if (alternate && c > 0) bulk_wait_read_1();
+              else bulk_wait_read_0();
+            }
+            __syncwarp();
+            if (in_tma) {
+              ok = __all_sync(0xffffffffu, mbar_wait(in_bar, in_phase, abort_flag, status, kStatusTimeoutWload));
+              if (!ok) break;
+              in_phase ^= 1u;
+            }
+          }
+          if (in_tma) {
+            unstage_row(stage + kBlockBytes, lane, c & 32, raw);
+            if ((c & 32) && c + 32 < C::kHalf && col + 32 < P.g.na) {
+              __syncwarp();                            // every lane has read the block: the next one may land in it
+              load_in(c + 32);
+            }
+          } else if (in) {
+            load_block(in, in_ld, row0, col, P.g.nb, P.g.na, P.in_vec != 0, table, lane, raw);
+          }
           float v[32];
           tmem_ld32(lane_addr + acc * kBN + c, v);
           if constexpr (kMode == kLinearDx) {
@@ -1256,9 +1321,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
               for (int j = 0; j < 32; ++j) v[j] += t[j];
             }
             if (P.g.z_out) {
-              if (P.out_tma) stage_bf16_rows(stage + kBlockBytes, lane, v);
+              if (P.out_tma) stage_row(stage + kBlockBytes, lane, c & 32, v);
               else
-                store_turned(P.g.z_out, P.g.z_ld, row0, col, P.g.nb, P.g.na, reinterpret_cast<float*>(stage), lane, v,
+                store_turned(P.g.z_out, P.g.z_ld, row0, col, P.g.nb, P.g.na, reinterpret_cast<float*>(table), lane, v,
                              [](uint16_t* p, float x) { *p = to_bf16(x); });
             }
             with_activation(P.g.act, [&](auto act) {
@@ -1271,22 +1336,31 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
             }
           }
           if (P.out_tma) {
-            stage_bf16_rows(buf, lane, v);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              const int x = static_cast<int>(col), y = static_cast<int>(row0);
-              tma_store_block(&map_out, smem_u32(buf), x, y);
-              if (kMode == kLinearForward && P.g.z_out) tma_store_block(&map_z, smem_u32(stage + kBlockBytes), x, y);
-              bulk_commit();
+            stage_row(buf, lane, c & 32, v);
+            if ((c & 32) || col + 32 >= P.g.na) {          // both halves of the block, or the last one
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                const int x = static_cast<int>(col) - (c & 32), y = static_cast<int>(row0);
+                tma_store_block(&map_out, smem_u32(buf), x, y);
+                if (kMode == kLinearForward && P.g.z_out) tma_store_block(&map_z, smem_u32(stage + kBlockBytes), x, y);
+                bulk_commit();
+              }
             }
           } else {
-            store_turned(P.g.y, P.g.y_ld, row0, col, P.g.nb, P.g.na, reinterpret_cast<float*>(stage), lane, v,
+            store_turned(P.g.y, P.g.y_ld, row0, col, P.g.nb, P.g.na, reinterpret_cast<float*>(table), lane, v,
                          [](uint16_t* p, float x) { *p = to_bf16(x); });
           }
         }
+        if (!ok) break;
         tc_fence_before();
         mbar_arrive_remote(empty_even + acc * 8);
+      }
+    }
+    if (!ok && lane == 0) {
+      // aborting: give an input block in flight time to land before the CTA exits
+      const unsigned long long t0 = global_ns();
+      while (global_ns() - t0 < 10000000ull) {
       }
     }
     if (lane == 0) bulk_wait_all();        // stores complete before the CTA exits
@@ -1296,7 +1370,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
     for (uint32_t seq = 0;; ++seq) {
       const uint32_t slot = seq % kTileSlots, sph = (seq / kTileSlots) & 1u;
       if (!mbar_wait(smem_u32(&tile_empty[slot]), sph ^ 1u, abort_flag, status, kStatusTimeoutTile)) break;
-      const int tile = seq == 0 ? pair : npairs + static_cast<int>(atomicAdd(status + kSchedWord, 1u));
+      const int tile = npairs + static_cast<int>(atomicAdd(status + kSchedWord, 1u));
       tile_ring[slot] = tile;
       st_cluster_u32(ring_odd + 4 * slot, static_cast<uint32_t>(tile));
       mbar_arrive_local(smem_u32(&tile_full[slot]));
@@ -1424,8 +1498,8 @@ bool rows_on_16(const void* p, int64_t ld, int64_t rows, int es) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows <= 1 || (ld * es) % 16 == 0);
 }
 
-// 2-D map of an output [rows][cols] of 2- or 4-byte elements in 32 x 32
-// blocks (64- or 128-byte swizzle); false when TMA cannot address it.
+// 2-D map of an output [rows][cols] in blocks of 32 rows x 128 bytes (128-byte
+// swizzle); false when TMA cannot address it.
 bool make_block_map(CUtensorMap* map, const void* p, int64_t ld, int64_t rows, int64_t cols, bool fp32) {
   const int es = fp32 ? 4 : 2;
   EncodeTiledFn fn = encode_fn();
@@ -1433,11 +1507,11 @@ bool make_block_map(CUtensorMap* map, const void* p, int64_t ld, int64_t rows, i
   if (rows <= 1) ld = (cols + 7) / 8 * 8;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * es)};
-  const cuuint32_t box[2] = {32, 32};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kRowBytes / es), 32};
   const cuuint32_t estr[2] = {1, 1};
   return fn(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p),
             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            fp32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1475,6 +1549,8 @@ cudaError_t launch_pair(const LinearArgs& a, int k_blocks, int tiles_a, int tile
     const uint16_t* in = kMode == kLinearDx ? a.z_in : a.residual;
     const int64_t in_ld = kMode == kLinearDx ? a.z_ld : a.residual_ld;
     P.in_vec = rows_on_16(in, in_ld, a.nb, 2);
+    if (in && !P.in_vec && a.z_out) P.out_tma = 0;       // the table would take z's staging area
+    P.in_tma = in && P.out_tma && P.in_vec && !a.z_out && make_block_map(&mz, in, in_ld, a.nb, a.na, false);
   }
   if ((e = allow_smem<linear_pair_kernel<kMode, kFp8, kBN>>(C::kSmemBytes)) != cudaSuccess) return e;
   const int max_pairs = num_sms() / 2;
