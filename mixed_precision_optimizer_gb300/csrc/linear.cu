@@ -1607,7 +1607,11 @@ cudaError_t launch_product(const LinearArgs& a, cudaStream_t stream) {
   const int k_blocks = static_cast<int>((a.nk + kElems - 1) / kElems);
   const int64_t tiles_b = (a.nb + 255) / 256, tiles256 = tiles_b * ((a.na + 255) / 256);
   const int64_t tiles128 = tiles_b * ((a.na + 127) / 128), pairs = num_sms() / 2;
-  if (tiles256 < (int64_t(1) << 30) && tiles128 >= pairs / 2) {
+  // The pair kernel once 256 x 128 tiles fill the pairs (64 of them: the split
+  // kernel takes 9.4 us for 2048 x 1024 x 1024 against 11.7, 14.6 for 1024 x 2048
+  // x 2048 against 16.4; 128: 45 us for 1024 x 4096 x 4096 against 28) and the
+  // rows fill more than half of a tile (128 x 4096 x 4096: 13 us against 25).
+  if (a.nb > 128 && tiles256 < (int64_t(1) << 30) && tiles128 >= pairs) {
     // a 128-wide tile takes about 0.6 of a 256-wide one's time: it pays where
     // the GPU would otherwise be filled badly
     const int64_t waves256 = (tiles256 + pairs - 1) / pairs, waves128 = (tiles128 + pairs - 1) / pairs;
