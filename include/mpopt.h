@@ -647,8 +647,9 @@ enum {
   OPT_KERNEL_LINEAR_DX = 17,
   OPT_KERNEL_LINEAR_DW = 18,
   OPT_KERNEL_LINEAR_DBIAS = 19,
-  OPT_KERNEL_LINEAR_REPACK = 20 /* operands (count of them) copied to 16-byte
+  OPT_KERNEL_LINEAR_REPACK = 20, /* operands (count of them) copied to 16-byte
                                    aligned rows; a, b of the largest             */
+  OPT_KERNEL_LINEAR_GRAD = 21   /* dx, dw and dbias of a short batch at once      */
 };
 
 MPOPT_API opt_status opt_profile_launches(void* const* events, opt_launch_info* info, int32_t capacity,

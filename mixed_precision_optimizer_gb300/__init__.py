@@ -96,7 +96,8 @@ EXPORTED = ("opt_workspace_size", "opt_adamw_step", "opt_muon_step", "opt_mixed_
 KERNEL_NAMES = {0: "ns_gram", 1: "ns_poly", 2: "ns_bx", 3: "adamw", 4: "muon_momentum", 5: "muon_norm",
                 6: "muon_apply", 7: "muon_fixup", 8: "grad_norm", 9: "clip_finalize", 10: "muon_sample",
                 11: "ns_sym", 12: "rmsnorm", 13: "rmsnorm_grad", 14: "rmsnorm_dgamma", 15: "quantize_rows",
-                16: "linear", 17: "linear_dx", 18: "linear_dw", 19: "linear_dbias", 20: "linear_repack"}
+                16: "linear", 17: "linear_dx", 18: "linear_dw", 19: "linear_dbias", 20: "linear_repack",
+                21: "linear_grad"}
 WORKSPACE_CLIP = 0x10
 WORKSPACE_GROUPED = 0x20
 

@@ -290,6 +290,8 @@ opt_status opt_linear_backward(const opt_linear_grad_args* a, void* workspace, s
                                          : 0;
   if (a->dx || a->dw || sums) MPOPT_TRY(check_workspace(workspace, workspace_bytes, kLinearHeaderBytes + products + sums));
   uint8_t* const scratch = static_cast<uint8_t*>(workspace) + kLinearHeaderBytes;
+  const ColumnSumArgs column_sums{a->dz,    a->dz_ld, a->m, a->n, a->dbias, reinterpret_cast<float*>(scratch),
+                                  a->accumulate};
   if (a->dx || a->dw) {
     Repacker rp{scratch + sums, workspace_bytes - kLinearHeaderBytes - sums, 2};
     LinearOperand dz{}, w{}, x{};
@@ -297,42 +299,46 @@ opt_status opt_linear_backward(const opt_linear_grad_args* a, void* workspace, s
     if (a->dx) MPOPT_TRY(rp.operand(a->w, a->w_ld, a->n, a->k, 1, &w));
     if (a->dw) MPOPT_TRY(rp.operand(a->x, a->x_ld, a->m, a->k, 1, &x));
     MPOPT_TRY(rp.launch(st));
-    if (a->dx) {
-      LinearArgs g{};
-      g.mode = kLinearDx;
-      g.A = w;
-      g.B = dz;
-      g.na = a->k;
-      g.nb = a->m;
-      g.nk = a->n;
-      g.act = a->act_prev;
-      g.z_in = a->z_prev;
-      g.z_ld = a->z_prev_ld;
-      g.y = a->dx;
-      g.y_ld = a->dx_ld;
-      g.header = static_cast<uint32_t*>(workspace);
-      MPOPT_TRY(run_product(g, OPT_KERNEL_LINEAR_DX, a->m, a->k, st, "linear dx launch"));
-    }
-    if (a->dw) {
-      LinearArgs g{};
-      g.mode = kLinearDw;
-      g.A = x;
-      g.B = dz;
-      g.B.mn_major = 1;
-      g.na = a->k;
-      g.nb = a->n;
-      g.nk = a->m;
-      g.dw = a->dw;
-      g.dw_ld = a->k;
-      g.accumulate = a->accumulate;
-      g.header = static_cast<uint32_t*>(workspace);
-      MPOPT_TRY(run_product(g, OPT_KERNEL_LINEAR_DW, a->n, a->k, st, "linear dw launch"));
+    LinearArgs gx{};
+    gx.mode = kLinearDx;
+    gx.A = w;
+    gx.B = dz;
+    gx.na = a->k;
+    gx.nb = a->m;
+    gx.nk = a->n;
+    gx.act = a->act_prev;
+    gx.z_in = a->z_prev;
+    gx.z_ld = a->z_prev_ld;
+    gx.y = a->dx;
+    gx.y_ld = a->dx_ld;
+    gx.header = static_cast<uint32_t*>(workspace);
+    LinearArgs gw{};
+    gw.mode = kLinearDw;
+    gw.A = x;
+    gw.B = dz;
+    gw.B.mn_major = 1;
+    gw.na = a->k;
+    gw.nb = a->n;
+    gw.nk = a->m;
+    gw.dw = a->dw;
+    gw.dw_ld = a->k;
+    gw.accumulate = a->accumulate;
+    gw.header = static_cast<uint32_t*>(workspace);
+    if (a->dx && a->dw && linear_grad_fits(gx, gw)) {
+      const bool with_sums = a->dbias && column_sum_slices(a->m, a->n) == 1;
+      prof_begin(OPT_KERNEL_LINEAR_GRAD, 1, a->m, a->n, st);
+      const cudaError_t e = launch_linear_grad(gx, gw, with_sums ? &column_sums : nullptr, st);
+      prof_end(st);
+      MPOPT_TRY(cuda_status(e, "linear gradient launch"));
+      if (with_sums) return OPT_OK;
+    } else {
+      if (a->dx) MPOPT_TRY(run_product(gx, OPT_KERNEL_LINEAR_DX, a->m, a->k, st, "linear dx launch"));
+      if (a->dw) MPOPT_TRY(run_product(gw, OPT_KERNEL_LINEAR_DW, a->n, a->k, st, "linear dw launch"));
     }
   }
   if (a->dbias) {
     prof_begin(OPT_KERNEL_LINEAR_DBIAS, 1, a->m, a->n, st);
-    const cudaError_t e = launch_column_sums(a->dz, a->dz_ld, a->m, a->n, a->dbias, reinterpret_cast<float*>(scratch),
-                                             a->accumulate, st);
+    const cudaError_t e = launch_column_sums(column_sums, st);
     prof_end(st);
     MPOPT_TRY(cuda_status(e, "linear bias gradient launch"));
   }

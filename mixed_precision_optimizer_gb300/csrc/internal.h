@@ -323,8 +323,18 @@ inline int64_t column_sum_slices(int64_t m, int64_t n) {
   const int64_t s = by_rows < wanted ? by_rows : wanted;
   return s < 1 ? 1 : s > 64 ? 64 : s;
 }
-cudaError_t launch_column_sums(const uint16_t* dz, int64_t ld, int64_t m, int64_t n, float* out, float* partial,
-                               int accumulate, cudaStream_t stream);
+struct ColumnSumArgs {
+  const uint16_t* dz;
+  int64_t ld, m, n;
+  float *out, *partial;
+  int accumulate;
+};
+cudaError_t launch_column_sums(const ColumnSumArgs& a, cudaStream_t stream);
+// dx, dw and (with one slice of rows, otherwise null) dbias in one launch, for
+// products that linear_grad_fits.
+bool linear_grad_fits(const LinearArgs& dx, const LinearArgs& dw);
+cudaError_t launch_linear_grad(const LinearArgs& dx, const LinearArgs& dw, const ColumnSumArgs* sums,
+                               cudaStream_t stream);
 // Copies of operands with rows on 16 bytes: dst rows (dst_ld elements apart, a
 // multiple of 16 bytes) <- src rows, elements of 1 or 2 bytes, zeros behind them.
 struct RepackMatrix {

@@ -462,8 +462,9 @@ struct SplitParams {
   int k_blocks;        // of the whole product
   int per_rank;        // k-blocks of one CTA of the cluster
   int segment;         // k-blocks accumulated in TMEM at a time
-  int split;           // CTAs per cluster
+  int split;           // CTAs that share a tile; divides the cluster's size
   int64_t tiles_m;     // tiles along the lanes' index
+  int64_t tiles;
   RowAccess access;
 };
 
@@ -482,10 +483,11 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t cluster_addr) {
   return v;
 }
 
+// The work of CTA `block` of a product's CTAs (maps and params are kernel
+// parameters).
 template <int kMode, bool kFp8, int kBN, bool kRows>
-__global__ void __launch_bounds__(kSplitThreads, 2)
-linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                    const __grid_constant__ SplitParams P) {
+__device__ __forceinline__ void split_tile(const CUtensorMap& map_a, const CUtensorMap& map_b, const SplitParams& P,
+                                           int64_t block) {
   using C = SplitConfig<kBN>;
   constexpr int kElems = kFp8 ? 128 : 64;
   // the MMA's A operand is the lanes' index: output rows (the product's B) or columns (its A)
@@ -503,12 +505,15 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
   volatile uint32_t* abort_flag = tmem_slot + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* status = P.g.header;
-  const int rank = P.split > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int64_t tile = blockIdx.x / P.split;
+  // the CTAs first_rank .. first_rank + split - 1 of the cluster share a tile
+  const int in_cluster = P.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int rank = in_cluster & (P.split - 1), first_rank = in_cluster - rank;
+  const int64_t tile = block / P.split;
+  const bool exists = tile < P.tiles;          // the last cluster may have CTAs to spare
   const int64_t m0 = tile % P.tiles_m * BM, n0 = tile / P.tiles_m * kBN;   // first lane's and first column's index
   const int64_t n_end = kRows ? P.g.na : P.g.nb;
   // this CTA's k-blocks; the last ranks may have none, and their sums are zero
-  const int kb0 = min(rank * P.per_rank, P.k_blocks), kb1 = min(kb0 + P.per_rank, P.k_blocks);
+  const int kb0 = min(rank * P.per_rank, P.k_blocks), kb1 = exists ? min(kb0 + P.per_rank, P.k_blocks) : kb0;
 
   const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
   const uint32_t sa0 = smem_u32(smem), sb0 = sa0 + C::kStages * kStageA;
@@ -625,10 +630,10 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
 #pragma unroll
     for (int c = 0; c < kSum; ++c) sum[c] = 0.f;
     uint32_t use = 0;
-    ready = true;
+    ready = exists;
     if constexpr (kMode == kLinearDw) {
       const int64_t c = n0 + rank * (kBN / P.split);
-      if (P.g.accumulate && index < P.g.nb && c < P.g.na) {
+      if (exists && P.g.accumulate && index < P.g.nb && c < P.g.na) {
         const float* p = P.g.dw + index * P.g.dw_ld + c;
         prefetch_l2(p);
         if (P.split == 1 && c + 32 < P.g.na) prefetch_l2(p + 32);
@@ -637,7 +642,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
       // the residual or pre-activation of this rank's share comes from DRAM while the MMAs run
       const uint16_t* in = kMode == kLinearDx ? P.g.z_in : P.g.residual;
       const int64_t c = n0 + rank * (kBN / P.split);
-      if (in && index < P.g.nb && c < P.g.na)
+      if (exists && in && index < P.g.nb && c < P.g.na)
         prefetch_l2(in + index * (kMode == kLinearDx ? P.g.z_ld : P.g.residual_ld) + c);
     }
     for (int k0 = kb0; ready && k0 < kb1; k0 += P.segment, ++use) {
@@ -709,7 +714,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
         float4 w[kSplit][kGroup / 4];
 #pragma unroll
         for (int p = 0; p < kSplit; ++p) {
-          const uint32_t peer = peer_addr(base, static_cast<uint32_t>(p));
+          const uint32_t peer = peer_addr(base, static_cast<uint32_t>(first_rank + p));
 #pragma unroll
           for (int i = 0; i < kGroup / 4; ++i) w[p][i] = ld_cluster_f32x4(peer + ((c4 + g) / 4 + i) * (BM * 16));
         }
@@ -781,6 +786,107 @@ linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::kTmemCols)
                  : "memory");
+  }
+}
+
+template <int kMode, bool kFp8, int kBN, bool kRows>
+__global__ void __launch_bounds__(kSplitThreads, 2)
+linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                    const __grid_constant__ SplitParams P) {
+  split_tile<kMode, kFp8, kBN, kRows>(map_a, map_b, P, blockIdx.x);
+}
+
+// The column sums of dz, in a fixed order.  CTA (x, y) takes 64 columns of the
+// rows of its y-th slice, each of its six warps every sixth of them, two
+// columns to a lane, and adds its warps' sums in order; with one slice that is
+// the result, otherwise the slices' sums go to `partial` and join_sums_kernel
+// adds them in order.
+struct ColumnSums {
+  const uint16_t* dz;
+  int64_t ld, m, n;
+  float *out, *partial;
+  int accumulate;
+  int vec;             // both columns of a lane in one 4-byte load
+};
+constexpr int kSumCols = 64;
+
+__device__ __forceinline__ void column_sums(const ColumnSums& p, int64_t x, int64_t y, int64_t slices) {
+  __shared__ float2 sums[kSplitThreads / 32][32];
+  constexpr int kWarps = kSplitThreads / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t c = x * kSumCols + 2 * lane;
+  const int64_t per = (p.m + slices - 1) / slices;
+  const int64_t r0 = per * y, r1 = r0 + per < p.m ? r0 + per : p.m;
+  float2 s = make_float2(0.f, 0.f);
+  if (c < p.n) {
+    if (p.vec) {
+#pragma unroll 16
+      for (int64_t r = r0 + warp; r < r1; r += kWarps) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(p.dz + r * p.ld + c);
+        s.x += __uint_as_float(w << 16);
+        s.y += __uint_as_float(w & 0xffff0000u);
+      }
+    } else {
+      const int64_t two = c + 1 < p.n ? 1 : 0;       // past the last column: that one again, not stored
+#pragma unroll 16
+      for (int64_t r = r0 + warp; r < r1; r += kWarps) {
+        s.x += bf16_at(p.dz + r * p.ld + c, 0);
+        s.y += bf16_at(p.dz + r * p.ld + c, two);
+      }
+    }
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0) {
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+      s.x += sums[w][lane].x;
+      s.y += sums[w][lane].y;
+    }
+    float* o = slices > 1 ? p.partial + y * p.n : p.out;
+    const bool add = slices == 1 && p.accumulate;
+    if (c < p.n) o[c] = add ? o[c] + s.x : s.x;
+    if (c + 1 < p.n) o[c + 1] = add ? o[c + 1] + s.y : s.y;
+  }
+}
+
+__global__ void __launch_bounds__(kSplitThreads) column_sums_kernel(const __grid_constant__ ColumnSums p) {
+  column_sums(p, blockIdx.x, blockIdx.y, gridDim.y);
+}
+
+__global__ void __launch_bounds__(128)
+join_sums_kernel(const float* partial, int slices, int64_t n, float* out, int accumulate) {
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
+  if (c >= n) return;
+  float s = 0.f;
+#pragma unroll 8
+  for (int p = 0; p < slices; ++p) s += partial[p * n + c];
+  out[c] = accumulate ? out[c] + s : s;
+}
+
+// dx, dw and dbias of a short batch in one launch: CTAs 0 .. dx_blocks - 1
+// compute dx, the next dw_blocks dw, the others 64 columns of dbias each.  The
+// three are independent and each alone leaves most of the GPU idle; every
+// result has the bits that it has from a launch of its own.
+struct GradParams {
+  SplitParams dx, dw;
+  ColumnSums sums;
+  int64_t dx_blocks, dw_blocks;      // multiples of the cluster's size
+};
+
+template <int kBN, bool kRows>
+__global__ void __launch_bounds__(kSplitThreads, 2)
+linear_grad_kernel(const __grid_constant__ CUtensorMap dx_a, const __grid_constant__ CUtensorMap dx_b,
+                   const __grid_constant__ CUtensorMap dw_a, const __grid_constant__ CUtensorMap dw_b,
+                   const __grid_constant__ GradParams P) {
+  const int64_t block = blockIdx.x;
+  if (block < P.dx_blocks) {
+    split_tile<kLinearDx, false, kBN, kRows>(dx_a, dx_b, P.dx, block);
+  } else if (block < P.dx_blocks + P.dw_blocks) {
+    split_tile<kLinearDw, false, 64, true>(dw_a, dw_b, P.dw, block - P.dx_blocks);
+  } else {
+    const int64_t x = block - P.dx_blocks - P.dw_blocks;
+    if (x * kSumCols < P.sums.n) column_sums(P.sums, x, 0, 1);
   }
 }
 
@@ -1399,60 +1505,6 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
 
 // ------------------------------------------------------- smaller kernels --
 
-// Column sums of dz in a fixed order.  CTA (x, y) takes 64 columns of the rows
-// of its y-th slice, each warp every eighth of them, two columns to a lane, and
-// adds its warps' sums in order; with one slice that is the result, otherwise
-// the slices' sums go to `partial` and join_sums_kernel adds them in order.
-constexpr int kSumCols = 64;
-
-template <bool kVec>
-__global__ void __launch_bounds__(256)
-column_sums_kernel(const uint16_t* dz, int64_t ld, int64_t m, int64_t n, float* out, float* partial, int accumulate) {
-  __shared__ float2 sums[8][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kSumCols + 2 * lane;
-  const int64_t per = (m + gridDim.y - 1) / gridDim.y;
-  const int64_t r0 = per * blockIdx.y, r1 = r0 + per < m ? r0 + per : m;
-  float2 s = make_float2(0.f, 0.f);
-  if (c < n) {
-    const bool two = c + 1 < n;
-#pragma unroll 8
-    for (int64_t r = r0 + warp; r < r1; r += 8) {
-      const uint16_t* p = dz + r * ld + c;
-      if (kVec) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-        s.x += __uint_as_float(w << 16);
-        s.y += __uint_as_float(w & 0xffff0000u);
-      } else {
-        s.x += bf16_at(p, 0);
-        if (two) s.y += bf16_at(p, 1);
-      }
-    }
-  }
-  sums[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0) {
-    for (int w = 1; w < 8; ++w) {
-      s.x += sums[w][lane].x;
-      s.y += sums[w][lane].y;
-    }
-    float* o = gridDim.y > 1 ? partial + static_cast<int64_t>(blockIdx.y) * n : out;
-    const bool add = gridDim.y == 1 && accumulate;
-    if (c < n) o[c] = add ? o[c] + s.x : s.x;
-    if (c + 1 < n) o[c + 1] = add ? o[c + 1] + s.y : s.y;
-  }
-}
-
-__global__ void __launch_bounds__(128)
-join_sums_kernel(const float* partial, int slices, int64_t n, float* out, int accumulate) {
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
-  if (c >= n) return;
-  float s = 0.f;
-#pragma unroll 8
-  for (int p = 0; p < slices; ++p) s += partial[p * n + c];
-  out[c] = accumulate ? out[c] + s : s;
-}
-
 // Operand copies with rows on 16 bytes, up to three in one launch.  A thread
 // writes one 16-byte piece of a row from as many single-element loads; a warp's
 // loads of one turn lie within 512 bytes of a row.
@@ -1559,73 +1611,117 @@ cudaError_t launch_pair(const LinearArgs& a, int k_blocks, int tiles_a, int tile
   return cudaGetLastError();
 }
 
+int k_blocks_of(const LinearArgs& a) {
+  const int64_t elems = a.fp8 ? 128 : 64;
+  return static_cast<int>((a.nk + elems - 1) / elems);
+}
+
+// Parameters and operand maps of a split product: m on the lanes, n on the columns.
 template <int kMode, bool kFp8, int kBN, bool kRows>
-cudaError_t launch_split(const LinearArgs& a, int k_blocks, cudaStream_t stream) {
-  using C = SplitConfig<kBN>;
-  SplitParams P{};
-  P.g = a;
-  P.k_blocks = k_blocks;
-  P.tiles_m = ((kRows ? a.nb : a.na) + BM - 1) / BM;
-  const int64_t tiles = P.tiles_m * (((kRows ? a.na : a.nb) + kBN - 1) / kBN);
-  // split while the clusters still run at once, two CTAs to an SM, and each
-  // CTA keeps 4 k-blocks (about the time its start and the join take)
-  P.split = 1;
-  while (P.split < kMaxSplit && tiles * P.split * 2 <= 2 * num_sms() && k_blocks >= P.split * 2 * 4) P.split *= 2;
-  P.per_rank = (k_blocks + P.split - 1) / P.split;
-  P.segment = kMode == kLinearDw ? kDwSegment : k_blocks;
+cudaError_t plan_split(const LinearArgs& a, SplitParams* P, CUtensorMap* m, CUtensorMap* n) {
+  P->g = a;
+  P->k_blocks = k_blocks_of(a);
+  P->tiles_m = ((kRows ? a.nb : a.na) + BM - 1) / BM;
+  P->tiles = P->tiles_m * (((kRows ? a.na : a.nb) + kBN - 1) / kBN);
+  // split while the CTAs still run at once, two to an SM, and each keeps 4
+  // k-blocks (8 or 12: 10 to 50 % slower on 100 x 776 x 1000 and 1 x 2048 x 2048;
+  // one CTA to an SM: 15 % slower on 331 x 2048 x 1024 and 64 x 4096 x 4096)
+  P->split = 1;
+  while (P->split < kMaxSplit && P->tiles * P->split * 2 <= 2 * num_sms() && P->k_blocks >= P->split * 2 * 4)
+    P->split *= 2;
+  P->per_rank = (P->k_blocks + P->split - 1) / P->split;
+  P->segment = kMode == kLinearDw ? kDwSegment : P->k_blocks;
   if (kMode == kLinearDw) {
-    P.access.out_vec = rows_on_16(a.dw, a.dw_ld, a.nb, 4);
+    P->access.out_vec = rows_on_16(a.dw, a.dw_ld, a.nb, 4);
   } else {
-    P.access.out_vec = rows_on_16(a.y, a.y_ld, a.nb, 2) && (!a.z_out || rows_on_16(a.z_out, a.z_ld, a.nb, 2));
-    P.access.in_vec = kMode == kLinearDx ? rows_on_16(a.z_in, a.z_ld, a.nb, 2)
-                                         : rows_on_16(a.residual, a.residual_ld, a.nb, 2);
+    P->access.out_vec = rows_on_16(a.y, a.y_ld, a.nb, 2) && (!a.z_out || rows_on_16(a.z_out, a.z_ld, a.nb, 2));
+    P->access.in_vec = kMode == kLinearDx ? rows_on_16(a.z_in, a.z_ld, a.nb, 2)
+                                          : rows_on_16(a.residual, a.residual_ld, a.nb, 2);
   }
-  if (tiles * P.split > 0x7fffffff) return cudaErrorInvalidValue;
-  CUtensorMap ma, mb;
-  cudaError_t e;
-  if ((e = make_operand_map(&ma, a.A, a.na, a.nk, kFp8, kRows ? kBN : BM)) != cudaSuccess) return e;
-  if ((e = make_operand_map(&mb, a.B, a.nb, a.nk, kFp8, kRows ? BM : kBN)) != cudaSuccess) return e;
-  if ((e = allow_smem<linear_split_kernel<kMode, kFp8, kBN, kRows>>(C::kSmemBytes)) != cudaSuccess) return e;
+  if (P->tiles > (int64_t(1) << 27)) return cudaErrorInvalidValue;
+  const cudaError_t e = make_operand_map(kRows ? n : m, a.A, a.na, a.nk, kFp8, kRows ? kBN : BM);
+  return e != cudaSuccess ? e : make_operand_map(kRows ? m : n, a.B, a.nb, a.nk, kFp8, kRows ? BM : kBN);
+}
+
+// A launch of `blocks` split CTAs in clusters of `cluster`.
+template <typename... Params, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(Params...), int64_t blocks, int cluster, uint32_t smem, cudaStream_t stream,
+                            const Args&... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * P.split));
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(kSplitThreads);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(P.split);
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, linear_split_kernel<kMode, kFp8, kBN, kRows>, kRows ? mb : ma, kRows ? ma : mb, P);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int kMode, bool kFp8, int kBN, bool kRows>
+cudaError_t launch_split(const LinearArgs& a, cudaStream_t stream) {
+  SplitParams P{};
+  CUtensorMap m, n;
+  cudaError_t e = plan_split<kMode, kFp8, kBN, kRows>(a, &P, &m, &n);
+  if (e != cudaSuccess) return e;
+  constexpr uint32_t kSmem = SplitConfig<kBN>::kSmemBytes;
+  if ((e = allow_smem<linear_split_kernel<kMode, kFp8, kBN, kRows>>(kSmem)) != cudaSuccess) return e;
+  return launch_clusters(linear_split_kernel<kMode, kFp8, kBN, kRows>, P.tiles * P.split, P.split, kSmem, stream, m, n,
+                         P);
+}
+
+template <int kBN, bool kRows>
+cudaError_t launch_grad(const LinearArgs& dx, const LinearArgs& dw, const ColumnSums* sums, cudaStream_t stream) {
+  GradParams P{};
+  CUtensorMap xm, xn, wm, wn;
+  cudaError_t e;
+  if ((e = plan_split<kLinearDx, false, kBN, kRows>(dx, &P.dx, &xm, &xn)) != cudaSuccess) return e;
+  if ((e = plan_split<kLinearDw, false, 64, true>(dw, &P.dw, &wm, &wn)) != cudaSuccess) return e;
+  const int cluster = P.dx.split > P.dw.split ? P.dx.split : P.dw.split;
+  const auto whole = [cluster](int64_t blocks) { return (blocks + cluster - 1) / cluster * cluster; };
+  P.dx_blocks = whole(P.dx.tiles * P.dx.split);
+  P.dw_blocks = whole(P.dw.tiles * P.dw.split);
+  int64_t blocks = P.dx_blocks + P.dw_blocks;
+  if (sums) {
+    P.sums = *sums;
+    blocks += whole((sums->n + kSumCols - 1) / kSumCols);
+  }
+  constexpr uint32_t kSmem = SplitConfig<kBN>::kSmemBytes > SplitConfig<64>::kSmemBytes ? SplitConfig<kBN>::kSmemBytes
+                                                                                     : SplitConfig<64>::kSmemBytes;
+  if ((e = allow_smem<linear_grad_kernel<kBN, kRows>>(kSmem)) != cudaSuccess) return e;
+  return launch_clusters(linear_grad_kernel<kBN, kRows>, blocks, cluster, kSmem, stream, xm, xn, wm, wn, P);
+}
+
+// The pair kernel once 256 x 128 tiles fill the pairs (64 of them: the split
+// kernel takes 9.4 us for 2048 x 1024 x 1024 against 11.7, 14.6 for 1024 x 2048
+// x 2048 against 16.4; 128: 45 us for 1024 x 4096 x 4096 against 28) and the
+// rows fill more than half of a tile (128 x 4096 x 4096: 13 us against 25).
+bool takes_pairs(const LinearArgs& a) {
+  const int64_t tiles_b = (a.nb + 255) / 256, tiles128 = tiles_b * ((a.na + 127) / 128);
+  return a.nb > 128 && tiles128 >= num_sms() / 2 && tiles128 < (int64_t(1) << 30);
 }
 
 template <int kMode, bool kFp8>
 cudaError_t launch_product(const LinearArgs& a, cudaStream_t stream) {
-  constexpr int kElems = kFp8 ? 128 : 64;
-  const int k_blocks = static_cast<int>((a.nk + kElems - 1) / kElems);
-  const int64_t tiles_b = (a.nb + 255) / 256, tiles256 = tiles_b * ((a.na + 255) / 256);
-  const int64_t tiles128 = tiles_b * ((a.na + 127) / 128), pairs = num_sms() / 2;
-  // The pair kernel once 256 x 128 tiles fill the pairs (64 of them: the split
-  // kernel takes 9.4 us for 2048 x 1024 x 1024 against 11.7, 14.6 for 1024 x 2048
-  // x 2048 against 16.4; 128: 45 us for 1024 x 4096 x 4096 against 28) and the
-  // rows fill more than half of a tile (128 x 4096 x 4096: 13 us against 25).
-  if (a.nb > 128 && tiles256 < (int64_t(1) << 30) && tiles128 >= pairs) {
+  if (takes_pairs(a)) {
+    const int64_t tiles_b = (a.nb + 255) / 256, pairs = num_sms() / 2;
+    const int64_t a256 = (a.na + 255) / 256, a128 = (a.na + 127) / 128;
     // a 128-wide tile takes about 0.6 of a 256-wide one's time: it pays where
     // the GPU would otherwise be filled badly
-    const int64_t waves256 = (tiles256 + pairs - 1) / pairs, waves128 = (tiles128 + pairs - 1) / pairs;
+    const int64_t waves256 = (tiles_b * a256 + pairs - 1) / pairs, waves128 = (tiles_b * a128 + pairs - 1) / pairs;
     if (5 * waves256 <= 3 * waves128)
-      return launch_pair<kMode, kFp8, 256>(a, k_blocks, static_cast<int>((a.na + 255) / 256),
-                                           static_cast<int>(tiles_b), stream);
-    return launch_pair<kMode, kFp8, 128>(a, k_blocks, static_cast<int>((a.na + 127) / 128), static_cast<int>(tiles_b),
-                                         stream);
+      return launch_pair<kMode, kFp8, 256>(a, k_blocks_of(a), static_cast<int>(a256), static_cast<int>(tiles_b), stream);
+    return launch_pair<kMode, kFp8, 128>(a, k_blocks_of(a), static_cast<int>(a128), static_cast<int>(tiles_b), stream);
   }
   if constexpr (kMode != kLinearDw) {
-    if (a.nb <= 16) return launch_split<kMode, kFp8, 16, false>(a, k_blocks, stream);
-    if (a.nb <= 32) return launch_split<kMode, kFp8, 32, false>(a, k_blocks, stream);
+    if (a.nb <= 16) return launch_split<kMode, kFp8, 16, false>(a, stream);
+    if (a.nb <= 32) return launch_split<kMode, kFp8, 32, false>(a, stream);
   }
-  return launch_split<kMode, kFp8, 64, true>(a, k_blocks, stream);
+  return launch_split<kMode, kFp8, 64, true>(a, stream);
 }
 
 }  // namespace
@@ -1637,17 +1733,33 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
   return a.fp8 ? launch_product<kLinearForward, true>(a, stream) : launch_product<kLinearForward, false>(a, stream);
 }
 
-cudaError_t launch_column_sums(const uint16_t* dz, int64_t ld, int64_t m, int64_t n, float* out, float* partial,
-                               int accumulate, cudaStream_t stream) {
-  const unsigned gx = static_cast<unsigned>((n + kSumCols - 1) / kSumCols);
-  const int64_t gy = column_sum_slices(m, n);
-  const bool vec = n % 2 == 0 && (reinterpret_cast<uintptr_t>(dz) & 3u) == 0 && (m <= 1 || ld % 2 == 0);
-  const dim3 grid(gx, static_cast<unsigned>(gy));
-  if (vec) column_sums_kernel<true><<<grid, 256, 0, stream>>>(dz, ld, m, n, out, partial, accumulate);
-  else column_sums_kernel<false><<<grid, 256, 0, stream>>>(dz, ld, m, n, out, partial, accumulate);
-  if (gy > 1)
-    join_sums_kernel<<<static_cast<unsigned>((n + 127) / 128), 128, 0, stream>>>(partial, static_cast<int>(gy), n, out,
-                                                                                 accumulate);
+namespace {
+
+ColumnSums plan_sums(const ColumnSumArgs& a) {
+  const bool vec = a.n % 2 == 0 && (reinterpret_cast<uintptr_t>(a.dz) & 3u) == 0 && (a.m <= 1 || a.ld % 2 == 0);
+  return ColumnSums{a.dz, a.ld, a.m, a.n, a.out, a.partial, a.accumulate, vec};
+}
+
+}  // namespace
+
+bool linear_grad_fits(const LinearArgs& dx, const LinearArgs& dw) { return !takes_pairs(dx) && !takes_pairs(dw); }
+
+cudaError_t launch_linear_grad(const LinearArgs& dx, const LinearArgs& dw, const ColumnSumArgs* sums,
+                               cudaStream_t stream) {
+  ColumnSums s{};
+  if (sums) s = plan_sums(*sums);
+  if (dx.nb <= 16) return launch_grad<16, false>(dx, dw, sums ? &s : nullptr, stream);
+  if (dx.nb <= 32) return launch_grad<32, false>(dx, dw, sums ? &s : nullptr, stream);
+  return launch_grad<64, true>(dx, dw, sums ? &s : nullptr, stream);
+}
+
+cudaError_t launch_column_sums(const ColumnSumArgs& a, cudaStream_t stream) {
+  const unsigned gx = static_cast<unsigned>((a.n + kSumCols - 1) / kSumCols);
+  const int64_t slices = column_sum_slices(a.m, a.n);
+  column_sums_kernel<<<dim3(gx, static_cast<unsigned>(slices)), kSplitThreads, 0, stream>>>(plan_sums(a));
+  if (slices > 1)
+    join_sums_kernel<<<static_cast<unsigned>((a.n + 127) / 128), 128, 0, stream>>>(
+        a.partial, static_cast<int>(slices), a.n, a.out, a.accumulate);
   return cudaGetLastError();
 }
 

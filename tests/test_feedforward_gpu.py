@@ -500,4 +500,4 @@ def test_launches_are_named():
         mp.rmsnorm(x, normal(3, (63,)), y=dx)
     torch.cuda.synchronize()
     names = {r["kernel"] for r in prof.records()}
-    assert {"linear", "linear_repack", "linear_dx", "linear_dw", "quantize_rows", "rmsnorm"} <= names
+    assert {"linear", "linear_repack", "linear_grad", "quantize_rows", "rmsnorm"} <= names
