@@ -112,6 +112,16 @@ __device__ __forceinline__ void store_group(T* row, int i, int t, int64_t cols, 
   }
 }
 
+// A group times inv in e4m3, 8 bytes.
+template <int kTPR>
+__device__ __forceinline__ void store_e4m3(uint8_t* row, int i, int t, int64_t cols, const float (&v)[8], float inv) {
+  const int64_t c = column<kTPR, true>(i, 0, t);
+  if (c < cols)
+    *reinterpret_cast<uint2*>(row + c) =
+        make_uint2(e4m3x2(v[0] * inv, v[1] * inv) | (e4m3x2(v[2] * inv, v[3] * inv) << 16),
+                   e4m3x2(v[4] * inv, v[5] * inv) | (e4m3x2(v[6] * inv, v[7] * inv) << 16));
+}
+
 template <int kTPR, bool kVec>
 __device__ __forceinline__ void load_gamma(const void* gamma, int dtype, int i, int t, int64_t cols, float (&v)[8]) {
   if (dtype == kBf16) load_group<kTPR, kVec>(static_cast<const __nv_bfloat16*>(gamma), i, t, cols, v);
@@ -135,6 +145,27 @@ __device__ __forceinline__ float row_reduce(float v, float* vals) {
     for (int w = 1; w < kTPR / 32; ++w) v = kMax ? fmaxf(v, vals[w]) : v + vals[w];
   }
   return v;
+}
+
+// The sums of kU rows at once, one barrier for all of them.
+template <int kTPR, int kU>
+__device__ __forceinline__ void rows_reduce(float (&v)[kU], float (*vals)[kTPR / 32]) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+    for (int u = 0; u < kU; ++u) v[u] += __shfl_xor_sync(0xffffffffu, v[u], off);
+  if constexpr (kTPR > 32) {
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+      for (int u = 0; u < kU; ++u) vals[u][threadIdx.x >> 5] = v[u];
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      v[u] = vals[u][0];
+#pragma unroll
+      for (int w = 1; w < kTPR / 32; ++w) v[u] += vals[u][w];
+    }
+  }
 }
 
 // -------------------------------------------------------------- forward --
@@ -209,11 +240,7 @@ rmsnorm_kernel(const __grid_constant__ RmsnormArgs a) {
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
       if constexpr (kVec) {
-        const int64_t c = column<kTPR, true>(i, 0, t);
-        if (c < cols)
-          *reinterpret_cast<uint2*>(q + c) =
-              make_uint2(e4m3x2(v[i][0] * inv, v[i][1] * inv) | (e4m3x2(v[i][2] * inv, v[i][3] * inv) << 16),
-                         e4m3x2(v[i][4] * inv, v[i][5] * inv) | (e4m3x2(v[i][6] * inv, v[i][7] * inv) << 16));
+        store_e4m3<kTPR>(q, i, t, cols, v[i], inv);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -221,6 +248,72 @@ rmsnorm_kernel(const __grid_constant__ RmsnormArgs a) {
           if (c < cols) q[c] = e4m3(v[i][j] * inv);
         }
       }
+    }
+  }
+}
+
+// bf16 rows without a residual stay packed in registers and are unpacked at
+// each use: half the registers a column, so twice the bytes in flight (the
+// loads are all there is to wait for; unpacked, 14336 x 4096 in e4m3 took 33
+// us, 5.4 TB/s).
+template <int kTPR, int kNV>
+__global__ void __launch_bounds__(kTPR) rmsnorm_packed_kernel(const __grid_constant__ RmsnormArgs a) {
+  __shared__ float vals[2][kTPR / 32];
+  const int t = threadIdx.x;
+  const int64_t r = blockIdx.x, cols = a.cols;
+  uint4 raw[kNV];
+  {
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + r * a.x_ld;
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+      const int64_t c = column<kTPR, true>(i, 0, t);
+      raw[i] = c < cols ? *reinterpret_cast<const uint4*>(x + c) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  float rstd = 1.f;
+  if (a.norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+      float v[8];
+      unpack8(raw[i], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss += v[j] * v[j];
+    }
+    ss = row_reduce<kTPR, false>(ss, vals[0]);
+    rstd = 1.f / sqrtf(ss / static_cast<float>(cols) + a.eps);
+    if (a.rstd && t == 0) a.rstd[r] = rstd;
+  }
+  auto values = [&](int i, float (&v)[8]) {
+    unpack8(raw[i], v);
+    if (a.norm) {
+      float g[8];
+      load_gamma<kTPR, true>(a.gamma, a.gamma_dtype, i, t, cols, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = v[j] * rstd * g[j];
+    }
+  };
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < kNV; ++i) {
+    const int64_t c = column<kTPR, true>(i, 0, t);
+    if (a.h && c < cols) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.h) + r * a.h_ld + c) = raw[i];
+    float v[8];
+    values(i, v);
+    if (a.y) store_group<kTPR, true>(reinterpret_cast<__nv_bfloat16*>(a.y) + r * a.y_ld, i, t, cols, v);
+    // columns past the end hold zeros times rstd, which may be NaN: fmaxf drops it
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+  }
+  if (a.q) {
+    const float scale = fmaxf(row_reduce<kTPR, true>(amax, vals[1]), kAmaxFloor) / kE4m3Max;
+    if (t == 0) a.q_scale[r] = scale;
+    const float inv = 1.f / scale;
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+      float v[8];
+      values(i, v);
+      store_e4m3<kTPR>(a.q + r * a.q_ld, i, t, cols, v, inv);
     }
   }
 }
@@ -268,15 +361,10 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_long_kernel(const __grid
 
 // ------------------------------------------------------------- gradient --
 
-// A group of 8 elements as loaded: bf16 stays packed until it is used, so that
-// a thread holds a row of h, dy and dh in few registers and more CTAs fit.
+// A group of 8 elements as loaded (bf16 stays packed until it is used).
 template <typename T, bool kVec>
 struct Raw {
   float v[8];
-  template <int kTPR>
-  __device__ __forceinline__ void load(const T* row, int i, int t, int64_t cols) {
-    load_group<kTPR, kVec>(row, i, t, cols, v);
-  }
   __device__ __forceinline__ void get(float (&out)[8]) const {
 #pragma unroll
     for (int j = 0; j < 8; ++j) out[j] = v[j];
@@ -285,96 +373,191 @@ struct Raw {
 template <>
 struct Raw<__nv_bfloat16, true> {
   uint4 w;
-  template <int kTPR>
-  __device__ __forceinline__ void load(const __nv_bfloat16* row, int i, int t, int64_t cols) {
-    const int64_t c = column<kTPR, true>(i, 0, t);
-    w = c < cols ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
-  }
   __device__ __forceinline__ void get(float (&out)[8]) const { unpack8(w, out); }
 };
 
-// CTA b takes rows b, b + gridDim.x, ... (kRows at a time when a row belongs to
-// a warp); a thread's columns stay the same, so its part of dgamma stays in
-// registers, and the CTA writes its partial sums once.  gamma is read again for
-// every row (from L1): keeping it would cost the registers of one more CTA.
-// CTAs that shall fit on an SM: registers for 64 (bf16) or 80 (fp32) a thread
-// at 16 columns each, half as many CTAs at 32.
-template <typename T, int kTPR, int kNV, bool kVec>
-constexpr int grad_ctas() {
-  if (!kVec || kNV > 2) return kTPR == 32 && kNV > 2 ? 2 : 1;
-  const int threads = kTPR == 32 ? 256 : kTPR;
-  const int n = (sizeof(T) == 2 ? 1024 : 768) / threads;
-  return n < 1 ? 1 : n;
+template <int kTPR, bool kVec, typename T>
+__device__ __forceinline__ void load_raw(const T* row, int i, int t, int64_t cols, Raw<T, kVec>& r) {
+  if constexpr (kVec && sizeof(T) == 2) {
+    const int64_t c = column<kTPR, true>(i, 0, t);
+    r.w = c < cols ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
+  } else {
+    load_group<kTPR, kVec>(row, i, t, cols, r.v);
+  }
 }
 
+// The gradient walks over many rows per CTA with a barrier in each, so it lives
+// from rows that are independent of one another.  bf16 at 16 columns a thread:
+// kU = 2 rows at a time share a barrier, and the loads run ahead of them in a
+// ring (every thread copies the 16-byte pieces of the coming rows that it will
+// itself use into its own places in shared memory, with cp.async: no registers,
+// no barrier).  The other forms load a row into registers, with as many CTAs to
+// an SM as that leaves; fp32, twice the bytes for the same work, reaches 6.1
+// TB/s so, and a ring of the two rows that fit took it down to 4.5.
 template <typename T, int kTPR, int kNV, bool kVec>
-__global__ void __launch_bounds__(kTPR == 32 ? 256 : kTPR, (grad_ctas<T, kTPR, kNV, kVec>()))
+struct GradConfig {
+  static constexpr int kThreads = kTPR == 32 ? 256 : kTPR;
+  static constexpr bool kRing = kVec && sizeof(T) == 2 && kNV == 2;
+  static constexpr int kU = kRing ? 2 : 1;
+  static constexpr int kPieces = 3 * kNV;                                  // of a row: h, dh, dy
+  static constexpr int kStageBytes = kU * kPieces * kThreads * 16;
+  // CTAs to an SM: without the ring registers for 64 (bf16) or 80 (fp32) a
+  // thread at 16 columns each, half as many CTAs at 32
+  static constexpr int plain_ctas() {
+    if (!kVec || kNV > 2) return kTPR == 32 && kNV > 2 ? 2 : 1;
+    const int n = (sizeof(T) == 2 ? 1024 : 768) / kThreads;
+    return n < 1 ? 1 : n;
+  }
+  static constexpr int kCtas = kRing ? 512 / kThreads : plain_ctas();
+  static constexpr int kStages = kRing ? (216 * 1024) / kCtas / kStageBytes : 0;
+  static_assert(!kRing || kStages >= 2, "the ring holds the rows in use and the ones on their way");
+  static constexpr int kBytes = kStages * kStageBytes;
+};
+
+__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+// CTA b takes rows b, b + gridDim.x, ... (a row to a warp where kTPR is 32); a
+// thread's columns stay the same, so its part of dgamma stays in registers, and
+// the CTA writes its partial sums once.
+template <typename T, int kTPR, int kNV, bool kVec>
+__global__ void __launch_bounds__(kTPR == 32 ? 256 : kTPR, (GradConfig<T, kTPR, kNV, kVec>::kCtas))
 rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
-  constexpr int kThreads = kTPR == 32 ? 256 : kTPR;
+  using C = GradConfig<T, kTPR, kNV, kVec>;
+  constexpr int kThreads = C::kThreads, kU = C::kU;
   constexpr int kRows = kThreads / kTPR;
-  __shared__ float vals[2][kTPR / 32];
+  extern __shared__ uint4 ring[];              // [kStages][kU][kPieces][kThreads]
+  __shared__ float vals[2][kU][kTPR / 32];
   __shared__ float join[kRows > 1 ? kRows * kTPR * 8 : 1];
   const int t = threadIdx.x % kTPR, sub = threadIdx.x / kTPR;
   const int64_t cols = a.cols;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
   const float inv_cols = 1.f / static_cast<float>(cols);
   float part[kNV][8];
 #pragma unroll
   for (int i = 0; i < kNV; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) part[i][j] = 0.f;
-  int parity = 0;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + sub; r < a.rows;
-       r += static_cast<int64_t>(gridDim.x) * kRows, parity ^= 1) {
-    const float rstd = a.rstd[r];
-    Raw<T, kVec> h[kNV], dh[kNV];
-    Raw<__nv_bfloat16, kVec> dy[kNV];
-    {
+
+  // this thread's pieces of rows r, r + step into stage s; a commit in any
+  // case, so that the count of groups is that of stages
+  auto fetch = [&](int64_t r, int s) {
+    uint4* p = ring + static_cast<size_t>(s) * (kU * C::kPieces * kThreads) + threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < kU; ++u, r += step)
+      if (r < a.rows) {
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) {
+          const int64_t c = column<kTPR, true>(i, 0, t);
+          if (c < cols) {
+            uint4* q = p + (u * C::kPieces + i) * kThreads;
+            copy16(q, static_cast<const T*>(a.h) + r * a.h_ld + c);
+            if (a.dh) copy16(q + kNV * kThreads, static_cast<const T*>(a.dh) + r * a.dh_ld + c);
+            copy16(q + 2 * kNV * kThreads, a.dy + r * a.dy_ld + c);
+          }
+        }
+      }
+    copy_commit();
+  };
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows + sub;
+  if constexpr (C::kRing) {
+    for (int s = 0; s < C::kStages - 1; ++s) fetch(r0 + s * kU * step, s);
+  }
+  int parity = 0, stage = 0;
+  for (int64_t r = r0; r < a.rows; r += kU * step, parity ^= 1) {
+    Raw<T, kVec> h[kU][kNV], dh[kU][kNV];
+    Raw<__nv_bfloat16, kVec> dy[kU][kNV];
+    float rstd[kU], dot[kU];
+    if constexpr (C::kRing) {
+      copy_wait<C::kStages - 2>();
+      const uint4* p = ring + static_cast<size_t>(stage) * (kU * C::kPieces * kThreads) + threadIdx.x;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const bool row = r + u * step < a.rows;
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) {
+          const bool in = row && column<kTPR, true>(i, 0, t) < cols;       // nothing was copied for the others
+          const uint4* q = p + (u * C::kPieces + i) * kThreads;
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          h[u][i].w = in ? q[0] : zero;
+          dh[u][i].w = in && a.dh ? q[kNV * kThreads] : zero;
+          dy[u][i].w = in ? q[2 * kNV * kThreads] : zero;
+        }
+      }
+    } else {
       const T* hp = static_cast<const T*>(a.h) + r * a.h_ld;
       const __nv_bfloat16* yp = reinterpret_cast<const __nv_bfloat16*>(a.dy) + r * a.dy_ld;
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
-        h[i].template load<kTPR>(hp, i, t, cols);
-        dy[i].template load<kTPR>(yp, i, t, cols);
+        load_raw<kTPR, kVec>(hp, i, t, cols, h[0][i]);
+        load_raw<kTPR, kVec>(yp, i, t, cols, dy[0][i]);
       }
       if (a.dh) {
         const T* sp = static_cast<const T*>(a.dh) + r * a.dh_ld;
 #pragma unroll
-        for (int i = 0; i < kNV; ++i) dh[i].template load<kTPR>(sp, i, t, cols);
+        for (int i = 0; i < kNV; ++i) load_raw<kTPR, kVec>(sp, i, t, cols, dh[0][i]);
       }
     }
-    float dot = 0.f;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      rstd[u] = r + u * step < a.rows ? a.rstd[r + u * step] : 0.f;
+      dot[u] = 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-      float n[8], g[8], gamma[8];
+      float gamma[8];
       load_gamma<kTPR, kVec>(a.gamma, a.gamma_dtype, i, t, cols, gamma);
-      h[i].get(n);
-      dy[i].get(g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        n[j] *= rstd;
-        const float p = g[j] * n[j];
-        part[i][j] += p;
-        dot += p * gamma[j];
+      for (int u = 0; u < kU; ++u) {
+        float n[8], g[8];
+        h[u][i].get(n);
+        dy[u][i].get(g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          n[j] *= rstd[u];
+          const float p = g[j] * n[j];
+          part[i][j] += p;
+          dot[u] += p * gamma[j];
+        }
       }
     }
+    if constexpr (C::kRing) {
+      // the stage read one turn ago (its values are in use by now) takes the rows kStages - 1 turns ahead
+      const int next = stage == 0 ? C::kStages - 1 : stage - 1;
+      fetch(r + (C::kStages - 1) * kU * step, next);
+      if (++stage == C::kStages) stage = 0;
+    }
     if (a.dx) {
-      const float mean = row_reduce<kTPR, false>(dot, vals[parity]) * inv_cols;
-      T* dx = static_cast<T*>(a.dx) + r * a.dx_ld;
+      rows_reduce<kTPR, kU>(dot, vals[parity]);
 #pragma unroll
-      for (int i = 0; i < kNV; ++i) {
-        float n[8], g[8], gamma[8], d[8];
-        load_gamma<kTPR, kVec>(a.gamma, a.gamma_dtype, i, t, cols, gamma);
-        h[i].get(n);
-        dy[i].get(g);
-        if (a.dh) {
-          dh[i].get(d);
-        } else {
+      for (int u = 0; u < kU; ++u) {
+        if (r + u * step >= a.rows) break;
+        const float mean = dot[u] * inv_cols;
+        T* dx = static_cast<T*>(a.dx) + (r + u * step) * a.dx_ld;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) d[j] = 0.f;
+        for (int i = 0; i < kNV; ++i) {
+          float n[8], g[8], gamma[8], d[8];
+          load_gamma<kTPR, kVec>(a.gamma, a.gamma_dtype, i, t, cols, gamma);
+          h[u][i].get(n);
+          dy[u][i].get(g);
+          if (a.dh) {
+            dh[u][i].get(d);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d[j] = 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j] += rstd[u] * (g[j] * gamma[j] - n[j] * rstd[u] * mean);
+          store_group<kTPR, kVec>(dx, i, t, cols, d);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] += rstd * (g[j] * gamma[j] - n[j] * rstd * mean);
-        store_group<kTPR, kVec>(dx, i, t, cols, d);
       }
     }
   }
@@ -443,21 +626,23 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_grad_long_kernel(const _
 }
 
 // dgamma (+)= the partial sums, in a fixed order: a CTA takes 32 columns, its
-// 8 warps every eighth partial row, and the warps' sums are added in order.
-__global__ void __launch_bounds__(256)
+// 32 warps every 32nd partial row (all of a warp's loads in flight together),
+// and the warps' sums are added in order.
+__global__ void __launch_bounds__(1024)
 dgamma_kernel(const float* partial, int n_partial, int64_t cols, float* dgamma, int accumulate) {
-  __shared__ float sums[8][32];
+  __shared__ float sums[32][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float s = 0.f;
   if (c < cols) {
-#pragma unroll 8
-    for (int p = warp; p < n_partial; p += 8) s += partial[static_cast<int64_t>(p) * cols + c];
+#pragma unroll 20
+    for (int p = warp; p < n_partial; p += 32) s += partial[static_cast<int64_t>(p) * cols + c];
   }
   sums[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < cols) {
-    for (int w = 1; w < 8; ++w) s += sums[w][lane];
+#pragma unroll
+    for (int w = 1; w < 32; ++w) s += sums[w][lane];
     dgamma[c] = accumulate ? dgamma[c] + s : s;
   }
 }
@@ -497,6 +682,16 @@ cudaError_t forward_typed(const RmsnormArgs& a, cudaStream_t stream) {
                    aligned(a.residual, a.residual_ld, a.residual ? a.rows : 1, es, 16) &&
                    aligned(a.h, a.h_ld, a.h ? a.rows : 1, es, 16) && aligned(a.y, a.y_ld, a.y ? a.rows : 1, 2, 16) &&
                    aligned(a.q, a.q_ld, a.q ? a.rows : 1, 1, 8) && aligned(a.gamma, 0, 1, 1, 16);
+  if constexpr (sizeof(T) == 2) {
+    // from 2049 columns on; a row of fewer is too short for CTAs of this kind
+    if (vec && !a.residual && a.cols > 2048 && a.cols <= kRegisterCols) {
+      const unsigned grid = static_cast<unsigned>(a.rows);
+      if (a.cols <= 4096) rmsnorm_packed_kernel<128, 4><<<grid, 128, 0, stream>>>(a);
+      else if (a.cols <= 8192) rmsnorm_packed_kernel<256, 4><<<grid, 256, 0, stream>>>(a);
+      else rmsnorm_packed_kernel<512, 4><<<grid, 512, 0, stream>>>(a);
+      return cudaGetLastError();
+    }
+  }
   if (a.cols <= 256) return forward_config<T, 32, 1>(a, vec, stream);
   if (a.cols <= 512) return forward_config<T, 32, 2>(a, vec, stream);
   if (a.cols <= 1024) return forward_config<T, 32, 4>(a, vec, stream);
@@ -512,13 +707,13 @@ cudaError_t forward_typed(const RmsnormArgs& a, cudaStream_t stream) {
 
 // CTAs of a kernel that the GPU holds at a time (kept per thread and device).
 template <auto kKernel>
-int resident_ctas(int threads) {
+int resident_ctas(int threads, int smem) {
   static thread_local int cached_dev = -1, cached = 1;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;
   if (dev != cached_dev) {
     int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kKernel, threads, 0) != cudaSuccess || per_sm < 1)
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kKernel, threads, smem) != cudaSuccess || per_sm < 1)
       per_sm = 1;
     cached = per_sm * num_sms();
     cached_dev = dev;
@@ -530,12 +725,15 @@ template <typename T, int kTPR, int kNV, bool kVec>
 cudaError_t grad_launch(const RmsnormGradArgs& a, int* grid, cudaStream_t stream) {
   constexpr int kThreads = kTPR == 32 ? 256 : kTPR;
   constexpr int kRows = kThreads / kTPR;
+  constexpr int kSmem = GradConfig<T, kTPR, kNV, kVec>::kBytes;
   int64_t n = (a.rows + kRows - 1) / kRows;
-  const int64_t most = resident_ctas<rmsnorm_grad_kernel<T, kTPR, kNV, kVec>>(kThreads);
+  const cudaError_t e = allow_smem<rmsnorm_grad_kernel<T, kTPR, kNV, kVec>>(kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t most = resident_ctas<rmsnorm_grad_kernel<T, kTPR, kNV, kVec>>(kThreads, kSmem);
   if (n > most) n = most;
   if (n > kNormPartialRows) n = kNormPartialRows;
   *grid = static_cast<int>(n);
-  rmsnorm_grad_kernel<T, kTPR, kNV, kVec><<<*grid, kThreads, 0, stream>>>(a);
+  rmsnorm_grad_kernel<T, kTPR, kNV, kVec><<<*grid, kThreads, kSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -583,8 +781,8 @@ cudaError_t launch_rmsnorm_grad(const RmsnormGradArgs& a, cudaStream_t stream) {
   }
   if (!a.dgamma) return cudaSuccess;
   prof_begin(OPT_KERNEL_RMSNORM_DGAMMA, 1, a.rows, a.cols, stream);
-  dgamma_kernel<<<static_cast<unsigned>((a.cols + 31) / 32), 256, 0, stream>>>(a.partial, grid, a.cols, a.dgamma,
-                                                                               a.accumulate);
+  dgamma_kernel<<<static_cast<unsigned>((a.cols + 31) / 32), 1024, 0, stream>>>(a.partial, grid, a.cols, a.dgamma,
+                                                                                a.accumulate);
   prof_end(stream);
   return cudaGetLastError();
 }
