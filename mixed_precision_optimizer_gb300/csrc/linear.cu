@@ -1276,6 +1276,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
     uint8_t* stage = scratch + (warp - 2) * C::kWarpScratch;
     uint32_t* table = reinterpret_cast<uint32_t*>(stage + C::kTableAt);
     const uint32_t in_bar = smem_u32(&in_full[warp - 2]);
+    uint32_t blocks = 0;                 // dw: blocks staged so far
     uint32_t in_phase = 0;
     uint32_t use = 0;
     bool ok = true;
@@ -1331,11 +1332,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
           for (int c = 0; c < C::kHalf; c += 32) {
             if (col0 + c >= P.g.na) break;
             if (P.out_tma) {
-              uint8_t* const buf = stage + (c & 32 ? 4096 : 0);
-              if (lane == 0) {                         // this buffer's previous store has read it
-                if (c > 0) bulk_wait_read_1();
-                else bulk_wait_read_0();               // the last tile may have left either half busy
-              }
+              uint8_t* const buf = stage + (blocks++ & 1) * kBlockBytes;
+              if (lane == 0) bulk_wait_read_1();     // the store that last used this block has read it
               __syncwarp();
 #pragma unroll
               for (int q = 0; q < 8; ++q)            // 128-byte swizzle
@@ -1700,9 +1698,12 @@ cudaError_t launch_grad(const LinearArgs& dx, const LinearArgs& dw, const Column
 // kernel takes 9.4 us for 2048 x 1024 x 1024 against 11.7, 14.6 for 1024 x 2048
 // x 2048 against 16.4; 128: 45 us for 1024 x 4096 x 4096 against 28) and the
 // rows fill more than half of a tile (128 x 4096 x 4096: 13 us against 25).
+// dw of a few tokens is little more than its stores: there twice the tiles (1 x
+// 2048 x 2048, 128 tiles: 10.9 us split against 12.0, and dx shares the launch).
 bool takes_pairs(const LinearArgs& a) {
   const int64_t tiles_b = (a.nb + 255) / 256, tiles128 = tiles_b * ((a.na + 127) / 128);
-  return a.nb > 128 && tiles128 >= num_sms() / 2 && tiles128 < (int64_t(1) << 30);
+  const int64_t enough = num_sms() / 2 * (a.mode == kLinearDw && k_blocks_of(a) <= 2 ? 2 : 1);
+  return a.nb > 128 && tiles128 >= enough && tiles128 < (int64_t(1) << 30);
 }
 
 template <int kMode, bool kFp8>
@@ -1710,10 +1711,13 @@ cudaError_t launch_product(const LinearArgs& a, cudaStream_t stream) {
   if (takes_pairs(a)) {
     const int64_t tiles_b = (a.nb + 255) / 256, pairs = num_sms() / 2;
     const int64_t a256 = (a.na + 255) / 256, a128 = (a.na + 127) / 128;
-    // a 128-wide tile takes about 0.6 of a 256-wide one's time: it pays where
-    // the GPU would otherwise be filled badly
+    // Measured cycles of a tile: 560 a k-block and 7000 besides when it is 256
+    // wide, 500 and 4500 when 128 (both wait for their operands from L2: 58 and
+    // 49 bytes a cycle per SM), so the narrow one pays where it fills the last
+    // wave better or the sum is short.
     const int64_t waves256 = (tiles_b * a256 + pairs - 1) / pairs, waves128 = (tiles_b * a128 + pairs - 1) / pairs;
-    if (5 * waves256 <= 3 * waves128)
+    const int64_t kb = k_blocks_of(a);
+    if (waves256 * (560 * kb + 7000) <= waves128 * (500 * kb + 4500))
       return launch_pair<kMode, kFp8, 256>(a, k_blocks_of(a), static_cast<int>(a256), static_cast<int>(tiles_b), stream);
     return launch_pair<kMode, kFp8, 128>(a, k_blocks_of(a), static_cast<int>(a128), static_cast<int>(tiles_b), stream);
   }
