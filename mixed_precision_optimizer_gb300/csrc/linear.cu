@@ -17,6 +17,7 @@
 
 #include "../../include/mpopt.h"
 #include "internal.h"
+#include "overlap.cuh"
 #include "tc_common.cuh"
 
 namespace mpopt {
@@ -537,6 +538,7 @@ __device__ __forceinline__ void split_tile(const CUtensorMap& map_a, const CUten
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    wait_for_predecessors();
     // the first loads fly while the CTA sets up: the ring is empty
     for (int s = 0; s < C::kStages && kb0 + s < kb1; ++s) load_stage(kb0 + s, s);
   }
@@ -546,6 +548,7 @@ __device__ __forceinline__ void split_tile(const CUtensorMap& map_a, const CUten
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  wait_for_predecessors();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -793,6 +796,7 @@ template <int kMode, bool kFp8, int kBN, bool kRows>
 __global__ void __launch_bounds__(kSplitThreads, 2)
 linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                     const __grid_constant__ SplitParams P) {
+  let_next_start();
   split_tile<kMode, kFp8, kBN, kRows>(map_a, map_b, P, blockIdx.x);
 }
 
@@ -851,12 +855,16 @@ __device__ __forceinline__ void column_sums(const ColumnSums& p, int64_t x, int6
 }
 
 __global__ void __launch_bounds__(kSplitThreads) column_sums_kernel(const __grid_constant__ ColumnSums p) {
+  let_next_start();
+  wait_for_predecessors();
   column_sums(p, blockIdx.x, blockIdx.y, gridDim.y);
 }
 
 __global__ void __launch_bounds__(128)
 join_sums_kernel(const float* partial, int slices, int64_t n, float* out, int accumulate) {
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
+  let_next_start();
+  wait_for_predecessors();
   if (c >= n) return;
   float s = 0.f;
 #pragma unroll 8
@@ -880,12 +888,14 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap dx_a, const __grid_consta
                    const __grid_constant__ CUtensorMap dw_a, const __grid_constant__ CUtensorMap dw_b,
                    const __grid_constant__ GradParams P) {
   const int64_t block = blockIdx.x;
+  let_next_start();
   if (block < P.dx_blocks) {
     split_tile<kLinearDx, false, kBN, kRows>(dx_a, dx_b, P.dx, block);
   } else if (block < P.dx_blocks + P.dw_blocks) {
     split_tile<kLinearDw, false, 64, true>(dw_a, dw_b, P.dw, block - P.dx_blocks);
   } else {
     const int64_t x = block - P.dx_blocks - P.dw_blocks;
+    wait_for_predecessors();
     if (x * kSumCols < P.sums.n) column_sums(P.sums, x, 0, 1);
   }
 }
@@ -1121,6 +1131,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   uint32_t* status = P.g.header;
+  let_next_start();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -1150,6 +1161,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  wait_for_predecessors();
   tc_fence_before();
   cluster_sync();            // barriers of both CTAs initialised, TMEM allocated in both
   tc_fence_after();
@@ -1509,6 +1521,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
 template <typename T>
 __global__ void __launch_bounds__(256) repack_kernel(const __grid_constant__ RepackBatch batch) {
   constexpr int kN = 16 / sizeof(T);
+  let_next_start();
+  wait_for_predecessors();
   int64_t piece = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   int i = 0;
   while (i < batch.n && piece >= batch.m[i].pieces) piece -= batch.m[i++].pieces;
@@ -1605,8 +1619,8 @@ cudaError_t launch_pair(const LinearArgs& a, int k_blocks, int tiles_a, int tile
   if ((e = allow_smem<linear_pair_kernel<kMode, kFp8, kBN>>(C::kSmemBytes)) != cudaSuccess) return e;
   const int max_pairs = num_sms() / 2;
   const int grid = 2 * (P.total_tiles < max_pairs ? P.total_tiles : max_pairs);
-  linear_pair_kernel<kMode, kFp8, kBN><<<grid, kPairThreads, C::kSmemBytes, stream>>>(mb, ma, mo, mz, P);
-  return cudaGetLastError();
+  return launch_overlapped(linear_pair_kernel<kMode, kFp8, kBN>, static_cast<unsigned>(grid), kPairThreads, C::kSmemBytes,
+                           stream, 0, mb, ma, mo, mz, P);
 }
 
 int k_blocks_of(const LinearArgs& a) {
@@ -1641,25 +1655,6 @@ cudaError_t plan_split(const LinearArgs& a, SplitParams* P, CUtensorMap* m, CUte
   return e != cudaSuccess ? e : make_operand_map(kRows ? m : n, a.B, a.nb, a.nk, kFp8, kRows ? BM : kBN);
 }
 
-// A launch of `blocks` split CTAs in clusters of `cluster`.
-template <typename... Params, typename... Args>
-cudaError_t launch_clusters(void (*kernel)(Params...), int64_t blocks, int cluster, uint32_t smem, cudaStream_t stream,
-                            const Args&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(kSplitThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int kMode, bool kFp8, int kBN, bool kRows>
 cudaError_t launch_split(const LinearArgs& a, cudaStream_t stream) {
   SplitParams P{};
@@ -1668,8 +1663,8 @@ cudaError_t launch_split(const LinearArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   constexpr uint32_t kSmem = SplitConfig<kBN>::kSmemBytes;
   if ((e = allow_smem<linear_split_kernel<kMode, kFp8, kBN, kRows>>(kSmem)) != cudaSuccess) return e;
-  return launch_clusters(linear_split_kernel<kMode, kFp8, kBN, kRows>, P.tiles * P.split, P.split, kSmem, stream, m, n,
-                         P);
+  return launch_overlapped(linear_split_kernel<kMode, kFp8, kBN, kRows>, static_cast<unsigned>(P.tiles * P.split),
+                           kSplitThreads, kSmem, stream, P.split, m, n, P);
 }
 
 template <int kBN, bool kRows>
@@ -1691,7 +1686,8 @@ cudaError_t launch_grad(const LinearArgs& dx, const LinearArgs& dw, const Column
   constexpr uint32_t kSmem = SplitConfig<kBN>::kSmemBytes > SplitConfig<64>::kSmemBytes ? SplitConfig<kBN>::kSmemBytes
                                                                                      : SplitConfig<64>::kSmemBytes;
   if ((e = allow_smem<linear_grad_kernel<kBN, kRows>>(kSmem)) != cudaSuccess) return e;
-  return launch_clusters(linear_grad_kernel<kBN, kRows>, blocks, cluster, kSmem, stream, xm, xn, wm, wn, P);
+  return launch_overlapped(linear_grad_kernel<kBN, kRows>, static_cast<unsigned>(blocks), kSplitThreads, kSmem, stream,
+                           cluster, xm, xn, wm, wn, P);
 }
 
 // The pair kernel once 256 x 128 tiles fill the pairs (64 of them: the split
@@ -1760,11 +1756,11 @@ cudaError_t launch_linear_grad(const LinearArgs& dx, const LinearArgs& dw, const
 cudaError_t launch_column_sums(const ColumnSumArgs& a, cudaStream_t stream) {
   const unsigned gx = static_cast<unsigned>((a.n + kSumCols - 1) / kSumCols);
   const int64_t slices = column_sum_slices(a.m, a.n);
-  column_sums_kernel<<<dim3(gx, static_cast<unsigned>(slices)), kSplitThreads, 0, stream>>>(plan_sums(a));
-  if (slices > 1)
-    join_sums_kernel<<<static_cast<unsigned>((a.n + 127) / 128), 128, 0, stream>>>(
-        a.partial, static_cast<int>(slices), a.n, a.out, a.accumulate);
-  return cudaGetLastError();
+  const cudaError_t e = launch_overlapped(column_sums_kernel, dim3(gx, static_cast<unsigned>(slices)), kSplitThreads, 0,
+                                          stream, 0, plan_sums(a));
+  if (e != cudaSuccess || slices == 1) return e;
+  return launch_overlapped(join_sums_kernel, static_cast<unsigned>((a.n + 127) / 128), 128, 0, stream, 0,
+                           static_cast<const float*>(a.partial), static_cast<int>(slices), a.n, a.out, a.accumulate);
 }
 
 cudaError_t launch_repack(const RepackBatch& batch, int esize, cudaStream_t stream) {
@@ -1773,9 +1769,8 @@ cudaError_t launch_repack(const RepackBatch& batch, int esize, cudaStream_t stre
   const int64_t grid = (pieces + 255) / 256;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   if (grid == 0) return cudaSuccess;
-  if (esize == 1) repack_kernel<uint8_t><<<static_cast<unsigned>(grid), 256, 0, stream>>>(batch);
-  else repack_kernel<uint16_t><<<static_cast<unsigned>(grid), 256, 0, stream>>>(batch);
-  return cudaGetLastError();
+  return launch_overlapped(esize == 1 ? repack_kernel<uint8_t> : repack_kernel<uint16_t>, static_cast<unsigned>(grid),
+                           256, 0, stream, 0, batch);
 }
 
 }  // namespace mpopt

@@ -20,6 +20,7 @@
 
 #include "../../include/mpopt.h"
 #include "internal.h"
+#include "overlap.cuh"
 
 namespace mpopt {
 namespace {
@@ -177,6 +178,8 @@ rmsnorm_kernel(const __grid_constant__ RmsnormArgs a) {
   constexpr int kThreads = kTPR == 32 ? 256 : kTPR;
   constexpr int kRows = kThreads / kTPR;
   __shared__ float vals[2][kTPR / 32];
+  let_next_start();
+  wait_for_predecessors();
   const int t = threadIdx.x % kTPR;
   const int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kTPR;
   if (r >= a.rows) return;                       // kTPR == 32: whole warps; otherwise the grid is exact
@@ -259,6 +262,8 @@ rmsnorm_kernel(const __grid_constant__ RmsnormArgs a) {
 template <int kTPR, int kNV>
 __global__ void __launch_bounds__(kTPR) rmsnorm_packed_kernel(const __grid_constant__ RmsnormArgs a) {
   __shared__ float vals[2][kTPR / 32];
+  let_next_start();
+  wait_for_predecessors();
   const int t = threadIdx.x;
   const int64_t r = blockIdx.x, cols = a.cols;
   uint4 raw[kNV];
@@ -323,6 +328,8 @@ template <typename T>
 __global__ void __launch_bounds__(kLongThreads) rmsnorm_long_kernel(const __grid_constant__ RmsnormArgs a) {
   extern __shared__ float row[];
   __shared__ float vals[2][kLongThreads / 32];
+  let_next_start();
+  wait_for_predecessors();
   const int64_t r = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + r * a.x_ld;
   const T* res = a.residual ? static_cast<const T*>(a.residual) + r * a.residual_ld : nullptr;
@@ -437,6 +444,8 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
   extern __shared__ uint4 ring[];              // [kStages][kU][kPieces][kThreads]
   __shared__ float vals[2][kU][kTPR / 32];
   __shared__ float join[kRows > 1 ? kRows * kTPR * 8 : 1];
+  let_next_start();
+  wait_for_predecessors();
   const int t = threadIdx.x % kTPR, sub = threadIdx.x / kTPR;
   const int64_t cols = a.cols;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
@@ -595,6 +604,8 @@ template <typename T>
 __global__ void __launch_bounds__(kLongThreads) rmsnorm_grad_long_kernel(const __grid_constant__ RmsnormGradArgs a) {
   extern __shared__ float rows[];
   __shared__ float vals[2][kLongThreads / 32];
+  let_next_start();
+  wait_for_predecessors();
   float* n_row = rows;
   float* g_row = rows + a.cols;
   float* part = a.dgamma ? a.partial + static_cast<int64_t>(blockIdx.x) * a.cols : nullptr;
@@ -631,6 +642,8 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_grad_long_kernel(const _
 __global__ void __launch_bounds__(1024)
 dgamma_kernel(const float* partial, int n_partial, int64_t cols, float* dgamma, int accumulate) {
   __shared__ float sums[32][32];
+  let_next_start();
+  wait_for_predecessors();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float s = 0.f;
@@ -670,9 +683,8 @@ cudaError_t forward_config(const RmsnormArgs& a, bool vec, cudaStream_t stream) 
   constexpr int kThreads = kTPR == 32 ? 256 : kTPR;
   constexpr int kRows = kThreads / kTPR;
   const unsigned grid = static_cast<unsigned>((a.rows + kRows - 1) / kRows);
-  if (vec) rmsnorm_kernel<T, kTPR, kNV, true><<<grid, kThreads, 0, stream>>>(a);
-  else rmsnorm_kernel<T, kTPR, kNV, false><<<grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(vec ? rmsnorm_kernel<T, kTPR, kNV, true> : rmsnorm_kernel<T, kTPR, kNV, false>, grid, kThreads,
+                           0, stream, 0, a);
 }
 
 template <typename T>
@@ -686,10 +698,9 @@ cudaError_t forward_typed(const RmsnormArgs& a, cudaStream_t stream) {
     // from 2049 columns on; a row of fewer is too short for CTAs of this kind
     if (vec && !a.residual && a.cols > 2048 && a.cols <= kRegisterCols) {
       const unsigned grid = static_cast<unsigned>(a.rows);
-      if (a.cols <= 4096) rmsnorm_packed_kernel<128, 4><<<grid, 128, 0, stream>>>(a);
-      else if (a.cols <= 8192) rmsnorm_packed_kernel<256, 4><<<grid, 256, 0, stream>>>(a);
-      else rmsnorm_packed_kernel<512, 4><<<grid, 512, 0, stream>>>(a);
-      return cudaGetLastError();
+      if (a.cols <= 4096) return launch_overlapped(rmsnorm_packed_kernel<128, 4>, grid, 128, 0, stream, 0, a);
+      if (a.cols <= 8192) return launch_overlapped(rmsnorm_packed_kernel<256, 4>, grid, 256, 0, stream, 0, a);
+      return launch_overlapped(rmsnorm_packed_kernel<512, 4>, grid, 512, 0, stream, 0, a);
     }
   }
   if (a.cols <= 256) return forward_config<T, 32, 1>(a, vec, stream);
@@ -701,8 +712,8 @@ cudaError_t forward_typed(const RmsnormArgs& a, cudaStream_t stream) {
   if (a.cols <= kRegisterCols) return forward_config<T, 512, 4>(a, vec, stream);
   const cudaError_t e = allow_smem<rmsnorm_long_kernel<T>>(static_cast<int>(kNormMaxCols * sizeof(float)));
   if (e != cudaSuccess) return e;
-  rmsnorm_long_kernel<T><<<static_cast<unsigned>(a.rows), kLongThreads, a.cols * sizeof(float), stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(rmsnorm_long_kernel<T>, static_cast<unsigned>(a.rows), kLongThreads, a.cols * sizeof(float),
+                           stream, 0, a);
 }
 
 // CTAs of a kernel that the GPU holds at a time (kept per thread and device).
@@ -733,8 +744,8 @@ cudaError_t grad_launch(const RmsnormGradArgs& a, int* grid, cudaStream_t stream
   if (n > most) n = most;
   if (n > kNormPartialRows) n = kNormPartialRows;
   *grid = static_cast<int>(n);
-  rmsnorm_grad_kernel<T, kTPR, kNV, kVec><<<*grid, kThreads, kSmem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(rmsnorm_grad_kernel<T, kTPR, kNV, kVec>, static_cast<unsigned>(*grid), kThreads, kSmem, stream,
+                           0, a);
 }
 
 template <typename T, int kTPR, int kNV>
@@ -759,8 +770,8 @@ cudaError_t grad_typed(const RmsnormGradArgs& a, int* grid, cudaStream_t stream)
   if (e != cudaSuccess) return e;
   const int64_t n = a.rows < num_sms() ? a.rows : num_sms();
   *grid = static_cast<int>(n < kNormPartialRows ? n : kNormPartialRows);
-  rmsnorm_grad_long_kernel<T><<<*grid, kLongThreads, 2 * a.cols * sizeof(float), stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(rmsnorm_grad_long_kernel<T>, static_cast<unsigned>(*grid), kLongThreads,
+                           2 * a.cols * sizeof(float), stream, 0, a);
 }
 
 }  // namespace
@@ -781,10 +792,10 @@ cudaError_t launch_rmsnorm_grad(const RmsnormGradArgs& a, cudaStream_t stream) {
   }
   if (!a.dgamma) return cudaSuccess;
   prof_begin(OPT_KERNEL_RMSNORM_DGAMMA, 1, a.rows, a.cols, stream);
-  dgamma_kernel<<<static_cast<unsigned>((a.cols + 31) / 32), 1024, 0, stream>>>(a.partial, grid, a.cols, a.dgamma,
-                                                                                a.accumulate);
+  const cudaError_t e = launch_overlapped(dgamma_kernel, static_cast<unsigned>((a.cols + 31) / 32), 1024, 0, stream, 0,
+                                          static_cast<const float*>(a.partial), grid, a.cols, a.dgamma, a.accumulate);
   prof_end(stream);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace mpopt
