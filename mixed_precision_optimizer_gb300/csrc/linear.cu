@@ -139,6 +139,17 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
   }
 }
 
+// main_grad += without reading it: each element gets one addition per launch,
+// rounded to nearest in fp32, in L2 (subnormal results become zero), so the
+// result does not depend on an order.
+__device__ __forceinline__ void red_add(float* p, float v) {
+  asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
+}
+__device__ __forceinline__ void red_add(float4* p, float4 v) {
+  asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+
 // -------------------------------------------------------------- epilogue --
 
 // What the epilogue needs of this lane's output column `a` throughout a tile.
@@ -326,44 +337,33 @@ __device__ __forceinline__ void store_row_out(uint16_t* p, int64_t ld, int64_t r
 template <int kN>
 __device__ __forceinline__ void store_row_dw(float* p, int64_t ld, int64_t row, int64_t rows, int64_t col,
                                              int64_t cols, bool vec, bool add, float* table, int lane,
-                                             float (&v)[kN]) {
+                                             const float (&v)[kN]) {
   if (vec && col + kN <= cols) {
     if (row < rows) {
       float4* q = reinterpret_cast<float4*>(p + row * ld + col);
-      float4 old[kN / 4];
-      if (add) {
 #pragma unroll
-        for (int i = 0; i < kN / 4; ++i) old[i] = q[i];
-#pragma unroll
-        for (int i = 0; i < kN / 4; ++i) {
-          v[4 * i] += old[i].x, v[4 * i + 1] += old[i].y, v[4 * i + 2] += old[i].z, v[4 * i + 3] += old[i].w;
-        }
+      for (int i = 0; i < kN / 4; ++i) {
+        const float4 x = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        if (add) red_add(q + i, x);
+        else q[i] = x;
       }
-#pragma unroll
-      for (int i = 0; i < kN / 4; ++i) q[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     }
     return;
   }
-  constexpr int kTurns = kN;          // 32 rows, 32 / kN at a time
-  const int sub = lane / kN, c = lane % kN;
+  const int sub = lane / kN, c = lane % kN;          // 32 rows, 32 / kN at a time
   const int64_t row0 = row - lane;
-  float old[kTurns];
-  if (add) {
-#pragma unroll
-    for (int i = 0; i < kTurns; ++i) {
-      const int64_t rr = row0 + i * (32 / kN) + sub;
-      old[i] = rr < rows && col + c < cols ? p[rr * ld + col + c] : 0.f;
-    }
-  }
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < kN; ++j) table[lane * (kN + 1) + j] = v[j];
   __syncwarp();
 #pragma unroll
-  for (int i = 0; i < kTurns; ++i) {
+  for (int i = 0; i < kN; ++i) {
     const int r = i * (32 / kN) + sub;
     const float x = table[r * (kN + 1) + c];
-    if (row0 + r < rows && col + c < cols) p[(row0 + r) * ld + col + c] = add ? old[i] + x : x;
+    if (row0 + r < rows && col + c < cols) {
+      if (add) red_add(p + (row0 + r) * ld + col + c, x);
+      else p[(row0 + r) * ld + col + c] = x;
+    }
   }
 }
 
@@ -634,14 +634,7 @@ __device__ __forceinline__ void split_tile(const CUtensorMap& map_a, const CUten
     for (int c = 0; c < kSum; ++c) sum[c] = 0.f;
     uint32_t use = 0;
     ready = exists;
-    if constexpr (kMode == kLinearDw) {
-      const int64_t c = n0 + rank * (kBN / P.split);
-      if (exists && P.g.accumulate && index < P.g.nb && c < P.g.na) {
-        const float* p = P.g.dw + index * P.g.dw_ld + c;
-        prefetch_l2(p);
-        if (P.split == 1 && c + 32 < P.g.na) prefetch_l2(p + 32);
-      }
-    } else if constexpr (kRows) {
+    if constexpr (kRows && kMode != kLinearDw) {
       // the residual or pre-activation of this rank's share comes from DRAM while the MMAs run
       const uint16_t* in = kMode == kLinearDx ? P.g.z_in : P.g.residual;
       const int64_t c = n0 + rank * (kBN / P.split);
@@ -703,7 +696,7 @@ __device__ __forceinline__ void split_tile(const CUtensorMap& map_a, const CUten
   // spent 5 us here).
   auto join = [&](auto split_tag) {
     constexpr int kSplit = decltype(split_tag)::value, kPer = kBN / kSplit;
-    constexpr int kMost = kMode == kLinearDw ? 16 : 32;          // dw keeps sums and main_grad's old values in registers
+    constexpr int kMost = kMode == kLinearDw ? 16 : 32;          // dw keeps its sums in registers
     constexpr int kN = kPer > kMost ? kMost : kPer < 4 ? 4 : kPer;     // kPer 2 (16 columns, 8 ranks): half of a word
     constexpr int kGroup = kSplit * kN > 128 ? 128 / kSplit : kN;   // columns loaded at a time: 128 registers at most
     const uint32_t base = smem_u32(smem) + (quarter * 32 + lane) * 16;
@@ -1079,9 +1072,11 @@ __device__ __forceinline__ void load_block(const uint16_t* p, int64_t ld, int64_
     return;
   }
   const bool ok = col0 + lane < cols;
-#pragma unroll 8
-  for (int r = 0; r < 32; ++r)
-    table[turn(r, lane)] = ok && row0 + r < rows ? p[(row0 + r) * ld + col0 + lane] : 0;
+  uint16_t got[32];                        // all loads in flight together
+#pragma unroll
+  for (int r = 0; r < 32; ++r) got[r] = ok && row0 + r < rows ? p[(row0 + r) * ld + col0 + lane] : 0;
+#pragma unroll
+  for (int r = 0; r < 32; ++r) table[turn(r, lane)] = got[r];
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < 16; ++i) raw[i] = table[turn(lane, 2 * i)] | (table[turn(lane, 2 * i + 1)] << 16);
@@ -1368,7 +1363,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
               for (int j = 0; j < 32; ++j) v[j] = sum[c + j];
               const bool add = P.g.accumulate != 0;
               store_turned(P.g.dw, P.g.dw_ld, row0, col0 + c, P.g.nb, P.g.na, reinterpret_cast<float*>(table), lane, v,
-                           [add](float* p, float x) { *p = add ? *p + x : x; });
+                           [add](float* p, float x) {
+                             if (add) red_add(p, x);
+                             else *p = x;
+                           });
             }
           }
         }
@@ -1385,6 +1383,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
         };
         const bool in_tma = P.in_tma != 0;
         if (in_tma && live && col0 < P.g.na) load_in(0);
+        if (in && !in_tma && row0 + lane < P.g.nb) {
+          // rows that TMA cannot read come into L2 meanwhile
+          const uint16_t* p = in + (row0 + lane) * in_ld + col0;
+          for (int64_t c = 0; c < C::kHalf && col0 + c < P.g.na; c += 64) prefetch_l2(p + c);
+        }
         const bool alternate = P.out_tma && !in && !(kMode == kLinearForward && P.g.z_out);
         float row_scale = 1.f;
         if (kFp8 && row0 + lane < P.g.nb) row_scale = P.g.b_scale[row0 + lane];
