@@ -966,6 +966,13 @@ struct PairParams {
   int in_tma;          // and there is no z: the input comes through map_z
 };
 
+struct PairSplitParams {
+  PairParams p;
+  RowAccess access;
+  int per_pair;        // k-blocks of one pair of the cluster
+  int tile0;           // the launch's first tile
+};
+
 // Tiles in groups of kGroupB tiles along b, a-major inside a group: about 76
 // tiles are in flight, a block of 12 x 6.3 tiles that shares its panels (4 and 6
 // wide: up to 5 % slower on 8192 x 14336 x 4096 and its gradients; 8 and 16 within 2 %).
@@ -1519,6 +1526,280 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   }
 }
 
+// ------------------------------------------------- pair kernel, k split --
+//
+// A last wave that less than half fills the GPU, or a product with that few
+// tiles: a cluster of two CTA pairs splits the k-blocks of one 256 x 256 tile
+// (four pairs: slower, the GPU holds too few clusters of eight such CTAs).
+// Every CTA leaves its sums in its shared memory, and the CTAs of the same 128
+// rows add their shares of the columns in order, as in the split kernel, and
+// run its epilogue.
+//   warp 0     TMA producer
+//   warp 1     TMEM allocation; in the even CTA of a pair the MMA issuer
+//   warps 2-9  epilogue: two warps per TMEM lane quarter, half of the columns each
+
+constexpr int kPairSplitThreads = 64 + 32 * kPairEpiWarps;
+constexpr int kPairSplit = 2;                  // pairs of a cluster
+
+struct PairSplitConfig {
+  static constexpr int kBN = 256;
+  static constexpr int kStageBytes = 2 * kStageA;
+  static constexpr int kStages = 6;
+  static constexpr int kPartBytes = BM * kBN * 4;
+  static constexpr uint32_t kSmemBytes = kStages * kStageBytes + 1024 /*align*/ + 256 /*barriers*/;
+  static_assert(kSmemBytes <= 232448, "dynamic shared memory above the 227 KB a CTA may use");
+  static_assert(kPartBytes + kPairEpiWarps * kTableWords<32> * 4 <= kStages * kStageBytes,
+                "partial sums and tables larger than the ring they replace");
+};
+
+// Arrive on `bar` in the CTAs of `mask` once all MMAs of this thread have completed.
+__device__ __forceinline__ void mma_commit_mask(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(mask)
+      : "memory");
+}
+
+template <int kMode, bool kFp8>
+__global__ void __launch_bounds__(kPairSplitThreads, 1)
+linear_pair_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                         const __grid_constant__ PairSplitParams P) {
+  using C = PairSplitConfig;
+  constexpr int kSplit = kPairSplit;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);   // even CTA: both CTAs' copies landed
+  uint64_t* empty = full + C::kStages;             // both CTAs: stage free again
+  uint64_t* acc_full = empty + C::kStages;         // [2] both CTAs: accumulator ready
+  uint64_t* acc_empty = acc_full + 2;              // [2] even CTA: both epilogues have read it
+  uint64_t* drain = acc_empty + 2;                 // even CTA: all MMAs complete
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+
+  constexpr int kElems = kFp8 ? 128 : 64;
+  // the MMA's A operand holds output rows (the product's B), its B operand output columns
+  constexpr bool a_mn = Order<kMode>::b_mn, b_mn = Order<kMode>::a_mn;
+  constexpr int kTmemCols = kMode == kLinearDw ? 512 : 256;       // dw: two accumulators
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t cta = cluster_rank(), rank = cta & 1u, even = cta & ~1u;
+  const int part = static_cast<int>(cta >> 1);                    // which share of the k-blocks
+  const uint16_t both = static_cast<uint16_t>(3u << even);
+  uint32_t* status = P.p.g.header;
+  const int kb0 = min(part * P.per_pair, P.p.k_blocks), kb1 = min(kb0 + P.per_pair, P.p.k_blocks);
+  int ta, tb;
+  pair_tile(P.p, P.tile0 + static_cast<int>(blockIdx.x) / (2 * kSplit), ta, tb);
+  let_next_start();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&acc_full[a]), 1);
+      mbar_init(smem_u32(&acc_empty[a]), 2 * 32 * kPairEpiWarps);
+    }
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0 && lane < 2) {
+    const CUtensorMap* map = lane == 0 ? &map_a : &map_b;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  wait_for_predecessors();
+  tc_fence_before();
+  cluster_sync();            // barriers of all CTAs initialised, TMEM allocated
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t sa0 = smem_u32(smem), sb0 = sa0 + C::kStages * kStageA;
+  const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+  const int quarter = warp & 3, half = (warp - 2) >> 2;
+  constexpr int kSum = kMode == kLinearDw ? 128 : 1;
+  float sum[kSum];
+  bool ready = false;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t full_even = peer_addr(full0, even);
+      const int ai = tb * 256 + static_cast<int>(rank) * BM, bi = ta * C::kBN + static_cast<int>(rank) * 128;
+      uint32_t s = 0, ph = 0;
+      int kb = kb0;
+      for (; kb < kb1; ++kb) {
+        if (!mbar_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, status, kStatusTimeoutEmpty)) break;
+        const uint32_t fb = full_even + 8 * s;
+        if (rank == 0) mbar_expect_tx(full0 + 8 * s, 2 * C::kStageBytes);
+        const uint32_t sa = sa0 + s * kStageA, sb = sb0 + s * kStageA;
+        if constexpr (a_mn) {
+          tma_load_2d_pair(sa, &map_a, fb, ai, kb * kElems);
+          tma_load_2d_pair(sa + kMnBlockBytes, &map_a, fb, ai + 64, kb * kElems);
+        } else {
+          tma_load_2d_pair(sa, &map_a, fb, kb * kElems, ai);
+        }
+        if constexpr (b_mn) {
+          tma_load_2d_pair(sb, &map_b, fb, bi, kb * kElems);
+          tma_load_2d_pair(sb + kMnBlockBytes, &map_b, fb, bi + 64, kb * kElems);
+        } else {
+          tma_load_2d_pair(sb, &map_b, fb, kb * kElems, bi);
+        }
+        if (++s == C::kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      if (kb < kb1) {
+        // aborting: give copies in flight time to land before the CTA exits
+        const unsigned long long t0 = global_ns();
+        while (global_ns() - t0 < 10000000ull) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0 && kb1 > kb0) {
+      constexpr uint32_t idesc = linear_idesc(kFp8, a_mn, b_mn, 256, C::kBN);
+      const uint64_t ad0 = a_mn ? smem_desc_mn(sa0) : smem_desc(sa0);
+      const uint64_t bd0 = b_mn ? smem_desc_mn(sb0) : smem_desc(sb0);
+      constexpr uint32_t ka = (a_mn ? 16 * kRowBytes : 32) >> 4, kbs = (b_mn ? 16 * kRowBytes : 32) >> 4;
+      uint32_t s = 0, ph = 0, use = 0;
+      bool ok = true;
+      for (int k0 = kb0; ok && k0 < kb1; k0 += P.p.segment, ++use) {
+        const uint32_t acc = use & 1;
+        if (!mbar_wait(smem_u32(&acc_empty[acc]), ((use >> 1) & 1u) ^ 1u, abort_flag, status, kStatusTimeoutAccFree))
+          break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * C::kBN;
+        const int k1 = min(k0 + P.p.segment, kb1);
+        for (int kb = k0; kb < k1; ++kb) {
+          if (!mbar_wait(full0 + 8 * s, ph, abort_flag, status, kStatusTimeoutFull)) {
+            ok = false;
+            break;
+          }
+          const uint64_t ad = ad0 + s * (kStageA >> 4), bd = bd0 + s * (kStageA >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_pair<kFp8>(d_tmem, ad + ka * kk, bd + kbs * kk, idesc, (kb > k0 || kk > 0) ? 1u : 0u);
+          mma_commit_mask(empty0 + 8 * s, both);
+          if (++s == C::kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (ok) mma_commit_mask(smem_u32(&acc_full[acc]), both);
+      }
+      // every MMA issued by this thread has completed before TMEM goes
+      mma_commit_local(smem_u32(drain));
+      const unsigned long long t0 = global_ns();
+      while (!mbar_try(smem_u32(drain), 0)) {
+        if (global_ns() - t0 > kWaitLimitNs) {
+          *abort_flag = 1u;
+          atomicCAS(status, 0u, static_cast<uint32_t>(kStatusTimeoutDrain));
+          break;
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < kSum; ++c) sum[c] = 0.f;
+    const uint32_t empty_even = peer_addr(smem_u32(&acc_empty[0]), even);
+    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
+    ready = true;
+    uint32_t use = 0;
+    for (int k0 = kb0; ready && k0 < kb1; k0 += P.p.segment, ++use) {
+      const uint32_t acc = use & 1;
+      ready = __all_sync(0xffffffffu, mbar_wait(smem_u32(&acc_full[acc]), (use >> 1) & 1u, abort_flag, status,
+                                                kStatusTimeoutAcc));
+      if (!ready) break;
+      tc_fence_after();
+      if constexpr (kMode == kLinearDw) {
+#pragma unroll
+        for (int c = 0; c < 128; c += 16) {
+          float v[16];
+          tmem_ld16(lane_addr + acc * C::kBN + c, v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sum[c + j] += v[j];
+        }
+        tc_fence_before();
+        mbar_arrive_remote(empty_even + acc * 8);
+      }
+    }
+    // the sums take the place of the ring: the pair's MMAs have completed
+    // (acc_full).  Four columns of a lane are one 16-byte word: [column / 4][lane]
+    if (ready) {
+      float4* sums = reinterpret_cast<float4*>(smem);
+#pragma unroll
+      for (int c = 0; c < 128; c += 16) {
+        float v[16];
+        if constexpr (kMode == kLinearDw) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = sum[c + j];
+        } else if (kb1 > kb0) {
+          tmem_ld16(lane_addr + c, v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+          sums[(half * 128 + c + j) / 4 * BM + quarter * 32 + lane] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+      }
+    }
+  }
+  __syncwarp();
+  cluster_sync();
+  if (ready) {
+    const LinearArgs& g = P.p.g;
+    const int64_t row = static_cast<int64_t>(tb) * 256 + rank * BM + quarter * 32 + lane;
+    float row_scale = 1.f;
+    if (kFp8 && row < g.nb) row_scale = g.b_scale[row];
+    uint32_t* table = reinterpret_cast<uint32_t*>(smem + C::kPartBytes) + (warp - 2) * kTableWords<32>;
+    const uint32_t base = smem_u32(smem) + (quarter * 32 + lane) * 16;
+    constexpr int kShare = C::kBN / kSplit / 2;                   // columns of this warp
+#pragma unroll
+    for (int c0 = 0; c0 < kShare; c0 += 32) {
+      const int c = (part * 2 + half) * kShare + c0;
+      const int64_t col = static_cast<int64_t>(ta) * C::kBN + c;
+      if (col >= g.na) break;
+      float v[32];
+      float4 w[kSplit][8];
+#pragma unroll
+      for (int q = 0; q < kSplit; ++q) {
+        const uint32_t peer = peer_addr(base, 2u * q + rank);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[q][i] = ld_cluster_f32x4(peer + (c / 4 + i) * (BM * 16));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float4 t = w[0][i];
+#pragma unroll
+        for (int q = 1; q < kSplit; ++q) {
+          t.x += w[q][i].x;
+          t.y += w[q][i].y;
+          t.z += w[q][i].z;
+          t.w += w[q][i].w;
+        }
+        v[4 * i] = t.x;
+        v[4 * i + 1] = t.y;
+        v[4 * i + 2] = t.z;
+        v[4 * i + 3] = t.w;
+      }
+      epilogue_row<kMode, kFp8, 32>(g, P.access, row_scale, row, col, table, lane, v);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();            // no CTA leaves while another reads its sums or may still signal it
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
+  }
+}
+
 // ------------------------------------------------------- smaller kernels --
 
 // Operand copies with rows on 16 bytes, up to three in one launch.  A thread
@@ -1597,16 +1878,41 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
-template <int kMode, bool kFp8, int kBN>
-cudaError_t launch_pair(const LinearArgs& a, int k_blocks, int tiles_a, int tiles_b, cudaStream_t stream) {
-  using C = PairConfig<kMode, kBN>;
+int k_blocks_of(const LinearArgs& a) {
+  const int64_t elems = a.fp8 ? 128 : 64;
+  return static_cast<int>((a.nk + elems - 1) / elems);
+}
+
+template <int kMode>
+PairParams pair_params(const LinearArgs& a, int bn, int total_tiles) {
   PairParams P{};
   P.g = a;
-  P.k_blocks = k_blocks;
-  P.segment = kMode == kLinearDw ? kDwSegment : k_blocks;
-  P.tiles_a = tiles_a;
-  P.tiles_b = tiles_b;
-  P.total_tiles = tiles_a * tiles_b;
+  P.k_blocks = k_blocks_of(a);
+  P.segment = kMode == kLinearDw ? kDwSegment : P.k_blocks;
+  P.tiles_a = static_cast<int>((a.na + bn - 1) / bn);
+  P.tiles_b = static_cast<int>((a.nb + 255) / 256);
+  P.total_tiles = total_tiles;
+  return P;
+}
+
+template <int kMode>
+RowAccess row_access(const LinearArgs& a) {
+  RowAccess r{};
+  if (kMode == kLinearDw) {
+    r.out_vec = rows_on_16(a.dw, a.dw_ld, a.nb, 4);
+  } else {
+    r.out_vec = rows_on_16(a.y, a.y_ld, a.nb, 2) && (!a.z_out || rows_on_16(a.z_out, a.z_ld, a.nb, 2));
+    r.in_vec = kMode == kLinearDx ? rows_on_16(a.z_in, a.z_ld, a.nb, 2)
+                                  : rows_on_16(a.residual, a.residual_ld, a.nb, 2);
+  }
+  return r;
+}
+
+// The first `tiles` tiles.
+template <int kMode, bool kFp8, int kBN>
+cudaError_t launch_pair(const LinearArgs& a, int64_t tiles, cudaStream_t stream) {
+  using C = PairConfig<kMode, kBN>;
+  PairParams P = pair_params<kMode>(a, kBN, static_cast<int>(tiles));
   CUtensorMap ma, mb, mo{}, mz{};
   cudaError_t e;
   if ((e = make_operand_map(&ma, a.A, a.na, a.nk, kFp8, C::kHalf)) != cudaSuccess) return e;
@@ -1629,9 +1935,21 @@ cudaError_t launch_pair(const LinearArgs& a, int k_blocks, int tiles_a, int tile
                            stream, 0, mb, ma, mo, mz, P);
 }
 
-int k_blocks_of(const LinearArgs& a) {
-  const int64_t elems = a.fp8 ? 128 : 64;
-  return static_cast<int>((a.nk + elems - 1) / elems);
+// Tiles tile0 .. tile0 + tiles - 1 of 256 x 256, each by a cluster of pairs.
+template <int kMode, bool kFp8>
+cudaError_t launch_pair_split(const LinearArgs& a, int64_t tile0, int64_t tiles, cudaStream_t stream) {
+  PairSplitParams P{};
+  P.p = pair_params<kMode>(a, 256, static_cast<int>(tile0 + tiles));
+  P.access = row_access<kMode>(a);
+  P.per_pair = (P.p.k_blocks + kPairSplit - 1) / kPairSplit;
+  P.tile0 = static_cast<int>(tile0);
+  CUtensorMap ma, mb;
+  cudaError_t e;
+  if ((e = make_operand_map(&ma, a.A, a.na, a.nk, kFp8, 128)) != cudaSuccess) return e;
+  if ((e = make_operand_map(&mb, a.B, a.nb, a.nk, kFp8, BM)) != cudaSuccess) return e;
+  if ((e = allow_smem<linear_pair_split_kernel<kMode, kFp8>>(PairSplitConfig::kSmemBytes)) != cudaSuccess) return e;
+  return launch_overlapped(linear_pair_split_kernel<kMode, kFp8>, static_cast<unsigned>(tiles * 2 * kPairSplit),
+                           kPairSplitThreads, PairSplitConfig::kSmemBytes, stream, 2 * kPairSplit, mb, ma, P);
 }
 
 // Parameters and operand maps of a split product: m on the lanes, n on the columns.
@@ -1649,13 +1967,7 @@ cudaError_t plan_split(const LinearArgs& a, SplitParams* P, CUtensorMap* m, CUte
     P->split *= 2;
   P->per_rank = (P->k_blocks + P->split - 1) / P->split;
   P->segment = kMode == kLinearDw ? kDwSegment : P->k_blocks;
-  if (kMode == kLinearDw) {
-    P->access.out_vec = rows_on_16(a.dw, a.dw_ld, a.nb, 4);
-  } else {
-    P->access.out_vec = rows_on_16(a.y, a.y_ld, a.nb, 2) && (!a.z_out || rows_on_16(a.z_out, a.z_ld, a.nb, 2));
-    P->access.in_vec = kMode == kLinearDx ? rows_on_16(a.z_in, a.z_ld, a.nb, 2)
-                                          : rows_on_16(a.residual, a.residual_ld, a.nb, 2);
-  }
+  P->access = row_access<kMode>(a);
   if (P->tiles > (int64_t(1) << 27)) return cudaErrorInvalidValue;
   const cudaError_t e = make_operand_map(kRows ? n : m, a.A, a.na, a.nk, kFp8, kRows ? kBN : BM);
   return e != cudaSuccess ? e : make_operand_map(kRows ? m : n, a.B, a.nb, a.nk, kFp8, kRows ? BM : kBN);
@@ -1696,16 +2008,44 @@ cudaError_t launch_grad(const LinearArgs& dx, const LinearArgs& dw, const Column
                            cluster, xm, xn, wm, wn, P);
 }
 
-// The pair kernel once 256 x 128 tiles fill the pairs (64 of them: the split
-// kernel takes 9.4 us for 2048 x 1024 x 1024 against 11.7, 14.6 for 1024 x 2048
-// x 2048 against 16.4; 128: 45 us for 1024 x 4096 x 4096 against 28) and the
-// rows fill more than half of a tile (128 x 4096 x 4096: 13 us against 25).
-// dw of a few tokens is little more than its stores: there twice the tiles (1 x
-// 2048 x 2048, 128 tiles: 10.9 us split against 12.0, and dx shares the launch).
-bool takes_pairs(const LinearArgs& a) {
-  const int64_t tiles_b = (a.nb + 255) / 256, tiles128 = tiles_b * ((a.na + 127) / 128);
-  const int64_t enough = num_sms() / 2 * (a.mode == kLinearDw && k_blocks_of(a) <= 2 ? 2 : 1);
-  return a.nb > 128 && tiles128 >= enough && tiles128 < (int64_t(1) << 30);
+// How a product runs.
+struct Plan {
+  int pair_width;        // of the pair kernel's tiles, or 0: the split kernel
+  int64_t pair_tiles;    // by the pair kernel, the first ones
+  int64_t tail_tiles;    // 256 x 256 tiles after them, by clusters of pairs
+};
+
+// The pair kernels take products of more than 128 rows (128 x 4096 x 4096: 25 us
+// against 13 of the split kernel) once 256 x 128 tiles fill the pairs (64 of
+// them: the split kernel takes 9.4 us for 2048 x 1024 x 1024 against 11.7), or
+// from 24 tiles of 256 x 256 with 32 k-blocks if clusters of pairs split them
+// (512 x 4096 x 4096, 32 tiles: 18 us against 25; 512 x 2048 x 2048, 16: 12.2
+// against 10.1).  dw of a few tokens is little more than its stores: there twice
+// the tiles (1 x 2048 x 2048, 128 tiles of 128: 10.9 us split against 12.0, and
+// dx shares the launch).
+//
+// Measured cycles of a tile: 560 a k-block and 7000 besides when it is 256 wide,
+// 500 and 4500 when 128 (both wait for their operands from L2: 58 and 49 bytes a
+// cycle per SM), so the narrow one pays where it fills the last wave better or
+// the sum is short.  A last wave of clusters takes 26000 besides its share of the
+// k-blocks, the start of its own launch included (8192 x 4096 x 4096's dw: 187
+// -> 179 us, 837 x 6784 x 8856: 112 -> 95 us).
+Plan plan_product(const LinearArgs& a) {
+  const int64_t pairs = num_sms() / 2, kb = k_blocks_of(a);
+  const int64_t tiles_b = (a.nb + 255) / 256;
+  const int64_t t256 = tiles_b * ((a.na + 255) / 256), t128 = tiles_b * ((a.na + 127) / 128);
+  if (a.nb <= 128 || t128 >= (int64_t(1) << 30)) return Plan{};
+  const auto waves = [pairs](int64_t t) { return (t + pairs - 1) / pairs; };
+  const int64_t full = t256 / pairs * pairs, rest = t256 - full;
+  if (t256 >= 24 && t256 <= pairs / kPairSplit && kb >= 32) return Plan{256, 0, t256};
+  if (t128 < pairs * (a.mode == kLinearDw && kb <= 2 ? 2 : 1)) return Plan{};
+  const int64_t tile256 = 560 * kb + 7000, tile128 = 500 * kb + 4500;
+  const int64_t c256 = waves(t256) * tile256, c128 = waves(t128) * tile128;
+  if (full > 0 && rest > 0 && rest <= pairs / kPairSplit) {
+    const int64_t tail = full / pairs * tile256 + 560 * ((kb + kPairSplit - 1) / kPairSplit) + 26000;
+    if (tail < c256 && tail < c128) return Plan{256, full, rest};
+  }
+  return c256 <= c128 ? Plan{256, t256, 0} : Plan{128, t128, 0};
 }
 
 // Rows to a tile of a split product with the lanes on the columns, or 0: the
@@ -1721,18 +2061,14 @@ int column_lanes(const LinearArgs& a) {
 
 template <int kMode, bool kFp8>
 cudaError_t launch_product(const LinearArgs& a, cudaStream_t stream) {
-  if (takes_pairs(a)) {
-    const int64_t tiles_b = (a.nb + 255) / 256, pairs = num_sms() / 2;
-    const int64_t a256 = (a.na + 255) / 256, a128 = (a.na + 127) / 128;
-    // Measured cycles of a tile: 560 a k-block and 7000 besides when it is 256
-    // wide, 500 and 4500 when 128 (both wait for their operands from L2: 58 and
-    // 49 bytes a cycle per SM), so the narrow one pays where it fills the last
-    // wave better or the sum is short.
-    const int64_t waves256 = (tiles_b * a256 + pairs - 1) / pairs, waves128 = (tiles_b * a128 + pairs - 1) / pairs;
-    const int64_t kb = k_blocks_of(a);
-    if (waves256 * (560 * kb + 7000) <= waves128 * (500 * kb + 4500))
-      return launch_pair<kMode, kFp8, 256>(a, k_blocks_of(a), static_cast<int>(a256), static_cast<int>(tiles_b), stream);
-    return launch_pair<kMode, kFp8, 128>(a, k_blocks_of(a), static_cast<int>(a128), static_cast<int>(tiles_b), stream);
+  const Plan plan = plan_product(a);
+  if (plan.pair_width) {
+    cudaError_t e = cudaSuccess;
+    if (plan.pair_tiles > 0)
+      e = plan.pair_width == 256 ? launch_pair<kMode, kFp8, 256>(a, plan.pair_tiles, stream)
+                                 : launch_pair<kMode, kFp8, 128>(a, plan.pair_tiles, stream);
+    if (e != cudaSuccess || plan.tail_tiles == 0) return e;
+    return launch_pair_split<kMode, kFp8>(a, plan.pair_tiles, plan.tail_tiles, stream);
   }
   if constexpr (kMode != kLinearDw) {
     switch (column_lanes(a)) {
@@ -1763,7 +2099,9 @@ ColumnSums plan_sums(const ColumnSumArgs& a) {
 
 }  // namespace
 
-bool linear_grad_fits(const LinearArgs& dx, const LinearArgs& dw) { return !takes_pairs(dx) && !takes_pairs(dw); }
+bool linear_grad_fits(const LinearArgs& dx, const LinearArgs& dw) {
+  return plan_product(dx).pair_width == 0 && plan_product(dw).pair_width == 0;
+}
 
 cudaError_t launch_linear_grad(const LinearArgs& dx, const LinearArgs& dw, const ColumnSumArgs* sums,
                                cudaStream_t stream) {

@@ -263,6 +263,26 @@ def test_linear_backward_large(m, n, k, layout, kind):
     check_linear_backward(m, n, k, layout, kind)
 
 
+# 24 to 38 tiles of 256 x 256 with 32 k-blocks or more: clusters of two CTA pairs
+# (of which the last may have a short share); 80 tiles with 88: 76 by pairs and a
+# last wave of 4 by clusters
+SPLIT_TILES = [(1000, 1500, 2200), (1500, 1530, 2060), (2000, 2500, 5600)]
+
+
+@pytest.mark.parametrize("m,n,k", SPLIT_TILES)
+@pytest.mark.parametrize("kind,layout,e4m3", [("silu", "dense", False), ("gelu", "odd slice", False),
+                                              ("none", "aligned slice", True)])
+def test_linear_tiles_shared_by_pairs(m, n, k, kind, layout, e4m3):
+    check_linear(m, n, k if not e4m3 else 2 * k, e4m3, layout, kind)
+
+
+@pytest.mark.parametrize("m,n,k", SPLIT_TILES)
+@pytest.mark.parametrize("kind,layout", [("gelu", "dense"), ("relu", "odd slice")])
+def test_linear_backward_tiles_shared_by_pairs(m, n, k, kind, layout):
+    check_linear_backward(m, k, n, layout, kind)        # dx: k in n's place
+    check_linear_backward(k, m, n, layout, kind)        # dw: k tokens
+
+
 def check_linear(m, n, k, e4m3, layout, kind):
     x, w, xs, wsc = linear_case(m, n, k, e4m3, layout)
     bias = normal(3, (n,), torch.bfloat16 if kind == "relu" else torch.float32) if kind != "gelu" else None
