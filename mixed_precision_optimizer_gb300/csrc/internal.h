@@ -319,7 +319,7 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream);
 // through `partial` [column_sum_slices][n] when there is more than one: enough
 // CTAs of 64 columns to fill the GPU, at least 256 rows to a slice.
 inline int64_t column_sum_slices(int64_t m, int64_t n) {
-  const int64_t by_rows = (m + 255) / 256, wanted = (152 * 4 * 64 + n - 1) / n;
+  const int64_t by_rows = (m + 255) / 256, wanted = (152 * 8 * 64 + n - 1) / n;
   const int64_t s = by_rows < wanted ? by_rows : wanted;
   return s < 1 ? 1 : s > 64 ? 64 : s;
 }

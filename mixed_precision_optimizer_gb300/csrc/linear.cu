@@ -816,19 +816,21 @@ __device__ __forceinline__ void column_sums(const ColumnSums& p, int64_t x, int6
   const int64_t r0 = per * y, r1 = r0 + per < p.m ? r0 + per : p.m;
   float2 s = make_float2(0.f, 0.f);
   if (c < p.n) {
-    if (p.vec) {
-#pragma unroll 16
-      for (int64_t r = r0 + warp; r < r1; r += kWarps) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(p.dz + r * p.ld + c);
-        s.x += __uint_as_float(w << 16);
-        s.y += __uint_as_float(w & 0xffff0000u);
+    // sixteen rows' loads in flight together
+    constexpr int kBatch = 16;
+    const int64_t two = c + 1 < p.n ? 1 : 0;         // past the last column: that one again, not stored
+    for (int64_t q = r0 + warp; q < r1; q += kWarps * kBatch) {
+      uint32_t v[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int64_t r = q + j * kWarps;
+        const uint16_t* x = p.dz + r * p.ld + c;
+        v[j] = r >= r1 ? 0u : p.vec ? *reinterpret_cast<const uint32_t*>(x) : x[0] | static_cast<uint32_t>(x[two]) << 16;
       }
-    } else {
-      const int64_t two = c + 1 < p.n ? 1 : 0;       // past the last column: that one again, not stored
-#pragma unroll 16
-      for (int64_t r = r0 + warp; r < r1; r += kWarps) {
-        s.x += bf16_at(p.dz + r * p.ld + c, 0);
-        s.y += bf16_at(p.dz + r * p.ld + c, two);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        s.x += __uint_as_float(v[j] << 16);
+        s.y += __uint_as_float(v[j] & 0xffff0000u);
       }
     }
   }

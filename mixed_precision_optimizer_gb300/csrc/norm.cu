@@ -531,9 +531,8 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
         dy[u][i].get(g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          n[j] *= rstd[u];
-          const float p = g[j] * n[j];
-          part[i][j] += p;
+          const float p = g[j] * n[j];            // dy h; rstd comes in once a sum
+          part[i][j] += p * rstd[u];
           dot[u] += p * gamma[j];
         }
       }
@@ -546,15 +545,18 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
     }
     if (a.dx) {
       rows_reduce<kTPR, kU>(dot, vals[parity]);
+      // rstd (g - n mean(g n)) = rstd g - (rstd^3 mean(g h)) h
+      float back[kU];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        if (r + u * step >= a.rows) break;
-        const float mean = dot[u] * inv_cols;
-        T* dx = static_cast<T*>(a.dx) + (r + u * step) * a.dx_ld;
+      for (int u = 0; u < kU; ++u) back[u] = -rstd[u] * rstd[u] * rstd[u] * (dot[u] * inv_cols);
 #pragma unroll
-        for (int i = 0; i < kNV; ++i) {
-          float n[8], g[8], gamma[8], d[8];
-          load_gamma<kTPR, kVec>(a.gamma, a.gamma_dtype, i, t, cols, gamma);
+      for (int i = 0; i < kNV; ++i) {
+        float gamma[8];
+        load_gamma<kTPR, kVec>(a.gamma, a.gamma_dtype, i, t, cols, gamma);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          if (r + u * step >= a.rows) break;
+          float n[8], g[8], d[8];
           h[u][i].get(n);
           dy[u][i].get(g);
           if (a.dh) {
@@ -564,8 +566,8 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
             for (int j = 0; j < 8; ++j) d[j] = 0.f;
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) d[j] += rstd[u] * (g[j] * gamma[j] - n[j] * rstd[u] * mean);
-          store_group<kTPR, kVec>(dx, i, t, cols, d);
+          for (int j = 0; j < 8; ++j) d[j] += rstd[u] * (g[j] * gamma[j]) + back[u] * n[j];
+          store_group<kTPR, kVec>(static_cast<T*>(a.dx) + (r + u * step) * a.dx_ld, i, t, cols, d);
         }
       }
     }
@@ -637,8 +639,8 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_grad_long_kernel(const _
 }
 
 // dgamma (+)= the partial sums, in a fixed order: a CTA takes 32 columns, its
-// 32 warps every 32nd partial row (all of a warp's loads in flight together),
-// and the warps' sums are added in order.
+// 32 warps every 32nd partial row, ten loads in flight together, and the warps'
+// sums are added in order.
 __global__ void __launch_bounds__(1024)
 dgamma_kernel(const float* partial, int n_partial, int64_t cols, float* dgamma, int accumulate) {
   __shared__ float sums[32][32];
@@ -648,8 +650,17 @@ dgamma_kernel(const float* partial, int n_partial, int64_t cols, float* dgamma, 
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float s = 0.f;
   if (c < cols) {
-#pragma unroll 20
-    for (int p = warp; p < n_partial; p += 32) s += partial[static_cast<int64_t>(p) * cols + c];
+    constexpr int kBatch = 10;
+    for (int p0 = warp; p0 < n_partial; p0 += 32 * kBatch) {
+      float v[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int p = p0 + 32 * j;
+        v[j] = p < n_partial ? partial[static_cast<int64_t>(p) * cols + c] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) s += v[j];
+    }
   }
   sums[warp][lane] = s;
   __syncthreads();
