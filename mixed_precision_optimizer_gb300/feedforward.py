@@ -140,11 +140,13 @@ def _mat(t, dtype, rows, cols, what):
     """(pointer, distance between rows) of a matrix argument; (0, 0) for None."""
     if t is None:
         return 0, 0
+    stride = t.stride()
+    if t.dtype is dtype and t.is_cuda and t.shape == (rows, cols) and stride[1] == 1:
+        return t.data_ptr(), stride[0]
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    stride = t.stride()
     if len(stride) != 2:
         t = t.view(_shape2(t, what))          # raises when the rows are not evenly spaced
         stride = t.stride()
@@ -159,13 +161,13 @@ def _vec(t, dtype, n, what):
     """Pointer of a dense vector argument; 0 for None."""
     if t is None:
         return 0
+    if t.dtype is dtype and t.is_cuda and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous with {n} elements")
-    return t.data_ptr()
+    raise ValueError(f"{what} must be contiguous with {n} elements")
 
 
 def _workspace(ws):

@@ -521,3 +521,34 @@ def test_launches_are_named():
     torch.cuda.synchronize()
     names = {r["kernel"] for r in prof.records()}
     assert {"linear", "linear_repack", "linear_grad", "quantize_rows", "rmsnorm"} <= names
+
+
+def test_python_argument_checks():
+    """Shapes, layouts and types that do not fit raise before the library is
+    called; leading dimensions and vectors count as rows."""
+    x, w, ws = normal(1, (4, 6, 64)), normal(2, (32, 64)), mp.linear_workspace(24, 32, 64)
+    y = empty((4, 6, 32))
+    mp.linear(x, w, y, workspace=ws)
+    flat = empty((24, 32))
+    mp.linear(x.view(24, 64), w, flat, workspace=ws)
+    assert torch.equal(y.view(24, 32), flat)
+    one = empty((32,))
+    mp.linear(x[0, 0], w, one, workspace=ws)
+    assert torch.equal(one, flat[0])
+    with pytest.raises(ValueError, match="y has shape"):
+        mp.linear(x, w, empty((24, 31)), workspace=ws)
+    with pytest.raises(ValueError, match="contiguous rows"):
+        mp.linear(x.view(24, 64), normal(3, (64, 32)).t(), flat, workspace=ws)
+    with pytest.raises(TypeError, match="w must be"):
+        mp.linear(x, w.float(), y, workspace=ws)
+    with pytest.raises(ValueError, match="x_scale"):
+        mp.linear(x.to(torch.float8_e4m3fn), w.to(torch.float8_e4m3fn), y, x_scale=torch.ones(3, device="cuda"),
+                  w_scale=torch.ones(32, device="cuda"), workspace=ws)
+    with pytest.raises(RuntimeError):
+        mp.linear(x.transpose(0, 1), w, y, workspace=ws)          # rows that are not evenly spaced
+    with pytest.raises(mp.MpoptError, match="WORKSPACE"):
+        mp.linear(x, w, y)
+    with pytest.raises(mp.MpoptError, match="INVALID"):
+        mp.rmsnorm(x, torch.ones(64, device="cuda"), -1.0, y=empty((4, 6, 64)))
+    with pytest.raises(ValueError, match="dw has shape"):
+        mp.linear_backward(flat, x.view(24, 64), None, dw=empty((64, 32), torch.float32), workspace=ws)
