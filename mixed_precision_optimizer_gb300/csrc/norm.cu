@@ -76,14 +76,14 @@ __device__ __forceinline__ uint8_t e4m3(float v) { return __nv_cvt_float_to_fp8(
 // starts at column (i * kTPR + t) * 8, otherwise its element j is column
 // (i * 8 + j) * kTPR + t.
 template <int kTPR, bool kVec>
-__device__ __forceinline__ int64_t column(int i, int j, int t) {
-  return kVec ? (static_cast<int64_t>(i) * kTPR + t) * 8 + j : static_cast<int64_t>(i * 8 + j) * kTPR + t;
+__device__ __forceinline__ int column(int i, int j, int t) {
+  return kVec ? (i * kTPR + t) * 8 + j : (i * 8 + j) * kTPR + t;
 }
 
 template <int kTPR, bool kVec, typename T>
-__device__ __forceinline__ void load_group(const T* row, int i, int t, int64_t cols, float (&v)[8]) {
+__device__ __forceinline__ void load_group(const T* row, int i, int t, int cols, float (&v)[8]) {
   if constexpr (kVec) {
-    const int64_t c = column<kTPR, true>(i, 0, t);
+    const int c = column<kTPR, true>(i, 0, t);
     if (c < cols) {
       load8(row + c, v);
     } else {
@@ -93,21 +93,21 @@ __device__ __forceinline__ void load_group(const T* row, int i, int t, int64_t c
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int64_t c = column<kTPR, false>(i, j, t);
+      const int c = column<kTPR, false>(i, j, t);
       v[j] = c < cols ? load_elem(row + c) : 0.f;
     }
   }
 }
 
 template <int kTPR, bool kVec, typename T>
-__device__ __forceinline__ void store_group(T* row, int i, int t, int64_t cols, const float (&v)[8]) {
+__device__ __forceinline__ void store_group(T* row, int i, int t, int cols, const float (&v)[8]) {
   if constexpr (kVec) {
-    const int64_t c = column<kTPR, true>(i, 0, t);
+    const int c = column<kTPR, true>(i, 0, t);
     if (c < cols) store8(row + c, v);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int64_t c = column<kTPR, false>(i, j, t);
+      const int c = column<kTPR, false>(i, j, t);
       if (c < cols) store_elem(row + c, v[j]);
     }
   }
@@ -115,8 +115,8 @@ __device__ __forceinline__ void store_group(T* row, int i, int t, int64_t cols, 
 
 // A group times inv in e4m3, 8 bytes.
 template <int kTPR>
-__device__ __forceinline__ void store_e4m3(uint8_t* row, int i, int t, int64_t cols, const float (&v)[8], float inv) {
-  const int64_t c = column<kTPR, true>(i, 0, t);
+__device__ __forceinline__ void store_e4m3(uint8_t* row, int i, int t, int cols, const float (&v)[8], float inv) {
+  const int c = column<kTPR, true>(i, 0, t);
   if (c < cols)
     *reinterpret_cast<uint2*>(row + c) =
         make_uint2(e4m3x2(v[0] * inv, v[1] * inv) | (e4m3x2(v[2] * inv, v[3] * inv) << 16),
@@ -124,7 +124,7 @@ __device__ __forceinline__ void store_e4m3(uint8_t* row, int i, int t, int64_t c
 }
 
 template <int kTPR, bool kVec>
-__device__ __forceinline__ void load_gamma(const void* gamma, int dtype, int i, int t, int64_t cols, float (&v)[8]) {
+__device__ __forceinline__ void load_gamma(const void* gamma, int dtype, int i, int t, int cols, float (&v)[8]) {
   if (dtype == kBf16) load_group<kTPR, kVec>(static_cast<const __nv_bfloat16*>(gamma), i, t, cols, v);
   else load_group<kTPR, kVec>(static_cast<const float*>(gamma), i, t, cols, v);
 }
@@ -183,7 +183,7 @@ rmsnorm_kernel(const __grid_constant__ RmsnormArgs a) {
   const int t = threadIdx.x % kTPR;
   const int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kTPR;
   if (r >= a.rows) return;                       // kTPR == 32: whole warps; otherwise the grid is exact
-  const int64_t cols = a.cols;
+  const int cols = static_cast<int>(a.cols);       // kNormMaxCols at most
   float v[kNV][8];
   {
     const T* x = static_cast<const T*>(a.x) + r * a.x_ld;
@@ -247,7 +247,7 @@ rmsnorm_kernel(const __grid_constant__ RmsnormArgs a) {
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int64_t c = column<kTPR, false>(i, j, t);
+          const int c = column<kTPR, false>(i, j, t);
           if (c < cols) q[c] = e4m3(v[i][j] * inv);
         }
       }
@@ -265,13 +265,14 @@ __global__ void __launch_bounds__(kTPR) rmsnorm_packed_kernel(const __grid_const
   let_next_start();
   wait_for_predecessors();
   const int t = threadIdx.x;
-  const int64_t r = blockIdx.x, cols = a.cols;
+  const int64_t r = blockIdx.x;
+  const int cols = static_cast<int>(a.cols);       // kNormMaxCols at most
   uint4 raw[kNV];
   {
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + r * a.x_ld;
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-      const int64_t c = column<kTPR, true>(i, 0, t);
+      const int c = column<kTPR, true>(i, 0, t);
       raw[i] = c < cols ? *reinterpret_cast<const uint4*>(x + c) : make_uint4(0, 0, 0, 0);
     }
   }
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kTPR) rmsnorm_packed_kernel(const __grid_const
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < kNV; ++i) {
-    const int64_t c = column<kTPR, true>(i, 0, t);
+    const int c = column<kTPR, true>(i, 0, t);
     if (a.h && c < cols) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.h) + r * a.h_ld + c) = raw[i];
     float v[8];
     values(i, v);
@@ -384,9 +385,9 @@ struct Raw<__nv_bfloat16, true> {
 };
 
 template <int kTPR, bool kVec, typename T>
-__device__ __forceinline__ void load_raw(const T* row, int i, int t, int64_t cols, Raw<T, kVec>& r) {
+__device__ __forceinline__ void load_raw(const T* row, int i, int t, int cols, Raw<T, kVec>& r) {
   if constexpr (kVec && sizeof(T) == 2) {
-    const int64_t c = column<kTPR, true>(i, 0, t);
+    const int c = column<kTPR, true>(i, 0, t);
     r.w = c < cols ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
   } else {
     load_group<kTPR, kVec>(row, i, t, cols, r.v);
@@ -447,7 +448,7 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
   let_next_start();
   wait_for_predecessors();
   const int t = threadIdx.x % kTPR, sub = threadIdx.x / kTPR;
-  const int64_t cols = a.cols;
+  const int cols = static_cast<int>(a.cols);       // kNormMaxCols at most
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
   const float inv_cols = 1.f / static_cast<float>(cols);
   float part[kNV][8];
@@ -465,7 +466,7 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
       if (r < a.rows) {
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
-          const int64_t c = column<kTPR, true>(i, 0, t);
+          const int c = column<kTPR, true>(i, 0, t);
           if (c < cols) {
             uint4* q = p + (u * C::kPieces + i) * kThreads;
             copy16(q, static_cast<const T*>(a.h) + r * a.h_ld + c);
@@ -573,13 +574,13 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
     }
   }
   if (!a.dgamma) return;
-  float* out = a.partial + static_cast<int64_t>(blockIdx.x) * cols;
+  float* out = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols;
   if constexpr (kRows == 1) {
 #pragma unroll
     for (int i = 0; i < kNV; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int64_t c = column<kTPR, kVec>(i, j, t);
+        const int c = column<kTPR, kVec>(i, j, t);
         if (c < cols) out[c] = part[i][j];
       }
   } else {
@@ -593,7 +594,7 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
       for (int e = threadIdx.x; e < 8 * kTPR; e += kThreads) {
         float s = join[e];
         for (int w = 1; w < kRows; ++w) s += join[w * 8 * kTPR + e];
-        const int64_t c = column<kTPR, kVec>(i, e / kTPR, e % kTPR);
+        const int c = column<kTPR, kVec>(i, e / kTPR, e % kTPR);
         if (c < cols) out[c] = s;
       }
     }
