@@ -903,7 +903,7 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap dx_a, const __grid_consta
 // per 128-byte k-block, where two separate 128 x 256 tiles would stage 96 KB
 // between them) and receives the accumulators of its own 128 rows.  Two
 // accumulators let the epilogue of one tile overlap the main loop of the next.
-// 8192 x 14336 x 4096: 495 us alone, 1.94 PFLOP/s; in e4m3 277 us, 3.4 PFLOP/s;
+// 8192 x 14336 x 4096: 498 us alone, 1.93 PFLOP/s; in e4m3 281 us, 3.4 PFLOP/s;
 // back to back the power limit sets the clock (1.55 PFLOP/s in bf16).
 //   warp 0      TMA producer (both CTAs; bytes counted on the even CTA's barrier)
 //   warp 1      TMEM allocation; in the even CTA the MMA issuer
