@@ -272,6 +272,7 @@ struct RmsnormArgs {
   int dtype, gamma_dtype;
   float eps;
   int norm;        // 0: y = x, nothing is normalised (opt_quantize_rows)
+  int shift;       // set by the launch: see common_shift in norm.cu
 };
 cudaError_t launch_rmsnorm(const RmsnormArgs& a, cudaStream_t stream);
 
@@ -284,6 +285,7 @@ struct RmsnormGradArgs {
   float *dgamma, *partial;   // partial: [kNormPartialRows][cols]
   int64_t rows, cols, dy_ld, h_ld, dh_ld, dx_ld;
   int dtype, gamma_dtype, accumulate;
+  int shift, dx_grouped;     // set by the launch: the inputs' common_shift (norm.cu), and whether dx shares it
 };
 cudaError_t launch_rmsnorm_grad(const RmsnormGradArgs& a, cudaStream_t stream);
 

@@ -12,8 +12,12 @@
 // its outputs.  A row of up to 1024 columns belongs to one warp (no barrier,
 // eight rows to a CTA), a longer one to a CTA of 128 to 512 threads, up to
 // 16384 columns in registers; longer rows are kept in fp32 in shared memory.
-// Where every row starts on 16 bytes a thread moves 8 elements at a time,
-// otherwise single elements, neighbours in neighbouring lanes.
+// Where every row starts on 16 bytes a thread moves 8 elements at a time
+// (kVector).  Rows of an odd width start anywhere, but where all tensors' rows
+// start equally far past a multiple of 8 elements (dense ones do), the groups
+// of 8 begin at the row's first multiple of 8, and the up to 14 elements before
+// the first and after the last group go to one thread each (kShifted).  Otherwise single elements, neighbours in
+// neighbouring lanes (kSingle).
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -29,6 +33,8 @@ constexpr float kE4m3Max = 448.f;
 constexpr float kAmaxFloor = 1e-30f;
 constexpr int kLongThreads = 512;             // rows longer than the register kernels take
 constexpr int64_t kRegisterCols = 16384;
+
+enum Access : int { kSingle = 0, kVector = 1, kShifted = 2 };
 
 // ------------------------------------------------------------- elements --
 
@@ -72,19 +78,39 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 }
 __device__ __forceinline__ uint8_t e4m3(float v) { return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3); }
 
-// A thread's share of a row: kNV groups of 8 columns.  With kVec group i
-// starts at column (i * kTPR + t) * 8, otherwise its element j is column
-// (i * 8 + j) * kTPR + t.
-template <int kTPR, bool kVec>
-__device__ __forceinline__ int column(int i, int j, int t) {
-  return kVec ? (i * kTPR + t) * 8 + j : (i * 8 + j) * kTPR + t;
+// A thread's share of a row: kNV groups of 8 columns.  With kSingle element j
+// of group i is column (i * 8 + j) * kTPR + t.  Otherwise the group starts at
+// column first + (i * kTPR + t) * 8 and there are groups up to column `end`: 0 and
+// the width with kVector; with kShifted `first` is where the row has its first
+// multiple of 8 elements, `end` where no whole group is left, and `edge` the
+// column outside of them that this thread takes (-1: none).
+struct Share {
+  int first, end, edge;
+};
+
+template <int kAccess>
+__device__ __forceinline__ Share share_of(int64_t start, int cols, int t) {
+  Share s{0, cols, -1};
+  if constexpr (kAccess == kShifted) {
+    const int head = static_cast<int>(-start & 7);
+    s.first = head < cols ? head : cols;
+    s.end = s.first + ((cols - s.first) & ~7);
+    const int e = t < 8 ? t : s.end + t - 8;
+    if (t < 8 ? e < s.first : t < 16 && e < cols) s.edge = e;
+  }
+  return s;
 }
 
-template <int kTPR, bool kVec, typename T>
-__device__ __forceinline__ void load_group(const T* row, int i, int t, int cols, float (&v)[8]) {
-  if constexpr (kVec) {
-    const int c = column<kTPR, true>(i, 0, t);
-    if (c < cols) {
+template <int kTPR, int kAccess>
+__device__ __forceinline__ int column(const Share& s, int i, int j, int t) {
+  return kAccess == kSingle ? (i * 8 + j) * kTPR + t : s.first + (i * kTPR + t) * 8 + j;
+}
+
+template <int kTPR, int kAccess, typename T>
+__device__ __forceinline__ void load_group(const T* row, const Share& s, int i, int t, float (&v)[8]) {
+  if constexpr (kAccess != kSingle) {
+    const int c = column<kTPR, kAccess>(s, i, 0, t);
+    if (c < s.end) {
       load8(row + c, v);
     } else {
 #pragma unroll
@@ -93,40 +119,109 @@ __device__ __forceinline__ void load_group(const T* row, int i, int t, int cols,
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int c = column<kTPR, false>(i, j, t);
-      v[j] = c < cols ? load_elem(row + c) : 0.f;
+      const int c = column<kTPR, kAccess>(s, i, j, t);
+      v[j] = c < s.end ? load_elem(row + c) : 0.f;
     }
   }
 }
 
-template <int kTPR, bool kVec, typename T>
-__device__ __forceinline__ void store_group(T* row, int i, int t, int cols, const float (&v)[8]) {
-  if constexpr (kVec) {
-    const int c = column<kTPR, true>(i, 0, t);
-    if (c < cols) store8(row + c, v);
-  } else {
+template <int kTPR, int kAccess, typename T>
+__device__ __forceinline__ void store_group(T* row, const Share& s, int i, int t, const float (&v)[8]) {
+  if constexpr (kAccess == kSingle) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int c = column<kTPR, false>(i, j, t);
-      if (c < cols) store_elem(row + c, v[j]);
+      const int c = column<kTPR, kAccess>(s, i, j, t);
+      if (c < s.end) store_elem(row + c, v[j]);
     }
+  } else {
+    const int c = column<kTPR, kAccess>(s, i, 0, t);
+    if (c < s.end) store8(row + c, v);
   }
+}
+
+// The same with kShifted for an output whose groups do not start on 16 bytes:
+// a warp's groups go through shared memory (256 floats a warp), so that
+// neighbouring lanes store neighbouring columns.  The whole warp calls.
+template <int kTPR, typename T>
+__device__ __forceinline__ void spread_group(T* row, const Share& s, int i, int t, const float (&v)[8], float* staging) {
+  const int lane = t & 31, base = column<kTPR, kShifted>(s, i, 0, t - lane);
+  float* mine = staging + (threadIdx.x >> 5) * 256;
+  reinterpret_cast<float4*>(mine)[lane] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(mine)[32 + lane] = make_float4(v[4], v[5], v[6], v[7]);
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int e = k * 32 + lane;                   // element e % 8 of lane e / 8
+    if (base + e < s.end) store_elem(row + base + e, mine[(e & 4) * 32 + (e / 8) * 4 + (e & 3)]);
+  }
+  __syncwarp();
 }
 
 // A group times inv in e4m3, 8 bytes.
-template <int kTPR>
-__device__ __forceinline__ void store_e4m3(uint8_t* row, int i, int t, int cols, const float (&v)[8], float inv) {
-  const int c = column<kTPR, true>(i, 0, t);
-  if (c < cols)
-    *reinterpret_cast<uint2*>(row + c) =
-        make_uint2(e4m3x2(v[0] * inv, v[1] * inv) | (e4m3x2(v[2] * inv, v[3] * inv) << 16),
-                   e4m3x2(v[4] * inv, v[5] * inv) | (e4m3x2(v[6] * inv, v[7] * inv) << 16));
+template <int kTPR, int kAccess>
+__device__ __forceinline__ void store_e4m3(uint8_t* row, const Share& s, int i, int t, const float (&v)[8], float inv) {
+  if constexpr (kAccess == kSingle) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = column<kTPR, kAccess>(s, i, j, t);
+      if (c < s.end) row[c] = e4m3(v[j] * inv);
+    }
+  } else {
+    const int c = column<kTPR, kAccess>(s, i, 0, t);
+    if (c < s.end)
+      *reinterpret_cast<uint2*>(row + c) =
+          make_uint2(e4m3x2(v[0] * inv, v[1] * inv) | (e4m3x2(v[2] * inv, v[3] * inv) << 16),
+                     e4m3x2(v[4] * inv, v[5] * inv) | (e4m3x2(v[6] * inv, v[7] * inv) << 16));
+  }
 }
 
-template <int kTPR, bool kVec>
-__device__ __forceinline__ void load_gamma(const void* gamma, int dtype, int i, int t, int cols, float (&v)[8]) {
-  if (dtype == kBf16) load_group<kTPR, kVec>(static_cast<const __nv_bfloat16*>(gamma), i, t, cols, v);
-  else load_group<kTPR, kVec>(static_cast<const float*>(gamma), i, t, cols, v);
+__device__ __forceinline__ float gamma_elem(const void* gamma, int dtype, int c) {
+  return dtype == kBf16 ? load_elem(static_cast<const __nv_bfloat16*>(gamma) + c) : static_cast<const float*>(gamma)[c];
+}
+
+// With kShifted gamma's groups do not start on 16 bytes: single elements.
+template <int kTPR, int kAccess, typename T>
+__device__ __forceinline__ void load_gamma_typed(const T* gamma, const Share& s, int i, int t, float (&v)[8]) {
+  if constexpr (kAccess == kShifted) {
+    const int c = column<kTPR, kAccess>(s, i, 0, t);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c < s.end ? load_elem(gamma + c + j) : 0.f;
+  } else {
+    load_group<kTPR, kAccess>(gamma, s, i, t, v);
+  }
+}
+template <int kTPR, int kAccess>
+__device__ __forceinline__ void load_gamma(const void* gamma, int dtype, const Share& s, int i, int t, float (&v)[8]) {
+  if (dtype == kBf16) load_gamma_typed<kTPR, kAccess>(static_cast<const __nv_bfloat16*>(gamma), s, i, t, v);
+  else load_gamma_typed<kTPR, kAccess>(static_cast<const float*>(gamma), s, i, t, v);
+}
+
+// A group of 8 elements as loaded (bf16 stays packed until it is used).
+template <typename T, int kAccess>
+struct Raw {
+  float v[8];
+  __device__ __forceinline__ void get(float (&out)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) out[j] = v[j];
+  }
+};
+struct PackedRaw {
+  uint4 w;
+  __device__ __forceinline__ void get(float (&out)[8]) const { unpack8(w, out); }
+};
+template <>
+struct Raw<__nv_bfloat16, kVector> : PackedRaw {};
+template <>
+struct Raw<__nv_bfloat16, kShifted> : PackedRaw {};
+
+template <int kTPR, int kAccess, typename T>
+__device__ __forceinline__ void load_raw(const T* row, const Share& s, int i, int t, Raw<T, kAccess>& r) {
+  if constexpr (kAccess != kSingle && sizeof(T) == 2) {
+    const int c = column<kTPR, kAccess>(s, i, 0, t);
+    r.w = c < s.end ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
+  } else {
+    load_group<kTPR, kAccess>(row, s, i, t, r.v);
+  }
 }
 
 // Sum or maximum over the kTPR threads of a row, the same value in each, in a
@@ -172,7 +267,7 @@ __device__ __forceinline__ void rows_reduce(float (&v)[kU], float (*vals)[kTPR /
 // -------------------------------------------------------------- forward --
 
 // One row per group of kTPR threads.
-template <typename T, int kTPR, int kNV, bool kVec>
+template <typename T, int kTPR, int kNV, int kAccess>
 __global__ void __launch_bounds__(kTPR == 32 ? 256 : kTPR)
 rmsnorm_kernel(const __grid_constant__ RmsnormArgs a) {
   constexpr int kThreads = kTPR == 32 ? 256 : kTPR;
@@ -184,29 +279,35 @@ rmsnorm_kernel(const __grid_constant__ RmsnormArgs a) {
   const int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kTPR;
   if (r >= a.rows) return;                       // kTPR == 32: whole warps; otherwise the grid is exact
   const int cols = static_cast<int>(a.cols);       // kNormMaxCols at most
-  float v[kNV][8];
+  const Share s = share_of<kAccess>(a.shift + r * a.x_ld, cols, t);
+  const bool edge = kAccess == kShifted && s.edge >= 0;
+  float v[kNV][8], ve = 0.f;
   {
     const T* x = static_cast<const T*>(a.x) + r * a.x_ld;
 #pragma unroll
-    for (int i = 0; i < kNV; ++i) load_group<kTPR, kVec>(x, i, t, cols, v[i]);
+    for (int i = 0; i < kNV; ++i) load_group<kTPR, kAccess>(x, s, i, t, v[i]);
+    if (edge) ve = load_elem(x + s.edge);
   }
   if (a.residual) {
     const T* p = static_cast<const T*>(a.residual) + r * a.residual_ld;
-    float w[kNV][8];
+    float w[kNV][8], we = 0.f;
 #pragma unroll
-    for (int i = 0; i < kNV; ++i) load_group<kTPR, kVec>(p, i, t, cols, w[i]);
+    for (int i = 0; i < kNV; ++i) load_group<kTPR, kAccess>(p, s, i, t, w[i]);
+    if (edge) we = load_elem(p + s.edge);
 #pragma unroll
     for (int i = 0; i < kNV; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] += w[i][j];
+    ve += we;
   }
   if (a.h) {
     T* h = static_cast<T*>(a.h) + r * a.h_ld;
 #pragma unroll
-    for (int i = 0; i < kNV; ++i) store_group<kTPR, kVec>(h, i, t, cols, v[i]);
+    for (int i = 0; i < kNV; ++i) store_group<kTPR, kAccess>(h, s, i, t, v[i]);
+    if (edge) store_elem(h + s.edge, ve);
   }
   if (a.norm) {
-    float ss = 0.f;
+    float ss = ve * ve;
 #pragma unroll
     for (int i = 0; i < kNV; ++i)
 #pragma unroll
@@ -217,18 +318,20 @@ rmsnorm_kernel(const __grid_constant__ RmsnormArgs a) {
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
       float g[8];
-      load_gamma<kTPR, kVec>(a.gamma, a.gamma_dtype, i, t, cols, g);
+      load_gamma<kTPR, kAccess>(a.gamma, a.gamma_dtype, s, i, t, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * g[j];
     }
+    if (edge) ve = ve * rstd * gamma_elem(a.gamma, a.gamma_dtype, s.edge);
   }
   if (a.y) {
     __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(a.y) + r * a.y_ld;
 #pragma unroll
-    for (int i = 0; i < kNV; ++i) store_group<kTPR, kVec>(y, i, t, cols, v[i]);
+    for (int i = 0; i < kNV; ++i) store_group<kTPR, kAccess>(y, s, i, t, v[i]);
+    if (edge) store_elem(y + s.edge, ve);
   }
   if (a.q) {
-    float amax = 0.f;
+    float amax = fabsf(ve);
 #pragma unroll
     for (int i = 0; i < kNV; ++i)
 #pragma unroll
@@ -241,17 +344,8 @@ rmsnorm_kernel(const __grid_constant__ RmsnormArgs a) {
     const float inv = 1.f / scale;
     uint8_t* q = a.q + r * a.q_ld;
 #pragma unroll
-    for (int i = 0; i < kNV; ++i) {
-      if constexpr (kVec) {
-        store_e4m3<kTPR>(q, i, t, cols, v[i], inv);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int c = column<kTPR, false>(i, j, t);
-          if (c < cols) q[c] = e4m3(v[i][j] * inv);
-        }
-      }
-    }
+    for (int i = 0; i < kNV; ++i) store_e4m3<kTPR, kAccess>(q, s, i, t, v[i], inv);
+    if (edge) q[s.edge] = e4m3(ve * inv);
   }
 }
 
@@ -267,12 +361,13 @@ __global__ void __launch_bounds__(kTPR) rmsnorm_packed_kernel(const __grid_const
   const int t = threadIdx.x;
   const int64_t r = blockIdx.x;
   const int cols = static_cast<int>(a.cols);       // kNormMaxCols at most
+  const Share s = share_of<kVector>(0, cols, t);
   uint4 raw[kNV];
   {
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + r * a.x_ld;
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-      const int c = column<kTPR, true>(i, 0, t);
+      const int c = column<kTPR, kVector>(s, i, 0, t);
       raw[i] = c < cols ? *reinterpret_cast<const uint4*>(x + c) : make_uint4(0, 0, 0, 0);
     }
   }
@@ -294,7 +389,7 @@ __global__ void __launch_bounds__(kTPR) rmsnorm_packed_kernel(const __grid_const
     unpack8(raw[i], v);
     if (a.norm) {
       float g[8];
-      load_gamma<kTPR, true>(a.gamma, a.gamma_dtype, i, t, cols, g);
+      load_gamma<kTPR, kVector>(a.gamma, a.gamma_dtype, s, i, t, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = v[j] * rstd * g[j];
     }
@@ -302,11 +397,11 @@ __global__ void __launch_bounds__(kTPR) rmsnorm_packed_kernel(const __grid_const
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < kNV; ++i) {
-    const int c = column<kTPR, true>(i, 0, t);
+    const int c = column<kTPR, kVector>(s, i, 0, t);
     if (a.h && c < cols) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.h) + r * a.h_ld + c) = raw[i];
     float v[8];
     values(i, v);
-    if (a.y) store_group<kTPR, true>(reinterpret_cast<__nv_bfloat16*>(a.y) + r * a.y_ld, i, t, cols, v);
+    if (a.y) store_group<kTPR, kVector>(reinterpret_cast<__nv_bfloat16*>(a.y) + r * a.y_ld, s, i, t, v);
     // columns past the end hold zeros times rstd, which may be NaN: fmaxf drops it
 #pragma unroll
     for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
@@ -319,7 +414,7 @@ __global__ void __launch_bounds__(kTPR) rmsnorm_packed_kernel(const __grid_const
     for (int i = 0; i < kNV; ++i) {
       float v[8];
       values(i, v);
-      store_e4m3<kTPR>(a.q + r * a.q_ld, i, t, cols, v, inv);
+      store_e4m3<kTPR, kVector>(a.q + r * a.q_ld, s, i, t, v, inv);
     }
   }
 }
@@ -369,31 +464,6 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_long_kernel(const __grid
 
 // ------------------------------------------------------------- gradient --
 
-// A group of 8 elements as loaded (bf16 stays packed until it is used).
-template <typename T, bool kVec>
-struct Raw {
-  float v[8];
-  __device__ __forceinline__ void get(float (&out)[8]) const {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) out[j] = v[j];
-  }
-};
-template <>
-struct Raw<__nv_bfloat16, true> {
-  uint4 w;
-  __device__ __forceinline__ void get(float (&out)[8]) const { unpack8(w, out); }
-};
-
-template <int kTPR, bool kVec, typename T>
-__device__ __forceinline__ void load_raw(const T* row, int i, int t, int cols, Raw<T, kVec>& r) {
-  if constexpr (kVec && sizeof(T) == 2) {
-    const int c = column<kTPR, true>(i, 0, t);
-    r.w = c < cols ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
-  } else {
-    load_group<kTPR, kVec>(row, i, t, cols, r.v);
-  }
-}
-
 // The gradient walks over many rows per CTA with a barrier in each, so it lives
 // from rows that are independent of one another.  bf16 at 16 columns a thread:
 // kU = 2 rows at a time share a barrier, and the loads run ahead of them in a
@@ -401,25 +471,34 @@ __device__ __forceinline__ void load_raw(const T* row, int i, int t, int cols, R
 // itself use into its own places in shared memory, with cp.async: no registers,
 // no barrier).  The other forms load a row into registers, with as many CTAs to
 // an SM as that leaves; fp32, twice the bytes for the same work, reaches 6.1
-// TB/s so, and a ring of the two rows that fit took it down to 4.5.
-template <typename T, int kTPR, int kNV, bool kVec>
+// TB/s so, and a ring of the two rows that fit took it down to 4.5.  With
+// kShifted a thread's gamma lies in fp32 in its own places in shared memory,
+// since its groups do not start on 16 bytes of gamma, and the rows' edges take
+// registers: 80 a thread (8192 x 2545 in bf16: 49 us, with 64 or 128 55 and 58;
+// in bf16 two CTAs of 512 need 64: 4096 x 4097 53 us, one CTA 69),
+// for a warp's row of two groups 128 (8192 x 505: 12.3 us, with 80 18.2), and
+// rows of 513 to 1024 columns take 128 threads instead of a warp (5000 x 1023:
+// 21 us against 23, in fp32 26 against 32).  Single elements took 149 us for
+// 8192 x 2545.
+template <typename T, int kTPR, int kNV, int kAccess>
 struct GradConfig {
   static constexpr int kThreads = kTPR == 32 ? 256 : kTPR;
-  static constexpr bool kRing = kVec && sizeof(T) == 2 && kNV == 2;
+  static constexpr bool kRing = kAccess == kVector && sizeof(T) == 2 && kNV == 2;
   static constexpr int kU = kRing ? 2 : 1;
   static constexpr int kPieces = 3 * kNV;                                  // of a row: h, dh, dy
   static constexpr int kStageBytes = kU * kPieces * kThreads * 16;
   // CTAs to an SM: without the ring registers for 64 (bf16) or 80 (fp32) a
   // thread at 16 columns each, half as many CTAs at 32
   static constexpr int plain_ctas() {
-    if (!kVec || kNV > 2) return kTPR == 32 && kNV > 2 ? 2 : 1;
-    const int n = (sizeof(T) == 2 ? 1024 : 768) / kThreads;
+    if (kAccess == kSingle || kNV > 2) return kTPR == 32 && kNV > 2 ? 2 : 1;
+    if (kAccess == kShifted && kTPR == 32 && kNV == 2) return 2;
+    const int n = (sizeof(T) == 2 && (kAccess != kShifted || kThreads == 512) ? 1024 : 768) / kThreads;
     return n < 1 ? 1 : n;
   }
   static constexpr int kCtas = kRing ? 512 / kThreads : plain_ctas();
   static constexpr int kStages = kRing ? (216 * 1024) / kCtas / kStageBytes : 0;
   static_assert(!kRing || kStages >= 2, "the ring holds the rows in use and the ones on their way");
-  static constexpr int kBytes = kStages * kStageBytes;
+  static constexpr int kBytes = kAccess == kShifted ? kThreads * (kNV + 1) * 32 : kStages * kStageBytes;
 };
 
 __device__ __forceinline__ void copy16(uint4* dst, const void* src) {
@@ -433,25 +512,30 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
-// CTA b takes rows b, b + gridDim.x, ... (a row to a warp where kTPR is 32); a
-// thread's columns stay the same, so its part of dgamma stays in registers, and
-// the CTA writes its partial sums once.
-template <typename T, int kTPR, int kNV, bool kVec>
-__global__ void __launch_bounds__(kTPR == 32 ? 256 : kTPR, (GradConfig<T, kTPR, kNV, kVec>::kCtas))
+// CTA b takes rows b, b + gridDim.x, ... (a row to a warp where kTPR is 32, with
+// kSingle and kVector rows next to one another); a thread's columns stay the
+// same, so its part of dgamma stays in registers, and the CTA writes its partial
+// sums once.  With kShifted gridDim.x is a multiple of 8 (or the number of rows),
+// which gives all rows of a CTA one shift.
+template <typename T, int kTPR, int kNV, int kAccess>
+__global__ void __launch_bounds__(kTPR == 32 ? 256 : kTPR, (GradConfig<T, kTPR, kNV, kAccess>::kCtas))
 rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
-  using C = GradConfig<T, kTPR, kNV, kVec>;
+  using C = GradConfig<T, kTPR, kNV, kAccess>;
   constexpr int kThreads = C::kThreads, kU = C::kU;
   constexpr int kRows = kThreads / kTPR;
-  extern __shared__ uint4 ring[];              // [kStages][kU][kPieces][kThreads]
+  extern __shared__ uint4 ring[];              // [kStages][kU][kPieces][kThreads]; 
+                                               // kShifted: gamma, [kNV][2][kThreads], and the warps' staging
   __shared__ float vals[2][kU][kTPR / 32];
   __shared__ float join[kRows > 1 ? kRows * kTPR * 8 : 1];
   let_next_start();
   wait_for_predecessors();
   const int t = threadIdx.x % kTPR, sub = threadIdx.x / kTPR;
   const int cols = static_cast<int>(a.cols);       // kNormMaxCols at most
+  const Share s = share_of<kAccess>(a.shift + blockIdx.x * a.h_ld, cols, t);
+  const bool edge = kAccess == kShifted && s.edge >= 0;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
   const float inv_cols = 1.f / static_cast<float>(cols);
-  float part[kNV][8];
+  float part[kNV][8], part_e = 0.f;
 #pragma unroll
   for (int i = 0; i < kNV; ++i)
 #pragma unroll
@@ -459,14 +543,14 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
 
   // this thread's pieces of rows r, r + step into stage s; a commit in any
   // case, so that the count of groups is that of stages
-  auto fetch = [&](int64_t r, int s) {
-    uint4* p = ring + static_cast<size_t>(s) * (kU * C::kPieces * kThreads) + threadIdx.x;
+  auto fetch = [&](int64_t r, int at) {
+    uint4* p = ring + static_cast<size_t>(at) * (kU * C::kPieces * kThreads) + threadIdx.x;
 #pragma unroll
     for (int u = 0; u < kU; ++u, r += step)
       if (r < a.rows) {
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
-          const int c = column<kTPR, true>(i, 0, t);
+          const int c = column<kTPR, kVector>(s, i, 0, t);
           if (c < cols) {
             uint4* q = p + (u * C::kPieces + i) * kThreads;
             copy16(q, static_cast<const T*>(a.h) + r * a.h_ld + c);
@@ -477,15 +561,37 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
       }
     copy_commit();
   };
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows + sub;
+  const int64_t r0 = kAccess == kShifted ? blockIdx.x + static_cast<int64_t>(sub) * gridDim.x
+                                         : static_cast<int64_t>(blockIdx.x) * kRows + sub;
+  float4* own_gamma = reinterpret_cast<float4*>(ring) + threadIdx.x;
+  if constexpr (kAccess == kShifted) {
+    if (r0 < a.rows) {
+#pragma unroll
+      for (int i = 0; i < kNV; ++i) {
+        float g[8];
+        load_gamma<kTPR, kAccess>(a.gamma, a.gamma_dtype, s, i, t, g);
+        own_gamma[(2 * i) * kThreads] = make_float4(g[0], g[1], g[2], g[3]);
+        own_gamma[(2 * i + 1) * kThreads] = make_float4(g[4], g[5], g[6], g[7]);
+      }
+    }
+  }
+  const float gamma_e = edge ? gamma_elem(a.gamma, a.gamma_dtype, s.edge) : 0.f;
+  auto gamma_group = [&](int i, float (&g)[8]) {
+    if constexpr (kAccess == kShifted) {
+      const float4 p = own_gamma[(2 * i) * kThreads], q = own_gamma[(2 * i + 1) * kThreads];
+      g[0] = p.x, g[1] = p.y, g[2] = p.z, g[3] = p.w, g[4] = q.x, g[5] = q.y, g[6] = q.z, g[7] = q.w;
+    } else {
+      load_gamma<kTPR, kAccess>(a.gamma, a.gamma_dtype, s, i, t, g);
+    }
+  };
   if constexpr (C::kRing) {
-    for (int s = 0; s < C::kStages - 1; ++s) fetch(r0 + s * kU * step, s);
+    for (int at = 0; at < C::kStages - 1; ++at) fetch(r0 + at * kU * step, at);
   }
   int parity = 0, stage = 0;
   for (int64_t r = r0; r < a.rows; r += kU * step, parity ^= 1) {
-    Raw<T, kVec> h[kU][kNV], dh[kU][kNV];
-    Raw<__nv_bfloat16, kVec> dy[kU][kNV];
-    float rstd[kU], dot[kU];
+    Raw<T, kAccess> h[kU][kNV], dh[kU][kNV];
+    Raw<__nv_bfloat16, kAccess> dy[kU][kNV];
+    float rstd[kU], dot[kU], he = 0.f, dhe = 0.f, dye = 0.f;      // kShifted has kU = 1
     if constexpr (C::kRing) {
       copy_wait<C::kStages - 2>();
       const uint4* p = ring + static_cast<size_t>(stage) * (kU * C::kPieces * kThreads) + threadIdx.x;
@@ -494,7 +600,7 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
         const bool row = r + u * step < a.rows;
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
-          const bool in = row && column<kTPR, true>(i, 0, t) < cols;       // nothing was copied for the others
+          const bool in = row && column<kTPR, kVector>(s, i, 0, t) < cols;       // nothing was copied for the others
           const uint4* q = p + (u * C::kPieces + i) * kThreads;
           const uint4 zero = make_uint4(0, 0, 0, 0);
           h[u][i].w = in ? q[0] : zero;
@@ -507,13 +613,18 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
       const __nv_bfloat16* yp = reinterpret_cast<const __nv_bfloat16*>(a.dy) + r * a.dy_ld;
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
-        load_raw<kTPR, kVec>(hp, i, t, cols, h[0][i]);
-        load_raw<kTPR, kVec>(yp, i, t, cols, dy[0][i]);
+        load_raw<kTPR, kAccess>(hp, s, i, t, h[0][i]);
+        load_raw<kTPR, kAccess>(yp, s, i, t, dy[0][i]);
+      }
+      if (edge) {
+        he = load_elem(hp + s.edge);
+        dye = load_elem(yp + s.edge);
+        if (a.dh) dhe = load_elem(static_cast<const T*>(a.dh) + r * a.dh_ld + s.edge);
       }
       if (a.dh) {
         const T* sp = static_cast<const T*>(a.dh) + r * a.dh_ld;
 #pragma unroll
-        for (int i = 0; i < kNV; ++i) load_raw<kTPR, kVec>(sp, i, t, cols, dh[0][i]);
+        for (int i = 0; i < kNV; ++i) load_raw<kTPR, kAccess>(sp, s, i, t, dh[0][i]);
       }
     }
 #pragma unroll
@@ -524,7 +635,7 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
       float gamma[8];
-      load_gamma<kTPR, kVec>(a.gamma, a.gamma_dtype, i, t, cols, gamma);
+      gamma_group(i, gamma);
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         float n[8], g[8];
@@ -537,6 +648,11 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
           dot[u] += p * gamma[j];
         }
       }
+    }
+    if constexpr (kAccess == kShifted) {
+      const float p = dye * he;
+      part_e += p * rstd[0];
+      dot[0] += p * gamma_e;
     }
     if constexpr (C::kRing) {
       // the stage read one turn ago (its values are in use by now) takes the rows kStages - 1 turns ahead
@@ -553,10 +669,10 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
         float gamma[8];
-        load_gamma<kTPR, kVec>(a.gamma, a.gamma_dtype, i, t, cols, gamma);
+        gamma_group(i, gamma);
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-          if (r + u * step >= a.rows) break;
+          if (r + u * step >= a.rows) break;     // the same for a warp
           float n[8], g[8], d[8];
           h[u][i].get(n);
           dy[u][i].get(g);
@@ -568,9 +684,15 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j) d[j] += rstd[u] * (g[j] * gamma[j]) + back[u] * n[j];
-          store_group<kTPR, kVec>(static_cast<T*>(a.dx) + (r + u * step) * a.dx_ld, i, t, cols, d);
+          T* dx = static_cast<T*>(a.dx) + (r + u * step) * a.dx_ld;
+          if (kAccess == kShifted && !a.dx_grouped)
+            spread_group<kTPR>(dx, s, i, t, d, reinterpret_cast<float*>(ring + 2 * kNV * kThreads));
+          else
+            store_group<kTPR, kAccess>(dx, s, i, t, d);
         }
       }
+      if (edge)
+        store_elem(static_cast<T*>(a.dx) + r * a.dx_ld + s.edge, dhe + (rstd[0] * (dye * gamma_e) + back[0] * he));
     }
   }
   if (!a.dgamma) return;
@@ -580,9 +702,10 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
     for (int i = 0; i < kNV; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int c = column<kTPR, kVec>(i, j, t);
-        if (c < cols) out[c] = part[i][j];
+        const int c = column<kTPR, kAccess>(s, i, j, t);
+        if (c < s.end) out[c] = part[i][j];
       }
+    if (edge) out[s.edge] = part_e;
   } else {
     // the warps' sums of 8 * kTPR columns at a time, added in order
 #pragma unroll
@@ -592,10 +715,20 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
       for (int j = 0; j < 8; ++j) join[(sub * 8 + j) * kTPR + t] = part[i][j];
       __syncthreads();
       for (int e = threadIdx.x; e < 8 * kTPR; e += kThreads) {
-        float s = join[e];
-        for (int w = 1; w < kRows; ++w) s += join[w * 8 * kTPR + e];
-        const int c = column<kTPR, kVec>(i, e / kTPR, e % kTPR);
-        if (c < cols) out[c] = s;
+        float sum = join[e];
+        for (int w = 1; w < kRows; ++w) sum += join[w * 8 * kTPR + e];
+        const int c = column<kTPR, kAccess>(s, i, e / kTPR, e % kTPR);
+        if (c < s.end) out[c] = sum;
+      }
+    }
+    if constexpr (kAccess == kShifted) {
+      __syncthreads();
+      join[sub * kTPR + t] = part_e;
+      __syncthreads();
+      if (sub == 0 && edge) {
+        float sum = part_e;
+        for (int w = 1; w < kRows; ++w) sum += join[w * kTPR + t];
+        out[s.edge] = sum;
       }
     }
   }
@@ -678,6 +811,27 @@ bool aligned(const void* p, int64_t ld, int64_t rows, int es, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) % bytes) == 0 && (rows <= 1 || (ld * es) % bytes == 0);
 }
 
+// How far past a multiple of 8 elements the first rows of all given tensors
+// start, if it is the same for all and stays so from row to row; otherwise -1.
+// The first one is always given.
+struct RowTensor {
+  const void* p;
+  int64_t ld;
+  int es;
+};
+template <int kN>
+int common_shift(const RowTensor (&tensors)[kN], int64_t rows) {
+  int shift = -1;
+  int64_t ld = 0;
+  for (const RowTensor& x : tensors) {
+    if (!x.p) continue;
+    const int own = static_cast<int>((reinterpret_cast<uintptr_t>(x.p) / x.es) & 7);
+    if (shift >= 0 && (own != shift || (rows > 1 && ((x.ld - ld) & 7) != 0))) return -1;
+    shift = own, ld = x.ld;
+  }
+  return shift;
+}
+
 // Raises a kernel's shared-memory limit once per thread and device.
 template <auto kKernel>
 cudaError_t allow_smem(int bytes) {
@@ -691,16 +845,18 @@ cudaError_t allow_smem(int bytes) {
 }
 
 template <typename T, int kTPR, int kNV>
-cudaError_t forward_config(const RmsnormArgs& a, bool vec, cudaStream_t stream) {
+cudaError_t forward_config(const RmsnormArgs& a, Access access, cudaStream_t stream) {
   constexpr int kThreads = kTPR == 32 ? 256 : kTPR;
   constexpr int kRows = kThreads / kTPR;
   const unsigned grid = static_cast<unsigned>((a.rows + kRows - 1) / kRows);
-  return launch_overlapped(vec ? rmsnorm_kernel<T, kTPR, kNV, true> : rmsnorm_kernel<T, kTPR, kNV, false>, grid, kThreads,
-                           0, stream, 0, a);
+  return launch_overlapped(access == kVector    ? rmsnorm_kernel<T, kTPR, kNV, kVector>
+                           : access == kShifted ? rmsnorm_kernel<T, kTPR, kNV, kShifted>
+                                                : rmsnorm_kernel<T, kTPR, kNV, kSingle>,
+                           grid, kThreads, 0, stream, 0, a);
 }
 
 template <typename T>
-cudaError_t forward_typed(const RmsnormArgs& a, cudaStream_t stream) {
+cudaError_t forward_typed(RmsnormArgs a, cudaStream_t stream) {
   const int es = static_cast<int>(sizeof(T));
   const bool vec = a.cols % 8 == 0 && aligned(a.x, a.x_ld, a.rows, es, 16) &&
                    aligned(a.residual, a.residual_ld, a.residual ? a.rows : 1, es, 16) &&
@@ -715,13 +871,19 @@ cudaError_t forward_typed(const RmsnormArgs& a, cudaStream_t stream) {
       return launch_overlapped(rmsnorm_packed_kernel<512, 4>, grid, 512, 0, stream, 0, a);
     }
   }
-  if (a.cols <= 256) return forward_config<T, 32, 1>(a, vec, stream);
-  if (a.cols <= 512) return forward_config<T, 32, 2>(a, vec, stream);
-  if (a.cols <= 1024) return forward_config<T, 32, 4>(a, vec, stream);
-  if (a.cols <= 2048) return forward_config<T, 128, 2>(a, vec, stream);
-  if (a.cols <= 4096) return forward_config<T, 256, 2>(a, vec, stream);
-  if (a.cols <= 8192) return forward_config<T, 512, 2>(a, vec, stream);
-  if (a.cols <= kRegisterCols) return forward_config<T, 512, 4>(a, vec, stream);
+  Access access = vec ? kVector : kSingle;
+  if (!vec && a.cols <= kRegisterCols) {
+    a.shift = common_shift({{a.x, a.x_ld, es}, {a.residual, a.residual_ld, es}, {a.h, a.h_ld, es},
+                            {a.y, a.y_ld, 2}, {a.q, a.q_ld, 1}}, a.rows);
+    if (a.shift >= 0) access = kShifted;
+  }
+  if (a.cols <= 256) return forward_config<T, 32, 1>(a, access, stream);
+  if (a.cols <= 512) return forward_config<T, 32, 2>(a, access, stream);
+  if (a.cols <= 1024) return forward_config<T, 32, 4>(a, access, stream);
+  if (a.cols <= 2048) return forward_config<T, 128, 2>(a, access, stream);
+  if (a.cols <= 4096) return forward_config<T, 256, 2>(a, access, stream);
+  if (a.cols <= 8192) return forward_config<T, 512, 2>(a, access, stream);
+  if (a.cols <= kRegisterCols) return forward_config<T, 512, 4>(a, access, stream);
   const cudaError_t e = allow_smem<rmsnorm_long_kernel<T>>(static_cast<int>(kNormMaxCols * sizeof(float)));
   if (e != cudaSuccess) return e;
   return launch_overlapped(rmsnorm_long_kernel<T>, static_cast<unsigned>(a.rows), kLongThreads, a.cols * sizeof(float),
@@ -744,40 +906,61 @@ int resident_ctas(int threads, int smem) {
   return cached;
 }
 
-template <typename T, int kTPR, int kNV, bool kVec>
+template <typename T, int kTPR, int kNV, int kAccess>
 cudaError_t grad_launch(const RmsnormGradArgs& a, int* grid, cudaStream_t stream) {
   constexpr int kThreads = kTPR == 32 ? 256 : kTPR;
   constexpr int kRows = kThreads / kTPR;
-  constexpr int kSmem = GradConfig<T, kTPR, kNV, kVec>::kBytes;
+  constexpr int kSmem = GradConfig<T, kTPR, kNV, kAccess>::kBytes;
   int64_t n = (a.rows + kRows - 1) / kRows;
-  const cudaError_t e = allow_smem<rmsnorm_grad_kernel<T, kTPR, kNV, kVec>>(kSmem);
+  const cudaError_t e = allow_smem<rmsnorm_grad_kernel<T, kTPR, kNV, kAccess>>(kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t most = resident_ctas<rmsnorm_grad_kernel<T, kTPR, kNV, kVec>>(kThreads, kSmem);
+  const int64_t most = resident_ctas<rmsnorm_grad_kernel<T, kTPR, kNV, kAccess>>(kThreads, kSmem);
   if (n > most) n = most;
   if (n > kNormPartialRows) n = kNormPartialRows;
+  if (kAccess == kShifted) {
+    // a multiple of 8, or as many CTAs as rows (then no CTA has a second row);
+    // never more than the rows, for which the workspace has been sized
+    n = n < most && n < kNormPartialRows ? (n + 7) / 8 * 8 : n < 8 ? 8 : n / 8 * 8;
+    if (n > a.rows) n = a.rows;
+  }
   *grid = static_cast<int>(n);
-  return launch_overlapped(rmsnorm_grad_kernel<T, kTPR, kNV, kVec>, static_cast<unsigned>(*grid), kThreads, kSmem, stream,
+  return launch_overlapped(rmsnorm_grad_kernel<T, kTPR, kNV, kAccess>, static_cast<unsigned>(*grid), kThreads, kSmem, stream,
                            0, a);
 }
 
 template <typename T, int kTPR, int kNV>
-cudaError_t grad_config(const RmsnormGradArgs& a, bool vec, int* grid, cudaStream_t stream) {
-  return vec ? grad_launch<T, kTPR, kNV, true>(a, grid, stream) : grad_launch<T, kTPR, kNV, false>(a, grid, stream);
+cudaError_t grad_config(const RmsnormGradArgs& a, Access access, int* grid, cudaStream_t stream) {
+  if (access == kVector) return grad_launch<T, kTPR, kNV, kVector>(a, grid, stream);
+  if (access == kShifted) return grad_launch<T, kTPR, kNV, kShifted>(a, grid, stream);
+  return grad_launch<T, kTPR, kNV, kSingle>(a, grid, stream);
 }
 
 template <typename T>
-cudaError_t grad_typed(const RmsnormGradArgs& a, int* grid, cudaStream_t stream) {
+cudaError_t grad_typed(RmsnormGradArgs a, int* grid, cudaStream_t stream) {
   const int es = static_cast<int>(sizeof(T));
   const bool vec = a.cols % 8 == 0 && aligned(a.h, a.h_ld, a.rows, es, 16) && aligned(a.dy, a.dy_ld, a.rows, 2, 16) &&
                    aligned(a.dh, a.dh_ld, a.dh ? a.rows : 1, es, 16) &&
                    aligned(a.dx, a.dx_ld, a.dx ? a.rows : 1, es, 16) && aligned(a.gamma, 0, 1, 1, 16);
-  if (a.cols <= 256) return grad_config<T, 32, 1>(a, vec, grid, stream);
-  if (a.cols <= 512) return grad_config<T, 32, 2>(a, vec, grid, stream);
-  if (a.cols <= 1024) return grad_config<T, 32, 4>(a, vec, grid, stream);
-  if (a.cols <= 2048) return grad_config<T, 128, 2>(a, vec, grid, stream);
-  if (a.cols <= 4096) return grad_config<T, 256, 2>(a, vec, grid, stream);
-  if (a.cols <= 8192) return grad_config<T, 512, 2>(a, vec, grid, stream);
-  if (a.cols <= kRegisterCols) return grad_config<T, 512, 4>(a, vec, grid, stream);
+  Access access = vec ? kVector : kSingle;
+  if (!vec && a.cols <= kRegisterCols) {
+    // dx has no part in the choice: its bits do not depend on where it lies
+    const RowTensor h{a.h, a.h_ld, es};
+    a.shift = common_shift({h, {a.dy, a.dy_ld, 2}, {a.dh, a.dh_ld, es}}, a.rows);
+    if (a.shift >= 0) {
+      access = kShifted;
+      a.dx_grouped = common_shift({h, {a.dx, a.dx_ld, es}}, a.rows) >= 0;
+    }
+  }
+  if (a.cols <= 256) return grad_config<T, 32, 1>(a, access, grid, stream);
+  if (a.cols <= 512) return grad_config<T, 32, 2>(a, access, grid, stream);
+  if (a.cols <= 1024) {
+    if (access == kShifted) return grad_launch<T, 128, 1, kShifted>(a, grid, stream);
+    return vec ? grad_launch<T, 32, 4, kVector>(a, grid, stream) : grad_launch<T, 32, 4, kSingle>(a, grid, stream);
+  }
+  if (a.cols <= 2048) return grad_config<T, 128, 2>(a, access, grid, stream);
+  if (a.cols <= 4096) return grad_config<T, 256, 2>(a, access, grid, stream);
+  if (a.cols <= 8192) return grad_config<T, 512, 2>(a, access, grid, stream);
+  if (a.cols <= kRegisterCols) return grad_config<T, 512, 4>(a, access, grid, stream);
   const cudaError_t e = allow_smem<rmsnorm_grad_long_kernel<T>>(static_cast<int>(2 * kNormGradMaxCols * sizeof(float)));
   if (e != cudaSuccess) return e;
   const int64_t n = a.rows < num_sms() ? a.rows : num_sms();

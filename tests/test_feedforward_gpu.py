@@ -215,6 +215,100 @@ def test_quantize_rows(rows, cols, dtype, layout):
     check_codes(q, s, np64(x))
 
 
+# widths on both sides of each kernel's span, where 7 more columns take the next one
+ODD_ROWS = [(1, 9), (9, 15), (700, 249), (20, 250), (5000, 251), (17, 505), (3, 506), (1300, 1017), (9, 1018), (40, 2041),
+            (9, 2042), (900, 2545), (5, 4089), (9, 4090), (9, 8185), (700, 8187), (9, 16377), (9, 16378)]
+
+
+def framed(rows, cols, dtype, off=3, pad=8):
+    """A buffer of ones around rows of NaN that start `off` elements into it."""
+    wide = torch.ones((rows, cols + pad), dtype=torch.float32, device="cuda").to(dtype)
+    t = wide[:, off:off + cols]
+    t.copy_(torch.full((rows, cols), float("nan"), device="cuda").to(dtype))
+    return wide, t
+
+
+def frame_intact(wide, cols, off=3):
+    w = wide.float()
+    return bool((w[:, :off] == 1).all()) and bool((w[:, off + cols:] == 1).all())
+
+
+@pytest.mark.parametrize("rows,cols", ODD_ROWS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("framing", [False, True])
+def test_rmsnorm_rows_with_one_shift(rows, cols, dtype, framing):
+    """All rows of a row index start equally far past a multiple of 8 elements:
+    every value is right and nothing beside the rows is written."""
+    pad, off = (8, 3) if framing else (0, 0)
+    x, r = normal(1, (rows, cols), dtype, 1.0, pad, off), normal(2, (rows, cols), dtype, 2.0, pad, off)
+    gamma = normal(3, (cols,), torch.bfloat16 if cols % 2 else torch.float32) + 1
+    (hw, h), (yw, y), (qw, q) = (framed(rows, cols, t, off, pad) for t in (dtype, torch.bfloat16, torch.float8_e4m3fn))
+    s, rstd = empty((rows,), torch.float32), empty((rows,), torch.float32)
+    mp.rmsnorm(x, gamma, 1e-5, residual=r, h=h, y=y, rstd=rstd)
+    wh, wy, wr = O.rmsnorm(np64(x), np64(gamma), 1e-5, np64(r))
+    within(rstd, wr, REL32 * wr, "rstd")
+    within(h, wh, (BF16 if dtype == torch.bfloat16 else 2.0 ** -23) * np.abs(wh), "h")
+    within(y, wy, (BF16 + REL32) * np.abs(wy), "y")
+    mp.rmsnorm(x, gamma, 1e-5, q=q, q_scale=s)
+    check_codes(q, s, O.rmsnorm(np64(x), np64(gamma), 1e-5, None)[1], "q")
+    mp.quantize_rows(x, q, s)
+    check_codes(q, s, np64(x), "rows")
+    assert frame_intact(hw, cols, off) and frame_intact(yw, cols, off) and frame_intact(qw, cols, off)
+
+
+@pytest.mark.parametrize("rows,cols", ODD_ROWS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("framing", [False, True])
+def test_rmsnorm_backward_rows_with_one_shift(rows, cols, dtype, framing):
+    pad, off = (8, 3) if framing else (0, 0)
+    dy, h = normal(1, (rows, cols), torch.bfloat16, 1, pad, off), normal(2, (rows, cols), dtype, 3, pad, off)
+    dh = normal(3, (rows, cols), dtype, 1, pad, off)
+    gamma = normal(4, (cols,)) + 1
+    rstd = (1 / torch.sqrt(h.double().square().mean(1) + 1e-6)).float()
+    (xw, dx), dgamma = framed(rows, cols, dtype, off, pad), empty((cols,), torch.float32)
+    ws = mp.rmsnorm_workspace(rows, cols)
+    mp.rmsnorm_backward(dy, h, gamma, rstd, dx, dh=dh, dgamma=dgamma, accumulate=False, workspace=ws)
+    wx, wg = O.rmsnorm_backward(np64(dy), np64(h), np64(gamma), np64(rstd), np64(dh))
+    n, g = np64(h) * np64(rstd)[:, None], np64(dy) * np64(gamma)
+    mag = np64(rstd)[:, None] * (np.abs(g) + np.abs(n) * np.mean(np.abs(g * n), 1, keepdims=True)) + np.abs(np64(dh))
+    within(dx, wx, (BF16 if dtype == torch.bfloat16 else 0) * np.abs(wx) + 2 * REL32 * mag, "dx")
+    within(dgamma, wg, ACC(rows) * np.sum(np.abs(np64(dy) * n), 0), "dgamma")
+    assert frame_intact(xw, cols, off)
+    inplace = dh.clone()
+    if not framing:                                  # dx in dh's place
+        mp.rmsnorm_backward(dy, h, gamma, rstd, inplace, dh=inplace)
+        assert torch.equal(inplace, dx)
+
+
+@pytest.mark.parametrize("rows,cols", [(9, 505), (700, 1023), (40, 2545), (9, 8187)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norm_gradient_does_not_depend_on_where_dx_lies(rows, cols, dtype):
+    x, r, dy, gamma = normal(1, (rows, cols), dtype), normal(2, (rows, cols), dtype), normal(3, (rows, cols)), normal(4, (cols,))
+    rstd = torch.rsqrt(x.float().square().mean(1))
+    runs = []
+    for pad, off in ((0, 0), (5, 3), (8, 1)):
+        (wide, dx), dgamma = framed(rows, cols, dtype, off, pad), empty((cols,), torch.float32)
+        mp.rmsnorm_backward(dy, x, gamma, rstd, dx, dh=r, dgamma=dgamma, accumulate=False,
+                            workspace=mp.rmsnorm_workspace(rows, cols))
+        assert frame_intact(wide, cols, off)
+        runs.append((dx.float(), dgamma))
+    for dx, dgamma in runs[1:]:
+        assert torch.equal(dx, runs[0][0]) and torch.equal(dgamma, runs[0][1])
+
+
+@pytest.mark.parametrize("rows,cols", [(9, 505), (700, 1023), (40, 2545), (9, 8187)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rmsnorm_outputs_that_lie_differently(rows, cols, dtype):
+    """Rows of an odd width whose outputs do not share the inputs' alignment."""
+    x, gamma = normal(1, (rows, cols), dtype), normal(4, (cols,))
+    (hw, h), (yw, y) = framed(rows, cols, dtype, 3, 5), framed(rows, cols, torch.bfloat16, 1, 8)
+    mp.rmsnorm(x, gamma, 1e-5, residual=x, h=h, y=y)
+    wh, wy, _ = O.rmsnorm(np64(x), np64(gamma), 1e-5, np64(x))
+    within(h, wh, (BF16 if dtype == torch.bfloat16 else 2.0 ** -23) * np.abs(wh), "h")
+    within(y, wy, (BF16 + REL32) * np.abs(wy), "y")
+    assert frame_intact(hw, cols, 3) and frame_intact(yw, cols, 1)
+
+
 # ----------------------------------------------------------------- linear --
 
 LINEAR_SHAPES = [(1, 1, 1), (1, 8, 16), (2, 129, 65), (17, 64, 1023), (130, 257, 33), (64, 512, 256), (129, 128, 4096),
