@@ -1,0 +1,69 @@
+"""Feed-forward operators on values far from one, against the fp64 oracle.
+
+Tolerances are those of the formats and of the order of operations (the same
+as for values of order one): a bf16 output is within 2^-8 of its magnitude, an
+fp32 chain of a few roundings within 2^-20 of its terms' magnitudes.
+"""
+
+import numpy as np
+import pytest
+
+from gpu_helpers import require_gpu, torch
+import mixed_precision_optimizer_gb300 as mp
+from oracle import feedforward as O
+
+pytestmark = pytest.mark.gpu
+
+BF16, REL32 = 2.0 ** -8, 2.0 ** -20
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def normal(seed, shape, dtype=torch.bfloat16, std=1.0, off=0):
+    """Normal values; `off`: a slice that starts so many elements into rows 8 wider."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    wide = tuple(shape[:-1]) + (shape[-1] + (8 if off else 0),)
+    t = (torch.randn(wide, generator=g, device="cuda", dtype=torch.float64) * std).to(dtype)
+    return t[..., off:off + shape[-1]]
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def within(got, want, bound, what=""):
+    got = np64(got)
+    assert np.isfinite(got).all(), f"{what}: not finite"
+    over = np.abs(got - want) / np.maximum(bound, 1e-300)
+    assert (over <= 1).all(), f"{what}: {int((over > 1).sum())} of {over.size} beyond the bound, worst {over.max():.3g} times"
+
+
+# a width for every kernel of the gradient: a warp's row of one, two and four groups,
+# rows of 128 to 512 threads (bf16 ones through the ring), and rows in shared memory; odd
+# widths and slices that share a shift, and slices that do not
+@pytest.mark.parametrize("rows,cols,dy_off,h_off", [
+    (40, 64, 0, 0), (40, 512, 0, 0), (40, 1024, 0, 0), (700, 2048, 0, 0), (9, 4096, 0, 0), (9, 8192, 0, 0), (5, 14336, 0, 0),
+    (40, 251, 0, 0), (40, 505, 0, 0), (40, 1017, 0, 0), (40, 2545, 3, 3), (9, 8187, 0, 0),
+    (40, 250, 1, 2), (40, 1023, 1, 2), (9, 4089, 1, 2), (3, 16391, 0, 0), (3, 20000, 0, 0)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("size", [1e-14, 1e14, 1e16])
+def test_norm_gradient_of_rows_of_any_magnitude(rows, cols, dy_off, h_off, dtype, size):
+    """dx = rstd (g - n mean(g n)): n = h rstd is of order one whatever h's
+    magnitude, so a row of 1e-14 (eps = 0), 1e14 or 1e16 keeps its projection."""
+    dy, h, gamma = normal(1, (rows, cols), off=dy_off), normal(2, (rows, cols), dtype, size, h_off), normal(3, (cols,)) + 1
+    y, rstd = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda"), torch.empty(rows, device="cuda")
+    mp.rmsnorm(h, gamma, 0.0, y=y, rstd=rstd)
+    wr = 1 / np.sqrt(np.mean(np64(h) ** 2, 1))
+    within(rstd, wr, REL32 * wr, "rstd")
+    within(y, O.rmsnorm(np64(h), np64(gamma), 0.0)[1], (BF16 + REL32) * np.abs(O.rmsnorm(np64(h), np64(gamma), 0.0)[1]), "y")
+    dx, dgamma = torch.full((rows, cols), float("nan"), dtype=dtype, device="cuda"), torch.empty(cols, device="cuda")
+    mp.rmsnorm_backward(dy, h, gamma, rstd, dx, dgamma=dgamma, accumulate=False, workspace=mp.rmsnorm_workspace(rows, cols))
+    wx, wg = O.rmsnorm_backward(np64(dy), np64(h), np64(gamma), np64(rstd))
+    n, g = np64(h) * np64(rstd)[:, None], np64(dy) * np64(gamma)
+    mag = np64(rstd)[:, None] * (np.abs(g) + np.abs(n) * np.mean(np.abs(g * n), 1, keepdims=True))
+    within(dx, wx, (BF16 if dtype == torch.bfloat16 else 0) * np.abs(wx) + 2 * REL32 * mag, "dx")
+    within(dgamma, wg, (rows + 8) * 2.0 ** -23 * np.sum(np.abs(np64(dy) * n), 0), "dgamma")
