@@ -601,6 +601,11 @@ MPOPT_API opt_status opt_linear_backward(const opt_linear_grad_args* args, void*
  * whose base or row distance is not a multiple of 16 bytes is first copied
  * into the workspace.  flags 0: room for the operands whose dense layout
  * needs that; OPT_LINEAR_ANY_LAYOUT: room for all of them.
+ *
+ * With OPT_LINEAR_ANY_LAYOUT the workspace also serves every call whose m, n
+ * and k are none larger; without it those of them whose operands need no copy.
+ * A call that needs more is refused with OPT_ERR_WORKSPACE.  A layer that is
+ * followed by one with n and k the other way round takes the larger of both sizes.
  */
 enum { OPT_LINEAR_ANY_LAYOUT = 1 };
 MPOPT_API size_t opt_linear_workspace_size(int64_t m, int64_t n, int64_t k, int32_t flags);

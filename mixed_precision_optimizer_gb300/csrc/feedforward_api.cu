@@ -212,7 +212,7 @@ size_t opt_linear_workspace_size(int64_t m, int64_t n, int64_t k, int32_t flags)
   // 16-byte rows: k a multiple of 16 also serves 8-bit operands
   const size_t x_w = any || k % 16 ? packed_bytes(m, k, 2) + packed_bytes(n, k, 2) : 0;
   const size_t dz = any || n % 8 ? packed_bytes(m, n, 2) : 0;
-  return kLinearHeaderBytes + x_w + dz + column_sum_bytes(m, n);
+  return kLinearHeaderBytes + x_w + dz + round_up(static_cast<size_t>(column_sum_most(m, n)) * 4, 256);
 }
 
 opt_status opt_linear_forward(const opt_linear_args* a, void* workspace, size_t workspace_bytes, void* stream) {

@@ -325,6 +325,15 @@ inline int64_t column_sum_slices(int64_t m, int64_t n) {
   const int64_t s = by_rows < wanted ? by_rows : wanted;
   return s < 1 ? 1 : s > 64 ? 64 : s;
 }
+// The most elements that `partial` needs for any m' <= m and n' <= n: slices
+// times n' goes up and down with n', but is at most 64 (or one for 256 rows)
+// times n', and below 152 * 8 * 64 + n'.
+inline int64_t column_sum_most(int64_t m, int64_t n) {
+  const int64_t fill = 152 * 8 * 64, by_rows = (m + 255) / 256, s = by_rows < 64 ? by_rows : 64;
+  if (s < 2) return 0;
+  if (n >= fill) n = fill - 1;                  // from here on one slice
+  return s * n < fill + n ? s * n : fill + n;
+}
 struct ColumnSumArgs {
   const uint16_t* dz;
   int64_t ld, m, n;

@@ -259,8 +259,11 @@ def linear_workspace_size(m, n, k, any_layout=False) -> int:
 
 
 def linear_workspace(m, n, k, any_layout=False, device=None):
-    """A workspace of linear_workspace_size bytes with its header zeroed.  One
-    workspace serves any calls of these sizes or smaller, in stream order."""
+    """A workspace of linear_workspace_size bytes with its header zeroed.  In
+    stream order it serves any number of calls: of these sizes, and of smaller
+    m, n and k -- with any_layout all of them, without it those whose operands'
+    rows start on 16 bytes (dense rows of a multiple of 8 bf16 or 16 e4m3
+    elements).  A call that needs more raises MpoptError."""
     ws = mp.alloc_workspace(linear_workspace_size(m, n, k, any_layout), device)
     if ws is not None:
         ws[:LINEAR_HEADER_BYTES].zero_()
