@@ -14,7 +14,8 @@ As in the rest of the package the caller owns every buffer: outputs are
 passed in and written in place, on the current CUDA stream or on ``stream``.
 Matrices are 2-D (or more leading dimensions that collapse into rows without a
 copy; a vector is one row) with contiguous rows that may be slices of wider
-ones.  ``include/mpopt.h`` defines every operator; arguments it refuses raise
+ones.  All tensors and the workspace are on the current device.
+``include/mpopt.h`` defines every operator; arguments it refuses raise
 ``MpoptError``, tensors of a wrong type, device or shape ``TypeError`` or
 ``ValueError``.
 """
@@ -93,24 +94,26 @@ _PACK_LINEAR_GRAD = struct.Struct("=7Q8q2i").pack
 _torch = None                 # torch, once a call has needed it (importing this package does not load it)
 _CODES = {}                   # torch dtype -> OPT_DTYPE_*
 _raw_stream = None
+_current_device = None        # torch's, without its checks (0.1 us)
 
 
 def _load_torch():
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _current_device
     import torch
     _CODES.update({torch.float32: DTYPE_FP32, torch.bfloat16: DTYPE_BF16, torch.float8_e4m3fn: DTYPE_E4M3})
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _torch = torch
     return torch
 
 
-def _stream(stream, t):
-    """Handle of `stream`, by default the current stream of t's device."""
+def _stream(stream, dev):
+    """Handle of `stream`, by default the device's current stream."""
     if stream is not None:
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if _raw_stream is not None:
-        return _raw_stream(t.get_device())
-    return _torch.cuda.current_stream(t.device).cuda_stream
+        return _raw_stream(dev)
+    return _torch.cuda.current_stream(dev).cuda_stream
 
 
 def _code(t, what, allowed):
@@ -136,17 +139,43 @@ def _shape2(t, what):
     return rows, shape[-1]
 
 
-def _mat(t, dtype, rows, cols, what):
+def _lead(t, what):
+    """(device, rows, cols, pointer, distance between rows) of the matrix that
+    sets a call's sizes and device.  That has to be the current device: the
+    library launches there, whatever its arguments' addresses."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if dev != _current_device():
+        raise ValueError(f"{what} is on cuda:{dev}, which is not the current device (cuda:{_current_device()})")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2:
+        t = t.view(_shape2(t, what))          # raises when the rows are not evenly spaced
+        shape, stride = t.shape, t.stride()
+    rows, cols = shape
+    if stride[1] != 1 and cols > 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return dev, rows, cols, t.data_ptr(), stride[0]
+
+
+def _elsewhere(t, dev, what):
+    """Raises for a tensor that is not on the call's device."""
+    if t.get_device() < 0:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on cuda:{t.get_device()}, the other tensors on cuda:{dev}")
+
+
+def _mat(t, dtype, rows, cols, what, dev):
     """(pointer, distance between rows) of a matrix argument; (0, 0) for None."""
     if t is None:
         return 0, 0
     stride = t.stride()
-    if t.dtype is dtype and t.is_cuda and t.shape == (rows, cols) and stride[1] == 1:
+    if t.dtype is dtype and t.get_device() == dev and t.shape == (rows, cols) and stride[1] == 1:
         return t.data_ptr(), stride[0]
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
+    _elsewhere(t, dev, what)
     if len(stride) != 2:
         t = t.view(_shape2(t, what))          # raises when the rows are not evenly spaced
         stride = t.stride()
@@ -157,22 +186,25 @@ def _mat(t, dtype, rows, cols, what):
     return t.data_ptr(), stride[0]
 
 
-def _vec(t, dtype, n, what):
+def _vec(t, dtype, n, what, dev):
     """Pointer of a dense vector argument; 0 for None."""
     if t is None:
         return 0
-    if t.dtype is dtype and t.is_cuda and t.numel() == n and t.is_contiguous():
+    if t.dtype is dtype and t.get_device() == dev and t.numel() == n and t.is_contiguous():
         return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
+    _elsewhere(t, dev, what)
     raise ValueError(f"{what} must be contiguous with {n} elements")
 
 
-def _workspace(ws):
+def _workspace(ws, dev):
     if ws is None:
         return None, 0
+    if ws.get_device() != dev:
+        _elsewhere(ws, dev, "workspace")
+    if not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
@@ -187,17 +219,17 @@ def rmsnorm(x, gamma, eps=1e-6, residual=None, h=None, y=None, q=None, q_scale=N
     rmsnorm_backward needs.  Outputs left out are not written.  h may be x or
     residual itself."""
     torch = _torch or _load_torch()
-    rows, cols = _shape2(x, "x")
     code, gcode = _code(x, "x", _FLOAT), _code(gamma, "gamma", _FLOAT)
     dt, f32 = x.dtype, torch.float32
-    xp, xl = _mat(x, dt, rows, cols, "x")
-    rp, rl = _mat(residual, dt, rows, cols, "residual")
-    hp, hl = _mat(h, dt, rows, cols, "h")
-    yp, yl = _mat(y, torch.bfloat16, rows, cols, "y")
-    qp, ql = _mat(q, torch.float8_e4m3fn, rows, cols, "q")
-    a = _PACK_NORM(xp, rp, _vec(gamma, gamma.dtype, cols, "gamma"), hp, yp, qp, _vec(q_scale, f32, rows, "q_scale"),
-                   _vec(rstd, f32, rows, "rstd"), rows, cols, xl, rl, hl, yl, ql, code, gcode, eps, 0)
-    status = mp.lib().opt_rmsnorm_forward(a, _stream(stream, x))
+    dev, rows, cols, xp, xl = _lead(x, "x")
+    rp, rl = _mat(residual, dt, rows, cols, "residual", dev)
+    hp, hl = _mat(h, dt, rows, cols, "h", dev)
+    yp, yl = _mat(y, torch.bfloat16, rows, cols, "y", dev)
+    qp, ql = _mat(q, torch.float8_e4m3fn, rows, cols, "q", dev)
+    gp, sp = _vec(gamma, gamma.dtype, cols, "gamma", dev), _vec(q_scale, f32, rows, "q_scale", dev)
+    a = _PACK_NORM(xp, rp, gp, hp, yp, qp, sp, _vec(rstd, f32, rows, "rstd", dev), rows, cols, xl, rl, hl, yl, ql, code,
+                   gcode, eps, 0)
+    status = mp.lib().opt_rmsnorm_forward(a, _stream(stream, dev))
     if status:
         mp._check(status, "opt_rmsnorm_forward")
 
@@ -208,18 +240,17 @@ def rmsnorm_backward(dy, h, gamma, rstd, dx, dh=None, dgamma=None, accumulate=Tr
     the gradient reaching h past the norm; dgamma fp32 [cols] is added to, or
     overwritten with accumulate=False, and needs rmsnorm_workspace(rows, cols)."""
     torch = _torch or _load_torch()
-    rows, cols = _shape2(h, "h")
     code, gcode = _code(h, "h", _FLOAT), _code(gamma, "gamma", _FLOAT)
     f32 = torch.float32
-    yp, yl = _mat(dy, torch.bfloat16, rows, cols, "dy")
-    hp, hl = _mat(h, h.dtype, rows, cols, "h")
-    sp, sl = _mat(dh, h.dtype, rows, cols, "dh")
-    xp, xl = _mat(dx, h.dtype, rows, cols, "dx")
-    a = _PACK_NORM_GRAD(yp, hp, _vec(gamma, gamma.dtype, cols, "gamma"), _vec(rstd, f32, rows, "rstd"), sp, xp,
-                        _vec(dgamma, f32, cols, "dgamma"), rows, cols, yl, hl, sl, xl, code, gcode,
-                        1 if accumulate else 0, 0)
-    w, nb = _workspace(workspace)
-    status = mp.lib().opt_rmsnorm_backward(a, w, nb, _stream(stream, h))
+    dev, rows, cols, hp, hl = _lead(h, "h")
+    yp, yl = _mat(dy, torch.bfloat16, rows, cols, "dy", dev)
+    sp, sl = _mat(dh, h.dtype, rows, cols, "dh", dev)
+    xp, xl = _mat(dx, h.dtype, rows, cols, "dx", dev)
+    gp, rp = _vec(gamma, gamma.dtype, cols, "gamma", dev), _vec(rstd, f32, rows, "rstd", dev)
+    a = _PACK_NORM_GRAD(yp, hp, gp, rp, sp, xp, _vec(dgamma, f32, cols, "dgamma", dev), rows, cols, yl, hl, sl, xl, code,
+                        gcode, 1 if accumulate else 0, 0)
+    w, nb = _workspace(workspace, dev)
+    status = mp.lib().opt_rmsnorm_backward(a, w, nb, _stream(stream, dev))
     if status:
         mp._check(status, "opt_rmsnorm_backward")
 
@@ -237,12 +268,11 @@ def quantize_rows(x, q, scale, stream=None):
     """q [rows][cols] (float8_e4m3fn), scale [rows] (fp32) <- x (bf16 or
     fp32): x ~ q * scale with the largest magnitude of a row at 448."""
     torch = _torch or _load_torch()
-    rows, cols = _shape2(x, "x")
     code = _code(x, "x", _FLOAT)
-    xp, xl = _mat(x, x.dtype, rows, cols, "x")
-    qp, ql = _mat(q, torch.float8_e4m3fn, rows, cols, "q")
-    status = mp.lib().opt_quantize_rows(xp, xl, code, rows, cols, qp, ql, _vec(scale, torch.float32, rows, "scale"),
-                                        _stream(stream, x))
+    dev, rows, cols, xp, xl = _lead(x, "x")
+    qp, ql = _mat(q, torch.float8_e4m3fn, rows, cols, "q", dev)
+    sp = _vec(scale, torch.float32, rows, "scale", dev)
+    status = mp.lib().opt_quantize_rows(xp, xl, code, rows, cols, qp, ql, sp, _stream(stream, dev))
     if status:
         mp._check(status, "opt_quantize_rows")
 
@@ -277,25 +307,24 @@ def linear(x, w, y, bias=None, act="none", residual=None, z=None, x_scale=None, 
     bf16 or fp32; z [m][n] (bf16, optional) receives the pre-activation.  y may
     be residual itself.  act: "none", "relu", "gelu" (tanh form), "silu"."""
     torch = _torch or _load_torch()
-    m, k = _shape2(x, "x")
-    n = _shape2(w, "w")[0]
     code = _code(x, "x", (DTYPE_BF16, DTYPE_E4M3))
     acode = ACTIVATIONS.get(act)
     if acode is None:
         raise ValueError(f"unknown activation {act!r}")
     bf16, f32 = torch.bfloat16, torch.float32
-    xp, xl = _mat(x, x.dtype, m, k, "x")
-    wp, wl = _mat(w, x.dtype, n, k, "w")
-    rp, rl = _mat(residual, bf16, m, n, "residual")
-    yp, yl = _mat(y, bf16, m, n, "y")
-    zp, zl = _mat(z, bf16, m, n, "z")
+    dev, m, k, xp, xl = _lead(x, "x")
+    n = _shape2(w, "w")[0]
+    wp, wl = _mat(w, x.dtype, n, k, "w", dev)
+    rp, rl = _mat(residual, bf16, m, n, "residual", dev)
+    yp, yl = _mat(y, bf16, m, n, "y", dev)
+    zp, zl = _mat(z, bf16, m, n, "z", dev)
     bp, bcode = 0, DTYPE_BF16
     if bias is not None:
-        bp, bcode = _vec(bias, bias.dtype, n, "bias"), _code(bias, "bias", _FLOAT)
-    a = _PACK_LINEAR(xp, wp, _vec(x_scale, f32, m, "x_scale"), _vec(w_scale, f32, n, "w_scale"), bp, rp, yp, zp, m, n,
-                     k, xl, wl, rl, yl, zl, code, bcode, acode, 0)
-    ws, nb = _workspace(workspace)
-    status = mp.lib().opt_linear_forward(a, ws, nb, _stream(stream, x))
+        bp, bcode = _vec(bias, bias.dtype, n, "bias", dev), _code(bias, "bias", _FLOAT)
+    xsp, wsp = _vec(x_scale, f32, m, "x_scale", dev), _vec(w_scale, f32, n, "w_scale", dev)
+    a = _PACK_LINEAR(xp, wp, xsp, wsp, bp, rp, yp, zp, m, n, k, xl, wl, rl, yl, zl, code, bcode, acode, 0)
+    ws, nb = _workspace(workspace, dev)
+    status = mp.lib().opt_linear_forward(a, ws, nb, _stream(stream, dev))
     if status:
         mp._check(status, "opt_linear_forward")
 
@@ -308,7 +337,6 @@ def linear_backward(dz, x, w, dx=None, z_prev=None, act_prev="none", dw=None, db
     Outputs left out are not computed; x and w may be None when only the other
     one's product is asked for."""
     torch = _torch or _load_torch()
-    m, n = _shape2(dz, "dz")
     if x is None and w is None and dbias is None:
         raise ValueError("linear_backward: nothing to compute")
     k = _shape2(x, "x")[1] if x is not None else _shape2(w, "w")[1] if w is not None else 1
@@ -316,16 +344,18 @@ def linear_backward(dz, x, w, dx=None, z_prev=None, act_prev="none", dw=None, db
     if acode is None:
         raise ValueError(f"unknown activation {act_prev!r}")
     bf16, f32 = torch.bfloat16, torch.float32
-    zp, zl = _mat(dz, bf16, m, n, "dz")
-    xp, xl = _mat(x, bf16, m, k, "x")
-    wp, wl = _mat(w, bf16, n, k, "w")
-    pp, pl = _mat(z_prev, bf16, m, k, "z_prev")
-    dp, dl = _mat(dx, bf16, m, k, "dx")
+    if dz.dtype != bf16:
+        raise TypeError(f"dz must be {bf16}, got {dz.dtype}")
+    dev, m, n, zp, zl = _lead(dz, "dz")
+    xp, xl = _mat(x, bf16, m, k, "x", dev)
+    wp, wl = _mat(w, bf16, n, k, "w", dev)
+    pp, pl = _mat(z_prev, bf16, m, k, "z_prev", dev)
+    dp, dl = _mat(dx, bf16, m, k, "dx", dev)
     if dw is not None and dw.shape != (n, k):
         raise ValueError(f"dw has shape {tuple(dw.shape)}, expected {(n, k)}")
-    a = _PACK_LINEAR_GRAD(zp, xp, wp, pp, dp, _vec(dw, f32, n * k, "dw"), _vec(dbias, f32, n, "dbias"), m, n, k, zl, xl,
-                          wl, pl, dl, acode, 1 if accumulate else 0)
-    ws, nb = _workspace(workspace)
-    status = mp.lib().opt_linear_backward(a, ws, nb, _stream(stream, dz))
+    wgp, bgp = _vec(dw, f32, n * k, "dw", dev), _vec(dbias, f32, n, "dbias", dev)
+    a = _PACK_LINEAR_GRAD(zp, xp, wp, pp, dp, wgp, bgp, m, n, k, zl, xl, wl, pl, dl, acode, 1 if accumulate else 0)
+    ws, nb = _workspace(workspace, dev)
+    status = mp.lib().opt_linear_backward(a, ws, nb, _stream(stream, dev))
     if status:
         mp._check(status, "opt_linear_backward")

@@ -46,3 +46,109 @@ def test_linear_workspace_of_every_width():
     assert mp.linear_workspace_size(8192, 128256, 4096) >= mp.linear_workspace_size(8192, 4096, 4096)
     assert mp.linear_workspace_size(8192, 9728, 2560) >= mp.linear_workspace_size(8192, 2560, 9728)
     assert mp.linear_workspace_size(128, 4096, 4096, any_layout=True) >= mp.linear_workspace_size(128, 4096, 1023)
+
+
+# -------------------------------------------------------------- devices --
+
+class OnDevice:
+    """Stands in for a dense tensor on a device that this machine need not have."""
+
+    def __init__(self, dtype, *shape, device=0, contiguous=True):
+        self.dtype, self.shape, self._device, self._contiguous = dtype, torch.Size(shape), device, contiguous
+
+    is_cuda = property(lambda self: self._device >= 0)
+    device = property(lambda self: torch.device("cuda", self._device) if self._device >= 0 else torch.device("cpu"))
+
+    def get_device(self):
+        return self._device
+
+    def stride(self):
+        return tuple(self.shape[i + 1:].numel() for i in range(len(self.shape)))
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return torch.empty(0, dtype=self.dtype).element_size()
+
+    def is_contiguous(self):
+        return self._contiguous
+
+    def data_ptr(self):
+        return 1 << 20
+
+
+BF, F32, E4 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+T = OnDevice
+
+
+def calls():
+    """name -> (function, the tensors it takes by name, with a workspace that is large enough)"""
+    ws = T(torch.uint8, 1 << 20)
+    return {
+        "rmsnorm": (mp.rmsnorm, dict(x=T(BF, 4, 64), gamma=T(BF, 64), residual=T(BF, 4, 64), h=T(BF, 4, 64), y=T(BF, 4, 64),
+                                     q=T(E4, 4, 64), q_scale=T(F32, 4), rstd=T(F32, 4))),
+        "rmsnorm_backward": (mp.rmsnorm_backward, dict(dy=T(BF, 4, 64), h=T(F32, 4, 64), gamma=T(F32, 64), rstd=T(F32, 4),
+                                                       dx=T(F32, 4, 64), dh=T(F32, 4, 64), dgamma=T(F32, 64), workspace=ws)),
+        "quantize_rows": (mp.quantize_rows, dict(x=T(BF, 4, 64), q=T(E4, 4, 64), scale=T(F32, 4))),
+        "linear": (mp.linear, dict(x=T(E4, 4, 64), w=T(E4, 32, 64), y=T(BF, 4, 32), bias=T(BF, 32), residual=T(BF, 4, 32),
+                                   z=T(BF, 4, 32), x_scale=T(F32, 4), w_scale=T(F32, 32), workspace=ws)),
+        "linear_backward": (mp.linear_backward, dict(dz=T(BF, 4, 32), x=T(BF, 4, 64), w=T(BF, 32, 64), dx=T(BF, 4, 64),
+                                                     z_prev=T(BF, 4, 64), dw=T(F32, 32, 64), dbias=T(F32, 32), workspace=ws)),
+    }
+
+
+@pytest.fixture
+def recorded(monkeypatch):
+    """Calls that would have reached the library, by name; nothing is launched."""
+    reached = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: reached.append(name) or 0
+    mp.feedforward._load_torch()
+    monkeypatch.setattr(mp, "lib", lambda: Library())
+    monkeypatch.setattr(mp.feedforward, "_current_device", lambda: 0, raising=False)
+    return reached
+
+
+OPERANDS = [(f, a) for f, (_, args) in calls().items() for a in args]
+
+
+@pytest.mark.parametrize("name", sorted(calls()))
+def test_tensors_of_one_device_pass(recorded, name):
+    f, args = calls()[name]
+    f(**args, stream=0)
+    assert len(recorded) == 1
+
+
+@pytest.mark.parametrize("name,argument", OPERANDS)
+@pytest.mark.parametrize("device", [1, -1])
+def test_a_tensor_elsewhere_is_refused(recorded, name, argument, device):
+    """One tensor, or the workspace, on another device or on the CPU."""
+    f, args = calls()[name]
+    args[argument]._device = device
+    with pytest.raises(ValueError, match="cuda|CUDA"):
+        f(**args, stream=0)
+    assert not recorded
+
+
+@pytest.mark.parametrize("name", sorted(calls()))
+def test_a_device_that_is_not_current_is_refused(recorded, name):
+    """All tensors on cuda:1 while cuda:0 is current: a launch would go to the
+    current device's stream with the other one's addresses."""
+    f, args = calls()[name]
+    for t in args.values():
+        t._device = 1
+    with pytest.raises(ValueError, match="current"):
+        f(**args, stream=0)
+    assert not recorded
+
+
+@pytest.mark.parametrize("name", ["rmsnorm_backward", "linear", "linear_backward"])
+def test_a_workspace_with_gaps_is_refused(recorded, name):
+    f, args = calls()[name]
+    args["workspace"] = T(torch.uint8, 1 << 20, contiguous=False)
+    with pytest.raises(ValueError, match="workspace"):
+        f(**args, stream=0)
+    assert not recorded
