@@ -417,7 +417,9 @@ MPOPT_API opt_status opt_noalloc_device_status(void* stream);
 /*
  * Synchronises `stream` and reports whether a kernel of the last step on this
  * workspace recorded a device-side timeout (OPT_ERR_DEVICE_TIMEOUT) or not
- * (OPT_OK).  Returns OPT_ERR_CUDA if the synchronisation itself fails.
+ * (OPT_OK).  Returns OPT_ERR_CUDA if the synchronisation itself fails, and for
+ * a workspace of opt_linear_* OPT_ERR_WORKSPACE if a call found that its header
+ * had not been zero (see there).
  */
 MPOPT_API opt_status opt_device_status(const void* workspace, void* stream);
 
@@ -470,7 +472,10 @@ MPOPT_API opt_status opt_selftest_wait_timeout(const float* G, float* O, int64_t
  *    device memory.  The first 256 bytes of a linear workspace must be zero
  *    before its first use (cudaMemset); every call leaves them zero unless a
  *    bounded device-side wait ran out.  opt_device_status() reports that, and
- *    the workspace must be zeroed again before its next use.
+ *    the workspace must be zeroed again before its next use.  A header that was
+ *    not zero costs a large product some of its tiles, whose outputs are then not
+ *    written; nothing is accessed out of range, and opt_device_status() reports
+ *    it too.
  */
 enum { OPT_DTYPE_FP32 = 0, OPT_DTYPE_BF16 = 1, OPT_DTYPE_E4M3 = 2 };
 

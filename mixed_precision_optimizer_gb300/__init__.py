@@ -35,6 +35,7 @@ LIB_PATH = os.path.join(_HERE, "libmpopt.so")
 OPT_OK = 0
 OPT_ERR_INVALID_ARG = 1
 OPT_ERR_MISALIGNED = 3
+OPT_ERR_WORKSPACE = 4
 OPT_ERR_DEVICE_TIMEOUT = 6
 STATUS_NAMES = {0: "OPT_OK", 1: "OPT_ERR_INVALID_ARG", 2: "OPT_ERR_UNSUPPORTED", 3: "OPT_ERR_MISALIGNED",
                 4: "OPT_ERR_WORKSPACE", 5: "OPT_ERR_CUDA", 6: "OPT_ERR_DEVICE_TIMEOUT"}

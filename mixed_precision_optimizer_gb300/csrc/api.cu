@@ -904,7 +904,7 @@ opt_status opt_device_status(const void* workspace, void* stream) {
                                   static_cast<cudaStream_t>(stream));
   if (e == cudaSuccess) e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "device status");
-  return code == 0 ? OPT_OK : OPT_ERR_DEVICE_TIMEOUT;
+  return code == 0 ? OPT_OK : code == kStatusHeader ? OPT_ERR_WORKSPACE : OPT_ERR_DEVICE_TIMEOUT;
 }
 
 const char* opt_strerror(opt_status s) {

@@ -196,7 +196,8 @@ enum : uint32_t {
   kStatusTimeoutAccFree = 4,  // MMA waited too long for a free accumulator
   kStatusTimeoutDrain = 5,
   kStatusTimeoutTile = 6,     // a role waited too long for the next tile index
-  kStatusTimeoutWload = 7     // an epilogue warp waited too long for its block of W
+  kStatusTimeoutWload = 7,    // an epilogue warp waited too long for its block of W
+  kStatusHeader = 8           // linear layer: the workspace's header was not zero, tiles are missing
 };
 
 // Workspace-header words (uint32 index) of the GEMM tile scheduler: the count

@@ -934,6 +934,8 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap dx_a, const __grid_consta
 constexpr int kPairEpiWarps = 8;
 constexpr int kPairThreads = 96 + 32 * kPairEpiWarps;
 constexpr int kTileSlots = 3;
+constexpr int kDoneWord = kSchedWord + 1;    // header words beside the tile counter: CTAs that have finished,
+constexpr int kTakenWord = kSchedWord + 2;   // and tiles claimed in all
 constexpr int kBlockBytes = 32 * 128;   // a staged block: 32 rows of 128 bytes
 constexpr uint32_t kTileConsumers = 2 + 1 + 2 * kPairEpiWarps;
 
@@ -1498,16 +1500,23 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   } else if (lane == 0 && rank == 0) {
     const uint32_t ring_odd = peer_addr(smem_u32(const_cast<int*>(tile_ring)), 1);
     const uint32_t tfull_odd = peer_addr(smem_u32(&tile_full[0]), 1);
+    // A counter that did not start at zero gives no tile out of range: it ends
+    // the claims early, and the last CTA finds tiles missing.
+    const uint32_t left = static_cast<uint32_t>(P.total_tiles - npairs);
+    uint32_t taken = 0;
     for (uint32_t seq = 0;; ++seq) {
       const uint32_t slot = seq % kTileSlots, sph = (seq / kTileSlots) & 1u;
       if (!mbar_wait(smem_u32(&tile_empty[slot]), sph ^ 1u, abort_flag, status, kStatusTimeoutTile)) break;
-      const int tile = npairs + static_cast<int>(atomicAdd(status + kSchedWord, 1u));
+      const uint32_t claim = atomicAdd(status + kSchedWord, 1u);
+      const int tile = claim < left ? npairs + static_cast<int>(claim) : P.total_tiles;
+      taken += claim < left ? 1u : 0u;
       tile_ring[slot] = tile;
       st_cluster_u32(ring_odd + 4 * slot, static_cast<uint32_t>(tile));
       mbar_arrive_local(smem_u32(&tile_full[slot]));
       mbar_arrive_remote(tfull_odd + 8 * slot);
       if (tile >= P.total_tiles) break;
     }
+    if (taken) atomicAdd(status + kTakenWord, taken);
   }
 
   tc_fence_before();
@@ -1516,10 +1525,14 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   if (threadIdx.x == 0) {
     // the last CTA to finish (every claim is made by then) leaves the header zero
     __threadfence();
-    if (atomicAdd(status + kSchedWord + 1, 1u) == gridDim.x - 1) {
+    const uint32_t before = atomicAdd(status + kDoneWord, 1u);
+    bool whole = before < gridDim.x;
+    if (before == gridDim.x - 1) {
+      whole = atomicExch(status + kTakenWord, 0u) == static_cast<uint32_t>(P.total_tiles - npairs);
       atomicExch(status + kSchedWord, 0u);
-      atomicExch(status + kSchedWord + 1, 0u);
+      atomicExch(status + kDoneWord, 0u);
     }
+    if (!whole) atomicCAS(status, 0u, static_cast<uint32_t>(kStatusHeader));
   }
   if (warp == 1) {
     tc_fence_after();

@@ -284,7 +284,8 @@ def quantize_rows(x, q, scale, stream=None):
 def linear_workspace_size(m, n, k, any_layout=False) -> int:
     """Workspace bytes of linear and linear_backward for x [m][k], w [n][k];
     any_layout: also for operands whose rows do not start on 16 bytes although
-    dense ones of these sizes would."""
+    dense ones of these sizes would.  The first LINEAR_HEADER_BYTES have to be
+    zero before the first call; linear_workspace sees to that."""
     return int(mp.lib().opt_linear_workspace_size(int(m), int(n), int(k), LINEAR_ANY_LAYOUT if any_layout else 0))
 
 

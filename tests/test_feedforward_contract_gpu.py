@@ -48,3 +48,30 @@ def test_the_two_products_of_a_block_share_the_larger_workspace():
     ws = max(mp.linear_workspace(tokens, hidden, width), mp.linear_workspace(tokens, width, hidden), key=torch.numel)
     layer(tokens, hidden, width, ws)
     layer(tokens, width, hidden, ws)
+
+
+# words of the header: the tile counter, the CTAs that have finished, the tiles claimed
+@pytest.mark.parametrize("words", [{32: 5}, {32: 0x7FFFFFFF}, {32: -2 ** 31}, {32: -1}, {33: 3}, {33: -1}, {34: 7},
+                                   {32: -16, 33: 151, 34: -1}])
+@pytest.mark.parametrize("shape", [(2100, 2300, 100), (4096, 2560, 264)])
+def test_a_header_that_is_not_zero_is_reported(shape, words):
+    """A large product in such a workspace ends, writes nothing outside its
+    output, and opt_device_status reports the workspace; zeroed, it works again.
+    (A counter of -1 costs one CTA pair its share; the others compute every tile.)"""
+    m, n, k = shape
+    x, w = normal(1, m, k), normal(2, n, k, std=0.1)
+    want, ws = torch.empty(m, n, dtype=torch.bfloat16, device="cuda"), mp.linear_workspace(m, n, k)
+    mp.linear(x, w, want, workspace=ws)
+    assert mp.device_status(ws) == mp.OPT_OK and not ws[:256].any()
+    header = ws[:256].view(torch.int32)
+    for i, v in words.items():
+        header[i] = v
+    wide = torch.full((m + 2, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = wide[1:-1]
+    mp.linear(x, w, y, workspace=ws)
+    status = mp.device_status(ws)
+    assert status == mp.OPT_ERR_WORKSPACE or (words == {32: -1} and status == mp.OPT_OK and torch.equal(y, want))
+    assert ((y == want) | (y == 7)).all() and (wide[0] == 7).all() and (wide[-1] == 7).all()
+    header.zero_()
+    mp.linear(x, w, y, workspace=ws)
+    assert mp.device_status(ws) == mp.OPT_OK and torch.equal(y, want)
