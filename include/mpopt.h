@@ -593,7 +593,7 @@ typedef struct {
   float* dbias;             /* [n] fp32, or NULL                               */
   int64_t m, n, k;
   int64_t dz_ld, x_ld, w_ld, z_prev_ld, dx_ld;
-  int32_t act_prev;         /* OPT_ACT_* (with z_prev)                         */
+  int32_t act_prev;         /* OPT_ACT_*; other than NONE, dx needs z_prev     */
   int32_t accumulate;       /* nonzero: dw, dbias += ...; zero: = ...          */
 } opt_linear_grad_args;
 

@@ -264,6 +264,7 @@ opt_status opt_linear_forward(const opt_linear_args* a, void* workspace, size_t 
 opt_status opt_linear_backward(const opt_linear_grad_args* a, void* workspace, size_t workspace_bytes, void* stream) {
   if (!a || !extents_ok(a->m, a->n, a->k)) return OPT_ERR_INVALID_ARG;
   if (a->act_prev < OPT_ACT_NONE || a->act_prev > OPT_ACT_SILU) return OPT_ERR_INVALID_ARG;
+  if (a->dx && a->act_prev != OPT_ACT_NONE && !a->z_prev && a->m > 0) return OPT_ERR_INVALID_ARG;
   MPOPT_TRY(check_vector(a->dw, true, 4));
   MPOPT_TRY(check_vector(a->dbias, true, 4));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -333,8 +333,9 @@ def linear(x, w, y, bias=None, act="none", residual=None, z=None, x_scale=None, 
 def linear_backward(dz, x, w, dx=None, z_prev=None, act_prev="none", dw=None, dbias=None, accumulate=True,
                     workspace=None, stream=None):
     """Gradients of z = x w^T + bias for dz [m][n] (bf16): dx [m][k] bf16 =
-    (dz w) * act_prev'(z_prev) (without z_prev: dz w); dw [n][k] and dbias [n]
-    fp32 main_grad buffers, added to or overwritten (accumulate=False).
+    (dz w) * act_prev'(z_prev) (with act_prev "none", which needs no z_prev,
+    dz w); dw [n][k] and dbias [n] fp32 main_grad buffers, added to or
+    overwritten (accumulate=False).
     Outputs left out are not computed; x and w may be None when only the other
     one's product is asked for."""
     torch = _torch or _load_torch()

@@ -1,6 +1,7 @@
 """What the feed-forward operators promise about their workspaces and check
 about their arguments, without a GPU."""
 
+import ctypes
 import itertools
 
 import pytest
@@ -152,3 +153,24 @@ def test_a_workspace_with_gaps_is_refused(recorded, name):
     with pytest.raises(ValueError, match="workspace"):
         f(**args, stream=0)
     assert not recorded
+
+
+# ------------------------------------------------- derivatives without z --
+
+def test_dx_through_an_activation_needs_its_argument():
+    """act_prev names a derivative that is taken at z_prev: dx without z_prev
+    is refused, not left without it.  Other outputs do not need z_prev."""
+    fake = 1 << 20
+    L = mp.lib()
+
+    def status(**kw):
+        a = mp.feedforward.OptLinearGradArgs(dz=fake, x=fake, w=fake, m=4, n=64, k=32, dz_ld=64, x_ld=32, w_ld=32, z_prev_ld=32,
+                                             dx_ld=32)
+        for name, v in kw.items():
+            setattr(a, name, v)
+        return L.opt_linear_backward(ctypes.byref(a), None, 0, None)      # no workspace: a call that is let through stops there
+    for act in (1, 2, 3):
+        assert status(dx=fake, act_prev=act) == mp.OPT_ERR_INVALID_ARG
+        assert status(dx=fake, act_prev=act, z_prev=fake) == mp.OPT_ERR_WORKSPACE
+        assert status(dw=fake, act_prev=act) == mp.OPT_ERR_WORKSPACE
+    assert status(dx=fake) == status(dx=fake, z_prev=fake) == mp.OPT_ERR_WORKSPACE
