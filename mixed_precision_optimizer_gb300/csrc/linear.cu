@@ -56,8 +56,9 @@ template <int kAct>
 __device__ __forceinline__ float activate_grad(float z) {
   if constexpr (kAct == OPT_ACT_RELU) return z > 0.f ? 1.f : 0.f;
   if constexpr (kAct == OPT_ACT_GELU) {
+    // z^2 kept finite: p (1 - p) is 0 where it would not be
     const float p = sigmoid(kGelu2 * (z + kGeluCubic * z * z * z));
-    return p + z * p * (1.f - p) * (kGelu2 * (1.f + 3.f * kGeluCubic * z * z));
+    return p + z * p * (1.f - p) * (kGelu2 * (1.f + 3.f * kGeluCubic * fminf(z * z, 1e30f)));
   }
   if constexpr (kAct == OPT_ACT_SILU) {
     const float p = sigmoid(z);

@@ -67,3 +67,22 @@ def test_norm_gradient_of_rows_of_any_magnitude(rows, cols, dy_off, h_off, dtype
     mag = np64(rstd)[:, None] * (np.abs(g) + np.abs(n) * np.mean(np.abs(g * n), 1, keepdims=True))
     within(dx, wx, (BF16 if dtype == torch.bfloat16 else 0) * np.abs(wx) + 2 * REL32 * mag, "dx")
     within(dgamma, wg, (rows + 8) * 2.0 ** -23 * np.sum(np.abs(np64(dy) * n), 0), "dgamma")
+
+
+# the split kernel with the lanes on columns (16, 32 and 64 rows) and on rows, the pair
+# kernel, and clusters of pairs; rows that move in 16-byte pieces and others
+@pytest.mark.parametrize("m,n,k", [(5, 64, 200), (30, 64, 200), (60, 1024, 200), (130, 128, 264), (2100, 100, 2300),
+                                   (1000, 2200, 1500), (40, 64, 201)])
+@pytest.mark.parametrize("kind", ["gelu", "silu"])
+def test_activation_gradient_of_large_values(m, n, k, kind):
+    """The derivative of gelu and silu is 1 or 0 far from zero, up to the
+    largest finite pre-activation."""
+    dz, w = normal(1, (m, n)), normal(2, (n, k), std=0.1)
+    far = torch.tensor([-3e38, -1e20, -3e19, -1e13, -60.0, 60.0, 1e13, 3e19, 1e20, 3e38], device="cuda")
+    z = far[torch.arange(m * k, device="cuda") % 10].to(torch.bfloat16).view(m, k)
+    dx = torch.full((m, k), float("nan"), dtype=torch.bfloat16, device="cuda")
+    mp.linear_backward(dz, None, w, dx=dx, z_prev=z, act_prev=kind, workspace=mp.linear_workspace(m, n, k))
+    plain = np64(dz) @ np64(w)
+    want = plain * O.act_grad(np64(z), kind)
+    err = (n + 8) * 2.0 ** -23 * (np.abs(np64(dz)) @ np.abs(np64(w)))
+    within(dx, want, BF16 * (np.abs(want) + err) + err, "dx")
