@@ -581,7 +581,7 @@ MPOPT_API opt_status opt_linear_forward(const opt_linear_args* args, void* works
  * Outputs that are NULL are not computed, and what only they need may be NULL.
  * Every sum has a fixed order: a call gives the same bits each time.  With
  * accumulate each element of dw is added once, in fp32, to what main_grad
- * holds (a subnormal result becomes zero).
+ * holds (subnormal values, what it holds and the result, count as zeros).
  */
 typedef struct {
   const uint16_t* dz;       /* [m][n] bf16                                     */

@@ -141,8 +141,8 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
 }
 
 // main_grad += without reading it: each element gets one addition per launch,
-// rounded to nearest in fp32, in L2 (subnormal results become zero), so the
-// result does not depend on an order.
+// rounded to nearest in fp32, in L2 (subnormal values and results become zero),
+// so the result does not depend on an order.
 __device__ __forceinline__ void red_add(float* p, float v) {
   asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
 }
@@ -924,9 +924,10 @@ linear_grad_kernel(const __grid_constant__ CUtensorMap dx_a, const __grid_consta
 // bytes) are turned in shared memory and stored 64 bytes at a time.
 //
 // dw sums over the tokens, and the tensor cores truncate each addition to the
-// accumulator: a sum of m tokens comes out low by about m 2^-30 of its value
-// (1.6e-5 at 16384).  So dw runs in segments of kDwSegment k-blocks (768
-// tokens, 7e-7): the epilogue adds each segment's accumulator to registers
+// accumulator: a sum of 16384 tokens comes out low by 1.6e-5 of its value when
+// the terms' signs are random and by 6.5e-5 when they are one (half of it where
+// two CTAs share the k-blocks).  So dw runs in segments of kDwSegment k-blocks
+// (768 tokens: 6e-7 at any number of tokens): the epilogue adds each segment's accumulator to registers
 // with rounding additions while the MMAs of the next segment run into the
 // other accumulator.  Two segments are also the time that a tile's stores have
 // before the MMAs stall: 8 k-blocks cost 6 % against one segment for all

@@ -86,3 +86,26 @@ def test_activation_gradient_of_large_values(m, n, k, kind):
     want = plain * O.act_grad(np64(z), kind)
     err = (n + 8) * 2.0 ** -23 * (np.abs(np64(dz)) @ np.abs(np64(w)))
     within(dx, want, BF16 * (np.abs(want) + err) + err, "dx")
+
+
+# dw of 16384 tokens by each kernel: pairs with a last wave of clusters, clusters alone, pairs with tiles
+# of 128 columns, and the split kernel with one and with two CTAs to a tile
+@pytest.mark.parametrize("n,k", [(2560, 2560), (1280, 1280), (19456, 100), (128, 10240), (128, 8192)])
+def test_weight_gradient_is_summed_in_segments(n, k):
+    """The tensor cores truncate each addition to the accumulator, 16 tokens at
+    a time.  Of positive terms an addition loses half a unit (2^-24 of the
+    partial sum) on average and the partial sum is half of the final one: 1024
+    additions in a row come out low by 1.5e-5 or more.  A segment of 768 tokens
+    is 48 additions, at most 48 * 2^-25 = 1.4e-6, and the rounding additions of
+    the segments do not add up; twice that is the bound."""
+    m = 16384
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    dz = torch.rand((m, n), generator=g, device="cuda").add_(0.5).to(torch.bfloat16)
+    x = torch.rand((m, k), generator=g, device="cuda").add_(0.5).to(torch.bfloat16)
+    dw = torch.full((n, k), float("nan"), device="cuda")
+    mp.linear_backward(dz, x, None, dw=dw, accumulate=False, workspace=mp.linear_workspace(m, n, k))
+    rows = torch.arange(0, n, max(1, n // 500), device="cuda")          # rows of every tile
+    want = dz[:, rows].double().t() @ x.double()
+    rel = float((dw[rows].double() - want).norm() / want.norm())
+    assert rel < 2 * 48 * 2.0 ** -25, rel
