@@ -464,7 +464,9 @@ MPOPT_API opt_status opt_selftest_wait_timeout(const float* G, float* O, int64_t
  *  - 8-bit values are e4m3 with one fp32 scale per row, value = q * scale:
  *      scale = max(max_j |y_j|, 1e-30) / 448,   q_j = rne_e4m3(y_j * (1 / scale))
  *    so the largest magnitude of a row maps to 448, and a row of zeros has
- *    q = 0.  A NaN stays a NaN; a row that holds an infinity has scale = inf
+ *    q = 0.  (y_j / scale in the second place of the product gives the same codes
+ *    but where it lies within two fp32 roundings of the middle between two of
+ *    them, which bf16 values meet: there either neighbour is the nearest.)  A NaN stays a NaN; a row that holds an infinity has scale = inf
  *    and stands for NaN throughout.
  *  - Zero rows (rows or m = 0) are allowed: nothing is read, and gradients of
  *    parameters are left as they are (accumulate) or set to zero.
@@ -480,7 +482,8 @@ MPOPT_API opt_status opt_selftest_wait_timeout(const float* G, float* O, int64_t
 enum { OPT_DTYPE_FP32 = 0, OPT_DTYPE_BF16 = 1, OPT_DTYPE_E4M3 = 2 };
 
 /* Activations: u; max(u, 0) (a NaN stays one); u (1 + tanh(sqrt(2/pi) (u +
-   0.044715 u^3))) / 2; u / (1 + exp(-u)). */
+   0.044715 u^3))) / 2; u / (1 + exp(-u)).  The last two are 0 where the factor
+   of u is below 2^-126 (silu: from u = -87 down, values under 1.1e-36). */
 enum { OPT_ACT_NONE = 0, OPT_ACT_RELU = 1, OPT_ACT_GELU = 2, OPT_ACT_SILU = 3 };
 
 /*

@@ -32,8 +32,7 @@ constexpr int kStageA = BM * kRowBytes;
 // (1 + tanh u) / 2 = sigmoid(2 u) both activations are u * sigmoid(t(u)).
 // 1 / (1 + 2^(-t log2 e)) from the two approximate instructions: each is within
 // 2 units, and the rounding of t log2 e adds 2^-23 |t| of the value, far below
-// the bf16 rounding that follows.  (exp and a division as CUDA functions cost
-// 35 issue slots an element in dx's epilogue, against 16 for these.)
+// the bf16 rounding that follows.  Below t = -87 the value, under 2^-126, is 0.
 __device__ __forceinline__ float sigmoid(float t) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * t));
@@ -448,7 +447,8 @@ template <int kBN>
 struct SplitConfig {
   static constexpr int kStageB = kBN * kRowBytes;
   static constexpr int kStageBytes = kStageA + kStageB;
-  static constexpr int kStages = kBN <= 16 ? 6 : kBN <= 32 ? 5 : kBN <= 64 ? 4 : 3;
+  static_assert(kBN == 16 || kBN == 32 || kBN == 64, "stages, and what join() loads at a time, are chosen for these");
+  static constexpr int kStages = kBN == 16 ? 6 : kBN == 32 ? 5 : 4;
   static constexpr uint32_t kSmemBytes = kStages * kStageBytes + 1024 /*align*/ + 256 /*barriers*/;
   static constexpr int kTmemCols = 2 * kBN < 32 ? 32 : 2 * kBN;     // two accumulators
   static_assert(kSmemBytes <= 116224, "two CTAs shall fit on an SM");
@@ -693,43 +693,38 @@ __device__ __forceinline__ void split_tile(const CUtensorMap& map_a, const CUten
   };
   // This rank's share of the columns of a cluster of kSplit, up to 32 at a
   // time with every peer's words and the epilogue's inputs in flight together
-  // (peers and 8 columns at a time one after the other, a tile of 128 columns
-  // spent 5 us here).
+  // (at most 64 words a lane).
   auto join = [&](auto split_tag) {
     constexpr int kSplit = decltype(split_tag)::value, kPer = kBN / kSplit;
     constexpr int kMost = kMode == kLinearDw ? 16 : 32;          // dw keeps its sums in registers
     constexpr int kN = kPer > kMost ? kMost : kPer < 4 ? 4 : kPer;     // kPer 2 (16 columns, 8 ranks): half of a word
-    constexpr int kGroup = kSplit * kN > 128 ? 128 / kSplit : kN;   // columns loaded at a time: 128 registers at most
     const uint32_t base = smem_u32(smem) + (quarter * 32 + lane) * 16;
 #pragma unroll
     for (int c0 = 0; c0 < kPer; c0 += kN) {
       const int c = rank * kPer + c0, c4 = c & ~3;
       if (n0 + c >= n_end) break;
       float v[kN];
+      float4 w[kSplit][kN / 4];
 #pragma unroll
-      for (int g = 0; g < kN; g += kGroup) {
-        float4 w[kSplit][kGroup / 4];
+      for (int p = 0; p < kSplit; ++p) {
+        const uint32_t peer = peer_addr(base, static_cast<uint32_t>(first_rank + p));
 #pragma unroll
-        for (int p = 0; p < kSplit; ++p) {
-          const uint32_t peer = peer_addr(base, static_cast<uint32_t>(first_rank + p));
+        for (int i = 0; i < kN / 4; ++i) w[p][i] = ld_cluster_f32x4(peer + (c4 / 4 + i) * (BM * 16));
+      }
 #pragma unroll
-          for (int i = 0; i < kGroup / 4; ++i) w[p][i] = ld_cluster_f32x4(peer + ((c4 + g) / 4 + i) * (BM * 16));
+      for (int i = 0; i < kN / 4; ++i) {
+        float4 t = w[0][i];
+#pragma unroll
+        for (int p = 1; p < kSplit; ++p) {
+          t.x += w[p][i].x;
+          t.y += w[p][i].y;
+          t.z += w[p][i].z;
+          t.w += w[p][i].w;
         }
-#pragma unroll
-        for (int i = 0; i < kGroup / 4; ++i) {
-          float4 t = w[0][i];
-#pragma unroll
-          for (int p = 1; p < kSplit; ++p) {
-            t.x += w[p][i].x;
-            t.y += w[p][i].y;
-            t.z += w[p][i].z;
-            t.w += w[p][i].w;
-          }
-          v[g + 4 * i] = t.x;
-          v[g + 4 * i + 1] = t.y;
-          v[g + 4 * i + 2] = t.z;
-          v[g + 4 * i + 3] = t.w;
-        }
+        v[4 * i] = t.x;
+        v[4 * i + 1] = t.y;
+        v[4 * i + 2] = t.z;
+        v[4 * i + 3] = t.w;
       }
       if constexpr (kPer < 4) {
         float part_word[kPer];

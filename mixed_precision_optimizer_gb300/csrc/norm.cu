@@ -2,7 +2,7 @@
 // (sm_103a):
 //
 //   h = x + residual;  rstd = 1 / sqrt(mean h^2 + eps);  y = h * rstd * gamma
-//   scale = max(max |y|, 1e-30) / 448;  q = rne_e4m3(y / scale)
+//   scale = max(max |y|, 1e-30) / 448;  q = rne_e4m3(y * (1 / scale))
 //
 //   n = h * rstd;  g = dy * gamma;  c = mean(g n)
 //   dx = rstd * (g - n c) + dh;  dgamma = sum over rows of dy n
@@ -16,8 +16,8 @@
 // (kVector).  Rows of an odd width start anywhere, but where all tensors' rows
 // start equally far past a multiple of 8 elements (dense ones do), the groups
 // of 8 begin at the row's first multiple of 8, and the up to 14 elements before
-// the first and after the last group go to one thread each (kShifted).  Otherwise single elements, neighbours in
-// neighbouring lanes (kSingle).
+// the first and after the last group go to one thread each (kShifted).
+// Otherwise single elements, neighbours in neighbouring lanes (kSingle).
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -278,7 +278,7 @@ rmsnorm_kernel(const __grid_constant__ RmsnormArgs a) {
   const int t = threadIdx.x % kTPR;
   const int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kTPR;
   if (r >= a.rows) return;                       // kTPR == 32: whole warps; otherwise the grid is exact
-  const int cols = static_cast<int>(a.cols);       // kNormMaxCols at most
+  const int cols = static_cast<int>(a.cols);       // kRegisterCols at most
   const Share s = share_of<kAccess>(a.shift + r * a.x_ld, cols, t);
   const bool edge = kAccess == kShifted && s.edge >= 0;
   float v[kNV][8], ve = 0.f;
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kTPR) rmsnorm_packed_kernel(const __grid_const
   wait_for_predecessors();
   const int t = threadIdx.x;
   const int64_t r = blockIdx.x;
-  const int cols = static_cast<int>(a.cols);       // kNormMaxCols at most
+  const int cols = static_cast<int>(a.cols);       // kRegisterCols at most
   const Share s = share_of<kVector>(0, cols, t);
   uint4 raw[kNV];
   {
@@ -530,7 +530,7 @@ rmsnorm_grad_kernel(const __grid_constant__ RmsnormGradArgs a) {
   let_next_start();
   wait_for_predecessors();
   const int t = threadIdx.x % kTPR, sub = threadIdx.x / kTPR;
-  const int cols = static_cast<int>(a.cols);       // kNormMaxCols at most
+  const int cols = static_cast<int>(a.cols);       // kRegisterCols at most
   const Share s = share_of<kAccess>(a.shift + blockIdx.x * a.h_ld, cols, t);
   const bool edge = kAccess == kShifted && s.edge >= 0;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
