@@ -491,7 +491,10 @@ enum { OPT_ACT_NONE = 0, OPT_ACT_RELU = 1, OPT_ACT_GELU = 2, OPT_ACT_SILU = 3 };
  *   h = x + residual          (residual NULL: h = x)
  *   rstd = 1 / sqrt(mean_j h_j^2 + eps)
  *   y_j = h_j * rstd * gamma_j
- * y is formed from the unrounded h.  Outputs that are NULL are not written.
+ * y is formed from the unrounded h.  Outputs that are NULL are not written.  The
+ * squares are summed in fp32, so the rms of a row is right from 1e-18 (below it
+ * eps decides, or with eps = 0 nothing does) to 1.8e19 / sqrt(cols); the gradient
+ * holds in the same range.
  */
 typedef struct {
   const void* x;          /* [rows][cols], dtype                               */

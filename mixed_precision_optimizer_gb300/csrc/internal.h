@@ -320,7 +320,8 @@ constexpr size_t kLinearHeaderBytes = 256;
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream);
 // dbias[n] (+)= column sums of dz [m][n], in slices of rows whose sums pass
 // through `partial` [column_sum_slices][n] when there is more than one: enough
-// CTAs of 64 columns to fill the GPU, at least 256 rows to a slice.
+// CTAs of 64 columns to fill the GPU (152 SMs, eight CTAs each; a constant, since
+// workspaces are sized without a GPU too), at least 256 rows to a slice.
 inline int64_t column_sum_slices(int64_t m, int64_t n) {
   const int64_t by_rows = (m + 255) / 256, wanted = (152 * 8 * 64 + n - 1) / n;
   const int64_t s = by_rows < wanted ? by_rows : wanted;
