@@ -622,6 +622,201 @@ enum { OPT_LINEAR_ANY_LAYOUT = 1 };
 MPOPT_API size_t opt_linear_workspace_size(int64_t m, int64_t n, int64_t k, int32_t flags);
 
 /*
+ * Language-model operators
+ * ------------------------
+ * What stands before, between and behind the feed-forward blocks when they
+ * train on tokens: the embedding and its gradient into main_grad, a gated
+ * recurrence along the rows (the operator that carries information from one
+ * token to the next), activations kept in 8 bits between the forward and the
+ * backward pass, and the loss with the logits' gradient.  The conventions are
+ * those of the feed-forward operators: row-major matrices with a row distance,
+ * sums and states in fp32, one rounding to an output's own type.  Every result
+ * has the same bits each time.  Outputs may not overlap inputs or one another
+ * but where an argument says so.
+ */
+
+/* Integer type of token and label arrays. */
+enum { OPT_INDEX_INT32 = 0, OPT_INDEX_INT64 = 1 };
+
+/*
+ * Embedding: y[r] = table[token[r]] * scale.  A token outside [0, vocab) (padding)
+ * gives a row of zeros.
+ */
+typedef struct {
+  const void* tokens;     /* [rows], index_dtype                               */
+  const void* table;      /* [vocab][cols], dtype                              */
+  void* y;                /* [rows][cols], y_dtype                             */
+  int64_t rows, vocab, cols;
+  int64_t table_ld, y_ld;
+  int32_t index_dtype;    /* OPT_INDEX_*                                       */
+  int32_t dtype, y_dtype; /* FP32 or BF16                                      */
+  float scale;            /* finite                                            */
+} opt_embedding_args;
+
+MPOPT_API opt_status opt_embedding_forward(const opt_embedding_args* args, void* stream);
+
+/*
+ * Gradient of the embedding, into the table's main_grad:
+ *   dtable[v] (+)= scale * sum over the rows r with token[r] = v of dy[r]
+ * Each sum is formed in fp32 in a fixed order: the rows with one token in
+ * ascending order, in pieces of the batch sorted by token.  Rows whose token is
+ * outside [0, vocab) are not read.  rows, vocab and cols are at most 2^30.
+ * Needs a workspace of opt_embedding_workspace_size bytes, whose contents do not
+ * matter; it serves calls with none of the three larger.
+ */
+typedef struct {
+  const void* tokens;     /* [rows], index_dtype                               */
+  const void* dy;         /* [rows][cols], dtype                               */
+  float* dtable;          /* [vocab][cols] fp32, dense                         */
+  int64_t rows, vocab, cols;
+  int64_t dy_ld;
+  int32_t index_dtype;
+  int32_t dtype;          /* FP32 or BF16                                      */
+  int32_t accumulate;     /* nonzero: dtable += ...; zero: dtable = ... (all of it) */
+  float scale;
+} opt_embedding_grad_args;
+
+MPOPT_API opt_status opt_embedding_backward(const opt_embedding_grad_args* args, void* workspace,
+                                            size_t workspace_bytes, void* stream);
+MPOPT_API size_t opt_embedding_workspace_size(int64_t rows, int64_t vocab, int64_t cols);
+
+/*
+ * Gated recurrence, for every column by itself, along the rows of a sequence:
+ *   h_t = h_{t-1} + c_t (x_t - h_{t-1}),  c_t = 1 / (1 + exp(-gate_t)),  y_t = h_t
+ * with h = h0 before the first row (zeros without h0) and hT = h behind the last.
+ * h is kept in fp32; y is its rounding.  x and gate are products of linear
+ * layers.
+ *
+ * The rows of `sequences` sequences are packed one behind the other:
+ *   starts [sequences + 1] (int32, on the device): sequence s has the rows
+ *     starts[s] .. starts[s + 1] - 1; starts does not decrease and stays in
+ *     [0, rows].  A sequence may be empty (hT = h0).  Rows before the first and
+ *     behind the last sequence are not read, and outputs are left as they are
+ *     there.
+ *   starts NULL: all have rows / sequences rows (which must divide), from one
+ *     (a step of single tokens) on.
+ * starts that break these rules give wrong results, but no access out of range.
+ *
+ * states, for opt_recurrence_backward: h before every opt_recurrence_state_rows-th
+ * row, [ceil(rows / state_rows)][cols] fp32.
+ *
+ * y may be x or gate itself (same pointer and row distance) when no gradient is
+ * wanted.  hT may be h0 itself when starts is NULL and each sequence has one row.
+ */
+typedef struct {
+  const void* x;          /* [rows][cols] dtype                                */
+  const void* gate;       /* [rows][cols] dtype                                */
+  const int32_t* starts;  /* see above                                         */
+  const float* h0;        /* [sequences][cols], or NULL                        */
+  void* y;                /* [rows][cols] dtype                                */
+  float* hT;              /* [sequences][cols], or NULL                        */
+  float* states;          /* see above, or NULL                                */
+  int64_t rows, cols, sequences;
+  int64_t x_ld, gate_ld, y_ld;
+  int32_t dtype;          /* FP32 or BF16                                      */
+  int32_t reserved;
+} opt_recurrence_args;
+
+MPOPT_API opt_status opt_recurrence_forward(const opt_recurrence_args* args, void* stream);
+
+/* Rows from one saved state to the next: 16 for BF16, 8 for FP32 (0 for others). */
+MPOPT_API int64_t opt_recurrence_state_rows(int32_t dtype);
+
+/*
+ * Gradient of opt_recurrence_forward from dy and dhT (NULL: zeros), with
+ * l_t = dy_t + (1 - c_{t+1}) l_{t+1}, where a sequence's last row has dhT in the
+ * second term's place:
+ *   dx_t = c_t l_t;  dgate_t = c_t (1 - c_t) l_t (x_t - h_{t-1});
+ *   dh0 = (1 - c) l of a sequence's first row (dhT for an empty sequence)
+ * h comes from states, which the forward call on the same x, gate, starts and h0
+ * wrote.  dx and dgate may each be dy, x or gate itself (same pointer and row
+ * distance).
+ */
+typedef struct {
+  const void* dy;         /* [rows][cols] dtype                                */
+  const void* x;          /* [rows][cols] dtype                                */
+  const void* gate;       /* [rows][cols] dtype                                */
+  const int32_t* starts;
+  const float* h0;        /* [sequences][cols], or NULL                        */
+  const float* states;
+  const float* dhT;       /* [sequences][cols], or NULL                        */
+  void* dx;               /* [rows][cols] dtype                                */
+  void* dgate;            /* [rows][cols] dtype                                */
+  float* dh0;             /* [sequences][cols], or NULL                        */
+  int64_t rows, cols, sequences;
+  int64_t dy_ld, x_ld, gate_ld, dx_ld, dgate_ld;
+  int32_t dtype;          /* FP32 or BF16                                      */
+  int32_t reserved;
+} opt_recurrence_grad_args;
+
+MPOPT_API opt_status opt_recurrence_backward(const opt_recurrence_grad_args* args, void* stream);
+
+/*
+ * Activation checkpoints in 8 bits.  Of each row, every OPT_CHECKPOINT_BLOCK
+ * columns (the last block may be shorter) share a power of two:
+ *   2^e, the smallest with max |x| <= 448 * 2^e over the block's finite values, e >= -116
+ *   q = rne_e4m3(x / 2^e);   scale byte = e + 127
+ * so a value is off by at most 2^-4 of itself or 2^(e-10), whichever is larger.
+ * Values are scaled by powers of two alone: x / 2^e is exact before its one
+ * rounding, and a restored value is exact in bf16.  An infinity or a NaN becomes
+ * a NaN and leaves its block's other values alone.
+ */
+enum { OPT_CHECKPOINT_BLOCK = 32 };
+MPOPT_API opt_status opt_checkpoint_save(const void* x, int64_t x_ld, int32_t dtype, int64_t rows, int64_t cols,
+                                         uint8_t* q, int64_t q_ld, uint8_t* scale, int64_t scale_ld, void* stream);
+
+/*
+ * A checkpoint's use in the backward pass, with z = q * 2^(scale - 127) (scale
+ * bytes from 11 to 247, as opt_checkpoint_save writes them):
+ *   z            the pre-activation (z_prev of opt_linear_backward)
+ *   y = act(z)   the next product's operand (x of opt_linear_backward)
+ *   dz = dy * act'(z)
+ * each of them optional, dz with dy.
+ */
+typedef struct {
+  const uint8_t* q;       /* [rows][cols] e4m3                                 */
+  const uint8_t* scale;   /* [rows][ceil(cols / 32)]                           */
+  const uint16_t* dy;     /* [rows][cols] bf16, or NULL                        */
+  uint16_t* z;            /* [rows][cols] bf16, or NULL                        */
+  uint16_t* y;            /* [rows][cols] bf16, or NULL                        */
+  uint16_t* dz;           /* [rows][cols] bf16, needs dy; may be dy itself     */
+  int64_t rows, cols;
+  int64_t q_ld, scale_ld, dy_ld, z_ld, y_ld, dz_ld;
+  int32_t act;            /* OPT_ACT_*                                         */
+  int32_t reserved;
+} opt_checkpoint_args;
+
+MPOPT_API opt_status opt_checkpoint_restore(const opt_checkpoint_args* args, void* stream);
+
+/*
+ * Cross-entropy of rows of logits against a label each, and its gradient:
+ *   lse = log(sum_j exp(logits_j));  loss = lse - logits_label
+ *   dlogits_j = (exp(logits_j - lse) - [j = label]) * scale * weight
+ * A label outside [0, cols) is ignored: its loss is 0, and so is its row of
+ * dlogits, whatever the logits hold.  Logits of -inf (masked columns) count as
+ * exp = 0; a label's own gives loss = inf.  A row that masks leave empty (all
+ * -inf) has lse = -inf, and with a label that counts loss = inf and dlogits = 0.
+ * A row with a NaN or +inf has NaN in lse, loss and dlogits.
+ */
+typedef struct {
+  const void* logits;     /* [rows][cols] dtype                                */
+  const void* labels;     /* [rows] index_dtype                                */
+  const float* weight;    /* [rows] factor of a row's gradient, or NULL (1)    */
+  float* loss;            /* [rows] (without weight and scale), or NULL        */
+  float* lse;             /* [rows], or NULL                                   */
+  void* dlogits;          /* [rows][cols] dtype, or NULL; may be logits itself
+                             (same pointer and row distance)                   */
+  int64_t rows, cols;
+  int64_t logits_ld, dlogits_ld;
+  int32_t dtype;          /* FP32 or BF16                                      */
+  int32_t index_dtype;    /* OPT_INDEX_*                                       */
+  float scale;            /* finite                                            */
+  int32_t reserved;
+} opt_cross_entropy_args;
+
+MPOPT_API opt_status opt_cross_entropy(const opt_cross_entropy_args* args, void* stream);
+
+/*
  * Optional launch instrumentation (off by default).  After
  *   opt_profile_launches(events, info, capacity, &count)
  * every kernel this library launches from the calling thread is bracketed by
@@ -667,7 +862,16 @@ enum {
   OPT_KERNEL_LINEAR_DBIAS = 19,
   OPT_KERNEL_LINEAR_REPACK = 20, /* operands (count of them) copied to 16-byte
                                    aligned rows; a, b of the largest             */
-  OPT_KERNEL_LINEAR_GRAD = 21   /* dx, dw and dbias of a short batch at once      */
+  OPT_KERNEL_LINEAR_GRAD = 21,  /* dx, dw and dbias of a short batch at once      */
+  OPT_KERNEL_EMBEDDING = 22,    /* language-model operators: a = rows, b = cols   */
+  OPT_KERNEL_EMBEDDING_SORT = 23, /* a = rows, b = vocab                          */
+  OPT_KERNEL_EMBEDDING_GRAD = 24,
+  OPT_KERNEL_EMBEDDING_JOIN = 25, /* sums of tokens that lie in several pieces    */
+  OPT_KERNEL_RECURRENCE = 26,
+  OPT_KERNEL_RECURRENCE_GRAD = 27,
+  OPT_KERNEL_CHECKPOINT_SAVE = 28,
+  OPT_KERNEL_CHECKPOINT_RESTORE = 29,
+  OPT_KERNEL_CROSS_ENTROPY = 30
 };
 
 MPOPT_API opt_status opt_profile_launches(void* const* events, opt_launch_info* info, int32_t capacity,
@@ -680,7 +884,7 @@ MPOPT_API const char* opt_strerror(opt_status status);
 MPOPT_API const char* opt_last_cuda_error(void);
 
 /* ABI version: (major << 16) | minor (2.0: Muon variants, scale shapes, clipping;
-   2.1: feed-forward operators). */
+   2.1: feed-forward operators; 2.2: language-model operators). */
 MPOPT_API int32_t opt_abi_version(void);
 
 #ifdef __cplusplus

@@ -18,6 +18,9 @@ Entry points (same names as the C ABI, without the ``opt_`` prefix):
 * ``rmsnorm``, ``rmsnorm_backward``, ``quantize_rows``, ``linear``,
   ``linear_backward`` -- the feed-forward operators around the parameters
   (``feedforward``)
+* ``embedding``, ``gated_recurrence``, ``checkpoint_save``, ``checkpoint_restore``,
+  ``cross_entropy`` and their gradients -- the language-model operators
+  (``language``)
 * ``sharded.shard_plan`` -- opt_shard_plan: the data-parallel sharding plan
   (``sharded`` also holds the per-rank views and the bf16 exchange)
 """
@@ -92,13 +95,18 @@ EXPORTED = ("opt_workspace_size", "opt_adamw_step", "opt_muon_step", "opt_mixed_
             "opt_strerror",
             "opt_last_cuda_error", "opt_abi_version",
             "opt_rmsnorm_forward", "opt_rmsnorm_backward", "opt_rmsnorm_workspace_size", "opt_quantize_rows",
-            "opt_linear_forward", "opt_linear_backward", "opt_linear_workspace_size")
+            "opt_linear_forward", "opt_linear_backward", "opt_linear_workspace_size",
+            "opt_embedding_forward", "opt_embedding_backward", "opt_embedding_workspace_size",
+            "opt_recurrence_forward", "opt_recurrence_backward", "opt_recurrence_state_rows",
+            "opt_checkpoint_save", "opt_checkpoint_restore", "opt_cross_entropy")
 
 KERNEL_NAMES = {0: "ns_gram", 1: "ns_poly", 2: "ns_bx", 3: "adamw", 4: "muon_momentum", 5: "muon_norm",
                 6: "muon_apply", 7: "muon_fixup", 8: "grad_norm", 9: "clip_finalize", 10: "muon_sample",
                 11: "ns_sym", 12: "rmsnorm", 13: "rmsnorm_grad", 14: "rmsnorm_dgamma", 15: "quantize_rows",
                 16: "linear", 17: "linear_dx", 18: "linear_dw", 19: "linear_dbias", 20: "linear_repack",
-                21: "linear_grad"}
+                21: "linear_grad", 22: "embedding", 23: "embedding_sort", 24: "embedding_grad", 25: "embedding_join",
+                26: "recurrence", 27: "recurrence_grad", 28: "checkpoint_save", 29: "checkpoint_restore",
+                30: "cross_entropy"}
 WORKSPACE_CLIP = 0x10
 WORKSPACE_GROUPED = 0x20
 
@@ -164,6 +172,7 @@ def lib():
     L.opt_abi_version.argtypes = []
     L.opt_abi_version.restype = i32
     feedforward.declare(L)
+    language.declare(L)
     _lib = L
     return L
 
@@ -487,3 +496,8 @@ class LaunchProfiler:
 from . import feedforward  # noqa: E402
 from .feedforward import (linear, linear_backward, linear_workspace, linear_workspace_size,  # noqa: E402,F401
                           quantize_rows, rmsnorm, rmsnorm_backward, rmsnorm_workspace, rmsnorm_workspace_size)
+# and the language-model operators
+from . import language  # noqa: E402
+from .language import (checkpoint_restore, checkpoint_save, cross_entropy, embedding, embedding_backward,  # noqa: E402,F401
+                       embedding_workspace, embedding_workspace_size, gated_recurrence, gated_recurrence_backward,
+                       recurrence_states)

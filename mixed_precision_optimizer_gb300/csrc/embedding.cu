@@ -1,0 +1,388 @@
+// Embedding lookup and its gradient (sm_103a):
+//
+//   y[r] = table[token[r]] * scale
+//   dtable[v] += scale * sum over the rows r with token[r] = v of dy[r]
+//
+// The lookup copies rows.  The gradient first sorts the rows by token, so that
+// the rows of one token are neighbours and one thread adds a column of all of
+// them in registers: dtable is touched once for each distinct token and no
+// addition is atomic.
+//   embedding_sort_kernel  a stable radix sort of (token, row) by one cluster
+//   embedding_sums_kernel  sums the runs of equal tokens within pieces of 64
+//                          sorted rows; a run that crosses a piece's border
+//                          leaves a partial sum for each piece
+//   embedding_join_kernel  adds the partial sums of such runs in order
+
+#include "elements.cuh"
+#include "internal.h"
+#include "overlap.cuh"
+
+namespace mpopt {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPiece = kEmbeddingPiece;
+
+bool rows_on_16(const void* p, int64_t ld, int es, int64_t rows) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || static_cast<uintptr_t>(ld) * es % 16 == 0);
+}
+
+__device__ __forceinline__ int64_t token_at(const void* tokens, int index_dtype, int64_t r) {
+  return index_dtype == OPT_INDEX_INT32 ? static_cast<int64_t>(static_cast<const int32_t*>(tokens)[r])
+                                        : static_cast<const int64_t*>(tokens)[r];
+}
+
+// ---------------------------------------------------------------- lookup --
+
+// A CTA has 2048 columns of a row (kVec), 8 to a thread, or 256 single ones.
+template <typename T, typename O, bool kVec>
+__global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_constant__ opt_embedding_args a, int64_t slices) {
+  let_next_start();
+  wait_for_predecessors();
+  const int64_t r = blockIdx.x / slices;
+  const int64_t c = ((blockIdx.x - r * slices) * kThreads + threadIdx.x) * (kVec ? 8 : 1);
+  if (c >= a.cols) return;
+  const int64_t token = token_at(a.tokens, a.index_dtype, r);
+  const bool known = token >= 0 && token < a.vocab;
+  const T* src = static_cast<const T*>(a.table) + (known ? token : 0) * a.table_ld + c;
+  O* dst = static_cast<O*>(a.y) + r * a.y_ld + c;
+  if constexpr (kVec) {
+    float v[8];
+    if (known) {
+      load8(src, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= a.scale;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    }
+    store8(dst, v);
+  } else {
+    store_elem(dst, known ? load_elem(src) * a.scale : 0.f);
+  }
+}
+
+template <typename T, typename O>
+cudaError_t lookup(const opt_embedding_args& a, cudaStream_t stream) {
+  const bool vec = a.cols % 8 == 0 && rows_on_16(a.table, a.table_ld, sizeof(T), a.vocab) &&
+                   rows_on_16(a.y, a.y_ld, sizeof(O), a.rows);
+  const int64_t per_cta = kThreads * (vec ? 8 : 1), slices = (a.cols + per_cta - 1) / per_cta;
+  const dim3 grid(static_cast<unsigned>(a.rows * slices));
+  return vec ? launch_overlapped(embedding_kernel<T, O, true>, grid, kThreads, 0, stream, 0, a, slices)
+             : launch_overlapped(embedding_kernel<T, O, false>, grid, kThreads, 0, stream, 0, a, slices);
+}
+
+// ------------------------------------------------------------------ sort --
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxBits = 10;                     // of a digit: [32][1024] counters fit shared memory
+constexpr int kSortCluster = 8;
+
+struct SortArgs {
+  const void* tokens;
+  int index_dtype;
+  int64_t rows, vocab;
+  EmbeddingScratch ws;
+  int passes, bits;
+  int64_t per_warp;      // rows of one warp, a multiple of 32
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// Orders global and distributed shared memory accesses of the cluster's threads.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_u32(const uint32_t* p, uint32_t rank) {
+  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+  uint32_t v;
+  asm volatile("{\n\t.reg .b32 m;\n\tmapa.shared::cluster.u32 m, %1, %2;\n\tld.shared::cluster.u32 %0, [m];\n\t}"
+               : "=r"(v)
+               : "r"(at), "r"(rank)
+               : "memory");
+  return v;
+}
+
+// Least significant digit first.  Every warp owns consecutive rows; a digit's
+// place is the rows of smaller digits, plus those with this digit of lower
+// CTAs, of lower warps, and earlier ones of the warp: a stable order.
+__global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __grid_constant__ SortArgs a) {
+  extern __shared__ uint32_t counts[];            // [kSortWarps][bins], then [bins] totals of this CTA
+  __shared__ uint32_t scan[kSortWarps];
+  let_next_start();
+  wait_for_predecessors();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t rank = cluster_rank(), ctas = cluster_size();
+  const int bins = 1 << a.bits;
+  uint32_t* total = counts + kSortWarps * bins;
+  uint32_t* mine = counts + warp * bins;
+  const int64_t first = (static_cast<int64_t>(rank) * kSortWarps + warp) * a.per_warp;
+  const int64_t last = first + a.per_warp < a.rows ? first + a.per_warp : a.rows;
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int shift = pass * a.bits;
+    const uint32_t *key_in = a.ws.key[pass & 1], *row_in = a.ws.row[pass & 1];
+    uint32_t *key_out = a.ws.key[(pass & 1) ^ 1], *row_out = a.ws.row[(pass & 1) ^ 1];
+    auto key_at = [&](int64_t i) {
+      if (pass) return key_in[i];
+      const int64_t t = token_at(a.tokens, a.index_dtype, i);
+      return static_cast<uint32_t>(t >= 0 && t < a.vocab ? t : a.vocab);
+    };
+    for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) counts[i] = 0;
+    __syncthreads();
+    for (int64_t i = first + lane; i - lane < last; i += 32) {
+      const uint32_t digit = i < last ? (key_at(i) >> shift) & (bins - 1) : static_cast<uint32_t>(bins);
+      const uint32_t same = __match_any_sync(0xffffffffu, digit);
+      if (i < last && lane == __ffs(same) - 1) mine[digit] += __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    // one thread to a digit (bins <= threads)
+    uint32_t sum = 0;
+    const int d = threadIdx.x;
+    if (d < bins) {
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t n = counts[w * bins + d];
+        counts[w * bins + d] = sum;
+        sum += n;
+      }
+      total[d] = sum;
+    }
+    cluster_sync();
+    uint32_t before = 0, all = 0;
+    if (d < bins) {
+      for (uint32_t r = 0; r < ctas; ++r) {
+        const uint32_t n = r == rank ? sum : peer_u32(total + d, r);
+        if (r < rank) before += n;
+        all += n;
+      }
+    }
+    // exclusive sum of `all` over the digits
+    uint32_t up = all;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, up, off);
+      if (lane >= off) up += o;
+    }
+    if (lane == 31) scan[warp] = up;
+    __syncthreads();
+    uint32_t base = up - all + before;
+    for (int w = 0; w < warp; ++w) base += scan[w];
+    if (d < bins)
+      for (int w = 0; w < kSortWarps; ++w) counts[w * bins + d] += base;
+    __syncthreads();
+    for (int64_t i = first + lane; i - lane < last; i += 32) {
+      const bool in = i < last;
+      const uint32_t key = in ? key_at(i) : 0u;
+      const uint32_t digit = in ? (key >> shift) & (bins - 1) : static_cast<uint32_t>(bins);
+      const uint32_t same = __match_any_sync(0xffffffffu, digit);
+      if (in) {
+        const uint32_t at = mine[digit] + __popc(same & ((1u << lane) - 1));
+        key_out[at] = key;
+        row_out[at] = pass ? row_in[i] : static_cast<uint32_t>(i);
+      }
+      __syncwarp();
+      if (in && lane == __ffs(same) - 1) mine[digit] += __popc(same);
+      __syncwarp();
+    }
+    cluster_sync();              // the next pass reads what other CTAs wrote; nobody leaves while `total` is read
+  }
+}
+
+// ------------------------------------------------------------------ sums --
+
+struct SumArgs {
+  opt_embedding_grad_args a;
+  const uint32_t *key, *row;
+  float* partial;
+  int64_t slices;          // CTAs to a piece
+};
+
+template <bool kVec>
+struct Columns {
+  static constexpr int kN = kVec ? 8 : 1;
+  static constexpr int64_t kPerCta = kThreads * kN;
+};
+
+template <bool kVec, typename T>
+__device__ __forceinline__ void load_columns(const T* p, float (&v)[Columns<kVec>::kN]) {
+  if constexpr (kVec) load8(p, v);
+  else v[0] = load_elem(p);
+}
+
+template <bool kVec>
+__device__ __forceinline__ void store_columns(float* p, const float (&v)[Columns<kVec>::kN]) {
+  if constexpr (kVec) store8(p, v);
+  else p[0] = v[0];
+}
+
+template <bool kVec>
+__device__ __forceinline__ void add_to_table(float* p, const float (&v)[Columns<kVec>::kN], float scale) {
+  float old[Columns<kVec>::kN];
+  load_columns<kVec>(static_cast<const float*>(p), old);
+#pragma unroll
+  for (int j = 0; j < Columns<kVec>::kN; ++j) old[j] += v[j] * scale;
+  store_columns<kVec>(p, old);
+}
+
+// A run's sum goes to the table if the run lies within the piece, else to the
+// piece's first partial row (a run that came from the piece before) or its
+// second (a run that starts here and goes on).
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kThreads) embedding_sums_kernel(const __grid_constant__ SumArgs p) {
+  constexpr int kN = Columns<kVec>::kN;
+  __shared__ uint32_t key[kPiece + 2], row[kPiece];
+  let_next_start();
+  wait_for_predecessors();
+  const opt_embedding_grad_args& a = p.a;
+  const int64_t piece = blockIdx.x / p.slices, first = piece * kPiece;
+  const int n = static_cast<int>(a.rows - first < kPiece ? a.rows - first : kPiece);
+  const uint32_t none = static_cast<uint32_t>(a.vocab);
+  // key[0] and key[n + 1]: the neighbouring pieces' (a token outside the table where there is none)
+  for (int i = threadIdx.x; i < n + 2; i += kThreads) {
+    const int64_t at = first + i - 1;
+    key[i] = at >= 0 && at < a.rows ? p.key[at] : none;
+  }
+  for (int i = threadIdx.x; i < n; i += kThreads) row[i] = p.row[first + i];
+  __syncthreads();
+  const int64_t c = (blockIdx.x - piece * p.slices) * Columns<kVec>::kPerCta + threadIdx.x * kN;
+  if (c >= a.cols) return;
+  const T* dy = static_cast<const T*>(a.dy) + c;
+  float sum[kN];
+#pragma unroll
+  for (int j = 0; j < kN; ++j) sum[j] = 0.f;
+  bool from_before = key[0] == key[1];
+  constexpr int kAhead = 4;                      // rows on their way
+  float next[kAhead][kN];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (u < n && key[u + 1] != none) load_columns<kVec>(dy + row[u] * a.dy_ld, next[u]);
+  for (int i0 = 0; i0 < n; i0 += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u;
+      if (i >= n) break;
+      const uint32_t v = key[i + 1];
+      if (v == none) return;                     // and so are all rows behind it
+#pragma unroll
+      for (int j = 0; j < kN; ++j) sum[j] += next[u][j];
+      if (i + kAhead < n && key[i + kAhead + 1] != none) load_columns<kVec>(dy + row[i + kAhead] * a.dy_ld, next[u]);
+      const bool ends_here = key[i + 2] != v;
+      if (!ends_here && i + 1 < n) continue;
+      if (from_before || !ends_here)
+        store_columns<kVec>(p.partial + (2 * piece + (from_before ? 0 : 1)) * a.cols + c, sum);
+      else
+        add_to_table<kVec>(a.dtable + v * a.cols + c, sum, a.scale);
+      from_before = false;
+#pragma unroll
+      for (int j = 0; j < kN; ++j) sum[j] = 0.f;
+    }
+  }
+}
+
+// The CTA of the piece in which a run starts that goes on behind it.
+template <bool kVec>
+__global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_constant__ SumArgs p) {
+  constexpr int kN = Columns<kVec>::kN;
+  let_next_start();
+  wait_for_predecessors();
+  const opt_embedding_grad_args& a = p.a;
+  const int64_t piece = blockIdx.x / p.slices, last = piece * kPiece + kPiece - 1;
+  if (last + 1 >= a.rows) return;
+  const uint32_t v = p.key[last];
+  if (v >= static_cast<uint32_t>(a.vocab) || p.key[last + 1] != v) return;
+  if (piece > 0 && p.key[piece * kPiece - 1] == v) return;        // it started earlier
+  const int64_t c = (blockIdx.x - piece * p.slices) * Columns<kVec>::kPerCta + threadIdx.x * kN;
+  if (c >= a.cols) return;
+  // the run's last row, by halving: key[lo] == v, key[hi] != v
+  int64_t lo = last + 1, hi = a.rows;
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) / 2;
+    if (p.key[mid] == v) lo = mid;
+    else hi = mid;
+  }
+  const int64_t last_piece = lo / kPiece;
+  float sum[kN];
+  load_columns<kVec>(p.partial + (2 * piece + 1) * a.cols + c, sum);
+  constexpr int kAhead = 8;
+  for (int64_t q0 = piece + 1; q0 <= last_piece; q0 += kAhead) {
+    float part[kAhead][kN];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (q0 + u <= last_piece) load_columns<kVec>(p.partial + 2 * (q0 + u) * a.cols + c, part[u]);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (q0 + u <= last_piece) {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) sum[j] += part[u][j];
+      }
+  }
+  add_to_table<kVec>(a.dtable + v * a.cols + c, sum, a.scale);
+}
+
+// 8 columns to a thread where rows of dy, the table and the partial sums start on 16 bytes.
+bool grad_vec(const opt_embedding_grad_args& a) {
+  return a.cols % 8 == 0 && rows_on_16(a.dy, a.dy_ld, a.dtype == kBf16 ? 2 : 4, a.rows) &&
+         reinterpret_cast<uintptr_t>(a.dtable) % 16 == 0;
+}
+
+SumArgs sum_args(const opt_embedding_grad_args& a, const EmbeddingScratch& ws, int sorted, bool vec) {
+  const int64_t per_cta = kThreads * (vec ? 8 : 1);
+  return SumArgs{a, ws.key[sorted], ws.row[sorted], ws.partial, (a.cols + per_cta - 1) / per_cta};
+}
+
+}  // namespace
+
+cudaError_t launch_embedding(const opt_embedding_args& a, cudaStream_t stream) {
+  if (a.dtype == kBf16)
+    return a.y_dtype == kBf16 ? lookup<__nv_bfloat16, __nv_bfloat16>(a, stream) : lookup<__nv_bfloat16, float>(a, stream);
+  return a.y_dtype == kBf16 ? lookup<float, __nv_bfloat16>(a, stream) : lookup<float, float>(a, stream);
+}
+
+cudaError_t launch_embedding_sort(const opt_embedding_grad_args& a, const EmbeddingScratch& ws, int* sorted,
+                                  cudaStream_t stream) {
+  int key_bits = 1;                              // of tokens 0 .. vocab
+  while (a.vocab >> key_bits) ++key_bits;
+  SortArgs s{a.tokens, a.index_dtype, a.rows, a.vocab, ws, (key_bits + kMaxBits - 1) / kMaxBits, 0, 0};
+  s.bits = (key_bits + s.passes - 1) / s.passes;
+  const int cluster = a.rows > 4096 ? kSortCluster : 1;
+  const int64_t warps = static_cast<int64_t>(cluster) * kSortWarps;
+  s.per_warp = ((a.rows + warps - 1) / warps + 31) & ~int64_t(31);
+  *sorted = s.passes & 1;
+  const size_t smem = static_cast<size_t>(kSortWarps + 1) * (size_t(1) << s.bits) * 4;
+  const cudaError_t e = cudaFuncSetAttribute(embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (kSortWarps + 1) * (1 << kMaxBits) * 4);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(embedding_sort_kernel, dim3(static_cast<unsigned>(cluster)), kSortThreads, smem, stream, cluster, s);
+}
+
+cudaError_t launch_embedding_sums(const opt_embedding_grad_args& a, const EmbeddingScratch& ws, int sorted,
+                                  cudaStream_t stream) {
+  const bool vec = grad_vec(a);
+  const SumArgs p = sum_args(a, ws, sorted, vec);
+  const dim3 grid(static_cast<unsigned>(embedding_pieces(a.rows) * p.slices));
+  if (a.dtype == kBf16)
+    return vec ? launch_overlapped(embedding_sums_kernel<__nv_bfloat16, true>, grid, kThreads, 0, stream, 0, p)
+               : launch_overlapped(embedding_sums_kernel<__nv_bfloat16, false>, grid, kThreads, 0, stream, 0, p);
+  return vec ? launch_overlapped(embedding_sums_kernel<float, true>, grid, kThreads, 0, stream, 0, p)
+             : launch_overlapped(embedding_sums_kernel<float, false>, grid, kThreads, 0, stream, 0, p);
+}
+
+cudaError_t launch_embedding_join(const opt_embedding_grad_args& a, const EmbeddingScratch& ws, int sorted,
+                                  cudaStream_t stream) {
+  const bool vec = grad_vec(a);
+  const SumArgs p = sum_args(a, ws, sorted, vec);
+  const dim3 grid(static_cast<unsigned>(embedding_pieces(a.rows) * p.slices));
+  return vec ? launch_overlapped(embedding_join_kernel<true>, grid, kThreads, 0, stream, 0, p)
+             : launch_overlapped(embedding_join_kernel<false>, grid, kThreads, 0, stream, 0, p);
+}
+
+}  // namespace mpopt

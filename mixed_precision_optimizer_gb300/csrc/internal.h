@@ -7,6 +7,8 @@
 #include <vector>
 #include <cuda_runtime.h>
 
+#include "../../include/mpopt.h"
+
 namespace mpopt {
 
 // ---------------------------------------------------------------- AdamW ----
@@ -361,6 +363,41 @@ struct RepackBatch {
   RepackMatrix m[3];
 };
 cudaError_t launch_repack(const RepackBatch& batch, int esize, cudaStream_t stream);
+
+// ------------------------------------------------ language-model operators --
+
+cudaError_t launch_embedding(const opt_embedding_args& a, cudaStream_t stream);
+
+// The embedding's gradient sums the rows of the batch sorted by token in pieces of
+// this many.
+constexpr int kEmbeddingPiece = 64;
+inline int64_t embedding_pieces(int64_t rows) { return (rows + kEmbeddingPiece - 1) / kEmbeddingPiece; }
+// Its workspace: two buffers of `rows` sort keys and two of row indices, then two
+// partial sums of `cols` columns for each piece.
+struct EmbeddingScratch {
+  uint32_t *key[2], *row[2];
+  float* partial;      // [pieces][2][cols]
+};
+// Sorts the rows by token (ascending, equal tokens in ascending order of rows;
+// tokens outside the table behind all others); *sorted: which of the two buffers
+// holds the result.
+cudaError_t launch_embedding_sort(const opt_embedding_grad_args& a, const EmbeddingScratch& ws, int* sorted,
+                                  cudaStream_t stream);
+cudaError_t launch_embedding_sums(const opt_embedding_grad_args& a, const EmbeddingScratch& ws, int sorted,
+                                  cudaStream_t stream);
+cudaError_t launch_embedding_join(const opt_embedding_grad_args& a, const EmbeddingScratch& ws, int sorted,
+                                  cudaStream_t stream);
+
+// Rows that a thread of the recurrence takes at a time; a state is saved before each group.
+constexpr int recurrence_state_rows(int dtype) { return dtype == kBf16 ? 16 : dtype == kFp32 ? 8 : 0; }
+cudaError_t launch_recurrence(const opt_recurrence_args& a, cudaStream_t stream);
+cudaError_t launch_recurrence_grad(const opt_recurrence_grad_args& a, cudaStream_t stream);
+
+cudaError_t launch_checkpoint_save(const void* x, int64_t x_ld, int dtype, int64_t rows, int64_t cols, uint8_t* q,
+                                   int64_t q_ld, uint8_t* scale, int64_t scale_ld, cudaStream_t stream);
+cudaError_t launch_checkpoint_restore(const opt_checkpoint_args& a, cudaStream_t stream);
+
+cudaError_t launch_cross_entropy(const opt_cross_entropy_args& a, cudaStream_t stream);
 
 // Records the CUDA error's text for opt_last_cuda_error; returns OPT_ERR_CUDA's value.
 int record_cuda_error(cudaError_t e, const char* where);
