@@ -756,6 +756,7 @@ MPOPT_API opt_status opt_recurrence_backward(const opt_recurrence_grad_args* arg
  * columns (the last block may be shorter) share a power of two:
  *   2^e, the smallest with max |x| <= 448 * 2^e over the block's finite values, e >= -116
  *   q = rne_e4m3(x / 2^e);   scale byte = e + 127
+ *   (with e = 120 at most 240: 256 * 2^120 is no finite number)
  * so a value is off by at most 2^-4 of itself or 2^(e-10), whichever is larger.
  * Values are scaled by powers of two alone: x / 2^e is exact before its one
  * rounding, and a restored value is exact in bf16.  An infinity or a NaN becomes

@@ -21,6 +21,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBlock = OPT_CHECKPOINT_BLOCK;
 constexpr int kMinExp = -116;            // the smallest code is 2^-9: restored values stay normal numbers
+constexpr int kMaxExp = 120;             // of the largest finite value, 2^128 less a step
+constexpr float kMaxTop = 240.f;         // the largest code there: 256 * 2^120 would be an infinity
 
 // Magnitude as an integer, 0 for an infinity or a NaN.
 __device__ __forceinline__ uint32_t magnitude(float v) {
@@ -41,6 +43,8 @@ __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(st
 __device__ __forceinline__ float code_input(float v, float inv) {
   return fabsf(v) == __uint_as_float(0x7f800000u) ? __uint_as_float(0x7fc00000u) : v * inv;
 }
+
+__device__ __forceinline__ float below_infinity(float v) { return v != v ? v : fminf(fmaxf(v, -kMaxTop), kMaxTop); }
 
 struct SaveArgs {
   const void* x;
@@ -76,6 +80,10 @@ __global__ void __launch_bounds__(kThreads) checkpoint_save_kernel(const __grid_
   const float inv = power_of_two(-e);
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = code_input(v[j], inv);
+  if (e == kMaxExp) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = below_infinity(v[j]);
+  }
   *reinterpret_cast<uint2*>(a.q + r * a.q_ld + g * 8) =
       make_uint2(e4m3x2(v[0], v[1]) | (e4m3x2(v[2], v[3]) << 16), e4m3x2(v[4], v[5]) | (e4m3x2(v[6], v[7]) << 16));
   if ((g & 3) == 0) a.scale[r * a.scale_ld + g / 4] = static_cast<uint8_t>(e + 127);
@@ -93,7 +101,8 @@ __global__ void __launch_bounds__(kThreads) checkpoint_save_single_kernel(const 
   const bool in = c < a.cols;
   const float v = in ? load_elem(static_cast<const T*>(a.x) + r * a.x_ld + c) : 0.f;
   const int e = scale_exponent(__reduce_max_sync(0xffffffffu, magnitude(v)));
-  if (in) a.q[r * a.q_ld + c] = e4m3(code_input(v, power_of_two(-e)));
+  const float t = code_input(v, power_of_two(-e));
+  if (in) a.q[r * a.q_ld + c] = e4m3(e == kMaxExp ? below_infinity(t) : t);
   if ((threadIdx.x & 31) == 0) a.scale[r * a.scale_ld + b] = static_cast<uint8_t>(e + 127);
 }
 
@@ -113,7 +122,7 @@ __device__ __forceinline__ float2 decode2(uint32_t codes) {
 // Bytes that no checkpoint has are taken as the nearest that it may have.
 __device__ __forceinline__ float scale_of(uint8_t byte) {
   const int b = byte, least = 127 + kMinExp;
-  return power_of_two((b < least ? least : b > 247 ? 247 : b) - 127);
+  return power_of_two((b < least ? least : b > 127 + kMaxExp ? 127 + kMaxExp : b) - 127);
 }
 
 template <int kAct>

@@ -10,7 +10,7 @@ import numpy as np
 from . import feedforward as F
 
 BLOCK = 32
-MIN_EXP = -116
+MIN_EXP, MAX_EXP = -116, 120
 
 
 def embedding(tokens, table, scale=1.0):
@@ -77,7 +77,9 @@ def checkpoint_save(x):
         k += amax > 448.0 * np.exp2(k)              # log2 may be off by a rounding
         k -= amax <= 448.0 * np.exp2(k - 1)
         e[:, b] = np.maximum(k, MIN_EXP).astype(int)
-        q[:, b * BLOCK:(b + 1) * BLOCK] = F.e4m3_rne(np.where(np.isfinite(part), part, np.nan) * np.exp2(-e[:, b, None].astype(float)))
+        v = np.where(np.isfinite(part), part, np.nan) * np.exp2(-e[:, b, None].astype(float))
+        v = np.where(e[:, b, None] == MAX_EXP, np.clip(v, -240.0, 240.0), v)       # 256 * 2^120 is no finite number
+        q[:, b * BLOCK:(b + 1) * BLOCK] = F.e4m3_rne(v)
     return q, e
 
 
