@@ -446,7 +446,8 @@ def test_checkpoint(rows, cols, dtype, layout):
         mp.checkpoint_restore(q, scale, z=z, y=y, act=act, dy=dy, dz=dz)
         assert np.array_equal(np64(z), wz)
         wy, wd = F.act(wz, act), F.act_grad(wz, act) * np64(dy)
-        tiny = 2.0 ** -126 * np.maximum(1, np.abs(wz))          # where the factor counts as 0
+        # where the factor counts as 0; and the oracle's own 1 + tanh, rounded in fp64 to 2^-53 beside a result of 1e-16 and less
+        tiny = (2.0 ** -126 + 2.0 ** -52) * np.maximum(1, np.abs(wz))
         within(y, wy, np.abs(wy) * (HALF + ACT) + tiny, act)
         within(dz, wd, HALF * 1.01 * np.abs(wd) + ACT * np.abs(np64(dy)) + tiny, act + " dz")
         for t in (z, y, dz):
