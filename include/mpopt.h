@@ -719,7 +719,7 @@ typedef struct {
 
 MPOPT_API opt_status opt_recurrence_forward(const opt_recurrence_args* args, void* stream);
 
-/* Rows from one saved state to the next: 16 for BF16, 8 for FP32 (0 for others). */
+/* Rows from one saved state to the next (0: no such dtype). */
 MPOPT_API int64_t opt_recurrence_state_rows(int32_t dtype);
 
 /*

@@ -50,43 +50,119 @@ struct SaveArgs {
   const void* x;
   uint8_t *q, *scale;
   int64_t rows, cols, x_ld, q_ld, scale_ld;
-  int64_t groups;        // of 8 columns to a row (vector access)
 };
 
+// A CTA's share where rows start on 16 bytes: 2^log_tpr threads to a row, a group
+// of 8 columns to each, and kRows rows to a thread, whose loads are on their way
+// together.
+struct Tiles {
+  int log_tpr;
+  uint32_t slices;       // CTAs to a row
+};
+
+struct Place {
+  int64_t row, group;    // of the first row
+  int step;              // rows from one of a thread's to the next
+};
+
+template <int kRows>
+__device__ __forceinline__ Place place_of(const Tiles& t) {
+  const uint32_t block = blockIdx.x / t.slices, slice = blockIdx.x - block * t.slices;
+  const int step = kThreads >> t.log_tpr;
+  return Place{static_cast<int64_t>(block) * step * kRows + (threadIdx.x >> t.log_tpr),
+               (static_cast<int64_t>(slice) << t.log_tpr) + (threadIdx.x & ((1 << t.log_tpr) - 1)), step};
+}
+
+// A group as loaded, and the largest of its magnitudes as the bits of an fp32 value
+// (an infinity's or a NaN's where it has one).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) checkpoint_save_kernel(const __grid_constant__ SaveArgs a) {
-  let_next_start();
-  wait_for_predecessors();
-  // four lanes to a block of 32 columns; lanes past the row's last group take part with zeros
-  const int64_t per_row = (a.groups + 3) & ~int64_t(3);
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t r = at / per_row;
-  const int64_t g = at - r * per_row;
-  const bool in = r < a.rows && g < a.groups;
+struct Group;
+template <>
+struct Group<__nv_bfloat16> {
+  uint4 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void clear() { w = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&v)[8]) const { unpack8(w, v); }
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t k = 0x7fff7fffu;
+    const uint32_t m = __vmaxu2(__vmaxu2(w.x & k, w.y & k), __vmaxu2(w.z & k, w.w & k));
+    return max(m << 16, m & 0xffff0000u);
+  }
+};
+template <>
+struct Group<float> {
   float v[8];
-  if (in) {
-    load8(static_cast<const T*>(a.x) + r * a.x_ld + g * 8, v);
-  } else {
+  __device__ __forceinline__ void load(const float* p) { load8(p, v); }
+  __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.f;
   }
-  uint32_t amax = 0;
+  __device__ __forceinline__ void get(float (&out)[8]) const {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) amax = max(amax, magnitude(v[j]));
-  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  if (!in) return;
-  const int e = scale_exponent(amax);
-  const float inv = power_of_two(-e);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = code_input(v[j], inv);
-  if (e == kMaxExp) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = below_infinity(v[j]);
+    for (int j = 0; j < 8; ++j) out[j] = v[j];
   }
-  *reinterpret_cast<uint2*>(a.q + r * a.q_ld + g * 8) =
-      make_uint2(e4m3x2(v[0], v[1]) | (e4m3x2(v[2], v[3]) << 16), e4m3x2(v[4], v[5]) | (e4m3x2(v[6], v[7]) << 16));
-  if ((g & 3) == 0) a.scale[r * a.scale_ld + g / 4] = static_cast<uint8_t>(e + 127);
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+    return m;
+  }
+};
+
+// The maximum over the four lanes of a block.
+__device__ __forceinline__ uint32_t block_max(uint32_t v) {
+  v = max(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return max(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+
+constexpr int kSaveRows = 4;
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) checkpoint_save_kernel(const __grid_constant__ SaveArgs a,
+                                                                   const __grid_constant__ Tiles tiles) {
+  let_next_start();
+  wait_for_predecessors();
+  const Place at = place_of<kSaveRows>(tiles);
+  Group<T> x[kSaveRows];
+  bool in[kSaveRows];
+#pragma unroll
+  for (int u = 0; u < kSaveRows; ++u) {
+    const int64_t r = at.row + u * at.step;
+    in[u] = r < a.rows && at.group * 8 < a.cols;       // lanes past the row take part with zeros
+    if (in[u]) x[u].load(static_cast<const T*>(a.x) + r * a.x_ld + at.group * 8);
+    else x[u].clear();
+  }
+#pragma unroll
+  for (int u = 0; u < kSaveRows; ++u) {
+    uint32_t amax = block_max(x[u].top());
+    float v[8];
+    x[u].get(v);
+    const bool odd = __any_sync(0xffffffffu, amax >= 0x7f800000u);
+    if (odd) {                                   // an infinity or a NaN in one of the warp's blocks
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, magnitude(v[j]));
+      amax = block_max(m);
+    }
+    if (!in[u]) continue;
+    const int64_t r = at.row + u * at.step;
+    const int e = scale_exponent(amax);
+    const float inv = power_of_two(-e);
+    if (odd || e == kMaxExp) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = code_input(v[j], inv);
+      if (e == kMaxExp) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = below_infinity(v[j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= inv;
+    }
+    *reinterpret_cast<uint2*>(a.q + r * a.q_ld + at.group * 8) =
+        make_uint2(e4m3x2(v[0], v[1]) | (e4m3x2(v[2], v[3]) << 16), e4m3x2(v[4], v[5]) | (e4m3x2(v[6], v[7]) << 16));
+    if ((at.group & 3) == 0) a.scale[r * a.scale_ld + at.group / 4] = static_cast<uint8_t>(e + 127);
+  }
 }
 
 template <typename T>
@@ -108,11 +184,6 @@ __global__ void __launch_bounds__(kThreads) checkpoint_save_single_kernel(const 
 
 // --------------------------------------------------------------- restore --
 
-struct RestoreArgs {
-  opt_checkpoint_args a;
-  int64_t groups;
-};
-
 // Two codes as fp32; e4m3 values are exact in fp16.
 __device__ __forceinline__ float2 decode2(uint32_t codes) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes & 0xffffu), __NV_E4M3);
@@ -125,44 +196,62 @@ __device__ __forceinline__ float scale_of(uint8_t byte) {
   return power_of_two((b < least ? least : b > 127 + kMaxExp ? 127 + kMaxExp : b) - 127);
 }
 
+constexpr int kRestoreRows = 2;
+
 template <int kAct>
-__global__ void __launch_bounds__(kThreads) checkpoint_restore_kernel(const __grid_constant__ RestoreArgs p) {
+__global__ void __launch_bounds__(kThreads) checkpoint_restore_kernel(const __grid_constant__ opt_checkpoint_args a,
+                                                                      const __grid_constant__ Tiles tiles) {
   let_next_start();
   wait_for_predecessors();
-  const opt_checkpoint_args& a = p.a;
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t r = at / p.groups, g = at - r * p.groups;
-  if (r >= a.rows) return;
-  const uint2 w = *reinterpret_cast<const uint2*>(a.q + r * a.q_ld + g * 8);
-  const float s = scale_of(a.scale[r * a.scale_ld + g / 4]);
-  float dy[8];
-  if (a.dz) load8(reinterpret_cast<const __nv_bfloat16*>(a.dy) + r * a.dy_ld + g * 8, dy);
-  float z[8], v[8];
-  const uint32_t u[2] = {w.x, w.y};
+  const Place at = place_of<kRestoreRows>(tiles);
+  const int64_t c = at.group * 8;
+  if (c >= a.cols) return;
+  uint2 w[kRestoreRows];
+  uint8_t byte[kRestoreRows];
+  uint4 dy[kRestoreRows];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 d = decode2(u[j / 2] >> (j % 2 * 16));
-    z[2 * j] = d.x * s;
-    z[2 * j + 1] = d.y * s;
+  for (int u = 0; u < kRestoreRows; ++u) {
+    const int64_t r = at.row + u * at.step;
+    if (r >= a.rows) break;
+    w[u] = *reinterpret_cast<const uint2*>(a.q + r * a.q_ld + c);
+    byte[u] = a.scale[r * a.scale_ld + at.group / 4];
+    if (a.dz) dy[u] = *reinterpret_cast<const uint4*>(a.dy + r * a.dy_ld + c);
   }
-  if (a.z) store8(reinterpret_cast<__nv_bfloat16*>(a.z) + r * a.z_ld + g * 8, z);
-  if (a.y) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = activate<kAct>(z[j]);
-    store8(reinterpret_cast<__nv_bfloat16*>(a.y) + r * a.y_ld + g * 8, v);
-  }
-  if (a.dz) {
+  for (int u = 0; u < kRestoreRows; ++u) {
+    const int64_t r = at.row + u * at.step;
+    if (r >= a.rows) break;
+    const float s = scale_of(byte[u]);
+    float z[8], v[8];
+    const uint32_t q[2] = {w[u].x, w[u].y};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = dy[j] * activate_grad<kAct>(z[j]);
-    store8(reinterpret_cast<__nv_bfloat16*>(a.dz) + r * a.dz_ld + g * 8, v);
+    for (int j = 0; j < 4; ++j) {
+      const float2 d = decode2(q[j / 2] >> (j % 2 * 16));
+      z[2 * j] = d.x * s;
+      z[2 * j + 1] = d.y * s;
+    }
+    if (a.z) store8(reinterpret_cast<__nv_bfloat16*>(a.z) + r * a.z_ld + c, z);
+    if (a.dz) {                                  // y and the derivative share their sigmoid
+      float g[8];
+      unpack8(dy[u], g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = activate<kAct>(z[j]);
+        g[j] *= activate_grad<kAct>(z[j]);
+      }
+      store8(reinterpret_cast<__nv_bfloat16*>(a.dz) + r * a.dz_ld + c, g);
+    } else if (a.y) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = activate<kAct>(z[j]);
+    }
+    if (a.y) store8(reinterpret_cast<__nv_bfloat16*>(a.y) + r * a.y_ld + c, v);
   }
 }
 
 template <int kAct>
-__global__ void __launch_bounds__(kThreads) checkpoint_restore_single_kernel(const __grid_constant__ RestoreArgs p) {
+__global__ void __launch_bounds__(kThreads) checkpoint_restore_single_kernel(const __grid_constant__ opt_checkpoint_args a) {
   let_next_start();
   wait_for_predecessors();
-  const opt_checkpoint_args& a = p.a;
   const int64_t blocks = (a.cols + kBlock - 1) / kBlock;
   const int64_t at = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / 32;
   const int64_t r = at / blocks, b = at - r * blocks;
@@ -183,40 +272,57 @@ bool rows_on(const void* p, int64_t ld, int es, int64_t rows, uintptr_t bytes) {
 
 dim3 grid_of(int64_t threads) { return dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads)); }
 
+// At least the four threads of a block to a row.
+Tiles tiles_of(int64_t cols) {
+  const int64_t groups = cols / 8;
+  int log_tpr = 2;
+  while (log_tpr < 8 && (int64_t(1) << log_tpr) < groups) ++log_tpr;
+  return Tiles{log_tpr, static_cast<uint32_t>((groups + (int64_t(1) << log_tpr) - 1) >> log_tpr)};
+}
+
+dim3 grid_of(const Tiles& t, int64_t rows, int rows_per_thread) {
+  const int64_t per_cta = static_cast<int64_t>(kThreads >> t.log_tpr) * rows_per_thread;
+  return dim3(static_cast<unsigned>((rows + per_cta - 1) / per_cta * t.slices));
+}
+
+template <typename T>
+cudaError_t save(const SaveArgs& a, bool vec, cudaStream_t stream) {
+  if (vec) {
+    const Tiles t = tiles_of(a.cols);
+    return launch_overlapped(checkpoint_save_kernel<T>, grid_of(t, a.rows, kSaveRows), kThreads, 0, stream, 0, a, t);
+  }
+  return launch_overlapped(checkpoint_save_single_kernel<T>, grid_of(a.rows * ((a.cols + kBlock - 1) / kBlock) * 32), kThreads, 0,
+                           stream, 0, a);
+}
+
 template <int kAct>
-cudaError_t restore_with(const RestoreArgs& p, bool vec, dim3 grid, cudaStream_t stream) {
-  return vec ? launch_overlapped(checkpoint_restore_kernel<kAct>, grid, kThreads, 0, stream, 0, p)
-             : launch_overlapped(checkpoint_restore_single_kernel<kAct>, grid, kThreads, 0, stream, 0, p);
+cudaError_t restore(const opt_checkpoint_args& a, bool vec, cudaStream_t stream) {
+  if (vec) {
+    const Tiles t = tiles_of(a.cols);
+    return launch_overlapped(checkpoint_restore_kernel<kAct>, grid_of(t, a.rows, kRestoreRows), kThreads, 0, stream, 0, a, t);
+  }
+  return launch_overlapped(checkpoint_restore_single_kernel<kAct>, grid_of(a.rows * ((a.cols + kBlock - 1) / kBlock) * 32),
+                           kThreads, 0, stream, 0, a);
 }
 
 }  // namespace
 
 cudaError_t launch_checkpoint_save(const void* x, int64_t x_ld, int dtype, int64_t rows, int64_t cols, uint8_t* q,
                                    int64_t q_ld, uint8_t* scale, int64_t scale_ld, cudaStream_t stream) {
-  const int es = dtype == kBf16 ? 2 : 4;
-  const bool vec = cols % 8 == 0 && rows_on(x, x_ld, es, rows, 16) && rows_on(q, q_ld, 1, rows, 8);
-  const SaveArgs a{x, q, scale, rows, cols, x_ld, q_ld, scale_ld, cols / 8};
-  if (vec) {
-    const dim3 grid = grid_of(rows * ((cols / 8 + 3) & ~int64_t(3)));
-    return dtype == kBf16 ? launch_overlapped(checkpoint_save_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, 0, a)
-                          : launch_overlapped(checkpoint_save_kernel<float>, grid, kThreads, 0, stream, 0, a);
-  }
-  const dim3 grid = grid_of(rows * ((cols + kBlock - 1) / kBlock) * 32);
-  return dtype == kBf16 ? launch_overlapped(checkpoint_save_single_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, 0, a)
-                        : launch_overlapped(checkpoint_save_single_kernel<float>, grid, kThreads, 0, stream, 0, a);
+  const bool vec = cols % 8 == 0 && rows_on(x, x_ld, dtype == kBf16 ? 2 : 4, rows, 16) && rows_on(q, q_ld, 1, rows, 8);
+  const SaveArgs a{x, q, scale, rows, cols, x_ld, q_ld, scale_ld};
+  return dtype == kBf16 ? save<__nv_bfloat16>(a, vec, stream) : save<float>(a, vec, stream);
 }
 
 cudaError_t launch_checkpoint_restore(const opt_checkpoint_args& a, cudaStream_t stream) {
   const bool vec = a.cols % 8 == 0 && rows_on(a.q, a.q_ld, 1, a.rows, 8) && rows_on(a.dy, a.dy_ld, 2, a.rows, 16) &&
                    rows_on(a.z, a.z_ld, 2, a.rows, 16) && rows_on(a.y, a.y_ld, 2, a.rows, 16) &&
                    rows_on(a.dz, a.dz_ld, 2, a.rows, 16);
-  const RestoreArgs p{a, a.cols / 8};
-  const dim3 grid = grid_of(vec ? a.rows * (a.cols / 8) : a.rows * ((a.cols + kBlock - 1) / kBlock) * 32);
   switch (a.act) {
-    case OPT_ACT_RELU: return restore_with<OPT_ACT_RELU>(p, vec, grid, stream);
-    case OPT_ACT_GELU: return restore_with<OPT_ACT_GELU>(p, vec, grid, stream);
-    case OPT_ACT_SILU: return restore_with<OPT_ACT_SILU>(p, vec, grid, stream);
-    default: return restore_with<OPT_ACT_NONE>(p, vec, grid, stream);
+    case OPT_ACT_RELU: return restore<OPT_ACT_RELU>(a, vec, stream);
+    case OPT_ACT_GELU: return restore<OPT_ACT_GELU>(a, vec, stream);
+    case OPT_ACT_SILU: return restore<OPT_ACT_SILU>(a, vec, stream);
+    default: return restore<OPT_ACT_NONE>(a, vec, stream);
   }
 }
 

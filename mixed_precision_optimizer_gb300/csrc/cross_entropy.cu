@@ -3,13 +3,19 @@
 //   lse = m + log(sum_j exp(x_j - m)), m = max_j x_j;  loss = lse - x_label
 //   dx_j = (exp(x_j - m) / sum - [j = label]) * scale * weight
 //
-// Bound by HBM: a row is read for its maximum and sum, kept together in one pass
-// (a thread's sum is scaled when its maximum grows), and the gradient written.
-// The second reading of the row comes out of L2.  A row of up to 1024 columns
-// belongs to a warp, a longer one to a CTA.  Groups of 16 bytes begin at the
-// row's first multiple of 16 bytes, the elements around them go to one thread
-// each.
+// Bound by HBM.  cross_entropy_cluster_kernel keeps a row on the chip: up to eight
+// CTAs of a cluster share it, each thread reads its 32 elements once, takes their
+// exponentials from its own maximum, and scales them when the row's maximum and
+// sum are known: one exponential an element (two, one for the sum and one for
+// the gradient, are 450 of the 620 us that the bytes of 8192 x 128256 in bf16
+// take).  The CTAs stay for many rows, and the next row's elements are on their
+// way (cp.async) meanwhile.  cross_entropy_kernel reads the row twice, the second
+// time out of L1 or L2: rows of up to 1024 columns by a warp each, and those
+// beyond eight CTAs' reach by a CTA.
+// Groups of 16 bytes begin at the row's first multiple of 16 bytes, the elements
+// around them go to one thread each.
 
+#include "cluster.cuh"
 #include "elements.cuh"
 #include "internal.h"
 #include "overlap.cuh"
@@ -143,11 +149,218 @@ cross_entropy_kernel(const __grid_constant__ opt_cross_entropy_args a) {
   }
 }
 
+// ---------------------------------------------------------------- cluster --
+
+// Threads of a CTA and elements of a thread; stages of the ring.
+constexpr int kElems = 32;
+constexpr int kMaxCluster = 8;
+
+template <typename T, int kThreads>
+struct Config {
+  static constexpr int kGroups = kElems / Group<T>::kN;            // of a thread
+  static constexpr int kStageBytes = kGroups * kThreads * 16;
+  static constexpr int kCtas = 1024 / kThreads;                    // to an SM: 64 registers a thread
+  static constexpr int kStages = (192 * 1024) / kCtas / kStageBytes;
+  static_assert(kStages >= 1, "the ring holds a row's share");
+};
+
+struct Place {
+  int64_t head, groups, end;       // the first group's column, their number, the column behind the last
+};
+
+template <typename T>
+__device__ __forceinline__ Place place_of(const T* x, int64_t cols) {
+  constexpr int kN = Group<T>::kN;
+  const int64_t ahead = -(reinterpret_cast<uintptr_t>(x) / sizeof(T)) & (kN - 1);
+  Place p;
+  p.head = ahead < cols ? ahead : cols;
+  p.groups = (cols - p.head) / kN;
+  p.end = p.head + p.groups * kN;
+  return p;
+}
+
+// The Stat of `n` values that the first lanes of a warp hold, in every lane.
+__device__ __forceinline__ Stat warp_join(Stat s, int most) {
+  float top = s.top;
+  for (int off = most / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  float sum = s.sum * exp_of(s.top - anchor(top));
+  for (int off = most / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  return Stat{top, sum};
+}
+
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, (Config<T, kThreads>::kCtas))
+cross_entropy_cluster_kernel(const __grid_constant__ opt_cross_entropy_args a, int cluster) {
+  using C = Config<T, kThreads>;
+  constexpr int kN = Group<T>::kN, kWarps = kThreads / 32, kGroups = C::kGroups;
+  extern __shared__ uint4 ring[];                // [kStages][kGroups][kThreads]
+  __shared__ float2 parts[2][kWarps], inbox[2][kMaxCluster];
+  let_next_start();
+  wait_for_predecessors();
+  const int t = threadIdx.x, lane = t & 31;
+  const int rank = cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
+  if (cluster > 1) cluster_sync();               // every CTA of the cluster has begun
+  const int64_t step = gridDim.x / cluster;
+  const int64_t mine = static_cast<int64_t>(rank) * kGroups * kThreads + t;     // this thread's first group
+  auto row_at = [&](int64_t r) { return static_cast<const T*>(a.logits) + r * a.logits_ld; };
+  auto label_at = [&](int64_t r) {
+    return a.index_dtype == OPT_INDEX_INT32 ? static_cast<int64_t>(static_cast<const int32_t*>(a.labels)[r])
+                                            : static_cast<const int64_t*>(a.labels)[r];
+  };
+  auto fetch = [&](int64_t r, int stage) {
+    if (r < a.rows) {
+      const T* x = row_at(r);
+      const Place p = place_of(x, a.cols);
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i)
+        if (mine + i * kThreads < p.groups)
+          copy16(ring + (stage * kGroups + i) * kThreads + t, x + p.head + (mine + i * kThreads) * kN);
+    }
+    copy_commit();
+  };
+  int64_t r = blockIdx.x / cluster;
+  for (int s = 0; s < C::kStages; ++s) fetch(r + s * step, s);
+  int64_t label = label_at(r), next_label = 0;   // the grid has no more clusters than rows
+  int parity = 0, stage = 0;
+  for (; r < a.rows; r += step, parity ^= 1, label = next_label) {
+    const T* x = row_at(r);
+    const Place p = place_of(x, a.cols);
+    if (r + step < a.rows) next_label = label_at(r + step);
+    const bool counts = label >= 0 && label < a.cols;
+    const float w = a.weight ? a.weight[r] * a.scale : a.scale;
+    float at_label = 0.f;
+    if (rank == 0 && t == 0 && counts) at_label = load_elem(x + label);
+    // the column outside of the groups that this thread has, or -1
+    const int64_t edge = rank ? -1 : t < p.head ? t : t < p.head + a.cols - p.end ? p.end + t - p.head : -1;
+    float e[kGroups][kN], ee = edge >= 0 ? load_elem(x + edge) : -INFINITY;
+    copy_wait<C::kStages - 1>();
+    float top = ee;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      if (mine + i * kThreads < p.groups) {
+        load_group(reinterpret_cast<const T*>(ring + (stage * kGroups + i) * kThreads + t), e[i]);
+#pragma unroll
+        for (int j = 0; j < kN; ++j) top = fmaxf(top, e[i][j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) e[i][j] = -INFINITY;
+      }
+    }
+    const float own = anchor(top);
+    float sum = ee = exp_of(ee - own);
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        e[i][j] = exp_of(e[i][j] - own);
+        sum += e[i][j];
+      }
+    fetch(r + C::kStages * step, stage);         // this thread's own places: it is done with them
+    stage = stage + 1 == C::kStages ? 0 : stage + 1;
+    Stat s = warp_join(Stat{top, sum}, 32);
+    if (lane == 0) parts[parity][t >> 5] = make_float2(s.top, s.sum);
+    __syncthreads();
+    const float2 part = lane < kWarps ? parts[parity][lane] : make_float2(-INFINITY, 0.f);
+    s = warp_join(Stat{part.x, part.y}, kWarps);
+    s = Stat{__shfl_sync(0xffffffffu, s.top, 0), __shfl_sync(0xffffffffu, s.sum, 0)};
+    if (cluster > 1) {
+      if (t < cluster) store_peer(at_peer(&inbox[parity][rank], t), make_float2(s.top, s.sum));
+      cluster_sync();
+      const float2 got = lane < cluster ? inbox[parity][lane] : make_float2(-INFINITY, 0.f);
+      s = warp_join(Stat{got.x, got.y}, kMaxCluster);
+      s = Stat{__shfl_sync(0xffffffffu, s.top, 0), __shfl_sync(0xffffffffu, s.sum, 0)};
+    }
+    const bool none = s.sum == 0.f;              // an empty row
+    if (rank == 0 && t == 0) {
+      const float log_sum = logf(s.sum);
+      if (a.lse) a.lse[r] = none ? -INFINITY : s.top + log_sum;
+      if (a.loss) a.loss[r] = !counts ? 0.f : none ? INFINITY : log_sum - (at_label - anchor(s.top));
+    }
+    if (!a.dlogits) continue;
+    T* g = static_cast<T*>(a.dlogits) + r * a.dlogits_ld;
+    const bool zero = !counts || none;
+    const float inv = exp_of(top - anchor(s.top)) / s.sum, inv_w = inv * w;
+    if (edge >= 0) store_elem(g + edge, zero ? 0.f : (ee * inv - (edge == label ? 1.f : 0.f)) * w);
+    const bool together = (reinterpret_cast<uintptr_t>(g + p.head) & 15u) == 0;
+    const int64_t hot = label - p.head;          // the label's element among the groups
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      const int64_t group = mine + i * kThreads;
+      if (group >= p.groups) break;
+      if (zero) {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) e[i][j] = 0.f;
+      } else if (group == hot / kN && hot >= 0) {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) e[i][j] = (e[i][j] * inv - (j == hot % kN ? 1.f : 0.f)) * w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) e[i][j] *= inv_w;
+      }
+      T* to = g + p.head + group * kN;
+      if (together) {
+        store_group(to, e[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) store_elem(to + j, e[i][j]);
+      }
+    }
+  }
+}
+
+// Clusters that the GPU holds at once (asked once for each device).
+template <typename T, int kThreads>
+int clusters_at_once(int cluster, size_t smem, cudaError_t* error) {
+  static thread_local int known_device = -1, known[kMaxCluster + 1];
+  int device = 0;
+  if ((*error = cudaGetDevice(&device)) != cudaSuccess) return 0;
+  if (device != known_device) {
+    for (int& k : known) k = 0;
+    known_device = device;
+  }
+  if (known[cluster] == 0) {
+    *error = cudaFuncSetAttribute(cross_entropy_cluster_kernel<T, kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  static_cast<int>(smem));
+    if (*error != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if ((*error = cudaOccupancyMaxActiveClusters(&n, cross_entropy_cluster_kernel<T, kThreads>, &cfg)) != cudaSuccess) return 0;
+    known[cluster] = n > 0 ? n : 1;
+  }
+  return known[cluster];
+}
+
+template <typename T, int kThreads>
+cudaError_t launch_cluster(const opt_cross_entropy_args& a, int cluster, cudaStream_t stream) {
+  using C = Config<T, kThreads>;
+  const size_t smem = static_cast<size_t>(C::kStages) * C::kStageBytes;
+  cudaError_t e = cudaSuccess;
+  const int64_t most = clusters_at_once<T, kThreads>(cluster, smem, &e);
+  if (e != cudaSuccess) return e;
+  const int64_t clusters = a.rows < most ? a.rows : most;
+  return launch_overlapped(cross_entropy_cluster_kernel<T, kThreads>, dim3(static_cast<unsigned>(clusters * cluster)), kThreads,
+                           smem, stream, cluster, a, cluster);
+}
+
 template <typename T>
 cudaError_t launch_rows(const opt_cross_entropy_args& a, cudaStream_t stream) {
   if (a.cols <= 1024)
     return launch_overlapped(cross_entropy_kernel<T, 32>, dim3(static_cast<unsigned>((a.rows + 7) / 8)), 256, 0, stream, 0, a);
-  return launch_overlapped(cross_entropy_kernel<T, 512>, dim3(static_cast<unsigned>(a.rows)), 512, 0, stream, 0, a);
+  if (a.cols <= 128 * kElems) return launch_cluster<T, 128>(a, 1, stream);
+  if (a.cols <= 256 * kElems) return launch_cluster<T, 256>(a, 1, stream);
+  int cluster = 1;
+  while (cluster < kMaxCluster && a.cols > static_cast<int64_t>(cluster) * 512 * kElems) cluster *= 2;
+  if (a.cols <= static_cast<int64_t>(cluster) * 512 * kElems) return launch_cluster<T, 512>(a, cluster, stream);
+  return launch_overlapped(cross_entropy_kernel<T, 1024>, dim3(static_cast<unsigned>(a.rows)), 1024, 0, stream, 0, a);
 }
 
 }  // namespace

@@ -13,6 +13,7 @@
 //                          leaves a partial sum for each piece
 //   embedding_join_kernel  adds the partial sums of such runs in order
 
+#include "cluster.cuh"
 #include "elements.cuh"
 #include "internal.h"
 #include "overlap.cuh"
@@ -34,31 +35,47 @@ __device__ __forceinline__ int64_t token_at(const void* tokens, int index_dtype,
 
 // ---------------------------------------------------------------- lookup --
 
-// A CTA has 2048 columns of a row (kVec), 8 to a thread, or 256 single ones.
+// A thread has 8 columns (kVec; else one) of kRows rows, whose loads are on their
+// way together: first the tokens, then the table's rows.  tpr threads to a row.
+constexpr int kRows = 4;
 template <typename T, typename O, bool kVec>
-__global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_constant__ opt_embedding_args a, int64_t slices) {
+__global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_constant__ opt_embedding_args a, int log_tpr,
+                                                             uint32_t slices) {
+  constexpr int kN = kVec ? 8 : 1;
   let_next_start();
   wait_for_predecessors();
-  const int64_t r = blockIdx.x / slices;
-  const int64_t c = ((blockIdx.x - r * slices) * kThreads + threadIdx.x) * (kVec ? 8 : 1);
+  const uint32_t block = blockIdx.x / slices, slice = blockIdx.x - block * slices;
+  const int64_t c = ((static_cast<int64_t>(slice) << log_tpr) + (threadIdx.x & ((1 << log_tpr) - 1))) * kN;
   if (c >= a.cols) return;
-  const int64_t token = token_at(a.tokens, a.index_dtype, r);
-  const bool known = token >= 0 && token < a.vocab;
-  const T* src = static_cast<const T*>(a.table) + (known ? token : 0) * a.table_ld + c;
-  O* dst = static_cast<O*>(a.y) + r * a.y_ld + c;
-  if constexpr (kVec) {
-    float v[8];
-    if (known) {
-      load8(src, v);
+  const int per_step = kThreads >> log_tpr;
+  const int64_t r0 = static_cast<int64_t>(block) * per_step * kRows + (threadIdx.x >> log_tpr);
+  int64_t token[kRows];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= a.scale;
+  for (int u = 0; u < kRows; ++u) {
+    const int64_t r = r0 + u * per_step;
+    token[u] = r < a.rows ? token_at(a.tokens, a.index_dtype, r) : -1;
+  }
+  float v[kRows][kN];
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    if (token[u] >= 0 && token[u] < a.vocab) {
+      const T* src = static_cast<const T*>(a.table) + token[u] * a.table_ld + c;
+      if constexpr (kVec) load8(src, v[u]);
+      else v[u][0] = load_elem(src);
+#pragma unroll
+      for (int j = 0; j < kN; ++j) v[u][j] *= a.scale;
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+      for (int j = 0; j < kN; ++j) v[u][j] = 0.f;
     }
-    store8(dst, v);
-  } else {
-    store_elem(dst, known ? load_elem(src) * a.scale : 0.f);
+  }
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const int64_t r = r0 + u * per_step;
+    if (r >= a.rows) return;
+    O* dst = static_cast<O*>(a.y) + r * a.y_ld + c;
+    if constexpr (kVec) store8(dst, v[u]);
+    else store_elem(dst, v[u][0]);
   }
 }
 
@@ -66,10 +83,13 @@ template <typename T, typename O>
 cudaError_t lookup(const opt_embedding_args& a, cudaStream_t stream) {
   const bool vec = a.cols % 8 == 0 && rows_on_16(a.table, a.table_ld, sizeof(T), a.vocab) &&
                    rows_on_16(a.y, a.y_ld, sizeof(O), a.rows);
-  const int64_t per_cta = kThreads * (vec ? 8 : 1), slices = (a.cols + per_cta - 1) / per_cta;
-  const dim3 grid(static_cast<unsigned>(a.rows * slices));
-  return vec ? launch_overlapped(embedding_kernel<T, O, true>, grid, kThreads, 0, stream, 0, a, slices)
-             : launch_overlapped(embedding_kernel<T, O, false>, grid, kThreads, 0, stream, 0, a, slices);
+  const int64_t groups = vec ? a.cols / 8 : a.cols;
+  int log_tpr = 0;
+  while (log_tpr < 8 && (int64_t(1) << log_tpr) < groups) ++log_tpr;
+  const int64_t slices = (groups + (int64_t(1) << log_tpr) - 1) >> log_tpr, per_cta = (kThreads >> log_tpr) * kRows;
+  const dim3 grid(static_cast<unsigned>((a.rows + per_cta - 1) / per_cta * slices));
+  return vec ? launch_overlapped(embedding_kernel<T, O, true>, grid, kThreads, 0, stream, 0, a, log_tpr, static_cast<uint32_t>(slices))
+             : launch_overlapped(embedding_kernel<T, O, false>, grid, kThreads, 0, stream, 0, a, log_tpr, static_cast<uint32_t>(slices));
 }
 
 // ------------------------------------------------------------------ sort --
@@ -87,30 +107,6 @@ struct SortArgs {
   int passes, bits;
   int64_t per_warp;      // rows of one warp, a multiple of 32
 };
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-// Orders global and distributed shared memory accesses of the cluster's threads.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t peer_u32(const uint32_t* p, uint32_t rank) {
-  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(p));
-  uint32_t v;
-  asm volatile("{\n\t.reg .b32 m;\n\tmapa.shared::cluster.u32 m, %1, %2;\n\tld.shared::cluster.u32 %0, [m];\n\t}"
-               : "=r"(v)
-               : "r"(at), "r"(rank)
-               : "memory");
-  return v;
-}
 
 // Least significant digit first.  Every warp owns consecutive rows; a digit's
 // place is the rows of smaller digits, plus those with this digit of lower
@@ -160,7 +156,7 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __gr
     uint32_t before = 0, all = 0;
     if (d < bins) {
       for (uint32_t r = 0; r < ctas; ++r) {
-        const uint32_t n = r == rank ? sum : peer_u32(total + d, r);
+        const uint32_t n = r == rank ? sum : load_peer_u32(at_peer(total + d, r));
         if (r < rank) before += n;
         all += n;
       }

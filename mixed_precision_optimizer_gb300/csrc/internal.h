@@ -389,7 +389,7 @@ cudaError_t launch_embedding_join(const opt_embedding_grad_args& a, const Embedd
                                   cudaStream_t stream);
 
 // Rows that a thread of the recurrence takes at a time; a state is saved before each group.
-constexpr int recurrence_state_rows(int dtype) { return dtype == kBf16 ? 16 : dtype == kFp32 ? 8 : 0; }
+constexpr int kRecurrenceStateRows = 8;
 cudaError_t launch_recurrence(const opt_recurrence_args& a, cudaStream_t stream);
 cudaError_t launch_recurrence_grad(const opt_recurrence_grad_args& a, cudaStream_t stream);
 

@@ -110,7 +110,7 @@ opt_status opt_embedding_backward(const opt_embedding_grad_args* a, void* worksp
              [&] { return launch_embedding_join(*a, ws, sorted, st); });
 }
 
-int64_t opt_recurrence_state_rows(int32_t dtype) { return recurrence_state_rows(dtype); }
+int64_t opt_recurrence_state_rows(int32_t dtype) { return float_dtype(dtype) ? kRecurrenceStateRows : 0; }
 
 opt_status opt_recurrence_forward(const opt_recurrence_args* a, void* stream) {
   if (!a || !float_dtype(a->dtype)) return OPT_ERR_INVALID_ARG;

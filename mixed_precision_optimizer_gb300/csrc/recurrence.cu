@@ -4,23 +4,24 @@
 //   l_t = dy_t + (1 - c_{t+1}) l_{t+1};  dx_t = c_t l_t
 //   dgate_t = c_t (1 - c_t) l_t (x_t - h_{t-1})
 //
-// Rows t1 .. t2 take a state h to  B + (1 - C) h,  where B is their result from
-// h = 0 and 1 - C the product of their 1 - c; the gradient passes them the same
-// way backwards.  C is kept, not 1 - C: slow channels have c far below 2^-24.
-// Two such pieces, the first (C1, B1) and behind it (C2, B2), make
-//   C = C1 + C2 - C1 C2,  B = B2 + (1 - C2) B1
-// A piece in which a sequence starts or ends does not depend on the state before
-// it: C = kReset, and B is selected, not multiplied, so that an infinity or a NaN
-// stays in its own sequence.
+// Rows t1 .. t2 take a state h to  P h + B, where B is their result from h = 0 and P
+// the product of their 1 - c; the gradient passes them the same way backwards.
+// Two such pieces, the first (P1, B1) and behind it (P2, B2), make
+//   P = P1 P2,  B = B2 + P2 B1
+// P is kept as P - c P, one rounding a row, no more than h's own.  A piece in which a
+// sequence starts or ends does not depend on the state before it: P = kReset,
+// and B is selected, not multiplied, so that an infinity or a NaN stays in its
+// own sequence.
 //
-// A warp has 64 columns, two to a lane, and 16 rows (bf16; fp32 8) at a time in
-// shared memory, fetched with cp.async while it works on the rows before.  Its
-// eight warps' pieces, and those of the CTAs of a cluster, which take the next
-// rows each, are joined through (distributed) shared memory; then every thread
-// runs through its rows again from the right state.  Bound by HBM: x and gate
-// are read once (and dy), the outputs written once; a state for every 16 rows
-// in fp32 is all that the gradient needs of the forward pass.
+// A warp has 64 columns, two to a lane, and 8 rows at a time in shared memory,
+// fetched with cp.async while it works on the rows before.  Its CTA's eight
+// pieces, and those of the CTAs of a cluster, which take the next rows each, are
+// joined through (distributed) shared memory; then every thread runs through its
+// rows again from the right state.  Bound by HBM: x and gate are read once (and
+// dy), the outputs written once; a state for every 8 rows in fp32 is all that the
+// gradient needs of the forward pass.
 
+#include "cluster.cuh"
 #include "elements.cuh"
 #include "internal.h"
 #include "overlap.cuh"
@@ -32,19 +33,20 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kCols = 64;                        // of a CTA
 constexpr int kMaxCluster = 8;                   // a warp of a CTA for each
-constexpr float kReset = 2.f;
+constexpr int kS = kRecurrenceStateRows;         // rows of a thread at a time
+constexpr int kChunk = kWarps * kS;              // of a CTA
+constexpr float kReset = -1.f;
 
 // ---------------------------------------------------------------- pieces --
 
 struct Piece {
-  float c, b;
+  float p, b;
 };
 __device__ __forceinline__ Piece then(Piece first, Piece second) {
-  if (second.c >= kReset) return second;
-  return Piece{first.c >= kReset ? kReset : fmaf(second.c, 1.f - first.c, first.c),
-               fmaf(-second.c, first.b, first.b) + second.b};
+  if (second.p < 0.f) return second;
+  return Piece{first.p < 0.f ? kReset : first.p * second.p, fmaf(second.p, first.b, second.b)};
 }
-__device__ __forceinline__ float through(Piece p, float h) { return p.c >= kReset ? p.b : fmaf(-p.c, h, h) + p.b; }
+__device__ __forceinline__ float through(Piece q, float h) { return q.p < 0.f ? q.b : fmaf(q.p, h, q.b); }
 
 // 1 / (1 + e^-g) from two approximate instructions of 2 units each; the rounding
 // of g log2 e adds 2^-24 |g| of the value.  0 below g = -87.
@@ -53,47 +55,23 @@ __device__ __forceinline__ float exp_neg(float g) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * g));
   return e;
 }
-__device__ __forceinline__ float update_gate(float g) {
+__device__ __forceinline__ float reciprocal(float v) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp_neg(g)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-// 1 - c, as exact as c where c is near one too.
-__device__ __forceinline__ float one_minus(float c, float g) { return g > 0.f ? c * exp_neg(g) : 1.f - c; }
-
-// --------------------------------------------------------------- cluster --
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t at_peer(const void* p, uint32_t rank) {
-  uint32_t m;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-               : "=r"(m)
-               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
-  return m;
-}
-__device__ __forceinline__ void store_peer(uint32_t at, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-               : "memory");
-}
-__device__ __forceinline__ void store_peer(uint32_t at, int64_t v) {
-  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
-}
+__device__ __forceinline__ float update_gate(float g) { return reciprocal(1.f + exp_neg(g)); }
 
 // ----------------------------------------------------------------- layout --
 
 template <typename T>
-struct Rows {
-  static constexpr int kS = 32 / sizeof(T);              // of a thread at a time
-  static constexpr int kChunk = kWarps * kS;             // of a CTA at a time
-  static constexpr int kTile = kS * kCols * sizeof(T);   // bytes of a warp's rows of one tensor
-};
+constexpr int kTile = kS * kCols * static_cast<int>(sizeof(T));   // bytes of a warp's rows of one tensor
+
+// CTAs to an SM, by registers and shared memory.
+template <typename T>
+constexpr int kForwardCtas = sizeof(T) == 2 ? 4 : 3;
+template <typename T>
+constexpr int kBackwardCtas = sizeof(T) == 2 ? 3 : 2;
 
 struct Plan {
   int cluster, ranges, groups;      // CTAs to a cluster; shares of the sequences; shares of the columns
@@ -106,18 +84,18 @@ struct Span {
 };
 
 struct Shared {
-  float4* pieces;        // [2][kWarps][32]: two columns' (c, b) of a warp
+  float4* pieces;        // [2][kWarps][32]: two columns' (p, b) of a warp
   float4* inbox;         // [2][cluster][32]: of a CTA
-  int* first;            // [kChunk] with starts: the sequence that a row starts, or -1
-  int* last;             // [kChunk]              the sequence that a row ends, or -1
+  int* first;            // [kChunk] with starts: the sequence that a row starts (set where one does)
+  int* last;             // [kChunk]              the sequence that a row ends
   Span* span;
 };
 
 template <typename T, int kTensors>
 struct Layout {
-  static constexpr int kStage = kTensors * Rows<T>::kTile * kWarps;
+  static constexpr int kStage = kTensors * kTile<T> * kWarps;
   static size_t bytes(int cluster) {
-    return 2 * kStage + 2 * kWarps * 512 + (cluster > 1 ? 2 * cluster * 512 : 0) + 2 * Rows<T>::kChunk * 4 + 64;
+    return 2 * kStage + 2 * kWarps * 512 + (cluster > 1 ? 2 * cluster * 512 : 0) + 2 * kChunk * 4 + 64;
   }
   static __device__ __forceinline__ Shared carve(uint8_t* base, int cluster) {
     Shared s;
@@ -125,8 +103,8 @@ struct Layout {
     s.pieces = reinterpret_cast<float4*>(base);
     s.inbox = s.pieces + 2 * kWarps * 32;
     s.first = reinterpret_cast<int*>(s.inbox + (cluster > 1 ? 2 * cluster * 32 : 0));
-    s.last = s.first + Rows<T>::kChunk;
-    s.span = reinterpret_cast<Span*>(s.last + Rows<T>::kChunk);
+    s.last = s.first + kChunk;
+    s.span = reinterpret_cast<Span*>(s.last + kChunk);
     return s;
   }
 };
@@ -187,10 +165,9 @@ struct Marks {
   int start_seq, end_seq;
 };
 
-template <typename T>
 __device__ __forceinline__ Marks marks_equal(const Plan& plan, const Span& span, int64_t row, int lane) {
   const int64_t r = row + lane;
-  const bool in = lane < Rows<T>::kS && r >= span.row && r < span.row_end;
+  const bool in = lane < kS && r >= span.row && r < span.row_end;
   Marks m;
   m.start_seq = m.end_seq = in ? static_cast<int>(static_cast<uint32_t>(r) / static_cast<uint32_t>(plan.length)) : 0;
   m.start = __ballot_sync(0xffffffffu, in && r == m.start_seq * plan.length);
@@ -198,43 +175,51 @@ __device__ __forceinline__ Marks marks_equal(const Plan& plan, const Span& span,
   return m;
 }
 
-// With starts, for the rows [row, row + kChunk) of the CTA.  `next` moves along the
-// sequences with the rows: starts before it (kBack: behind it) are of no use to
-// these rows and those that are taken after them.  All threads call.
-template <typename T, bool kBack>
-__device__ __forceinline__ void mark_rows(const int32_t* starts, int64_t rows, const Span& span, int64_t row, int64_t& next,
-                                          const Shared& sh) {
-  constexpr int kChunk = Rows<T>::kChunk;
-  const int64_t r0 = row > span.row ? row : span.row;
-  const int64_t r1 = row + kChunk < span.row_end ? row + kChunk : span.row_end;
-  for (int i = threadIdx.x; i < 2 * kChunk; i += kThreads) sh.first[i] = -1;       // first and last
-  for (int done = kThreads; done == kThreads; next += kBack ? -done : done) {
-    const int64_t i = kBack ? next - threadIdx.x : next + threadIdx.x;
+// With starts, for a warp's rows [row, row + kS).  `next` follows the rows: it is
+// moved to the first sequence of the span (its end counting as one) that does
+// not start before them, up or (kBack) down.  Most groups of rows have no mark:
+// one load and two ballots then.
+template <bool kBack>
+__device__ __forceinline__ Marks marks_ragged(const int32_t* starts, int64_t rows, const Span& span, int64_t row,
+                                              int64_t& next, const Shared& sh, int warp, int lane) {
+  const int64_t r0 = row > span.row ? row : span.row, r1 = row + kS < span.row_end ? row + kS : span.row_end;
+  Marks m{0, 0, -1, -1};
+  if (r0 >= r1) return m;
+  for (int n = 32; n == 32;) {
+    const int64_t i = kBack ? next - 1 - lane : next + lane;
     const bool there = i >= span.seq && i <= span.seq_end;
     const int64_t v = there ? start_at(starts, i, rows) : 0;
-    done = __syncthreads_count(there && (kBack ? v > r1 : v < r0));
+    n = __popc(__ballot_sync(0xffffffffu, there && (kBack ? v >= r0 : v < r0)));
+    next += kBack ? -n : n;
   }
-  int64_t at = next;
-  for (int within = kThreads; within == kThreads; at += kBack ? -kThreads : kThreads) {
-    const int64_t i = kBack ? at - threadIdx.x : at + threadIdx.x;
-    const bool there = i >= span.seq && i <= span.seq_end;
-    const int64_t v = there ? start_at(starts, i, rows) : 0;
-    if (there && r0 < r1) {
-      if (i < span.seq_end && v >= r0 && v < r1 && start_at(starts, i + 1, rows) > v) sh.first[v - row] = static_cast<int>(i);
-      if (i > span.seq && v > r0 && v <= r1 && start_at(starts, i - 1, rows) < v) sh.last[v - 1 - row] = static_cast<int>(i - 1);
+  int *first = sh.first + warp * kS, *last = sh.last + warp * kS;
+  uint32_t start = 0, end = 0;
+  for (int64_t base = next;; base += 32) {
+    const int64_t i = base + lane;
+    const bool here = i <= span.seq_end && start_at(starts, i, rows) <= r1;
+    const uint32_t any = __ballot_sync(0xffffffffu, here);
+    if (any == 0) break;
+    if (here) {
+      const int64_t v = start_at(starts, i, rows);
+      if (i < span.seq_end && v >= r0 && v < r1 && start_at(starts, i + 1, rows) > v) {
+        first[v - row] = static_cast<int>(i);
+        start |= 1u << (v - row);
+      }
+      if (i > span.seq && v > r0 && start_at(starts, i - 1, rows) < v) {
+        last[v - 1 - row] = static_cast<int>(i - 1);
+        end |= 1u << (v - 1 - row);
+      }
     }
-    within = __syncthreads_count(there && (kBack ? v >= r0 : v <= r1));
+    if (any != 0xffffffffu) break;
   }
-}
-
-template <typename T>
-__device__ __forceinline__ Marks marks_of(const Shared& sh, int warp, int lane) {
-  Marks m;
-  const bool in = lane < Rows<T>::kS;
-  m.start_seq = in ? sh.first[warp * Rows<T>::kS + lane] : -1;
-  m.end_seq = in ? sh.last[warp * Rows<T>::kS + lane] : -1;
-  m.start = __ballot_sync(0xffffffffu, m.start_seq >= 0);
-  m.end = __ballot_sync(0xffffffffu, m.end_seq >= 0);
+  m.start = __reduce_or_sync(0xffffffffu, start);
+  m.end = __reduce_or_sync(0xffffffffu, end);
+  if (m.start | m.end) {
+    __syncwarp();
+    if (m.start >> lane & 1) m.start_seq = first[lane];
+    if (m.end >> lane & 1) m.end_seq = last[lane];
+    __syncwarp();
+  }
   return m;
 }
 
@@ -254,7 +239,6 @@ __device__ __forceinline__ void pass_empty(const int32_t* starts, const Span& sp
 template <typename T, bool kVec>
 __device__ __forceinline__ void fetch_rows(uint8_t* dst, const void* src, int64_t ld, int64_t row, const Span& span,
                                            int64_t col, int64_t cols, int lane) {
-  constexpr int kS = Rows<T>::kS;
   const T* p = static_cast<const T*>(src);
   if constexpr (kVec) {
     constexpr int kPer = 16 / sizeof(T), kPieces = kCols / kPer;      // 16-byte pieces of a row
@@ -337,7 +321,7 @@ template <bool kBack>
 __device__ __forceinline__ void exchange(const Shared& sh, int parity, int cluster, uint32_t rank, int warp, int lane,
                                          const Piece (&mine)[2], float (&carry)[2], float (&state)[2]) {
   float4* pieces = sh.pieces + parity * kWarps * 32;
-  pieces[warp * 32 + lane] = make_float4(mine[0].c, mine[0].b, mine[1].c, mine[1].b);
+  pieces[warp * 32 + lane] = make_float4(mine[0].p, mine[0].b, mine[1].p, mine[1].b);
   __syncthreads();
   auto both = [](const float4& p, float (&h)[2]) {
     h[0] = through(Piece{p.x, p.y}, h[0]);
@@ -348,14 +332,14 @@ __device__ __forceinline__ void exchange(const Shared& sh, int parity, int clust
   if (cluster > 1) {
     float4* inbox = sh.inbox + parity * cluster * 32;
     if (warp < cluster) {                        // warp w tells CTA w of the cluster this CTA's piece
-      Piece p[2] = {{0.f, 0.f}, {0.f, 0.f}};
+      Piece p[2] = {{1.f, 0.f}, {1.f, 0.f}};
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) {
         const float4 q = pieces[(kBack ? kWarps - 1 - i : i) * 32 + lane];
         p[0] = then(p[0], Piece{q.x, q.y});
         p[1] = then(p[1], Piece{q.z, q.w});
       }
-      store_peer(at_peer(inbox + rank * 32 + lane, warp), make_float4(p[0].c, p[0].b, p[1].c, p[1].b));
+      store_peer(at_peer(inbox + rank * 32 + lane, warp), make_float4(p[0].p, p[0].b, p[1].p, p[1].b));
     }
     cluster_sync();
     for (int i = 0; i < cluster; ++i) {
@@ -380,10 +364,14 @@ __device__ __forceinline__ void exchange(const Shared& sh, int parity, int clust
 
 // --------------------------------------------------------------- forward --
 
+template <bool kValue>
+struct Flag {
+  static constexpr bool value = kValue;
+};
+
 template <typename T, bool kVec, bool kRagged>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kForwardCtas<T>)
 recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_constant__ Plan plan) {
-  constexpr int kS = Rows<T>::kS, kChunk = Rows<T>::kChunk, kTile = Rows<T>::kTile;
   using L = Layout<T, 2>;
   extern __shared__ __align__(128) uint8_t smem[];
   let_next_start();
@@ -391,76 +379,84 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
   const Shared sh = L::carve(smem, plan.cluster);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t rank = plan.cluster > 1 ? cluster_rank() : 0;
-  const int64_t id = blockIdx.x / plan.cluster, col = id % plan.groups * kCols;
+  const int id = blockIdx.x / plan.cluster;
+  const int64_t col = static_cast<int64_t>(id % plan.groups) * kCols;
   if (plan.cluster > 1) cluster_sync();          // every CTA of the cluster has begun
-  const Span span = span_of<kRagged>(plan, a.starts, a.rows, a.sequences, static_cast<int>(id / plan.groups), rank, sh);
+  const Span span = span_of<kRagged>(plan, a.starts, a.rows, a.sequences, id / plan.groups, rank, sh);
   if (kRagged && rank == 0) pass_empty(a.starts, span, a.hT, a.h0, col, a.cols);
   const int64_t base = span.row / kS * kS, step = static_cast<int64_t>(plan.cluster) * kChunk;
   const int64_t turns = span.row_end > span.row ? (span.row_end - base + step - 1) / step : 0;
-  int64_t next = span.seq;
-  auto row_of = [&](int64_t turn) { return base + turn * step + static_cast<int64_t>(rank) * kChunk; };
-  auto stage = [&](int64_t turn) { return smem + (turn & 1) * L::kStage + warp * 2 * kTile; };
-  auto fetch = [&](int64_t turn) {
-    if (turn < turns) {
-      const int64_t r = row_of(turn) + warp * kS;
+  int64_t next = span.seq, row = base + (static_cast<int64_t>(rank) * kWarps + warp) * kS;
+  auto stage = [&](int turn) { return smem + (turn & 1) * L::kStage + warp * 2 * kTile<T>; };
+  auto fetch = [&](int64_t r, int turn) {
+    if (r < span.row_end) {
       fetch_rows<T, kVec>(stage(turn), a.x, a.x_ld, r, span, col, a.cols, lane);
-      fetch_rows<T, kVec>(stage(turn) + kTile, a.gate, a.gate_ld, r, span, col, a.cols, lane);
+      fetch_rows<T, kVec>(stage(turn) + kTile<T>, a.gate, a.gate_ld, r, span, col, a.cols, lane);
     }
     copy_commit();
   };
-  fetch(0);
+  fetch(row, 0);
   float carry[2] = {0.f, 0.f};
-  for (int64_t turn = 0; turn < turns; ++turn) {
+  for (int turn = 0; turn < turns; ++turn, row += step) {
     copy_wait<0>();
     __syncwarp();
-    fetch(turn + 1);                             // over the rows of the turn before, which this warp is done with
-    const int64_t row = row_of(turn) + warp * kS;
+    fetch(row + step, turn + 1);                 // over the rows of the turn before, which this warp is done with
     Marks m;
-    if constexpr (kRagged) {
-      mark_rows<T, false>(a.starts, a.rows, span, row_of(turn), next, sh);
-      m = marks_of<T>(sh, warp, lane);
-    } else {
-      m = marks_equal<T>(plan, span, row, lane);
-    }
-    const uint8_t *xs = stage(turn), *gs = xs + kTile;
+    if constexpr (kRagged) m = marks_ragged<false>(a.starts, a.rows, span, row, next, sh, warp, lane);
+    else m = marks_equal(plan, span, row, lane);
+    const uint8_t *xs = stage(turn), *gs = xs + kTile<T>;
     float c[kS][2];
-    Piece mine[2] = {{0.f, 0.f}, {0.f, 0.f}};
+    Piece mine[2] = {{1.f, 0.f}, {1.f, 0.f}};
+    auto pieces = [&](auto plain) {              // plain: all rows are there, no sequence starts or ends
 #pragma unroll
-    for (int j = 0; j < kS; ++j) {
-      float g[2], x[2];
-      pair_at<T, kVec>(gs, j, lane, g);
-      pair_at<T, kVec>(xs, j, lane, x);
-      const bool in = row + j >= span.row && row + j < span.row_end;
-      if (m.start >> j & 1) {
-        float h0[2];
-        load_state<kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, a.cols, lane, h0);
-        mine[0].b = h0[0];
-        mine[1].b = h0[1];
-      }
+      for (int j = 0; j < kS; ++j) {
+        float g[2], x[2];
+        pair_at<T, kVec>(gs, j, lane, g);
+        pair_at<T, kVec>(xs, j, lane, x);
+        const bool in = plain.value || (row + j >= span.row && row + j < span.row_end);
+        if (!plain.value && (m.start >> j & 1)) {
+          float h0[2];
+          load_state<kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, a.cols, lane, h0);
+          mine[0].b = h0[0];
+          mine[1].b = h0[1];
+        }
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        c[j][k] = in ? update_gate(g[k]) : 0.f;
-        mine[k].b = fmaf(c[j][k], x[k] - mine[k].b, mine[k].b);
-        mine[k].c = fmaf(c[j][k], 1.f - mine[k].c, mine[k].c);
+        for (int k = 0; k < 2; ++k) {
+          c[j][k] = in ? update_gate(g[k]) : 0.f;
+          // a row that is not there leaves b alone, whatever lies in its place
+          mine[k].b = in ? fmaf(c[j][k], x[k] - mine[k].b, mine[k].b) : mine[k].b;
+          mine[k].p = fmaf(-c[j][k], mine[k].p, mine[k].p);
+        }
       }
-    }
-    if (m.start) mine[0].c = mine[1].c = kReset;
+      if (!plain.value && m.start) mine[0].p = mine[1].p = kReset;
+    };
+    const bool plain = row >= span.row && row + kS <= span.row_end && (m.start | m.end) == 0;
+    if (plain) pieces(Flag<true>{});
+    else pieces(Flag<false>{});
     float h[2];
-    exchange<false>(sh, static_cast<int>(turn & 1), plan.cluster, rank, warp, lane, mine, carry, h);
+    exchange<false>(sh, turn & 1, plan.cluster, rank, warp, lane, mine, carry, h);
     if (a.states && row >= span.row && row < span.row_end)
       store_pair<float, kVec>(a.states + row / kS * a.cols, col, a.cols, lane, h[0], h[1]);
     T* y = static_cast<T*>(a.y) + row * a.y_ld;
+    auto outputs = [&](auto plain) {
 #pragma unroll
-    for (int j = 0; j < kS; ++j, y += a.y_ld) {
-      float x[2];
-      pair_at<T, kVec>(xs, j, lane, x);
-      if (m.start >> j & 1) load_state<kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, a.cols, lane, h);
+      for (int j = 0; j < kS; ++j, y += a.y_ld) {
+        float x[2];
+        pair_at<T, kVec>(xs, j, lane, x);
+        const bool in = plain.value || (row + j >= span.row && row + j < span.row_end);
+        if (!plain.value && (m.start >> j & 1))
+          load_state<kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, a.cols, lane, h);
+        if (in) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) h[k] = fmaf(c[j][k], x[k] - h[k], h[k]);
-      if (row + j >= span.row && row + j < span.row_end) store_pair<T, kVec>(y, col, a.cols, lane, h[0], h[1]);
-      if ((m.end >> j & 1) && a.hT)
-        store_pair<float, kVec>(a.hT + __shfl_sync(0xffffffffu, m.end_seq, j) * a.cols, col, a.cols, lane, h[0], h[1]);
-    }
+          for (int k = 0; k < 2; ++k) h[k] = fmaf(c[j][k], x[k] - h[k], h[k]);
+          store_pair<T, kVec>(y, col, a.cols, lane, h[0], h[1]);
+        }
+        if (!plain.value && (m.end >> j & 1) && a.hT)
+          store_pair<float, kVec>(a.hT + __shfl_sync(0xffffffffu, m.end_seq, j) * a.cols, col, a.cols, lane, h[0], h[1]);
+      }
+    };
+    if (plain) outputs(Flag<true>{});
+    else outputs(Flag<false>{});
     __syncwarp();                                // the tile may be written over
   }
 }
@@ -501,11 +497,10 @@ __global__ void __launch_bounds__(kThreads) recurrence_step_kernel(const __grid_
 // -------------------------------------------------------------- gradient --
 
 // From the last row to the first.  Each warp runs through its rows forward from
-// the saved state for x_t - h_{t-1}, then backward.
+// the saved state for (1 - c) (x_t - h_{t-1}), then backward twice.
 template <typename T, bool kVec, bool kRagged>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kBackwardCtas<T>)
 recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const __grid_constant__ Plan plan) {
-  constexpr int kS = Rows<T>::kS, kChunk = Rows<T>::kChunk, kTile = Rows<T>::kTile;
   using L = Layout<T, 3>;
   extern __shared__ __align__(128) uint8_t smem[];
   let_next_start();
@@ -513,102 +508,114 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
   const Shared sh = L::carve(smem, plan.cluster);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t rank = plan.cluster > 1 ? cluster_rank() : 0;
-  const int64_t id = blockIdx.x / plan.cluster, col = id % plan.groups * kCols;
+  const int id = blockIdx.x / plan.cluster;
+  const int64_t col = static_cast<int64_t>(id % plan.groups) * kCols;
   if (plan.cluster > 1) cluster_sync();          // every CTA of the cluster has begun
-  const Span span = span_of<kRagged>(plan, a.starts, a.rows, a.sequences, static_cast<int>(id / plan.groups), rank, sh);
+  const Span span = span_of<kRagged>(plan, a.starts, a.rows, a.sequences, id / plan.groups, rank, sh);
   if (kRagged && rank == 0) pass_empty(a.starts, span, a.dh0, a.dhT, col, a.cols);
   const int64_t base = span.row / kS * kS, step = static_cast<int64_t>(plan.cluster) * kChunk;
   const int64_t turns = span.row_end > span.row ? (span.row_end - base + step - 1) / step : 0;
-  int64_t next = span.seq_end;
-  auto row_of = [&](int64_t turn) { return base + (turns - 1 - turn) * step + static_cast<int64_t>(rank) * kChunk; };
-  auto stage = [&](int64_t turn) { return smem + (turn & 1) * L::kStage + warp * 3 * kTile; };
-  auto fetch = [&](int64_t turn) {
-    if (turn < turns) {
-      const int64_t r = row_of(turn) + warp * kS;
+  int64_t next = span.seq_end + 1, row = base + (turns - 1) * step + (static_cast<int64_t>(rank) * kWarps + warp) * kS;
+  auto stage = [&](int turn) { return smem + (turn & 1) * L::kStage + warp * 3 * kTile<T>; };
+  auto fetch = [&](int64_t r, int turn) {
+    if (r >= base && r < span.row_end) {
       fetch_rows<T, kVec>(stage(turn), a.x, a.x_ld, r, span, col, a.cols, lane);
-      fetch_rows<T, kVec>(stage(turn) + kTile, a.gate, a.gate_ld, r, span, col, a.cols, lane);
-      fetch_rows<T, kVec>(stage(turn) + 2 * kTile, a.dy, a.dy_ld, r, span, col, a.cols, lane);
+      fetch_rows<T, kVec>(stage(turn) + kTile<T>, a.gate, a.gate_ld, r, span, col, a.cols, lane);
+      fetch_rows<T, kVec>(stage(turn) + 2 * kTile<T>, a.dy, a.dy_ld, r, span, col, a.cols, lane);
     }
     copy_commit();
   };
-  fetch(0);
+  auto saved = [&](int64_t r, float (&h)[2]) {   // h before row r, where that is a row of the span
+    load_state<kVec>(r >= span.row && r < span.row_end ? a.states : nullptr, r / kS, col, a.cols, lane, h);
+  };
+  float coming[2];
+  fetch(row, 0);
+  saved(row, coming);
   float carry[2] = {0.f, 0.f};
-  for (int64_t turn = 0; turn < turns; ++turn) {
-    const int64_t row = row_of(turn) + warp * kS;
-    float h[2];
-    load_state<kVec>(row >= span.row && row < span.row_end ? a.states : nullptr, row / kS, col, a.cols, lane, h);
+  for (int turn = 0; turn < turns; ++turn, row -= step) {
     copy_wait<0>();
     __syncwarp();
-    fetch(turn + 1);                             // over the rows of the turn before, which this warp is done with
+    float h[2] = {coming[0], coming[1]};
+    fetch(row - step, turn + 1);                 // over the rows of the turn before, which this warp is done with
+    saved(row - step, coming);
     Marks m;
-    if constexpr (kRagged) {
-      mark_rows<T, true>(a.starts, a.rows, span, row_of(turn), next, sh);
-      m = marks_of<T>(sh, warp, lane);
-    } else {
-      m = marks_equal<T>(plan, span, row, lane);
-    }
-    const uint8_t *xs = stage(turn), *gs = xs + kTile, *ys = gs + kTile;
-    float c[kS][2], d[kS][2];
+    if constexpr (kRagged) m = marks_ragged<true>(a.starts, a.rows, span, row, next, sh, warp, lane);
+    else m = marks_equal(plan, span, row, lane);
+    const uint8_t *xs = stage(turn), *gs = xs + kTile<T>, *ys = gs + kTile<T>;
+    float c[kS][2], q[kS][2];                    // q = (1 - c) (x_t - h_{t-1})
+    Piece mine[2] = {{1.f, 0.f}, {1.f, 0.f}};
+    auto pieces = [&](auto plain) {              // plain: all rows are there, no sequence starts or ends
 #pragma unroll
-    for (int j = 0; j < kS; ++j) {
-      float g[2], x[2];
-      pair_at<T, kVec>(gs, j, lane, g);
-      pair_at<T, kVec>(xs, j, lane, x);
-      const bool in = row + j >= span.row && row + j < span.row_end;
-      if (m.start >> j & 1) load_state<kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, a.cols, lane, h);
+      for (int j = 0; j < kS; ++j) {
+        float g[2], x[2];
+        pair_at<T, kVec>(gs, j, lane, g);
+        pair_at<T, kVec>(xs, j, lane, x);
+        const bool in = plain.value || (row + j >= span.row && row + j < span.row_end);
+        if (!plain.value && (m.start >> j & 1))
+          load_state<kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, a.cols, lane, h);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        c[j][k] = in ? update_gate(g[k]) : 0.f;
-        d[j][k] = x[k] - h[k];
-        h[k] = fmaf(c[j][k], d[j][k], h[k]);
-      }
-    }
-    Piece mine[2] = {{0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-    for (int j = kS - 1; j >= 0; --j) {
-      float dy[2];
-      pair_at<T, kVec>(ys, j, lane, dy);
-      if (m.end >> j & 1) {
-        float dhT[2];
-        load_state<kVec>(a.dhT, __shfl_sync(0xffffffffu, m.end_seq, j), col, a.cols, lane, dhT);
-        mine[0].b = dhT[0];
-        mine[1].b = dhT[1];
+        for (int k = 0; k < 2; ++k) {
+          const float e = exp_neg(g[k]), r = reciprocal(1.f + e), d = x[k] - h[k];
+          c[j][k] = in ? r : 0.f;
+          q[j][k] = (g[k] > 0.f ? e * r : 1.f - r) * d;       // 1 - c, as exact as c where c is near one too
+          h[k] = in ? fmaf(c[j][k], d, h[k]) : h[k];
+        }
       }
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float l = dy[k] + mine[k].b;
-        mine[k].b = (m.start >> j & 1) ? 0.f : fmaf(-c[j][k], l, l);
-        mine[k].c = fmaf(c[j][k], 1.f - mine[k].c, mine[k].c);
+      for (int j = kS - 1; j >= 0; --j) {
+        float dy[2];
+        pair_at<T, kVec>(ys, j, lane, dy);
+        const bool in = plain.value || (row + j >= span.row && row + j < span.row_end);
+        if (!plain.value && (m.end >> j & 1)) {
+          float dhT[2];
+          load_state<kVec>(a.dhT, __shfl_sync(0xffffffffu, m.end_seq, j), col, a.cols, lane, dhT);
+          mine[0].b = dhT[0];
+          mine[1].b = dhT[1];
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float l = dy[k] + mine[k].b;
+          mine[k].b = !in ? mine[k].b : !plain.value && (m.start >> j & 1) ? 0.f : fmaf(-c[j][k], l, l);
+          mine[k].p = fmaf(-c[j][k], mine[k].p, mine[k].p);
+        }
       }
-    }
-    if (m.start | m.end) mine[0].c = mine[1].c = kReset;
+      if (!plain.value && (m.start | m.end)) mine[0].p = mine[1].p = kReset;
+    };
+    const bool plain = row >= span.row && row + kS <= span.row_end && (m.start | m.end) == 0;
+    if (plain) pieces(Flag<true>{});
+    else pieces(Flag<false>{});
     float b[2];                                  // (1 - c) l of the row behind
-    exchange<true>(sh, static_cast<int>(turn & 1), plan.cluster, rank, warp, lane, mine, carry, b);
+    exchange<true>(sh, turn & 1, plan.cluster, rank, warp, lane, mine, carry, b);
     T* dx = static_cast<T*>(a.dx) + (row + kS - 1) * a.dx_ld;
     T* dg = static_cast<T*>(a.dgate) + (row + kS - 1) * a.dgate_ld;
+    auto outputs = [&](auto plain) {
 #pragma unroll
-    for (int j = kS - 1; j >= 0; --j, dx -= a.dx_ld, dg -= a.dgate_ld) {
-      float dy[2], g[2], ox[2], og[2];
-      pair_at<T, kVec>(ys, j, lane, dy);
-      pair_at<T, kVec>(gs, j, lane, g);
-      if (m.end >> j & 1) load_state<kVec>(a.dhT, __shfl_sync(0xffffffffu, m.end_seq, j), col, a.cols, lane, b);
+      for (int j = kS - 1; j >= 0; --j, dx -= a.dx_ld, dg -= a.dgate_ld) {
+        float dy[2], ox[2], og[2];
+        pair_at<T, kVec>(ys, j, lane, dy);
+        const bool in = plain.value || (row + j >= span.row && row + j < span.row_end);
+        if (!plain.value && (m.end >> j & 1))
+          load_state<kVec>(a.dhT, __shfl_sync(0xffffffffu, m.end_seq, j), col, a.cols, lane, b);
+        if (in) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float l = dy[k] + b[k];
-        ox[k] = c[j][k] * l;
-        og[k] = ox[k] * one_minus(c[j][k], g[k]) * d[j][k];
-        b[k] = fmaf(-c[j][k], l, l);
+          for (int k = 0; k < 2; ++k) {
+            const float l = dy[k] + b[k];
+            ox[k] = c[j][k] * l;
+            og[k] = ox[k] * q[j][k];
+            b[k] = fmaf(-c[j][k], l, l);
+          }
+          store_pair<T, kVec>(dx, col, a.cols, lane, ox[0], ox[1]);
+          store_pair<T, kVec>(dg, col, a.cols, lane, og[0], og[1]);
+        }
+        if (!plain.value && (m.start >> j & 1)) {
+          if (a.dh0)
+            store_pair<float, kVec>(a.dh0 + __shfl_sync(0xffffffffu, m.start_seq, j) * a.cols, col, a.cols, lane, b[0], b[1]);
+          b[0] = b[1] = 0.f;
+        }
       }
-      if (row + j >= span.row && row + j < span.row_end) {
-        store_pair<T, kVec>(dx, col, a.cols, lane, ox[0], ox[1]);
-        store_pair<T, kVec>(dg, col, a.cols, lane, og[0], og[1]);
-      }
-      if (m.start >> j & 1) {
-        if (a.dh0)
-          store_pair<float, kVec>(a.dh0 + __shfl_sync(0xffffffffu, m.start_seq, j) * a.cols, col, a.cols, lane, b[0], b[1]);
-        b[0] = b[1] = 0.f;
-      }
-    }
+    };
+    if (plain) outputs(Flag<true>{});
+    else outputs(Flag<false>{});
     __syncwarp();                                // the tile may be written over
   }
 }
@@ -620,12 +627,12 @@ bool rows_on(const void* p, int64_t ld, int es, int64_t rows, uintptr_t bytes) {
 }
 
 // How many CTAs share the rows of a sequence (a cluster) and how many shares the
-// sequences make, so that two CTAs of 64 columns to an SM have as few turns as
-// possible.  A share of ragged sequences is taken to be longer than the others by
+// sequences make, so that the CTAs of 64 columns that the SMs hold at once have as
+// few turns as possible.  A share of ragged sequences is taken to be longer than the others by
 // an average sequence.
-Plan make_plan(int64_t rows, int64_t cols, int64_t sequences, bool ragged, int chunk) {
+Plan make_plan(int64_t rows, int64_t cols, int64_t sequences, bool ragged, int ctas_per_sm) {
   Plan best{1, 1, static_cast<int>((cols + kCols - 1) / kCols), ragged ? 0 : rows / sequences};
-  const int64_t target = 2 * num_sms(), average = (rows + sequences - 1) / sequences;
+  const int64_t target = static_cast<int64_t>(ctas_per_sm) * num_sms(), average = (rows + sequences - 1) / sequences;
   double least = 0;
   for (int cluster = 1; cluster <= kMaxCluster; cluster *= 2) {
     int64_t ranges = target / (static_cast<int64_t>(best.groups) * cluster);
@@ -637,7 +644,7 @@ Plan make_plan(int64_t rows, int64_t cols, int64_t sequences, bool ragged, int c
     const int64_t most = ranges == 1 ? rows
                          : ragged    ? rows / ranges + average
                                      : (sequences + ranges - 1) / ranges * average;
-    const int64_t turns = (most + cluster * chunk - 1) / (static_cast<int64_t>(cluster) * chunk);
+    const int64_t turns = (most + cluster * kChunk - 1) / (cluster * kChunk);
     const int64_t waves = (ranges * best.groups * cluster + target - 1) / target;
     const double cost = static_cast<double>(turns * waves) * (cluster > 1 ? 1.25 : 1.0);
     if (cluster == 1 || cost < least) {
@@ -664,7 +671,7 @@ cudaError_t forward(const opt_recurrence_args& a, cudaStream_t stream) {
     return launch_overlapped(recurrence_step_kernel<T, kVec>, dim3(static_cast<unsigned>(a.rows * slices)), kThreads, 0, stream,
                              0, a, slices);
   }
-  const Plan plan = make_plan(a.rows, a.cols, a.sequences, a.starts != nullptr, Rows<T>::kChunk);
+  const Plan plan = make_plan(a.rows, a.cols, a.sequences, a.starts != nullptr, kForwardCtas<T>);
   const size_t smem = Layout<T, 2>::bytes(plan.cluster);
   return a.starts ? launch_plan(recurrence_kernel<T, kVec, true>, a, plan, smem, stream)
                   : launch_plan(recurrence_kernel<T, kVec, false>, a, plan, smem, stream);
@@ -672,7 +679,7 @@ cudaError_t forward(const opt_recurrence_args& a, cudaStream_t stream) {
 
 template <typename T, bool kVec>
 cudaError_t backward(const opt_recurrence_grad_args& a, cudaStream_t stream) {
-  const Plan plan = make_plan(a.rows, a.cols, a.sequences, a.starts != nullptr, Rows<T>::kChunk);
+  const Plan plan = make_plan(a.rows, a.cols, a.sequences, a.starts != nullptr, kBackwardCtas<T>);
   const size_t smem = Layout<T, 3>::bytes(plan.cluster);
   return a.starts ? launch_plan(recurrence_grad_kernel<T, kVec, true>, a, plan, smem, stream)
                   : launch_plan(recurrence_grad_kernel<T, kVec, false>, a, plan, smem, stream);

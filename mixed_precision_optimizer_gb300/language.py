@@ -28,12 +28,13 @@ import struct
 
 import mixed_precision_optimizer_gb300 as mp
 from . import feedforward as ff
-from .feedforward import ACTIVATIONS, DTYPE_BF16, _code, _elsewhere, _FLOAT, _lead, _mat, _stream, _vec, _workspace
+from .feedforward import ACTIVATIONS, _code, _elsewhere, _FLOAT, _lead, _mat, _stream, _vec, _workspace
 
 _vp, _i32, _i64, _sz, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 
 INDEX_INT32, INDEX_INT64 = 0, 1
 CHECKPOINT_BLOCK = 32
+STATE_ROWS = 8                # opt_recurrence_state_rows
 
 
 class OptEmbeddingArgs(ctypes.Structure):
@@ -188,15 +189,13 @@ def recurrence_states(rows, cols, dtype, device=None):
     """Buffer for gated_recurrence's states: what gated_recurrence_backward needs
     of a forward pass over this many rows of this type (bf16 or fp32)."""
     torch = _torch or _load_torch()
-    code = ff._CODES.get(dtype)
-    if code not in _FLOAT:
+    if ff._CODES.get(dtype) not in _FLOAT:
         raise TypeError(f"unsupported type, {dtype}")
-    step = int(mp.lib().opt_recurrence_state_rows(code))
-    return torch.empty((-(-int(rows) // step), int(cols)), dtype=torch.float32, device=device or "cuda")
+    return torch.empty((-(-int(rows) // STATE_ROWS), int(cols)), dtype=torch.float32, device=device or "cuda")
 
 
-def _states(t, code, rows, cols, dev):
-    return _grid(t, -(-rows // (16 if code == DTYPE_BF16 else 8)), cols, "states", dev)
+def _states(t, rows, cols, dev):
+    return _grid(t, -(-rows // STATE_ROWS), cols, "states", dev)
 
 
 def _sequences(starts, sequences):
@@ -225,7 +224,7 @@ def gated_recurrence(x, gate, y, starts=None, sequences=None, h0=None, hT=None, 
     sequences = _sequences(starts, sequences)
     sp = _vec(starts, torch.int32, sequences + 1, "starts", dev)
     a = _PACK_RECURRENCE(xp, gp, sp, _grid(h0, sequences, cols, "h0", dev), yp, _grid(hT, sequences, cols, "hT", dev),
-                         _states(states, code, rows, cols, dev), rows, cols, sequences, xl, gl, yl, code, 0)
+                         _states(states, rows, cols, dev), rows, cols, sequences, xl, gl, yl, code, 0)
     status = mp.lib().opt_recurrence_forward(a, _stream(stream, dev))
     if status:
         mp._check(status, "opt_recurrence_forward")
@@ -245,7 +244,7 @@ def gated_recurrence_backward(dy, x, gate, states, dx, dgate, starts=None, seque
     dgp, dgl = _mat(dgate, dt, rows, cols, "dgate", dev)
     sequences = _sequences(starts, sequences)
     sp = _vec(starts, torch.int32, sequences + 1, "starts", dev)
-    a = _PACK_RECURRENCE_GRAD(yp, xp, gp, sp, _grid(h0, sequences, cols, "h0", dev), _states(states, code, rows, cols, dev),
+    a = _PACK_RECURRENCE_GRAD(yp, xp, gp, sp, _grid(h0, sequences, cols, "h0", dev), _states(states, rows, cols, dev),
                               _grid(dhT, sequences, cols, "dhT", dev), dxp, dgp, _grid(dh0, sequences, cols, "dh0", dev),
                               rows, cols, sequences, yl, xl, gl, dxl, dgl, code, 0)
     status = mp.lib().opt_recurrence_backward(a, _stream(stream, dev))

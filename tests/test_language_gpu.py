@@ -10,8 +10,9 @@ Tolerances, from the formats and the order of operations:
   2^-20 (GATE);
 * the recurrence: with M the largest |x|, |h0| of a column (so |h| <= M), a row
   adds its own rounding and that of x - h (2^-23 M), c's error times |x - h|, and,
-  every 16 rows, the joining of two pieces (2 roundings, and 1 - C's error, which
-  is that of its c's); twice the first and four times the second cover both:
+  every 8 rows, the joining of pieces (2 roundings, and the error of the product
+  of 1 - c: a rounding a row and that of its c's); twice the first and four times
+  the second cover both:
     e_t = (1 - c_t) e_{t-1} + M (2^-22 + 4 c_t GATE)
   and the same backwards for l with M the largest |l|;
 * an activation is within 2^-16 of itself (sigmoid(t), 2^-24 |t| of the value for

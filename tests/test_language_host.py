@@ -179,7 +179,7 @@ def test_recurrence_backward_refusals(L, kw, want):
 
 
 def test_state_rows(L):
-    assert [L.opt_recurrence_state_rows(d) for d in (0, 1, 2, -1)] == [8, 16, 0, 0]
+    assert [L.opt_recurrence_state_rows(d) for d in (0, 1, 2, -1)] == [lm.STATE_ROWS, lm.STATE_ROWS, 0, 0]
 
 
 @pytest.mark.parametrize("args,want", [
