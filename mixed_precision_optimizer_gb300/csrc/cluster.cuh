@@ -41,10 +41,8 @@ __device__ __forceinline__ void store_peer(uint32_t at, float2 v) {
 __device__ __forceinline__ void store_peer(uint32_t at, int64_t v) {
   asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
 }
-__device__ __forceinline__ uint32_t load_peer_u32(uint32_t at) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return v;
+__device__ __forceinline__ void store_peer(uint32_t at, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
 }  // namespace

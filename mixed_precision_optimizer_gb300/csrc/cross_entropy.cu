@@ -164,27 +164,44 @@ struct Config {
   static_assert(kStages >= 1, "the ring holds a row's share");
 };
 
+// A row in elements: the first group's column, the groups, the column behind the last.
 struct Place {
-  int64_t head, groups, end;       // the first group's column, their number, the column behind the last
+  int head, groups, end;
 };
 
 template <typename T>
-__device__ __forceinline__ Place place_of(const T* x, int64_t cols) {
+__device__ __forceinline__ Place place_of(const T* x, int cols) {
   constexpr int kN = Group<T>::kN;
-  const int64_t ahead = -(reinterpret_cast<uintptr_t>(x) / sizeof(T)) & (kN - 1);
+  const int ahead = static_cast<int>(-(reinterpret_cast<uintptr_t>(x) / sizeof(T)) & (kN - 1));
   Place p;
   p.head = ahead < cols ? ahead : cols;
-  p.groups = (cols - p.head) / kN;
+  p.groups = static_cast<uint32_t>(cols - p.head) / kN;
   p.end = p.head + p.groups * kN;
   return p;
 }
 
-// The Stat of `n` values that the first lanes of a warp hold, in every lane.
-__device__ __forceinline__ Stat warp_join(Stat s, int most) {
+// The maximum of a group; a NaN counts only where there is nothing else.
+__device__ __forceinline__ float group_max(const uint4& w, const __nv_bfloat16*) {
+  auto two = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
+  const __nv_bfloat162 m = __hmax2(__hmax2(two(w.x), two(w.y)), __hmax2(two(w.z), two(w.w)));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float group_max(const uint4& w, const float*) {
+  return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+__device__ __forceinline__ void group_values(const uint4& w, float (&v)[8]) { unpack8(w, v); }
+__device__ __forceinline__ void group_values(const uint4& w, float (&v)[4]) {
+  v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y), v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
+}
+
+// The Stat of all that the lanes hold, in every lane.
+__device__ __forceinline__ Stat warp_join(Stat s) {
   float top = s.top;
-  for (int off = most / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
   float sum = s.sum * exp_of(s.top - anchor(top));
-  for (int off = most / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   return Stat{top, sum};
 }
 
@@ -194,14 +211,14 @@ cross_entropy_cluster_kernel(const __grid_constant__ opt_cross_entropy_args a, i
   using C = Config<T, kThreads>;
   constexpr int kN = Group<T>::kN, kWarps = kThreads / 32, kGroups = C::kGroups;
   extern __shared__ uint4 ring[];                // [kStages][kGroups][kThreads]
-  __shared__ float2 parts[2][kWarps], inbox[2][kMaxCluster];
+  __shared__ float2 parts[2][kMaxCluster * kWarps];        // every warp's of the cluster
   let_next_start();
   wait_for_predecessors();
-  const int t = threadIdx.x, lane = t & 31;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, cols = static_cast<int>(a.cols);
   const int rank = cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
   if (cluster > 1) cluster_sync();               // every CTA of the cluster has begun
   const int64_t step = gridDim.x / cluster;
-  const int64_t mine = static_cast<int64_t>(rank) * kGroups * kThreads + t;     // this thread's first group
+  const int mine = rank * kGroups * kThreads + t;          // this thread's first group
   auto row_at = [&](int64_t r) { return static_cast<const T*>(a.logits) + r * a.logits_ld; };
   auto label_at = [&](int64_t r) {
     return a.index_dtype == OPT_INDEX_INT32 ? static_cast<int64_t>(static_cast<const int32_t*>(a.labels)[r])
@@ -210,11 +227,11 @@ cross_entropy_cluster_kernel(const __grid_constant__ opt_cross_entropy_args a, i
   auto fetch = [&](int64_t r, int stage) {
     if (r < a.rows) {
       const T* x = row_at(r);
-      const Place p = place_of(x, a.cols);
+      const Place p = place_of(x, cols);
+      const T* from = x + p.head + mine * kN;
 #pragma unroll
       for (int i = 0; i < kGroups; ++i)
-        if (mine + i * kThreads < p.groups)
-          copy16(ring + (stage * kGroups + i) * kThreads + t, x + p.head + (mine + i * kThreads) * kN);
+        if (mine + i * kThreads < p.groups) copy16(ring + (stage * kGroups + i) * kThreads + t, from + i * kThreads * kN);
     }
     copy_commit();
   };
@@ -224,27 +241,25 @@ cross_entropy_cluster_kernel(const __grid_constant__ opt_cross_entropy_args a, i
   int parity = 0, stage = 0;
   for (; r < a.rows; r += step, parity ^= 1, label = next_label) {
     const T* x = row_at(r);
-    const Place p = place_of(x, a.cols);
+    const Place p = place_of(x, cols);
     if (r + step < a.rows) next_label = label_at(r + step);
-    const bool counts = label >= 0 && label < a.cols;
+    const bool counts = label >= 0 && label < cols;
     const float w = a.weight ? a.weight[r] * a.scale : a.scale;
-    float at_label = 0.f;
-    if (rank == 0 && t == 0 && counts) at_label = load_elem(x + label);
+    const float at_label = rank == 0 && t == 0 && counts ? load_elem(x + label) : 0.f;
     // the column outside of the groups that this thread has, or -1
-    const int64_t edge = rank ? -1 : t < p.head ? t : t < p.head + a.cols - p.end ? p.end + t - p.head : -1;
-    float e[kGroups][kN], ee = edge >= 0 ? load_elem(x + edge) : -INFINITY;
+    const int edge = rank ? -1 : t < p.head ? t : t < p.head + cols - p.end ? p.end + t - p.head : -1;
+    float e[kGroups][kN], ee = edge >= 0 ? load_elem(x + edge) : -INFINITY, top = ee;
     copy_wait<C::kStages - 1>();
-    float top = ee;
+    {
+      uint4 raw[kGroups];
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      if (mine + i * kThreads < p.groups) {
-        load_group(reinterpret_cast<const T*>(ring + (stage * kGroups + i) * kThreads + t), e[i]);
-#pragma unroll
-        for (int j = 0; j < kN; ++j) top = fmaxf(top, e[i][j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < kN; ++j) e[i][j] = -INFINITY;
+      for (int i = 0; i < kGroups; ++i) {
+        const uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;       // -inf
+        raw[i] = mine + i * kThreads < p.groups ? ring[(stage * kGroups + i) * kThreads + t] : make_uint4(none, none, none, none);
+        top = fmaxf(top, group_max(raw[i], static_cast<const T*>(nullptr)));
       }
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) group_values(raw[i], e[i]);
     }
     const float own = anchor(top);
     float sum = ee = exp_of(ee - own);
@@ -257,19 +272,20 @@ cross_entropy_cluster_kernel(const __grid_constant__ opt_cross_entropy_args a, i
       }
     fetch(r + C::kStages * step, stage);         // this thread's own places: it is done with them
     stage = stage + 1 == C::kStages ? 0 : stage + 1;
-    Stat s = warp_join(Stat{top, sum}, 32);
-    if (lane == 0) parts[parity][t >> 5] = make_float2(s.top, s.sum);
-    __syncthreads();
-    const float2 part = lane < kWarps ? parts[parity][lane] : make_float2(-INFINITY, 0.f);
-    s = warp_join(Stat{part.x, part.y}, kWarps);
-    s = Stat{__shfl_sync(0xffffffffu, s.top, 0), __shfl_sync(0xffffffffu, s.sum, 0)};
-    if (cluster > 1) {
-      if (t < cluster) store_peer(at_peer(&inbox[parity][rank], t), make_float2(s.top, s.sum));
+    Stat s = warp_join(Stat{top, sum});
+    if (cluster > 1) {                           // lane i tells CTA i
+      if (lane < cluster) store_peer(at_peer(&parts[parity][rank * kWarps + warp], lane), make_float2(s.top, s.sum));
       cluster_sync();
-      const float2 got = lane < cluster ? inbox[parity][lane] : make_float2(-INFINITY, 0.f);
-      s = warp_join(Stat{got.x, got.y}, kMaxCluster);
-      s = Stat{__shfl_sync(0xffffffffu, s.top, 0), __shfl_sync(0xffffffffu, s.sum, 0)};
+    } else {
+      if (lane == 0) parts[parity][warp] = make_float2(s.top, s.sum);
+      __syncthreads();
     }
+    s = Stat{-INFINITY, 0.f};
+    for (int i = lane; i < cluster * kWarps; i += 32) {
+      const float2 q = parts[parity][i];
+      s = join(s, Stat{q.x, q.y});
+    }
+    s = warp_join(s);
     const bool none = s.sum == 0.f;              // an empty row
     if (rank == 0 && t == 0) {
       const float log_sum = logf(s.sum);
@@ -280,29 +296,31 @@ cross_entropy_cluster_kernel(const __grid_constant__ opt_cross_entropy_args a, i
     T* g = static_cast<T*>(a.dlogits) + r * a.dlogits_ld;
     const bool zero = !counts || none;
     const float inv = exp_of(top - anchor(s.top)) / s.sum, inv_w = inv * w;
-    if (edge >= 0) store_elem(g + edge, zero ? 0.f : (ee * inv - (edge == label ? 1.f : 0.f)) * w);
+    if (edge >= 0) store_elem(g + edge, zero ? 0.f : (ee * inv - (edge == static_cast<int>(label) ? 1.f : 0.f)) * w);
     const bool together = (reinterpret_cast<uintptr_t>(g + p.head) & 15u) == 0;
-    const int64_t hot = label - p.head;          // the label's element among the groups
+    // the label's group and its place there
+    const int hot = counts ? static_cast<int>(label) - p.head : -1;
+    const int hot_group = hot >= 0 ? hot / kN : -1;
+    T* to = g + p.head + mine * kN;
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
-      const int64_t group = mine + i * kThreads;
+      const int group = mine + i * kThreads;
       if (group >= p.groups) break;
       if (zero) {
 #pragma unroll
         for (int j = 0; j < kN; ++j) e[i][j] = 0.f;
-      } else if (group == hot / kN && hot >= 0) {
+      } else if (group == hot_group) {
 #pragma unroll
-        for (int j = 0; j < kN; ++j) e[i][j] = (e[i][j] * inv - (j == hot % kN ? 1.f : 0.f)) * w;
+        for (int j = 0; j < kN; ++j) e[i][j] = (e[i][j] * inv - (j == (hot & (kN - 1)) ? 1.f : 0.f)) * w;
       } else {
 #pragma unroll
         for (int j = 0; j < kN; ++j) e[i][j] *= inv_w;
       }
-      T* to = g + p.head + group * kN;
       if (together) {
-        store_group(to, e[i]);
+        store_group(to + i * kThreads * kN, e[i]);
       } else {
 #pragma unroll
-        for (int j = 0; j < kN; ++j) store_elem(to + j, e[i][j]);
+        for (int j = 0; j < kN; ++j) store_elem(to + i * kThreads * kN + j, e[i][j]);
       }
     }
   }

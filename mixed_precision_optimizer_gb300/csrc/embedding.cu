@@ -8,7 +8,7 @@
 // them in registers: dtable is touched once for each distinct token and no
 // addition is atomic.
 //   embedding_sort_kernel  a stable radix sort of (token, row) by one cluster
-//   embedding_sums_kernel  sums the runs of equal tokens within pieces of 64
+//   embedding_sums_kernel  sums the runs of equal tokens within pieces of the
 //                          sorted rows; a run that crosses a piece's border
 //                          leaves a partial sum for each piece
 //   embedding_join_kernel  adds the partial sums of such runs in order
@@ -22,7 +22,6 @@ namespace mpopt {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPiece = kEmbeddingPiece;
 
 bool rows_on_16(const void* p, int64_t ld, int es, int64_t rows) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || static_cast<uintptr_t>(ld) * es % 16 == 0);
@@ -33,15 +32,51 @@ __device__ __forceinline__ int64_t token_at(const void* tokens, int index_dtype,
                                         : static_cast<const int64_t*>(tokens)[r];
 }
 
+// --------------------------------------------------------------- columns --
+
+// One, 4 or 8 neighbouring columns.
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
+  const float4 f = *reinterpret_cast<const float4*>(p);
+  v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&v)[4]) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xffff0000u);
+  v[2] = __uint_as_float(u.y << 16), v[3] = __uint_as_float(u.y & 0xffff0000u);
+}
+__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+}
+template <typename T, int kN>
+__device__ __forceinline__ void load_columns(const T* p, float (&v)[kN]) {
+  if constexpr (kN == 8) load8(p, v);
+  else if constexpr (kN == 4) load4(p, v);
+  else v[0] = load_elem(p);
+}
+template <typename T, int kN>
+__device__ __forceinline__ void store_columns(T* p, const float (&v)[kN]) {
+  if constexpr (kN == 8) store8(p, v);
+  else if constexpr (kN == 4) store4(p, v);
+  else store_elem(p, v[0]);
+}
+
 // ---------------------------------------------------------------- lookup --
 
-// A thread has 8 columns (kVec; else one) of kRows rows, whose loads are on their
-// way together: first the tokens, then the table's rows.  tpr threads to a row.
+// A thread has some columns of kRows rows, whose loads are on their way together:
+// first the tokens, then the table's rows; 2^log_tpr threads to a row.  The columns
+// are 16 bytes of the wider type (4, or 8 where both are bf16: neighbouring lanes
+// store neighbouring 16 bytes; 8 columns of an fp32 output took 16384 x 4096
+// from 59 to 66 us), or one where rows do not start on 16 bytes.
 constexpr int kRows = 4;
+template <typename T, typename O, bool kVec>
+constexpr int kLookupCols = !kVec ? 1 : sizeof(T) == 2 && sizeof(O) == 2 ? 8 : 4;
 template <typename T, typename O, bool kVec>
 __global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_constant__ opt_embedding_args a, int log_tpr,
                                                              uint32_t slices) {
-  constexpr int kN = kVec ? 8 : 1;
+  constexpr int kN = kLookupCols<T, O, kVec>;
   let_next_start();
   wait_for_predecessors();
   const uint32_t block = blockIdx.x / slices, slice = blockIdx.x - block * slices;
@@ -60,8 +95,7 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_consta
   for (int u = 0; u < kRows; ++u) {
     if (token[u] >= 0 && token[u] < a.vocab) {
       const T* src = static_cast<const T*>(a.table) + token[u] * a.table_ld + c;
-      if constexpr (kVec) load8(src, v[u]);
-      else v[u][0] = load_elem(src);
+      load_columns(src, v[u]);
 #pragma unroll
       for (int j = 0; j < kN; ++j) v[u][j] *= a.scale;
     } else {
@@ -74,8 +108,7 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_consta
     const int64_t r = r0 + u * per_step;
     if (r >= a.rows) return;
     O* dst = static_cast<O*>(a.y) + r * a.y_ld + c;
-    if constexpr (kVec) store8(dst, v[u]);
-    else store_elem(dst, v[u][0]);
+    store_columns(dst, v[u]);
   }
 }
 
@@ -83,7 +116,7 @@ template <typename T, typename O>
 cudaError_t lookup(const opt_embedding_args& a, cudaStream_t stream) {
   const bool vec = a.cols % 8 == 0 && rows_on_16(a.table, a.table_ld, sizeof(T), a.vocab) &&
                    rows_on_16(a.y, a.y_ld, sizeof(O), a.rows);
-  const int64_t groups = vec ? a.cols / 8 : a.cols;
+  const int64_t groups = a.cols / (vec ? kLookupCols<T, O, true> : 1);
   int log_tpr = 0;
   while (log_tpr < 8 && (int64_t(1) << log_tpr) < groups) ++log_tpr;
   const int64_t slices = (groups + (int64_t(1) << log_tpr) - 1) >> log_tpr, per_cta = (kThreads >> log_tpr) * kRows;
@@ -110,9 +143,13 @@ struct SortArgs {
 
 // Least significant digit first.  Every warp owns consecutive rows; a digit's
 // place is the rows of smaller digits, plus those with this digit of lower
-// CTAs, of lower warps, and earlier ones of the warp: a stable order.
+// CTAs, of lower warps, and earlier ones of the warp: a stable order.  Bound by
+// latency: the first kHeld keys of a lane are loaded at once and kept for the
+// second look at them, and every CTA stores its totals into the others' memory.
+constexpr int kHeld = 4;
+
 __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __grid_constant__ SortArgs a) {
-  extern __shared__ uint32_t counts[];            // [kSortWarps][bins], then [bins] totals of this CTA
+  extern __shared__ uint32_t counts[];            // [kSortWarps][bins], then [CTAs][bins] totals
   __shared__ uint32_t scan[kSortWarps];
   let_next_start();
   wait_for_predecessors();
@@ -123,40 +160,59 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __gr
   uint32_t* mine = counts + warp * bins;
   const int64_t first = (static_cast<int64_t>(rank) * kSortWarps + warp) * a.per_warp;
   const int64_t last = first + a.per_warp < a.rows ? first + a.per_warp : a.rows;
+  cluster_sync();                                 // every CTA has begun
   for (int pass = 0; pass < a.passes; ++pass) {
     const int shift = pass * a.bits;
     const uint32_t *key_in = a.ws.key[pass & 1], *row_in = a.ws.row[pass & 1];
     uint32_t *key_out = a.ws.key[(pass & 1) ^ 1], *row_out = a.ws.row[(pass & 1) ^ 1];
     auto key_at = [&](int64_t i) {
+      if (i >= last) return 0u;
       if (pass) return key_in[i];
       const int64_t t = token_at(a.tokens, a.index_dtype, i);
       return static_cast<uint32_t>(t >= 0 && t < a.vocab ? t : a.vocab);
     };
+    auto row_at = [&](int64_t i) { return pass && i < last ? row_in[i] : static_cast<uint32_t>(i); };
+    uint32_t held[kHeld], held_row[kHeld];
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      held[k] = key_at(first + k * 32 + lane);
+      held_row[k] = row_at(first + k * 32 + lane);
+    }
     for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) counts[i] = 0;
     __syncthreads();
-    for (int64_t i = first + lane; i - lane < last; i += 32) {
-      const uint32_t digit = i < last ? (key_at(i) >> shift) & (bins - 1) : static_cast<uint32_t>(bins);
-      const uint32_t same = __match_any_sync(0xffffffffu, digit);
+    // the lanes with this lane's digit (none beyond the last row: they share a digit that does not exist)
+    auto same_digit = [&](int64_t i, uint32_t key, uint32_t& digit) {
+      digit = i < last ? (key >> shift) & (bins - 1) : static_cast<uint32_t>(bins);
+      return __match_any_sync(0xffffffffu, digit);
+    };
+    auto count = [&](int64_t i, uint32_t key) {
+      uint32_t digit;
+      const uint32_t same = same_digit(i, key, digit);
       if (i < last && lane == __ffs(same) - 1) mine[digit] += __popc(same);
       __syncwarp();
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (first + k * 32 < last) count(first + k * 32 + lane, held[k]);
+    for (int64_t i = first + kHeld * 32 + lane; i - lane < last; i += 32) count(i, key_at(i));
     __syncthreads();
     // one thread to a digit (bins <= threads)
-    uint32_t sum = 0;
     const int d = threadIdx.x;
     if (d < bins) {
+      uint32_t sum = 0;
+#pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
         const uint32_t n = counts[w * bins + d];
         counts[w * bins + d] = sum;
         sum += n;
       }
-      total[d] = sum;
+      for (uint32_t r = 0; r < ctas; ++r) store_peer(at_peer(total + rank * bins + d, r), sum);
     }
     cluster_sync();
     uint32_t before = 0, all = 0;
     if (d < bins) {
       for (uint32_t r = 0; r < ctas; ++r) {
-        const uint32_t n = r == rank ? sum : load_peer_u32(at_peer(total + d, r));
+        const uint32_t n = total[r * bins + d];
         if (r < rank) before += n;
         all += n;
       }
@@ -172,24 +228,28 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __gr
     __syncthreads();
     uint32_t base = up - all + before;
     for (int w = 0; w < warp; ++w) base += scan[w];
-    if (d < bins)
+    if (d < bins) {
+#pragma unroll
       for (int w = 0; w < kSortWarps; ++w) counts[w * bins + d] += base;
+    }
     __syncthreads();
-    for (int64_t i = first + lane; i - lane < last; i += 32) {
-      const bool in = i < last;
-      const uint32_t key = in ? key_at(i) : 0u;
-      const uint32_t digit = in ? (key >> shift) & (bins - 1) : static_cast<uint32_t>(bins);
-      const uint32_t same = __match_any_sync(0xffffffffu, digit);
-      if (in) {
+    auto place = [&](int64_t i, uint32_t key, uint32_t row) {
+      uint32_t digit;
+      const uint32_t same = same_digit(i, key, digit);
+      if (i < last) {
         const uint32_t at = mine[digit] + __popc(same & ((1u << lane) - 1));
         key_out[at] = key;
-        row_out[at] = pass ? row_in[i] : static_cast<uint32_t>(i);
+        row_out[at] = row;
       }
       __syncwarp();
-      if (in && lane == __ffs(same) - 1) mine[digit] += __popc(same);
+      if (i < last && lane == __ffs(same) - 1) mine[digit] += __popc(same);
       __syncwarp();
-    }
-    cluster_sync();              // the next pass reads what other CTAs wrote; nobody leaves while `total` is read
+    };
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (first + k * 32 < last) place(first + k * 32 + lane, held[k], held_row[k]);
+    for (int64_t i = first + kHeld * 32 + lane; i - lane < last; i += 32) place(i, key_at(i), row_at(i));
+    cluster_sync();              // the next pass reads what other CTAs wrote, and writes to their totals
   }
 }
 
@@ -198,49 +258,30 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __gr
 struct SumArgs {
   opt_embedding_grad_args a;
   const uint32_t *key, *row;
-  float* partial;
-  int64_t slices;          // CTAs to a piece
+  float* partial;          // [pieces][2][cols]
+  uint32_t slices;         // CTAs to a piece
+  int piece;               // rows
 };
 
+// 4 columns to a thread, 16 bytes of the table, or one.
 template <bool kVec>
-struct Columns {
-  static constexpr int kN = kVec ? 8 : 1;
-  static constexpr int64_t kPerCta = kThreads * kN;
-};
-
-template <bool kVec, typename T>
-__device__ __forceinline__ void load_columns(const T* p, float (&v)[Columns<kVec>::kN]) {
-  if constexpr (kVec) load8(p, v);
-  else v[0] = load_elem(p);
-}
-
-template <bool kVec>
-__device__ __forceinline__ void store_columns(float* p, const float (&v)[Columns<kVec>::kN]) {
-  if constexpr (kVec) store8(p, v);
-  else p[0] = v[0];
-}
-
-template <bool kVec>
-__device__ __forceinline__ void add_to_table(float* p, const float (&v)[Columns<kVec>::kN], float scale) {
-  float old[Columns<kVec>::kN];
-  load_columns<kVec>(static_cast<const float*>(p), old);
-#pragma unroll
-  for (int j = 0; j < Columns<kVec>::kN; ++j) old[j] += v[j] * scale;
-  store_columns<kVec>(p, old);
-}
+constexpr int kSumCols = kVec ? 4 : 1;
+constexpr int kAhead = 8;                        // rows on their way to a thread
 
 // A run's sum goes to the table if the run lies within the piece, else to the
 // piece's first partial row (a run that came from the piece before) or its
-// second (a run that starts here and goes on).
+// second (a run that starts here and goes on).  What the table holds at a run's
+// end is loaded with the run's last row.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) embedding_sums_kernel(const __grid_constant__ SumArgs p) {
-  constexpr int kN = Columns<kVec>::kN;
-  __shared__ uint32_t key[kPiece + 2], row[kPiece];
+  constexpr int kN = kSumCols<kVec>;
+  __shared__ uint32_t key[kEmbeddingPiece + 2], row[kEmbeddingPiece];
   let_next_start();
   wait_for_predecessors();
   const opt_embedding_grad_args& a = p.a;
-  const int64_t piece = blockIdx.x / p.slices, first = piece * kPiece;
-  const int n = static_cast<int>(a.rows - first < kPiece ? a.rows - first : kPiece);
+  const uint32_t piece = blockIdx.x / p.slices;
+  const int64_t first = static_cast<int64_t>(piece) * p.piece;
+  const int n = static_cast<int>(a.rows - first < p.piece ? a.rows - first : p.piece);
   const uint32_t none = static_cast<uint32_t>(a.vocab);
   // key[0] and key[n + 1]: the neighbouring pieces' (a token outside the table where there is none)
   for (int i = threadIdx.x; i < n + 2; i += kThreads) {
@@ -249,37 +290,45 @@ __global__ void __launch_bounds__(kThreads) embedding_sums_kernel(const __grid_c
   }
   for (int i = threadIdx.x; i < n; i += kThreads) row[i] = p.row[first + i];
   __syncthreads();
-  const int64_t c = (blockIdx.x - piece * p.slices) * Columns<kVec>::kPerCta + threadIdx.x * kN;
+  const int64_t c = (static_cast<int64_t>(blockIdx.x - piece * p.slices) * kThreads + threadIdx.x) * kN;
   if (c >= a.cols) return;
   const T* dy = static_cast<const T*>(a.dy) + c;
+  float* table = a.dtable + c;
   float sum[kN];
 #pragma unroll
   for (int j = 0; j < kN; ++j) sum[j] = 0.f;
   bool from_before = key[0] == key[1];
-  constexpr int kAhead = 4;                      // rows on their way
-  float next[kAhead][kN];
+  float next[kAhead][kN], old[kAhead][kN];
+  auto fetch = [&](int i, float (&v)[kN], float (&o)[kN]) {
+    if (i >= n || key[i + 1] == none) return;
+    load_columns(dy + row[i] * a.dy_ld, v);
+    if (key[i + 2] != key[i + 1]) load_columns(static_cast<const float*>(table) + key[i + 1] * a.cols, o);
+  };
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u)
-    if (u < n && key[u + 1] != none) load_columns<kVec>(dy + row[u] * a.dy_ld, next[u]);
+  for (int u = 0; u < kAhead; ++u) fetch(u, next[u], old[u]);
   for (int i0 = 0; i0 < n; i0 += kAhead) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int i = i0 + u;
-      if (i >= n) break;
+      if (i >= n) return;
       const uint32_t v = key[i + 1];
       if (v == none) return;                     // and so are all rows behind it
 #pragma unroll
       for (int j = 0; j < kN; ++j) sum[j] += next[u][j];
-      if (i + kAhead < n && key[i + kAhead + 1] != none) load_columns<kVec>(dy + row[i + kAhead] * a.dy_ld, next[u]);
       const bool ends_here = key[i + 2] != v;
-      if (!ends_here && i + 1 < n) continue;
-      if (from_before || !ends_here)
-        store_columns<kVec>(p.partial + (2 * piece + (from_before ? 0 : 1)) * a.cols + c, sum);
-      else
-        add_to_table<kVec>(a.dtable + v * a.cols + c, sum, a.scale);
-      from_before = false;
+      if (ends_here || i + 1 == n) {
+        if (from_before || !ends_here) {
+          store_columns(p.partial + (2 * static_cast<int64_t>(piece) + (from_before ? 0 : 1)) * a.cols + c, sum);
+        } else {
 #pragma unroll
-      for (int j = 0; j < kN; ++j) sum[j] = 0.f;
+          for (int j = 0; j < kN; ++j) old[u][j] += sum[j] * a.scale;
+          store_columns(table + v * a.cols, old[u]);
+        }
+        from_before = false;
+#pragma unroll
+        for (int j = 0; j < kN; ++j) sum[j] = 0.f;
+      }
+      fetch(i + kAhead, next[u], old[u]);
     }
   }
 }
@@ -287,16 +336,17 @@ __global__ void __launch_bounds__(kThreads) embedding_sums_kernel(const __grid_c
 // The CTA of the piece in which a run starts that goes on behind it.
 template <bool kVec>
 __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_constant__ SumArgs p) {
-  constexpr int kN = Columns<kVec>::kN;
+  constexpr int kN = kSumCols<kVec>;
   let_next_start();
   wait_for_predecessors();
   const opt_embedding_grad_args& a = p.a;
-  const int64_t piece = blockIdx.x / p.slices, last = piece * kPiece + kPiece - 1;
+  const uint32_t piece = blockIdx.x / p.slices;
+  const int64_t start = static_cast<int64_t>(piece) * p.piece, last = start + p.piece - 1;
   if (last + 1 >= a.rows) return;
   const uint32_t v = p.key[last];
   if (v >= static_cast<uint32_t>(a.vocab) || p.key[last + 1] != v) return;
-  if (piece > 0 && p.key[piece * kPiece - 1] == v) return;        // it started earlier
-  const int64_t c = (blockIdx.x - piece * p.slices) * Columns<kVec>::kPerCta + threadIdx.x * kN;
+  if (piece > 0 && p.key[start - 1] == v && p.key[start] == v) return;        // it started earlier
+  const int64_t c = (static_cast<int64_t>(blockIdx.x - piece * p.slices) * kThreads + threadIdx.x) * kN;
   if (c >= a.cols) return;
   // the run's last row, by halving: key[lo] == v, key[hi] != v
   int64_t lo = last + 1, hi = a.rows;
@@ -305,15 +355,16 @@ __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_c
     if (p.key[mid] == v) lo = mid;
     else hi = mid;
   }
-  const int64_t last_piece = lo / kPiece;
-  float sum[kN];
-  load_columns<kVec>(p.partial + (2 * piece + 1) * a.cols + c, sum);
-  constexpr int kAhead = 8;
+  const int64_t last_piece = lo / p.piece;
+  float sum[kN], old[kN];
+  float* table = a.dtable + v * a.cols + c;
+  load_columns(static_cast<const float*>(table), old);
+  load_columns(static_cast<const float*>(p.partial) + (2 * static_cast<int64_t>(piece) + 1) * a.cols + c, sum);
   for (int64_t q0 = piece + 1; q0 <= last_piece; q0 += kAhead) {
     float part[kAhead][kN];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
-      if (q0 + u <= last_piece) load_columns<kVec>(p.partial + 2 * (q0 + u) * a.cols + c, part[u]);
+      if (q0 + u <= last_piece) load_columns(static_cast<const float*>(p.partial) + 2 * (q0 + u) * a.cols + c, part[u]);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
       if (q0 + u <= last_piece) {
@@ -321,18 +372,21 @@ __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_c
         for (int j = 0; j < kN; ++j) sum[j] += part[u][j];
       }
   }
-  add_to_table<kVec>(a.dtable + v * a.cols + c, sum, a.scale);
+#pragma unroll
+  for (int j = 0; j < kN; ++j) old[j] += sum[j] * a.scale;
+  store_columns(table, old);
 }
 
-// 8 columns to a thread where rows of dy, the table and the partial sums start on 16 bytes.
+// 4 columns to a thread where rows of dy, the table and the partial sums start on 16 bytes.
 bool grad_vec(const opt_embedding_grad_args& a) {
   return a.cols % 8 == 0 && rows_on_16(a.dy, a.dy_ld, a.dtype == kBf16 ? 2 : 4, a.rows) &&
          reinterpret_cast<uintptr_t>(a.dtable) % 16 == 0;
 }
 
 SumArgs sum_args(const opt_embedding_grad_args& a, const EmbeddingScratch& ws, int sorted, bool vec) {
-  const int64_t per_cta = kThreads * (vec ? 8 : 1);
-  return SumArgs{a, ws.key[sorted], ws.row[sorted], ws.partial, (a.cols + per_cta - 1) / per_cta};
+  const int64_t per_cta = kThreads * (vec ? kSumCols<true> : 1);
+  return SumArgs{a, ws.key[sorted], ws.row[sorted], ws.partial, static_cast<uint32_t>((a.cols + per_cta - 1) / per_cta),
+                 embedding_piece(a.rows)};
 }
 
 }  // namespace
@@ -353,9 +407,9 @@ cudaError_t launch_embedding_sort(const opt_embedding_grad_args& a, const Embedd
   const int64_t warps = static_cast<int64_t>(cluster) * kSortWarps;
   s.per_warp = ((a.rows + warps - 1) / warps + 31) & ~int64_t(31);
   *sorted = s.passes & 1;
-  const size_t smem = static_cast<size_t>(kSortWarps + 1) * (size_t(1) << s.bits) * 4;
+  const size_t smem = static_cast<size_t>(kSortWarps + cluster) * (size_t(1) << s.bits) * 4;
   const cudaError_t e = cudaFuncSetAttribute(embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (kSortWarps + 1) * (1 << kMaxBits) * 4);
+                                             (kSortWarps + kSortCluster) * (1 << kMaxBits) * 4);
   if (e != cudaSuccess) return e;
   return launch_overlapped(embedding_sort_kernel, dim3(static_cast<unsigned>(cluster)), kSortThreads, smem, stream, cluster, s);
 }

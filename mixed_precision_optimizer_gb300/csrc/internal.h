@@ -369,9 +369,17 @@ cudaError_t launch_repack(const RepackBatch& batch, int esize, cudaStream_t stre
 cudaError_t launch_embedding(const opt_embedding_args& a, cudaStream_t stream);
 
 // The embedding's gradient sums the rows of the batch sorted by token in pieces of
-// this many.
-constexpr int kEmbeddingPiece = 64;
-inline int64_t embedding_pieces(int64_t rows) { return (rows + kEmbeddingPiece - 1) / kEmbeddingPiece; }
+// kEmbeddingPiece, of few rows in shorter ones: what a CTA adds one row after
+// another is what such a call waits for.
+constexpr int kEmbeddingPiece = 64, kEmbeddingShortPiece = 16;
+constexpr int64_t kEmbeddingShort = 8192;
+inline int embedding_piece(int64_t rows) { return rows <= kEmbeddingShort ? kEmbeddingShortPiece : kEmbeddingPiece; }
+inline int64_t embedding_pieces(int64_t rows) { return (rows + embedding_piece(rows) - 1) / embedding_piece(rows); }
+// The most pieces of any number of rows up to this one.
+inline int64_t embedding_most_pieces(int64_t rows) {
+  const int64_t shorter = embedding_pieces(rows < kEmbeddingShort ? rows : kEmbeddingShort), n = embedding_pieces(rows);
+  return n > shorter ? n : shorter;
+}
 // Its workspace: two buffers of `rows` sort keys and two of row indices, then two
 // partial sums of `cols` columns for each piece.
 struct EmbeddingScratch {

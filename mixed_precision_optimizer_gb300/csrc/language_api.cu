@@ -74,7 +74,7 @@ opt_status opt_embedding_forward(const opt_embedding_args* a, void* stream) {
 
 size_t opt_embedding_workspace_size(int64_t rows, int64_t vocab, int64_t cols) {
   if (!extent(rows, 1) || !extent(vocab, 1) || !extent(cols, 1)) return 0;
-  return 4 * key_bytes(rows) + static_cast<size_t>(embedding_pieces(rows)) * 2 * static_cast<size_t>(cols) * 4;
+  return 4 * key_bytes(rows) + static_cast<size_t>(embedding_most_pieces(rows)) * 2 * static_cast<size_t>(cols) * 4;
 }
 
 opt_status opt_embedding_backward(const opt_embedding_grad_args* a, void* workspace, size_t workspace_bytes,

@@ -32,7 +32,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kCols = 64;                        // of a CTA
-constexpr int kMaxCluster = 8;                   // a warp of a CTA for each
+constexpr int kMaxCluster = 8;
 constexpr int kS = kRecurrenceStateRows;         // rows of a thread at a time
 constexpr int kChunk = kWarps * kS;              // of a CTA
 constexpr float kReset = -1.f;
@@ -84,8 +84,9 @@ struct Span {
 };
 
 struct Shared {
-  float4* pieces;        // [2][kWarps][32]: two columns' (p, b) of a warp
-  float4* inbox;         // [2][cluster][32]: of a CTA
+  float2* pieces;        // [2][kWarps][kCols]: (p, b) of a warp's rows; then of all warps' before it
+  float2* inbox;         // [2][cluster][kCols]: of a CTA's rows
+  float* state;          // [2][kCols]: before the CTA's rows
   int* first;            // [kChunk] with starts: the sequence that a row starts (set where one does)
   int* last;             // [kChunk]              the sequence that a row ends
   Span* span;
@@ -95,14 +96,15 @@ template <typename T, int kTensors>
 struct Layout {
   static constexpr int kStage = kTensors * kTile<T> * kWarps;
   static size_t bytes(int cluster) {
-    return 2 * kStage + 2 * kWarps * 512 + (cluster > 1 ? 2 * cluster * 512 : 0) + 2 * kChunk * 4 + 64;
+    return 2 * kStage + (2 * kWarps * 8 + (cluster > 1 ? 2 * cluster * 8 : 0) + 2 * 4) * kCols + 2 * kChunk * 4 + sizeof(Span);
   }
   static __device__ __forceinline__ Shared carve(uint8_t* base, int cluster) {
     Shared s;
     base += 2 * kStage;
-    s.pieces = reinterpret_cast<float4*>(base);
-    s.inbox = s.pieces + 2 * kWarps * 32;
-    s.first = reinterpret_cast<int*>(s.inbox + (cluster > 1 ? 2 * cluster * 32 : 0));
+    s.pieces = reinterpret_cast<float2*>(base);
+    s.inbox = s.pieces + 2 * kWarps * kCols;
+    s.state = reinterpret_cast<float*>(s.inbox + (cluster > 1 ? 2 * cluster * kCols : 0));
+    s.first = reinterpret_cast<int*>(s.state + 2 * kCols);
     s.last = s.first + kChunk;
     s.span = reinterpret_cast<Span*>(s.last + kChunk);
     return s;
@@ -165,10 +167,19 @@ struct Marks {
   int start_seq, end_seq;
 };
 
-__device__ __forceinline__ Marks marks_equal(const Plan& plan, const Span& span, int64_t row, int lane) {
+// Sequences of one length.  `near` is the first sequence's start from these rows on
+// (kBack: the last one up to the row behind them), kept from call to call: the
+// division is needed only when it has been passed.
+template <bool kBack>
+__device__ __forceinline__ Marks marks_equal(const Plan& plan, const Span& span, int64_t row, int64_t& near, int lane) {
+  Marks m{0, 0, 0, 0};
+  if (kBack ? near > row + kS : near < row) {
+    const uint32_t len = static_cast<uint32_t>(plan.length);
+    near = static_cast<int64_t>((static_cast<uint32_t>(kBack ? row + kS : row + len - 1)) / len) * len;
+  }
+  if (kBack ? near < row : near > row + kS) return m;
   const int64_t r = row + lane;
   const bool in = lane < kS && r >= span.row && r < span.row_end;
-  Marks m;
   m.start_seq = m.end_seq = in ? static_cast<int>(static_cast<uint32_t>(r) / static_cast<uint32_t>(plan.length)) : 0;
   m.start = __ballot_sync(0xffffffffu, in && r == m.start_seq * plan.length);
   m.end = __ballot_sync(0xffffffffu, in && r + 1 == (m.start_seq + 1) * plan.length);
@@ -235,30 +246,40 @@ __device__ __forceinline__ void pass_empty(const int32_t* starts, const Span& sp
 // --------------------------------------------------------------- elements --
 
 // Copies a warp's rows of one tensor to its place in shared memory, [kS][64], zeros
-// where there is no row or column.
+// where there is no row or column.  `whole`: they are all there.
 template <typename T, bool kVec>
 __device__ __forceinline__ void fetch_rows(uint8_t* dst, const void* src, int64_t ld, int64_t row, const Span& span,
-                                           int64_t col, int64_t cols, int lane) {
+                                           int64_t col, int64_t cols, int lane, bool whole) {
   const T* p = static_cast<const T*>(src);
   if constexpr (kVec) {
-    constexpr int kPer = 16 / sizeof(T), kPieces = kCols / kPer;      // 16-byte pieces of a row
+    constexpr int kPer = 16 / sizeof(T), kPieces = kCols / kPer, kStep = 32 / kPieces;   // 16-byte pieces of a row, rows a step
+    const int64_t r0 = row + lane / kPieces, c = col + lane % kPieces * kPer;
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst)) + lane * 16;
+    if (whole) {
+      const T* q = p + r0 * ld + c;
 #pragma unroll
-    for (int i = 0; i < kS * kPieces / 32; ++i) {
-      const int k = i * 32 + lane;
-      const int64_t r = row + k / kPieces, c = col + k % kPieces * kPer;
-      const bool in = r >= span.row && r < span.row_end && c < cols;
-      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst)) + k * 16;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p + (in ? r * ld + c : 0)),
-                   "r"(in ? 16 : 0)
-                   : "memory");
+      for (int i = 0; i < kS / kStep; ++i, q += kStep * ld)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 512), "l"(q) : "memory");
+    } else {
+#pragma unroll
+      for (int i = 0; i < kS / kStep; ++i) {
+        const int64_t r = r0 + i * kStep;
+        const bool in = r >= span.row && r < span.row_end && c < cols;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * 512), "l"(p + (in ? r * ld + c : 0)),
+                     "r"(in ? 16 : 0)
+                     : "memory");
+      }
     }
   } else {
     T* to = reinterpret_cast<T*>(dst);
-#pragma unroll 8
-    for (int k = lane; k < kS * kCols; k += 32) {
-      const int64_t r = row + k / kCols, c = col + k % kCols;
-      const bool in = r >= span.row && r < span.row_end && c < cols;
-      store_elem(to + k, in ? load_elem(p + r * ld + c) : 0.f);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int64_t c = col + k * 32 + lane;
+#pragma unroll
+      for (int j = 0; j < kS; ++j) {
+        const bool in = whole || (row + j >= span.row && row + j < span.row_end && c < cols);
+        store_elem(to + j * kCols + k * 32 + lane, in ? load_elem(p + (row + j) * ld + c) : 0.f);
+      }
     }
   }
 }
@@ -311,55 +332,56 @@ __device__ __forceinline__ void load_state(const float* states, int64_t seq, int
   }
 }
 
-// The state that a warp's rows begin with, and in `carry` the one behind the rows of
-// the whole cluster: the pieces of the CTAs and warps in between, in order.
-// kBack: rows, warps and CTAs are taken from the last to the first.  Pieces and
-// inbox alternate between two places with the turns (`parity`): a thread writes
-// to one again only after a barrier that all threads reach when they have
-// read it.
-template <bool kBack>
+// The state that a warp's rows begin with.  The first kCols threads of a CTA have a
+// column each: they join the warps' pieces to what stands before every warp, tell
+// the CTAs of the cluster the whole of it, and keep in `carry` the state behind
+// all their rows.  kBack: rows, warps and CTAs are taken from the last to the
+// first.  The places alternate with the turns (`parity`): a thread writes to one
+// again only after a barrier that all threads reach when they have read it.
+template <bool kVec, bool kBack>
 __device__ __forceinline__ void exchange(const Shared& sh, int parity, int cluster, uint32_t rank, int warp, int lane,
-                                         const Piece (&mine)[2], float (&carry)[2], float (&state)[2]) {
-  float4* pieces = sh.pieces + parity * kWarps * 32;
-  pieces[warp * 32 + lane] = make_float4(mine[0].p, mine[0].b, mine[1].p, mine[1].b);
+                                         const Piece (&mine)[2], float& carry, float (&state)[2]) {
+  float2* pieces = sh.pieces + parity * kWarps * kCols;
+  float* before = sh.state + parity * kCols;
+  const int c0 = kVec ? 2 * lane : lane, c1 = kVec ? 2 * lane + 1 : lane + 32;
+  pieces[warp * kCols + c0] = make_float2(mine[0].p, mine[0].b);
+  pieces[warp * kCols + c1] = make_float2(mine[1].p, mine[1].b);
   __syncthreads();
-  auto both = [](const float4& p, float (&h)[2]) {
-    h[0] = through(Piece{p.x, p.y}, h[0]);
-    h[1] = through(Piece{p.z, p.w}, h[1]);
-  };
-  state[0] = carry[0];
-  state[1] = carry[1];
+  const int c = threadIdx.x;
+  Piece all{1.f, 0.f};
+  if (c < kCols) {
+    float2 q[kWarps];
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) q[i] = pieces[i * kCols + c];
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const int w = kBack ? kWarps - 1 - i : i;
+      pieces[w * kCols + c] = make_float2(all.p, all.b);
+      all = then(all, Piece{q[w].x, q[w].y});
+    }
+    if (cluster == 1) {
+      before[c] = carry;
+      carry = through(all, carry);
+    }
+  }
   if (cluster > 1) {
-    float4* inbox = sh.inbox + parity * cluster * 32;
-    if (warp < cluster) {                        // warp w tells CTA w of the cluster this CTA's piece
-      Piece p[2] = {{1.f, 0.f}, {1.f, 0.f}};
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        const float4 q = pieces[(kBack ? kWarps - 1 - i : i) * 32 + lane];
-        p[0] = then(p[0], Piece{q.x, q.y});
-        p[1] = then(p[1], Piece{q.z, q.w});
-      }
-      store_peer(at_peer(inbox + rank * 32 + lane, warp), make_float4(p[0].p, p[0].b, p[1].p, p[1].b));
-    }
+    float2* inbox = sh.inbox + parity * cluster * kCols;
+    if (c < kCols)
+      for (int i = 0; i < cluster; ++i) store_peer(at_peer(inbox + rank * kCols + c, i), make_float2(all.p, all.b));
     cluster_sync();
-    for (int i = 0; i < cluster; ++i) {
-      const int q = kBack ? cluster - 1 - i : i;
-      if (q == static_cast<int>(rank)) {
-        state[0] = carry[0];
-        state[1] = carry[1];
+    if (c < kCols) {
+      for (int i = 0; i < cluster; ++i) {
+        const int w = kBack ? cluster - 1 - i : i;
+        if (w == static_cast<int>(rank)) before[c] = carry;
+        const float2 q = inbox[w * kCols + c];
+        carry = through(Piece{q.x, q.y}, carry);
       }
-      both(inbox[q * 32 + lane], carry);
     }
   }
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    const int w = kBack ? kWarps - 1 - i : i;
-    if (kBack ? w > warp : w < warp) both(pieces[w * 32 + lane], state);
-  }
-  if (cluster == 1) {
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) both(pieces[(kBack ? kWarps - 1 - i : i) * 32 + lane], carry);
-  }
+  __syncthreads();
+  const float2 p0 = pieces[warp * kCols + c0], p1 = pieces[warp * kCols + c1];
+  state[0] = through(Piece{p0.x, p0.y}, before[c0]);
+  state[1] = through(Piece{p1.x, p1.y}, before[c1]);
 }
 
 // --------------------------------------------------------------- forward --
@@ -386,24 +408,25 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
   if (kRagged && rank == 0) pass_empty(a.starts, span, a.hT, a.h0, col, a.cols);
   const int64_t base = span.row / kS * kS, step = static_cast<int64_t>(plan.cluster) * kChunk;
   const int64_t turns = span.row_end > span.row ? (span.row_end - base + step - 1) / step : 0;
-  int64_t next = span.seq, row = base + (static_cast<int64_t>(rank) * kWarps + warp) * kS;
+  int64_t next = kRagged ? span.seq : span.row, row = base + (static_cast<int64_t>(rank) * kWarps + warp) * kS;
   auto stage = [&](int turn) { return smem + (turn & 1) * L::kStage + warp * 2 * kTile<T>; };
   auto fetch = [&](int64_t r, int turn) {
     if (r < span.row_end) {
-      fetch_rows<T, kVec>(stage(turn), a.x, a.x_ld, r, span, col, a.cols, lane);
-      fetch_rows<T, kVec>(stage(turn) + kTile<T>, a.gate, a.gate_ld, r, span, col, a.cols, lane);
+      const bool whole = r >= span.row && r + kS <= span.row_end && col + kCols <= a.cols;
+      fetch_rows<T, kVec>(stage(turn), a.x, a.x_ld, r, span, col, a.cols, lane, whole);
+      fetch_rows<T, kVec>(stage(turn) + kTile<T>, a.gate, a.gate_ld, r, span, col, a.cols, lane, whole);
     }
     copy_commit();
   };
   fetch(row, 0);
-  float carry[2] = {0.f, 0.f};
+  float carry = 0.f;                             // the first kCols threads: behind all rows so far
   for (int turn = 0; turn < turns; ++turn, row += step) {
     copy_wait<0>();
     __syncwarp();
     fetch(row + step, turn + 1);                 // over the rows of the turn before, which this warp is done with
     Marks m;
     if constexpr (kRagged) m = marks_ragged<false>(a.starts, a.rows, span, row, next, sh, warp, lane);
-    else m = marks_equal(plan, span, row, lane);
+    else m = marks_equal<false>(plan, span, row, next, lane);
     const uint8_t *xs = stage(turn), *gs = xs + kTile<T>;
     float c[kS][2];
     Piece mine[2] = {{1.f, 0.f}, {1.f, 0.f}};
@@ -434,7 +457,7 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
     if (plain) pieces(Flag<true>{});
     else pieces(Flag<false>{});
     float h[2];
-    exchange<false>(sh, turn & 1, plan.cluster, rank, warp, lane, mine, carry, h);
+    exchange<kVec, false>(sh, turn & 1, plan.cluster, rank, warp, lane, mine, carry, h);
     if (a.states && row >= span.row && row < span.row_end)
       store_pair<float, kVec>(a.states + row / kS * a.cols, col, a.cols, lane, h[0], h[1]);
     T* y = static_cast<T*>(a.y) + row * a.y_ld;
@@ -464,12 +487,12 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
 // One row to each sequence: nothing depends on another row.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) recurrence_step_kernel(const __grid_constant__ opt_recurrence_args a,
-                                                                   int64_t slices) {
+                                                                   uint32_t slices) {
   constexpr int kN = kVec ? 8 : 1;
   let_next_start();
   wait_for_predecessors();
-  const int64_t r = blockIdx.x / slices;
-  const int64_t c = ((blockIdx.x - r * slices) * kThreads + threadIdx.x) * kN;
+  const uint32_t block = blockIdx.x / slices;
+  const int64_t r = block, c = static_cast<int64_t>((blockIdx.x - block * slices) * kThreads + threadIdx.x) * kN;
   if (c >= a.cols) return;
   float x[kN], g[kN], h[kN];
 #pragma unroll
@@ -515,13 +538,14 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
   if (kRagged && rank == 0) pass_empty(a.starts, span, a.dh0, a.dhT, col, a.cols);
   const int64_t base = span.row / kS * kS, step = static_cast<int64_t>(plan.cluster) * kChunk;
   const int64_t turns = span.row_end > span.row ? (span.row_end - base + step - 1) / step : 0;
-  int64_t next = span.seq_end + 1, row = base + (turns - 1) * step + (static_cast<int64_t>(rank) * kWarps + warp) * kS;
+  int64_t next = kRagged ? span.seq_end + 1 : span.row_end, row = base + (turns - 1) * step + (static_cast<int64_t>(rank) * kWarps + warp) * kS;
   auto stage = [&](int turn) { return smem + (turn & 1) * L::kStage + warp * 3 * kTile<T>; };
   auto fetch = [&](int64_t r, int turn) {
     if (r >= base && r < span.row_end) {
-      fetch_rows<T, kVec>(stage(turn), a.x, a.x_ld, r, span, col, a.cols, lane);
-      fetch_rows<T, kVec>(stage(turn) + kTile<T>, a.gate, a.gate_ld, r, span, col, a.cols, lane);
-      fetch_rows<T, kVec>(stage(turn) + 2 * kTile<T>, a.dy, a.dy_ld, r, span, col, a.cols, lane);
+      const bool whole = r >= span.row && r + kS <= span.row_end && col + kCols <= a.cols;
+      fetch_rows<T, kVec>(stage(turn), a.x, a.x_ld, r, span, col, a.cols, lane, whole);
+      fetch_rows<T, kVec>(stage(turn) + kTile<T>, a.gate, a.gate_ld, r, span, col, a.cols, lane, whole);
+      fetch_rows<T, kVec>(stage(turn) + 2 * kTile<T>, a.dy, a.dy_ld, r, span, col, a.cols, lane, whole);
     }
     copy_commit();
   };
@@ -531,7 +555,7 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
   float coming[2];
   fetch(row, 0);
   saved(row, coming);
-  float carry[2] = {0.f, 0.f};
+  float carry = 0.f;                             // the first kCols threads: behind all rows so far
   for (int turn = 0; turn < turns; ++turn, row -= step) {
     copy_wait<0>();
     __syncwarp();
@@ -540,7 +564,7 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
     saved(row - step, coming);
     Marks m;
     if constexpr (kRagged) m = marks_ragged<true>(a.starts, a.rows, span, row, next, sh, warp, lane);
-    else m = marks_equal(plan, span, row, lane);
+    else m = marks_equal<true>(plan, span, row, next, lane);
     const uint8_t *xs = stage(turn), *gs = xs + kTile<T>, *ys = gs + kTile<T>;
     float c[kS][2], q[kS][2];                    // q = (1 - c) (x_t - h_{t-1})
     Piece mine[2] = {{1.f, 0.f}, {1.f, 0.f}};
@@ -585,7 +609,7 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
     if (plain) pieces(Flag<true>{});
     else pieces(Flag<false>{});
     float b[2];                                  // (1 - c) l of the row behind
-    exchange<true>(sh, turn & 1, plan.cluster, rank, warp, lane, mine, carry, b);
+    exchange<kVec, true>(sh, turn & 1, plan.cluster, rank, warp, lane, mine, carry, b);
     T* dx = static_cast<T*>(a.dx) + (row + kS - 1) * a.dx_ld;
     T* dg = static_cast<T*>(a.dgate) + (row + kS - 1) * a.dgate_ld;
     auto outputs = [&](auto plain) {
@@ -628,8 +652,8 @@ bool rows_on(const void* p, int64_t ld, int es, int64_t rows, uintptr_t bytes) {
 
 // How many CTAs share the rows of a sequence (a cluster) and how many shares the
 // sequences make, so that the CTAs of 64 columns that the SMs hold at once have as
-// few turns as possible.  A share of ragged sequences is taken to be longer than the others by
-// an average sequence.
+// few turns as possible.  A share of ragged sequences is taken to be longer than the
+// others by three average sequences.
 Plan make_plan(int64_t rows, int64_t cols, int64_t sequences, bool ragged, int ctas_per_sm) {
   Plan best{1, 1, static_cast<int>((cols + kCols - 1) / kCols), ragged ? 0 : rows / sequences};
   const int64_t target = static_cast<int64_t>(ctas_per_sm) * num_sms(), average = (rows + sequences - 1) / sequences;
@@ -642,7 +666,7 @@ Plan make_plan(int64_t rows, int64_t cols, int64_t sequences, bool ragged, int c
     }
     if (ranges > sequences) ranges = sequences;
     const int64_t most = ranges == 1 ? rows
-                         : ragged    ? rows / ranges + average
+                         : ragged    ? rows / ranges + 3 * average
                                      : (sequences + ranges - 1) / ranges * average;
     const int64_t turns = (most + cluster * kChunk - 1) / (cluster * kChunk);
     const int64_t waves = (ranges * best.groups * cluster + target - 1) / target;
@@ -669,7 +693,7 @@ cudaError_t forward(const opt_recurrence_args& a, cudaStream_t stream) {
   if (!a.starts && a.rows == a.sequences) {
     const int64_t per_cta = kThreads * (kVec ? 8 : 1), slices = (a.cols + per_cta - 1) / per_cta;
     return launch_overlapped(recurrence_step_kernel<T, kVec>, dim3(static_cast<unsigned>(a.rows * slices)), kThreads, 0, stream,
-                             0, a, slices);
+                             0, a, static_cast<uint32_t>(slices));
   }
   const Plan plan = make_plan(a.rows, a.cols, a.sequences, a.starts != nullptr, kForwardCtas<T>);
   const size_t smem = Layout<T, 2>::bytes(plan.cluster);

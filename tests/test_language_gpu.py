@@ -156,14 +156,14 @@ def test_embedding_backward(rows, vocab, cols, dtype, layout):
     check_embedding_backward(tokens.to(index), normal(4, (rows, cols), dtype, layout=layout), vocab, 0.3, rows % 2 == 0)
 
 
-@pytest.mark.parametrize("pattern", ["one token", "all padding", "all different", "runs of 64", "runs of 65", "padding first",
-                                     "two halves"])
-@pytest.mark.parametrize("rows", [64, 128, 129, 1000, 8200])
+@pytest.mark.parametrize("pattern", ["one token", "all padding", "all different", "runs of 16", "runs of 17", "runs of 64",
+                                     "runs of 65", "padding first", "two halves"])
+@pytest.mark.parametrize("rows", [16, 32, 33, 1000, 8200])
 def test_embedding_backward_runs(pattern, rows):
     """Runs of equal tokens that start, end and go on at every place of a piece."""
     i = torch.arange(rows, device="cuda")
-    tokens = {"one token": i * 0 + 5, "all padding": i * 0 - 1, "all different": (i * 7919) % rows, "runs of 64": i // 64,
-              "runs of 65": i // 65, "padding first": torch.where(i < rows // 2, -1, i % 3), "two halves": i * 2 // rows}[pattern]
+    tokens = {"one token": i * 0 + 5, "all padding": i * 0 - 1, "all different": (i * 7919) % rows, "runs of 16": i // 16,
+              "runs of 17": i // 17, "runs of 64": i // 64, "runs of 65": i // 65, "padding first": torch.where(i < rows // 2, -1, i % 3), "two halves": i * 2 // rows}[pattern]
     check_embedding_backward(tokens, normal(5, (rows, 40)), max(rows, 6), 1.0, True, pattern)
 
 

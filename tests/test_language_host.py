@@ -141,6 +141,8 @@ def test_embedding_workspace(L):
     for rows, vocab, cols in ((999, 500, 64), (1000, 1, 64), (1, 500, 63), (64, 3, 1)):
         assert mp.embedding_workspace_size(rows, vocab, cols) <= need
     assert mp.embedding_workspace_size(0, 500, 64) == mp.embedding_workspace_size(4, 0, 64) == 0
+    for rows in (8193, 20000, 40000):               # fewer rows in shorter pieces
+        assert mp.embedding_workspace_size(rows, 10, 64) >= mp.embedding_workspace_size(8192, 10, 64)
     need = mp.embedding_workspace_size(4, 10, 64)
     for ws, nb in ((None, 1 << 20), (FAKE, need - 1), (FAKE + 64, 1 << 20)):
         assert call(L, "opt_embedding_backward", lm.OptEmbeddingGradArgs, EMBEDDING_GRAD, {}, ws, nb, None) == WS
