@@ -4,14 +4,14 @@
 //   dx_j = (exp(x_j - m) / sum - [j = label]) * scale * weight
 //
 // Bound by HBM.  cross_entropy_cluster_kernel keeps a row on the chip: up to eight
-// CTAs of a cluster share it, each thread reads its 32 elements once, takes their
+// CTAs of a cluster share it, each thread reads its 64 elements once, takes their
 // exponentials from its own maximum, and scales them when the row's maximum and
-// sum are known: one exponential an element (two, one for the sum and one for
-// the gradient, are 450 of the 620 us that the bytes of 8192 x 128256 in bf16
-// take).  The CTAs stay for many rows, and the next row's elements are on their
-// way (cp.async) meanwhile.  cross_entropy_kernel reads the row twice, the second
-// time out of L1 or L2: rows of up to 1024 columns by a warp each, and those
-// beyond eight CTAs' reach by a CTA.
+// sum are known: one exponential an element (with two, one for the sum and one
+// for the gradient, 8192 x 128256 in bf16 took 1190 us).  The CTAs stay for many
+// rows, and the next rows' elements are on their way (cp.async) meanwhile.
+// cross_entropy_kernel reads the row twice, the second time out of L1 or L2: rows
+// of up to 1024 columns by a warp each, and those beyond eight CTAs' reach by a
+// CTA.
 // Groups of 16 bytes begin at the row's first multiple of 16 bytes, the elements
 // around them go to one thread each.
 
@@ -151,16 +151,16 @@ cross_entropy_kernel(const __grid_constant__ opt_cross_entropy_args a) {
 
 // ---------------------------------------------------------------- cluster --
 
-// Threads of a CTA and elements of a thread; stages of the ring.
-constexpr int kElems = 32;
+constexpr int kElems = 64;                       // of a thread
 constexpr int kMaxCluster = 8;
 
 template <typename T, int kThreads>
 struct Config {
   static constexpr int kGroups = kElems / Group<T>::kN;            // of a thread
   static constexpr int kStageBytes = kGroups * kThreads * 16;
-  static constexpr int kCtas = 1024 / kThreads;                    // to an SM: 64 registers a thread
-  static constexpr int kStages = (192 * 1024) / kCtas / kStageBytes;
+  static constexpr int kCtas = 512 / kThreads;                     // to an SM: 128 registers a thread
+  static constexpr int kStages = 192 * 1024 / kCtas / kStageBytes; // rows on their way
+  static constexpr int kBytes = kStages * kStageBytes;
   static_assert(kStages >= 1, "the ring holds a row's share");
 };
 
@@ -212,104 +212,119 @@ cross_entropy_cluster_kernel(const __grid_constant__ opt_cross_entropy_args a, i
   constexpr int kN = Group<T>::kN, kWarps = kThreads / 32, kGroups = C::kGroups;
   extern __shared__ uint4 ring[];                // [kStages][kGroups][kThreads]
   __shared__ float2 parts[2][kMaxCluster * kWarps];        // every warp's of the cluster
+  __shared__ uint64_t bars[2];
   let_next_start();
   wait_for_predecessors();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, cols = static_cast<int>(a.cols);
   const int rank = cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
-  if (cluster > 1) cluster_sync();               // every CTA of the cluster has begun
+  const Mailbox mail{bars};
+  if (cluster > 1) {                             // every CTA of the cluster has begun
+    if (t == 0) mail.init();
+    cluster_sync();
+  }
   const int64_t step = gridDim.x / cluster;
   const int mine = rank * kGroups * kThreads + t;          // this thread's first group
   auto row_at = [&](int64_t r) { return static_cast<const T*>(a.logits) + r * a.logits_ld; };
   auto label_at = [&](int64_t r) {
-    return a.index_dtype == OPT_INDEX_INT32 ? static_cast<int64_t>(static_cast<const int32_t*>(a.labels)[r])
-                                            : static_cast<const int64_t*>(a.labels)[r];
+    const int64_t v = a.index_dtype == OPT_INDEX_INT32 ? static_cast<int64_t>(static_cast<const int32_t*>(a.labels)[r])
+                                                       : static_cast<const int64_t*>(a.labels)[r];
+    return v >= 0 && v < cols ? static_cast<int>(v) : -1;
   };
+  // row r into a stage, this thread's own places; a commit in any case
   auto fetch = [&](int64_t r, int stage) {
     if (r < a.rows) {
       const T* x = row_at(r);
       const Place p = place_of(x, cols);
       const T* from = x + p.head + mine * kN;
+      uint4* to = ring + stage * kGroups * kThreads + t;
 #pragma unroll
       for (int i = 0; i < kGroups; ++i)
-        if (mine + i * kThreads < p.groups) copy16(ring + (stage * kGroups + i) * kThreads + t, from + i * kThreads * kN);
+        if (mine + i * kThreads < p.groups) copy16(to + i * kThreads, from + i * kThreads * kN);
     }
     copy_commit();
   };
   int64_t r = blockIdx.x / cluster;
   for (int s = 0; s < C::kStages; ++s) fetch(r + s * step, s);
-  int64_t label = label_at(r), next_label = 0;   // the grid has no more clusters than rows
-  int parity = 0, stage = 0;
-  for (; r < a.rows; r += step, parity ^= 1, label = next_label) {
+  int label = label_at(r), next_label = -1;      // the grid has no more clusters than rows
+  bool lost = false;                             // a message of the cluster's
+  for (int k = 0, stage = 0; r < a.rows; ++k, r += step, label = next_label, stage = stage + 1 == C::kStages ? 0 : stage + 1) {
     const T* x = row_at(r);
     const Place p = place_of(x, cols);
     if (r + step < a.rows) next_label = label_at(r + step);
-    const bool counts = label >= 0 && label < cols;
     const float w = a.weight ? a.weight[r] * a.scale : a.scale;
-    const float at_label = rank == 0 && t == 0 && counts ? load_elem(x + label) : 0.f;
     // the column outside of the groups that this thread has, or -1
     const int edge = rank ? -1 : t < p.head ? t : t < p.head + cols - p.end ? p.end + t - p.head : -1;
-    float e[kGroups][kN], ee = edge >= 0 ? load_elem(x + edge) : -INFINITY, top = ee;
+    const float at_edge = edge >= 0 ? load_elem(x + edge) : -INFINITY;
     copy_wait<C::kStages - 1>();
+    const uint4* from = ring + stage * kGroups * kThreads + t;
+    float e[kGroups][kN], top = at_edge;
     {
       uint4 raw[kGroups];
 #pragma unroll
       for (int i = 0; i < kGroups; ++i) {
         const uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;       // -inf
-        raw[i] = mine + i * kThreads < p.groups ? ring[(stage * kGroups + i) * kThreads + t] : make_uint4(none, none, none, none);
+        raw[i] = mine + i * kThreads < p.groups ? from[i * kThreads] : make_uint4(none, none, none, none);
         top = fmaxf(top, group_max(raw[i], static_cast<const T*>(nullptr)));
       }
 #pragma unroll
       for (int i = 0; i < kGroups; ++i) group_values(raw[i], e[i]);
     }
-    const float own = anchor(top);
-    float sum = ee = exp_of(ee - own);
+    // the label's group and its place there, where it is this thread's
+    const int hot = label - p.head, away = hot / kN - mine;
+    const bool hot_here = label >= 0 && hot >= 0 && hot < p.groups * kN && away >= 0 && away < kGroups * kThreads &&
+                          away % kThreads == 0;
+    float at_label = at_edge;
+    if (hot_here) at_label = load_elem(reinterpret_cast<const T*>(from + away) + (hot & (kN - 1)));
+    const float own = anchor(top), edge_e = exp_of(at_edge - own);
+    float sum = edge_e;
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i)
+    for (int i = 0; i < kGroups; ++i) {
+      float part = 0.f;
 #pragma unroll
       for (int j = 0; j < kN; ++j) {
         e[i][j] = exp_of(e[i][j] - own);
-        sum += e[i][j];
+        part += e[i][j];
       }
-    fetch(r + C::kStages * step, stage);         // this thread's own places: it is done with them
-    stage = stage + 1 == C::kStages ? 0 : stage + 1;
+      sum += part;
+    }
+    fetch(r + C::kStages * step, stage);         // over what this thread has read
     Stat s = warp_join(Stat{top, sum});
     if (cluster > 1) {                           // lane i tells CTA i
-      if (lane < cluster) store_peer(at_peer(&parts[parity][rank * kWarps + warp], lane), make_float2(s.top, s.sum));
-      cluster_sync();
+      if (t == 0) mail.expect(k, static_cast<uint32_t>(cluster) * kWarps * 8);
+      if (lane < cluster) mail.send(k, &parts[k & 1][rank * kWarps + warp], lane, make_float2(s.top, s.sum));
+      lost = lost || !mail.wait(k);
     } else {
-      if (lane == 0) parts[parity][warp] = make_float2(s.top, s.sum);
+      if (lane == 0) parts[k & 1][warp] = make_float2(s.top, s.sum);
       __syncthreads();
     }
     s = Stat{-INFINITY, 0.f};
     for (int i = lane; i < cluster * kWarps; i += 32) {
-      const float2 q = parts[parity][i];
+      const float2 q = parts[k & 1][i];
       s = join(s, Stat{q.x, q.y});
     }
     s = warp_join(s);
+    if (lost) s.sum = __uint_as_float(0x7fc00000u);
     const bool none = s.sum == 0.f;              // an empty row
     if (rank == 0 && t == 0) {
-      const float log_sum = logf(s.sum);
-      if (a.lse) a.lse[r] = none ? -INFINITY : s.top + log_sum;
-      if (a.loss) a.loss[r] = !counts ? 0.f : none ? INFINITY : log_sum - (at_label - anchor(s.top));
+      if (a.lse) a.lse[r] = none ? -INFINITY : s.top + logf(s.sum);
+      if (a.loss && label < 0) a.loss[r] = 0.f;
     }
+    if (a.loss && label >= 0 && (hot_here || edge == label))
+      a.loss[r] = none ? INFINITY : logf(s.sum) - (at_label - anchor(s.top));
     if (!a.dlogits) continue;
     T* g = static_cast<T*>(a.dlogits) + r * a.dlogits_ld;
-    const bool zero = !counts || none;
+    const bool zero = label < 0 || none;
     const float inv = exp_of(top - anchor(s.top)) / s.sum, inv_w = inv * w;
-    if (edge >= 0) store_elem(g + edge, zero ? 0.f : (ee * inv - (edge == static_cast<int>(label) ? 1.f : 0.f)) * w);
+    if (edge >= 0) store_elem(g + edge, zero ? 0.f : (edge_e * inv - (edge == label ? 1.f : 0.f)) * w);
     const bool together = (reinterpret_cast<uintptr_t>(g + p.head) & 15u) == 0;
-    // the label's group and its place there
-    const int hot = counts ? static_cast<int>(label) - p.head : -1;
-    const int hot_group = hot >= 0 ? hot / kN : -1;
     T* to = g + p.head + mine * kN;
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
-      const int group = mine + i * kThreads;
-      if (group >= p.groups) break;
+      if (mine + i * kThreads >= p.groups) break;
       if (zero) {
 #pragma unroll
         for (int j = 0; j < kN; ++j) e[i][j] = 0.f;
-      } else if (group == hot_group) {
+      } else if (hot_here && away == i * kThreads) {
 #pragma unroll
         for (int j = 0; j < kN; ++j) e[i][j] = (e[i][j] * inv - (j == (hot & (kN - 1)) ? 1.f : 0.f)) * w;
       } else {
@@ -324,6 +339,7 @@ cross_entropy_cluster_kernel(const __grid_constant__ opt_cross_entropy_args a, i
       }
     }
   }
+  if (cluster > 1) cluster_sync();               // nobody leaves while mail to it is on its way
 }
 
 // Clusters that the GPU holds at once (asked once for each device).
@@ -360,7 +376,7 @@ int clusters_at_once(int cluster, size_t smem, cudaError_t* error) {
 template <typename T, int kThreads>
 cudaError_t launch_cluster(const opt_cross_entropy_args& a, int cluster, cudaStream_t stream) {
   using C = Config<T, kThreads>;
-  const size_t smem = static_cast<size_t>(C::kStages) * C::kStageBytes;
+  const size_t smem = C::kBytes;
   cudaError_t e = cudaSuccess;
   const int64_t most = clusters_at_once<T, kThreads>(cluster, smem, &e);
   if (e != cudaSuccess) return e;
@@ -373,11 +389,11 @@ template <typename T>
 cudaError_t launch_rows(const opt_cross_entropy_args& a, cudaStream_t stream) {
   if (a.cols <= 1024)
     return launch_overlapped(cross_entropy_kernel<T, 32>, dim3(static_cast<unsigned>((a.rows + 7) / 8)), 256, 0, stream, 0, a);
+  if (a.cols <= 64 * kElems) return launch_cluster<T, 64>(a, 1, stream);
   if (a.cols <= 128 * kElems) return launch_cluster<T, 128>(a, 1, stream);
-  if (a.cols <= 256 * kElems) return launch_cluster<T, 256>(a, 1, stream);
   int cluster = 1;
-  while (cluster < kMaxCluster && a.cols > static_cast<int64_t>(cluster) * 512 * kElems) cluster *= 2;
-  if (a.cols <= static_cast<int64_t>(cluster) * 512 * kElems) return launch_cluster<T, 512>(a, cluster, stream);
+  while (cluster < kMaxCluster && a.cols > static_cast<int64_t>(cluster) * 256 * kElems) cluster *= 2;
+  if (a.cols <= static_cast<int64_t>(cluster) * 256 * kElems) return launch_cluster<T, 256>(a, cluster, stream);
   return launch_overlapped(cross_entropy_kernel<T, 1024>, dim3(static_cast<unsigned>(a.rows)), 1024, 0, stream, 0, a);
 }
 

@@ -226,8 +226,8 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __gr
     }
     if (lane == 31) scan[warp] = up;
     __syncthreads();
-    uint32_t base = up - all + before;
-    for (int w = 0; w < warp; ++w) base += scan[w];
+    uint32_t base = lane < warp ? scan[lane] : 0u;               // the warps before this one
+    base = __reduce_add_sync(0xffffffffu, base) + up - all + before;
     if (d < bins) {
 #pragma unroll
       for (int w = 0; w < kSortWarps; ++w) counts[w * bins + d] += base;
@@ -266,7 +266,8 @@ struct SumArgs {
 // 4 columns to a thread, 16 bytes of the table, or one.
 template <bool kVec>
 constexpr int kSumCols = kVec ? 4 : 1;
-constexpr int kAhead = 8;                        // rows on their way to a thread
+constexpr int kAhead = 4;                        // rows on their way to a thread together
+constexpr int kJoinAhead = 8;
 
 // A run's sum goes to the table if the run lies within the piece, else to the
 // piece's first partial row (a run that came from the piece before) or its
@@ -298,15 +299,15 @@ __global__ void __launch_bounds__(kThreads) embedding_sums_kernel(const __grid_c
 #pragma unroll
   for (int j = 0; j < kN; ++j) sum[j] = 0.f;
   bool from_before = key[0] == key[1];
-  float next[kAhead][kN], old[kAhead][kN];
-  auto fetch = [&](int i, float (&v)[kN], float (&o)[kN]) {
-    if (i >= n || key[i + 1] == none) return;
-    load_columns(dy + row[i] * a.dy_ld, v);
-    if (key[i + 2] != key[i + 1]) load_columns(static_cast<const float*>(table) + key[i + 1] * a.cols, o);
-  };
-#pragma unroll
-  for (int u = 0; u < kAhead; ++u) fetch(u, next[u], old[u]);
   for (int i0 = 0; i0 < n; i0 += kAhead) {
+    float next[kAhead][kN], old[kAhead][kN];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u;
+      if (i >= n || key[i + 1] == none) break;
+      load_columns(dy + row[i] * a.dy_ld, next[u]);
+      if (key[i + 2] != key[i + 1]) load_columns(static_cast<const float*>(table) + key[i + 1] * a.cols, old[u]);
+    }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int i = i0 + u;
@@ -328,7 +329,6 @@ __global__ void __launch_bounds__(kThreads) embedding_sums_kernel(const __grid_c
 #pragma unroll
         for (int j = 0; j < kN; ++j) sum[j] = 0.f;
       }
-      fetch(i + kAhead, next[u], old[u]);
     }
   }
 }
@@ -360,13 +360,13 @@ __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_c
   float* table = a.dtable + v * a.cols + c;
   load_columns(static_cast<const float*>(table), old);
   load_columns(static_cast<const float*>(p.partial) + (2 * static_cast<int64_t>(piece) + 1) * a.cols + c, sum);
-  for (int64_t q0 = piece + 1; q0 <= last_piece; q0 += kAhead) {
-    float part[kAhead][kN];
+  for (int64_t q0 = piece + 1; q0 <= last_piece; q0 += kJoinAhead) {
+    float part[kJoinAhead][kN];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
+    for (int u = 0; u < kJoinAhead; ++u)
       if (q0 + u <= last_piece) load_columns(static_cast<const float*>(p.partial) + 2 * (q0 + u) * a.cols + c, part[u]);
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
+    for (int u = 0; u < kJoinAhead; ++u)
       if (q0 + u <= last_piece) {
 #pragma unroll
         for (int j = 0; j < kN; ++j) sum[j] += part[u][j];

@@ -371,7 +371,7 @@ cudaError_t launch_embedding(const opt_embedding_args& a, cudaStream_t stream);
 // The embedding's gradient sums the rows of the batch sorted by token in pieces of
 // kEmbeddingPiece, of few rows in shorter ones: what a CTA adds one row after
 // another is what such a call waits for.
-constexpr int kEmbeddingPiece = 64, kEmbeddingShortPiece = 16;
+constexpr int kEmbeddingPiece = 32, kEmbeddingShortPiece = 16;
 constexpr int64_t kEmbeddingShort = 8192;
 inline int embedding_piece(int64_t rows) { return rows <= kEmbeddingShort ? kEmbeddingShortPiece : kEmbeddingPiece; }
 inline int64_t embedding_pieces(int64_t rows) { return (rows + embedding_piece(rows) - 1) / embedding_piece(rows); }

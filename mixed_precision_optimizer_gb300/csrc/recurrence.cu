@@ -90,13 +90,14 @@ struct Shared {
   int* first;            // [kChunk] with starts: the sequence that a row starts (set where one does)
   int* last;             // [kChunk]              the sequence that a row ends
   Span* span;
+  Mailbox mail;
 };
 
 template <typename T, int kTensors>
 struct Layout {
   static constexpr int kStage = kTensors * kTile<T> * kWarps;
   static size_t bytes(int cluster) {
-    return 2 * kStage + (2 * kWarps * 8 + (cluster > 1 ? 2 * cluster * 8 : 0) + 2 * 4) * kCols + 2 * kChunk * 4 + sizeof(Span);
+    return 2 * kStage + (2 * kWarps * 8 + (cluster > 1 ? 2 * cluster * 8 : 0) + 2 * 4) * kCols + 2 * kChunk * 4 + sizeof(Span) + 16;
   }
   static __device__ __forceinline__ Shared carve(uint8_t* base, int cluster) {
     Shared s;
@@ -107,6 +108,7 @@ struct Layout {
     s.first = reinterpret_cast<int*>(s.state + 2 * kCols);
     s.last = s.first + kChunk;
     s.span = reinterpret_cast<Span*>(s.last + kChunk);
+    s.mail.bar = reinterpret_cast<uint64_t*>(s.span + 1);
     return s;
   }
 };
@@ -336,11 +338,13 @@ __device__ __forceinline__ void load_state(const float* states, int64_t seq, int
 // column each: they join the warps' pieces to what stands before every warp, tell
 // the CTAs of the cluster the whole of it, and keep in `carry` the state behind
 // all their rows.  kBack: rows, warps and CTAs are taken from the last to the
-// first.  The places alternate with the turns (`parity`): a thread writes to one
-// again only after a barrier that all threads reach when they have read it.
+// first.  The places alternate with the turns: a thread writes to one again only
+// after a barrier, or a message from every CTA, that comes when it has been read.
+// A message that does not come leaves NaN.
 template <bool kVec, bool kBack>
-__device__ __forceinline__ void exchange(const Shared& sh, int parity, int cluster, uint32_t rank, int warp, int lane,
-                                         const Piece (&mine)[2], float& carry, float (&state)[2]) {
+__device__ __forceinline__ void exchange(const Shared& sh, int turn, int cluster, uint32_t rank, int warp, int lane,
+                                         const Piece (&mine)[2], float& carry, bool& lost, float (&state)[2]) {
+  const int parity = turn & 1;
   float2* pieces = sh.pieces + parity * kWarps * kCols;
   float* before = sh.state + parity * kCols;
   const int c0 = kVec ? 2 * lane : lane, c1 = kVec ? 2 * lane + 1 : lane + 32;
@@ -362,19 +366,17 @@ __device__ __forceinline__ void exchange(const Shared& sh, int parity, int clust
     if (cluster == 1) {
       before[c] = carry;
       carry = through(all, carry);
-    }
-  }
-  if (cluster > 1) {
-    float2* inbox = sh.inbox + parity * cluster * kCols;
-    if (c < kCols)
-      for (int i = 0; i < cluster; ++i) store_peer(at_peer(inbox + rank * kCols + c, i), make_float2(all.p, all.b));
-    cluster_sync();
-    if (c < kCols) {
+    } else {
+      float2* inbox = sh.inbox + parity * cluster * kCols;
+      if (c == 0) sh.mail.expect(turn, static_cast<uint32_t>(cluster) * kCols * 8);
+      for (int i = 0; i < cluster; ++i) sh.mail.send(turn, inbox + rank * kCols + c, i, make_float2(all.p, all.b));
+      lost = lost || !sh.mail.wait(turn);
+      if (lost) carry = __uint_as_float(0x7fc00000u);
       for (int i = 0; i < cluster; ++i) {
         const int w = kBack ? cluster - 1 - i : i;
         if (w == static_cast<int>(rank)) before[c] = carry;
         const float2 q = inbox[w * kCols + c];
-        carry = through(Piece{q.x, q.y}, carry);
+        carry = lost ? carry : through(Piece{q.x, q.y}, carry);
       }
     }
   }
@@ -403,7 +405,10 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
   const uint32_t rank = plan.cluster > 1 ? cluster_rank() : 0;
   const int id = blockIdx.x / plan.cluster;
   const int64_t col = static_cast<int64_t>(id % plan.groups) * kCols;
-  if (plan.cluster > 1) cluster_sync();          // every CTA of the cluster has begun
+  if (plan.cluster > 1) {                        // every CTA of the cluster has begun
+    if (threadIdx.x == 0) sh.mail.init();
+    cluster_sync();
+  }
   const Span span = span_of<kRagged>(plan, a.starts, a.rows, a.sequences, id / plan.groups, rank, sh);
   if (kRagged && rank == 0) pass_empty(a.starts, span, a.hT, a.h0, col, a.cols);
   const int64_t base = span.row / kS * kS, step = static_cast<int64_t>(plan.cluster) * kChunk;
@@ -420,6 +425,7 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
   };
   fetch(row, 0);
   float carry = 0.f;                             // the first kCols threads: behind all rows so far
+  bool lost = false;                             // a message of the cluster's
   for (int turn = 0; turn < turns; ++turn, row += step) {
     copy_wait<0>();
     __syncwarp();
@@ -457,7 +463,7 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
     if (plain) pieces(Flag<true>{});
     else pieces(Flag<false>{});
     float h[2];
-    exchange<kVec, false>(sh, turn & 1, plan.cluster, rank, warp, lane, mine, carry, h);
+    exchange<kVec, false>(sh, turn, plan.cluster, rank, warp, lane, mine, carry, lost, h);
     if (a.states && row >= span.row && row < span.row_end)
       store_pair<float, kVec>(a.states + row / kS * a.cols, col, a.cols, lane, h[0], h[1]);
     T* y = static_cast<T*>(a.y) + row * a.y_ld;
@@ -482,6 +488,7 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
     else outputs(Flag<false>{});
     __syncwarp();                                // the tile may be written over
   }
+  if (plan.cluster > 1) cluster_sync();          // nobody leaves while mail to it is on its way
 }
 
 // One row to each sequence: nothing depends on another row.
@@ -533,7 +540,10 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
   const uint32_t rank = plan.cluster > 1 ? cluster_rank() : 0;
   const int id = blockIdx.x / plan.cluster;
   const int64_t col = static_cast<int64_t>(id % plan.groups) * kCols;
-  if (plan.cluster > 1) cluster_sync();          // every CTA of the cluster has begun
+  if (plan.cluster > 1) {                        // every CTA of the cluster has begun
+    if (threadIdx.x == 0) sh.mail.init();
+    cluster_sync();
+  }
   const Span span = span_of<kRagged>(plan, a.starts, a.rows, a.sequences, id / plan.groups, rank, sh);
   if (kRagged && rank == 0) pass_empty(a.starts, span, a.dh0, a.dhT, col, a.cols);
   const int64_t base = span.row / kS * kS, step = static_cast<int64_t>(plan.cluster) * kChunk;
@@ -556,6 +566,7 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
   fetch(row, 0);
   saved(row, coming);
   float carry = 0.f;                             // the first kCols threads: behind all rows so far
+  bool lost = false;                             // a message of the cluster's
   for (int turn = 0; turn < turns; ++turn, row -= step) {
     copy_wait<0>();
     __syncwarp();
@@ -609,7 +620,7 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
     if (plain) pieces(Flag<true>{});
     else pieces(Flag<false>{});
     float b[2];                                  // (1 - c) l of the row behind
-    exchange<kVec, true>(sh, turn & 1, plan.cluster, rank, warp, lane, mine, carry, b);
+    exchange<kVec, true>(sh, turn, plan.cluster, rank, warp, lane, mine, carry, lost, b);
     T* dx = static_cast<T*>(a.dx) + (row + kS - 1) * a.dx_ld;
     T* dg = static_cast<T*>(a.dgate) + (row + kS - 1) * a.dgate_ld;
     auto outputs = [&](auto plain) {
@@ -642,6 +653,7 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
     else outputs(Flag<false>{});
     __syncwarp();                                // the tile may be written over
   }
+  if (plan.cluster > 1) cluster_sync();          // nobody leaves while mail to it is on its way
 }
 
 // ---------------------------------------------------------------- launch --
