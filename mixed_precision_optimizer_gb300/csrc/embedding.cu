@@ -34,6 +34,23 @@ __device__ __forceinline__ int64_t token_at(const void* tokens, int index_dtype,
 
 // --------------------------------------------------------------- columns --
 
+// Four columns as loaded (bf16 stays packed until it is used), or one.
+template <typename T, int kN>
+struct Raw {
+  float v[kN];
+  __device__ __forceinline__ void load(const T* p);
+  __device__ __forceinline__ float get(int j) const { return v[j]; }
+};
+template <>
+struct Raw<__nv_bfloat16, 4> {
+  uint2 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ float get(int j) const {
+    const uint32_t u = j < 2 ? w.x : w.y;
+    return __uint_as_float(j & 1 ? u & 0xffff0000u : u << 16);
+  }
+};
+
 // One, 4 or 8 neighbouring columns.
 __device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
   const float4 f = *reinterpret_cast<const float4*>(p);
@@ -61,6 +78,11 @@ __device__ __forceinline__ void store_columns(T* p, const float (&v)[kN]) {
   if constexpr (kN == 8) store8(p, v);
   else if constexpr (kN == 4) store4(p, v);
   else store_elem(p, v[0]);
+}
+
+template <typename T, int kN>
+__device__ __forceinline__ void Raw<T, kN>::load(const T* p) {
+  load_columns(p, v);
 }
 
 // ---------------------------------------------------------------- lookup --
@@ -266,7 +288,7 @@ struct SumArgs {
 // 4 columns to a thread, 16 bytes of the table, or one.
 template <bool kVec>
 constexpr int kSumCols = kVec ? 4 : 1;
-constexpr int kAhead = 4;                        // rows on their way to a thread together
+constexpr int kAhead = 8;                        // rows on their way to a thread together
 constexpr int kJoinAhead = 8;
 
 // A run's sum goes to the table if the run lies within the piece, else to the
@@ -300,12 +322,13 @@ __global__ void __launch_bounds__(kThreads) embedding_sums_kernel(const __grid_c
   for (int j = 0; j < kN; ++j) sum[j] = 0.f;
   bool from_before = key[0] == key[1];
   for (int i0 = 0; i0 < n; i0 += kAhead) {
-    float next[kAhead][kN], old[kAhead][kN];
+    Raw<T, kN> next[kAhead];
+    float old[kAhead][kN];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int i = i0 + u;
       if (i >= n || key[i + 1] == none) break;
-      load_columns(dy + row[i] * a.dy_ld, next[u]);
+      next[u].load(dy + row[i] * a.dy_ld);
       if (key[i + 2] != key[i + 1]) load_columns(static_cast<const float*>(table) + key[i + 1] * a.cols, old[u]);
     }
 #pragma unroll
@@ -315,7 +338,7 @@ __global__ void __launch_bounds__(kThreads) embedding_sums_kernel(const __grid_c
       const uint32_t v = key[i + 1];
       if (v == none) return;                     // and so are all rows behind it
 #pragma unroll
-      for (int j = 0; j < kN; ++j) sum[j] += next[u][j];
+      for (int j = 0; j < kN; ++j) sum[j] += next[u].get(j);
       const bool ends_here = key[i + 2] != v;
       if (ends_here || i + 1 == n) {
         if (from_before || !ends_here) {

@@ -13,7 +13,7 @@
 // and B is selected, not multiplied, so that an infinity or a NaN stays in its
 // own sequence.
 //
-// A warp has 64 columns, two to a lane, and 8 rows at a time in shared memory,
+// A warp has 64 columns, two to a lane (or 128, four), and 8 rows at a time in shared memory,
 // fetched with cp.async while it works on the rows before.  Its CTA's eight
 // pieces, and those of the CTAs of a cluster, which take the next rows each, are
 // joined through (distributed) shared memory; then every thread runs through its
@@ -31,7 +31,6 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCols = 64;                        // of a CTA
 constexpr int kMaxCluster = 8;
 constexpr int kS = kRecurrenceStateRows;         // rows of a thread at a time
 constexpr int kChunk = kWarps * kS;              // of a CTA
@@ -64,12 +63,13 @@ __device__ __forceinline__ float update_gate(float g) { return reciprocal(1.f + 
 
 // ----------------------------------------------------------------- layout --
 
-template <typename T>
-constexpr int kTile = kS * kCols * static_cast<int>(sizeof(T));   // bytes of a warp's rows of one tensor
+// kC columns to a lane, 32 kC to a CTA.
+template <typename T, int kC>
+constexpr int kTile = kS * 32 * kC * static_cast<int>(sizeof(T));   // bytes of a warp's rows of one tensor
 
 // CTAs to an SM, by registers and shared memory.
-template <typename T>
-constexpr int kForwardCtas = sizeof(T) == 2 ? 4 : 3;
+template <typename T, int kC>
+constexpr int kForwardCtas = kC == 4 ? 2 : sizeof(T) == 2 ? 4 : 3;
 template <typename T>
 constexpr int kBackwardCtas = sizeof(T) == 2 ? 3 : 2;
 
@@ -93,9 +93,10 @@ struct Shared {
   Mailbox mail;
 };
 
-template <typename T, int kTensors>
+template <typename T, int kC, int kTensors>
 struct Layout {
-  static constexpr int kStage = kTensors * kTile<T> * kWarps;
+  static constexpr int kCols = 32 * kC;
+  static constexpr int kStage = kTensors * kTile<T, kC> * kWarps;
   static size_t bytes(int cluster) {
     return 2 * kStage + (2 * kWarps * 8 + (cluster > 1 ? 2 * cluster * 8 : 0) + 2 * 4) * kCols + 2 * kChunk * 4 + sizeof(Span) + 16;
   }
@@ -237,6 +238,7 @@ __device__ __forceinline__ Marks marks_ragged(const int32_t* starts, int64_t row
 }
 
 // out[s] <- in[s] (zeros without in) for the span's sequences that have no row.
+template <int kCols>
 __device__ __forceinline__ void pass_empty(const int32_t* starts, const Span& span, float* out, const float* in,
                                            int64_t col, int64_t cols) {
   if (!out) return;
@@ -247,14 +249,16 @@ __device__ __forceinline__ void pass_empty(const int32_t* starts, const Span& sp
 
 // --------------------------------------------------------------- elements --
 
-// Copies a warp's rows of one tensor to its place in shared memory, [kS][64], zeros
+// Copies a warp's rows of one tensor to its place in shared memory, [kS][kCols], zeros
 // where there is no row or column.  `whole`: they are all there.
-template <typename T, bool kVec>
+template <typename T, int kC, bool kVec>
 __device__ __forceinline__ void fetch_rows(uint8_t* dst, const void* src, int64_t ld, int64_t row, const Span& span,
                                            int64_t col, int64_t cols, int lane, bool whole) {
+  constexpr int kCols = 32 * kC;
   const T* p = static_cast<const T*>(src);
   if constexpr (kVec) {
     constexpr int kPer = 16 / sizeof(T), kPieces = kCols / kPer, kStep = 32 / kPieces;   // 16-byte pieces of a row, rows a step
+    static_assert(kPieces <= 32, "a step takes whole rows");
     const int64_t r0 = row + lane / kPieces, c = col + lane % kPieces * kPer;
     const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst)) + lane * 16;
     if (whole) {
@@ -275,7 +279,7 @@ __device__ __forceinline__ void fetch_rows(uint8_t* dst, const void* src, int64_
   } else {
     T* to = reinterpret_cast<T*>(dst);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < kC; ++k) {
       const int64_t c = col + k * 32 + lane;
 #pragma unroll
       for (int j = 0; j < kS; ++j) {
@@ -286,50 +290,63 @@ __device__ __forceinline__ void fetch_rows(uint8_t* dst, const void* src, int64_
   }
 }
 
-// A lane's two columns of a row in shared memory: neighbours (kVec), or 32 apart.
-template <typename T, bool kVec>
-__device__ __forceinline__ void pair_at(const uint8_t* tile, int j, int lane, float (&v)[2]) {
-  const T* row = reinterpret_cast<const T*>(tile) + j * kCols;
+// A lane's columns of a row in shared memory: neighbours (kVec), or 32 apart.
+template <typename T, int kC, bool kVec>
+__device__ __forceinline__ void columns_at(const uint8_t* tile, int j, int lane, float (&v)[kC]) {
+  const T* row = reinterpret_cast<const T*>(tile) + j * 32 * kC;
   if constexpr (!kVec) {
-    v[0] = load_elem(row + lane);
-    v[1] = load_elem(row + 32 + lane);
+#pragma unroll
+    for (int k = 0; k < kC; ++k) v[k] = load_elem(row + 32 * k + lane);
   } else if constexpr (sizeof(T) == 2) {
-    const uint32_t u = reinterpret_cast<const uint32_t*>(row)[lane];
-    v[0] = __uint_as_float(u << 16);
-    v[1] = __uint_as_float(u & 0xffff0000u);
-  } else {
+    uint32_t u[kC / 2];
+    if constexpr (kC == 2) {
+      u[0] = reinterpret_cast<const uint32_t*>(row)[lane];
+    } else {
+      const uint2 w = reinterpret_cast<const uint2*>(row)[lane];
+      u[0] = w.x, u[1] = w.y;
+    }
+#pragma unroll
+    for (int k = 0; k < kC; ++k) v[k] = __uint_as_float(k & 1 ? u[k / 2] & 0xffff0000u : u[k / 2] << 16);
+  } else if constexpr (kC == 2) {
     const float2 f = reinterpret_cast<const float2*>(row)[lane];
-    v[0] = f.x;
-    v[1] = f.y;
+    v[0] = f.x, v[1] = f.y;
+  } else {
+    const float4 f = reinterpret_cast<const float4*>(row)[lane];
+    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
   }
 }
 
-template <bool kVec>
-__device__ __forceinline__ int64_t column(int64_t col, int lane, int k) {
-  return kVec ? col + 2 * lane + k : col + 32 * k + lane;
+template <int kC, bool kVec>
+__device__ __forceinline__ int column(int lane, int k) {
+  return kVec ? kC * lane + k : 32 * k + lane;
 }
 
-// Stores a lane's two columns; with kVec the number of columns is a multiple of 8.
-template <typename T, bool kVec>
-__device__ __forceinline__ void store_pair(T* row, int64_t col, int64_t cols, int lane, float a, float b) {
+// Stores a lane's columns; with kVec the number of columns is a multiple of 8.
+template <typename T, int kC, bool kVec>
+__device__ __forceinline__ void store_columns(T* row, int64_t col, int64_t cols, int lane, const float (&v)[kC]) {
   if constexpr (kVec) {
-    const int64_t c = column<true>(col, lane, 0);
-    if (c < cols) {
-      if constexpr (sizeof(T) == 2) *reinterpret_cast<uint32_t*>(row + c) = pack2(a, b);
-      else *reinterpret_cast<float2*>(row + c) = make_float2(a, b);
+    const int64_t c = col + kC * lane;
+    if (c >= cols) return;
+    if constexpr (sizeof(T) == 2) {
+      if constexpr (kC == 2) *reinterpret_cast<uint32_t*>(row + c) = pack2(v[0], v[1]);
+      else *reinterpret_cast<uint2*>(row + c) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+    } else {
+      if constexpr (kC == 2) *reinterpret_cast<float2*>(row + c) = make_float2(v[0], v[1]);
+      else *reinterpret_cast<float4*>(row + c) = make_float4(v[0], v[1], v[2], v[3]);
     }
   } else {
-    if (column<false>(col, lane, 0) < cols) store_elem(row + column<false>(col, lane, 0), a);
-    if (column<false>(col, lane, 1) < cols) store_elem(row + column<false>(col, lane, 1), b);
+#pragma unroll
+    for (int k = 0; k < kC; ++k)
+      if (col + column<kC, false>(lane, k) < cols) store_elem(row + col + column<kC, false>(lane, k), v[k]);
   }
 }
 
-template <bool kVec>
+template <int kC, bool kVec>
 __device__ __forceinline__ void load_state(const float* states, int64_t seq, int64_t col, int64_t cols, int lane,
-                                           float (&v)[2]) {
+                                           float (&v)[kC]) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int64_t c = column<kVec>(col, lane, k);
+  for (int k = 0; k < kC; ++k) {
+    const int64_t c = col + column<kC, kVec>(lane, k);
     v[k] = states && c < cols ? states[seq * cols + c] : 0.f;
   }
 }
@@ -341,15 +358,15 @@ __device__ __forceinline__ void load_state(const float* states, int64_t seq, int
 // first.  The places alternate with the turns: a thread writes to one again only
 // after a barrier, or a message from every CTA, that comes when it has been read.
 // A message that does not come leaves NaN.
-template <bool kVec, bool kBack>
+template <int kC, bool kVec, bool kBack>
 __device__ __forceinline__ void exchange(const Shared& sh, int turn, int cluster, uint32_t rank, int warp, int lane,
-                                         const Piece (&mine)[2], float& carry, bool& lost, float (&state)[2]) {
+                                         const Piece (&mine)[kC], float& carry, bool& lost, float (&state)[kC]) {
+  constexpr int kCols = 32 * kC;
   const int parity = turn & 1;
   float2* pieces = sh.pieces + parity * kWarps * kCols;
   float* before = sh.state + parity * kCols;
-  const int c0 = kVec ? 2 * lane : lane, c1 = kVec ? 2 * lane + 1 : lane + 32;
-  pieces[warp * kCols + c0] = make_float2(mine[0].p, mine[0].b);
-  pieces[warp * kCols + c1] = make_float2(mine[1].p, mine[1].b);
+#pragma unroll
+  for (int k = 0; k < kC; ++k) pieces[warp * kCols + column<kC, kVec>(lane, k)] = make_float2(mine[k].p, mine[k].b);
   __syncthreads();
   const int c = threadIdx.x;
   Piece all{1.f, 0.f};
@@ -381,9 +398,12 @@ __device__ __forceinline__ void exchange(const Shared& sh, int turn, int cluster
     }
   }
   __syncthreads();
-  const float2 p0 = pieces[warp * kCols + c0], p1 = pieces[warp * kCols + c1];
-  state[0] = through(Piece{p0.x, p0.y}, before[c0]);
-  state[1] = through(Piece{p1.x, p1.y}, before[c1]);
+#pragma unroll
+  for (int k = 0; k < kC; ++k) {
+    const int at = column<kC, kVec>(lane, k);
+    const float2 q = pieces[warp * kCols + at];
+    state[k] = through(Piece{q.x, q.y}, before[at]);
+  }
 }
 
 // --------------------------------------------------------------- forward --
@@ -393,10 +413,11 @@ struct Flag {
   static constexpr bool value = kValue;
 };
 
-template <typename T, bool kVec, bool kRagged>
-__global__ void __launch_bounds__(kThreads, kForwardCtas<T>)
+template <typename T, int kC, bool kVec, bool kRagged>
+__global__ void __launch_bounds__(kThreads, (kForwardCtas<T, kC>))
 recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_constant__ Plan plan) {
-  using L = Layout<T, 2>;
+  constexpr int kCols = 32 * kC;
+  using L = Layout<T, kC, 2>;
   extern __shared__ __align__(128) uint8_t smem[];
   let_next_start();
   wait_for_predecessors();
@@ -410,16 +431,16 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
     cluster_sync();
   }
   const Span span = span_of<kRagged>(plan, a.starts, a.rows, a.sequences, id / plan.groups, rank, sh);
-  if (kRagged && rank == 0) pass_empty(a.starts, span, a.hT, a.h0, col, a.cols);
+  if (kRagged && rank == 0) pass_empty<kCols>(a.starts, span, a.hT, a.h0, col, a.cols);
   const int64_t base = span.row / kS * kS, step = static_cast<int64_t>(plan.cluster) * kChunk;
   const int64_t turns = span.row_end > span.row ? (span.row_end - base + step - 1) / step : 0;
   int64_t next = kRagged ? span.seq : span.row, row = base + (static_cast<int64_t>(rank) * kWarps + warp) * kS;
-  auto stage = [&](int turn) { return smem + (turn & 1) * L::kStage + warp * 2 * kTile<T>; };
+  auto stage = [&](int turn) { return smem + (turn & 1) * L::kStage + warp * 2 * kTile<T, kC>; };
   auto fetch = [&](int64_t r, int turn) {
     if (r < span.row_end) {
       const bool whole = r >= span.row && r + kS <= span.row_end && col + kCols <= a.cols;
-      fetch_rows<T, kVec>(stage(turn), a.x, a.x_ld, r, span, col, a.cols, lane, whole);
-      fetch_rows<T, kVec>(stage(turn) + kTile<T>, a.gate, a.gate_ld, r, span, col, a.cols, lane, whole);
+      fetch_rows<T, kC, kVec>(stage(turn), a.x, a.x_ld, r, span, col, a.cols, lane, whole);
+      fetch_rows<T, kC, kVec>(stage(turn) + kTile<T, kC>, a.gate, a.gate_ld, r, span, col, a.cols, lane, whole);
     }
     copy_commit();
   };
@@ -433,55 +454,60 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
     Marks m;
     if constexpr (kRagged) m = marks_ragged<false>(a.starts, a.rows, span, row, next, sh, warp, lane);
     else m = marks_equal<false>(plan, span, row, next, lane);
-    const uint8_t *xs = stage(turn), *gs = xs + kTile<T>;
-    float c[kS][2];
-    Piece mine[2] = {{1.f, 0.f}, {1.f, 0.f}};
+    const uint8_t *xs = stage(turn), *gs = xs + kTile<T, kC>;
+    float c[kS][kC];
+    Piece mine[kC];
+#pragma unroll
+    for (int k = 0; k < kC; ++k) mine[k] = Piece{1.f, 0.f};
     auto pieces = [&](auto plain) {              // plain: all rows are there, no sequence starts or ends
 #pragma unroll
       for (int j = 0; j < kS; ++j) {
-        float g[2], x[2];
-        pair_at<T, kVec>(gs, j, lane, g);
-        pair_at<T, kVec>(xs, j, lane, x);
+        float g[kC], x[kC];
+        columns_at<T, kC, kVec>(gs, j, lane, g);
+        columns_at<T, kC, kVec>(xs, j, lane, x);
         const bool in = plain.value || (row + j >= span.row && row + j < span.row_end);
         if (!plain.value && (m.start >> j & 1)) {
-          float h0[2];
-          load_state<kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, a.cols, lane, h0);
-          mine[0].b = h0[0];
-          mine[1].b = h0[1];
+          float h0[kC];
+          load_state<kC, kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, a.cols, lane, h0);
+#pragma unroll
+          for (int k = 0; k < kC; ++k) mine[k].b = h0[k];
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < kC; ++k) {
           c[j][k] = in ? update_gate(g[k]) : 0.f;
           // a row that is not there leaves b alone, whatever lies in its place
           mine[k].b = in ? fmaf(c[j][k], x[k] - mine[k].b, mine[k].b) : mine[k].b;
           mine[k].p = fmaf(-c[j][k], mine[k].p, mine[k].p);
         }
       }
-      if (!plain.value && m.start) mine[0].p = mine[1].p = kReset;
+      if (!plain.value && m.start) {
+#pragma unroll
+        for (int k = 0; k < kC; ++k) mine[k].p = kReset;
+      }
     };
     const bool plain = row >= span.row && row + kS <= span.row_end && (m.start | m.end) == 0;
     if (plain) pieces(Flag<true>{});
     else pieces(Flag<false>{});
-    float h[2];
-    exchange<kVec, false>(sh, turn, plan.cluster, rank, warp, lane, mine, carry, lost, h);
+    float h[kC];
+    exchange<kC, kVec, false>(sh, turn, plan.cluster, rank, warp, lane, mine, carry, lost, h);
     if (a.states && row >= span.row && row < span.row_end)
-      store_pair<float, kVec>(a.states + row / kS * a.cols, col, a.cols, lane, h[0], h[1]);
+      store_columns<float, kC, kVec>(a.states + row / kS * a.cols, col, a.cols, lane, h);
     T* y = static_cast<T*>(a.y) + row * a.y_ld;
     auto outputs = [&](auto plain) {
 #pragma unroll
       for (int j = 0; j < kS; ++j, y += a.y_ld) {
-        float x[2];
-        pair_at<T, kVec>(xs, j, lane, x);
+        float x[kC];
+        columns_at<T, kC, kVec>(xs, j, lane, x);
         const bool in = plain.value || (row + j >= span.row && row + j < span.row_end);
         if (!plain.value && (m.start >> j & 1))
-          load_state<kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, a.cols, lane, h);
+          load_state<kC, kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, a.cols, lane, h);
         if (in) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) h[k] = fmaf(c[j][k], x[k] - h[k], h[k]);
-          store_pair<T, kVec>(y, col, a.cols, lane, h[0], h[1]);
+          for (int k = 0; k < kC; ++k) h[k] = fmaf(c[j][k], x[k] - h[k], h[k]);
+          store_columns<T, kC, kVec>(y, col, a.cols, lane, h);
         }
         if (!plain.value && (m.end >> j & 1) && a.hT)
-          store_pair<float, kVec>(a.hT + __shfl_sync(0xffffffffu, m.end_seq, j) * a.cols, col, a.cols, lane, h[0], h[1]);
+          store_columns<float, kC, kVec>(a.hT + __shfl_sync(0xffffffffu, m.end_seq, j) * a.cols, col, a.cols, lane, h);
       }
     };
     if (plain) outputs(Flag<true>{});
@@ -528,10 +554,11 @@ __global__ void __launch_bounds__(kThreads) recurrence_step_kernel(const __grid_
 
 // From the last row to the first.  Each warp runs through its rows forward from
 // the saved state for (1 - c) (x_t - h_{t-1}), then backward twice.
-template <typename T, bool kVec, bool kRagged>
+template <typename T, int kC, bool kVec, bool kRagged>
 __global__ void __launch_bounds__(kThreads, kBackwardCtas<T>)
 recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const __grid_constant__ Plan plan) {
-  using L = Layout<T, 3>;
+  constexpr int kCols = 32 * kC;
+  using L = Layout<T, kC, 3>;
   extern __shared__ __align__(128) uint8_t smem[];
   let_next_start();
   wait_for_predecessors();
@@ -545,24 +572,24 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
     cluster_sync();
   }
   const Span span = span_of<kRagged>(plan, a.starts, a.rows, a.sequences, id / plan.groups, rank, sh);
-  if (kRagged && rank == 0) pass_empty(a.starts, span, a.dh0, a.dhT, col, a.cols);
+  if (kRagged && rank == 0) pass_empty<kCols>(a.starts, span, a.dh0, a.dhT, col, a.cols);
   const int64_t base = span.row / kS * kS, step = static_cast<int64_t>(plan.cluster) * kChunk;
   const int64_t turns = span.row_end > span.row ? (span.row_end - base + step - 1) / step : 0;
   int64_t next = kRagged ? span.seq_end + 1 : span.row_end, row = base + (turns - 1) * step + (static_cast<int64_t>(rank) * kWarps + warp) * kS;
-  auto stage = [&](int turn) { return smem + (turn & 1) * L::kStage + warp * 3 * kTile<T>; };
+  auto stage = [&](int turn) { return smem + (turn & 1) * L::kStage + warp * 3 * kTile<T, kC>; };
   auto fetch = [&](int64_t r, int turn) {
     if (r >= base && r < span.row_end) {
       const bool whole = r >= span.row && r + kS <= span.row_end && col + kCols <= a.cols;
-      fetch_rows<T, kVec>(stage(turn), a.x, a.x_ld, r, span, col, a.cols, lane, whole);
-      fetch_rows<T, kVec>(stage(turn) + kTile<T>, a.gate, a.gate_ld, r, span, col, a.cols, lane, whole);
-      fetch_rows<T, kVec>(stage(turn) + 2 * kTile<T>, a.dy, a.dy_ld, r, span, col, a.cols, lane, whole);
+      fetch_rows<T, kC, kVec>(stage(turn), a.x, a.x_ld, r, span, col, a.cols, lane, whole);
+      fetch_rows<T, kC, kVec>(stage(turn) + kTile<T, kC>, a.gate, a.gate_ld, r, span, col, a.cols, lane, whole);
+      fetch_rows<T, kC, kVec>(stage(turn) + 2 * kTile<T, kC>, a.dy, a.dy_ld, r, span, col, a.cols, lane, whole);
     }
     copy_commit();
   };
-  auto saved = [&](int64_t r, float (&h)[2]) {   // h before row r, where that is a row of the span
-    load_state<kVec>(r >= span.row && r < span.row_end ? a.states : nullptr, r / kS, col, a.cols, lane, h);
+  auto saved = [&](int64_t r, float (&h)[kC]) {   // h before row r, where that is a row of the span
+    load_state<kC, kVec>(r >= span.row && r < span.row_end ? a.states : nullptr, r / kS, col, a.cols, lane, h);
   };
-  float coming[2];
+  float coming[kC];
   fetch(row, 0);
   saved(row, coming);
   float carry = 0.f;                             // the first kCols threads: behind all rows so far
@@ -570,26 +597,30 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
   for (int turn = 0; turn < turns; ++turn, row -= step) {
     copy_wait<0>();
     __syncwarp();
-    float h[2] = {coming[0], coming[1]};
+    float h[kC];
+#pragma unroll
+    for (int k = 0; k < kC; ++k) h[k] = coming[k];
     fetch(row - step, turn + 1);                 // over the rows of the turn before, which this warp is done with
     saved(row - step, coming);
     Marks m;
     if constexpr (kRagged) m = marks_ragged<true>(a.starts, a.rows, span, row, next, sh, warp, lane);
     else m = marks_equal<true>(plan, span, row, next, lane);
-    const uint8_t *xs = stage(turn), *gs = xs + kTile<T>, *ys = gs + kTile<T>;
-    float c[kS][2], q[kS][2];                    // q = (1 - c) (x_t - h_{t-1})
-    Piece mine[2] = {{1.f, 0.f}, {1.f, 0.f}};
+    const uint8_t *xs = stage(turn), *gs = xs + kTile<T, kC>, *ys = gs + kTile<T, kC>;
+    float c[kS][kC], q[kS][kC];                    // q = (1 - c) (x_t - h_{t-1})
+    Piece mine[kC];
+#pragma unroll
+    for (int k = 0; k < kC; ++k) mine[k] = Piece{1.f, 0.f};
     auto pieces = [&](auto plain) {              // plain: all rows are there, no sequence starts or ends
 #pragma unroll
       for (int j = 0; j < kS; ++j) {
-        float g[2], x[2];
-        pair_at<T, kVec>(gs, j, lane, g);
-        pair_at<T, kVec>(xs, j, lane, x);
+        float g[kC], x[kC];
+        columns_at<T, kC, kVec>(gs, j, lane, g);
+        columns_at<T, kC, kVec>(xs, j, lane, x);
         const bool in = plain.value || (row + j >= span.row && row + j < span.row_end);
         if (!plain.value && (m.start >> j & 1))
-          load_state<kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, a.cols, lane, h);
+          load_state<kC, kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, a.cols, lane, h);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < kC; ++k) {
           const float e = exp_neg(g[k]), r = reciprocal(1.f + e), d = x[k] - h[k];
           c[j][k] = in ? r : 0.f;
           q[j][k] = (g[k] > 0.f ? e * r : 1.f - r) * d;       // 1 - c, as exact as c where c is near one too
@@ -598,54 +629,58 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
       }
 #pragma unroll
       for (int j = kS - 1; j >= 0; --j) {
-        float dy[2];
-        pair_at<T, kVec>(ys, j, lane, dy);
+        float dy[kC];
+        columns_at<T, kC, kVec>(ys, j, lane, dy);
         const bool in = plain.value || (row + j >= span.row && row + j < span.row_end);
         if (!plain.value && (m.end >> j & 1)) {
-          float dhT[2];
-          load_state<kVec>(a.dhT, __shfl_sync(0xffffffffu, m.end_seq, j), col, a.cols, lane, dhT);
-          mine[0].b = dhT[0];
-          mine[1].b = dhT[1];
+          float dhT[kC];
+          load_state<kC, kVec>(a.dhT, __shfl_sync(0xffffffffu, m.end_seq, j), col, a.cols, lane, dhT);
+#pragma unroll
+          for (int k = 0; k < kC; ++k) mine[k].b = dhT[k];
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < kC; ++k) {
           const float l = dy[k] + mine[k].b;
           mine[k].b = !in ? mine[k].b : !plain.value && (m.start >> j & 1) ? 0.f : fmaf(-c[j][k], l, l);
           mine[k].p = fmaf(-c[j][k], mine[k].p, mine[k].p);
         }
       }
-      if (!plain.value && (m.start | m.end)) mine[0].p = mine[1].p = kReset;
+      if (!plain.value && (m.start | m.end)) {
+#pragma unroll
+        for (int k = 0; k < kC; ++k) mine[k].p = kReset;
+      }
     };
     const bool plain = row >= span.row && row + kS <= span.row_end && (m.start | m.end) == 0;
     if (plain) pieces(Flag<true>{});
     else pieces(Flag<false>{});
-    float b[2];                                  // (1 - c) l of the row behind
-    exchange<kVec, true>(sh, turn, plan.cluster, rank, warp, lane, mine, carry, lost, b);
+    float b[kC];                                  // (1 - c) l of the row behind
+    exchange<kC, kVec, true>(sh, turn, plan.cluster, rank, warp, lane, mine, carry, lost, b);
     T* dx = static_cast<T*>(a.dx) + (row + kS - 1) * a.dx_ld;
     T* dg = static_cast<T*>(a.dgate) + (row + kS - 1) * a.dgate_ld;
     auto outputs = [&](auto plain) {
 #pragma unroll
       for (int j = kS - 1; j >= 0; --j, dx -= a.dx_ld, dg -= a.dgate_ld) {
-        float dy[2], ox[2], og[2];
-        pair_at<T, kVec>(ys, j, lane, dy);
+        float dy[kC], ox[kC], og[kC];
+        columns_at<T, kC, kVec>(ys, j, lane, dy);
         const bool in = plain.value || (row + j >= span.row && row + j < span.row_end);
         if (!plain.value && (m.end >> j & 1))
-          load_state<kVec>(a.dhT, __shfl_sync(0xffffffffu, m.end_seq, j), col, a.cols, lane, b);
+          load_state<kC, kVec>(a.dhT, __shfl_sync(0xffffffffu, m.end_seq, j), col, a.cols, lane, b);
         if (in) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
+          for (int k = 0; k < kC; ++k) {
             const float l = dy[k] + b[k];
             ox[k] = c[j][k] * l;
             og[k] = ox[k] * q[j][k];
             b[k] = fmaf(-c[j][k], l, l);
           }
-          store_pair<T, kVec>(dx, col, a.cols, lane, ox[0], ox[1]);
-          store_pair<T, kVec>(dg, col, a.cols, lane, og[0], og[1]);
+          store_columns<T, kC, kVec>(dx, col, a.cols, lane, ox);
+          store_columns<T, kC, kVec>(dg, col, a.cols, lane, og);
         }
         if (!plain.value && (m.start >> j & 1)) {
           if (a.dh0)
-            store_pair<float, kVec>(a.dh0 + __shfl_sync(0xffffffffu, m.start_seq, j) * a.cols, col, a.cols, lane, b[0], b[1]);
-          b[0] = b[1] = 0.f;
+            store_columns<float, kC, kVec>(a.dh0 + __shfl_sync(0xffffffffu, m.start_seq, j) * a.cols, col, a.cols, lane, b);
+#pragma unroll
+          for (int k = 0; k < kC; ++k) b[k] = 0.f;
         }
       }
     };
@@ -663,14 +698,14 @@ bool rows_on(const void* p, int64_t ld, int es, int64_t rows, uintptr_t bytes) {
 }
 
 // How many CTAs share the rows of a sequence (a cluster) and how many shares the
-// sequences make, so that the CTAs of 64 columns that the SMs hold at once have as
-// few turns as possible.  A share of ragged sequences is taken to be longer than the
-// others by three average sequences.
-Plan make_plan(int64_t rows, int64_t cols, int64_t sequences, bool ragged, int ctas_per_sm) {
-  Plan best{1, 1, static_cast<int>((cols + kCols - 1) / kCols), ragged ? 0 : rows / sequences};
+// sequences make, so that the CTAs that the SMs hold at once have as few turns as
+// possible.  A share of ragged sequences is taken to be longer than the others by
+// three average sequences.
+Plan make_plan(int64_t rows, int64_t cols, int64_t sequences, bool ragged, int cols_per_cta, int ctas_per_sm) {
+  Plan best{1, 1, static_cast<int>((cols + cols_per_cta - 1) / cols_per_cta), ragged ? 0 : rows / sequences};
   const int64_t target = static_cast<int64_t>(ctas_per_sm) * num_sms(), average = (rows + sequences - 1) / sequences;
   double least = 0;
-  for (int cluster = 1; cluster <= kMaxCluster; cluster *= 2) {
+  for (int cluster = 1; cluster <= kMaxCluster; ++cluster) {
     int64_t ranges = target / (static_cast<int64_t>(best.groups) * cluster);
     if (ranges < 1) {
       if (cluster > 1) break;
@@ -700,6 +735,18 @@ cudaError_t launch_plan(Kernel kernel, const Args& a, const Plan& plan, size_t s
   return launch_overlapped(kernel, dim3(static_cast<unsigned>(ctas)), kThreads, smem, stream, plan.cluster, a, plan);
 }
 
+template <typename T, int kC, bool kVec>
+cudaError_t run_forward(const opt_recurrence_args& a, cudaStream_t stream) {
+  const Plan plan = make_plan(a.rows, a.cols, a.sequences, a.starts != nullptr, 32 * kC, kForwardCtas<T, kC>);
+  const size_t smem = Layout<T, kC, 2>::bytes(plan.cluster);
+  return a.starts ? launch_plan(recurrence_kernel<T, kC, kVec, true>, a, plan, smem, stream)
+                  : launch_plan(recurrence_kernel<T, kC, kVec, false>, a, plan, smem, stream);
+}
+
+// Four columns to a lane from here on: half the instructions around a row's
+// arithmetic; narrower ones need the CTAs.
+constexpr int64_t kWideCols = 2048;
+
 template <typename T, bool kVec>
 cudaError_t forward(const opt_recurrence_args& a, cudaStream_t stream) {
   if (!a.starts && a.rows == a.sequences) {
@@ -707,18 +754,18 @@ cudaError_t forward(const opt_recurrence_args& a, cudaStream_t stream) {
     return launch_overlapped(recurrence_step_kernel<T, kVec>, dim3(static_cast<unsigned>(a.rows * slices)), kThreads, 0, stream,
                              0, a, static_cast<uint32_t>(slices));
   }
-  const Plan plan = make_plan(a.rows, a.cols, a.sequences, a.starts != nullptr, kForwardCtas<T>);
-  const size_t smem = Layout<T, 2>::bytes(plan.cluster);
-  return a.starts ? launch_plan(recurrence_kernel<T, kVec, true>, a, plan, smem, stream)
-                  : launch_plan(recurrence_kernel<T, kVec, false>, a, plan, smem, stream);
+  if constexpr (kVec && sizeof(T) == 2) {
+    if (a.cols >= kWideCols) return run_forward<T, 4, kVec>(a, stream);
+  }
+  return run_forward<T, 2, kVec>(a, stream);
 }
 
 template <typename T, bool kVec>
 cudaError_t backward(const opt_recurrence_grad_args& a, cudaStream_t stream) {
-  const Plan plan = make_plan(a.rows, a.cols, a.sequences, a.starts != nullptr, kBackwardCtas<T>);
-  const size_t smem = Layout<T, 3>::bytes(plan.cluster);
-  return a.starts ? launch_plan(recurrence_grad_kernel<T, kVec, true>, a, plan, smem, stream)
-                  : launch_plan(recurrence_grad_kernel<T, kVec, false>, a, plan, smem, stream);
+  const Plan plan = make_plan(a.rows, a.cols, a.sequences, a.starts != nullptr, 64, kBackwardCtas<T>);
+  const size_t smem = Layout<T, 2, 3>::bytes(plan.cluster);
+  return a.starts ? launch_plan(recurrence_grad_kernel<T, 2, kVec, true>, a, plan, smem, stream)
+                  : launch_plan(recurrence_grad_kernel<T, 2, kVec, false>, a, plan, smem, stream);
 }
 
 }  // namespace
@@ -727,7 +774,7 @@ cudaError_t launch_recurrence(const opt_recurrence_args& a, cudaStream_t stream)
   const int es = a.dtype == kBf16 ? 2 : 4;
   const bool vec = a.cols % 8 == 0 && rows_on(a.x, a.x_ld, es, a.rows, 16) && rows_on(a.gate, a.gate_ld, es, a.rows, 16) &&
                    rows_on(a.y, a.y_ld, es, a.rows, 16) && rows_on(a.h0, a.cols, 4, 1, 16) &&
-                   rows_on(a.hT, a.cols, 4, 1, 16) && rows_on(a.states, a.cols, 4, 1, 8);
+                   rows_on(a.hT, a.cols, 4, 1, 16) && rows_on(a.states, a.cols, 4, 1, 16);
   if (a.dtype == kBf16) return vec ? forward<__nv_bfloat16, true>(a, stream) : forward<__nv_bfloat16, false>(a, stream);
   return vec ? forward<float, true>(a, stream) : forward<float, false>(a, stream);
 }
