@@ -21,6 +21,8 @@
 // dy), the outputs written once; a state for every 8 rows in fp32 is all that the
 // gradient needs of the forward pass.
 
+#include <climits>
+
 #include "cluster.cuh"
 #include "elements.cuh"
 #include "internal.h"
@@ -75,12 +77,12 @@ constexpr int kBackwardCtas = sizeof(T) == 2 ? 3 : 2;
 
 struct Plan {
   int cluster, ranges, groups;      // CTAs to a cluster; shares of the sequences; shares of the columns
-  int64_t length;                   // rows of a sequence without starts
+  int length;                       // rows of a sequence without starts
 };
 
-// The sequences and rows of a cluster.
+// The sequences and rows of a cluster; both are at most 2^30.
 struct Span {
-  int64_t seq, seq_end, row, row_end;
+  int seq, seq_end, row, row_end;
 };
 
 struct Shared {
@@ -116,45 +118,47 @@ struct Layout {
 
 // -------------------------------------------------------------- sequences --
 
-__device__ __forceinline__ int64_t start_at(const int32_t* starts, int64_t i, int64_t rows) {
-  const int64_t v = starts[i];
+__device__ __forceinline__ int start_at(const int32_t* starts, int i, int rows) {
+  const int v = starts[i];
   return v < 0 ? 0 : v > rows ? rows : v;
 }
 
 // First index in [0, n] whose start is not below v (n: none), by one warp: 32 probes a step.
-__device__ __forceinline__ int64_t lower_bound(const int32_t* starts, int64_t n, int64_t v, int lane) {
-  int64_t lo = 0, hi = n;                        // starts before lo are below v, those from hi on are not
+__device__ __forceinline__ int lower_bound(const int32_t* starts, int n, int v, int lane) {
+  int lo = 0, hi = n;                            // starts before lo are below v, those from hi on are not
   while (hi > lo) {
-    const int64_t step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const int step = (hi - lo + 31) / 32;
+    const int64_t at = lo + static_cast<int64_t>(lane) * step;
     const int k = __popc(__ballot_sync(0xffffffffu, at < hi && starts[at] < v));
     if (k == 0) return lo;
-    const int64_t next_hi = lo + k * step;
+    const int64_t next_hi = lo + static_cast<int64_t>(k) * step;
     lo += (k - 1) * step + 1;
-    hi = next_hi < hi ? next_hi : hi;
+    hi = next_hi < hi ? static_cast<int>(next_hi) : hi;
   }
   return lo;
 }
+
+__device__ __forceinline__ int share(int64_t n, int part, int parts) { return static_cast<int>(n * part / parts); }
 
 // The share of the sequences that this cluster has.  With starts, rank 0 reads
 // them and tells the others: the CTAs of a cluster loop over the same rows
 // whatever becomes of the array meanwhile.
 template <bool kRagged>
-__device__ __forceinline__ Span span_of(const Plan& plan, const int32_t* starts, int64_t rows, int64_t sequences,
-                                        int range, uint32_t rank, const Shared& sh) {
+__device__ __forceinline__ Span span_of(const Plan& plan, const int32_t* starts, int rows, int sequences, int range,
+                                        uint32_t rank, const Shared& sh) {
   if constexpr (!kRagged) {
-    const int64_t s0 = sequences * range / plan.ranges, s1 = sequences * (range + 1) / plan.ranges;
+    const int s0 = share(sequences, range, plan.ranges), s1 = share(sequences, range + 1, plan.ranges);
     return Span{s0, s1, s0 * plan.length, s1 * plan.length};
   } else {
     const int lane = threadIdx.x & 31;
     if (rank == 0 && threadIdx.x < 32) {
-      const int64_t s0 = range == 0 ? 0 : lower_bound(starts, sequences, rows * range / plan.ranges, lane);
-      const int64_t s1 = range + 1 == plan.ranges ? sequences
-                                                  : lower_bound(starts, sequences, rows * (range + 1) / plan.ranges, lane);
-      const int64_t r0 = start_at(starts, s0, rows), r1 = start_at(starts, s1, rows);
+      const int s0 = range == 0 ? 0 : lower_bound(starts, sequences, share(rows, range, plan.ranges), lane);
+      const int s1 = range + 1 == plan.ranges ? sequences : lower_bound(starts, sequences, share(rows, range + 1, plan.ranges), lane);
+      const int r0 = start_at(starts, s0, rows), r1 = start_at(starts, s1, rows);
       for (int i = lane; i < plan.cluster * 4; i += 32) {
-        const int64_t v = i % 4 == 0 ? s0 : i % 4 == 1 ? s1 : i % 4 == 2 ? r0 : r1;
-        if (plan.cluster > 1) store_peer(at_peer(reinterpret_cast<int64_t*>(sh.span) + i % 4, i / 4), v);
-        else reinterpret_cast<int64_t*>(sh.span)[i] = v;
+        const int v = i % 4 == 0 ? s0 : i % 4 == 1 ? s1 : i % 4 == 2 ? r0 : r1;
+        if (plan.cluster > 1) store_peer(at_peer(reinterpret_cast<int*>(sh.span) + i % 4, i / 4), static_cast<uint32_t>(v));
+        else reinterpret_cast<int*>(sh.span)[i] = v;
       }
     }
     if (plan.cluster > 1) cluster_sync();
@@ -170,61 +174,70 @@ struct Marks {
   int start_seq, end_seq;
 };
 
-// Sequences of one length.  `near` is the first sequence's start from these rows on
-// (kBack: the last one up to the row behind them), kept from call to call: the
-// division is needed only when it has been passed.
+// How far a warp's rows have come along the starts: `near` is the first start from
+// its rows on (kBack: the last one before the rows it has looked at), so that
+// most groups of rows are known to have no mark by one comparison; `next`, with
+// starts, the first sequence that does not start before the rows.
+struct Cursor {
+  int near, next;
+};
 template <bool kBack>
-__device__ __forceinline__ Marks marks_equal(const Plan& plan, const Span& span, int64_t row, int64_t& near, int lane) {
+__device__ __forceinline__ Cursor first_cursor(const Span& span) {
+  return kBack ? Cursor{span.row_end, span.seq_end + 1} : Cursor{span.row, span.seq};
+}
+
+// Sequences of one length.
+template <bool kBack>
+__device__ __forceinline__ Marks marks_equal(const Plan& plan, const Span& span, int row, Cursor& at, int lane) {
   Marks m{0, 0, 0, 0};
-  if (kBack ? near > row + kS : near < row) {
+  if (row >= span.row_end) return m;
+  if (kBack ? at.near > row + kS : at.near < row) {
     const uint32_t len = static_cast<uint32_t>(plan.length);
-    near = static_cast<int64_t>((static_cast<uint32_t>(kBack ? row + kS : row + len - 1)) / len) * len;
+    at.near = static_cast<int>(static_cast<uint32_t>(kBack ? row + kS : row + plan.length - 1) / len * len);
   }
-  if (kBack ? near < row : near > row + kS) return m;
-  const int64_t r = row + lane;
+  if (kBack ? at.near < row : at.near > row + kS) return m;
+  const int r = row + lane;
   const bool in = lane < kS && r >= span.row && r < span.row_end;
-  m.start_seq = m.end_seq = in ? static_cast<int>(static_cast<uint32_t>(r) / static_cast<uint32_t>(plan.length)) : 0;
-  m.start = __ballot_sync(0xffffffffu, in && r == m.start_seq * plan.length);
-  m.end = __ballot_sync(0xffffffffu, in && r + 1 == (m.start_seq + 1) * plan.length);
+  const int seq = in ? r / plan.length : 0, rest = r - seq * plan.length;
+  m.start_seq = m.end_seq = seq;
+  m.start = __ballot_sync(0xffffffffu, in && rest == 0);
+  m.end = __ballot_sync(0xffffffffu, in && rest == plan.length - 1);
   return m;
 }
 
-// With starts, for a warp's rows [row, row + kS).  `next` follows the rows: it is
-// moved to the first sequence of the span (its end counting as one) that does
-// not start before them, up or (kBack) down.  Most groups of rows have no mark:
-// one load and two ballots then.
+// With starts; the span's end counts as one.
 template <bool kBack>
-__device__ __forceinline__ Marks marks_ragged(const int32_t* starts, int64_t rows, const Span& span, int64_t row,
-                                              int64_t& next, const Shared& sh, int warp, int lane) {
-  const int64_t r0 = row > span.row ? row : span.row, r1 = row + kS < span.row_end ? row + kS : span.row_end;
+__device__ __forceinline__ Marks marks_ragged(const int32_t* starts, int rows, const Span& span, int row, Cursor& at,
+                                              const Shared& sh, int warp, int lane) {
+  const int r0 = row > span.row ? row : span.row, r1 = row + kS < span.row_end ? row + kS : span.row_end;
   Marks m{0, 0, -1, -1};
-  if (r0 >= r1) return m;
+  if (r0 >= r1 || (kBack ? at.near < row : at.near > row + kS)) return m;
   for (int n = 32; n == 32;) {
-    const int64_t i = kBack ? next - 1 - lane : next + lane;
+    const int i = kBack ? at.next - 1 - lane : at.next + lane;
     const bool there = i >= span.seq && i <= span.seq_end;
-    const int64_t v = there ? start_at(starts, i, rows) : 0;
+    const int v = there ? start_at(starts, i, rows) : 0;
     n = __popc(__ballot_sync(0xffffffffu, there && (kBack ? v >= r0 : v < r0)));
-    next += kBack ? -n : n;
+    at.next += kBack ? -n : n;
   }
+  if (kBack) at.near = at.next > span.seq ? start_at(starts, at.next - 1, rows) : -1;
+  else at.near = at.next <= span.seq_end ? start_at(starts, at.next, rows) : INT_MAX;
   int *first = sh.first + warp * kS, *last = sh.last + warp * kS;
   uint32_t start = 0, end = 0;
-  for (int64_t base = next;; base += 32) {
+  for (int64_t base = at.next;; base += 32) {
     const int64_t i = base + lane;
-    const bool here = i <= span.seq_end && start_at(starts, i, rows) <= r1;
-    const uint32_t any = __ballot_sync(0xffffffffu, here);
-    if (any == 0) break;
-    if (here) {
-      const int64_t v = start_at(starts, i, rows);
-      if (i < span.seq_end && v >= r0 && v < r1 && start_at(starts, i + 1, rows) > v) {
+    const int v = i <= span.seq_end ? start_at(starts, static_cast<int>(i), rows) : INT_MAX;
+    const uint32_t here = __ballot_sync(0xffffffffu, v <= r1);
+    if (here >> lane & 1) {
+      if (i < span.seq_end && v >= r0 && v < r1 && start_at(starts, static_cast<int>(i + 1), rows) > v) {
         first[v - row] = static_cast<int>(i);
         start |= 1u << (v - row);
       }
-      if (i > span.seq && v > r0 && start_at(starts, i - 1, rows) < v) {
+      if (i > span.seq && v > r0 && start_at(starts, static_cast<int>(i - 1), rows) < v) {
         last[v - 1 - row] = static_cast<int>(i - 1);
         end |= 1u << (v - 1 - row);
       }
     }
-    if (any != 0xffffffffu) break;
+    if (here != 0xffffffffu) break;
   }
   m.start = __reduce_or_sync(0xffffffffu, start);
   m.end = __reduce_or_sync(0xffffffffu, end);
@@ -240,11 +253,11 @@ __device__ __forceinline__ Marks marks_ragged(const int32_t* starts, int64_t row
 // out[s] <- in[s] (zeros without in) for the span's sequences that have no row.
 template <int kCols>
 __device__ __forceinline__ void pass_empty(const int32_t* starts, const Span& span, float* out, const float* in,
-                                           int64_t col, int64_t cols) {
+                                           int col, int cols) {
   if (!out) return;
-  for (int64_t s = span.seq + threadIdx.x; s < span.seq_end; s += kThreads)
+  for (int s = span.seq + static_cast<int>(threadIdx.x); s < span.seq_end; s += kThreads)
     if (starts[s + 1] <= starts[s])
-      for (int64_t c = col; c < col + kCols && c < cols; ++c) out[s * cols + c] = in ? in[s * cols + c] : 0.f;
+      for (int64_t c = static_cast<int64_t>(s) * cols + col, n = min(kCols, cols - col); n > 0; ++c, --n) out[c] = in ? in[c] : 0.f;
 }
 
 // --------------------------------------------------------------- elements --
@@ -252,14 +265,14 @@ __device__ __forceinline__ void pass_empty(const int32_t* starts, const Span& sp
 // Copies a warp's rows of one tensor to its place in shared memory, [kS][kCols], zeros
 // where there is no row or column.  `whole`: they are all there.
 template <typename T, int kC, bool kVec>
-__device__ __forceinline__ void fetch_rows(uint8_t* dst, const void* src, int64_t ld, int64_t row, const Span& span,
-                                           int64_t col, int64_t cols, int lane, bool whole) {
+__device__ __forceinline__ void fetch_rows(uint8_t* dst, const void* src, int64_t ld, int row, const Span& span,
+                                           int col, int cols, int lane, bool whole) {
   constexpr int kCols = 32 * kC;
   const T* p = static_cast<const T*>(src);
   if constexpr (kVec) {
     constexpr int kPer = 16 / sizeof(T), kPieces = kCols / kPer, kStep = 32 / kPieces;   // 16-byte pieces of a row, rows a step
     static_assert(kPieces <= 32, "a step takes whole rows");
-    const int64_t r0 = row + lane / kPieces, c = col + lane % kPieces * kPer;
+    const int r0 = row + lane / kPieces, c = col + lane % kPieces * kPer;
     const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst)) + lane * 16;
     if (whole) {
       const T* q = p + r0 * ld + c;
@@ -269,7 +282,7 @@ __device__ __forceinline__ void fetch_rows(uint8_t* dst, const void* src, int64_
     } else {
 #pragma unroll
       for (int i = 0; i < kS / kStep; ++i) {
-        const int64_t r = r0 + i * kStep;
+        const int r = r0 + i * kStep;
         const bool in = r >= span.row && r < span.row_end && c < cols;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * 512), "l"(p + (in ? r * ld + c : 0)),
                      "r"(in ? 16 : 0)
@@ -280,11 +293,11 @@ __device__ __forceinline__ void fetch_rows(uint8_t* dst, const void* src, int64_
     T* to = reinterpret_cast<T*>(dst);
 #pragma unroll
     for (int k = 0; k < kC; ++k) {
-      const int64_t c = col + k * 32 + lane;
+      const int c = col + k * 32 + lane;
 #pragma unroll
       for (int j = 0; j < kS; ++j) {
         const bool in = whole || (row + j >= span.row && row + j < span.row_end && c < cols);
-        store_elem(to + j * kCols + k * 32 + lane, in ? load_elem(p + (row + j) * ld + c) : 0.f);
+        store_elem(to + j * kCols + k * 32 + lane, in ? load_elem(p + static_cast<int64_t>(row + j) * ld + c) : 0.f);
       }
     }
   }
@@ -323,9 +336,9 @@ __device__ __forceinline__ int column(int lane, int k) {
 
 // Stores a lane's columns; with kVec the number of columns is a multiple of 8.
 template <typename T, int kC, bool kVec>
-__device__ __forceinline__ void store_columns(T* row, int64_t col, int64_t cols, int lane, const float (&v)[kC]) {
+__device__ __forceinline__ void store_columns(T* row, int col, int cols, int lane, const float (&v)[kC]) {
   if constexpr (kVec) {
-    const int64_t c = col + kC * lane;
+    const int c = col + kC * lane;
     if (c >= cols) return;
     if constexpr (sizeof(T) == 2) {
       if constexpr (kC == 2) *reinterpret_cast<uint32_t*>(row + c) = pack2(v[0], v[1]);
@@ -342,12 +355,13 @@ __device__ __forceinline__ void store_columns(T* row, int64_t col, int64_t cols,
 }
 
 template <int kC, bool kVec>
-__device__ __forceinline__ void load_state(const float* states, int64_t seq, int64_t col, int64_t cols, int lane,
+__device__ __forceinline__ void load_state(const float* states, int seq, int col, int cols, int lane,
                                            float (&v)[kC]) {
+  const float* from = states + static_cast<int64_t>(seq) * cols;
 #pragma unroll
   for (int k = 0; k < kC; ++k) {
-    const int64_t c = col + column<kC, kVec>(lane, k);
-    v[k] = states && c < cols ? states[seq * cols + c] : 0.f;
+    const int c = col + column<kC, kVec>(lane, k);
+    v[k] = states && c < cols ? from[c] : 0.f;
   }
 }
 
@@ -425,22 +439,23 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t rank = plan.cluster > 1 ? cluster_rank() : 0;
   const int id = blockIdx.x / plan.cluster;
-  const int64_t col = static_cast<int64_t>(id % plan.groups) * kCols;
+  const int rows = static_cast<int>(a.rows), cols = static_cast<int>(a.cols), col = id % plan.groups * kCols;
   if (plan.cluster > 1) {                        // every CTA of the cluster has begun
     if (threadIdx.x == 0) sh.mail.init();
     cluster_sync();
   }
-  const Span span = span_of<kRagged>(plan, a.starts, a.rows, a.sequences, id / plan.groups, rank, sh);
-  if (kRagged && rank == 0) pass_empty<kCols>(a.starts, span, a.hT, a.h0, col, a.cols);
-  const int64_t base = span.row / kS * kS, step = static_cast<int64_t>(plan.cluster) * kChunk;
-  const int64_t turns = span.row_end > span.row ? (span.row_end - base + step - 1) / step : 0;
-  int64_t next = kRagged ? span.seq : span.row, row = base + (static_cast<int64_t>(rank) * kWarps + warp) * kS;
+  const Span span = span_of<kRagged>(plan, a.starts, rows, static_cast<int>(a.sequences), id / plan.groups, rank, sh);
+  if (kRagged && rank == 0) pass_empty<kCols>(a.starts, span, a.hT, a.h0, col, cols);
+  const int base = span.row / kS * kS, step = plan.cluster * kChunk;
+  const int turns = span.row_end > span.row ? (span.row_end - base + step - 1) / step : 0;
+  int row = base + (static_cast<int>(rank) * kWarps + warp) * kS;
+  Cursor at = first_cursor<false>(span);
   auto stage = [&](int turn) { return smem + (turn & 1) * L::kStage + warp * 2 * kTile<T, kC>; };
-  auto fetch = [&](int64_t r, int turn) {
+  auto fetch = [&](int r, int turn) {
     if (r < span.row_end) {
-      const bool whole = r >= span.row && r + kS <= span.row_end && col + kCols <= a.cols;
-      fetch_rows<T, kC, kVec>(stage(turn), a.x, a.x_ld, r, span, col, a.cols, lane, whole);
-      fetch_rows<T, kC, kVec>(stage(turn) + kTile<T, kC>, a.gate, a.gate_ld, r, span, col, a.cols, lane, whole);
+      const bool whole = r >= span.row && r + kS <= span.row_end && col + kCols <= cols;
+      fetch_rows<T, kC, kVec>(stage(turn), a.x, a.x_ld, r, span, col, cols, lane, whole);
+      fetch_rows<T, kC, kVec>(stage(turn) + kTile<T, kC>, a.gate, a.gate_ld, r, span, col, cols, lane, whole);
     }
     copy_commit();
   };
@@ -452,8 +467,8 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
     __syncwarp();
     fetch(row + step, turn + 1);                 // over the rows of the turn before, which this warp is done with
     Marks m;
-    if constexpr (kRagged) m = marks_ragged<false>(a.starts, a.rows, span, row, next, sh, warp, lane);
-    else m = marks_equal<false>(plan, span, row, next, lane);
+    if constexpr (kRagged) m = marks_ragged<false>(a.starts, rows, span, row, at, sh, warp, lane);
+    else m = marks_equal<false>(plan, span, row, at, lane);
     const uint8_t *xs = stage(turn), *gs = xs + kTile<T, kC>;
     float c[kS][kC];
     Piece mine[kC];
@@ -468,7 +483,7 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
         const bool in = plain.value || (row + j >= span.row && row + j < span.row_end);
         if (!plain.value && (m.start >> j & 1)) {
           float h0[kC];
-          load_state<kC, kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, a.cols, lane, h0);
+          load_state<kC, kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, cols, lane, h0);
 #pragma unroll
           for (int k = 0; k < kC; ++k) mine[k].b = h0[k];
         }
@@ -491,8 +506,8 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
     float h[kC];
     exchange<kC, kVec, false>(sh, turn, plan.cluster, rank, warp, lane, mine, carry, lost, h);
     if (a.states && row >= span.row && row < span.row_end)
-      store_columns<float, kC, kVec>(a.states + row / kS * a.cols, col, a.cols, lane, h);
-    T* y = static_cast<T*>(a.y) + row * a.y_ld;
+      store_columns<float, kC, kVec>(a.states + static_cast<int64_t>(row / kS) * cols, col, cols, lane, h);
+    T* y = static_cast<T*>(a.y) + static_cast<int64_t>(row) * a.y_ld;
     auto outputs = [&](auto plain) {
 #pragma unroll
       for (int j = 0; j < kS; ++j, y += a.y_ld) {
@@ -500,14 +515,14 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
         columns_at<T, kC, kVec>(xs, j, lane, x);
         const bool in = plain.value || (row + j >= span.row && row + j < span.row_end);
         if (!plain.value && (m.start >> j & 1))
-          load_state<kC, kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, a.cols, lane, h);
+          load_state<kC, kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, cols, lane, h);
         if (in) {
 #pragma unroll
           for (int k = 0; k < kC; ++k) h[k] = fmaf(c[j][k], x[k] - h[k], h[k]);
-          store_columns<T, kC, kVec>(y, col, a.cols, lane, h);
+          store_columns<T, kC, kVec>(y, col, cols, lane, h);
         }
         if (!plain.value && (m.end >> j & 1) && a.hT)
-          store_columns<float, kC, kVec>(a.hT + __shfl_sync(0xffffffffu, m.end_seq, j) * a.cols, col, a.cols, lane, h);
+          store_columns<float, kC, kVec>(a.hT + static_cast<int64_t>(__shfl_sync(0xffffffffu, m.end_seq, j)) * cols, col, cols, lane, h);
       }
     };
     if (plain) outputs(Flag<true>{});
@@ -566,28 +581,29 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t rank = plan.cluster > 1 ? cluster_rank() : 0;
   const int id = blockIdx.x / plan.cluster;
-  const int64_t col = static_cast<int64_t>(id % plan.groups) * kCols;
+  const int rows = static_cast<int>(a.rows), cols = static_cast<int>(a.cols), col = id % plan.groups * kCols;
   if (plan.cluster > 1) {                        // every CTA of the cluster has begun
     if (threadIdx.x == 0) sh.mail.init();
     cluster_sync();
   }
-  const Span span = span_of<kRagged>(plan, a.starts, a.rows, a.sequences, id / plan.groups, rank, sh);
-  if (kRagged && rank == 0) pass_empty<kCols>(a.starts, span, a.dh0, a.dhT, col, a.cols);
-  const int64_t base = span.row / kS * kS, step = static_cast<int64_t>(plan.cluster) * kChunk;
-  const int64_t turns = span.row_end > span.row ? (span.row_end - base + step - 1) / step : 0;
-  int64_t next = kRagged ? span.seq_end + 1 : span.row_end, row = base + (turns - 1) * step + (static_cast<int64_t>(rank) * kWarps + warp) * kS;
+  const Span span = span_of<kRagged>(plan, a.starts, rows, static_cast<int>(a.sequences), id / plan.groups, rank, sh);
+  if (kRagged && rank == 0) pass_empty<kCols>(a.starts, span, a.dh0, a.dhT, col, cols);
+  const int base = span.row / kS * kS, step = plan.cluster * kChunk;
+  const int turns = span.row_end > span.row ? (span.row_end - base + step - 1) / step : 0;
+  int row = base + (turns - 1) * step + (static_cast<int>(rank) * kWarps + warp) * kS;
+  Cursor at = first_cursor<true>(span);
   auto stage = [&](int turn) { return smem + (turn & 1) * L::kStage + warp * 3 * kTile<T, kC>; };
-  auto fetch = [&](int64_t r, int turn) {
+  auto fetch = [&](int r, int turn) {
     if (r >= base && r < span.row_end) {
-      const bool whole = r >= span.row && r + kS <= span.row_end && col + kCols <= a.cols;
-      fetch_rows<T, kC, kVec>(stage(turn), a.x, a.x_ld, r, span, col, a.cols, lane, whole);
-      fetch_rows<T, kC, kVec>(stage(turn) + kTile<T, kC>, a.gate, a.gate_ld, r, span, col, a.cols, lane, whole);
-      fetch_rows<T, kC, kVec>(stage(turn) + 2 * kTile<T, kC>, a.dy, a.dy_ld, r, span, col, a.cols, lane, whole);
+      const bool whole = r >= span.row && r + kS <= span.row_end && col + kCols <= cols;
+      fetch_rows<T, kC, kVec>(stage(turn), a.x, a.x_ld, r, span, col, cols, lane, whole);
+      fetch_rows<T, kC, kVec>(stage(turn) + kTile<T, kC>, a.gate, a.gate_ld, r, span, col, cols, lane, whole);
+      fetch_rows<T, kC, kVec>(stage(turn) + 2 * kTile<T, kC>, a.dy, a.dy_ld, r, span, col, cols, lane, whole);
     }
     copy_commit();
   };
-  auto saved = [&](int64_t r, float (&h)[kC]) {   // h before row r, where that is a row of the span
-    load_state<kC, kVec>(r >= span.row && r < span.row_end ? a.states : nullptr, r / kS, col, a.cols, lane, h);
+  auto saved = [&](int r, float (&h)[kC]) {   // h before row r, where that is a row of the span
+    load_state<kC, kVec>(r >= span.row && r < span.row_end ? a.states : nullptr, r / kS, col, cols, lane, h);
   };
   float coming[kC];
   fetch(row, 0);
@@ -603,8 +619,8 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
     fetch(row - step, turn + 1);                 // over the rows of the turn before, which this warp is done with
     saved(row - step, coming);
     Marks m;
-    if constexpr (kRagged) m = marks_ragged<true>(a.starts, a.rows, span, row, next, sh, warp, lane);
-    else m = marks_equal<true>(plan, span, row, next, lane);
+    if constexpr (kRagged) m = marks_ragged<true>(a.starts, rows, span, row, at, sh, warp, lane);
+    else m = marks_equal<true>(plan, span, row, at, lane);
     const uint8_t *xs = stage(turn), *gs = xs + kTile<T, kC>, *ys = gs + kTile<T, kC>;
     float c[kS][kC], q[kS][kC];                    // q = (1 - c) (x_t - h_{t-1})
     Piece mine[kC];
@@ -618,7 +634,7 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
         columns_at<T, kC, kVec>(xs, j, lane, x);
         const bool in = plain.value || (row + j >= span.row && row + j < span.row_end);
         if (!plain.value && (m.start >> j & 1))
-          load_state<kC, kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, a.cols, lane, h);
+          load_state<kC, kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, cols, lane, h);
 #pragma unroll
         for (int k = 0; k < kC; ++k) {
           const float e = exp_neg(g[k]), r = reciprocal(1.f + e), d = x[k] - h[k];
@@ -634,7 +650,7 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
         const bool in = plain.value || (row + j >= span.row && row + j < span.row_end);
         if (!plain.value && (m.end >> j & 1)) {
           float dhT[kC];
-          load_state<kC, kVec>(a.dhT, __shfl_sync(0xffffffffu, m.end_seq, j), col, a.cols, lane, dhT);
+          load_state<kC, kVec>(a.dhT, __shfl_sync(0xffffffffu, m.end_seq, j), col, cols, lane, dhT);
 #pragma unroll
           for (int k = 0; k < kC; ++k) mine[k].b = dhT[k];
         }
@@ -655,8 +671,8 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
     else pieces(Flag<false>{});
     float b[kC];                                  // (1 - c) l of the row behind
     exchange<kC, kVec, true>(sh, turn, plan.cluster, rank, warp, lane, mine, carry, lost, b);
-    T* dx = static_cast<T*>(a.dx) + (row + kS - 1) * a.dx_ld;
-    T* dg = static_cast<T*>(a.dgate) + (row + kS - 1) * a.dgate_ld;
+    T* dx = static_cast<T*>(a.dx) + static_cast<int64_t>(row + kS - 1) * a.dx_ld;
+    T* dg = static_cast<T*>(a.dgate) + static_cast<int64_t>(row + kS - 1) * a.dgate_ld;
     auto outputs = [&](auto plain) {
 #pragma unroll
       for (int j = kS - 1; j >= 0; --j, dx -= a.dx_ld, dg -= a.dgate_ld) {
@@ -664,7 +680,7 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
         columns_at<T, kC, kVec>(ys, j, lane, dy);
         const bool in = plain.value || (row + j >= span.row && row + j < span.row_end);
         if (!plain.value && (m.end >> j & 1))
-          load_state<kC, kVec>(a.dhT, __shfl_sync(0xffffffffu, m.end_seq, j), col, a.cols, lane, b);
+          load_state<kC, kVec>(a.dhT, __shfl_sync(0xffffffffu, m.end_seq, j), col, cols, lane, b);
         if (in) {
 #pragma unroll
           for (int k = 0; k < kC; ++k) {
@@ -673,12 +689,12 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
             og[k] = ox[k] * q[j][k];
             b[k] = fmaf(-c[j][k], l, l);
           }
-          store_columns<T, kC, kVec>(dx, col, a.cols, lane, ox);
-          store_columns<T, kC, kVec>(dg, col, a.cols, lane, og);
+          store_columns<T, kC, kVec>(dx, col, cols, lane, ox);
+          store_columns<T, kC, kVec>(dg, col, cols, lane, og);
         }
         if (!plain.value && (m.start >> j & 1)) {
           if (a.dh0)
-            store_columns<float, kC, kVec>(a.dh0 + __shfl_sync(0xffffffffu, m.start_seq, j) * a.cols, col, a.cols, lane, b);
+            store_columns<float, kC, kVec>(a.dh0 + static_cast<int64_t>(__shfl_sync(0xffffffffu, m.start_seq, j)) * cols, col, cols, lane, b);
 #pragma unroll
           for (int k = 0; k < kC; ++k) b[k] = 0.f;
         }
@@ -697,50 +713,83 @@ bool rows_on(const void* p, int64_t ld, int es, int64_t rows, uintptr_t bytes) {
   return !p || (reinterpret_cast<uintptr_t>(p) % bytes == 0 && (rows <= 1 || static_cast<uintptr_t>(ld) * es % bytes == 0));
 }
 
+// CTAs of a kernel that the GPU holds at once in clusters of a size (asked once for
+// each device; the kernels differ in registers and shared memory).
+template <auto kKernel>
+cudaError_t ctas_at_once(int cluster, size_t smem, int* ctas) {
+  static thread_local int known_device = -1, known[kMaxCluster + 1];
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  if (device != known_device) {
+    for (int& k : known) k = 0;
+    known_device = device;
+  }
+  if (known[cluster] == 0) {
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, kKernel, &cfg);
+    if (e != cudaSuccess) return e;
+    known[cluster] = n > 0 ? n * cluster : 1;
+  }
+  *ctas = known[cluster];
+  return cudaSuccess;
+}
+
 // How many CTAs share the rows of a sequence (a cluster) and how many shares the
 // sequences make, so that the CTAs that the SMs hold at once have as few turns as
 // possible.  A share of ragged sequences is taken to be longer than the others by
 // three average sequences.
-Plan make_plan(int64_t rows, int64_t cols, int64_t sequences, bool ragged, int cols_per_cta, int ctas_per_sm) {
-  Plan best{1, 1, static_cast<int>((cols + cols_per_cta - 1) / cols_per_cta), ragged ? 0 : rows / sequences};
-  const int64_t target = static_cast<int64_t>(ctas_per_sm) * num_sms(), average = (rows + sequences - 1) / sequences;
+template <auto kKernel, typename L, typename Args>
+cudaError_t launch_rows(const Args& a, cudaStream_t stream) {
+  const int64_t average = (a.rows + a.sequences - 1) / a.sequences;
+  const bool ragged = a.starts != nullptr;
+  Plan plan{1, 1, static_cast<int>((a.cols + L::kCols - 1) / L::kCols), ragged ? 0 : static_cast<int>(average)};
+  const int groups = plan.groups;
   double least = 0;
   for (int cluster = 1; cluster <= kMaxCluster; ++cluster) {
-    int64_t ranges = target / (static_cast<int64_t>(best.groups) * cluster);
+    int held = 0;
+    const cudaError_t e = ctas_at_once<kKernel>(cluster, L::bytes(kMaxCluster), &held);
+    if (e != cudaSuccess) return e;
+    int64_t ranges = held / (static_cast<int64_t>(groups) * cluster);
     if (ranges < 1) {
       if (cluster > 1) break;
       ranges = 1;
     }
-    if (ranges > sequences) ranges = sequences;
-    const int64_t most = ranges == 1 ? rows
-                         : ragged    ? rows / ranges + 3 * average
-                                     : (sequences + ranges - 1) / ranges * average;
+    if (ranges > a.sequences) ranges = a.sequences;
+    const int64_t most = ranges == 1 ? a.rows
+                         : ragged    ? a.rows / ranges + 3 * average
+                                     : (a.sequences + ranges - 1) / ranges * average;
     const int64_t turns = (most + cluster * kChunk - 1) / (cluster * kChunk);
-    const int64_t waves = (ranges * best.groups * cluster + target - 1) / target;
+    const int64_t waves = (ranges * groups * cluster + held - 1) / held;
     const double cost = static_cast<double>(turns * waves) * (cluster > 1 ? 1.25 : 1.0);
     if (cluster == 1 || cost < least) {
       least = cost;
-      best.cluster = cluster;
-      best.ranges = static_cast<int>(ranges);
+      plan.cluster = cluster;
+      plan.ranges = static_cast<int>(ranges);
     }
   }
-  return best;
-}
-
-template <typename Kernel, typename Args>
-cudaError_t launch_plan(Kernel kernel, const Args& a, const Plan& plan, size_t smem, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  const int64_t ctas = static_cast<int64_t>(plan.cluster) * plan.groups * plan.ranges;
-  return launch_overlapped(kernel, dim3(static_cast<unsigned>(ctas)), kThreads, smem, stream, plan.cluster, a, plan);
+  const int64_t ctas = static_cast<int64_t>(plan.cluster) * groups * plan.ranges;
+  return launch_overlapped(kKernel, dim3(static_cast<unsigned>(ctas)), kThreads, L::bytes(plan.cluster), stream, plan.cluster, a,
+                           plan);
 }
 
 template <typename T, int kC, bool kVec>
 cudaError_t run_forward(const opt_recurrence_args& a, cudaStream_t stream) {
-  const Plan plan = make_plan(a.rows, a.cols, a.sequences, a.starts != nullptr, 32 * kC, kForwardCtas<T, kC>);
-  const size_t smem = Layout<T, kC, 2>::bytes(plan.cluster);
-  return a.starts ? launch_plan(recurrence_kernel<T, kC, kVec, true>, a, plan, smem, stream)
-                  : launch_plan(recurrence_kernel<T, kC, kVec, false>, a, plan, smem, stream);
+  using L = Layout<T, kC, 2>;
+  return a.starts ? launch_rows<recurrence_kernel<T, kC, kVec, true>, L>(a, stream)
+                  : launch_rows<recurrence_kernel<T, kC, kVec, false>, L>(a, stream);
 }
 
 // Four columns to a lane from here on: half the instructions around a row's
@@ -762,10 +811,9 @@ cudaError_t forward(const opt_recurrence_args& a, cudaStream_t stream) {
 
 template <typename T, bool kVec>
 cudaError_t backward(const opt_recurrence_grad_args& a, cudaStream_t stream) {
-  const Plan plan = make_plan(a.rows, a.cols, a.sequences, a.starts != nullptr, 64, kBackwardCtas<T>);
-  const size_t smem = Layout<T, 2, 3>::bytes(plan.cluster);
-  return a.starts ? launch_plan(recurrence_grad_kernel<T, 2, kVec, true>, a, plan, smem, stream)
-                  : launch_plan(recurrence_grad_kernel<T, 2, kVec, false>, a, plan, smem, stream);
+  using L = Layout<T, 2, 3>;
+  return a.starts ? launch_rows<recurrence_grad_kernel<T, 2, kVec, true>, L>(a, stream)
+                  : launch_rows<recurrence_grad_kernel<T, 2, kVec, false>, L>(a, stream);
 }
 
 }  // namespace
