@@ -297,7 +297,14 @@ __device__ __forceinline__ void fetch_rows(uint8_t* dst, const void* src, int64_
 #pragma unroll
       for (int j = 0; j < kS; ++j) {
         const bool in = whole || (row + j >= span.row && row + j < span.row_end && c < cols);
-        store_elem(to + j * kCols + k * 32 + lane, in ? load_elem(p + static_cast<int64_t>(row + j) * ld + c) : 0.f);
+        const T* q = p + (in ? static_cast<int64_t>(row + j) * ld + c : 0);
+        T* at = to + j * kCols + k * 32 + lane;
+        if constexpr (sizeof(T) == 4)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(at))),
+                       "l"(q), "r"(in ? 4 : 0)
+                       : "memory");
+        else
+          store_elem(at, in ? load_elem(q) : 0.f);
       }
     }
   }
