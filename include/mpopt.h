@@ -632,7 +632,9 @@ MPOPT_API size_t opt_linear_workspace_size(int64_t m, int64_t n, int64_t k, int3
  * those of the feed-forward operators: row-major matrices with a row distance,
  * sums and states in fp32, one rounding to an output's own type.  Every result
  * has the same bits each time.  Outputs may not overlap inputs or one another
- * but where an argument says so.
+ * but where an argument says so.  CTAs that share a row or a sequence wait for
+ * one another for two seconds at most; a wait that runs out leaves NaN in the
+ * outputs that depend on it.
  */
 
 /* Integer type of token and label arrays. */

@@ -34,9 +34,6 @@ __device__ __forceinline__ uint32_t at_peer(const void* p, uint32_t rank) {
                : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
   return m;
 }
-__device__ __forceinline__ void store_peer(uint32_t at, int64_t v) {
-  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
-}
 __device__ __forceinline__ void store_peer(uint32_t at, uint32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
@@ -64,24 +61,69 @@ struct Mailbox {
                  "f"(v.x), "f"(v.y), "r"(at_peer(bar + (k & 1), rank))
                  : "memory");
   }
-  // Whether message k is there: every try may suspend the thread for a while, and
-  // after kTries of them (a second or more) the wait gives up.
-  static constexpr int kTries = 1 << 20;
+  // Whether message k is there; a wait gives up after two seconds.
   __device__ __forceinline__ bool wait(int k) const {
     const uint32_t at = u32(bar + (k & 1)), parity = static_cast<uint32_t>(k >> 1) & 1u;
-    for (int i = 0; i < kTries; ++i) {
-      uint32_t there;
-      asm volatile(
-          "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-          " selp.u32 %0, 1, 0, p;\n}"
-          : "=r"(there)
-          : "r"(at), "r"(parity)
-          : "memory");
-      if (there) return true;
+    if (there(at, parity)) return true;
+    const unsigned long long t0 = nanoseconds();
+    for (uint32_t i = 1;; ++i) {
+      if (there(at, parity)) return true;
+      if ((i & 63u) == 0 && nanoseconds() - t0 > 2000000000ull) return false;
     }
-    return false;
+  }
+
+ private:
+  static __device__ __forceinline__ bool there(uint32_t at, uint32_t parity) {
+    uint32_t yes;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(yes)
+        : "r"(at), "r"(parity)
+        : "memory");
+    return yes != 0;
+  }
+  static __device__ __forceinline__ unsigned long long nanoseconds() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
   }
 };
+
+// Clusters of a kernel that the GPU holds at once (asked once for each device and
+// size; smem: the most that the kernel is launched with).
+constexpr int kMostClusterCtas = 8;
+template <auto kKernel>
+cudaError_t clusters_at_once(int cluster, int threads, size_t smem, int* clusters) {
+  static thread_local int known_device = -1, known[kMostClusterCtas + 1];
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  if (device != known_device) {
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    for (int& k : known) k = 0;
+    known_device = device;
+  }
+  if (known[cluster] == 0) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, kKernel, &cfg);
+    if (e != cudaSuccess) return e;
+    known[cluster] = n > 0 ? n : 1;
+  }
+  *clusters = known[cluster];
+  return cudaSuccess;
+}
 
 }  // namespace
 }  // namespace mpopt

@@ -152,7 +152,7 @@ cross_entropy_kernel(const __grid_constant__ opt_cross_entropy_args a) {
 // ---------------------------------------------------------------- cluster --
 
 constexpr int kElems = 64;                       // of a thread
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = kMostClusterCtas;
 
 template <typename T, int kThreads>
 struct Config {
@@ -342,43 +342,12 @@ cross_entropy_cluster_kernel(const __grid_constant__ opt_cross_entropy_args a, i
   if (cluster > 1) cluster_sync();               // nobody leaves while mail to it is on its way
 }
 
-// Clusters that the GPU holds at once (asked once for each device).
-template <typename T, int kThreads>
-int clusters_at_once(int cluster, size_t smem, cudaError_t* error) {
-  static thread_local int known_device = -1, known[kMaxCluster + 1];
-  int device = 0;
-  if ((*error = cudaGetDevice(&device)) != cudaSuccess) return 0;
-  if (device != known_device) {
-    for (int& k : known) k = 0;
-    known_device = device;
-  }
-  if (known[cluster] == 0) {
-    *error = cudaFuncSetAttribute(cross_entropy_cluster_kernel<T, kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  static_cast<int>(smem));
-    if (*error != cudaSuccess) return 0;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(cluster));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if ((*error = cudaOccupancyMaxActiveClusters(&n, cross_entropy_cluster_kernel<T, kThreads>, &cfg)) != cudaSuccess) return 0;
-    known[cluster] = n > 0 ? n : 1;
-  }
-  return known[cluster];
-}
-
 template <typename T, int kThreads>
 cudaError_t launch_cluster(const opt_cross_entropy_args& a, int cluster, cudaStream_t stream) {
   using C = Config<T, kThreads>;
   const size_t smem = C::kBytes;
-  cudaError_t e = cudaSuccess;
-  const int64_t most = clusters_at_once<T, kThreads>(cluster, smem, &e);
+  int most = 0;
+  const cudaError_t e = clusters_at_once<cross_entropy_cluster_kernel<T, kThreads>>(cluster, kThreads, smem, &most);
   if (e != cudaSuccess) return e;
   const int64_t clusters = a.rows < most ? a.rows : most;
   return launch_overlapped(cross_entropy_cluster_kernel<T, kThreads>, dim3(static_cast<unsigned>(clusters * cluster)), kThreads,

@@ -33,7 +33,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = kMostClusterCtas;
 constexpr int kS = kRecurrenceStateRows;         // rows of a thread at a time
 constexpr int kChunk = kWarps * kS;              // of a CTA
 constexpr float kReset = -1.f;
@@ -720,40 +720,6 @@ bool rows_on(const void* p, int64_t ld, int es, int64_t rows, uintptr_t bytes) {
   return !p || (reinterpret_cast<uintptr_t>(p) % bytes == 0 && (rows <= 1 || static_cast<uintptr_t>(ld) * es % bytes == 0));
 }
 
-// CTAs of a kernel that the GPU holds at once in clusters of a size (asked once for
-// each device; the kernels differ in registers and shared memory).
-template <auto kKernel>
-cudaError_t ctas_at_once(int cluster, size_t smem, int* ctas) {
-  static thread_local int known_device = -1, known[kMaxCluster + 1];
-  int device = 0;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e != cudaSuccess) return e;
-  if (device != known_device) {
-    for (int& k : known) k = 0;
-    known_device = device;
-  }
-  if (known[cluster] == 0) {
-    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(cluster));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, kKernel, &cfg);
-    if (e != cudaSuccess) return e;
-    known[cluster] = n > 0 ? n * cluster : 1;
-  }
-  *ctas = known[cluster];
-  return cudaSuccess;
-}
-
 // How many CTAs share the rows of a sequence (a cluster) and how many shares the
 // sequences make, so that the CTAs that the SMs hold at once have as few turns as
 // possible.  A share of ragged sequences is taken to be longer than the others by
@@ -767,8 +733,9 @@ cudaError_t launch_rows(const Args& a, cudaStream_t stream) {
   double least = 0;
   for (int cluster = 1; cluster <= kMaxCluster; ++cluster) {
     int held = 0;
-    const cudaError_t e = ctas_at_once<kKernel>(cluster, L::bytes(kMaxCluster), &held);
+    const cudaError_t e = clusters_at_once<kKernel>(cluster, kThreads, L::bytes(kMaxCluster), &held);
     if (e != cudaSuccess) return e;
+    held *= cluster;
     int64_t ranges = held / (static_cast<int64_t>(groups) * cluster);
     if (ranges < 1) {
       if (cluster > 1) break;
