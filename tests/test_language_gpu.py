@@ -167,6 +167,14 @@ def test_embedding_backward_runs(pattern, rows):
     check_embedding_backward(tokens, normal(5, (rows, 40)), max(rows, 6), 1.0, True, pattern)
 
 
+@pytest.mark.parametrize("rows", [8191, 8192, 8193])
+@pytest.mark.parametrize("vocab", [3, 1024, 300000])
+def test_embedding_backward_sorts_few_and_many_rows_alike(rows, vocab):
+    """The two ways to sort, at the number of rows where one takes over."""
+    tokens = torch.randint(-1, vocab + 1, (rows,), generator=gen(6), device="cuda")
+    check_embedding_backward(tokens, normal(5, (rows, 8)), vocab, 1.0, True)
+
+
 def test_embedding_backward_no_rows():
     g = normal(1, (5, 8), FP32)
     old = g.clone()
@@ -292,6 +300,16 @@ def test_recurrence_borders(starts, with_h0):
     for dtype in (BF16, FP32):
         for layout in ("dense", "odd slice"):
             check_recurrence(40, 24, np.array(starts), len(starts) - 1, dtype, layout, with_h0, what=str(starts))
+
+
+@pytest.mark.parametrize("cols", [2040, 2048, 2056, 2176])
+@pytest.mark.parametrize("layout", ["dense", "aligned slice"])
+def test_recurrence_wide(cols, layout):
+    """From 2048 columns on a lane has four of them."""
+    check_recurrence(700, cols, None, 1, BF16, layout)
+    check_recurrence(140, cols, None, 7, BF16, layout)
+    check_recurrence(300, cols, np.array([3, 3, 19, 20, 100, 100, 297]), 6, BF16, layout)
+    check_recurrence(40, cols, np.array([0, 15, 16, 17, 32, 33]), 5, BF16, layout, False)
 
 
 @pytest.mark.parametrize("sequences,rows,cols", [(3000, 9000, 8), (70, 9000, 16), (5, 9000, 640)])
@@ -539,6 +557,24 @@ def test_cross_entropy(rows, cols, dtype, layout):
         dense = output((rows, cols), dtype)
         mp.cross_entropy(x, labels, dlogits=dense, scale=0.37, weight=weight)
         assert torch.equal(dense, g)
+
+
+@pytest.mark.parametrize("cols", [4096, 4097, 8193, 16384, 16385, 16391, 32769, 65543, 131072, 131079])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_cross_entropy_shares(cols, dtype):
+    """Widths where a row's threads or CTAs become more; the label first, last and
+    beside every border; more rows than the GPU holds at once in the narrow ones."""
+    rows = 700 if cols < 20000 else 9
+    x = normal(1, (rows, cols), dtype, 3.0)
+    labels = torch.randint(0, cols, (rows,), generator=gen(2), device="cuda")
+    edges = [0, cols - 1, 1, cols - 2, 7, 8, cols // 2, 4095, cols - 9]
+    labels[:len(edges)] = torch.tensor(edges, device="cuda")
+    check_cross_entropy(x, labels, 0.37)
+    over = x.clone()
+    g = output((rows, cols), dtype)
+    mp.cross_entropy(x, labels, dlogits=g)
+    mp.cross_entropy(over, labels, dlogits=over)
+    assert torch.equal(over, g)
 
 
 @pytest.mark.parametrize("cols", [5, 64, 1500, 40000])
