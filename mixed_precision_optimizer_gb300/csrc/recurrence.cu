@@ -15,7 +15,7 @@
 //
 // A warp has 64 columns, two to a lane (or 128, four), and 8 rows at a time in shared memory,
 // fetched with cp.async while it works on the rows before.  Its CTA's eight
-// pieces, and those of the CTAs of a cluster, which take the next rows each, are
+// (or 16) pieces, and those of the CTAs of a cluster, which take the next rows each, are
 // joined through (distributed) shared memory; then every thread runs through its
 // rows again from the right state.  Bound by HBM: x and gate are read once (and
 // dy), the outputs written once; a state for every 8 rows in fp32 is all that the
@@ -31,11 +31,9 @@
 namespace mpopt {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kStepThreads = 256;
 constexpr int kMaxCluster = kMostClusterCtas;
 constexpr int kS = kRecurrenceStateRows;         // rows of a thread at a time
-constexpr int kChunk = kWarps * kS;              // of a CTA
 constexpr float kReset = -1.f;
 
 // ---------------------------------------------------------------- pieces --
@@ -70,10 +68,10 @@ template <typename T, int kC>
 constexpr int kTile = kS * 32 * kC * static_cast<int>(sizeof(T));   // bytes of a warp's rows of one tensor
 
 // CTAs to an SM, by registers and shared memory.
-template <typename T, int kC>
-constexpr int kForwardCtas = kC == 4 ? 2 : sizeof(T) == 2 ? 4 : 3;
-template <typename T>
-constexpr int kBackwardCtas = sizeof(T) == 2 ? 3 : 2;
+template <typename T, int kC, int kW>
+constexpr int kForwardCtas = kW == 16 ? (sizeof(T) == 2 ? 2 : 1) : kC == 4 ? 2 : sizeof(T) == 2 ? 4 : 3;
+template <typename T, int kW>
+constexpr int kBackwardCtas = kW == 16 ? 1 : sizeof(T) == 2 ? 3 : 2;
 
 struct Plan {
   int cluster, ranges, groups;      // CTAs to a cluster; shares of the sequences; shares of the columns
@@ -95,9 +93,9 @@ struct Shared {
   Mailbox mail;
 };
 
-template <typename T, int kC, int kTensors>
+template <typename T, int kC, int kW, int kTensors>
 struct Layout {
-  static constexpr int kCols = 32 * kC;
+  static constexpr int kCols = 32 * kC, kWarps = kW, kThreads = 32 * kW, kChunk = kW * kS;
   static constexpr int kStage = kTensors * kTile<T, kC> * kWarps;
   static size_t bytes(int cluster) {
     return 2 * kStage + (2 * kWarps * 8 + (cluster > 1 ? 2 * cluster * 8 : 0) + 2 * 4) * kCols + 2 * kChunk * 4 + sizeof(Span) + 16;
@@ -255,7 +253,7 @@ template <int kCols>
 __device__ __forceinline__ void pass_empty(const int32_t* starts, const Span& span, float* out, const float* in,
                                            int col, int cols) {
   if (!out) return;
-  for (int s = span.seq + static_cast<int>(threadIdx.x); s < span.seq_end; s += kThreads)
+  for (int s = span.seq + static_cast<int>(threadIdx.x); s < span.seq_end; s += static_cast<int>(blockDim.x))
     if (starts[s + 1] <= starts[s])
       for (int64_t c = static_cast<int64_t>(s) * cols + col, n = min(kCols, cols - col); n > 0; ++c, --n) out[c] = in ? in[c] : 0.f;
 }
@@ -379,10 +377,10 @@ __device__ __forceinline__ void load_state(const float* states, int seq, int col
 // first.  The places alternate with the turns: a thread writes to one again only
 // after a barrier, or a message from every CTA, that comes when it has been read.
 // A message that does not come leaves NaN.
-template <int kC, bool kVec, bool kBack>
+template <int kC, int kW, bool kVec, bool kBack>
 __device__ __forceinline__ void exchange(const Shared& sh, int turn, int cluster, uint32_t rank, int warp, int lane,
                                          const Piece (&mine)[kC], float& carry, bool& lost, float (&state)[kC]) {
-  constexpr int kCols = 32 * kC;
+  constexpr int kCols = 32 * kC, kWarps = kW;
   const int parity = turn & 1;
   float2* pieces = sh.pieces + parity * kWarps * kCols;
   float* before = sh.state + parity * kCols;
@@ -434,11 +432,11 @@ struct Flag {
   static constexpr bool value = kValue;
 };
 
-template <typename T, int kC, bool kVec, bool kRagged>
-__global__ void __launch_bounds__(kThreads, (kForwardCtas<T, kC>))
+template <typename T, int kC, int kW, bool kVec, bool kRagged>
+__global__ void __launch_bounds__(32 * kW, (kForwardCtas<T, kC, kW>))
 recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_constant__ Plan plan) {
   constexpr int kCols = 32 * kC;
-  using L = Layout<T, kC, 2>;
+  using L = Layout<T, kC, kW, 2>;
   extern __shared__ __align__(128) uint8_t smem[];
   let_next_start();
   wait_for_predecessors();
@@ -453,9 +451,9 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
   }
   const Span span = span_of<kRagged>(plan, a.starts, rows, static_cast<int>(a.sequences), id / plan.groups, rank, sh);
   if (kRagged && rank == 0) pass_empty<kCols>(a.starts, span, a.hT, a.h0, col, cols);
-  const int base = span.row / kS * kS, step = plan.cluster * kChunk;
+  const int base = span.row / kS * kS, step = plan.cluster * L::kChunk;
   const int turns = span.row_end > span.row ? (span.row_end - base + step - 1) / step : 0;
-  int row = base + (static_cast<int>(rank) * kWarps + warp) * kS;
+  int row = base + (static_cast<int>(rank) * kW + warp) * kS;
   Cursor at = first_cursor<false>(span);
   auto stage = [&](int turn) { return smem + (turn & 1) * L::kStage + warp * 2 * kTile<T, kC>; };
   auto fetch = [&](int r, int turn) {
@@ -511,7 +509,7 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
     if (plain) pieces(Flag<true>{});
     else pieces(Flag<false>{});
     float h[kC];
-    exchange<kC, kVec, false>(sh, turn, plan.cluster, rank, warp, lane, mine, carry, lost, h);
+    exchange<kC, kW, kVec, false>(sh, turn, plan.cluster, rank, warp, lane, mine, carry, lost, h);
     if (a.states && row >= span.row && row < span.row_end)
       store_columns<float, kC, kVec>(a.states + static_cast<int64_t>(row / kS) * cols, col, cols, lane, h);
     T* y = static_cast<T*>(a.y) + static_cast<int64_t>(row) * a.y_ld;
@@ -541,13 +539,13 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
 
 // One row to each sequence: nothing depends on another row.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads) recurrence_step_kernel(const __grid_constant__ opt_recurrence_args a,
+__global__ void __launch_bounds__(kStepThreads) recurrence_step_kernel(const __grid_constant__ opt_recurrence_args a,
                                                                    uint32_t slices) {
   constexpr int kN = kVec ? 8 : 1;
   let_next_start();
   wait_for_predecessors();
   const uint32_t block = blockIdx.x / slices;
-  const int64_t r = block, c = static_cast<int64_t>((blockIdx.x - block * slices) * kThreads + threadIdx.x) * kN;
+  const int64_t r = block, c = static_cast<int64_t>((blockIdx.x - block * slices) * kStepThreads + threadIdx.x) * kN;
   if (c >= a.cols) return;
   float x[kN], g[kN], h[kN];
 #pragma unroll
@@ -576,11 +574,11 @@ __global__ void __launch_bounds__(kThreads) recurrence_step_kernel(const __grid_
 
 // From the last row to the first.  Each warp runs through its rows forward from
 // the saved state for (1 - c) (x_t - h_{t-1}), then backward twice.
-template <typename T, int kC, bool kVec, bool kRagged>
-__global__ void __launch_bounds__(kThreads, kBackwardCtas<T>)
+template <typename T, int kC, int kW, bool kVec, bool kRagged>
+__global__ void __launch_bounds__(32 * kW, (kBackwardCtas<T, kW>))
 recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const __grid_constant__ Plan plan) {
   constexpr int kCols = 32 * kC;
-  using L = Layout<T, kC, 3>;
+  using L = Layout<T, kC, kW, 3>;
   extern __shared__ __align__(128) uint8_t smem[];
   let_next_start();
   wait_for_predecessors();
@@ -595,9 +593,9 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
   }
   const Span span = span_of<kRagged>(plan, a.starts, rows, static_cast<int>(a.sequences), id / plan.groups, rank, sh);
   if (kRagged && rank == 0) pass_empty<kCols>(a.starts, span, a.dh0, a.dhT, col, cols);
-  const int base = span.row / kS * kS, step = plan.cluster * kChunk;
+  const int base = span.row / kS * kS, step = plan.cluster * L::kChunk;
   const int turns = span.row_end > span.row ? (span.row_end - base + step - 1) / step : 0;
-  int row = base + (turns - 1) * step + (static_cast<int>(rank) * kWarps + warp) * kS;
+  int row = base + (turns - 1) * step + (static_cast<int>(rank) * kW + warp) * kS;
   Cursor at = first_cursor<true>(span);
   auto stage = [&](int turn) { return smem + (turn & 1) * L::kStage + warp * 3 * kTile<T, kC>; };
   auto fetch = [&](int r, int turn) {
@@ -677,7 +675,7 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
     if (plain) pieces(Flag<true>{});
     else pieces(Flag<false>{});
     float b[kC];                                  // (1 - c) l of the row behind
-    exchange<kC, kVec, true>(sh, turn, plan.cluster, rank, warp, lane, mine, carry, lost, b);
+    exchange<kC, kW, kVec, true>(sh, turn, plan.cluster, rank, warp, lane, mine, carry, lost, b);
     T* dx = static_cast<T*>(a.dx) + static_cast<int64_t>(row + kS - 1) * a.dx_ld;
     T* dg = static_cast<T*>(a.dgate) + static_cast<int64_t>(row + kS - 1) * a.dgate_ld;
     auto outputs = [&](auto plain) {
@@ -733,7 +731,7 @@ cudaError_t launch_rows(const Args& a, cudaStream_t stream) {
   double least = 0;
   for (int cluster = 1; cluster <= kMaxCluster; ++cluster) {
     int held = 0;
-    const cudaError_t e = clusters_at_once<kKernel>(cluster, kThreads, L::bytes(kMaxCluster), &held);
+    const cudaError_t e = clusters_at_once<kKernel>(cluster, L::kThreads, L::bytes(kMaxCluster), &held);
     if (e != cudaSuccess) return e;
     held *= cluster;
     int64_t ranges = held / (static_cast<int64_t>(groups) * cluster);
@@ -745,7 +743,7 @@ cudaError_t launch_rows(const Args& a, cudaStream_t stream) {
     const int64_t most = ranges == 1 ? a.rows
                          : ragged    ? a.rows / ranges + 3 * average
                                      : (a.sequences + ranges - 1) / ranges * average;
-    const int64_t turns = (most + cluster * kChunk - 1) / (cluster * kChunk);
+    const int64_t turns = (most + cluster * L::kChunk - 1) / (cluster * L::kChunk);
     const int64_t waves = (ranges * groups * cluster + held - 1) / held;
     const double cost = static_cast<double>(turns * waves) * (cluster > 1 ? 1.25 : 1.0);
     if (cluster == 1 || cost < least) {
@@ -755,39 +753,47 @@ cudaError_t launch_rows(const Args& a, cudaStream_t stream) {
     }
   }
   const int64_t ctas = static_cast<int64_t>(plan.cluster) * groups * plan.ranges;
-  return launch_overlapped(kKernel, dim3(static_cast<unsigned>(ctas)), kThreads, L::bytes(plan.cluster), stream, plan.cluster, a,
+  return launch_overlapped(kKernel, dim3(static_cast<unsigned>(ctas)), L::kThreads, L::bytes(plan.cluster), stream, plan.cluster, a,
                            plan);
 }
 
-template <typename T, int kC, bool kVec>
+template <typename T, int kC, int kW, bool kVec>
 cudaError_t run_forward(const opt_recurrence_args& a, cudaStream_t stream) {
-  using L = Layout<T, kC, 2>;
-  return a.starts ? launch_rows<recurrence_kernel<T, kC, kVec, true>, L>(a, stream)
-                  : launch_rows<recurrence_kernel<T, kC, kVec, false>, L>(a, stream);
+  using L = Layout<T, kC, kW, 2>;
+  return a.starts ? launch_rows<recurrence_kernel<T, kC, kW, kVec, true>, L>(a, stream)
+                  : launch_rows<recurrence_kernel<T, kC, kW, kVec, false>, L>(a, stream);
 }
 
-// Four columns to a lane from here on: half the instructions around a row's
-// arithmetic; narrower ones need the CTAs.
-constexpr int64_t kWideCols = 2048;
+template <typename T, int kW, bool kVec>
+cudaError_t run_backward(const opt_recurrence_grad_args& a, cudaStream_t stream) {
+  using L = Layout<T, 2, kW, 3>;
+  return a.starts ? launch_rows<recurrence_grad_kernel<T, 2, kW, kVec, true>, L>(a, stream)
+                  : launch_rows<recurrence_grad_kernel<T, 2, kW, kVec, false>, L>(a, stream);
+}
+
+// The time is that of the turns, one after another, until the columns fill the
+// GPU: narrow recurrences take 16 warps, that is twice the rows, a turn (16384
+// rows in bf16, between events: 512 columns 44 us forward and 52 backward, with 8
+// warps 60 and 70; 2048 columns 61 and 87, with 8 warps 70 and 91; the gradient of
+// 4096 columns 152, with 8 warps 147).  From kWideCols on the forward pass has
+// four columns to a lane: half the instructions around a row's arithmetic (4096
+// columns 97 us, with two columns 104; 2048 columns 93, with two 71: too few CTAs).
+constexpr int64_t kWideCols = 4096, kFewGradCols = 2048;
 
 template <typename T, bool kVec>
 cudaError_t forward(const opt_recurrence_args& a, cudaStream_t stream) {
   if (!a.starts && a.rows == a.sequences) {
-    const int64_t per_cta = kThreads * (kVec ? 8 : 1), slices = (a.cols + per_cta - 1) / per_cta;
-    return launch_overlapped(recurrence_step_kernel<T, kVec>, dim3(static_cast<unsigned>(a.rows * slices)), kThreads, 0, stream,
+    const int64_t per_cta = kStepThreads * (kVec ? 8 : 1), slices = (a.cols + per_cta - 1) / per_cta;
+    return launch_overlapped(recurrence_step_kernel<T, kVec>, dim3(static_cast<unsigned>(a.rows * slices)), kStepThreads, 0, stream,
                              0, a, static_cast<uint32_t>(slices));
   }
-  if constexpr (kVec && sizeof(T) == 2) {
-    if (a.cols >= kWideCols) return run_forward<T, 4, kVec>(a, stream);
-  }
-  return run_forward<T, 2, kVec>(a, stream);
+  if (a.cols < kWideCols) return run_forward<T, 2, 16, kVec>(a, stream);
+  return run_forward<T, kVec && sizeof(T) == 2 ? 4 : 2, 8, kVec>(a, stream);
 }
 
 template <typename T, bool kVec>
 cudaError_t backward(const opt_recurrence_grad_args& a, cudaStream_t stream) {
-  using L = Layout<T, 2, 3>;
-  return a.starts ? launch_rows<recurrence_grad_kernel<T, 2, kVec, true>, L>(a, stream)
-                  : launch_rows<recurrence_grad_kernel<T, 2, kVec, false>, L>(a, stream);
+  return a.cols <= kFewGradCols ? run_backward<T, 16, kVec>(a, stream) : run_backward<T, 8, kVec>(a, stream);
 }
 
 }  // namespace

@@ -302,10 +302,10 @@ def test_recurrence_borders(starts, with_h0):
             check_recurrence(40, 24, np.array(starts), len(starts) - 1, dtype, layout, with_h0, what=str(starts))
 
 
-@pytest.mark.parametrize("cols", [2040, 2048, 2056, 2176])
+@pytest.mark.parametrize("cols", [2048, 2056, 4088, 4096, 4104, 4107, 4224])
 @pytest.mark.parametrize("layout", ["dense", "aligned slice"])
 def test_recurrence_wide(cols, layout):
-    """From 2048 columns on a lane has four of them."""
+    """Where the warps of a CTA and the columns of a lane change."""
     check_recurrence(700, cols, None, 1, BF16, layout)
     check_recurrence(140, cols, None, 7, BF16, layout)
     check_recurrence(300, cols, np.array([3, 3, 19, 20, 100, 100, 297]), 6, BF16, layout)
