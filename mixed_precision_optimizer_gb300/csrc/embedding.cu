@@ -94,7 +94,7 @@ __device__ __forceinline__ void Raw<T, kN>::load(const T* p) {
 // first the tokens, then the table's rows; 2^log_tpr threads to a row.  The columns
 // are 16 bytes of the wider type (4, or 8 where both are bf16: neighbouring lanes
 // store neighbouring 16 bytes; 8 columns of an fp32 output took 16384 x 4096
-// from 59 to 66 us), or one where rows do not start on 16 bytes.
+// from 59 to 66 us, four take 54), or one where rows do not start on 16 bytes.
 constexpr int kRows = 4;
 template <typename T, typename O, bool kVec>
 constexpr int kLookupCols = !kVec ? 1 : sizeof(T) == 2 && sizeof(O) == 2 ? 8 : 4;
@@ -169,8 +169,9 @@ struct SortArgs {
 // Least significant digit first.  Every warp owns consecutive rows; a digit's
 // place is the rows of smaller digits, plus those with this digit of lower
 // CTAs, of lower warps, and earlier ones of the warp: a stable order.  Bound by
-// latency: the first kHeld keys of a lane are loaded at once and kept for the
-// second look at them, and every CTA stores its totals into the others' memory.
+// latency (20 us for 16384 rows in two passes, 52 between events for 65536): the
+// first kHeld keys of a lane are loaded at once and kept for the second look at
+// them, and every CTA stores its totals into the others' memory.
 constexpr int kHeld = 4;
 
 __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __grid_constant__ SortArgs a) {
@@ -283,7 +284,9 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __gr
 // A row's place is the number of smaller tokens and of equal ones before it.  Every
 // CTA has 32 rows and the tokens of all, 1024 at a time in shared memory, of
 // which each of a row's eight threads compares an eighth: rows^2 comparisons over
-// all SMs, 7 us for 8192 rows, in one step without a barrier between CTAs.
+// all SMs in one step without a barrier between CTAs.  Bound by latency for few rows,
+// by the comparisons for many (between events 777 rows take 10 us, 4096 14, 8192 25,
+// 16384 58; the radix sort 18 and, from 4096 rows on, 25).
 constexpr int kRankRows = 32, kRankTile = 1024;
 constexpr int64_t kRankMost = 8192;
 
@@ -343,7 +346,10 @@ constexpr int kJoinAhead = 8;
 // A run's sum goes to the table if the run lies within the piece, else to the
 // piece's first partial row (a run that came from the piece before) or its
 // second (a run that starts here and goes on).  What the table holds at a run's
-// end is loaded with the run's last row.
+// end is loaded with the run's last row.  Bound by HBM: 16384 rows of 4096 bf16
+// columns into a table of 128256 rows take 59 us, 0.9 of the measured copy rate;
+// with four rows on their way instead of eight 95, with each row's place filled
+// again as it is used 165 (a wait for one load waits for others).
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) embedding_sums_kernel(const __grid_constant__ SumArgs p) {
   constexpr int kN = kSumCols<kVec>;
@@ -418,16 +424,17 @@ __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_c
   const uint32_t v = p.key[last];
   if (v >= static_cast<uint32_t>(a.vocab) || p.key[last + 1] != v) return;
   if (piece > 0 && p.key[start - 1] == v && p.key[start] == v) return;        // it started earlier
+  // the run's last piece: the first one behind this that it does not fill, or, where
+  // that does not begin with it, the one before; each warp looks at 32 pieces a time
+  int64_t last_piece = piece + 1;
+  for (uint32_t full = 0xffffffffu; full == 0xffffffffu;) {
+    const int64_t end = (last_piece + static_cast<int>(threadIdx.x & 31) + 1) * p.piece - 1;
+    full = __ballot_sync(0xffffffffu, end < a.rows && p.key[end] == v);
+    last_piece += full == 0xffffffffu ? 32 : __ffs(~full) - 1;
+  }
+  if (last_piece * p.piece >= a.rows || p.key[last_piece * p.piece] != v) --last_piece;
   const int64_t c = (static_cast<int64_t>(blockIdx.x - piece * p.slices) * kThreads + threadIdx.x) * kN;
   if (c >= a.cols) return;
-  // the run's last row, by halving: key[lo] == v, key[hi] != v
-  int64_t lo = last + 1, hi = a.rows;
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) / 2;
-    if (p.key[mid] == v) lo = mid;
-    else hi = mid;
-  }
-  const int64_t last_piece = lo / p.piece;
   float sum[kN], old[kN];
   float* table = a.dtable + v * a.cols + c;
   load_columns(static_cast<const float*>(table), old);
