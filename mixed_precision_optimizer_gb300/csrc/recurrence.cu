@@ -13,12 +13,15 @@
 // and B is selected, not multiplied, so that an infinity or a NaN stays in its
 // own sequence.
 //
-// A warp has 64 columns, two to a lane (or 128, four), and 8 rows at a time in shared memory,
-// fetched with cp.async while it works on the rows before.  Its CTA's eight
-// (or 16) pieces, and those of the CTAs of a cluster, which take the next rows each, are
-// joined through (distributed) shared memory; then every thread runs through its
-// rows again from the right state.  Bound by HBM: x and gate are read once (and
-// dy), the outputs written once; a state for every 8 rows in fp32 is all that the
+// A warp has 64 columns, two to a lane (or 128, four), and 8 rows at a time in shared
+// memory, fetched with cp.async while it works on the rows before.  The pieces of
+// its CTA's eight or 16 warps, and those of the CTAs of a cluster, which take the
+// next rows each, are joined through (distributed) shared memory; then every
+// thread runs through its rows again from the right state.  x and gate are read
+// once (and dy), the outputs written once: HBM's floor is 59 us for 16384 x 4096 in
+// bf16, 50 for the gradient of 8192 x 4096.  They take 92 and 91: a turn of 512 (384)
+// rows is a chain of the pieces, their join, the mail and the outputs, 2.9 us, with
+// 25 (52) instructions an element.  A state for every 8 rows in fp32 is all that the
 // gradient needs of the forward pass.
 
 #include <climits>
@@ -34,7 +37,8 @@ namespace {
 constexpr int kStepThreads = 256;
 constexpr int kMaxCluster = kMostClusterCtas;
 constexpr int kS = kRecurrenceStateRows;         // rows of a thread at a time
-constexpr float kReset = -1.f;
+constexpr float kReset = -1.f;                   // a product of 1 - c is not below a rounding of 0
+__device__ __forceinline__ bool is_reset(float p) { return p < -0.5f; }
 
 // ---------------------------------------------------------------- pieces --
 
@@ -42,10 +46,10 @@ struct Piece {
   float p, b;
 };
 __device__ __forceinline__ Piece then(Piece first, Piece second) {
-  if (second.p < 0.f) return second;
-  return Piece{first.p < 0.f ? kReset : first.p * second.p, fmaf(second.p, first.b, second.b)};
+  if (is_reset(second.p)) return second;
+  return Piece{is_reset(first.p) ? kReset : first.p * second.p, fmaf(second.p, first.b, second.b)};
 }
-__device__ __forceinline__ float through(Piece q, float h) { return q.p < 0.f ? q.b : fmaf(q.p, h, q.b); }
+__device__ __forceinline__ float through(Piece q, float h) { return is_reset(q.p) ? q.b : fmaf(q.p, h, q.b); }
 
 // 1 / (1 + e^-g) from two approximate instructions of 2 units each; the rounding
 // of g log2 e adds 2^-24 |g| of the value.  0 below g = -87.
@@ -527,7 +531,8 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
           store_columns<T, kC, kVec>(y, col, cols, lane, h);
         }
         if (!plain.value && (m.end >> j & 1) && a.hT)
-          store_columns<float, kC, kVec>(a.hT + static_cast<int64_t>(__shfl_sync(0xffffffffu, m.end_seq, j)) * cols, col, cols, lane, h);
+          store_columns<float, kC, kVec>(a.hT + static_cast<int64_t>(__shfl_sync(0xffffffffu, m.end_seq, j)) * cols, col, cols,
+                                         lane, h);
       }
     };
     if (plain) outputs(Flag<true>{});
@@ -607,7 +612,7 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
     }
     copy_commit();
   };
-  auto saved = [&](int r, float (&h)[kC]) {   // h before row r, where that is a row of the span
+  auto saved = [&](int r, float (&h)[kC]) {      // h before row r, where that is a row of the span
     load_state<kC, kVec>(r >= span.row && r < span.row_end ? a.states : nullptr, r / kS, col, cols, lane, h);
   };
   float coming[kC];
@@ -627,7 +632,7 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
     if constexpr (kRagged) m = marks_ragged<true>(a.starts, rows, span, row, at, sh, warp, lane);
     else m = marks_equal<true>(plan, span, row, at, lane);
     const uint8_t *xs = stage(turn), *gs = xs + kTile<T, kC>, *ys = gs + kTile<T, kC>;
-    float c[kS][kC], q[kS][kC];                    // q = (1 - c) (x_t - h_{t-1})
+    float c[kS][kC], q[kS][kC];                  // q = (1 - c) (x_t - h_{t-1})
     Piece mine[kC];
 #pragma unroll
     for (int k = 0; k < kC; ++k) mine[k] = Piece{1.f, 0.f};
@@ -674,7 +679,7 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
     const bool plain = row >= span.row && row + kS <= span.row_end && (m.start | m.end) == 0;
     if (plain) pieces(Flag<true>{});
     else pieces(Flag<false>{});
-    float b[kC];                                  // (1 - c) l of the row behind
+    float b[kC];                                 // (1 - c) l of the row behind
     exchange<kC, kW, kVec, true>(sh, turn, plan.cluster, rank, warp, lane, mine, carry, lost, b);
     T* dx = static_cast<T*>(a.dx) + static_cast<int64_t>(row + kS - 1) * a.dx_ld;
     T* dg = static_cast<T*>(a.dgate) + static_cast<int64_t>(row + kS - 1) * a.dgate_ld;
@@ -699,7 +704,8 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
         }
         if (!plain.value && (m.start >> j & 1)) {
           if (a.dh0)
-            store_columns<float, kC, kVec>(a.dh0 + static_cast<int64_t>(__shfl_sync(0xffffffffu, m.start_seq, j)) * cols, col, cols, lane, b);
+            store_columns<float, kC, kVec>(a.dh0 + static_cast<int64_t>(__shfl_sync(0xffffffffu, m.start_seq, j)) * cols, col,
+                                           cols, lane, b);
 #pragma unroll
           for (int k = 0; k < kC; ++k) b[k] = 0.f;
         }
