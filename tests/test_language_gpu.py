@@ -759,6 +759,47 @@ def test_other_stream_and_graph():
         assert torch.equal(t, v)
 
 
+FIRST_CALLS_CAPTURED = """
+import torch, mixed_precision_optimizer_gb300 as mp
+x, gate, dy = (torch.randn(500, 2048, device="cuda").to(torch.bfloat16) for _ in range(3))
+labels, tokens = torch.arange(500, device="cuda"), torch.arange(500, device="cuda") % 7
+y, g, dx, dg = (torch.zeros_like(x) for _ in range(4))
+wide = torch.randn(40, 40000, device="cuda")
+states, table = mp.recurrence_states(500, 2048, x.dtype), torch.zeros(9, 2048, device="cuda")
+loss, ws, dwide = torch.zeros(40, device="cuda"), mp.embedding_workspace(9000, 9, 2048), torch.zeros_like(wide)
+many = torch.arange(9000, device="cuda") % 9
+rows = torch.randn(9000, 2048, device="cuda")
+def step():
+    mp.gated_recurrence(x, gate, y, states=states)
+    mp.cross_entropy(y, labels, dlogits=g)
+    mp.cross_entropy(wide, labels[:40], loss, dlogits=dwide)
+    mp.gated_recurrence_backward(dy, x, gate, states, dx, dg)
+    mp.embedding_backward(many, rows, table, accumulate=False, workspace=ws)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+graph.replay()
+torch.cuda.synchronize()
+outs = [t.clone() for t in (y, g, loss, dwide, dx, dg, table)]
+step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(outs, (y, g, loss, dwide, dx, dg, table))) and y.any() and table.any()
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_are_captured():
+    """What a kernel asks once (its shared memory, the clusters that fit) may be asked
+    while a stream is captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS_CAPTURED], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
 def test_calls_on_two_streams_at_once():
     """Calls that share inputs, each with outputs and a workspace of its own."""
     rows, cols, vocab = 3000, 512, 700
