@@ -783,7 +783,8 @@ cudaError_t run_backward(const opt_recurrence_grad_args& a, cudaStream_t stream)
 // warps 60 and 70; 2048 columns 61 and 87, with 8 warps 70 and 91; the gradient of
 // 4096 columns 152, with 8 warps 147).  From kWideCols on the forward pass has
 // four columns to a lane: half the instructions around a row's arithmetic (4096
-// columns 97 us, with two columns 104; 2048 columns 93, with two 71: too few CTAs).
+// columns 97 us, with two columns 99 by 16 warps and 104 by 8; 2048 columns 93,
+// with two 61: too few CTAs).
 constexpr int64_t kWideCols = 4096, kFewGradCols = 2048;
 
 template <typename T, bool kVec>
