@@ -8,7 +8,9 @@
 // the product of their 1 - c; the gradient passes them the same way backwards.
 // Two such pieces, the first (P1, B1) and behind it (P2, B2), make
 //   P = P1 P2,  B = B2 + P2 B1
-// P is kept as P - c P, one rounding a row, no more than h's own.  A piece in which a
+// Both c and 1 - c are taken from the smaller of them, which is exact to 2^-20 of
+// itself however far the gate is open or closed: (1 - c) v is v - c v where
+// c < 1/2, one rounding of v, and the product with 1 - c beyond.  A piece in which a
 // sequence starts or ends does not depend on the state before it: P = kReset,
 // and B is selected, not multiplied, so that an infinity or a NaN stays in its
 // own sequence.
@@ -17,12 +19,13 @@
 // memory, fetched with cp.async while it works on the rows before.  The pieces of
 // its CTA's eight or 16 warps, and those of the CTAs of a cluster, which take the
 // next rows each, are joined through (distributed) shared memory; then every
-// thread runs through its rows again from the right state.  x and gate are read
-// once (and dy), the outputs written once: HBM's floor is 59 us for 16384 x 4096 in
-// bf16, 50 for the gradient of 8192 x 4096.  They take 92 and 91: a turn of 512 (384)
-// rows is a chain of the pieces, their join, the mail and the outputs, 2.9 us, with
-// 25 (52) instructions an element.  A state for every 8 rows in fp32 is all that the
-// gradient needs of the forward pass.
+// thread applies the pieces up to each of its rows to the right state (the gradient runs
+// through its rows again; for the forward pass that took 109 us in place of 97.6, the
+// gradient's registers do not hold the pieces).  x and gate are read
+// once (and dy), the outputs written once: HBM's floor is 60 us for 16384 x 4096 in
+// bf16, 50 for the gradient of 8192 x 4096.  They take 98 and 99: a turn of 512 (384)
+// rows is a chain of the pieces, their join, the mail and the outputs, 3.1 us.  A state
+// for every 8 rows in fp32 is all that the gradient needs of the forward pass.
 
 #include <climits>
 
@@ -37,7 +40,7 @@ namespace {
 constexpr int kStepThreads = 256;
 constexpr int kMaxCluster = kMostClusterCtas;
 constexpr int kS = kRecurrenceStateRows;         // rows of a thread at a time
-constexpr float kReset = -1.f;                   // a product of 1 - c is not below a rounding of 0
+constexpr float kReset = -1.f;                   // a product of 1 - c is not below 0
 __device__ __forceinline__ bool is_reset(float p) { return p < -0.5f; }
 
 // ---------------------------------------------------------------- pieces --
@@ -51,19 +54,42 @@ __device__ __forceinline__ Piece then(Piece first, Piece second) {
 }
 __device__ __forceinline__ float through(Piece q, float h) { return is_reset(q.p) ? q.b : fmaf(q.p, h, q.b); }
 
-// 1 / (1 + e^-g) from two approximate instructions of 2 units each; the rounding
-// of g log2 e adds 2^-24 |g| of the value.  0 below g = -87.
-__device__ __forceinline__ float exp_neg(float g) {
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * g));
-  return e;
+// A row's gate: w = c where gate < 0, and -(1 - c), with its sign bit even where that is
+// 0, where the gate is open.  |w| = e / (1 + e), e = exp(-|gate|), from two approximate
+// instructions of 2 units each; the rounding of gate log2 e adds 2^-24 |gate| of the
+// value.  0 beyond |gate| = 87.  From c alone 1 - c would be off by 2^-24 of 1, that is 1 %
+// of itself at a gate of 12 and all of it from 17 on; the selects that this takes cost
+// the forward pass 6 % (16384 x 4096: 97.6 us for 91.3) and the gradient 10 % (8192 x
+// 4096 packed: 98.8 for 89.8).
+__device__ __forceinline__ float gate_of(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * fabsf(g)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return __uint_as_float(__float_as_uint(e * r) | (~__float_as_uint(g) & 0x80000000u));
 }
-__device__ __forceinline__ float reciprocal(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
+__device__ __forceinline__ bool is_open(float w) { return __float_as_int(w) < 0; }
+// h + c (x - h)
+__device__ __forceinline__ float advance(float w, float x, float h) { return fmaf(w, x - h, is_open(w) ? x : h); }
+// (1 - c) v
+__device__ __forceinline__ float keep(float w, float v) { return fmaf(-w, v, is_open(w) ? 0.f : v); }
+// c v and (1 - c) v: the smaller is a product, the other what it leaves of v.
+struct Parts {
+  float taken, kept;
+};
+__device__ __forceinline__ Parts parts_of(float w, float v) {
+  const float small = fabsf(w) * v, large = v - small;
+  return is_open(w) ? Parts{large, small} : Parts{small, large};
 }
-__device__ __forceinline__ float update_gate(float g) { return reciprocal(1.f + exp_neg(g)); }
+
+// Two columns' pieces with one row more, advance() and keep() by packed instructions
+// (one column at a time took 16384 x 4096 to 101.7 us; with the gates packed too, 117).
+__device__ __forceinline__ void add_row(float wa, float wb, float xa, float xb, Piece& a, Piece& b) {
+  const float2 n = make_float2(-wa, -wb), d = make_float2(a.b - xa, b.b - xb), p = make_float2(a.p, b.p);
+  const float2 h = __ffma2_rn(n, d, make_float2(is_open(wa) ? xa : a.b, is_open(wb) ? xb : b.b));
+  const float2 q = __ffma2_rn(n, p, make_float2(is_open(wa) ? 0.f : p.x, is_open(wb) ? 0.f : p.y));
+  a = Piece{q.x, h.x};
+  b = Piece{q.y, h.y};
+}
 
 // ----------------------------------------------------------------- layout --
 
@@ -479,8 +505,7 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
     if constexpr (kRagged) m = marks_ragged<false>(a.starts, rows, span, row, at, sh, warp, lane);
     else m = marks_equal<false>(plan, span, row, at, lane);
     const uint8_t *xs = stage(turn), *gs = xs + kTile<T, kC>;
-    float c[kS][kC];
-    Piece mine[kC];
+    Piece upto[kS][kC], mine[kC];                // of the rows up to each, of all
 #pragma unroll
     for (int k = 0; k < kC; ++k) mine[k] = Piece{1.f, 0.f};
     auto pieces = [&](auto plain) {              // plain: all rows are there, no sequence starts or ends
@@ -497,11 +522,11 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
           for (int k = 0; k < kC; ++k) mine[k].b = h0[k];
         }
 #pragma unroll
-        for (int k = 0; k < kC; ++k) {
-          c[j][k] = in ? update_gate(g[k]) : 0.f;
-          // a row that is not there leaves b alone, whatever lies in its place
-          mine[k].b = in ? fmaf(c[j][k], x[k] - mine[k].b, mine[k].b) : mine[k].b;
-          mine[k].p = fmaf(-c[j][k], mine[k].p, mine[k].p);
+        for (int k = 0; k < kC; k += 2) {
+          // a row that is not there leaves both alone, whatever lies in its place
+          if (in) add_row(gate_of(g[k]), gate_of(g[k + 1]), x[k], x[k + 1], mine[k], mine[k + 1]);
+          upto[j][k] = mine[k];
+          upto[j][k + 1] = mine[k + 1];
         }
       }
       if (!plain.value && m.start) {
@@ -520,19 +545,20 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
     auto outputs = [&](auto plain) {
 #pragma unroll
       for (int j = 0; j < kS; ++j, y += a.y_ld) {
-        float x[kC];
-        columns_at<T, kC, kVec>(xs, j, lane, x);
         const bool in = plain.value || (row + j >= span.row && row + j < span.row_end);
-        if (!plain.value && (m.start >> j & 1))
-          load_state<kC, kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, cols, lane, h);
-        if (in) {
+        const bool begun = !plain.value && (m.start & ((2u << j) - 1)) != 0;      // a sequence, among these rows
+        float v[kC];
 #pragma unroll
-          for (int k = 0; k < kC; ++k) h[k] = fmaf(c[j][k], x[k] - h[k], h[k]);
-          store_columns<T, kC, kVec>(y, col, cols, lane, h);
+        for (int k = 0; k < kC; k += 2) {
+          const Piece p = upto[j][k], q = upto[j][k + 1];
+          const float2 f = __ffma2_rn(make_float2(p.p, q.p), make_float2(h[k], h[k + 1]), make_float2(p.b, q.b));
+          v[k] = begun ? p.b : f.x;
+          v[k + 1] = begun ? q.b : f.y;
         }
+        if (in) store_columns<T, kC, kVec>(y, col, cols, lane, v);
         if (!plain.value && (m.end >> j & 1) && a.hT)
           store_columns<float, kC, kVec>(a.hT + static_cast<int64_t>(__shfl_sync(0xffffffffu, m.end_seq, j)) * cols, col, cols,
-                                         lane, h);
+                                         lane, v);
       }
     };
     if (plain) outputs(Flag<true>{});
@@ -565,7 +591,7 @@ __global__ void __launch_bounds__(kStepThreads) recurrence_step_kernel(const __g
     if (a.h0) h[0] = a.h0[r * a.cols + c];
   }
 #pragma unroll
-  for (int j = 0; j < kN; ++j) h[j] = fmaf(update_gate(g[j]), x[j] - h[j], h[j]);
+  for (int j = 0; j < kN; ++j) h[j] = advance(gate_of(g[j]), x[j], h[j]);
   if constexpr (kVec) {
     store8(static_cast<T*>(a.y) + r * a.y_ld + c, h);
     if (a.hT) store8(a.hT + r * a.cols + c, h);
@@ -632,7 +658,7 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
     if constexpr (kRagged) m = marks_ragged<true>(a.starts, rows, span, row, at, sh, warp, lane);
     else m = marks_equal<true>(plan, span, row, at, lane);
     const uint8_t *xs = stage(turn), *gs = xs + kTile<T, kC>, *ys = gs + kTile<T, kC>;
-    float c[kS][kC], q[kS][kC];                  // q = (1 - c) (x_t - h_{t-1})
+    float w[kS][kC], q[kS][kC];                  // q = (1 - c) (x_t - h_{t-1})
     Piece mine[kC];
 #pragma unroll
     for (int k = 0; k < kC; ++k) mine[k] = Piece{1.f, 0.f};
@@ -647,10 +673,9 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
           load_state<kC, kVec>(a.h0, __shfl_sync(0xffffffffu, m.start_seq, j), col, cols, lane, h);
 #pragma unroll
         for (int k = 0; k < kC; ++k) {
-          const float e = exp_neg(g[k]), r = reciprocal(1.f + e), d = x[k] - h[k];
-          c[j][k] = in ? r : 0.f;
-          q[j][k] = (g[k] > 0.f ? e * r : 1.f - r) * d;       // 1 - c, as exact as c where c is near one too
-          h[k] = in ? fmaf(c[j][k], d, h[k]) : h[k];
+          w[j][k] = in ? gate_of(g[k]) : 0.f;
+          q[j][k] = parts_of(w[j][k], x[k] - h[k]).kept;
+          h[k] = in ? advance(w[j][k], x[k], h[k]) : h[k];
         }
       }
 #pragma unroll
@@ -667,8 +692,8 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
 #pragma unroll
         for (int k = 0; k < kC; ++k) {
           const float l = dy[k] + mine[k].b;
-          mine[k].b = !in ? mine[k].b : !plain.value && (m.start >> j & 1) ? 0.f : fmaf(-c[j][k], l, l);
-          mine[k].p = fmaf(-c[j][k], mine[k].p, mine[k].p);
+          mine[k].b = !in ? mine[k].b : !plain.value && (m.start >> j & 1) ? 0.f : keep(w[j][k], l);
+          mine[k].p = keep(w[j][k], mine[k].p);
         }
       }
       if (!plain.value && (m.start | m.end)) {
@@ -694,10 +719,10 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
         if (in) {
 #pragma unroll
           for (int k = 0; k < kC; ++k) {
-            const float l = dy[k] + b[k];
-            ox[k] = c[j][k] * l;
+            const Parts l = parts_of(w[j][k], dy[k] + b[k]);
+            ox[k] = l.taken;
             og[k] = ox[k] * q[j][k];
-            b[k] = fmaf(-c[j][k], l, l);
+            b[k] = l.kept;
           }
           store_columns<T, kC, kVec>(dx, col, cols, lane, ox);
           store_columns<T, kC, kVec>(dg, col, cols, lane, og);
@@ -779,12 +804,12 @@ cudaError_t run_backward(const opt_recurrence_grad_args& a, cudaStream_t stream)
 
 // The time is that of the turns, one after another, until the columns fill the
 // GPU: narrow recurrences take 16 warps, that is twice the rows, a turn (16384
-// rows in bf16, between events: 512 columns 44 us forward and 52 backward, with 8
-// warps 60 and 70; 2048 columns 61 and 87, with 8 warps 70 and 91; the gradient of
-// 4096 columns 152, with 8 warps 147).  From kWideCols on the forward pass has
-// four columns to a lane: half the instructions around a row's arithmetic (4096
-// columns 97 us, with two columns 99 by 16 warps and 104 by 8; 2048 columns 93,
-// with two 61: too few CTAs).
+// rows in bf16, back to back: 512 columns 54 us forward and 50 backward, with 8
+// warps 59 and 96; 2048 columns 60 and 87, with 8 warps 102 and 131; the gradient of
+// 8192 packed rows of 4096 columns 100, with 8 warps 99).  From kWideCols on the
+// forward pass has four columns to a lane: half the instructions around a row's
+// arithmetic (4096 columns 98 us, with two columns 108 by 16 warps and 109 by 8; 2048
+// columns 94, with two 60: too few CTAs).
 constexpr int64_t kWideCols = 4096, kFewGradCols = 2048;
 
 template <typename T, bool kVec>
