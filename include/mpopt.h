@@ -632,9 +632,12 @@ MPOPT_API size_t opt_linear_workspace_size(int64_t m, int64_t n, int64_t k, int3
  * those of the feed-forward operators: row-major matrices with a row distance,
  * sums and states in fp32, one rounding to an output's own type.  Every result
  * has the same bits each time.  Outputs may not overlap inputs or one another
- * but where an argument says so.  CTAs that share a row or a sequence wait for
- * one another for two seconds at most; a wait that runs out leaves NaN in the
- * outputs that depend on it.
+ * but where an argument says so.  CTAs that share a row or a sequence send one
+ * another messages.  A wait for one gives up after two seconds; from then on the
+ * CTAs that share the row or the sequence exchange no more, and the outputs
+ * that depend on a message that did not come are NaN, the others right.  (What
+ * the cluster's hardware barrier at a kernel's start and end waits for is that
+ * its CTAs run; no clock bounds it.)
  */
 
 /* Integer type of token and label arrays. */
@@ -820,6 +823,20 @@ typedef struct {
 MPOPT_API opt_status opt_cross_entropy(const opt_cross_entropy_args* args, void* stream);
 
 /*
+ * Self-test of the messages between the CTAs of a cluster (for tests of the
+ * failure path).  `ctas` CTAs (2 to 8) of OPT_MAIL_SELFTEST_THREADS threads send
+ * one another `messages` messages (up to 64); sums [ctas][messages][threads] gets
+ * what each thread has received: sum over the CTAs c of 1000 k + 64 c + t for
+ * message k and thread t.  The last CTA's first thread holds back its part of
+ * message held_back (-1: none) to the first CTA, whose waits for that message run
+ * out after 0.2 s, the others' for the next one after that.  NaN stands for each
+ * message that has not come, in the first CTA from held_back on and in the others
+ * from the one after it on.  Nothing faults, and the CUDA context stays usable.
+ */
+enum { OPT_MAIL_SELFTEST_THREADS = 64 };
+MPOPT_API opt_status opt_selftest_mail(float* sums, int32_t ctas, int32_t messages, int32_t held_back, void* stream);
+
+/*
  * Optional launch instrumentation (off by default).  After
  *   opt_profile_launches(events, info, capacity, &count)
  * every kernel this library launches from the calling thread is bracketed by
@@ -887,7 +904,8 @@ MPOPT_API const char* opt_strerror(opt_status status);
 MPOPT_API const char* opt_last_cuda_error(void);
 
 /* ABI version: (major << 16) | minor (2.0: Muon variants, scale shapes, clipping;
-   2.1: feed-forward operators; 2.2: language-model operators). */
+   2.1: feed-forward operators; 2.2: language-model operators; 2.3: their
+   messages' self-test). */
 MPOPT_API int32_t opt_abi_version(void);
 
 #ifdef __cplusplus

@@ -98,7 +98,7 @@ EXPORTED = ("opt_workspace_size", "opt_adamw_step", "opt_muon_step", "opt_mixed_
             "opt_linear_forward", "opt_linear_backward", "opt_linear_workspace_size",
             "opt_embedding_forward", "opt_embedding_backward", "opt_embedding_workspace_size",
             "opt_recurrence_forward", "opt_recurrence_backward", "opt_recurrence_state_rows",
-            "opt_checkpoint_save", "opt_checkpoint_restore", "opt_cross_entropy")
+            "opt_checkpoint_save", "opt_checkpoint_restore", "opt_cross_entropy", "opt_selftest_mail")
 
 KERNEL_NAMES = {0: "ns_gram", 1: "ns_poly", 2: "ns_bx", 3: "adamw", 4: "muon_momentum", 5: "muon_norm",
                 6: "muon_apply", 7: "muon_fixup", 8: "grad_norm", 9: "clip_finalize", 10: "muon_sample",
@@ -500,4 +500,4 @@ from .feedforward import (linear, linear_backward, linear_workspace, linear_work
 from . import language  # noqa: E402
 from .language import (checkpoint_restore, checkpoint_save, cross_entropy, embedding, embedding_backward,  # noqa: E402,F401
                        embedding_workspace, embedding_workspace_size, gated_recurrence, gated_recurrence_backward,
-                       recurrence_states)
+                       recurrence_states, selftest_mail)

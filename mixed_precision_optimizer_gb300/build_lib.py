@@ -22,7 +22,7 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmpopt.so")
 SOURCES = ["api.cu", "adamw.cu", "checkpoint.cu", "clip.cu", "cross_entropy.cu", "embedding.cu", "feedforward_api.cu",
            "hostcopy.cu", "language_api.cu", "lifecycle.cu", "linear.cu", "muon_elementwise.cu", "norm.cu", "ns_gemm.cu",
-           "recurrence.cu"]
+           "recurrence.cu", "selftest.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

@@ -936,7 +936,7 @@ opt_status opt_profile_launches(void* const* events, opt_launch_info* info, int3
   return OPT_OK;
 }
 
-int32_t opt_abi_version(void) { return (2 << 16) | 2; }
+int32_t opt_abi_version(void) { return (2 << 16) | 3; }
 
 }  // extern "C"
 

@@ -9,6 +9,8 @@
 
 #include <cstdint>
 
+#include "mail.h"
+
 namespace mpopt {
 namespace {
 
@@ -43,9 +45,11 @@ __device__ __forceinline__ void store_peer(uint32_t at, uint32_t v) {
 // thread of each CTA calls expect(k, bytes) with what all CTAs send it, the
 // senders send(), the readers wait(k).  A place is used again for message k + 2:
 // who sends that has to have waited for message k + 1, and its readers to have
-// read message k before they sent theirs.
+// read message k before they sent theirs (exchange_message in mail.h sees to both,
+// where waits run out too).
 struct Mailbox {
   uint64_t* bar;         // [2] in shared memory
+  unsigned long long limit_ns = 2000000000ull;
 
   static __device__ __forceinline__ uint32_t u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
   __device__ __forceinline__ void init() const {
@@ -61,14 +65,14 @@ struct Mailbox {
                  "f"(v.x), "f"(v.y), "r"(at_peer(bar + (k & 1), rank))
                  : "memory");
   }
-  // Whether message k is there; a wait gives up after two seconds.
+  // Whether message k is there; a wait gives up after two seconds (limit_ns).
   __device__ __forceinline__ bool wait(int k) const {
     const uint32_t at = u32(bar + (k & 1)), parity = static_cast<uint32_t>(k >> 1) & 1u;
     if (there(at, parity)) return true;
     const unsigned long long t0 = nanoseconds();
     for (uint32_t i = 1;; ++i) {
       if (there(at, parity)) return true;
-      if ((i & 63u) == 0 && nanoseconds() - t0 > 2000000000ull) return false;
+      if ((i & 63u) == 0 && nanoseconds() - t0 > limit_ns) return false;
     }
   }
 

@@ -248,7 +248,7 @@ cross_entropy_cluster_kernel(const __grid_constant__ opt_cross_entropy_args a, i
   int64_t r = blockIdx.x / cluster;
   for (int s = 0; s < C::kStages; ++s) fetch(r + s * step, s);
   int label = label_at(r), next_label = -1;      // the grid has no more clusters than rows
-  bool lost = false;                             // a message of the cluster's
+  int lost_at = kNoneLost;                       // a message of the cluster's
   for (int k = 0, stage = 0; r < a.rows; ++k, r += step, label = next_label, stage = stage + 1 == C::kStages ? 0 : stage + 1) {
     const T* x = row_at(r);
     const Place p = place_of(x, cols);
@@ -292,9 +292,10 @@ cross_entropy_cluster_kernel(const __grid_constant__ opt_cross_entropy_args a, i
     fetch(r + C::kStages * step, stage);         // over what this thread has read
     Stat s = warp_join(Stat{top, sum});
     if (cluster > 1) {                           // lane i tells CTA i
-      if (t == 0) mail.expect(k, static_cast<uint32_t>(cluster) * kWarps * 8);
-      if (lane < cluster) mail.send(k, &parts[k & 1][rank * kWarps + warp], lane, make_float2(s.top, s.sum));
-      lost = lost || !mail.wait(k);
+      const bool there = exchange_message(mail, k, t == 0, static_cast<uint32_t>(cluster) * kWarps * 8, lost_at, [&] {
+        if (lane < cluster) mail.send(k, &parts[k & 1][rank * kWarps + warp], lane, make_float2(s.top, s.sum));
+      });
+      if (!__all_sync(0xffffffffu, there) && lost_at == kNoneLost) lost_at = k;      // a warp reads and sends as one
     } else {
       if (lane == 0) parts[k & 1][warp] = make_float2(s.top, s.sum);
       __syncthreads();
@@ -305,7 +306,7 @@ cross_entropy_cluster_kernel(const __grid_constant__ opt_cross_entropy_args a, i
       s = join(s, Stat{q.x, q.y});
     }
     s = warp_join(s);
-    if (lost) s.sum = __uint_as_float(0x7fc00000u);
+    if (lost_at != kNoneLost) s.sum = __uint_as_float(0x7fc00000u);
     const bool none = s.sum == 0.f;              // an empty row
     if (rank == 0 && t == 0) {
       if (a.lse) a.lse[r] = none ? -INFINITY : s.top + logf(s.sum);
@@ -341,7 +342,10 @@ cross_entropy_cluster_kernel(const __grid_constant__ opt_cross_entropy_args a, i
       }
     }
   }
-  if (cluster > 1) cluster_sync();               // nobody leaves while mail to it is on its way
+  if (cluster > 1) {                             // nobody leaves while mail to it is on its way
+    cluster_sync();
+    leave_mail(mail, lost_at);
+  }
 }
 
 template <typename T, int kThreads>

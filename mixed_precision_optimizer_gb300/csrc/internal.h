@@ -407,6 +407,9 @@ cudaError_t launch_checkpoint_restore(const opt_checkpoint_args& a, cudaStream_t
 
 cudaError_t launch_cross_entropy(const opt_cross_entropy_args& a, cudaStream_t stream);
 
+constexpr int kMailSelftestThreads = OPT_MAIL_SELFTEST_THREADS;
+cudaError_t launch_mail_selftest(float* sums, int ctas, int messages, int held_back, cudaStream_t stream);
+
 // Records the CUDA error's text for opt_last_cuda_error; returns OPT_ERR_CUDA's value.
 int record_cuda_error(cudaError_t e, const char* where);
 

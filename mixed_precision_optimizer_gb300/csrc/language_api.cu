@@ -206,4 +206,10 @@ opt_status opt_cross_entropy(const opt_cross_entropy_args* a, void* stream) {
   return run(OPT_KERNEL_CROSS_ENTROPY, a->rows, a->cols, st, "cross-entropy launch", [&] { return launch_cross_entropy(*a, st); });
 }
 
+opt_status opt_selftest_mail(float* sums, int32_t ctas, int32_t messages, int32_t held_back, void* stream) {
+  if (ctas < 2 || ctas > 8 || messages < 1 || messages > 64 || held_back < -1 || held_back >= messages) return OPT_ERR_INVALID_ARG;
+  MPOPT_TRY(check_vector(sums, false, 4));
+  return cuda_status(launch_mail_selftest(sums, ctas, messages, held_back, static_cast<cudaStream_t>(stream)), "mail self-test launch");
+}
+
 }  // extern "C"

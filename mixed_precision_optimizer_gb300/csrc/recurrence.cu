@@ -406,10 +406,10 @@ __device__ __forceinline__ void load_state(const float* states, int seq, int col
 // all their rows.  kBack: rows, warps and CTAs are taken from the last to the
 // first.  The places alternate with the turns: a thread writes to one again only
 // after a barrier, or a message from every CTA, that comes when it has been read.
-// A message that does not come leaves NaN.
+// From a message that does not come on, `carry` is NaN.
 template <int kC, int kW, bool kVec, bool kBack>
 __device__ __forceinline__ void exchange(const Shared& sh, int turn, int cluster, uint32_t rank, int warp, int lane,
-                                         const Piece (&mine)[kC], float& carry, bool& lost, float (&state)[kC]) {
+                                         const Piece (&mine)[kC], float& carry, int& lost_at, float (&state)[kC]) {
   constexpr int kCols = 32 * kC, kWarps = kW;
   const int parity = turn & 1;
   float2* pieces = sh.pieces + parity * kWarps * kCols;
@@ -434,15 +434,15 @@ __device__ __forceinline__ void exchange(const Shared& sh, int turn, int cluster
       carry = through(all, carry);
     } else {
       float2* inbox = sh.inbox + parity * cluster * kCols;
-      if (c == 0) sh.mail.expect(turn, static_cast<uint32_t>(cluster) * kCols * 8);
-      for (int i = 0; i < cluster; ++i) sh.mail.send(turn, inbox + rank * kCols + c, i, make_float2(all.p, all.b));
-      lost = lost || !sh.mail.wait(turn);
-      if (lost) carry = __uint_as_float(0x7fc00000u);
+      const bool there = exchange_message(sh.mail, turn, c == 0, static_cast<uint32_t>(cluster) * kCols * 8, lost_at, [&] {
+        for (int i = 0; i < cluster; ++i) sh.mail.send(turn, inbox + rank * kCols + c, i, make_float2(all.p, all.b));
+      });
+      if (!there) carry = __uint_as_float(0x7fc00000u);
       for (int i = 0; i < cluster; ++i) {
         const int w = kBack ? cluster - 1 - i : i;
         if (w == static_cast<int>(rank)) before[c] = carry;
         const float2 q = inbox[w * kCols + c];
-        carry = lost ? carry : through(Piece{q.x, q.y}, carry);
+        carry = there ? through(Piece{q.x, q.y}, carry) : carry;
       }
     }
   }
@@ -496,7 +496,7 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
   };
   fetch(row, 0);
   float carry = 0.f;                             // the first kCols threads: behind all rows so far
-  bool lost = false;                             // a message of the cluster's
+  int lost_at = kNoneLost;                       // a message of the cluster's
   for (int turn = 0; turn < turns; ++turn, row += step) {
     copy_wait<0>();
     __syncwarp();
@@ -538,7 +538,7 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
     if (plain) pieces(Flag<true>{});
     else pieces(Flag<false>{});
     float h[kC];
-    exchange<kC, kW, kVec, false>(sh, turn, plan.cluster, rank, warp, lane, mine, carry, lost, h);
+    exchange<kC, kW, kVec, false>(sh, turn, plan.cluster, rank, warp, lane, mine, carry, lost_at, h);
     if (a.states && row >= span.row && row < span.row_end)
       store_columns<float, kC, kVec>(a.states + static_cast<int64_t>(row / kS) * cols, col, cols, lane, h);
     T* y = static_cast<T*>(a.y) + static_cast<int64_t>(row) * a.y_ld;
@@ -565,7 +565,10 @@ recurrence_kernel(const __grid_constant__ opt_recurrence_args a, const __grid_co
     else outputs(Flag<false>{});
     __syncwarp();                                // the tile may be written over
   }
-  if (plan.cluster > 1) cluster_sync();          // nobody leaves while mail to it is on its way
+  if (plan.cluster > 1) {                        // nobody leaves while mail to it is on its way
+    cluster_sync();
+    leave_mail(sh.mail, lost_at);
+  }
 }
 
 // One row to each sequence: nothing depends on another row.
@@ -645,7 +648,7 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
   fetch(row, 0);
   saved(row, coming);
   float carry = 0.f;                             // the first kCols threads: behind all rows so far
-  bool lost = false;                             // a message of the cluster's
+  int lost_at = kNoneLost;                       // a message of the cluster's
   for (int turn = 0; turn < turns; ++turn, row -= step) {
     copy_wait<0>();
     __syncwarp();
@@ -705,7 +708,7 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
     if (plain) pieces(Flag<true>{});
     else pieces(Flag<false>{});
     float b[kC];                                 // (1 - c) l of the row behind
-    exchange<kC, kW, kVec, true>(sh, turn, plan.cluster, rank, warp, lane, mine, carry, lost, b);
+    exchange<kC, kW, kVec, true>(sh, turn, plan.cluster, rank, warp, lane, mine, carry, lost_at, b);
     T* dx = static_cast<T*>(a.dx) + static_cast<int64_t>(row + kS - 1) * a.dx_ld;
     T* dg = static_cast<T*>(a.dgate) + static_cast<int64_t>(row + kS - 1) * a.dgate_ld;
     auto outputs = [&](auto plain) {
@@ -740,7 +743,10 @@ recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const
     else outputs(Flag<false>{});
     __syncwarp();                                // the tile may be written over
   }
-  if (plan.cluster > 1) cluster_sync();          // nobody leaves while mail to it is on its way
+  if (plan.cluster > 1) {                        // nobody leaves while mail to it is on its way
+    cluster_sync();
+    leave_mail(sh.mail, lost_at);
+  }
 }
 
 // ---------------------------------------------------------------- launch --

@@ -35,6 +35,7 @@ _vp, _i32, _i64, _sz, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ct
 INDEX_INT32, INDEX_INT64 = 0, 1
 CHECKPOINT_BLOCK = 32
 STATE_ROWS = 8                # opt_recurrence_state_rows
+MAIL_SELFTEST_THREADS = 64
 
 
 class OptEmbeddingArgs(ctypes.Structure):
@@ -84,7 +85,8 @@ def declare(L):
             ("opt_recurrence_state_rows", [_i32], _i64),
             ("opt_checkpoint_save", [_vp, _i64, _i32, _i64, _i64, _vp, _i64, _vp, _i64, _vp], ctypes.c_int),
             ("opt_checkpoint_restore", [_vp, _vp], ctypes.c_int),
-            ("opt_cross_entropy", [_vp, _vp], ctypes.c_int)):
+            ("opt_cross_entropy", [_vp, _vp], ctypes.c_int),
+            ("opt_selftest_mail", [_vp, _i32, _i32, _i32, _vp], ctypes.c_int)):
         f = getattr(L, name)
         f.argtypes, f.restype = args, res
 
@@ -311,3 +313,22 @@ def cross_entropy(logits, labels, loss=None, lse=None, dlogits=None, scale=1.0, 
     status = mp.lib().opt_cross_entropy(a, _stream(stream, dev))
     if status:
         mp._check(status, "opt_cross_entropy")
+
+
+# --------------------------------------------------------------------------
+# self-test
+# --------------------------------------------------------------------------
+
+def selftest_mail(sums, held_back=-1, stream=None):
+    """The messages between the CTAs of a cluster, with a part of one held back (see
+    opt_selftest_mail).  sums [CTAs][messages][64] fp32: what each thread received,
+    NaN for a message that did not come.  For tests of the failure path."""
+    torch = _torch or _load_torch()
+    ctas, messages, threads = sums.shape
+    if threads != MAIL_SELFTEST_THREADS:
+        raise ValueError(f"sums has shape {tuple(sums.shape)}, expected (CTAs, messages, {MAIL_SELFTEST_THREADS})")
+    dev = sums.get_device()
+    status = mp.lib().opt_selftest_mail(_vec(sums, torch.float32, sums.numel(), "sums", dev), ctas, messages, held_back,
+                                        _stream(stream, dev))
+    if status:
+        mp._check(status, "opt_selftest_mail")
