@@ -702,8 +702,11 @@ MPOPT_API size_t opt_embedding_workspace_size(int64_t rows, int64_t vocab, int64
  *     (a step of single tokens) on.
  * starts that break these rules give wrong results, but no access out of range.
  *
- * states, for opt_recurrence_backward: h before every opt_recurrence_state_rows-th
- * row, [ceil(rows / state_rows)][cols] fp32.
+ * states [ceil(rows / state_rows)][cols] fp32, state_rows from
+ * opt_recurrence_state_rows, is what opt_recurrence_backward needs: h before every
+ * state_rows-th row.  It is not for callers to read, and not all of it is written:
+ * nothing of it when starts is NULL and each sequence has one row, and the place
+ * of a row that begins a sequence or belongs to none holds anything.
  *
  * y may be x or gate itself (same pointer and row distance) when no gradient is
  * wanted.  hT may be h0 itself when starts is NULL and each sequence has one row.

@@ -189,7 +189,8 @@ def embedding_workspace(rows, vocab, cols, device=None):
 
 def recurrence_states(rows, cols, dtype, device=None):
     """Buffer for gated_recurrence's states: what gated_recurrence_backward needs
-    of a forward pass over this many rows of this type (bf16 or fp32)."""
+    of a forward pass over this many rows of this type (bf16 or fp32).  Only that
+    reads it; where it has no use for a value, the forward pass writes none."""
     torch = _torch or _load_torch()
     if ff._CODES.get(dtype) not in _FLOAT:
         raise TypeError(f"unsupported type, {dtype}")
