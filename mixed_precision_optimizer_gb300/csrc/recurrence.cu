@@ -100,8 +100,8 @@ constexpr int kTile = kS * 32 * kC * static_cast<int>(sizeof(T));   // bytes of 
 // CTAs to an SM, by registers and shared memory.
 template <typename T, int kC, int kW>
 constexpr int kForwardCtas = kW == 16 ? (sizeof(T) == 2 ? 2 : 1) : kC == 4 ? 2 : sizeof(T) == 2 ? 4 : 3;
-template <typename T, int kW>
-constexpr int kBackwardCtas = kW == 16 ? 1 : sizeof(T) == 2 ? 3 : 2;
+template <int kW>
+constexpr int kBackwardCtas = kW == 16 ? 1 : 3;
 
 struct Plan {
   int cluster, ranges, groups;      // CTAs to a cluster; shares of the sequences; shares of the columns
@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(kStepThreads) recurrence_step_kernel(const __g
 // From the last row to the first.  Each warp runs through its rows forward from
 // the saved state for (1 - c) (x_t - h_{t-1}), then backward twice.
 template <typename T, int kC, int kW, bool kVec, bool kRagged>
-__global__ void __launch_bounds__(32 * kW, (kBackwardCtas<T, kW>))
+__global__ void __launch_bounds__(32 * kW, kBackwardCtas<kW>)
 recurrence_grad_kernel(const __grid_constant__ opt_recurrence_grad_args a, const __grid_constant__ Plan plan) {
   constexpr int kCols = 32 * kC;
   using L = Layout<T, kC, kW, 3>;
@@ -811,11 +811,15 @@ cudaError_t run_backward(const opt_recurrence_grad_args& a, cudaStream_t stream)
 // The time is that of the turns, one after another, until the columns fill the
 // GPU: narrow recurrences take 16 warps, that is twice the rows, a turn (16384
 // rows in bf16, back to back: 512 columns 54 us forward and 50 backward, with 8
-// warps 59 and 96; 2048 columns 60 and 87, with 8 warps 102 and 131; the gradient of
-// 8192 packed rows of 4096 columns 100, with 8 warps 99).  From kWideCols on the
-// forward pass has four columns to a lane: half the instructions around a row's
-// arithmetic (4096 columns 98 us, with two columns 108 by 16 warps and 109 by 8; 2048
-// columns 94, with two 60: too few CTAs).
+// warps 59 and 96; 2048 columns 60 and 87, with 8 warps 102 and 131).  The gradient
+// in bf16 beyond kFewGradCols columns has 8, three CTAs to an SM: 8192 packed rows of
+// 4096 columns 99 us and 100 with 16, of 6144 133 and 151, of 4095, one element at a
+// time, 459 and 657 (8192 columns the other way round: 175 and 151).  In fp32, whose
+// registers leave room for two such CTAs only, it has 16 throughout: 8192 rows of
+// 2560 columns 72 us and 118 with 8, of 4096 108 and 167, of 4095 244 and 431.  From
+// kWideCols on the forward pass has four columns to a lane: half the instructions
+// around a row's arithmetic (4096 columns 98 us, with two columns 108 by 16 warps and
+// 109 by 8; 2048 columns 94, with two 60: too few CTAs).
 constexpr int64_t kWideCols = 4096, kFewGradCols = 2048;
 
 template <typename T, bool kVec>
@@ -831,7 +835,10 @@ cudaError_t forward(const opt_recurrence_args& a, cudaStream_t stream) {
 
 template <typename T, bool kVec>
 cudaError_t backward(const opt_recurrence_grad_args& a, cudaStream_t stream) {
-  return a.cols <= kFewGradCols ? run_backward<T, 16, kVec>(a, stream) : run_backward<T, 8, kVec>(a, stream);
+  if constexpr (sizeof(T) == 2) {
+    if (a.cols > kFewGradCols) return run_backward<T, 8, kVec>(a, stream);
+  }
+  return run_backward<T, 16, kVec>(a, stream);
 }
 
 }  // namespace
