@@ -689,8 +689,9 @@ MPOPT_API size_t opt_embedding_workspace_size(int64_t rows, int64_t vocab, int64
  * Gated recurrence, for every column by itself, along the rows of a sequence:
  *   h_t = h_{t-1} + c_t (x_t - h_{t-1}),  c_t = 1 / (1 + exp(-gate_t)),  y_t = h_t
  * with h = h0 before the first row (zeros without h0) and hT = h behind the last.
- * h is kept in fp32; y is its rounding.  x and gate are products of linear
- * layers.
+ * h is kept in fp32; y is its rounding.  Of c and 1 - c the smaller is computed,
+ * within (2 |gate| + 16) 2^-24 of itself (0 beyond |gate| = 87), and used for both.
+ * x and gate are products of linear layers.
  *
  * The rows of `sequences` sequences are packed one behind the other:
  *   starts [sequences + 1] (int32, on the device): sequence s has the rows

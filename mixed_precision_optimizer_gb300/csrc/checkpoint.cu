@@ -8,8 +8,8 @@
 // two cost no rounding, so z needs no more than e4m3's four significant bits and
 // a bf16 output is z itself.  Where rows start on 16 bytes a thread has 8 columns
 // of four (two) rows, four neighbouring lanes a block of 32: 8192 x 14336 in bf16
-// 54 us (0.97 of the measured copy rate), back through GELU with its gradient 127
-// (0.96); a row a thread and a flat grid, whose 64-bit divisions are a third of
+// 54 us (0.99 of the measured copy rate), back through GELU with its gradient 126
+// (0.98); a row a thread and a flat grid, whose 64-bit divisions are a third of
 // the instructions, took 89 and 158.  Otherwise a warp has a block, an element to
 // each lane.
 

@@ -8,9 +8,9 @@
 // the product of their 1 - c; the gradient passes them the same way backwards.
 // Two such pieces, the first (P1, B1) and behind it (P2, B2), make
 //   P = P1 P2,  B = B2 + P2 B1
-// Both c and 1 - c are taken from the smaller of them, which is exact to 2^-20 of
-// itself however far the gate is open or closed: (1 - c) v is v - c v where
-// c < 1/2, one rounding of v, and the product with 1 - c beyond.  A piece in which a
+// Both c and 1 - c are taken from the smaller of them, which keeps its digits however
+// far the gate is open or closed: (1 - c) v is v - c v where c < 1/2, one rounding
+// of v, and the product with 1 - c beyond.  A piece in which a
 // sequence starts or ends does not depend on the state before it: P = kReset,
 // and B is selected, not multiplied, so that an infinity or a NaN stays in its
 // own sequence.
@@ -19,13 +19,14 @@
 // memory, fetched with cp.async while it works on the rows before.  The pieces of
 // its CTA's eight or 16 warps, and those of the CTAs of a cluster, which take the
 // next rows each, are joined through (distributed) shared memory; then every
-// thread applies the pieces up to each of its rows to the right state (the gradient runs
-// through its rows again; for the forward pass that took 109 us in place of 97.6, the
-// gradient's registers do not hold the pieces).  x and gate are read
-// once (and dy), the outputs written once: HBM's floor is 60 us for 16384 x 4096 in
-// bf16, 50 for the gradient of 8192 x 4096.  They take 98 and 99: a turn of 512 (384)
-// rows is a chain of the pieces, their join, the mail and the outputs, 3.1 us.  A state
-// for every 8 rows in fp32 is all that the gradient needs of the forward pass.
+// thread applies the pieces up to each of its rows to the right state (the gradient,
+// whose registers do not hold them, runs through its rows again; that way the
+// forward pass takes 12 % longer).  x and gate are read once (and dy), the outputs
+// written once: HBM's floor is 60 us for 16384 x 4096 in bf16, 50 for the gradient of
+// 8192 x 4096.  They take 99 and 103: a turn of 512 (384) rows is a chain of the
+// pieces, their join, the mail and the outputs, 3.1 (4.7) us, with 27 (59)
+// instructions an element.  A state for every 8 rows in fp32 is all that the gradient
+// needs of the forward pass.
 
 #include <climits>
 
@@ -59,8 +60,8 @@ __device__ __forceinline__ float through(Piece q, float h) { return is_reset(q.p
 // instructions of 2 units each; the rounding of gate log2 e adds 2^-24 |gate| of the
 // value.  0 beyond |gate| = 87.  From c alone 1 - c would be off by 2^-24 of 1, that is 1 %
 // of itself at a gate of 12 and all of it from 17 on; the selects that this takes cost
-// the forward pass 6 % (16384 x 4096: 97.6 us for 91.3) and the gradient 10 % (8192 x
-// 4096 packed: 98.8 for 89.8).
+// the forward pass 7 % (16384 x 4096: 99 us for 92) and the gradient 11 % (8192 x 4096
+// packed: 103 for 91 to 94).
 __device__ __forceinline__ float gate_of(float g) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * fabsf(g)));
@@ -82,7 +83,8 @@ __device__ __forceinline__ Parts parts_of(float w, float v) {
 }
 
 // Two columns' pieces with one row more, advance() and keep() by packed instructions
-// (one column at a time took 16384 x 4096 to 101.7 us; with the gates packed too, 117).
+// (one column at a time 16384 x 4096 takes 4 % longer; with the gates packed too, 20 %:
+// more registers than there are).
 __device__ __forceinline__ void add_row(float wa, float wb, float xa, float xb, Piece& a, Piece& b) {
   const float2 n = make_float2(-wa, -wb), d = make_float2(a.b - xa, b.b - xb), p = make_float2(a.p, b.p);
   const float2 h = __ffma2_rn(n, d, make_float2(is_open(wa) ? xa : a.b, is_open(wb) ? xb : b.b));

@@ -125,6 +125,34 @@ def test_gates_of_any_size(sequences, dtype):
     check(24, 200, np.arange(sequences + 1) * (24 // sequences), gate, dtype, 1.0)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("where", [0, 7, 60, 99, 100, 103, 199])
+def test_a_gate_that_is_no_number_stays_in_its_sequence(bad, where):
+    """And an infinite one is open or closed: nothing else in its sequence is lost."""
+    starts = [0, 60, 60, 100, 200]
+    st = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    r = np.random.default_rng(1)
+    x, gate, dy = (dev(r.normal(size=(200, 72)).astype(np.float32)) for _ in range(3))
+    outs = []
+    for hit in (False, True):
+        if hit:
+            gate[where, 5] = bad
+        y, dx, dg = (torch.zeros_like(x) for _ in range(3))
+        states, hT, dh0 = mp.recurrence_states(200, 72, FP32), torch.zeros(4, 72, device="cuda"), torch.zeros(4, 72, device="cuda")
+        mp.gated_recurrence(x, gate, y, starts=st, hT=hT, states=states)
+        mp.gated_recurrence_backward(dy, x, gate, states, dx, dg, starts=st, dh0=dh0)
+        outs.append((y, dx, dg, hT, dh0))
+    seq = max(i for i in range(4) if starts[i] <= where)
+    for a, b in zip(*outs):
+        own = torch.zeros(len(a), 72, dtype=torch.bool, device="cuda")
+        own[(slice(starts[seq], starts[seq + 1]) if len(a) == 200 else seq), 5] = True
+        assert torch.equal(a[~own], b[~own])
+        if bad == bad:
+            assert torch.isfinite(b).all()
+    if bad != bad:
+        assert torch.isnan(outs[1][0][where:starts[seq + 1], 5]).all() and torch.isnan(outs[1][1][starts[seq]:where + 1, 5]).all()
+
+
 def test_open_gate_takes_x_itself():
     """Beyond 87 nothing of h is left, whatever its size."""
     x, h0 = torch.full((2, 64), 1e-3, device="cuda"), torch.full((2, 64), 1e30, device="cuda")
