@@ -12,9 +12,9 @@
 #include <cstdint>
 
 #ifdef __CUDACC__
-#define MPOPT_BOTH __host__ __device__ __forceinline__
+#define MPOPT_MAIL __device__ __forceinline__
 #else
-#define MPOPT_BOTH inline
+#define MPOPT_MAIL inline
 #endif
 
 namespace mpopt {
@@ -25,7 +25,7 @@ constexpr int kNoneLost = -1;
 // Message k; `counts`: this thread expects its CTA's `bytes`; send() sends this part's.
 // lost_at: kNoneLost, or the message that has not come.  Whether message k is there.
 template <typename Mail, typename Send>
-MPOPT_BOTH bool exchange_message(const Mail& mail, int k, bool counts, uint32_t bytes, int& lost_at, Send&& send) {
+MPOPT_MAIL bool exchange_message(const Mail& mail, int k, bool counts, uint32_t bytes, int& lost_at, Send&& send) {
   if (lost_at != kNoneLost) return false;
   if (counts) mail.expect(k, bytes);
   send();
@@ -37,7 +37,7 @@ MPOPT_BOTH bool exchange_message(const Mail& mail, int k, bool counts, uint32_t 
 // Behind the last message and a barrier of the cluster, behind which nothing is sent:
 // mail that was late may still be on its way here.
 template <typename Mail>
-MPOPT_BOTH void leave_mail(const Mail& mail, int lost_at) {
+MPOPT_MAIL void leave_mail(const Mail& mail, int lost_at) {
   if (lost_at != kNoneLost) mail.wait(lost_at);
 }
 

@@ -328,7 +328,7 @@ def selftest_mail(sums, held_back=-1, stream=None):
     ctas, messages, threads = sums.shape
     if threads != MAIL_SELFTEST_THREADS:
         raise ValueError(f"sums has shape {tuple(sums.shape)}, expected (CTAs, messages, {MAIL_SELFTEST_THREADS})")
-    dev = sums.get_device()
+    dev = _lead(sums, "sums")[0]
     status = mp.lib().opt_selftest_mail(_vec(sums, torch.float32, sums.numel(), "sums", dev), ctas, messages, held_back,
                                         _stream(stream, dev))
     if status:

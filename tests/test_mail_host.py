@@ -66,6 +66,13 @@ def test_the_model_sees_a_part_that_goes_on_sending(tmp_path_factory):
     assert code == 1 and "took message" in out
 
 
+def test_selftest_refuses_host_memory():
+    torch = pytest.importorskip("torch")
+    import mixed_precision_optimizer_gb300 as mp
+    with pytest.raises(ValueError, match="CUDA"):
+        mp.selftest_mail(torch.zeros(2, 4, 64))
+
+
 def test_selftest_refusals():
     pytest.importorskip("torch")
     import mixed_precision_optimizer_gb300 as mp
